@@ -16,7 +16,7 @@ import torch
 from .builder import LIBPATH
 
 MAX_LAYERS = 16
-BF16, F32 = 0, 1
+BF16, F32, F16 = 0, 1, 2
 BIDIRECTIONAL, CAUSAL = 0, 1
 
 STATUS = {0: "BD_OK", -1: "BD_ERR_INVALID_ARG", -2: "BD_ERR_UNSUPPORTED", -3: "BD_ERR_CUDA",
@@ -26,7 +26,8 @@ EXPORTS = ("bd_abi_version", "bd_workspace_bytes", "bd_ctx_kv_materialize", "bd_
            "bd_lm_head_argmax", "bd_last_error", "bd_sync_status", "bd_kernel_launches",
            "bd_packed_bytes", "bd_pack_weights", "bd_lm_head_argmax_noalloc", "bd_lm_head_topk",
            "bd_refine_tail", "bd_head_fp8_bytes", "bd_pack_head_fp8", "bd_lm_head_topk_fp8",
-           "bd_selftest_wait", "bd_set_timing_events")
+           "bd_selftest_wait", "bd_set_timing_events", "bd_paged_workspace_bytes", "bd_paged_append",
+           "bd_paged_attention", "bd_paged_weights", "bd_paged_evict")
 
 TOPK_MAX = 16
 
@@ -72,6 +73,19 @@ class KvCache(C.Structure):
 class Pending(C.Structure):
     _fields_ = [("feats", C.c_void_p), ("request", C.c_void_p), ("pos", C.c_void_p),
                 ("n_rows", C.c_int)]
+
+
+class PagedKv(C.Structure):
+    _fields_ = [("n_q_heads", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("dtype", C.c_int), ("page_size", C.c_int), ("n_pages", C.c_int),
+                ("page_stride", C.c_int64), ("head_stride", C.c_int64), ("slot_stride", C.c_int64),
+                ("k", C.c_void_p), ("v", C.c_void_p)]
+
+
+class PagedBatch(C.Structure):
+    _fields_ = [("n_requests", C.c_int), ("table_width", C.c_int), ("n_rows", C.c_int),
+                ("max_rows", C.c_int), ("max_len", C.c_int), ("page_table", C.c_void_p),
+                ("seq_len", C.c_void_p), ("row_start", C.c_void_p)]
 
 
 _lib = None
@@ -126,6 +140,17 @@ def lib() -> C.CDLL:
                                           vp, vp, vp, sz, vp]
         L.bd_set_timing_events.restype = i
         L.bd_set_timing_events.argtypes = [i, C.POINTER(vp), C.POINTER(vp), i]
+        kvp, btp, f, i64 = C.POINTER(PagedKv), C.POINTER(PagedBatch), C.c_float, C.c_int64
+        L.bd_paged_workspace_bytes.restype = sz
+        L.bd_paged_workspace_bytes.argtypes = [kvp, i, i]
+        L.bd_paged_append.restype = i
+        L.bd_paged_append.argtypes = [kvp, btp, vp, i64, vp, i64, vp]
+        L.bd_paged_attention.restype = i
+        L.bd_paged_attention.argtypes = [kvp, btp, vp, i64, vp, i64, vp, i, i, f, vp, sz, vp]
+        L.bd_paged_weights.restype = i
+        L.bd_paged_weights.argtypes = [kvp, btp, vp, i64, vp, vp, i, i, f, f, vp, vp, i64, vp]
+        L.bd_paged_evict.restype = i
+        L.bd_paged_evict.argtypes = [kvp, btp, vp, i64, i, i, i, vp, i, vp, vp, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -312,6 +337,41 @@ def lm_head_argmax_noalloc(cfg: Config, weights: Weights, hidden: torch.Tensor,
     _check(lib().bd_lm_head_argmax_noalloc(
         C.byref(cfg), C.byref(weights), _ptr(hidden), int(hidden.shape[0]), _ptr(token_out),
         _ptr(max_logit_out), _stream(stream)))
+
+
+# The paged-cache calls take the row tensors' addresses and row strides (in elements) as the C
+# ABI does; ``paged.PagedCache`` checks tensors and fills the two structures.
+def paged_workspace_bytes(kv: PagedKv, n_requests: int, max_rows: int) -> int:
+    n = lib().bd_paged_workspace_bytes(C.byref(kv), n_requests, max_rows)
+    if n == 0:
+        raise BdError(-1, lib().bd_last_error().decode())
+    return n
+
+
+def paged_append(kv: PagedKv, batch: PagedBatch, k_new: int, k_stride: int, v_new: int,
+                 v_stride: int, stream: int):
+    _check(lib().bd_paged_append(kv, batch, k_new, k_stride, v_new, v_stride, stream))
+
+
+def paged_attention(kv: PagedKv, batch: PagedBatch, q: int, q_stride: int, out: int,
+                    out_stride: int, lse: Optional[int], window: int, n_sink: int, scale: float,
+                    workspace: int, workspace_nbytes: int, stream: int):
+    _check(lib().bd_paged_attention(kv, batch, q, q_stride, out, out_stride, lse, window, n_sink,
+                                    scale, workspace, workspace_nbytes, stream))
+
+
+def paged_weights(kv: PagedKv, batch: PagedBatch, q: int, q_stride: int, lse: int,
+                  rows_used: Optional[int], window: int, n_sink: int, scale: float, decay: float,
+                  score_in: Optional[int], score_out: int, score_stride: int, stream: int):
+    _check(lib().bd_paged_weights(kv, batch, q, q_stride, lse, rows_used, window, n_sink, scale,
+                                  decay, score_in, score_out, score_stride, stream))
+
+
+def paged_evict(kv: PagedKv, batch: PagedBatch, score: int, score_stride: int, budget: int,
+                n_sink: int, n_recent: int, dst_table: Optional[int], dst_width: int, kept: int,
+                len_out: int, score_out: Optional[int], score_out_stride: int, stream: int):
+    _check(lib().bd_paged_evict(kv, batch, score, score_stride, budget, n_sink, n_recent, dst_table,
+                                dst_width, kept, len_out, score_out, score_out_stride, stream))
 
 
 TIME_KINDS = {"qkv": 1, "attention": 2, "wo": 3, "gate_up": 4, "down": 5, "bridge": 6, "head": 7}

@@ -1,0 +1,539 @@
+// Paged K/V cache: the entry points' checks, and the kernels of the append, the accumulated
+// attention weights and the eviction.
+#include "bd_paged_device.cuh"
+
+#include <cmath>
+
+namespace bd {
+
+BD_DEFINE_ERROR_TAKER(take_error_word_paged)
+
+// ------------------------------------------------------------------ append
+// Copies each row's keys and values into its slot, 16 bytes a thread.  A block takes rows_per_cta
+// consecutive rows and first finds the request of each: every thread tests some of the requests'
+// row ranges against the block's.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 8;
+
+struct PagedAppendArgs {
+  PagedArgs p;
+  const void *k_new, *v_new;
+  int64_t k_stride, v_stride;
+  int rows_per_cta;
+};
+
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs A) {
+  const PagedArgs &a = A.p;
+  __shared__ int64_t off[kAppendRows];  // element offset of the row's slot, -1: not stored
+  const int r0 = blockIdx.x * A.rows_per_cta, r1 = min(a.n_rows, r0 + A.rows_per_cta);
+  if (threadIdx.x < kAppendRows) off[threadIdx.x] = -1;
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.n_requests; b += kAppendThreads) {
+    const int s = a.row_start[b], e = a.row_start[b + 1];
+    if (s < 0 || e < s || e > a.n_rows || e - s > a.max_rows) {
+      atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+      continue;
+    }
+    if (s >= r1 || e <= r0) continue;
+    const int n = request_len(a, b);
+    for (int r = max(s, r0); r < min(e, r1); ++r) {
+      const int p = n - (e - r);
+      off[r - r0] = p < 0 ? -1 : slot_offset(a, a.page_table + static_cast<int64_t>(b) * a.table_width, p);
+    }
+  }
+  __syncthreads();
+  const int per_head = a.head_dim / 8, per_side = a.n_kv_heads * per_head, per_row = 2 * per_side;
+  for (int c = threadIdx.x; c < (r1 - r0) * per_row; c += kAppendThreads) {
+    const int r = c / per_row, u = c - r * per_row;
+    if (off[r] < 0) continue;
+    const bool v = u >= per_side;
+    const int w = v ? u - per_side : u, h = w / per_head, x = (w - h * per_head) * 8;
+    const uint16_t *src = static_cast<const uint16_t *>(v ? A.v_new : A.k_new) +
+                          (r0 + r) * (v ? A.v_stride : A.k_stride) + w * 8;
+    uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(v ? a.v : a.k)) + off[r] + h * a.head_stride + x;
+    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src);
+  }
+}
+
+static std::string launch_append(PagedAppendArgs &A, cudaStream_t s) {
+  A.rows_per_cta = A.p.n_rows > 8 * num_sms() ? kAppendRows : 1;
+  const int grid = (A.p.n_rows + A.rows_per_cta - 1) / A.rows_per_cta;
+  const cudaError_t e = launch_pdl(paged_append_kernel, dim3(grid), dim3(kAppendThreads), 0, s, A);
+  return e == cudaSuccess ? std::string() : std::string("paged append: ") + cudaGetErrorString(e);
+}
+
+// ------------------------------------------------------------------ accumulated weights
+// One warp per slot j: for each row that sees it and each query head, s = q.k over the lanes'
+// D/32 columns, then exp2(s - lse / ln 2).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_weights_kernel(const __grid_constant__ PagedWeightsArgs A) {
+  const PagedArgs &a = A.p;
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31, b = blockIdx.y;
+  const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
+  const Request rq = request_of(a, b);
+  if (j >= rq.n) return;
+  const int used = A.rows_used ? max(0, min(A.rows_used[b], rq.rows)) : rq.rows;
+  const int hq = a.n_kv_heads * a.group;
+  const int64_t off = slot_offset(a, a.page_table + static_cast<int64_t>(b) * a.table_width, j);
+  float sum = 0.f;
+  for (int h = 0; h < a.n_kv_heads && off >= 0; ++h) {
+    float k[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) k[c] = to_f(static_cast<const T *>(a.k)[off + h * a.head_stride + c * 32 + lane]);
+    for (int i = max(0, j - (rq.n - rq.rows)); i < used; ++i) {
+      const int p = rq.n - rq.rows + i;
+      if (j >= a.n_sink && j < window_first(a, p)) break;
+      for (int g = 0; g < a.group; ++g) {
+        const int head = h * a.group + g;
+        const T *q = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + head * D;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) s += k[c] * to_f(q[c * 32 + lane]);
+        const float lse = A.lse[static_cast<int64_t>(rq.row0 + i) * hq + head];
+        sum += exp2f(warp_sum(s) * a.scale_log2 - lse * (1.f / kLn2));
+      }
+    }
+  }
+  if (lane == 0) {
+    const int64_t x = b * A.score_stride + j;
+    A.score_out[x] = (A.score_in ? A.decay * A.score_in[x] : 0.f) + sum;
+  }
+}
+
+static std::string launch_weights(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
+  const PagedArgs &a = A.p;
+  const dim3 grid((a.max_len + 7) / 8, a.n_requests);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, A); };
+  cudaError_t e;
+  if (dtype == BD_BF16)
+    e = a.head_dim == 128 ? go(paged_weights_kernel<__nv_bfloat16, 128>) : go(paged_weights_kernel<__nv_bfloat16, 64>);
+  else
+    e = a.head_dim == 128 ? go(paged_weights_kernel<__half, 128>) : go(paged_weights_kernel<__half, 64>);
+  return e == cudaSuccess ? std::string() : std::string("paged weights: ") + cudaGetErrorString(e);
+}
+
+// ------------------------------------------------------------------ eviction
+// Order-preserving integer image of a score: NaN as -inf, -0 as +0.
+__device__ __forceinline__ uint32_t score_key(float x) {
+  if (x != x) x = -INFINITY;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+constexpr int kSelThreads = 1024;
+
+// One block per request.  The score of the last slot that stays is found by radix selection,
+// eight bits of the key a pass: a histogram of the slots that match the bits found so far, then
+// the digit that holds the wanted rank.  A last pass in slot order keeps what is larger, and of
+// what is equal the first ones; ballots and the warps' counts give each kept slot its place.
+__global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_constant__ PagedEvictArgs A) {
+  __shared__ int hist[256];
+  __shared__ int warp_cnt[2][kSelThreads / 32];
+  __shared__ uint32_t s_key;
+  __shared__ int s_need;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int n = request_len(A.p, b);
+  const float *score = A.score + b * A.score_stride;
+  float *score_out = A.score_out ? A.score_out + b * A.score_out_stride : nullptr;
+  int32_t *kept = A.kept + static_cast<int64_t>(b) * A.budget;
+  const bool all = n <= A.budget;
+  // slots [lo, hi) compete; those outside stay
+  const int lo = all ? n : A.n_sink, hi = all ? n : n - A.n_recent;
+  int need = all ? 0 : A.budget - A.n_sink - A.n_recent;  // of them, how many stay
+  uint32_t key = 0;                                       // key of the last one that stays
+  if (need > 0) {
+    uint32_t mask = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int d = tid; d < 256; d += kSelThreads) hist[d] = 0;
+      __syncthreads();
+      for (int j = lo + tid; j < hi; j += kSelThreads) {
+        const uint32_t u = score_key(score[j]);
+        if ((u & mask) == key) atomicAdd(&hist[(u >> shift) & 255], 1);
+      }
+      __syncthreads();
+      if (warp == 0) {  // lane l holds digits 255-8l .. 248-8l, largest first
+        int c[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += x;
+        }
+        before -= sum;
+        if (before < need && before + sum >= need) {
+          int i = 0;
+          while (before + c[i] < need) before += c[i++];
+          s_key = key | static_cast<uint32_t>(255 - 8 * lane - i) << shift;
+          s_need = need - before;
+        }
+      }
+      __syncthreads();
+      key = s_key;
+      need = s_need;
+      mask |= 255u << shift;
+      __syncthreads();
+    }
+  }
+  // need: how many of the slots whose key is `key` stay (the first ones)
+  int placed = 0, ties = 0;
+  const bool some = !all && A.budget > A.n_sink + A.n_recent;
+  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+    const int j = j0 + tid;
+    const float x = j < n ? score[j] : 0.f;
+    const bool in = j >= lo && j < hi;
+    const uint32_t u = in && some ? score_key(x) : 0u;
+    const bool tie = in && some && u == key;
+    const unsigned tie_bits = __ballot_sync(0xffffffffu, tie);
+    if (lane == 0) warp_cnt[0][warp] = __popc(tie_bits);
+    __syncthreads();
+    int ties_before = ties + __popc(tie_bits & ((1u << lane) - 1));
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      const int c = warp_cnt[0][w];
+      if (w < warp) ties_before += c;
+      ties += c;
+    }
+    const bool keep = j < n && (!in || (some && (u > key || (tie && ties_before < need))));
+    const unsigned keep_bits = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) warp_cnt[1][warp] = __popc(keep_bits);
+    __syncthreads();
+    int place = placed + __popc(keep_bits & ((1u << lane) - 1));
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      const int c = warp_cnt[1][w];
+      if (w < warp) place += c;
+      placed += c;
+    }
+    if (keep) {
+      kept[place] = j;
+      if (score_out) score_out[place] = x;
+    }
+  }
+  if (score_out == score)  // slots filled later start from zero
+    for (int j = placed + tid; j < n; j += kSelThreads) score_out[j] = 0.f;
+  __syncthreads();
+  if (tid == 0) A.len_out[b] = placed;
+}
+
+// Moves the kept slots.  Slot i's row of one pool and KV head is D contiguous values; a thread
+// moves 16 bytes of it.  To other pages every block takes kMoveRows slots of its own.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 64;
+
+__device__ __forceinline__ int64_t dst_offset(const PagedEvictArgs &A, int b, int i) {
+  if (!A.dst_table) return slot_offset(A.p, A.p.page_table + static_cast<int64_t>(b) * A.p.table_width, i);
+  return slot_offset(A.p, A.dst_table + static_cast<int64_t>(b) * A.dst_width, i);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_constant__ PagedEvictArgs A) {
+  const PagedArgs &a = A.p;
+  const int b = blockIdx.z, h = blockIdx.y >> 1;
+  uint16_t *pool = static_cast<uint16_t *>(const_cast<void *>(blockIdx.y & 1 ? a.v : a.k)) + h * a.head_stride;
+  const int cpr = a.head_dim / 8;
+  pdl_wait();
+  pdl_trigger();
+  const int n = min(A.len_out[b], A.budget);
+  const int32_t *kept = A.kept + static_cast<int64_t>(b) * A.budget;
+  const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+  const int i0 = blockIdx.x * kMoveRows;
+  for (int c = threadIdx.x; c < kMoveRows * cpr; c += kMoveThreads) {
+    const int i = i0 + c / cpr, x = (c % cpr) * 8;
+    if (i >= n) break;
+    const int64_t src = slot_offset(a, table, kept[i]), dst = dst_offset(A, b, i);
+    if (src >= 0 && dst >= 0)
+      *reinterpret_cast<uint4 *>(pool + dst + x) = *reinterpret_cast<const uint4 *>(pool + src + x);
+  }
+}
+
+// In place, one block per (request, KV head, pool) goes up through the slots in chunks of
+// kChunkRows.  Slot i comes from old slot kept[i] >= i, so a chunk's writes can only hit rows that
+// this chunk or an earlier one reads: a chunk is written after all of it has been read, and the
+// next chunk's reads may go ahead of it.
+constexpr int kInThreads = 512;
+constexpr int kInRegs = 8;  // 16-byte pieces of a chunk per thread
+
+__global__ void __launch_bounds__(kInThreads) paged_move_in_place_kernel(const __grid_constant__ PagedEvictArgs A) {
+  const PagedArgs &a = A.p;
+  const int b = blockIdx.y, h = blockIdx.x >> 1;
+  uint16_t *pool = static_cast<uint16_t *>(const_cast<void *>(blockIdx.x & 1 ? a.v : a.k)) + h * a.head_stride;
+  const int cpr = a.head_dim / 8;
+  const int chunk = kInThreads * kInRegs / cpr;  // rows
+  pdl_wait();
+  pdl_trigger();
+  const int n = min(A.len_out[b], A.budget);
+  const int32_t *kept = A.kept + static_cast<int64_t>(b) * A.budget;
+  const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+  for (int i0 = 0; i0 < n; i0 += chunk) {
+    uint4 v[kInRegs];
+    int64_t dst[kInRegs];
+#pragma unroll
+    for (int u = 0; u < kInRegs; ++u) {
+      const int c = u * kInThreads + threadIdx.x, i = i0 + c / cpr, x = (c % cpr) * 8;
+      dst[u] = -1;
+      if (i < n) {
+        const int j = kept[i];
+        if (j != i) {
+          const int64_t src = slot_offset(a, table, j), d = slot_offset(a, table, i);
+          if (src >= 0 && d >= 0) {
+            dst[u] = d + x;
+            v[u] = *reinterpret_cast<const uint4 *>(pool + src + x);
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kInRegs; ++u)
+      if (dst[u] >= 0) *reinterpret_cast<uint4 *>(pool + dst[u]) = v[u];
+  }
+}
+
+static std::string launch_evict(const PagedEvictArgs &A, cudaStream_t s) {
+  const PagedArgs &a = A.p;
+  cudaError_t e = launch_pdl(paged_select_kernel, dim3(a.n_requests), dim3(kSelThreads), 0, s, A);
+  if (e == cudaSuccess) {
+    const int most = A.budget < a.max_len ? A.budget : a.max_len;
+    if (A.dst_table) {
+      const dim3 grid((most + kMoveRows - 1) / kMoveRows, 2 * a.n_kv_heads, a.n_requests);
+      if (most > 0) e = launch_pdl(paged_move_kernel, grid, dim3(kMoveThreads), 0, s, A);
+    } else if (A.budget < a.max_len) {  // else nothing can leave
+      e = launch_pdl(paged_move_in_place_kernel, dim3(2 * a.n_kv_heads, a.n_requests), dim3(kInThreads), 0, s, A);
+    }
+  }
+  return e == cudaSuccess ? std::string() : std::string("paged eviction: ") + cudaGetErrorString(e);
+}
+
+// ------------------------------------------------------------------ host checks
+namespace {
+
+bd_status refuse(bd_status st, const std::string &msg) {
+  set_last_error(msg);
+  return st;
+}
+bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// Whether [p, p + np) and [q, q + nq) (bytes) share any.
+bool overlap(const void *p, int64_t np, const void *q, int64_t nq) {
+  const char *a = static_cast<const char *>(p), *b = static_cast<const char *>(q);
+  return np > 0 && nq > 0 && a < b + nq && b < a + np;
+}
+
+bd_status check_kv(const bd_paged_kv *c) {
+  if (!c) return refuse(BD_ERR_INVALID_ARG, "paged kv is NULL");
+  if (c->dtype != BD_BF16 && c->dtype != BD_F16)
+    return refuse(BD_ERR_UNSUPPORTED, "paged kv: dtype must be BD_BF16 or BD_F16");
+  if (c->head_dim != 64 && c->head_dim != 128) return refuse(BD_ERR_UNSUPPORTED, "paged kv: head_dim must be 64 or 128");
+  if (c->n_kv_heads <= 0 || c->n_q_heads <= 0 || c->n_q_heads % c->n_kv_heads != 0)
+    return refuse(BD_ERR_INVALID_ARG, "paged kv: n_q_heads must be a positive multiple of n_kv_heads");
+  if (c->n_q_heads / c->n_kv_heads > BD_PAGED_MAX_GROUP || c->n_kv_heads > 1024)
+    return refuse(BD_ERR_UNSUPPORTED, "paged kv: at most 128 query heads per KV head and 1024 KV heads");
+  if (c->page_size < 1 || c->n_pages < 1) return refuse(BD_ERR_INVALID_ARG, "paged kv: page_size and n_pages must be >= 1");
+  if (!c->k || !c->v || misaligned(c->k, 16) || misaligned(c->v, 16))
+    return refuse(BD_ERR_INVALID_ARG, "paged kv: k and v must be 16-byte aligned pools");
+  for (int64_t s : {c->page_stride, c->head_stride, c->slot_stride})
+    if (s < 0 || s % 8) return refuse(BD_ERR_INVALID_ARG, "paged kv: strides must be multiples of 8 elements, >= 0");
+  if ((c->page_size > 1 && c->slot_stride < c->head_dim) || (c->n_kv_heads > 1 && c->head_stride < c->head_dim) ||
+      (c->n_pages > 1 && c->page_stride < c->head_dim))
+    return refuse(BD_ERR_INVALID_ARG, "paged kv: strides must be at least head_dim elements");
+  return BD_OK;
+}
+
+bd_status check_batch(const bd_paged_kv *c, const bd_paged_batch *t, bool rows) {
+  if (bd_status st = check_kv(c)) return st;
+  if (!t) return refuse(BD_ERR_INVALID_ARG, "paged batch is NULL");
+  if (t->n_requests < 1 || t->n_requests > BD_PAGED_MAX_REQUESTS)
+    return refuse(BD_ERR_INVALID_ARG, "paged batch: n_requests must be in 1..1024");
+  if (t->table_width < 1 || t->max_len < 0 ||
+      t->max_len > static_cast<int64_t>(t->table_width) * c->page_size || t->max_len > (1 << 30))
+    return refuse(BD_ERR_INVALID_ARG, "paged batch: max_len must be within table_width * page_size (and 2^30)");
+  if (!t->page_table || !t->seq_len || misaligned(t->page_table, 4) || misaligned(t->seq_len, 4))
+    return refuse(BD_ERR_INVALID_ARG, "paged batch: page_table and seq_len must be given");
+  if (rows) {
+    if (!t->row_start || misaligned(t->row_start, 4)) return refuse(BD_ERR_INVALID_ARG, "paged batch: row_start must be given");
+    if (t->n_rows < 0 || t->max_rows < 0 || t->max_rows > t->n_rows || t->n_rows > (1 << 28))
+      return refuse(BD_ERR_INVALID_ARG, "paged batch: 0 <= max_rows <= n_rows <= 2^28");
+  }
+  return BD_OK;
+}
+
+bd_status check_rows(const void *p, int64_t stride, int64_t width, int n_rows, const char *name) {
+  if (!p || misaligned(p, 16) || stride % 8 || (n_rows > 1 && stride < width))
+    return refuse(BD_ERR_INVALID_ARG, std::string("paged cache: ") + name +
+                                          " must be 16-byte aligned rows with a stride that is a multiple of 8 and holds a row");
+  return BD_OK;
+}
+int64_t row_bytes(int64_t stride, int64_t width, int n_rows) {
+  return n_rows < 1 ? 0 : ((n_rows - 1) * stride + width) * 2;
+}
+
+bd_status check_mask(int window, int n_sink, float scale) {
+  if (window < 0 || n_sink < 0) return refuse(BD_ERR_INVALID_ARG, "paged attention: window and n_sink must be >= 0");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return refuse(BD_ERR_INVALID_ARG, "paged attention: scale must be > 0 and finite");
+  return BD_OK;
+}
+
+PagedArgs args_of(const bd_paged_kv *c, const bd_paged_batch *t) {
+  PagedArgs a = {};
+  a.k = c->k;
+  a.v = c->v;
+  a.page_stride = c->page_stride;
+  a.head_stride = c->head_stride;
+  a.slot_stride = c->slot_stride;
+  a.n_kv_heads = c->n_kv_heads;
+  a.group = c->n_q_heads / c->n_kv_heads;
+  a.head_dim = c->head_dim;
+  a.page_size = c->page_size;
+  a.n_pages = c->n_pages;
+  a.n_requests = t->n_requests;
+  a.table_width = t->table_width;
+  a.n_rows = t->n_rows;
+  a.max_rows = t->max_rows;
+  a.max_len = t->max_len;
+  a.page_table = t->page_table;
+  a.seq_len = t->seq_len;
+  a.row_start = t->row_start;
+  return a;
+}
+bd_status ran(const std::string &e) { return e.empty() ? BD_OK : refuse(BD_ERR_CUDA, e); }
+
+}  // namespace
+}  // namespace bd
+
+using namespace bd;
+
+extern "C" {
+
+size_t bd_paged_workspace_bytes(const bd_paged_kv *kv, int n_requests, int max_rows) {
+  if (check_kv(kv)) return 0;
+  if (n_requests < 1 || n_requests > BD_PAGED_MAX_REQUESTS || max_rows < 0) {
+    refuse(BD_ERR_INVALID_ARG, "paged workspace: n_requests must be in 1..1024 and max_rows >= 0");
+    return 0;
+  }
+  return 256;
+}
+
+bd_status bd_paged_append(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *k_new, int64_t k_stride,
+                          const void *v_new, int64_t v_stride, void *stream) {
+  if (bd_status st = check_batch(kv, batch, true)) return st;
+  if (batch->n_rows == 0) return BD_OK;
+  const int64_t width = static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim;
+  if (bd_status st = check_rows(k_new, k_stride, width, batch->n_rows, "k_new")) return st;
+  if (bd_status st = check_rows(v_new, v_stride, width, batch->n_rows, "v_new")) return st;
+  PagedAppendArgs A = {};
+  A.p = args_of(kv, batch);
+  A.k_new = k_new;
+  A.v_new = v_new;
+  A.k_stride = k_stride;
+  A.v_stride = v_stride;
+  return ran(launch_append(A, static_cast<cudaStream_t>(stream)));
+}
+
+bd_status bd_paged_attention(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *q, int64_t q_stride, void *out,
+                             int64_t out_stride, float *lse, int window, int n_sink, float scale, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  if (bd_status st = check_batch(kv, batch, true)) return st;
+  if (bd_status st = check_mask(window, n_sink, scale)) return st;
+  if (batch->max_rows == 0) return BD_OK;
+  const int64_t width = static_cast<int64_t>(kv->n_q_heads) * kv->head_dim;
+  if (bd_status st = check_rows(q, q_stride, width, batch->n_rows, "q")) return st;
+  if (bd_status st = check_rows(out, out_stride, width, batch->n_rows, "out")) return st;
+  if (overlap(q, row_bytes(q_stride, width, batch->n_rows), out, row_bytes(out_stride, width, batch->n_rows)))
+    return refuse(BD_ERR_INVALID_ARG, "paged attention: q and out overlap");
+  if (misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged attention: lse misaligned");
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < bd_paged_workspace_bytes(kv, batch->n_requests, batch->max_rows))
+    return refuse(BD_ERR_WORKSPACE, "paged attention: workspace NULL, not 256-byte aligned or too small");
+  PagedAttnArgs A = {};
+  A.p = args_of(kv, batch);
+  A.p.q = q;
+  A.p.q_stride = q_stride;
+  A.p.window = window;
+  A.p.n_sink = n_sink;
+  A.p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  A.out = out;
+  A.out_stride = out_stride;
+  A.lse = lse;
+  return ran(launch_paged_attention(A, kv->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+bd_status bd_paged_weights(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *q, int64_t q_stride,
+                           const float *lse, const int32_t *rows_used, int window, int n_sink, float scale, float decay,
+                           const float *score_in, float *score_out, int64_t score_stride, void *stream) {
+  if (bd_status st = check_batch(kv, batch, true)) return st;
+  if (bd_status st = check_mask(window, n_sink, scale)) return st;
+  if (batch->max_len == 0) return BD_OK;
+  const int64_t width = static_cast<int64_t>(kv->n_q_heads) * kv->head_dim;
+  if (batch->max_rows > 0) {
+    if (bd_status st = check_rows(q, q_stride, width, batch->n_rows, "q")) return st;
+    if (!lse || misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged weights: lse must be given");
+  }
+  if (misaligned(rows_used, 4)) return refuse(BD_ERR_INVALID_ARG, "paged weights: rows_used misaligned");
+  if (!std::isfinite(decay)) return refuse(BD_ERR_INVALID_ARG, "paged weights: decay must be finite");
+  if (!score_out || misaligned(score_out, 4) || misaligned(score_in, 4) || score_stride < batch->max_len)
+    return refuse(BD_ERR_INVALID_ARG, "paged weights: score_out must be given, with rows of at least max_len entries");
+  const int64_t bytes = ((batch->n_requests - 1) * score_stride + batch->max_len) * 4;
+  if (score_in && score_in != score_out && overlap(score_in, bytes, score_out, bytes))
+    return refuse(BD_ERR_INVALID_ARG, "paged weights: score_in must be score_out or not overlap it");
+  PagedWeightsArgs A = {};
+  A.p = args_of(kv, batch);
+  A.p.q = q;
+  A.p.q_stride = q_stride;
+  A.p.window = window;
+  A.p.n_sink = n_sink;
+  A.p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  A.lse = lse;
+  A.rows_used = rows_used;
+  A.decay = decay;
+  A.score_in = score_in;
+  A.score_out = score_out;
+  A.score_stride = score_stride;
+  return ran(launch_weights(A, kv->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+bd_status bd_paged_evict(const bd_paged_kv *kv, const bd_paged_batch *batch, const float *score, int64_t score_stride,
+                         int budget, int n_sink, int n_recent, const int32_t *dst_table, int dst_width, int32_t *kept_out,
+                         int32_t *len_out, float *score_out, int64_t score_out_stride, void *stream) {
+  if (bd_status st = check_batch(kv, batch, false)) return st;
+  if (budget < 1 || n_sink < 0 || n_recent < 0 || static_cast<int64_t>(n_sink) + n_recent > budget)
+    return refuse(BD_ERR_INVALID_ARG, "paged eviction: budget must be >= 1 and hold n_sink + n_recent");
+  const int most = budget < batch->max_len ? budget : batch->max_len;
+  if (!score || misaligned(score, 4) || score_stride < batch->max_len)
+    return refuse(BD_ERR_INVALID_ARG, "paged eviction: score must be given, with rows of at least max_len entries");
+  if (!kept_out || !len_out || misaligned(kept_out, 4) || misaligned(len_out, 4))
+    return refuse(BD_ERR_INVALID_ARG, "paged eviction: kept_out and len_out must be given");
+  if (dst_table && (misaligned(dst_table, 4) || dst_width < 1 || static_cast<int64_t>(dst_width) * kv->page_size < most))
+    return refuse(BD_ERR_INVALID_ARG, "paged eviction: dst_table's rows must hold min(budget, max_len) slots");
+  if (dst_table == batch->page_table && dst_table)
+    return refuse(BD_ERR_INVALID_ARG, "paged eviction: dst_table is page_table (NULL moves in place)");
+  if (score_out) {
+    if (misaligned(score_out, 4) || score_out_stride < most)
+      return refuse(BD_ERR_INVALID_ARG, "paged eviction: score_out's rows must hold min(budget, max_len) entries");
+    const int64_t in = ((batch->n_requests - 1) * score_stride + batch->max_len) * 4;
+    const int64_t out = ((batch->n_requests - 1) * score_out_stride + most) * 4;
+    if (score_out == score ? score_out_stride != score_stride : overlap(score, in, score_out, out))
+      return refuse(BD_ERR_INVALID_ARG, "paged eviction: score_out must be score (same stride) or not overlap it");
+  }
+  PagedEvictArgs A = {};
+  A.p = args_of(kv, batch);
+  A.score = score;
+  A.score_stride = score_stride;
+  A.budget = budget;
+  A.n_sink = n_sink;
+  A.n_recent = n_recent;
+  A.dst_table = dst_table;
+  A.dst_width = dst_width;
+  A.kept = kept_out;
+  A.len_out = len_out;
+  A.score_out = score_out;
+  A.score_out_stride = score_out_stride;
+  return ran(launch_evict(A, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,60 @@
+// Paged K/V cache: arguments its kernels share.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "bd_internal.h"
+
+namespace bd {
+
+// One layer's pool and one batch of requests, as include/blockdrafter.h defines them.
+struct PagedArgs {
+  const void *k, *v;
+  int64_t page_stride, head_stride, slot_stride;  // elements
+  int n_kv_heads, group, head_dim, page_size, n_pages;
+  int n_requests, table_width, n_rows, max_rows, max_len;
+  const int32_t *page_table, *seq_len, *row_start;
+  int window, n_sink;
+  float scale_log2;  // scale * log2(e): scores in log2 units
+  const void *q;
+  int64_t q_stride;
+};
+
+struct PagedAttnArgs {
+  PagedArgs p;
+  void *out;
+  int64_t out_stride;
+  float *lse;  // [n_rows][n_q_heads] or null
+};
+
+struct PagedWeightsArgs {
+  PagedArgs p;
+  const float *lse;
+  const int32_t *rows_used;  // or null
+  float decay;
+  const float *score_in;     // or null
+  float *score_out;
+  int64_t score_stride;
+};
+
+struct PagedEvictArgs {
+  PagedArgs p;
+  const float *score;
+  int64_t score_stride;
+  int budget, n_sink, n_recent;
+  const int32_t *dst_table;  // null: in place
+  int dst_width;
+  int32_t *kept, *len_out;
+  float *score_out;          // or null
+  int64_t score_out_stride;
+};
+
+std::string launch_paged_attention(const PagedAttnArgs &a, int dtype, cudaStream_t s);
+
+unsigned take_error_word_paged();
+unsigned take_error_word_paged_attn();
+
+}  // namespace bd

@@ -36,7 +36,7 @@
 extern "C" {
 #endif
 
-#define BD_ABI_VERSION 8
+#define BD_ABI_VERSION 9
 #define BD_MAX_LAYERS 16
 
 typedef enum {
@@ -51,7 +51,8 @@ typedef enum {
                                   way into an fp16 tensor-core operand (bd_sync_status)     */
 } bd_status;
 
-typedef enum { BD_BF16 = 0, BD_F32 = 1 } bd_dtype;
+/* BD_F16 is a type of the paged cache only (bd_paged_kv); draft configs refuse it. */
+typedef enum { BD_BF16 = 0, BD_F32 = 1, BD_F16 = 2 } bd_dtype;
 
 /* Block attention among the W block rows.  [DFlash-notes] is bidirectional;
  * [BlockCausal] lets row i see block rows 0..i only.  Context keys are unaffected. */
@@ -406,6 +407,137 @@ bd_status bd_refine_tail(const bd_config *cfg, const bd_weights *w, const float 
 bd_status bd_lm_head_argmax_noalloc(const bd_config *cfg, const bd_weights *w,
                                     const float *hidden, int rows, int32_t *token_out,
                                     float *max_logit_out, void *stream);
+
+/*
+ * ------------------------------------------------------------------ paged K/V cache
+ * The target's side of a speculative round: the cache that holds its context in pages, the
+ * attention that reads it, and the eviction that bounds it.  (The drafter's own context stays
+ * in the rings of bd_kv_cache.)  One call works on one layer's pool.
+ *
+ * Slots.  Request b holds seq_len[b] slots; slot j is row j mod page_size of page
+ * page_table[b][j / page_size].  Its rows of a call are row_start[b] .. row_start[b+1]-1 of the
+ * call's row tensors and are the LAST of its slots: with r rows, row i is slot
+ * p_i = seq_len[b] - r + i (seq_len counts the call's own rows; append before attending).
+ * Row i sees slot j iff
+ *     0 <= j <= p_i  and  (window == 0  or  j > p_i - window  or  j < n_sink):
+ * causal, optionally through a sliding window beside which the first n_sink slots stay visible.
+ * The window and the sinks count slots.  After an eviction slot numbers are no longer text
+ * positions (keys keep the rotation they were stored with).
+ *
+ * Values.  q, k, v and out have the pool's type; products accumulate in fp32, softmax statistics,
+ * lse and accumulated weights are fp32.  A slot that no row of the call sees is never used,
+ * whatever its page holds; a slot that a row does not see does not reach that row's results,
+ * even if it holds infinities or NaN.
+ *
+ * Lengths and page ids live on the device and are checked there: a request whose rows are not
+ * 0 <= row_start[b] <= row_start[b+1] <= n_rows with at most max_rows rows takes no part; one
+ * whose seq_len is negative or beyond max_len or its page_table row counts as empty; a page id
+ * outside the pool is not followed (the slot's values count as zero and nothing is stored
+ * there).  Each sets the device error word (bd_sync_status: BD_ERR_INVALID_ARG), and that
+ * request's results are unspecified.  Rows outside every request are left as they were.
+ *
+ * Tensors belong to the current device.  Errors: BD_ERR_INVALID_ARG (NULL, misaligned or
+ * overlapping arrays, sizes out of range), BD_ERR_UNSUPPORTED (type, head size),
+ * BD_ERR_WORKSPACE.  The workspace holds nothing between calls; calls that share one must be
+ * ordered on one stream.  No call synchronises, allocates or needs initialised scratch, and
+ * every call can be captured into a graph.  Results do not depend on the run (no atomics on
+ * floating-point values).
+ */
+#define BD_PAGED_MAX_REQUESTS 1024
+#define BD_PAGED_MAX_GROUP 128
+
+typedef struct {
+  int n_q_heads, n_kv_heads;  /* query heads h*G .. h*G+G-1 read KV head h, G = n_q / n_kv <= 128 */
+  int head_dim;               /* D: 64 or 128                                                     */
+  int dtype;                  /* BD_BF16 or BD_F16                                                */
+  int page_size;              /* slots per page, >= 1                                             */
+  int n_pages;                /* pages of the pool: valid page ids are 0 .. n_pages-1             */
+  int64_t page_stride;        /* elements between pages, KV heads and slots of the pool (each a   */
+  int64_t head_stride;        /*   multiple of 8; the D values of a slot are contiguous); the     */
+  int64_t slot_stride;        /*   same for k and v                                               */
+  void *k, *v;                /* dev pools, 16-byte aligned                                       */
+} bd_paged_kv;
+
+typedef struct {
+  int n_requests;             /* 1 .. BD_PAGED_MAX_REQUESTS                                       */
+  int table_width;            /* entries of one page_table row                                    */
+  int n_rows;                 /* rows of the call's row tensors (>= 0)                            */
+  int max_rows;               /* bound on the rows of any request (>= 0)                          */
+  int max_len;                /* bound on any seq_len                                             */
+  const int32_t *page_table;  /* dev [n_requests, table_width]                                    */
+  const int32_t *seq_len;     /* dev [n_requests]                                                 */
+  const int32_t *row_start;   /* dev [n_requests + 1]                                             */
+} bd_paged_batch;
+
+/* Bytes of workspace bd_paged_attention needs for a batch of up to n_requests requests of up
+ * to max_rows rows each.  Returns 0 for an invalid or unsupported kv. */
+size_t bd_paged_workspace_bytes(const bd_paged_kv *kv, int n_requests, int max_rows);
+
+/*
+ * Stores the rows' keys and values in their slots:  K[slot p_i] = k_new_i,  V[slot p_i] = v_new_i.
+ * Rows with p_i < 0 are not stored.  Two rows of a call must not share a slot.
+ *   k_new, v_new  dev [n_rows, n_kv_heads, D], rows k_stride / v_stride elements apart (multiples
+ *                 of 8), 16-byte aligned (views into a wider projection output will do)
+ */
+bd_status bd_paged_append(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *k_new,
+                          int64_t k_stride, const void *v_new, int64_t v_stride, void *stream);
+
+/*
+ * Attention of the rows over their requests' slots:
+ *   s_ij = scale * q_i . k_j ;  out_i = sum_j softmax_j(s_ij) v_j ;  lse_i = log sum_j exp(s_ij)
+ * over the slots j that row i sees.  A row that sees none gets out = 0 and lse = -inf.  One row
+ * per request is plain decoding, K+1 rows verify a drafted block, longer ones are prompt chunks.
+ *   q, out  dev [n_rows, n_q_heads, D], rows q_stride / out_stride elements apart (multiples of
+ *           8), 16-byte aligned; they must not overlap each other
+ *   lse     dev fp32 [n_rows, n_q_heads] OUT (natural logarithm), or NULL
+ *   window  0 = none;  n_sink >= 0;  scale > 0, finite
+ */
+bd_status bd_paged_attention(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *q,
+                             int64_t q_stride, void *out, int64_t out_stride, float *lse,
+                             int window, int n_sink, float scale, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * Accumulated attention weights, the score an eviction goes by: for every slot j < seq_len[b]
+ *   score_out[b][j] = decay * score_in[b][j] + sum_i sum_h exp(s_ijh - lse_ih)
+ * over all query heads h and the first rows_used[b] rows i of the request that see slot j (a
+ * verification's accepted rows; lse as bd_paged_attention gave it, so that each row and head
+ * spreads a weight of one).  Entries at or behind seq_len[b] are left as they were.
+ *   q          dev [n_rows, n_q_heads, D] as in bd_paged_attention;  lse dev fp32 [n_rows, n_q_heads]
+ *   rows_used  dev int32 [n_requests], clamped to 0 .. the request's rows; NULL = all rows
+ *   score_in   dev fp32 [n_requests, score_stride], or NULL for zero;  decay finite
+ *   score_out  dev fp32 [n_requests, score_stride] OUT; score_in itself, or not overlapping it
+ *   score_stride >= max_len
+ */
+bd_status bd_paged_weights(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *q,
+                           int64_t q_stride, const float *lse, const int32_t *rows_used, int window,
+                           int n_sink, float scale, float decay, const float *score_in,
+                           float *score_out, int64_t score_stride, void *stream);
+
+/*
+ * Eviction by accumulated weight.  A request of n = seq_len[b] slots keeps all of them if
+ * n <= budget; else the first n_sink, the last n_recent and, of those between, the
+ * budget - n_sink - n_recent slots of the largest score (equal scores: the lower slot; NaN
+ * counts as -inf).  The kept slots move, in their order, to slots 0, 1, ... of the request:
+ *   slot i <- old slot kept_out[b][i],  score_out[b][i] = score[b][kept_out[b][i]],  i < len_out[b]
+ * Entries of kept_out and score_out at or behind len_out[b] are left as they were, but with
+ * score_out = score those of the slots given up become zero (slots filled later start from there).
+ * The batch's rows (row_start, n_rows, max_rows) are not looked at; row_start may be NULL.
+ *   score      dev fp32 [n_requests, score_stride], score_stride >= max_len
+ *   budget     >= 1, n_sink + n_recent <= budget
+ *   dst_table  dev int32 [n_requests, dst_width]: pages of the same pool that take the kept slots
+ *              (dst_width * page_size >= min(budget, max_len)), none of them a page that any
+ *              request of the call reads; or NULL: in place, in the pages of page_table, of which
+ *              a request that loses slots must not share any it moves slots in
+ *   kept_out   dev int32 [n_requests, budget] OUT (ascending)
+ *   len_out    dev int32 [n_requests] OUT; may be seq_len itself
+ *   score_out  dev fp32 [n_requests, score_out_stride] OUT (score_out_stride >= min(budget,
+ *              max_len)); or NULL; may be score itself, with the same stride
+ */
+bd_status bd_paged_evict(const bd_paged_kv *kv, const bd_paged_batch *batch, const float *score,
+                         int64_t score_stride, int budget, int n_sink, int n_recent,
+                         const int32_t *dst_table, int dst_width, int32_t *kept_out,
+                         int32_t *len_out, float *score_out, int64_t score_out_stride, void *stream);
 
 /*
  * Measurement hook (no counterpart in the papers): brackets single kernel launches with

@@ -1,0 +1,473 @@
+"""Paged cache on the GPU against the fp64 oracle: append, attention, accumulated weights,
+eviction, and a run of them together.  Every place no request holds is NaN in the pools."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as P
+from paged_harness import TYPES, PagedCase
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_drafter_gb300 import builder
+    builder.build()
+
+
+def sync():
+    from block_drafter_gb300 import binding
+    binding.sync_status()
+
+
+# ------------------------------------------------------------------ attention
+ATTENTION = {
+    "one_slot": PagedCase((1,), (1,)),
+    "one_token_each": PagedCase((1, 2, 15, 16, 17, 63, 64, 65), (1,) * 8),
+    "ragged": PagedCase((5, 130, 700, 257, 1), (1, 3, 2, 1, 1), lead=2),
+    "fp16_d64": PagedCase((33, 400, 1000), (1, 1, 1), d=64, dtype="fp16", group=1, hkv=3),
+    "long": PagedCase((5000, 4097), (1, 1), hkv=1, group=8),
+    "wide_group": PagedCase((300, 77), (1, 2), hkv=1, group=32),
+    "widest_group": PagedCase((200, 40), (2, 1), hkv=1, group=128, d=64),
+    "odd_group": PagedCase((100, 321), (3, 5), group=5, hkv=2),
+    "block": PagedCase((600, 16, 1111), (16, 16, 16)),
+    "block_window": PagedCase((600, 40, 1111), (16, 7, 13), window=64, n_sink=4),
+    "window_token": PagedCase((600, 40, 1111, 3), (1, 1, 1, 1), window=100, n_sink=3),
+    "window_no_sinks": PagedCase((601, 40), (1, 2), window=17),
+    "window_one": PagedCase((300, 20), (2, 1), window=1),
+    "window_one_sink": PagedCase((300, 20), (2, 18), window=1, n_sink=1),
+    "sinks_reach_window": PagedCase((90, 300), (4, 4), window=50, n_sink=60),
+    "sinks_beyond_length": PagedCase((50, 300), (4, 40), window=8, n_sink=1000),
+    "window_beyond_length": PagedCase((50, 130), (4, 40), window=5000, n_sink=2),
+    "page_1": PagedCase((37, 129), (1, 9), page=1),
+    "page_odd": PagedCase((37, 200, 66), (1, 9, 33), page=33),
+    "page_256": PagedCase((300, 257), (1, 40), page=256),
+    "nhd_pool": PagedCase((137, 256), (1, 20), nhd=True),
+    "padded": PagedCase((137, 250), (1, 20), pad=8, lead=3),
+    "nhd_padded_fp16": PagedCase((137, 250), (30, 20), pad=8, nhd=True, dtype="fp16", d=64),
+    "chunk": PagedCase((300, 64), (130, 64)),
+    "chunk_whole": PagedCase((333,), (333,), hkv=1),
+    "chunk_mha": PagedCase((333, 129), (200, 129), hkv=3, group=1),
+    "chunk_fp16_d64": PagedCase((400, 255), (257, 255), d=64, dtype="fp16", lead=5),
+    "chunk_window": PagedCase((700, 300), (300, 130), window=128, n_sink=4),
+    "chunk_window_odd": PagedCase((701, 299), (301, 299), window=77, n_sink=130, group=3),
+    "chunk_and_tokens": PagedCase((500, 20, 1, 900, 40), (200, 1, 1, 1, 39)),
+    "more_rows_than_slots": PagedCase((5, 0, 100), (9, 3, 120), lead=1),
+    "empty_requests": PagedCase((0, 50, 20, 0), (0, 0, 2, 1)),
+    "peaked": PagedCase((400, 130), (1, 60), std=12.0),
+    "peaked_fp16": PagedCase((400, 130), (1, 60), std=12.0, dtype="fp16"),
+    "table_has_spare_entries": PagedCase((40, 90), (1, 50), spare=5),
+}
+
+
+@pytest.mark.parametrize("name", list(ATTENTION))
+def test_attention_matches_the_oracle(name):
+    c = ATTENTION[name].build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    c.check_guards(out, lse)
+    again, lse2 = c.attend()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)   # nothing depends on the run
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128])
+@pytest.mark.parametrize("d,group", [(128, 4), (64, 1)])
+def test_attention_of_every_row_count(rows, d, group):
+    c = PagedCase((rows + 150, 129 + rows), (rows, rows), d=d, group=group, hkv=1, seed=rows).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+
+
+def test_attention_without_lse_and_with_a_scale():
+    c = PagedCase((90, 200), (1, 40)).build()
+    c.scale = 0.3
+    out, lse = c.attend(scale=0.3)
+    c.check_attention(out, lse)
+    alone, _ = c.outputs()
+    c.cache.attention(c.batch, c.qd, alone, scale=0.3)
+    sync()
+    assert torch.equal(alone, out)
+
+
+@pytest.mark.parametrize("rows,window", [(1, 0), (4, 0), (4, 20), (100, 0), (100, 40)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_garbage_in_slots_a_row_does_not_see_stays_out(rows, window, bad):
+    """Slots of later rows, and slots the window hides from later rows, hold infinities or NaN:
+    only the rows that see them may show it."""
+    c = PagedCase((260, 300), (rows, rows), window=window, n_sink=2, hkv=1).build()
+    hit = [c.lens[0] - 1]                       # the last row's own slot: earlier rows do not see it
+    if window:
+        hit.append(c.lens[0] - rows - window + 1)   # seen by the first row alone
+    for j in hit:
+        page = c.table[0, j // c.page].item()
+        c.vd[page, 0, j % c.page, 3] = bad
+    out, lse = c.attend()
+    sync()
+    got = out[:rows].double().cpu().numpy()
+    see = P.visible(c.lens[0], rows, window, 2)
+    for i in range(rows):
+        touched = any(see[i, j] for j in hit)
+        fine = np.ones((c.group, c.d), bool)
+        fine[:, 3] = not touched
+        assert (np.isfinite(got[i]) == fine).all(), i
+    clean = PagedCase((260, 300), (rows, rows), window=window, n_sink=2, hkv=1).build()
+    ref, lref = clean.attend()
+    keep = torch.ones_like(ref, dtype=torch.bool)
+    keep[:rows, :, 3] = torch.tensor([[not any(see[i, j] for j in hit)] for i in range(rows)], device="cuda")
+    torch.testing.assert_close(out[keep].float(), ref[keep].float(), rtol=2 ** -6, atol=2 ** -7)
+    assert torch.equal(lse, lref)
+
+
+def test_bad_keys_in_unseen_slots_stay_out():
+    c = PagedCase((200,), (3,), hkv=1).build()
+    c.kd[c.table[0, 199 // 16].item(), 0, 199 % 16] = float("nan")
+    out, lse = c.attend()
+    sync()
+    assert torch.isfinite(out[:2]).all() and torch.isfinite(lse[:2]).all() and torch.isnan(out[2]).all()
+
+
+def test_bad_sizes_and_pages_are_reported_and_other_requests_stand():
+    from block_drafter_gb300 import binding as B
+    for spoil in ("page", "negative_page", "length", "negative_length", "rows", "rows_out"):
+        c = PagedCase((200, 100, 70), (2, 3, 1)).build()
+        if spoil == "page":
+            c.table[1, 6] = 10 ** 6                             # slots 96 .. 99
+        elif spoil == "negative_page":
+            c.table[1, 6] = -1
+        elif spoil == "length":
+            c.lend[1] = 201
+        elif spoil == "negative_length":
+            c.lend[1] = -5
+        elif spoil == "rows":
+            c.startd.copy_(torch.tensor([0, 4, 2, 6]))         # request 1 ends before it begins
+        else:
+            c.startd.copy_(torch.tensor([0, 2, 5, 600]))       # request 2 goes beyond the rows
+        out, lse = c.attend()
+        with pytest.raises(B.BdError) as err:
+            B.sync_status()
+        assert err.value.status == -1
+        B.sync_status()
+        if spoil not in ("rows", "rows_out"):
+            c.check_attention(out, lse, requests=(0, 2))
+        elif spoil == "rows_out":
+            c.check_attention(out, lse, requests=(0, 1))
+        k = torch.randn(c.n_rows, c.hkv, c.d, device="cuda").to(torch.bfloat16)
+        before = c.kd.clone()
+        c.cache.append(c.batch, k, k)
+        with pytest.raises(B.BdError):
+            B.sync_status()
+        changed = (c.kd.view(torch.int16) != before.view(torch.int16)).flatten(2).any(2).any(1).sum().item()
+        assert changed <= 5
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("case", [PagedCase((1,), (1,)), PagedCase((17, 300, 64), (1, 16, 64), lead=2),
+                                  PagedCase((5, 0, 9), (9, 2, 0), page=4),
+                                  PagedCase((700, 33), (700, 33), page=33, dtype="fp16", d=64, pad=8, nhd=True),
+                                  PagedCase((3000,), (2900,), hkv=8, page=64)])
+def test_append_stores_the_rows_and_nothing_else(case):
+    c = case.build()
+    g = torch.Generator().manual_seed(5)
+    new = [torch.randn(c.n_rows, c.hkv, c.d, generator=g).to(TYPES[c.dtype]) for _ in range(2)]
+    want = [c.kd.cpu().clone(), c.vd.cpu().clone()]
+    for b, (n, r) in enumerate(zip(c.lens, c.rows)):
+        for i in range(r):
+            p = n - r + i
+            if p >= 0:
+                for w, x in zip(want, new):
+                    w[c.table[b, p // c.page].item(), :, p % c.page] = x[c.starts[b] + i]
+    c.cache.append(c.batch, c.strided(new[0]), c.strided(new[1]))
+    sync()
+    for got, w in zip((c.kd, c.vd), want):
+        assert torch.equal(got.cpu().contiguous().view(torch.int16), w.contiguous().view(torch.int16))
+
+
+# ------------------------------------------------------------------ weights
+WEIGHTS = {
+    "token": (PagedCase((1, 40, 700), (1, 1, 1)), None),
+    "block_accepted": (PagedCase((60, 300, 90), (16, 16, 16), lead=1), (16, 3, 0)),
+    "accepted_out_of_range": (PagedCase((60, 300), (5, 6)), (-3, 99)),
+    "window": (PagedCase((400, 90), (9, 40), window=50, n_sink=3), None),
+    "prompt": (PagedCase((300, 129), (200, 129), d=64, dtype="fp16", hkv=3, group=2), None),
+    "more_rows_than_slots": (PagedCase((5, 20), (9, 1)), None),
+    "wide_group": (PagedCase((200,), (3,), hkv=1, group=40), None),
+    "odd_pages": (PagedCase((100, 77), (2, 5), page=7, nhd=True, pad=8), None),
+    "peaked": (PagedCase((333,), (33,), std=8.0), None),
+}
+
+
+@pytest.mark.parametrize("inout", [False, True])
+@pytest.mark.parametrize("name", list(WEIGHTS))
+def test_weights_match_the_oracle(name, inout):
+    case, used = WEIGHTS[name]
+    c = case.build()
+    _, lse = c.attend()
+    B, width = len(c.lens), c.max_len + 3
+    g = torch.Generator().manual_seed(3)
+    start = torch.rand(B, width, generator=g).cuda()
+    score = start.clone() if inout else torch.full((B, width), -7.0, device="cuda")
+    ud = None if used is None else torch.tensor(used, dtype=torch.int32, device="cuda")
+    kw = dict(rows_used=ud, window=c.window, n_sink=c.n_sink)
+    c.cache.weights(c.batch, c.qd, lse, score, score_in=score if inout else None, decay=0.75, **kw)
+    sync()
+    got, lse = score.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, (n, r) in enumerate(zip(c.lens, c.rows)):
+        s = slice(c.starts[b], c.starts[b] + r)
+        w = P.weights(c.qf[s], c.k[b], lse[s], r if used is None else used[b], c.window, c.n_sink, c.scale)
+        _, _, _, size = P.attention(c.qf[s], c.k[b], c.v[b], c.window, c.n_sink, c.scale)
+        # scores off by ds as in the attention (their size S; the lse adds |lse| <= S + log n to what
+        # is rounded), weights by a relative 1.01 ds, sums of the rows and heads by 2^-23 each
+        S = size.max() if size.size else 0.0
+        ds = c.d * 2.0 ** -23 * S + (2 * S + np.log(n + 1) + 8) * 2.0 ** -22
+        base = 0.75 * start[b, :n].double().cpu().numpy() if inout else 0.0
+        tol = (1.01 * ds + (r * c.hkv * c.group + 32) * 2.0 ** -23) * w + 2.0 ** -22 * base + 2.0 ** -100
+        assert (np.abs(got[b, :n] - (base + w)) <= tol).all(), b
+        rest = start[b, n:].double().cpu().numpy() if inout else -7.0
+        assert (got[b, n:] == rest).all()
+
+
+# ------------------------------------------------------------------ eviction
+def _scores(kind, B, n, g):
+    s = torch.randn(B, n, generator=g)
+    if kind == "ties":
+        s = torch.randint(0, 3, (B, n), generator=g).float()
+    elif kind == "same":
+        s = torch.zeros(B, n)
+        s[:, ::2] = -0.0
+    elif kind == "odd":
+        s = s.exp()
+        s[:, ::5], s[:, 1::7], s[:, 2::11] = float("nan"), float("-inf"), float("inf")
+    elif kind == "tiny":
+        s = s * 1e-42
+    return s
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("kind", ["normal", "ties", "same", "odd", "tiny"])
+@pytest.mark.parametrize("lens,budget,sink,recent,page", [
+    ((50, 20, 7), 20, 2, 5, 16), ((300, 129, 1, 0), 128, 4, 32, 16), ((65, 64), 1, 0, 0, 16), ((65, 64), 1, 1, 0, 7),
+    ((65, 64), 1, 0, 1, 1), ((2500, 1025, 3000), 1024, 4, 1020, 64), ((4000,), 2000, 0, 0, 33), ((40, 30), 50, 10, 10, 16),
+    ((1500, 1300), 1299, 64, 100, 256)])
+def test_eviction_keeps_what_the_oracle_keeps(lens, budget, sink, recent, page, kind, in_place):
+    c = PagedCase(lens, (0,) * len(lens), page=page, hkv=2, d=64 if page == 7 else 128, spare=1).build()
+    g = torch.Generator().manual_seed(budget + sink)
+    B, n = len(lens), max(lens)
+    host = _scores(kind, B, n + 2, g)
+    score, most = host.cuda(), min(budget, n)
+    kept = torch.full((B, budget), -9, dtype=torch.int32, device="cuda")
+    new_len = torch.full((B,), -9, dtype=torch.int32, device="cuda")
+    before = [c.kd.cpu().clone(), c.vd.cpu().clone()]
+    table, dst, out, k, v = c.table, None, score, c.kd, c.vd
+    if not in_place:  # other pages of the same pool: the pool of a second set of pages behind it
+        cols, total = -(-most // page), c.kd.shape[0]
+        k, v = (torch.cat([x.contiguous(), torch.full((B * cols,) + x.shape[1:], float("nan"), dtype=x.dtype, device="cuda")])
+                for x in (c.kd, c.vd))
+        dst = (total + torch.randperm(B * cols, generator=g)).int().reshape(B, cols).cuda()
+        out = torch.full((B, most + 1), -9.0, device="cuda")
+        c.cache = type(c.cache)(k, v, n_q_heads=c.hkv * c.group)
+        c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, 0, c.max_len)
+        table = dst
+    c.cache.evict(c.batch, score, budget, kept, new_len, n_sink=sink, n_recent=recent, dst_table=dst, score_out=out)
+    sync()
+    for b in range(B):
+        ids = P.evict(host[b].numpy(), lens[b], budget, sink, recent)
+        m = len(ids)
+        assert new_len[b].item() == m and kept[b, :m].tolist() == ids and (kept[b, m:] == -9).all()
+        i = torch.arange(m)
+        np.testing.assert_array_equal(out[b, :m].cpu().numpy(), host[b, ids].numpy())
+        if not in_place:
+            assert (out[b, m:] == -9).all()
+        else:
+            assert (out[b, m:lens[b]] == 0).all()
+            np.testing.assert_array_equal(out[b, lens[b]:].cpu().numpy(), host[b, lens[b]:].numpy())
+        for pool, was in zip((k, v), before):
+            old = torch.tensor(ids, dtype=torch.long)
+            want = was[c.table[b].cpu().long()[old // page], :, old % page]
+            got = pool.cpu()[table[b].cpu().long()[i // page], :, i % page]
+            assert torch.equal(got.contiguous().view(torch.int16), want.contiguous().view(torch.int16)), b
+    if not in_place:
+        total = before[0].shape[0]
+        for pool, was in zip((k, v), before):   # the pages read are as they were
+            assert torch.equal(pool[:total].cpu().view(torch.int16), was.contiguous().view(torch.int16))
+
+
+def test_eviction_writes_the_new_lengths_over_the_old():
+    c = PagedCase((90, 30, 200), (0, 0, 0)).build()
+    score = torch.rand(3, 200, device="cuda")
+    kept = torch.zeros(3, 50, dtype=torch.int32, device="cuda")
+    c.cache.evict(c.batch, score, 50, kept, c.lend, n_recent=10)
+    sync()
+    assert c.lend.tolist() == [50, 30, 50]
+
+
+# ------------------------------------------------------------------ together
+def _step(c, k, v, out, lse, score, accepted):
+    c.cache.append(c.batch, k, v)
+    c.cache.attention(c.batch, c.qd, out, lse=lse)
+    c.cache.weights(c.batch, c.qd, lse, score, score_in=score, rows_used=accepted)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_a_run_of_steps_with_evictions(rows, graph):
+    """Several steps of append, attention and accumulation, then an eviction in place, against the
+    oracle on a growing and shrinking list of slots; captured once and replayed in one variant."""
+    c = PagedCase((rows + 50, rows + 131, rows), (rows, rows, rows), hkv=2, spare=40).build()
+    B, width, t = 3, c.table.shape[1] * c.page, TYPES[c.dtype]
+    total = B * c.table.shape[1]
+    ids = torch.randperm(total, generator=torch.Generator().manual_seed(1)).int().reshape(B, -1).cuda()
+    c.table.copy_(ids)
+    k_pool = torch.full((total, c.hkv, c.page, c.d), float("nan"), dtype=t, device="cuda")
+    v_pool = k_pool.clone()
+    hist = []
+    for b in range(B):
+        n = c.lens[b] - rows
+        kb, vb = (torch.from_numpy(x[b][:n]).to(t) for x in (c.k, c.v))
+        j = torch.arange(n)
+        for pool, x in ((k_pool, kb), (v_pool, vb)):
+            pool[c.table[b].cpu().long()[j // c.page].cuda(), :, (j % c.page).cuda()] = x.cuda()
+        hist.append([kb.double().numpy(), vb.double().numpy(), np.zeros(n)])
+    c.cache = type(c.cache)(k_pool, v_pool, n_q_heads=c.hkv * c.group)
+    c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, rows, width)
+    k = torch.empty(c.n_rows, c.hkv, c.d, dtype=t, device="cuda")
+    v, q = torch.empty_like(k), c.qd
+    out, lse = c.outputs()
+    score = torch.zeros(B, width, device="cuda")
+    accepted = torch.full((B,), rows, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(B, 90, dtype=torch.int32, device="cuda")
+    lens = [c.lens[b] - rows for b in range(B)]
+    g = torch.Generator().manual_seed(9)
+    run = None
+    for step in range(4):
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, generator=g).to(t))
+        for b in range(B):
+            lens[b] += rows
+        c.lend.copy_(torch.tensor(lens, dtype=torch.int32))
+        if not graph:
+            _step(c, k, v, out, lse, score, accepted)
+        else:
+            if run is None:
+                run = torch.cuda.CUDAGraph()
+                torch.cuda.synchronize()
+                with torch.cuda.graph(run):
+                    _step(c, k, v, out, lse, score, accepted)
+            run.replay()
+        sync()
+        c.lens, c.qf = tuple(lens), q.double().cpu().numpy()
+        for b in range(B):
+            s = slice(c.starts[b], c.starts[b] + rows)
+            hist[b][0] = np.concatenate([hist[b][0], k[s].double().cpu().numpy()])
+            hist[b][1] = np.concatenate([hist[b][1], v[s].double().cpu().numpy()])
+            _, l, _, _ = P.attention(c.qf[s], hist[b][0], hist[b][1], 0, 0, c.scale)
+            w = P.weights(c.qf[s], hist[b][0], l, rows, 0, 0, c.scale)
+            hist[b][2] = np.concatenate([hist[b][2], np.zeros(rows)]) + w
+            np.testing.assert_allclose(score[b, :lens[b]].cpu().numpy(), hist[b][2], rtol=1e-4, atol=1e-6)
+        c.k, c.v = [h[0] for h in hist], [h[1] for h in hist]
+        c.check_attention(out, lse)
+        if step % 2:
+            host = score.cpu().numpy()
+            c.cache.evict(c.batch, score, 90, kept, c.lend, n_sink=2, n_recent=20, score_out=score)
+            sync()
+            for b in range(B):
+                stay = P.evict(host[b], lens[b], 90, 2, 20)
+                hist[b] = [h[stay] for h in hist[b]]
+                lens[b] = len(stay)
+                hist[b][2] = host[b][stay].astype(np.float64)
+            assert c.lend.tolist() == lens
+
+
+def test_two_streams_with_their_own_workspaces_and_two_graphs_sharing_one():
+    c = PagedCase((700, 300), (1, 1), hkv=2).build()
+    d = PagedCase((260, 500), (40, 60), hkv=2, seed=4).build()
+    want = [x.attend() for x in (c, d)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [c.outputs(), d.outputs()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, s, (o, l) in zip((c, d), streams, got):
+            x.cache.attention(x.batch, x.qd, o, lse=l, stream=s)
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+    big = max((c.batch, d.batch), key=lambda x: x.ws_bytes).workspace
+    graphs = []
+    for x in (c, d):
+        x.batch = x.cache.batch(x.table, x.lend, x.startd, x.n_rows, x.max_rows, x.max_len, workspace=big)
+        gr = torch.cuda.CUDAGraph()
+        o, l = x.outputs()
+        with torch.cuda.graph(gr):
+            x.cache.attention(x.batch, x.qd, o, lse=l)
+        graphs.append((gr, o, l))
+    for _ in range(3):
+        for gr, o, l in graphs:
+            o.fill_(0)
+            gr.replay()
+        for (gr, o, l), (wo, wl) in zip(graphs, want):
+            torch.cuda.synchronize()
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+    sync()
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes and more than 2^31 elements per pool side: the request's pages
+    lie at its far end."""
+    page, hkv, d = 64, 8, 128
+    n_pages = (1 << 32) // (page * hkv * d) + 8          # just over 2^32 elements
+    k = torch.empty(n_pages, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    c = PagedCase((200, 130), (1, 20), hkv=hkv, group=1, page=page).build()
+    held = [-(-n // page) for n in c.lens]
+    far = torch.arange(n_pages - 7, n_pages, device="cuda", dtype=torch.int32)
+    table = torch.zeros_like(c.table)
+    at = 0
+    for b, h in enumerate(held):
+        for i in range(h):
+            k[far[at].item()] = c.kd[c.table[b, i].item()]
+            v[far[at].item()] = c.vd[c.table[b, i].item()]
+            table[b, i] = far[at]
+            at += 1
+    c.cache = type(c.cache)(k, v, n_q_heads=hkv)
+    c.batch = c.cache.batch(table, c.lend, c.startd, c.n_rows, c.max_rows, c.max_len)
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    new = torch.randn(c.n_rows, hkv, d, device="cuda").to(torch.bfloat16)
+    c.cache.append(c.batch, new, new)
+    sync()
+    assert torch.equal(k[table[1, 2].item(), :, 1], new[20])
+    score, kept = torch.rand(2, 200, device="cuda"), torch.zeros(2, 100, dtype=torch.int32, device="cuda")
+    c.cache.evict(c.batch, score, 100, kept, c.lend)
+    sync()
+    assert c.lend.tolist() == [100, 100]
+
+
+def test_python_checks():
+    from block_drafter_gb300.paged import PagedCache
+    c = PagedCase((40, 50), (1, 2)).build()
+    out, lse = c.outputs()
+    for bad in (c.qd.float(), c.qd[:2], c.qd[:, :3], c.qd.transpose(1, 2)):
+        with pytest.raises(ValueError):
+            c.cache.attention(c.batch, bad, out)
+    with pytest.raises(ValueError):
+        c.cache.attention(c.batch, c.qd, out, lse=lse.double())
+    with pytest.raises(ValueError):
+        c.cache.attention(c.batch, c.qd.cpu(), out)
+    with pytest.raises(RuntimeError, match="overlap"):
+        c.cache.attention(c.batch, c.qd, c.qd)
+    with pytest.raises(ValueError):
+        c.cache.batch(c.table.long(), c.lend, c.startd, 3, 2, 50)
+    with pytest.raises(ValueError):
+        c.cache.batch(c.table, c.lend, None, 3, 2, 50)
+    with pytest.raises(RuntimeError, match="max_len"):
+        t = c.cache.batch(c.table, c.lend, c.startd, 3, 2, 10 ** 6)
+        c.cache.attention(t, c.qd, out)
+    with pytest.raises(ValueError):
+        c.cache.evict(c.batch, lse, 10, c.table, c.lend)
+    with pytest.raises(RuntimeError, match="workspace"):
+        t = c.cache.batch(c.table, c.lend, c.startd, 3, 2, 50, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        c.cache.attention(t, c.qd, out)
+    assert isinstance(c.cache, PagedCache)
