@@ -28,7 +28,17 @@ struct PagedAttnArgs {
   void *out;
   int64_t out_stride;
   float *lse;  // [n_rows][n_q_heads] or null
+  // workspace: the units before each request [n_requests + 1], then the parts of split items
+  int64_t *unit_start;
+  float *part_o;   // [2 * n_ctas][part_rows][head_dim] unnormalised sums
+  float2 *part_ml; // [2 * n_ctas][part_rows] (reference, row sum), reference in log2 units
+  int n_ctas;
 };
+
+// Query rows (of one KV head) a block of the few-rows attention takes.
+constexpr int kFewRows = 16;
+// Blocks of the few-rows attention: two on every SM.
+inline int few_ctas() { return 2 * num_sms(); }
 
 struct PagedWeightsArgs {
   PagedArgs p;
@@ -52,6 +62,9 @@ struct PagedEvictArgs {
   int64_t score_out_stride;
 };
 
+size_t paged_attention_bytes(int n_requests, int max_rows, int group, int head_dim);
+// Splits `workspace` (paged_attention_bytes) into the fields of A.
+void paged_attention_carve(PagedAttnArgs &A, void *workspace);
 std::string launch_paged_attention(const PagedAttnArgs &a, int dtype, cudaStream_t s);
 
 unsigned take_error_word_paged();

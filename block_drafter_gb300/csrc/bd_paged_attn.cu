@@ -1,17 +1,37 @@
 // Attention of a call's rows over their requests' paged slots (bd_paged_attention).
 //
-// One warp per (row, query head): it walks the slots the row sees 32 at a time -- each lane
-// forms one slot's score, the warp keeps the running maximum m and sum l of exp2(s - m), and each
-// lane adds the 32 weighted values of its own D/32 columns:
+// One pass over the keys and values with the running maximum m and sum l of a softmax:
 //   m' = max(m, max s),  l' = l 2^(m-m') + sum 2^(s-m'),  o' = o 2^(m-m') + sum 2^(s-m') v
+// (scores s in log2 units), and parts over different slots joined by the same rule.
+//
+// attention_few: calls whose rows of one KV head (rows x group) are at most kFewRows = 16 --
+// decoding and short blocks.  Bound by the bytes of K and V, so it is built to keep loads in
+// flight.  The work of a call is a list of units of 16 slots, ordered by request, KV head and
+// slot; the blocks (two an SM) take equal shares of it whatever the lengths are, so that one long
+// request spreads over all SMs and short ones share a block.  Inside a block every warp works alone:
+// it takes every fourth unit of the block's share, copies the unit's K and V rows page by page into
+// its own shared memory with cp.async (kStages units deep, no barrier between warps), and feeds
+// mma.sync m16n8k16 from there (the tensor work is small: tcgen05's 128-row tiles would be 7/8
+// padding).  The warps join at the end of each (request, KV head); heads that several blocks worked
+// on are joined by attention_join from fp32 parts in the workspace.
+//
+// The weights enter the second product as a 16-bit high part and a 16-bit rest: the rounding to
+// 16 bits (2^-9 relative, as large as the output's own) then disappears from the result.  With at
+// most 8 rows the rest takes the idle upper 8 rows of the product and costs nothing.
 #include "bd_paged_device.cuh"
 
 namespace bd {
 
 BD_DEFINE_ERROR_TAKER(take_error_word_paged_attn)
 
+// One row of one query head by one warp, over exactly the slots it sees: each lane forms one
+// slot's score, then adds the 32 weighted values of its own D/32 columns.  The tiled kernels
+// multiply hidden slots by a zero weight, which an infinity or NaN among the hidden values turns
+// into NaN; they send a row whose result is not finite through here (its lse is
+// right already: a hidden slot's score is dropped, not multiplied).
 template <typename T, int D>
-__device__ void attend_row(const PagedAttnArgs &A, const Request &rq, int b, int i, int head, float *qs, int lane) {
+__device__ __noinline__ void attend_row(const PagedAttnArgs &A, const Request &rq, int b, int i, int head, float *qs, int lane,
+                                        bool write_lse) {
   const PagedArgs &a = A.p;
   const int hq = a.n_kv_heads * a.group, row = rq.row0 + i, p = rq.n - rq.rows + i;
   const T *q = static_cast<const T *>(a.q) + row * a.q_stride + head * D;
@@ -67,11 +87,466 @@ __device__ void attend_row(const PagedAttnArgs &A, const Request &rq, int b, int
   T *out = static_cast<T *>(A.out) + row * A.out_stride + head * D;
 #pragma unroll
   for (int c = 0; c < C; ++c) out[c * 32 + lane] = from_f<T>(l == 0.f ? 0.f : o[c] / l);
-  if (A.lse && lane == 0)
+  if (write_lse && A.lse && lane == 0)
     A.lse[static_cast<int64_t>(row) * hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
   __syncwarp();
 }
 
+// ------------------------------------------------------------------ few rows: layout
+constexpr int kUnit = 16;  // slots of a unit
+constexpr int kFewWarps = 4;
+constexpr int kFewThreads = 32 * kFewWarps;
+template <int D> struct Few {
+  static constexpr int kRowBytes = 2 * D;
+  static constexpr int kTile = kUnit * kRowBytes;       // K (or V) of a unit
+  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kWarpBytes = kStages * 2 * kTile;  // 24 KB / 20 KB
+  static constexpr int kSmem = kFewWarps * kWarpBytes;
+};
+// Weights are formed against 2^-kHead of the maximum: fp16 keeps small ones above its subnormals.
+template <typename T> struct Head { static constexpr float k = 0.f; };
+template <> struct Head<__half> { static constexpr float k = 12.f; };
+
+// The slots some row of a request sees, as tiles of kUnit: the sinks' tiles, then those from the
+// earliest row's window on.
+struct Tiles {
+  int sinks, first, count;  // tiles of sinks, first tile behind them, tiles in all
+  __device__ int at(int t) const { return t < sinks ? t : first + t - sinks; }
+};
+__device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq) {
+  Tiles t = {0, 0, 0};
+  if (rq.rows == 0 || rq.n == 0) return t;
+  const int first = window_first(a, max(0, rq.n - rq.rows));
+  t.first = first / kUnit;
+  t.sinks = min((min(a.n_sink, first) + kUnit - 1) / kUnit, t.first);
+  t.count = t.sinks + (rq.n + kUnit - 1) / kUnit - t.first;
+  return t;
+}
+
+// Share of block g among `ctas` blocks of `units` units.
+__device__ __forceinline__ int64_t share_begin(int64_t units, int ctas, int g) { return units * g / ctas; }
+__device__ __forceinline__ int ctas_used(int64_t units, int most) {
+  const int64_t c = (units + kFewWarps - 1) / kFewWarps;
+  return c < 1 ? 1 : static_cast<int>(c < most ? c : most);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Writes rows r0.. of an item: output row r = token r / group, head r % group of KV head h.
+template <typename T>
+__device__ __forceinline__ void store4(const PagedAttnArgs &A, const Request &rq, int h, int r, int d, float4 o, float inv) {
+  const int g = A.p.group, i = r / g, head = h * g + r - i * g;
+  T *out = static_cast<T *>(A.out) + (rq.row0 + i) * A.out_stride + head * A.p.head_dim + d;
+  *reinterpret_cast<uint2 *>(out) = make_uint2(Pair<T>::pack(o.x * inv, o.y * inv), Pair<T>::pack(o.z * inv, o.w * inv));
+}
+__device__ __forceinline__ void store_lse(const PagedAttnArgs &A, const Request &rq, int h, int r, float m, float l) {
+  if (!A.lse) return;
+  const int g = A.p.group, i = r / g, head = h * g + r - i * g;
+  A.lse[static_cast<int64_t>(rq.row0 + i) * A.p.n_kv_heads * g + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+}
+
+// The part of one (request, KV head) over tiles [t0, t1) by one warp (every kFewWarps-th tile):
+// o, m, l of its rows.  HALF: at most 8 rows; rows 8..15 of the second product carry the rest of
+// the weights.  Row r of the fragment (lane / 4, and + 8) is token r / group.
+template <typename T, int D, bool HALF>
+struct FewWarp {
+  static constexpr int NK = D / 16, NV = D / 8;
+  float o[NV][4];
+  float m[2], l[2];
+
+  __device__ __forceinline__ void run(const PagedAttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int t0, int t1,
+                                      uint32_t sm, int warp, int lane) {
+    const PagedArgs &a = A.p;
+    using F = Few<D>;
+    constexpr int CPR = D / 8;       // 16-byte pieces of a row
+    constexpr int RPI = 32 / CPR;    // rows one copy instruction of the warp covers
+    const int quad = lane >> 2, col = (lane & 3) * 2;
+    const int R = rq.rows * a.group;
+    // query fragments
+    uint32_t q[NK][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = quad + 8 * half;
+      const bool ok = (half == 0 || !HALF) && r < R;
+      const int i = ok ? r / a.group : 0;
+      const T *src = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + (h * a.group + (ok ? r - i * a.group : 0)) * D + col;
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        q[kk][half] = ok ? *reinterpret_cast<const uint32_t *>(src + kk * 16) : 0u;
+        q[kk][half + 2] = ok ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
+      }
+    }
+    // what this thread's rows see: slots <= p, from f on or among the sinks
+    int p[2], f[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = quad + 8 * half;
+      p[half] = r < R ? rq.n - rq.rows + r / a.group : -1;
+      f[half] = p[half] >= 0 ? window_first(a, p[half]) : 0;
+    }
+    const int p_low = rq.n - rq.rows, f_high = window_first(a, rq.n - 1);
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+
+    const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+    const int64_t head_off = static_cast<int64_t>(h) * a.head_stride;
+    const T *K = static_cast<const T *>(a.k) + head_off, *V = static_cast<const T *>(a.v) + head_off;
+    // offset of slot lane % 16 of tile t, -1 for a slot no row sees
+    auto offset = [&](int t) -> int64_t {
+      if (t >= t1) return -1;
+      const int j = tl.at(t) * kUnit + (lane & 15);
+      if (j >= rq.n || (j >= a.n_sink && j < window_first(a, max(0, p_low)))) return -1;
+      return slot_offset(a, table, j);
+    };
+    auto issue = [&](int t, int stage, int64_t off) {
+      if (t < t1) {
+        const uint32_t dst = sm + stage * 2 * F::kTile;
+        const int c = lane % CPR;
+#pragma unroll
+        for (int u = 0; u < kUnit / RPI; ++u) {
+          const int r = u * RPI + lane / CPR;
+          const int64_t ro = __shfl_sync(0xffffffffu, off, r);
+          const uint32_t d = dst + r * F::kRowBytes + ((c ^ (r & 7)) << 4);
+          const int64_t so = ro < 0 ? 0 : ro + c * 8;
+          cp_async16(d, K + so, ro >= 0);
+          cp_async16(d + F::kTile, V + so, ro >= 0);
+        }
+      }
+      cp_async_commit();
+    };
+    int t = t0 + warp;
+#pragma unroll
+    for (int s = 0; s < F::kStages - 1; ++s) issue(t + s * kFewWarps, s, offset(t + s * kFewWarps));
+    int64_t next = offset(t + (F::kStages - 1) * kFewWarps);
+    int stage = 0;
+    for (; t < t1; t += kFewWarps) {
+      cp_async_wait<F::kStages - 2>();
+      __syncwarp();
+      {  // the stage freed by the previous tile takes the tile kStages - 1 ahead
+        const int ahead = t + (F::kStages - 1) * kFewWarps;
+        issue(ahead, stage == 0 ? F::kStages - 1 : stage - 1, next);
+        next = offset(ahead + kFewWarps);
+      }
+      const uint32_t kb = sm + stage * 2 * F::kTile, vb = kb + F::kTile;
+      // scores: 16 rows x 16 slots
+      float c[2][4] = {};
+      {
+        const int r = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+          uint32_t kf[4];
+          ldmatrix4(kb + r * F::kRowBytes + (((kk * 2 + cc) ^ (r & 7)) << 4), kf);
+          mma16816<T>(c[0], q[kk], kf[0], kf[1]);
+          mma16816<T>(c[1], q[kk], kf[2], kf[3]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[n][e] *= a.scale_log2;
+      const int j0 = tl.at(t) * kUnit;
+      if (!(j0 + kUnit - 1 <= p_low && (j0 >= f_high || j0 + kUnit <= a.n_sink))) {  // some row does not see all of it
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + n * 8 + col + (e & 1), half = e >> 1;
+            if (!(j <= p[half] && (j >= f[half] || j < a.n_sink))) c[n][e] = -INFINITY;
+          }
+      }
+      // running maximum; the sums are rescaled only when a row's moves
+      uint32_t hi[4], lo[4];
+      float mx[2];
+#pragma unroll
+      for (int half = 0; half < (HALF ? 1 : 2); ++half) {
+        float x = fmaxf(fmaxf(c[0][2 * half], c[0][2 * half + 1]), fmaxf(c[1][2 * half], c[1][2 * half + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        mx[half] = fmaxf(m[half], x);
+      }
+      const bool moved = mx[0] > m[0] || (!HALF && mx[1] > m[1]);
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int half = 0; half < (HALF ? 1 : 2); ++half) {
+          const float w = m[half] == mx[half] ? 1.f : exp2_fast(m[half] - mx[half]);
+          m[half] = mx[half];
+          l[half] *= w;
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            o[n][2 * half] *= w;
+            o[n][2 * half + 1] *= w;
+            if (HALF) {
+              o[n][2] *= w;
+              o[n][3] *= w;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int half = 0; half < (HALF ? 1 : 2); ++half) {
+        const float ref = m[half] == -INFINITY ? 0.f : m[half] - Head<T>::k;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float x = exp2_fast(c[n][2 * half] - ref), y = exp2_fast(c[n][2 * half + 1] - ref);
+          l[half] += x + y;
+          const uint32_t hv = Pair<T>::pack(x, y);
+          const float2 back = Pair<T>::unpack(hv);
+          hi[2 * n + half] = hv;
+          lo[2 * n + half] = Pair<T>::pack(x - back.x, y - back.y);
+        }
+      }
+      if (HALF) {
+        hi[1] = lo[0];
+        hi[3] = lo[2];
+      }
+      {
+        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), cc = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < NV / 2; ++n) {
+          uint32_t vf[4];
+          ldmatrix4t(vb + r * F::kRowBytes + (((n * 2 + cc) ^ (r & 7)) << 4), vf);
+          mma16816<T>(o[2 * n], hi, vf[0], vf[1]);
+          mma16816<T>(o[2 * n + 1], hi, vf[2], vf[3]);
+          if (!HALF) {
+            mma16816<T>(o[2 * n], lo, vf[0], vf[1]);
+            mma16816<T>(o[2 * n + 1], lo, vf[2], vf[3]);
+          }
+        }
+      }
+      __syncwarp();
+      stage = stage + 1 == F::kStages ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+      if (m[half] != -INFINITY) m[half] -= Head<T>::k;  // the reference the sums are against
+    }
+  }
+};
+
+// Joins np parts of rows 0..R-1 (part i: sums at o(i) + r*D, (reference, sum) at ml(i)[r]) and
+// writes the rows, or (part_o) one joined part.  All threads of the block.
+template <typename T, int D, int NT, typename PO, typename PM>
+__device__ void join_parts(const PagedAttnArgs &A, const Request &rq, int b, int h, int R, int np, PO po, PM pm, float *part_o,
+                           float2 *part_ml, unsigned *bad_rows, float (*scratch)[D]) {
+  constexpr int C4 = D / 4;
+  const int tid = threadIdx.x;
+  bool bad = false;  // a result of this thread is not finite
+  if (tid < 4) bad_rows[tid] = 0u;
+  __syncthreads();
+  for (int c = tid; c < R * C4; c += NT) {
+    const int r = c / C4, d = (c - r * C4) * 4;
+    float M = -INFINITY;
+    for (int i = 0; i < np; ++i) {
+      const float2 x = pm(i, r);
+      if (!(x.y == 0.f)) M = fmaxf(M, x.x);
+    }
+    float L = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < np; ++i) {
+      const float2 x = pm(i, r);
+      const float4 v = po(i, r, d);
+      const float w = x.y == 0.f ? 0.f : exp2f(x.x - M);
+      if (w != 0.f) {
+        L += w * x.y;
+        s.x += w * v.x;
+        s.y += w * v.y;
+        s.z += w * v.z;
+        s.w += w * v.w;
+      }
+    }
+    if (part_o) {
+      *reinterpret_cast<float4 *>(part_o + r * D + d) = s;
+      if (d == 0) part_ml[r] = make_float2(M, L);
+    } else {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float sum = (s.x + s.y + s.z + s.w) * inv;
+      if (!(fabsf(sum) <= 3.4e38f)) {
+        atomicOr(&bad_rows[r >> 5], 1u << (r & 31));
+        bad = true;
+      }
+      store4<T>(A, rq, h, r, d, s, inv);
+      if (d == 0) store_lse(A, rq, h, r, M, L);
+    }
+  }
+  if (!__syncthreads_or(bad)) return;
+  for (int r = tid >> 5; r < R; r += NT / 32)
+    if (bad_rows[r >> 5] >> (r & 31) & 1)
+      attend_row<T, D>(A, rq, b, r / A.p.group, h * A.p.group + r % A.p.group, scratch[tid >> 5], tid & 31, false);
+  __syncthreads();
+}
+
+// unit_start[b] = units of the requests before b; all threads of the block.
+template <int NT>
+__device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.n_requests; b0 += NT) {
+    const int b = b0 + tid;
+    int64_t v = 0;
+    if (b < a.n_requests) v = static_cast<int64_t>(tiles_of(a, request_of(a, b)).count) * a.n_kv_heads;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum_s[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) x += warp_sum_s[w];
+    }
+    if (b < a.n_requests) start[b + 1] = base + x;
+    for (int w = 0; w < NT / 32; ++w) base += warp_sum_s[w];
+    __syncthreads();
+  }
+  if (tid == 0) start[0] = 0;
+  __syncthreads();
+}
+// Request of unit u (the last one that starts at or before it and has units).
+__device__ __forceinline__ int request_at(const int64_t *start, int n, int64_t u) {
+  int lo = 0, hi = n;  // start[lo] <= u < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <typename T, int D, bool HALF>
+__global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_constant__ PagedAttnArgs A) {
+  extern __shared__ __align__(1024) uint8_t sm_raw[];
+  __shared__ int64_t start[BD_PAGED_MAX_REQUESTS + 1];
+  __shared__ int64_t warp_sum_s[kFewWarps];
+  __shared__ float2 ml[kFewWarps][kFewRows];
+  __shared__ unsigned bad_rows[4];
+  __shared__ float scratch[kFewWarps][D];
+  const PagedArgs &a = A.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  scan_requests<kFewThreads>(a, start, warp_sum_s);
+  const int64_t units = start[a.n_requests];
+  const int ctas = ctas_used(units, A.n_ctas), g = blockIdx.x;
+  if (g == 0)
+    for (int b = tid; b <= a.n_requests; b += kFewThreads) A.unit_start[b] = start[b];
+  if (g >= ctas) return;
+  const int64_t u0 = share_begin(units, ctas, g), u1 = share_begin(units, ctas, g + 1);
+  uint8_t *mine = sm_raw + warp * Few<D>::kWarpBytes;
+  for (int64_t u = u0; u < u1;) {
+    const int b = request_at(start, a.n_requests, u);
+    const Request rq = request_of(a, b);
+    const Tiles tl = tiles_of(a, rq);
+    const int64_t in = u - start[b];
+    const int h = static_cast<int>(in / tl.count), t0 = static_cast<int>(in - static_cast<int64_t>(h) * tl.count);
+    const int t1 = static_cast<int>(u1 - u < tl.count - t0 ? t0 + (u1 - u) : tl.count);
+    const int R = rq.rows * a.group;
+    {
+      FewWarp<T, D, HALF> w;
+      w.run(A, rq, tl, b, h, t0, t1, smem_u32(mine), warp, lane);
+      float *so = reinterpret_cast<float *>(mine);
+      const int quad = lane >> 2, col = (lane & 3) * 2;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        if (HALF) {
+          *reinterpret_cast<float2 *>(so + quad * D + n * 8 + col) = make_float2(w.o[n][0] + w.o[n][2], w.o[n][1] + w.o[n][3]);
+        } else {
+          *reinterpret_cast<float2 *>(so + quad * D + n * 8 + col) = make_float2(w.o[n][0], w.o[n][1]);
+          *reinterpret_cast<float2 *>(so + (quad + 8) * D + n * 8 + col) = make_float2(w.o[n][2], w.o[n][3]);
+        }
+      }
+      if ((lane & 3) == 0) {
+        ml[warp][quad] = make_float2(w.m[0], w.l[0]);
+        ml[warp][quad + 8] = make_float2(w.m[1], w.l[1]);
+      }
+    }
+    const bool whole = t0 == 0 && t1 == tl.count;
+    const int slot = 2 * g + (u == u0 ? 0 : 1);
+    join_parts<T, D, kFewThreads>(
+        A, rq, b, h, R, kFewWarps,
+        [&](int i, int r, int d) { return *reinterpret_cast<const float4 *>(sm_raw + i * Few<D>::kWarpBytes + (r * D + d) * 4); },
+        [&](int i, int r) { return ml[i][r]; },
+        whole ? nullptr : A.part_o + static_cast<int64_t>(slot) * kFewRows * D,
+        whole ? nullptr : A.part_ml + static_cast<int64_t>(slot) * kFewRows, bad_rows, scratch);
+    u += t1 - t0;
+  }
+}
+
+// One block per (request, KV head): joins the parts of a head that several blocks worked on, and
+// writes the rows of a request without slots.
+constexpr int kJoinThreads = 128;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_constant__ PagedAttnArgs A) {
+  __shared__ unsigned bad_rows[4];
+  __shared__ float scratch[kJoinThreads / 32][D];
+  const PagedArgs &a = A.p;
+  const int h = blockIdx.x, b = blockIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t begin = A.unit_start[b], units = A.unit_start[a.n_requests];
+  const int64_t count = (A.unit_start[b + 1] - begin) / a.n_kv_heads;
+  int np = 0, g0 = 0;
+  int64_t u = 0;
+  int ctas = 1;
+  if (count > 0) {
+    ctas = ctas_used(units, A.n_ctas);
+    u = begin + h * count;
+    auto owner = [&](int64_t x) {  // block whose share holds unit x
+      int g = static_cast<int>(x * ctas / units);
+      while (share_begin(units, ctas, g + 1) <= x) ++g;
+      while (share_begin(units, ctas, g) > x) --g;
+      return g;
+    };
+    g0 = owner(u);
+    np = owner(u + count - 1) - g0 + 1;
+    if (np == 1) return;
+  }
+  const Request rq = request_of(a, b);
+  const int first = np > 0 && share_begin(units, ctas, g0) < u ? 1 : 0;  // the head began inside its first block
+  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g0 + i) + (i == 0 ? first : 0)) * kFewRows; };
+  join_parts<T, D, kJoinThreads>(
+      A, rq, b, h, rq.rows * a.group, np,
+      [&](int i, int r, int d) { return __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d)); },
+      [&](int i, int r) { return __ldcg(A.part_ml + slot(i) + r); }, nullptr, nullptr, bad_rows, scratch);
+}
+
+// ------------------------------------------------------------------ many rows: one warp per row
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_attention_rows(const __grid_constant__ PagedAttnArgs A) {
   __shared__ float qs[4][D];
@@ -81,16 +556,56 @@ __global__ void __launch_bounds__(128) paged_attention_rows(const __grid_constan
   const Request rq = request_of(A.p, b);
   const int hq = A.p.n_kv_heads * A.p.group;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + warp; u < static_cast<int64_t>(rq.rows) * hq; u += gridDim.x * 4)
-    attend_row<T, D>(A, rq, b, static_cast<int>(u / hq), static_cast<int>(u % hq), qs[warp], lane);
+    attend_row<T, D>(A, rq, b, static_cast<int>(u / hq), static_cast<int>(u % hq), qs[warp], lane, true);
+}
+
+// ------------------------------------------------------------------ host
+namespace {
+constexpr size_t kAlign = 256;
+size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+size_t start_bytes(int n_requests) { return up((static_cast<size_t>(n_requests) + 1) * 8); }
+}  // namespace
+
+size_t paged_attention_bytes(int n_requests, int max_rows, int group, int head_dim) {
+  const size_t parts = 2 * static_cast<size_t>(few_ctas()) * kFewRows;
+  return start_bytes(n_requests) + up(parts * head_dim * 4) + up(parts * 8);
+}
+
+void paged_attention_carve(PagedAttnArgs &A, void *workspace) {
+  uint8_t *p = static_cast<uint8_t *>(workspace);
+  A.n_ctas = few_ctas();
+  const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
+  A.unit_start = reinterpret_cast<int64_t *>(p);
+  p += start_bytes(A.p.n_requests);
+  A.part_o = reinterpret_cast<float *>(p);
+  p += up(parts * A.p.head_dim * 4);
+  A.part_ml = reinterpret_cast<float2 *>(p);
+}
+
+template <typename T, int D>
+static cudaError_t launch_few(const PagedAttnArgs &A, cudaStream_t s) {
+  const PagedArgs &a = A.p;
+  auto kernel = a.max_rows * a.group <= 8 ? attention_few<T, D, true> : attention_few<T, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
+  if (e == cudaSuccess) e = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Few<D>::kSmem, s, A);
+  if (e == cudaSuccess) e = launch_pdl(attention_join<T, D>, dim3(a.n_kv_heads, a.n_requests), dim3(kJoinThreads), 0, s, A);
+  return e;
 }
 
 std::string launch_paged_attention(const PagedAttnArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
+  cudaError_t e;
+  if (static_cast<int64_t>(a.max_rows) * a.group <= kFewRows) {
+    if (dtype == BD_BF16)
+      e = a.head_dim == 128 ? launch_few<__nv_bfloat16, 128>(A, s) : launch_few<__nv_bfloat16, 64>(A, s);
+    else
+      e = a.head_dim == 128 ? launch_few<__half, 128>(A, s) : launch_few<__half, 64>(A, s);
+    return e == cudaSuccess ? std::string() : std::string("paged attention: ") + cudaGetErrorString(e);
+  }
   const int64_t units = static_cast<int64_t>(a.max_rows) * a.n_kv_heads * a.group;
   const int64_t blocks = (units + 3) / 4;
   const dim3 grid(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), a.n_requests);
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(128), 0, s, A); };
-  cudaError_t e;
   if (dtype == BD_BF16)
     e = a.head_dim == 128 ? go(paged_attention_rows<__nv_bfloat16, 128>) : go(paged_attention_rows<__nv_bfloat16, 64>);
   else
