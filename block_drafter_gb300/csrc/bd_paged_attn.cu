@@ -223,12 +223,14 @@ struct FewWarp {
     const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
     const int64_t head_off = static_cast<int64_t>(h) * a.head_stride;
     const T *K = static_cast<const T *>(a.k) + head_off, *V = static_cast<const T *>(a.v) + head_off;
-    // offset of slot lane % 16 of tile t, -1 for a slot no row sees
-    auto offset = [&](int t) -> int64_t {
-      if (t >= t1) return -1;
+    // page of slot lane % 16 of tile t (the load alone: several go out side by side), then the
+    // slot's offset, -1 for a slot no row sees
+    const int f_low = window_first(a, max(0, p_low));
+    auto page_of = [&](int t) { return __ldg(table + min(tl.at(min(t, t1 - 1)) * kUnit + (lane & 15), rq.n - 1) / a.page_size); };
+    auto offset = [&](int t, int page) -> int64_t {
       const int j = tl.at(t) * kUnit + (lane & 15);
-      if (j >= rq.n || (j >= a.n_sink && j < window_first(a, max(0, p_low)))) return -1;
-      return slot_offset(a, table, j);
+      if (t >= t1 || j >= rq.n || (j >= a.n_sink && j < f_low)) return -1;
+      return page_offset(a, page, j);
     };
     auto issue = [&](int t, int stage, int64_t off) {
       if (t < t1) {
@@ -247,17 +249,20 @@ struct FewWarp {
       cp_async_commit();
     };
     int t = t0 + warp;
+    int pages[F::kStages];
 #pragma unroll
-    for (int s = 0; s < F::kStages - 1; ++s) issue(t + s * kFewWarps, s, offset(t + s * kFewWarps));
-    int64_t next = offset(t + (F::kStages - 1) * kFewWarps);
+    for (int s = 0; s < F::kStages; ++s) pages[s] = page_of(t + s * kFewWarps);
+#pragma unroll
+    for (int s = 0; s < F::kStages - 1; ++s) issue(t + s * kFewWarps, s, offset(t + s * kFewWarps, pages[s]));
+    int next = pages[F::kStages - 1];
     int stage = 0;
     for (; t < t1; t += kFewWarps) {
       cp_async_wait<F::kStages - 2>();
       __syncwarp();
       {  // the stage freed by the previous tile takes the tile kStages - 1 ahead
         const int ahead = t + (F::kStages - 1) * kFewWarps;
-        issue(ahead, stage == 0 ? F::kStages - 1 : stage - 1, next);
-        next = offset(ahead + kFewWarps);
+        issue(ahead, stage == 0 ? F::kStages - 1 : stage - 1, offset(ahead, next));
+        next = page_of(ahead + kFewWarps);
       }
       const uint32_t kb = sm + stage * 2 * F::kTile, vb = kb + F::kTile;
       // scores: 16 rows x 16 slots
@@ -359,56 +364,22 @@ struct FewWarp {
   }
 };
 
-// Joins np parts of rows 0..R-1 (part i: sums at o(i) + r*D, (reference, sum) at ml(i)[r]) and
-// writes the rows, or (part_o) one joined part.  All threads of the block.
-template <typename T, int D, int NT, typename PO, typename PM>
-__device__ void join_parts(const PagedAttnArgs &A, const Request &rq, int b, int h, int R, int np, PO po, PM pm, float *part_o,
-                           float2 *part_ml, unsigned *bad_rows, float (*scratch)[D]) {
-  constexpr int C4 = D / 4;
-  const int tid = threadIdx.x;
-  bool bad = false;  // a result of this thread is not finite
-  if (tid < 4) bad_rows[tid] = 0u;
-  __syncthreads();
-  for (int c = tid; c < R * C4; c += NT) {
-    const int r = c / C4, d = (c - r * C4) * 4;
-    float M = -INFINITY;
-    for (int i = 0; i < np; ++i) {
-      const float2 x = pm(i, r);
-      if (!(x.y == 0.f)) M = fmaxf(M, x.x);
-    }
-    float L = 0.f;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < np; ++i) {
-      const float2 x = pm(i, r);
-      const float4 v = po(i, r, d);
-      const float w = x.y == 0.f ? 0.f : exp2f(x.x - M);
-      if (w != 0.f) {
-        L += w * x.y;
-        s.x += w * v.x;
-        s.y += w * v.y;
-        s.z += w * v.z;
-        s.w += w * v.w;
-      }
-    }
-    if (part_o) {
-      *reinterpret_cast<float4 *>(part_o + r * D + d) = s;
-      if (d == 0) part_ml[r] = make_float2(M, L);
-    } else {
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      const float sum = (s.x + s.y + s.z + s.w) * inv;
-      if (!(fabsf(sum) <= 3.4e38f)) {
-        atomicOr(&bad_rows[r >> 5], 1u << (r & 31));
-        bad = true;
-      }
-      store4<T>(A, rq, h, r, d, s, inv);
-      if (d == 0) store_lse(A, rq, h, r, M, L);
-    }
-  }
-  if (!__syncthreads_or(bad)) return;
-  for (int r = tid >> 5; r < R; r += NT / 32)
-    if (bad_rows[r >> 5] >> (r & 31) & 1)
-      attend_row<T, D>(A, rq, b, r / A.p.group, h * A.p.group + r % A.p.group, scratch[tid >> 5], tid & 31, false);
+// One finished piece of a row (4 columns from d on): sums o against the reference m, row sum l.
+// Returns whether it is not finite.
+template <typename T>
+__device__ __forceinline__ bool finish4(const PagedAttnArgs &A, const Request &rq, int h, int r, int d, float4 o, float m, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store4<T>(A, rq, h, r, d, o, inv);
+  if (d == 0) store_lse(A, rq, h, r, m, l);
+  return !(fabsf((o.x + o.y + o.z + o.w) * inv) <= 3.4e38f);
+}
+// Does the rows of bad_rows again, a warp each; all threads of the block.
+template <typename T, int D, int NT>
+__device__ __noinline__ void redo_rows(const PagedAttnArgs &A, const Request &rq, int b, int h, int R, const unsigned &bad_rows,
+                                       float (*scratch)[D]) {
+  for (int r = threadIdx.x >> 5; r < R; r += NT / 32)
+    if (bad_rows >> r & 1)
+      attend_row<T, D>(A, rq, b, r / A.p.group, h * A.p.group + r % A.p.group, scratch[threadIdx.x >> 5], threadIdx.x & 31, false);
   __syncthreads();
 }
 
@@ -455,7 +426,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   __shared__ int64_t start[BD_PAGED_MAX_REQUESTS + 1];
   __shared__ int64_t warp_sum_s[kFewWarps];
   __shared__ float2 ml[kFewWarps][kFewRows];
-  __shared__ unsigned bad_rows[4];
+  __shared__ unsigned bad_rows;
   __shared__ float scratch[kFewWarps][D];
   const PagedArgs &a = A.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -497,36 +468,75 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
       }
     }
     const bool whole = t0 == 0 && t1 == tl.count;
-    const int slot = 2 * g + (u == u0 ? 0 : 1);
-    join_parts<T, D, kFewThreads>(
-        A, rq, b, h, R, kFewWarps,
-        [&](int i, int r, int d) { return *reinterpret_cast<const float4 *>(sm_raw + i * Few<D>::kWarpBytes + (r * D + d) * 4); },
-        [&](int i, int r) { return ml[i][r]; },
-        whole ? nullptr : A.part_o + static_cast<int64_t>(slot) * kFewRows * D,
-        whole ? nullptr : A.part_ml + static_cast<int64_t>(slot) * kFewRows, bad_rows, scratch);
+    const int64_t slot = (2 * g + (u == u0 ? 0 : 1)) * kFewRows;
+    bool bad = false;
+    if (tid == 0) bad_rows = 0u;
+    __syncthreads();
+    for (int c = tid; c < R * (D / 4); c += kFewThreads) {  // join the warps
+      const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
+      float2 x[kFewWarps];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFewWarps; ++i) {
+        x[i] = ml[i][r];
+        if (x[i].y != 0.f) M = fmaxf(M, x[i].x);
+      }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kFewWarps; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(sm_raw + i * Few<D>::kWarpBytes + (r * D + d) * 4);
+        const float w = x[i].y == 0.f ? 0.f : exp2f(x[i].x - M);
+        if (w != 0.f) {
+          L += w * x[i].y;
+          o.x += w * v.x;
+          o.y += w * v.y;
+          o.z += w * v.z;
+          o.w += w * v.w;
+        }
+      }
+      if (whole) {
+        if (finish4<T>(A, rq, h, r, d, o, M, L)) {
+          atomicOr(&bad_rows, 1u << r);
+          bad = true;
+        }
+      } else {
+        *reinterpret_cast<float4 *>(A.part_o + (slot + r) * D + d) = o;
+        if (d == 0) A.part_ml[slot + r] = make_float2(M, L);
+      }
+    }
+    if (__syncthreads_or(bad)) redo_rows<T, D, kFewThreads>(A, rq, b, h, R, bad_rows, scratch);
     u += t1 - t0;
   }
 }
 
 // One block per (request, KV head): joins the parts of a head that several blocks worked on, and
-// writes the rows of a request without slots.
-constexpr int kJoinThreads = 128;
+// writes the rows of a request without slots.  A part's share of the result is a round trip to L2
+// away, so nothing here waits for one part at a time: a warp takes the references and row sums of a
+// row's parts side by side and leaves their weights in shared memory, and the threads, as many
+// groups of them as fit, then each add every kth part with eight loads in flight.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinParts = 320;  // weights kept: at least the blocks of the kernel before
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_constant__ PagedAttnArgs A) {
-  __shared__ unsigned bad_rows[4];
+  __shared__ unsigned bad_rows;
+  __shared__ float weight[kFewRows][kJoinParts];
+  __shared__ float2 row_ml[kFewRows];
+  __shared__ float4 sums[kJoinThreads];
   __shared__ float scratch[kJoinThreads / 32][D];
   const PagedArgs &a = A.p;
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) bad_rows = 0u;
   pdl_wait();
   pdl_trigger();
-  const int64_t begin = A.unit_start[b], units = A.unit_start[a.n_requests];
-  const int64_t count = (A.unit_start[b + 1] - begin) / a.n_kv_heads;
-  int np = 0, g0 = 0;
-  int64_t u = 0;
-  int ctas = 1;
+  const int64_t begin = A.unit_start[b], end = A.unit_start[b + 1], units = A.unit_start[a.n_requests];
+  const Request rq = request_of(a, b);
+  const int R = rq.rows * a.group;
+  if (R == 0) return;
+  const int64_t count = (end - begin) / a.n_kv_heads;
+  int np = 0, g0 = 0, first = 0;
   if (count > 0) {
-    ctas = ctas_used(units, A.n_ctas);
-    u = begin + h * count;
+    const int ctas = ctas_used(units, A.n_ctas);
+    const int64_t u = begin + h * count;
     auto owner = [&](int64_t x) {  // block whose share holds unit x
       int g = static_cast<int>(x * ctas / units);
       while (share_begin(units, ctas, g + 1) <= x) ++g;
@@ -536,14 +546,66 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
     g0 = owner(u);
     np = owner(u + count - 1) - g0 + 1;
     if (np == 1) return;
+    first = share_begin(units, ctas, g0) < u ? 1 : 0;  // the head began inside its first block
   }
-  const Request rq = request_of(a, b);
-  const int first = np > 0 && share_begin(units, ctas, g0) < u ? 1 : 0;  // the head began inside its first block
   auto slot = [&](int i) { return static_cast<int64_t>(2 * (g0 + i) + (i == 0 ? first : 0)) * kFewRows; };
-  join_parts<T, D, kJoinThreads>(
-      A, rq, b, h, rq.rows * a.group, np,
-      [&](int i, int r, int d) { return __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d)); },
-      [&](int i, int r) { return __ldcg(A.part_ml + slot(i) + r); }, nullptr, nullptr, bad_rows, scratch);
+  for (int r = tid >> 5; r < R; r += kJoinThreads / 32) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < np; i += 32) {
+      const float2 x = __ldcg(A.part_ml + slot(i) + r);
+      const float mn = x.y == 0.f ? m : fmaxf(m, x.x);
+      l = (l == 0.f ? 0.f : l * exp2f(m - mn)) + (x.y == 0.f ? 0.f : x.y * exp2f(x.x - mn));
+      m = mn;
+      weight[r][i] = x.y == 0.f ? -INFINITY : x.x;
+    }
+    const float M = warp_max(m);
+    const float L = warp_sum(l == 0.f ? 0.f : l * exp2f(m - M));
+    for (int i = lane; i < np; i += 32) {
+      const float x = weight[r][i];
+      weight[r][i] = x == -INFINITY ? 0.f : exp2f(x - M);
+    }
+    if (lane == 0) row_ml[r] = make_float2(M, L);
+  }
+  __syncthreads();
+  const int pieces = R * (D / 4);
+  const int groups = pieces < kJoinThreads ? kJoinThreads / pieces : 1;
+  bool bad = false;
+  for (int c0 = 0; c0 < pieces; c0 += kJoinThreads) {
+    const int k = groups > 1 ? tid / pieces : 0, c = groups > 1 ? tid - k * pieces : c0 + tid;
+    const bool mine = k < groups && c < pieces;
+    const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine) {
+#pragma unroll 8
+      for (int i = k; i < np; i += groups) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
+        const float w = weight[r][i];
+        if (w != 0.f) {
+          o.x += w * v.x;
+          o.y += w * v.y;
+          o.z += w * v.z;
+          o.w += w * v.w;
+        }
+      }
+    }
+    if (groups > 1) {
+      sums[tid] = o;
+      __syncthreads();
+      if (k > 0) continue;
+      for (int i = 1; i < groups; ++i) {
+        const float4 v = sums[tid + i * pieces];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+    }
+    if (mine && finish4<T>(A, rq, h, r, d, o, row_ml[r].x, row_ml[r].y)) {
+      atomicOr(&bad_rows, 1u << r);
+      bad = true;
+    }
+  }
+  if (__syncthreads_or(bad)) redo_rows<T, D, kJoinThreads>(A, rq, b, h, R, bad_rows, scratch);
 }
 
 // ------------------------------------------------------------------ many rows: one warp per row
@@ -566,14 +628,15 @@ size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 size_t start_bytes(int n_requests) { return up((static_cast<size_t>(n_requests) + 1) * 8); }
 }  // namespace
 
+static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts; }
 size_t paged_attention_bytes(int n_requests, int max_rows, int group, int head_dim) {
-  const size_t parts = 2 * static_cast<size_t>(few_ctas()) * kFewRows;
+  const size_t parts = 2 * static_cast<size_t>(few_blocks()) * kFewRows;
   return start_bytes(n_requests) + up(parts * head_dim * 4) + up(parts * 8);
 }
 
 void paged_attention_carve(PagedAttnArgs &A, void *workspace) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
-  A.n_ctas = few_ctas();
+  A.n_ctas = few_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
   A.unit_start = reinterpret_cast<int64_t *>(p);
   p += start_bytes(A.p.n_requests);

@@ -36,16 +36,18 @@ __device__ __forceinline__ Request request_of(const PagedArgs &a, int b) {
   return r;
 }
 
-// Element offset of slot j of request b (KV head 0) in the pools, or -1 (flagged) where its page
-// id lies outside the pool.  0 <= j < the request's checked length.
-__device__ __forceinline__ int64_t slot_offset(const PagedArgs &a, const int32_t *table_row, int j) {
-  const int c = j / a.page_size;
-  const int page = __ldg(table_row + c);
+// Element offset of slot j (KV head 0) in the pools where it lies in `page`, or -1 (flagged) where
+// that is no page of the pool.
+__device__ __forceinline__ int64_t page_offset(const PagedArgs &a, int page, int j) {
   if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
     atomicOr(&g_error_word, DEVERR_BAD_INDEX);
     return -1;
   }
-  return page * a.page_stride + (j - c * a.page_size) * a.slot_stride;
+  return page * a.page_stride + (j % a.page_size) * a.slot_stride;
+}
+// The same by the request's row of the page table.  0 <= j < the request's checked length.
+__device__ __forceinline__ int64_t slot_offset(const PagedArgs &a, const int32_t *table_row, int j) {
+  return page_offset(a, __ldg(table_row + j / a.page_size), j);
 }
 
 // First slot beside the sinks that the row at slot p sees (p >= 0).

@@ -16,13 +16,19 @@ on the given stream, or on the current stream of the pools' device.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 from typing import Optional
 
 import torch
 
 from . import binding as B
+
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current stream's handle without building a torch.cuda.Stream (2.8 us a call), where torch has it.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 _TYPES = {torch.bfloat16: B.BF16, torch.float16: B.F16, torch.float32: B.F32}
 
@@ -49,6 +55,9 @@ class PagedBatch:
                   "seq_len [requests], row_start [requests + 1])")
             cache._on_device(name, t)
         self.n_requests, self.n_rows, self.max_len = n, int(n_rows), int(max_len)
+        self.q_shape = (self.n_rows, cache.n_q_heads, cache.head_dim)
+        self.kv_shape = (self.n_rows, cache.n_kv_heads, cache.head_dim)
+        self.lse_shape = (self.n_rows, cache.n_q_heads)
         self.tensors = (page_table, seq_len, row_start)
         self.struct = B.PagedBatch(n, page_table.shape[1], int(n_rows), int(max_rows), int(max_len),
                                    page_table.data_ptr(), seq_len.data_ptr(),
@@ -71,7 +80,7 @@ class PagedCache:
               "k and v: two pools [pages, KV heads, page size, D] of one shape, type and layout are wanted")
         _need(k.dtype in _TYPES, f"pools of {k.dtype} are not supported")
         _need(k.stride(3) == 1, "the D values of a slot must be contiguous")
-        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.k, self.v, self.dtype, self.device, self.index = k, v, k.dtype, k.device, k.get_device()
         self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), k.shape[1], k.shape[3]
         self.scale = 1.0 / math.sqrt(self.head_dim)
         self.struct = B.PagedKv(self.n_q_heads, self.n_kv_heads, self.head_dim, _TYPES[k.dtype],
@@ -80,43 +89,51 @@ class PagedCache:
         B.paged_workspace_bytes(self.struct, 1, 1)  # the library's checks of the pools
         self._on_device("v", v)
 
+    # The checks of a call are written for their cost: a decoding step makes one call per layer.
     def _on_device(self, name: str, t: torch.Tensor):
-        _need(t.device == self.device and t.is_cuda, f"{name} is on {t.device}, the pools on {self.device} "
-              "(a CUDA device is wanted)")
+        if t.get_device() != self.index or self.index < 0:
+            raise ValueError(f"{name} is on {t.device}, the pools on {self.device} (a CUDA device is wanted)")
 
-    def _rows(self, name: str, t: torch.Tensor, batch: PagedBatch, heads: int) -> int:
+    def _rows(self, name: str, t: torch.Tensor, shape: tuple) -> int:
         """Row stride of a row tensor [n_rows, heads, D]."""
-        _need(t.dim() == 3 and t.shape == (batch.n_rows, heads, self.head_dim) and t.dtype == self.dtype,
-              f"{name}: [{batch.n_rows}, {heads}, {self.head_dim}] of {self.dtype} is wanted, "
-              f"got {list(t.shape)} of {t.dtype}")
-        s = t.stride()
-        _need(s[2] == 1 and (s[1] == self.head_dim or heads == 1), f"{name}: a row's heads must be contiguous")
-        self._on_device(name, t)
-        return s[0]
+        if t.shape != shape or t.dtype is not self.dtype:
+            raise ValueError(f"{name}: {list(shape)} of {self.dtype} is wanted, got {list(t.shape)} of {t.dtype}")
+        row, head, one = t.stride()
+        if one != 1 or (head != shape[2] and shape[1] != 1):
+            raise ValueError(f"{name}: a row's heads must be contiguous")
+        if t.get_device() != self.index:
+            self._on_device(name, t)
+        return row
 
     def _floats(self, name: str, t: torch.Tensor, rows: int, width: int) -> int:
         """Row stride of an fp32 matrix with at least ``width`` columns."""
-        _need(t.dim() == 2 and t.dtype == torch.float32 and t.shape[0] == rows and t.shape[1] >= width
-              and (t.stride(1) == 1 or t.shape[1] <= 1) and t.stride(0) >= t.shape[1],
-              f"{name}: float32 [{rows}, >= {width}] with contiguous rows is wanted, got {list(t.shape)} of {t.dtype}")
-        self._on_device(name, t)
-        return t.stride(0)
+        s, n = t.stride(), t.shape
+        if len(n) != 2 or t.dtype is not torch.float32 or n[0] != rows or n[1] < width or (s[1] != 1 and n[1] > 1) or s[0] < n[1]:
+            raise ValueError(f"{name}: float32 [{rows}, >= {width}] with contiguous rows is wanted, got {list(n)} of {t.dtype}")
+        if t.get_device() != self.index:
+            self._on_device(name, t)
+        return s[0]
 
     def _ints(self, name: str, t: torch.Tensor, shape):
-        _need(t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-              f"{name}: contiguous int32 {list(shape)} is wanted, got {list(t.shape)} of {t.dtype}")
-        self._on_device(name, t)
+        if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous int32 {list(shape)} is wanted, got {list(t.shape)} of {t.dtype}")
+        if t.get_device() != self.index:
+            self._on_device(name, t)
 
     def _lse(self, lse: torch.Tensor, batch: PagedBatch):
-        _need(lse.dtype == torch.float32 and lse.shape == (batch.n_rows, self.n_q_heads) and lse.is_contiguous(),
-              f"lse: contiguous float32 [{batch.n_rows}, {self.n_q_heads}] is wanted")
-        self._on_device("lse", lse)
+        if lse.dtype is not torch.float32 or lse.shape != batch.lse_shape or not lse.is_contiguous():
+            raise ValueError(f"lse: contiguous float32 {list(batch.lse_shape)} is wanted")
+        if lse.get_device() != self.index:
+            self._on_device("lse", lse)
 
-    def _here(self):
-        """The pools' device as the current one during a call."""
-        if torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(self.device)
+    def _call(self, fn, *args, stream):
+        """The library's call on the pools' device, on the given stream or that device's current one."""
+        stream = _current_stream(self.index) if stream is None else getattr(stream, "cuda_stream", stream)
+        if torch.cuda.current_device() == self.index:
+            fn(self.struct, *args, stream)
+        else:
+            with torch.cuda.device(self.index):
+                fn(self.struct, *args, stream)
 
     def batch(self, page_table: torch.Tensor, seq_len: torch.Tensor, row_start: Optional[torch.Tensor],
               n_rows: int, max_rows: int, max_len: int, workspace: Optional[torch.Tensor] = None) -> PagedBatch:
@@ -127,24 +144,22 @@ class PagedCache:
 
     def append(self, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
         """Stores the rows' keys and values ([n_rows, KV heads, D]) in their slots."""
-        ks = self._rows("k_new", k_new, batch, self.n_kv_heads)
-        vs = self._rows("v_new", v_new, batch, self.n_kv_heads)
-        with self._here():
-            B.paged_append(self.struct, batch.struct, k_new.data_ptr(), ks, v_new.data_ptr(), vs, B._stream(stream))
+        ks = self._rows("k_new", k_new, batch.kv_shape)
+        vs = self._rows("v_new", v_new, batch.kv_shape)
+        self._call(B.paged_append, batch.struct, k_new.data_ptr(), ks, v_new.data_ptr(), vs, stream=stream)
 
     def attention(self, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
                   window: int = 0, n_sink: int = 0, scale: Optional[float] = None, stream=None):
         """Attention of the rows q [n_rows, query heads, D] into out, causal, optionally through a
         sliding window beside n_sink first slots; lse float32 [n_rows, query heads] or None.
         scale: 1/sqrt(D) if None."""
-        qs = self._rows("q", q, batch, self.n_q_heads)
-        os = self._rows("out", out, batch, self.n_q_heads)
+        qs = self._rows("q", q, batch.q_shape)
+        os = self._rows("out", out, batch.q_shape)
         if lse is not None:
             self._lse(lse, batch)
-        with self._here():
-            B.paged_attention(self.struct, batch.struct, q.data_ptr(), qs, out.data_ptr(), os,
-                              None if lse is None else lse.data_ptr(), window, n_sink,
-                              self.scale if scale is None else scale, batch.ws_ptr, batch.ws_bytes, B._stream(stream))
+        self._call(B.paged_attention, batch.struct, q.data_ptr(), qs, out.data_ptr(), os,
+                   None if lse is None else lse.data_ptr(), window, n_sink,
+                   self.scale if scale is None else scale, batch.ws_ptr, batch.ws_bytes, stream=stream)
 
     def weights(self, batch: PagedBatch, q: torch.Tensor, lse: torch.Tensor, score_out: torch.Tensor,
                 score_in: Optional[torch.Tensor] = None, decay: float = 1.0,
@@ -152,7 +167,7 @@ class PagedCache:
                 scale: Optional[float] = None, stream=None):
         """score_out[b, j] = decay * score_in[b, j] + the attention weight slot j got from the first
         rows_used[b] rows (all if None), over all heads; score_in may be score_out, or None for zero."""
-        qs = self._rows("q", q, batch, self.n_q_heads)
+        qs = self._rows("q", q, batch.q_shape)
         self._lse(lse, batch)
         stride = self._floats("score_out", score_out, batch.n_requests, batch.max_len)
         if score_in is not None:
@@ -160,12 +175,10 @@ class PagedCache:
                   "score_in and score_out: the same row stride is wanted")
         if rows_used is not None:
             self._ints("rows_used", rows_used, (batch.n_requests,))
-        with self._here():
-            B.paged_weights(self.struct, batch.struct, q.data_ptr(), qs, lse.data_ptr(),
-                            None if rows_used is None else rows_used.data_ptr(), window, n_sink,
-                            self.scale if scale is None else scale, decay,
-                            None if score_in is None else score_in.data_ptr(), score_out.data_ptr(), stride,
-                            B._stream(stream))
+        self._call(B.paged_weights, batch.struct, q.data_ptr(), qs, lse.data_ptr(),
+                   None if rows_used is None else rows_used.data_ptr(), window, n_sink,
+                   self.scale if scale is None else scale, decay,
+                   None if score_in is None else score_in.data_ptr(), score_out.data_ptr(), stride, stream=stream)
 
     def evict(self, batch: PagedBatch, score: torch.Tensor, budget: int, kept: torch.Tensor, len_out: torch.Tensor,
               n_sink: int = 0, n_recent: int = 0, dst_table: Optional[torch.Tensor] = None,
@@ -186,8 +199,6 @@ class PagedCache:
         ostride = 0
         if score_out is not None:
             ostride = self._floats("score_out", score_out, batch.n_requests, min(budget, batch.max_len))
-        with self._here():
-            B.paged_evict(self.struct, batch.struct, score.data_ptr(), stride, budget, n_sink, n_recent,
-                          None if dst_table is None else dst_table.data_ptr(), width, kept.data_ptr(),
-                          len_out.data_ptr(), None if score_out is None else score_out.data_ptr(), ostride,
-                          B._stream(stream))
+        self._call(B.paged_evict, batch.struct, score.data_ptr(), stride, budget, n_sink, n_recent,
+                   None if dst_table is None else dst_table.data_ptr(), width, kept.data_ptr(),
+                   len_out.data_ptr(), None if score_out is None else score_out.data_ptr(), ostride, stream=stream)
