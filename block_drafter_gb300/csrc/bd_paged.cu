@@ -416,7 +416,10 @@ size_t bd_paged_workspace_bytes(const bd_paged_kv *kv, int n_requests, int max_r
     refuse(BD_ERR_INVALID_ARG, "paged workspace: n_requests must be in 1..1024 and max_rows >= 0");
     return 0;
   }
-  return paged_attention_bytes(n_requests, max_rows, kv->n_q_heads / kv->n_kv_heads, kv->head_dim);
+  // a batch made for many rows may hold few (and the other way round): the larger of the two
+  const size_t few = few_bytes(n_requests, kv->head_dim);
+  const size_t many = many_bytes(n_requests, max_rows, kv->n_q_heads / kv->n_kv_heads, kv->head_dim);
+  return few > many ? few : many;
 }
 
 bd_status bd_paged_append(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *k_new, int64_t k_stride,
@@ -460,8 +463,8 @@ bd_status bd_paged_attention(const bd_paged_kv *kv, const bd_paged_batch *batch,
   A.out = out;
   A.out_stride = out_stride;
   A.lse = lse;
-  paged_attention_carve(A, workspace);
-  return ran(launch_paged_attention(A, kv->dtype, static_cast<cudaStream_t>(stream)));
+  const bool few = static_cast<int64_t>(batch->max_rows) * A.p.group <= kFewRows;
+  return ran((few ? launch_attention_few : launch_attention_many)(A, workspace, kv->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 bd_status bd_paged_weights(const bd_paged_kv *kv, const bd_paged_batch *batch, const void *q, int64_t q_stride,

@@ -28,10 +28,12 @@ struct PagedAttnArgs {
   void *out;
   int64_t out_stride;
   float *lse;  // [n_rows][n_q_heads] or null
-  // workspace: the units before each request [n_requests + 1], then the parts of split items
+  // workspace: the units before each request (few rows) or item (many rows), the item each block
+  // begins with (many rows), and the parts of items that several blocks work on
   int64_t *unit_start;
-  float *part_o;   // [2 * n_ctas][part_rows][head_dim] unnormalised sums
-  float2 *part_ml; // [2 * n_ctas][part_rows] (reference, row sum), reference in log2 units
+  int32_t *cta_item;
+  float *part_o;    // [2 * n_ctas][part rows][head_dim] unnormalised sums
+  float2 *part_ml;  // [2 * n_ctas][part rows] (reference in log2 units, row sum)
   int n_ctas;
 };
 
@@ -62,12 +64,14 @@ struct PagedEvictArgs {
   int64_t score_out_stride;
 };
 
-size_t paged_attention_bytes(int n_requests, int max_rows, int group, int head_dim);
-// Splits `workspace` (paged_attention_bytes) into the fields of A.
-void paged_attention_carve(PagedAttnArgs &A, void *workspace);
-std::string launch_paged_attention(const PagedAttnArgs &a, int dtype, cudaStream_t s);
+inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+size_t few_bytes(int n_requests, int head_dim);
+size_t many_bytes(int n_requests, int max_rows, int group, int head_dim);
+std::string launch_attention_few(PagedAttnArgs a, void *workspace, int dtype, cudaStream_t s);
+std::string launch_attention_many(PagedAttnArgs a, void *workspace, int dtype, cudaStream_t s);
 
 unsigned take_error_word_paged();
 unsigned take_error_word_paged_attn();
+unsigned take_error_word_paged_tc();
 
 }  // namespace bd

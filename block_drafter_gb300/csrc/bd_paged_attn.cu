@@ -18,79 +18,11 @@
 // The weights enter the second product as a 16-bit high part and a 16-bit rest: the rounding to
 // 16 bits (2^-9 relative, as large as the output's own) then disappears from the result.  With at
 // most 8 rows the rest takes the idle upper 8 rows of the product and costs nothing.
-#include "bd_paged_device.cuh"
+#include "bd_paged_attn.cuh"
 
 namespace bd {
 
 BD_DEFINE_ERROR_TAKER(take_error_word_paged_attn)
-
-// One row of one query head by one warp, over exactly the slots it sees: each lane forms one
-// slot's score, then adds the 32 weighted values of its own D/32 columns.  The tiled kernels
-// multiply hidden slots by a zero weight, which an infinity or NaN among the hidden values turns
-// into NaN; they send a row whose result is not finite through here (its lse is
-// right already: a hidden slot's score is dropped, not multiplied).
-template <typename T, int D>
-__device__ __noinline__ void attend_row(const PagedAttnArgs &A, const Request &rq, int b, int i, int head, float *qs, int lane,
-                                        bool write_lse) {
-  const PagedArgs &a = A.p;
-  const int hq = a.n_kv_heads * a.group, row = rq.row0 + i, p = rq.n - rq.rows + i;
-  const T *q = static_cast<const T *>(a.q) + row * a.q_stride + head * D;
-  constexpr int C = D / 32;  // columns of a lane
-#pragma unroll
-  for (int c = 0; c < C; ++c) qs[c * 32 + lane] = to_f(q[c * 32 + lane]);
-  __syncwarp();
-  const int first = p >= 0 ? window_first(a, p) : 0;
-  const int n_sinks = min(a.n_sink, first);
-  const int count = p >= 0 ? n_sinks + p + 1 - first : 0;
-  const int64_t head_off = static_cast<int64_t>(head / a.group) * a.head_stride;
-  const T *K = static_cast<const T *>(a.k) + head_off, *V = static_cast<const T *>(a.v) + head_off;
-  const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
-  float m = -INFINITY, l = 0.f, o[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) o[c] = 0.f;
-  for (int t0 = 0; t0 < count; t0 += 32) {
-    const int t = t0 + lane;
-    int64_t off = -1;
-    float s = -INFINITY;
-    if (t < count) {
-      off = slot_offset(a, table, t < n_sinks ? t : first + t - n_sinks);
-      if (off >= 0) {
-        s = 0.f;
-        const uint4 *kr = reinterpret_cast<const uint4 *>(K + off);
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = __ldg(kr + c);
-          const float2 x0 = Pair<T>::unpack(w.x), x1 = Pair<T>::unpack(w.y), x2 = Pair<T>::unpack(w.z),
-                       x3 = Pair<T>::unpack(w.w);
-          const float *y = qs + c * 8;
-          s += x0.x * y[0] + x0.y * y[1] + x1.x * y[2] + x1.y * y[3] + x2.x * y[4] + x2.y * y[5] + x3.x * y[6] +
-               x3.y * y[7];
-        }
-        s *= a.scale_log2;
-      }
-    }
-    const float mn = fmaxf(m, warp_max(s));
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float w = exp2f(s - ref), scale = exp2f(m - ref);
-    m = mn;
-    l = l * scale + warp_sum(w);
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] *= scale;
-    for (int u = 0; u < 32; ++u) {
-      const int64_t ou = __shfl_sync(0xffffffffu, off, u);
-      const float wu = __shfl_sync(0xffffffffu, w, u);
-      if (ou < 0) continue;
-#pragma unroll
-      for (int c = 0; c < C; ++c) o[c] += wu * to_f(V[ou + c * 32 + lane]);
-    }
-  }
-  T *out = static_cast<T *>(A.out) + row * A.out_stride + head * D;
-#pragma unroll
-  for (int c = 0; c < C; ++c) out[c * 32 + lane] = from_f<T>(l == 0.f ? 0.f : o[c] / l);
-  if (write_lse && A.lse && lane == 0)
-    A.lse[static_cast<int64_t>(row) * hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
-  __syncwarp();
-}
 
 // ------------------------------------------------------------------ few rows: layout
 constexpr int kUnit = 16;  // slots of a unit
@@ -123,20 +55,11 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq)
   return t;
 }
 
-// Share of block g among `ctas` blocks of `units` units.
-__device__ __forceinline__ int64_t share_begin(int64_t units, int ctas, int g) { return units * g / ctas; }
 __device__ __forceinline__ int ctas_used(int64_t units, int most) {
   const int64_t c = (units + kFewWarps - 1) / kFewWarps;
   return c < 1 ? 1 : static_cast<int>(c < most ? c : most);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -158,19 +81,6 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Writes rows r0.. of an item: output row r = token r / group, head r % group of KV head h.
-template <typename T>
-__device__ __forceinline__ void store4(const PagedAttnArgs &A, const Request &rq, int h, int r, int d, float4 o, float inv) {
-  const int g = A.p.group, i = r / g, head = h * g + r - i * g;
-  T *out = static_cast<T *>(A.out) + (rq.row0 + i) * A.out_stride + head * A.p.head_dim + d;
-  *reinterpret_cast<uint2 *>(out) = make_uint2(Pair<T>::pack(o.x * inv, o.y * inv), Pair<T>::pack(o.z * inv, o.w * inv));
-}
-__device__ __forceinline__ void store_lse(const PagedAttnArgs &A, const Request &rq, int h, int r, float m, float l) {
-  if (!A.lse) return;
-  const int g = A.p.group, i = r / g, head = h * g + r - i * g;
-  A.lse[static_cast<int64_t>(rq.row0 + i) * A.p.n_kv_heads * g + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
 // The part of one (request, KV head) over tiles [t0, t1) by one warp (every kFewWarps-th tile):
@@ -364,25 +274,6 @@ struct FewWarp {
   }
 };
 
-// One finished piece of a row (4 columns from d on): sums o against the reference m, row sum l.
-// Returns whether it is not finite.
-template <typename T>
-__device__ __forceinline__ bool finish4(const PagedAttnArgs &A, const Request &rq, int h, int r, int d, float4 o, float m, float l) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  store4<T>(A, rq, h, r, d, o, inv);
-  if (d == 0) store_lse(A, rq, h, r, m, l);
-  return !(fabsf((o.x + o.y + o.z + o.w) * inv) <= 3.4e38f);
-}
-// Does the rows of bad_rows again, a warp each; all threads of the block.
-template <typename T, int D, int NT>
-__device__ __noinline__ void redo_rows(const PagedAttnArgs &A, const Request &rq, int b, int h, int R, const unsigned &bad_rows,
-                                       float (*scratch)[D]) {
-  for (int r = threadIdx.x >> 5; r < R; r += NT / 32)
-    if (bad_rows >> r & 1)
-      attend_row<T, D>(A, rq, b, r / A.p.group, h * A.p.group + r % A.p.group, scratch[threadIdx.x >> 5], threadIdx.x & 31, false);
-  __syncthreads();
-}
-
 // unit_start[b] = units of the requests before b; all threads of the block.
 template <int NT>
 __device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s) {
@@ -427,7 +318,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   __shared__ int64_t warp_sum_s[kFewWarps];
   __shared__ float2 ml[kFewWarps][kFewRows];
   __shared__ unsigned bad_rows;
-  __shared__ float scratch[kFewWarps][D];
   const PagedArgs &a = A.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -504,34 +394,23 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
         if (d == 0) A.part_ml[slot + r] = make_float2(M, L);
       }
     }
-    if (__syncthreads_or(bad)) redo_rows<T, D, kFewThreads>(A, rq, b, h, R, bad_rows, scratch);
+    if (__syncthreads_or(bad)) redo_rows<T, D, kFewThreads>(A, rq, b, h, 0, R, bad_rows);
     u += t1 - t0;
   }
 }
 
 // One block per (request, KV head): joins the parts of a head that several blocks worked on, and
-// writes the rows of a request without slots.  A part's share of the result is a round trip to L2
-// away, so nothing here waits for one part at a time: a warp takes the references and row sums of a
-// row's parts side by side and leaves their weights in shared memory, and the threads, as many
-// groups of them as fit, then each add every kth part with eight loads in flight.
+// writes the rows of a request without slots.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinParts = 320;  // weights kept: at least the blocks of the kernel before
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_constant__ PagedAttnArgs A) {
-  __shared__ unsigned bad_rows;
-  __shared__ float weight[kFewRows][kJoinParts];
-  __shared__ float2 row_ml[kFewRows];
-  __shared__ float4 sums[kJoinThreads];
-  __shared__ float scratch[kJoinThreads / 32][D];
   const PagedArgs &a = A.p;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  if (tid == 0) bad_rows = 0u;
+  const int h = blockIdx.x, b = blockIdx.y;
   pdl_wait();
   pdl_trigger();
   const int64_t begin = A.unit_start[b], end = A.unit_start[b + 1], units = A.unit_start[a.n_requests];
   const Request rq = request_of(a, b);
-  const int R = rq.rows * a.group;
-  if (R == 0) return;
+  if (rq.rows == 0) return;
   const int64_t count = (end - begin) / a.n_kv_heads;
   int np = 0, g0 = 0, first = 0;
   if (count > 0) {
@@ -548,105 +427,21 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
     if (np == 1) return;
     first = share_begin(units, ctas, g0) < u ? 1 : 0;  // the head began inside its first block
   }
-  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g0 + i) + (i == 0 ? first : 0)) * kFewRows; };
-  for (int r = tid >> 5; r < R; r += kJoinThreads / 32) {
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < np; i += 32) {
-      const float2 x = __ldcg(A.part_ml + slot(i) + r);
-      const float mn = x.y == 0.f ? m : fmaxf(m, x.x);
-      l = (l == 0.f ? 0.f : l * exp2f(m - mn)) + (x.y == 0.f ? 0.f : x.y * exp2f(x.x - mn));
-      m = mn;
-      weight[r][i] = x.y == 0.f ? -INFINITY : x.x;
-    }
-    const float M = warp_max(m);
-    const float L = warp_sum(l == 0.f ? 0.f : l * exp2f(m - M));
-    for (int i = lane; i < np; i += 32) {
-      const float x = weight[r][i];
-      weight[r][i] = x == -INFINITY ? 0.f : exp2f(x - M);
-    }
-    if (lane == 0) row_ml[r] = make_float2(M, L);
-  }
-  __syncthreads();
-  const int pieces = R * (D / 4);
-  const int groups = pieces < kJoinThreads ? kJoinThreads / pieces : 1;
-  bool bad = false;
-  for (int c0 = 0; c0 < pieces; c0 += kJoinThreads) {
-    const int k = groups > 1 ? tid / pieces : 0, c = groups > 1 ? tid - k * pieces : c0 + tid;
-    const bool mine = k < groups && c < pieces;
-    const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mine) {
-#pragma unroll 8
-      for (int i = k; i < np; i += groups) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
-        const float w = weight[r][i];
-        if (w != 0.f) {
-          o.x += w * v.x;
-          o.y += w * v.y;
-          o.z += w * v.z;
-          o.w += w * v.w;
-        }
-      }
-    }
-    if (groups > 1) {
-      sums[tid] = o;
-      __syncthreads();
-      if (k > 0) continue;
-      for (int i = 1; i < groups; ++i) {
-        const float4 v = sums[tid + i * pieces];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
-      }
-    }
-    if (mine && finish4<T>(A, rq, h, r, d, o, row_ml[r].x, row_ml[r].y)) {
-      atomicOr(&bad_rows, 1u << r);
-      bad = true;
-    }
-  }
-  if (__syncthreads_or(bad)) redo_rows<T, D, kJoinThreads>(A, rq, b, h, R, bad_rows, scratch);
-}
-
-// ------------------------------------------------------------------ many rows: one warp per row
-template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_attention_rows(const __grid_constant__ PagedAttnArgs A) {
-  __shared__ float qs[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
-  pdl_wait();
-  pdl_trigger();
-  const Request rq = request_of(A.p, b);
-  const int hq = A.p.n_kv_heads * A.p.group;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + warp; u < static_cast<int64_t>(rq.rows) * hq; u += gridDim.x * 4)
-    attend_row<T, D>(A, rq, b, static_cast<int>(u / hq), static_cast<int>(u % hq), qs[warp], lane, true);
+  join_rows<T, D, kJoinThreads, kFewRows>(A, rq, b, h, 0, rq.rows * a.group, np, [&](int i) {
+    return static_cast<int64_t>(2 * (g0 + i) + (i == 0 ? first : 0)) * kFewRows;
+  });
 }
 
 // ------------------------------------------------------------------ host
-namespace {
-constexpr size_t kAlign = 256;
-size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-size_t start_bytes(int n_requests) { return up((static_cast<size_t>(n_requests) + 1) * 8); }
-}  // namespace
-
 static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts; }
-size_t paged_attention_bytes(int n_requests, int max_rows, int group, int head_dim) {
-  const size_t parts = 2 * static_cast<size_t>(few_blocks()) * kFewRows;
-  return start_bytes(n_requests) + up(parts * head_dim * 4) + up(parts * 8);
-}
 
-void paged_attention_carve(PagedAttnArgs &A, void *workspace) {
-  uint8_t *p = static_cast<uint8_t *>(workspace);
-  A.n_ctas = few_blocks();
-  const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
-  A.unit_start = reinterpret_cast<int64_t *>(p);
-  p += start_bytes(A.p.n_requests);
-  A.part_o = reinterpret_cast<float *>(p);
-  p += up(parts * A.p.head_dim * 4);
-  A.part_ml = reinterpret_cast<float2 *>(p);
+size_t few_bytes(int n_requests, int head_dim) {
+  const size_t parts = 2 * static_cast<size_t>(few_blocks()) * kFewRows;
+  return align256((static_cast<size_t>(n_requests) + 1) * 8) + align256(parts * head_dim * 4) + align256(parts * 8);
 }
 
 template <typename T, int D>
-static cudaError_t launch_few(const PagedAttnArgs &A, cudaStream_t s) {
+static cudaError_t launch(const PagedAttnArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
   auto kernel = a.max_rows * a.group <= 8 ? attention_few<T, D, true> : attention_few<T, D, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
@@ -655,24 +450,20 @@ static cudaError_t launch_few(const PagedAttnArgs &A, cudaStream_t s) {
   return e;
 }
 
-std::string launch_paged_attention(const PagedAttnArgs &A, int dtype, cudaStream_t s) {
-  const PagedArgs &a = A.p;
+std::string launch_attention_few(PagedAttnArgs A, void *workspace, int dtype, cudaStream_t s) {
+  uint8_t *p = static_cast<uint8_t *>(workspace);
+  A.n_ctas = few_blocks();
+  const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
+  A.unit_start = reinterpret_cast<int64_t *>(p);
+  p += align256((static_cast<size_t>(A.p.n_requests) + 1) * 8);
+  A.part_o = reinterpret_cast<float *>(p);
+  p += align256(parts * A.p.head_dim * 4);
+  A.part_ml = reinterpret_cast<float2 *>(p);
   cudaError_t e;
-  if (static_cast<int64_t>(a.max_rows) * a.group <= kFewRows) {
-    if (dtype == BD_BF16)
-      e = a.head_dim == 128 ? launch_few<__nv_bfloat16, 128>(A, s) : launch_few<__nv_bfloat16, 64>(A, s);
-    else
-      e = a.head_dim == 128 ? launch_few<__half, 128>(A, s) : launch_few<__half, 64>(A, s);
-    return e == cudaSuccess ? std::string() : std::string("paged attention: ") + cudaGetErrorString(e);
-  }
-  const int64_t units = static_cast<int64_t>(a.max_rows) * a.n_kv_heads * a.group;
-  const int64_t blocks = (units + 3) / 4;
-  const dim3 grid(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), a.n_requests);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(128), 0, s, A); };
   if (dtype == BD_BF16)
-    e = a.head_dim == 128 ? go(paged_attention_rows<__nv_bfloat16, 128>) : go(paged_attention_rows<__nv_bfloat16, 64>);
+    e = A.p.head_dim == 128 ? launch<__nv_bfloat16, 128>(A, s) : launch<__nv_bfloat16, 64>(A, s);
   else
-    e = a.head_dim == 128 ? go(paged_attention_rows<__half, 128>) : go(paged_attention_rows<__half, 64>);
+    e = A.p.head_dim == 128 ? launch<__half, 128>(A, s) : launch<__half, 64>(A, s);
   return e == cudaSuccess ? std::string() : std::string("paged attention: ") + cudaGetErrorString(e);
 }
 

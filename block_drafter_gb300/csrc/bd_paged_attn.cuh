@@ -1,0 +1,188 @@
+// What both attention kernels of the paged cache share: results, the joining of parts, and the
+// exact row.
+#pragma once
+#include "bd_paged_device.cuh"
+
+namespace bd {
+
+// Share of block g among `ctas` blocks of `units` units.
+__device__ __forceinline__ int64_t share_begin(int64_t units, int ctas, int g) { return units * g / ctas; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One row of one query head by one warp, over exactly the slots it sees: each lane forms one
+// slot's score, then adds the 32 weighted values of its own D/32 columns.  The tiled kernels
+// multiply hidden slots by a zero weight, which an infinity or NaN among the hidden values turns
+// into NaN; they send a row whose result is not finite through here (its lse is
+// right already: a hidden slot's score is dropped, not multiplied).
+template <typename T, int D>
+__device__ __noinline__ void attend_row(const PagedAttnArgs &A, const Request &rq, int b, int i, int head, int lane) {
+  const PagedArgs &a = A.p;
+  const int row = rq.row0 + i, p = rq.n - rq.rows + i;
+  const T *q = static_cast<const T *>(a.q) + row * a.q_stride + head * D;
+  constexpr int C = D / 32;  // columns of a lane
+  const int first = p >= 0 ? window_first(a, p) : 0;
+  const int n_sinks = min(a.n_sink, first);
+  const int count = p >= 0 ? n_sinks + p + 1 - first : 0;
+  const int64_t head_off = static_cast<int64_t>(head / a.group) * a.head_stride;
+  const T *K = static_cast<const T *>(a.k) + head_off, *V = static_cast<const T *>(a.v) + head_off;
+  const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+  float m = -INFINITY, l = 0.f, o[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
+  for (int t0 = 0; t0 < count; t0 += 32) {
+    const int t = t0 + lane;
+    int64_t off = -1;
+    float s = -INFINITY;
+    if (t < count) {
+      off = slot_offset(a, table, t < n_sinks ? t : first + t - n_sinks);
+      if (off >= 0) {
+        s = 0.f;
+        const uint4 *kr = reinterpret_cast<const uint4 *>(K + off);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = __ldg(kr + c);
+          const float2 x0 = Pair<T>::unpack(w.x), x1 = Pair<T>::unpack(w.y), x2 = Pair<T>::unpack(w.z),
+                       x3 = Pair<T>::unpack(w.w);
+          const uint4 z = __ldg(reinterpret_cast<const uint4 *>(q) + c);
+          const float2 y0 = Pair<T>::unpack(z.x), y1 = Pair<T>::unpack(z.y), y2 = Pair<T>::unpack(z.z),
+                       y3 = Pair<T>::unpack(z.w);
+          s += x0.x * y0.x + x0.y * y0.y + x1.x * y1.x + x1.y * y1.y + x2.x * y2.x + x2.y * y2.y + x3.x * y3.x +
+               x3.y * y3.y;
+        }
+        s *= a.scale_log2;
+      }
+    }
+    const float mn = fmaxf(m, warp_max(s));
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float w = exp2f(s - ref), scale = exp2f(m - ref);
+    m = mn;
+    l = l * scale + warp_sum(w);
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] *= scale;
+    for (int u = 0; u < 32; ++u) {
+      const int64_t ou = __shfl_sync(0xffffffffu, off, u);
+      const float wu = __shfl_sync(0xffffffffu, w, u);
+      if (ou < 0) continue;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] += wu * to_f(V[ou + c * 32 + lane]);
+    }
+  }
+  T *out = static_cast<T *>(A.out) + row * A.out_stride + head * D;
+#pragma unroll
+  for (int c = 0; c < C; ++c) out[c * 32 + lane] = from_f<T>(l == 0.f ? 0.f : o[c] / l);
+}
+
+// Writes rows r0.. of an item: output row r = token r / group, head r % group of KV head h.
+template <typename T>
+__device__ __forceinline__ void store4(const PagedAttnArgs &A, const Request &rq, int h, int r, int d, float4 o, float inv) {
+  const int g = A.p.group, i = r / g, head = h * g + r - i * g;
+  T *out = static_cast<T *>(A.out) + (rq.row0 + i) * A.out_stride + head * A.p.head_dim + d;
+  *reinterpret_cast<uint2 *>(out) = make_uint2(Pair<T>::pack(o.x * inv, o.y * inv), Pair<T>::pack(o.z * inv, o.w * inv));
+}
+__device__ __forceinline__ void store_lse(const PagedAttnArgs &A, const Request &rq, int h, int r, float m, float l) {
+  if (!A.lse) return;
+  const int g = A.p.group, i = r / g, head = h * g + r - i * g;
+  A.lse[static_cast<int64_t>(rq.row0 + i) * A.p.n_kv_heads * g + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+}
+
+// One finished piece of a row (4 columns from d on): sums o against the reference m, row sum l.
+// Returns whether it is not finite.
+template <typename T>
+__device__ __forceinline__ bool finish4(const PagedAttnArgs &A, const Request &rq, int h, int r, int d, float4 o, float m, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store4<T>(A, rq, h, r, d, o, inv);
+  if (d == 0) store_lse(A, rq, h, r, m, l);
+  return !(fabsf((o.x + o.y + o.z + o.w) * inv) <= 3.4e38f);
+}
+// Does the rows of bad_rows (from row `from` on) again, a warp each; all threads of the block.
+template <typename T, int D, int NT>
+__device__ __noinline__ void redo_rows(const PagedAttnArgs &A, const Request &rq, int b, int h, int from, int n,
+                                       const unsigned &bad_rows) {
+  for (int r = threadIdx.x >> 5; r < n; r += NT / 32)
+    if (bad_rows >> r & 1)
+      attend_row<T, D>(A, rq, b, (from + r) / A.p.group, h * A.p.group + (from + r) % A.p.group, threadIdx.x & 31);
+  __syncthreads();
+}
+
+// Joins np parts of n rows (at most JR) of KV head h, from row `from` of the request on: part i of
+// row r lies at slot(i) + r of part_o / part_ml.  A part's share of the result is a round trip to L2
+// away, so nothing here waits for one part at a time: a warp takes the references and row sums of a
+// row's parts side by side and leaves their weights in shared memory, and the threads, as many
+// groups of them as fit, then each add every kth part with eight loads in flight.  All threads of
+// the block; np = 0 writes empty rows.
+constexpr int kJoinParts = 320;  // weights kept: at least the blocks of the kernel before
+template <typename T, int D, int NT, int JR, typename S>
+__device__ __forceinline__ void join_rows(const PagedAttnArgs &A, const Request &rq, int b, int h, int from, int n, int np, S slot) {
+  __shared__ unsigned bad_rows;
+  __shared__ float weight[JR][kJoinParts];
+  __shared__ float2 row_ml[JR];
+  __shared__ float4 sums[NT];
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) bad_rows = 0u;
+  for (int r = tid >> 5; r < n; r += NT / 32) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < np; i += 32) {
+      const float2 x = __ldcg(A.part_ml + slot(i) + r);
+      const float mn = x.y == 0.f ? m : fmaxf(m, x.x);
+      l = (l == 0.f ? 0.f : l * exp2f(m - mn)) + (x.y == 0.f ? 0.f : x.y * exp2f(x.x - mn));
+      m = mn;
+      weight[r][i] = x.y == 0.f ? -INFINITY : x.x;
+    }
+    const float M = warp_max(m);
+    const float L = warp_sum(l == 0.f ? 0.f : l * exp2f(m - M));
+    for (int i = lane; i < np; i += 32) {
+      const float x = weight[r][i];
+      weight[r][i] = x == -INFINITY ? 0.f : exp2f(x - M);
+    }
+    if (lane == 0) row_ml[r] = make_float2(M, L);
+  }
+  __syncthreads();
+  const int pieces = n * (D / 4);
+  const int groups = pieces < NT ? NT / pieces : 1;
+  bool bad = false;
+  for (int c0 = 0; c0 < pieces; c0 += NT) {
+    const int k = groups > 1 ? tid / pieces : 0, c = groups > 1 ? tid - k * pieces : c0 + tid;
+    const bool mine = k < groups && c < pieces;
+    const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine) {
+#pragma unroll 8
+      for (int i = k; i < np; i += groups) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
+        const float w = weight[r][i];
+        if (w != 0.f) {
+          o.x += w * v.x;
+          o.y += w * v.y;
+          o.z += w * v.z;
+          o.w += w * v.w;
+        }
+      }
+    }
+    if (groups > 1) {
+      sums[tid] = o;
+      __syncthreads();
+      if (k > 0) continue;
+      for (int i = 1; i < groups; ++i) {
+        const float4 v = sums[tid + i * pieces];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+    }
+    if (mine && finish4<T>(A, rq, h, from + r, d, o, row_ml[r].x, row_ml[r].y)) {
+      atomicOr(&bad_rows, 1u << r);
+      bad = true;
+    }
+  }
+  if (__syncthreads_or(bad)) redo_rows<T, D, NT>(A, rq, b, h, from, n, bad_rows);
+}
+
+}  // namespace bd
