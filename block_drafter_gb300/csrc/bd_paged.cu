@@ -450,6 +450,9 @@ bd_status bd_paged_attention(const bd_paged_kv *kv, const bd_paged_batch *batch,
   if (overlap(q, row_bytes(q_stride, width, batch->n_rows), out, row_bytes(out_stride, width, batch->n_rows)))
     return refuse(BD_ERR_INVALID_ARG, "paged attention: q and out overlap");
   if (misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged attention: lse misaligned");
+  if ((static_cast<int64_t>(batch->max_len) / 16 + 8) * kv->n_kv_heads >= (1ll << 31) ||
+      static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30))
+    return refuse(BD_ERR_UNSUPPORTED, "paged attention: max_len * n_kv_heads or max_rows * n_q_heads too large");
   if (!workspace || misaligned(workspace, 256) ||
       workspace_bytes < bd_paged_workspace_bytes(kv, batch->n_requests, batch->max_rows))
     return refuse(BD_ERR_WORKSPACE, "paged attention: workspace NULL, not 256-byte aligned or too small");

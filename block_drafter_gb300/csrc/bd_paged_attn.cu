@@ -56,7 +56,7 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq)
 }
 
 __device__ __forceinline__ int ctas_used(int64_t units, int most) {
-  const int64_t c = (units + kFewWarps - 1) / kFewWarps;
+  const int64_t c = (units + kFewWarps - 1) >> 2;  // at least a unit for each of the four warps
   return c < 1 ? 1 : static_cast<int>(c < most ? c : most);
 }
 
@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
     const int b = request_at(start, a.n_requests, u);
     const Request rq = request_of(a, b);
     const Tiles tl = tiles_of(a, rq);
-    const int64_t in = u - start[b];
-    const int h = static_cast<int>(in / tl.count), t0 = static_cast<int>(in - static_cast<int64_t>(h) * tl.count);
+    const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
+    const int h = in / static_cast<uint32_t>(tl.count), t0 = in - h * tl.count;
     const int t1 = static_cast<int>(u1 - u < tl.count - t0 ? t0 + (u1 - u) : tl.count);
     const int R = rq.rows * a.group;
     {
@@ -408,32 +408,26 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
   const int h = blockIdx.x, b = blockIdx.y;
   pdl_wait();
   pdl_trigger();
-  const int64_t begin = A.unit_start[b], end = A.unit_start[b + 1], units = A.unit_start[a.n_requests];
+  const int64_t begin = A.unit_start[b], units = A.unit_start[a.n_requests];
   const Request rq = request_of(a, b);
   if (rq.rows == 0) return;
-  const int64_t count = (end - begin) / a.n_kv_heads;
+  const int count = tiles_of(a, rq).count;  // units of a head
   int np = 0, g0 = 0, first = 0;
   if (count > 0) {
     const int ctas = ctas_used(units, A.n_ctas);
-    const int64_t u = begin + h * count;
-    auto owner = [&](int64_t x) {  // block whose share holds unit x
-      int g = static_cast<int>(x * ctas / units);
-      while (share_begin(units, ctas, g + 1) <= x) ++g;
-      while (share_begin(units, ctas, g) > x) --g;
-      return g;
-    };
-    g0 = owner(u);
-    np = owner(u + count - 1) - g0 + 1;
+    const int64_t u = begin + static_cast<int64_t>(h) * count;
+    g0 = share_owner(units, ctas, u);
+    np = share_owner(units, ctas, u + count - 1) - g0 + 1;
     if (np == 1) return;
     first = share_begin(units, ctas, g0) < u ? 1 : 0;  // the head began inside its first block
   }
-  join_rows<T, D, kJoinThreads, kFewRows>(A, rq, b, h, 0, rq.rows * a.group, np, [&](int i) {
+  join_rows<T, D, kJoinThreads, kFewRows, kJoinParts>(A, rq, b, h, 0, rq.rows * a.group, np, [&](int i) {
     return static_cast<int64_t>(2 * (g0 + i) + (i == 0 ? first : 0)) * kFewRows;
   });
 }
 
 // ------------------------------------------------------------------ host
-static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts; }
+static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts - 1; }
 
 size_t few_bytes(int n_requests, int head_dim) {
   const size_t parts = 2 * static_cast<size_t>(few_blocks()) * kFewRows;

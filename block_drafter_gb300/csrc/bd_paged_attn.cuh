@@ -5,8 +5,20 @@
 
 namespace bd {
 
-// Share of block g among `ctas` blocks of `units` units.
-__device__ __forceinline__ int64_t share_begin(int64_t units, int ctas, int g) { return units * g / ctas; }
+// First unit of block g's share among `ctas` <= 1024 blocks of `units` units (a 64-bit division takes
+// some hundred cycles: the usual sizes do without).
+__device__ __forceinline__ int64_t share_begin(int64_t units, int ctas, int g) {
+  if (units < (1 << 22)) return static_cast<uint32_t>(units) * static_cast<uint32_t>(g) / static_cast<uint32_t>(ctas);
+  return units * g / ctas;
+}
+// Block whose share holds unit u.
+__device__ __forceinline__ int share_owner(int64_t units, int ctas, int64_t u) {
+  int g = units < (1 << 22) ? static_cast<int>(static_cast<uint32_t>(u) * static_cast<uint32_t>(ctas) / static_cast<uint32_t>(units))
+                            : static_cast<int>(u * ctas / units);
+  while (share_begin(units, ctas, g + 1) <= u) ++g;
+  while (share_begin(units, ctas, g) > u) --g;
+  return g;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -111,17 +123,17 @@ __device__ __noinline__ void redo_rows(const PagedAttnArgs &A, const Request &rq
   __syncthreads();
 }
 
-// Joins np parts of n rows (at most JR) of KV head h, from row `from` of the request on: part i of
+// Joins np <= JP parts of n <= JR rows of KV head h, from row `from` of the request on: part i of
 // row r lies at slot(i) + r of part_o / part_ml.  A part's share of the result is a round trip to L2
 // away, so nothing here waits for one part at a time: a warp takes the references and row sums of a
 // row's parts side by side and leaves their weights in shared memory, and the threads, as many
 // groups of them as fit, then each add every kth part with eight loads in flight.  All threads of
 // the block; np = 0 writes empty rows.
-constexpr int kJoinParts = 320;  // weights kept: at least the blocks of the kernel before
-template <typename T, int D, int NT, int JR, typename S>
+constexpr int kJoinParts = 320;  // parts of an item at most: the blocks of the kernel before, and one more
+template <typename T, int D, int NT, int JR, int JP, typename S>
 __device__ __forceinline__ void join_rows(const PagedAttnArgs &A, const Request &rq, int b, int h, int from, int n, int np, S slot) {
   __shared__ unsigned bad_rows;
-  __shared__ float weight[JR][kJoinParts];
+  __shared__ float weight[JR][JP];
   __shared__ float2 row_ml[JR];
   __shared__ float4 sums[NT];
   const int tid = threadIdx.x, lane = tid & 31;

@@ -8,17 +8,19 @@
 // for long chunks (4 * 128 * 128 * D flops a tile and stream), by the K/V bytes for blocks.
 //   warps 0-3, 4-7  softmax of stream 0 and 1, one row a thread: S from TMEM, P back to TMEM (the
 //                   second product takes it from there as its A operand), results at the end
-//   warp 8          one thread issues the MMAs
-//   warps 10, 11    copy K and V rows with cp.async into a ring of shared-memory tiles; slots lie in
-//                   pages of any size, so every row has its own address, and a row that nobody sees
-//                   becomes zero
+//   warp 8          issues the MMAs
+//   warp 9          works out the block's segments ahead of the others
+//   warps 10, 11    bring K and V into a ring of shared-memory tiles: TMA boxes of as many slots as
+//                   lie together in a page (a power of two, 8 to 128), where every slot of the tile
+//                   is seen by some row; else, and for page sizes that are not a multiple of 8, rows
+//                   one by one with cp.async, those that nobody sees as zero
 // While one stream's softmax works, the tensor cores run the other stream's products.  An item of
 // more than 128 rows gives each stream 128 of them; a smaller one gives the streams every other key
 // tile of the same rows, joined at the end through TMEM.
 //
-// A call's units (key tiles of all items) are split evenly over one block an SM whatever lengths and
-// masks are: attention_plan counts them, attention_many works, attention_join_many joins the items
-// that were split.  The reference of a row moves only when a score exceeds it by more than 2^8, so
+// A call's units (key tiles of all items, and kItemCost for beginning and ending each) are split evenly
+// over one block an SM whatever lengths and masks are: attention_plan counts them, attention_many works,
+// attention_join_many joins the items that were split.  The reference of a row moves only when a score exceeds it by more than 2^8, so
 // sums are rarely rescaled; weights round to 16 bits (2^-9 relative), as the result does.
 #include "bd_paged_attn.cuh"
 
@@ -38,7 +40,12 @@ constexpr int kLoaderThreads = 64;
 // Registers a thread: the softmax warpgroups take what the third one gives up.  The sum may not
 // exceed what the block starts with (checked at the first launch).
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kSegments = 4;         // segments worked out ahead
+constexpr int kSegmentReaders = 11;  // warps that read them
 constexpr uint32_t kAtom = 16384;  // 128 rows x 128 bytes, 128-byte swizzled
+// What an item costs besides its tiles, in tiles (measured: queries in, pipeline filled and drained,
+// results out take about 16000 cycles, a tile about 2900).
+constexpr int kItemCost = 5;
 constexpr int kLag = 2;            // copy groups in flight behind the one just issued
 
 template <int D> struct Tc {
@@ -46,7 +53,8 @@ template <int D> struct Tc {
   static constexpr int kSlots = D == 128 ? 5 : 8;          // ring tiles
   static constexpr uint32_t kOffRing = 2 * kTile;          // behind the two query tiles
   static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
-  static constexpr size_t kSmem = 1024 + kOffBar + 256;
+  static constexpr uint32_t kOffSeg = kOffBar + 320;       // [kSegments] segments of 64 bytes
+  static constexpr size_t kSmem = 1024 + kOffSeg + kSegments * 64;
   // TMEM columns of stream s.  With D = 128 the weights take the place of their scores: the products
   // have one shape, so the next scores are written after the weights have been read.
   static constexpr uint32_t kS = 0, kO = 256, kP = D == 128 ? 0 : 384;
@@ -60,13 +68,102 @@ constexpr float kMove = 8.f;
 
 template <typename T> constexpr uint32_t ab_format() { return std::is_same<T, __half>::value ? 0u : 1u; }
 
-// A from TMEM, B from shared memory.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+struct PoolMaps {  // [page][KV head][slot][D], boxes of `rows` slots x 64 values, 128-byte swizzled
+  CUtensorMap k, v;
+};
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int slot, int head, int page) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(slot), "r"(head), "r"(page)
+      : "memory");
+}
+// 32 lanes x 16 consecutive columns stored from registers.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+      : "memory");
+}
+// The values of a TMEM load are there (after its wait): nothing that uses them moves before this.
+__device__ __forceinline__ void tmem_values(uint32_t (&r)[32]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+  asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+               "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_bits(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Bit x: whether column 32k + x lies at or before `last` and, from `from` on or before `sink`, in view.
+__device__ __forceinline__ uint32_t seen_bits(int last, int from, int sink) {
+  const uint32_t a = last < 0 ? 0u : last >= 31 ? ~0u : (2u << last) - 1u;
+  const uint32_t b = from <= 0 ? ~0u : from > 31 ? 0u : ~0u << from;
+  const uint32_t c = sink <= 0 ? 0u : sink > 31 ? ~0u : (1u << sink) - 1u;
+  return a & (b | c);
+}
+
+// Products issued by one thread (`lead`) of a warp that runs the issuing code as a whole: in uniform
+// control flow the operands stay in uniform registers (issued from a one-thread branch the same code
+// took about twice as long per product, more than the product itself).
+__device__ __forceinline__ uint32_t elect_lead() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+template <bool ADD> __device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(lead), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+// A from TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(lead), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 
@@ -75,19 +172,29 @@ struct ItemTiles {
   int sinks, first, count;
   __device__ int at(int t) const { return t < sinks ? t : first + t - sinks; }
 };
-__device__ __forceinline__ ItemTiles item_tiles(const PagedArgs &a, const Request &rq, int qt) {
+// Rows of the item list entry qt, and the slots of its first and last row (rows * group < 2^30).
+struct ItemRows {
+  int r0, n, p_low, p_high;  // n <= 0: none
+};
+__device__ __forceinline__ ItemRows item_rows(const PagedArgs &a, const Request &rq, int qt) {
+  ItemRows x;
+  x.r0 = qt * kItemRows;
+  x.n = min(rq.rows * a.group - x.r0, kItemRows);
+  x.p_low = rq.n - rq.rows + x.r0 / static_cast<uint32_t>(a.group);
+  x.p_high = rq.n - rq.rows + (x.r0 + max(x.n, 1) - 1) / static_cast<uint32_t>(a.group);
+  return x;
+}
+__device__ __forceinline__ ItemTiles item_tiles(const PagedArgs &a, const ItemRows &x) {
   ItemTiles t = {0, 0, 0};
-  const int64_t r0 = static_cast<int64_t>(qt) * kItemRows, R = static_cast<int64_t>(rq.rows) * a.group;
-  if (r0 >= R) return t;
-  const int base = rq.n - rq.rows;
-  const int p_high = base + static_cast<int>(((r0 + kItemRows < R ? r0 + kItemRows : R) - 1) / a.group);
-  if (p_high < 0) return t;
-  const int first = window_first(a, max(0, base + static_cast<int>(r0 / a.group)));
+  if (x.n <= 0 || x.p_high < 0) return t;
+  const int first = window_first(a, max(0, x.p_low));
   t.first = first / kTileSlots;
   t.sinks = min((min(a.n_sink, first) + kTileSlots - 1) / kTileSlots, t.first);
-  t.count = t.sinks + p_high / kTileSlots + 1 - t.first;
+  t.count = t.sinks + x.p_high / kTileSlots + 1 - t.first;
   return t;
 }
+// Units of one KV head of an item.
+__device__ __forceinline__ int item_units(const ItemTiles &t) { return t.count > 0 ? t.count + kItemCost : 0; }
 __device__ __forceinline__ int many_ctas_used(int64_t units, int most) {
   return static_cast<int>(units < 1 ? 1 : units < most ? units : most);
 }
@@ -109,7 +216,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan(const __grid_cons
     int64_t x = 0;
     if (i < N) {
       const int b = i / nqt;
-      x = static_cast<int64_t>(item_tiles(a, request_of(a, b), i - b * nqt).count) * a.n_kv_heads;
+      x = static_cast<int64_t>(item_units(item_tiles(a, item_rows(a, request_of(a, b), i - b * nqt)))) * a.n_kv_heads;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -136,53 +243,19 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan(const __grid_cons
   for (int i = tid; i < N; i += kPlanThreads) {
     const int64_t s = A.unit_start[i], e = A.unit_start[i + 1];
     if (s == e) continue;
-    int g = static_cast<int>(s * ctas / units);
-    while (share_begin(units, ctas, g) < s) ++g;
+    int g = share_owner(units, ctas, s);
+    if (share_begin(units, ctas, g) < s) ++g;
     for (; g < ctas && share_begin(units, ctas, g) < e; ++g) A.cta_item[g] = i;
   }
 }
 
 // ------------------------------------------------------------------ the block's segments
-// A segment: tiles [t0, t1) of one item and KV head.
-struct Segment {
-  Request rq;
-  ItemTiles tl;
-  int b, h, qt, t0, t1;
-  bool whole, split;  // split: at most 128 rows, the streams share them
-  int64_t u;          // first unit
-};
-struct Walk {
-  int64_t u, end;
-  int i;
-  __device__ Walk(const PagedAttnArgs &A, int64_t units, int ctas) {
-    u = share_begin(units, ctas, blockIdx.x);
-    end = share_begin(units, ctas, blockIdx.x + 1);
-    i = A.cta_item[blockIdx.x];
-  }
-  __device__ bool next(const PagedAttnArgs &A, int nqt, Segment &s) {
-    if (u >= end) return false;
-    while (A.unit_start[i + 1] <= u) ++i;
-    const PagedArgs &a = A.p;
-    s.b = i / nqt;
-    s.qt = i - s.b * nqt;
-    s.rq = request_of(a, s.b);
-    s.tl = item_tiles(a, s.rq, s.qt);
-    const int64_t in = u - A.unit_start[i];
-    s.h = static_cast<int>(in / s.tl.count);
-    s.t0 = static_cast<int>(in - static_cast<int64_t>(s.h) * s.tl.count);
-    s.t1 = static_cast<int>(end - u < s.tl.count - s.t0 ? s.t0 + (end - u) : s.tl.count);
-    s.whole = s.t0 == 0 && s.t1 == s.tl.count;
-    s.split = static_cast<int64_t>(s.rq.rows) * a.group - static_cast<int64_t>(s.qt) * kItemRows <= 128;
-    s.u = u;
-    u += s.t1 - s.t0;
-    return true;
-  }
-};
-
 struct Bars {
-  uint64_t *full, *empty;                    // ring tiles
-  uint64_t *s_full, *p_full, *o_full, *q_full;  // of each stream
-  volatile int *stop;                        // a wait gave up: every role ends
+  uint64_t *full, *empty;                       // ring tiles
+  uint64_t *s_full, *p_full, *o_full, *q_full;  // of each stream (p_full: of each half of a tile's slots)
+  uint64_t *seg_full, *seg_empty;               // segments
+  uint64_t *x_ready, *x_done;                   // stream 1's part of a segment they share
+  volatile int *stop;                           // a wait gave up: every role ends
 };
 
 __device__ __forceinline__ bool wait_or_stop(const Bars &B, uint64_t *bar, uint32_t parity) {
@@ -195,42 +268,151 @@ __device__ __forceinline__ bool wait_warp(const Bars &B, uint64_t *bar, uint32_t
   return __all_sync(0xffffffffu, wait_or_stop(B, bar, parity));
 }
 
+// Key tiles t0 .. t1-1 of one item and KV head.
+struct __align__(16) Segment {
+  int b, h, t0, t1;              // t0 == t1: no more
+  int row0, base;                // request: first row of the call; slot of its row 0
+  int r0, n;                     // the item's rows (of the request's rows * group)
+  int p_low, p_high;             // slots of its first and last row
+  int sinks, first;              // ItemTiles
+  int whole, split;              // all of the item; at most 128 rows (the streams share them)
+  int len;                       // slots of the request
+  int pad;
+  __device__ int tile(int t) const { return t < sinks ? t : first + t - sinks; }
+};
+static_assert(sizeof(Segment) == 64, "segment ring");
+
+// Reads the segments in order: seg = next() until it is null; done() when it is not needed any more.
+struct Segments {
+  const Bars &B;
+  const Segment *ring;
+  uint32_t k = 0;
+  __device__ Segments(const Bars &b, const Segment *r) : B(b), ring(r) {}
+  __device__ const Segment *next() {
+    if (!wait_warp(B, &B.seg_full[k % kSegments], (k / kSegments) & 1)) return nullptr;
+    const Segment *s = ring + k % kSegments;
+    return s->t0 == s->t1 ? nullptr : s;
+  }
+  __device__ void done(int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&B.seg_empty[k % kSegments]);
+    ++k;
+  }
+};
+
+// One thread works them out.
+__device__ void segment_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, Segment *ring, const Bars &B) {
+  const PagedArgs &a = A.p;
+  int64_t u = share_begin(units, ctas, blockIdx.x);
+  const int64_t end = share_begin(units, ctas, blockIdx.x + 1);
+  int i = A.cta_item[blockIdx.x];
+  for (uint32_t k = 0;; ++k) {
+    Segment s = {};
+    while (u < end && s.t0 == s.t1) {
+      while (A.unit_start[i + 1] <= u) ++i;
+      s.b = i / nqt;
+      const Request rq = request_of(a, s.b);
+      const ItemRows ir = item_rows(a, rq, i - s.b * nqt);
+      const ItemTiles tl = item_tiles(a, ir);
+      const uint32_t in = static_cast<uint32_t>(u - A.unit_start[i]), per = item_units(tl);  // below 2^31: checked by the host
+      s.h = in / per;
+      const int from = in - s.h * per, to = end - u < per - from ? from + static_cast<int>(end - u) : per;
+      s.t0 = min(from, tl.count);  // the units behind the tiles hold nothing
+      s.t1 = min(to, tl.count);
+      u += to - from;
+      s.row0 = rq.row0;
+      s.base = rq.n - rq.rows;
+      s.r0 = ir.r0;
+      s.n = ir.n;
+      s.p_low = ir.p_low;
+      s.p_high = ir.p_high;
+      s.sinks = tl.sinks;
+      s.first = tl.first;
+      s.whole = s.t0 == 0 && s.t1 == tl.count;
+      s.split = ir.n <= 128;
+      s.len = rq.n;
+    }
+    if (k >= kSegments && !wait_or_stop(B, &B.seg_empty[k % kSegments], ((k / kSegments) - 1) & 1)) return;
+    ring[k % kSegments] = s;
+    mbar_arrive(&B.seg_full[k % kSegments]);
+    if (s.t0 == s.t1) return;
+  }
+}
+
 // ------------------------------------------------------------------ copies
-// Warp w of the two copies rows 64w .. 64w+63 of every tile; lane l holds the places of rows 64w + l
-// and 64w + 32 + l.  Copies are announced kLag groups later, when they have landed: the writing threads
-// order them before the tensor cores' reads (async proxy) and arrive.
+// Both warps arrive on every tile with all their threads.  By TMA, lane l of the first warp brings
+// box l / (D/64), columns 64 (l % (D/64)) .. of it.  Row by row, warp w copies rows 64w .. 64w+63, lane
+// l holding the places of rows 64w + l and 64w + 32 + l; such copies are announced when they have
+// landed, up to kLag groups later: the writing threads order them before the tensor cores' reads
+// (async proxy) and arrive.
 template <typename T, int D>
-__device__ void load_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, uint32_t ring, const Bars &B, int warp, int lane) {
+__device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, const Segment *segs, uint32_t ring, const Bars &B,
+                          int warp, int lane) {
   constexpr uint32_t NS = Tc<D>::kSlots;
   constexpr int CPR = D / 8, RPI = 32 / CPR;
   const PagedArgs &a = A.p;
-  Walk walk(A, units, ctas);
-  Segment s;
-  uint32_t q = 0;  // copy groups issued
-  auto announce = [&](uint32_t g) {
-    fence_proxy_async_shared();
-    mbar_arrive(&B.full[g % NS]);
+  Segments walk(B, segs);
+  uint32_t q = 0, late = 0;  // groups issued; of them, the last `late` are not announced
+  auto announce = [&](uint32_t most) {
+    for (; late > most; --late) {
+      fence_proxy_async_shared();
+      mbar_arrive(&B.full[(q - late) % NS]);
+    }
   };
-  while (walk.next(A, nqt, s)) {
+  constexpr int ATOMS = D / 64;
+  const int boxes = box ? kTileSlots / box : 0;
+  const bool mine = warp == 0 && lane < boxes * ATOMS;  // this thread issues a TMA box
+  const int bx = mine ? lane / ATOMS * box : 0;         // its first row in the tile
+  while (const Segment *seg = walk.next()) {
+    const Segment s = *seg;
+    walk.done(lane);
     const int32_t *table = a.page_table + static_cast<int64_t>(s.b) * a.table_width;
     const int64_t head_off = static_cast<int64_t>(s.h) * a.head_stride;
     const T *K = static_cast<const T *>(a.k) + head_off, *V = static_cast<const T *>(a.v) + head_off;
-    const int64_t r0 = static_cast<int64_t>(s.qt) * kItemRows, R = static_cast<int64_t>(s.rq.rows) * a.group;
-    const int base = s.rq.n - s.rq.rows;
-    const int f_low = window_first(a, max(0, base + static_cast<int>(r0 / a.group)));
-    const int p_high = base + static_cast<int>(((r0 + kItemRows < R ? r0 + kItemRows : R) - 1) / a.group);
-    auto slot_of = [&](int t, int k) { return s.tl.at(min(t, s.t1 - 1)) * kTileSlots + warp * 64 + k * 32 + lane; };
+    const int f_low = window_first(a, max(0, s.p_low)), p_high = s.p_high;
+    auto slot_of = [&](int t, int k) { return s.tile(min(t, s.t1 - 1)) * kTileSlots + warp * 64 + k * 32 + lane; };
     auto page_at = [&](int t, int k) { return __ldg(table + min(slot_of(t, k), p_high) / a.page_size); };
-    int page[2] = {page_at(s.t0, 0), page_at(s.t0, 1)};
+    auto box_page = [&](int t) { return __ldg(table + min(s.tile(min(t, s.t1 - 1)) * kTileSlots + bx, p_high) / a.page_size); };
+    int page[2] = {0, 0};
+    if (box)
+      page[0] = box_page(s.t0);
+    else
+      page[0] = page_at(s.t0, 0), page[1] = page_at(s.t0, 1);
     for (int t = s.t0; t < s.t1; ++t) {
+      const int j0 = s.tile(t) * kTileSlots;
+      if (box && j0 + kTileSlots - 1 <= p_high && (j0 >= f_low || j0 + kTileSlots <= a.n_sink)) {
+        cp_async_wait<0>();
+        announce(0);
+        const int pg = static_cast<unsigned>(page[0]) < static_cast<unsigned>(a.n_pages) ? page[0] : a.n_pages;  // beyond: zeros
+        if (mine && pg == a.n_pages) atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+        page[0] = box_page(t + 1);
+        const int in_page = (j0 + bx) % a.page_size;
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t slot = q % NS;
+          if (q >= NS && !wait_warp(B, &B.empty[slot], ((q / NS) - 1) & 1)) return;
+          if (mine) {
+            mbar_arrive_expect_tx(&B.full[slot], static_cast<uint32_t>(box) * 128);
+            tma_load_4d(ring + slot * Tc<D>::kTile + (lane % ATOMS) * kAtom + bx * 128, v ? &M.v : &M.k, &B.full[slot],
+                        (lane % ATOMS) * 64, in_page, s.h, pg);
+          } else {
+            mbar_arrive(&B.full[slot]);
+          }
+          ++q;
+        }
+        continue;
+      }
+      if (box) page[0] = page_at(t, 0), page[1] = page_at(t, 1);
       int64_t off[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int j = slot_of(t, k);
         off[k] = j <= p_high && (j >= f_low || j < a.n_sink) ? page_offset(a, page[k], j) : -1;
       }
-      page[0] = page_at(t + 1, 0);
-      page[1] = page_at(t + 1, 1);
+      if (box)
+        page[0] = box_page(t + 1);
+      else
+        page[0] = page_at(t + 1, 0), page[1] = page_at(t + 1, 1);
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
         const uint32_t slot = q % NS;
@@ -241,111 +423,119 @@ __device__ void load_role(const PagedAttnArgs &A, int nqt, int64_t units, int ct
         const T *src = v ? V : K;
         const int c = lane % CPR;
         const uint32_t dst = ring + slot * Tc<D>::kTile + (c >> 3) * kAtom;
-#pragma unroll
+#pragma unroll 4
         for (int u = 0; u < 64 / RPI; ++u) {
           const int rl = u * RPI + lane / CPR, r = warp * 64 + rl;
-          const int64_t ro = __shfl_sync(0xffffffffu, off[u * RPI / 32], rl & 31);
+          const int64_t ro = __shfl_sync(0xffffffffu, u * RPI < 32 ? off[0] : off[1], rl & 31);
           cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (ro < 0 ? 0 : ro + c * 8), ro >= 0);
         }
         cp_async_commit();
         ++q;
-        if (q > kLag) {
+        ++late;
+        if (late > kLag) {
           cp_async_wait<kLag>();
-          announce(q - 1 - kLag);
+          announce(kLag);
         }
       }
     }
   }
   cp_async_wait<0>();
-  for (uint32_t g = q > kLag ? q - kLag : 0; g < q; ++g) announce(g);
+  announce(0);
 }
 
-// ------------------------------------------------------------------ products (one thread)
+// ------------------------------------------------------------------ products (one warp)
 template <typename T, int D>
-__device__ void mma_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, uint32_t sm, const Bars &B, uint32_t tmem) {
+__device__ void mma_role(const Segment *segs, uint32_t sm, const Bars &B, uint32_t tmem, int lane) {
   using C = Tc<D>;
   constexpr uint32_t NS = C::kSlots;
+  const uint32_t lead = elect_lead();
   const uint32_t idesc_s = umma_idesc(ab_format<T>(), 128, kTileSlots);
   const uint32_t idesc_o = umma_idesc(ab_format<T>(), 128, D) | (1u << 16);  // V: N-major
   const uint32_t ring = sm + C::kOffRing;
   uint32_t base = 0;           // ring group of the segment's first key tile
   uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};
   auto ready = [&](uint32_t g) {
-    const bool ok = wait_or_stop(B, &B.full[g % NS], (g / NS) & 1);
+    const bool ok = wait_warp(B, &B.full[g % NS], (g / NS) & 1);
     tc_fence_after();
     return ok;
   };
+  // descriptors differ in their address field alone (16-byte units; the ring ends below 2^18 bytes)
+  const uint64_t q0 = umma_desc_sw128(sm), k0 = umma_desc_sw128(ring), v0 = umma_desc_sw128_mn(ring, kAtom, 1024);
   auto scores = [&](int s, int qtile, uint32_t g) {
-    const uint32_t qb = sm + qtile * C::kTile, kb = ring + (g % NS) * C::kTile;
+    const uint64_t qd = q0 + qtile * (C::kTile >> 4), kd = k0 + (g % NS) * (C::kTile >> 4);
+    const uint32_t d = tmem + C::kS + s * C::kStepS;
+    mma_ss<false>(lead, d, qd, kd, idesc_s);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const uint32_t off = (kk >> 2) * kAtom + (kk & 3) * 32;
-      umma_bf16(tmem + C::kS + s * C::kStepS, umma_desc_sw128(qb + off), umma_desc_sw128(kb + off), idesc_s, kk > 0);
+    for (int kk = 1; kk < D / 16; ++kk) {
+      const uint32_t off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
+      mma_ss<true>(lead, d, qd + off, kd + off, idesc_s);
     }
-    umma_commit(&B.s_full[s]);
+    commit(lead, &B.s_full[s]);
   };
+  // the first half of the tile's slots as soon as its weights are there
   auto values = [&](int s, uint32_t g, bool add) {
-    const uint32_t vb = ring + (g % NS) * C::kTile;
+    const uint64_t vd = v0 + (g % NS) * (C::kTile >> 4);
+    const uint32_t d = tmem + C::kO + s * C::kStepO, p = tmem + C::kP + s * C::kStepP;
+    const uint32_t parity = n_p[s]++ & 1;
+    if (!wait_warp(B, &B.p_full[2 * s], parity)) return false;
+    tc_fence_after();
+    mma_ts(lead, d, p, vd, idesc_o, add);
 #pragma unroll
-    for (int kk = 0; kk < kTileSlots / 16; ++kk)
-      umma_ts(tmem + C::kO + s * C::kStepO, tmem + C::kP + s * C::kStepP + kk * 8,
-              umma_desc_sw128_mn(vb + kk * 2048, kAtom, 1024), idesc_o, add || kk > 0);
-  };
-  auto weights = [&](int s) {
-    const bool ok = wait_or_stop(B, &B.p_full[s], n_p[s]++ & 1);
+    for (int kk = 1; kk < 4; ++kk) mma_ts(lead, d, p + kk * 8, vd + kk * 128, idesc_o, 1);
+    if (!wait_warp(B, &B.p_full[2 * s + 1], parity)) return false;
     tc_fence_after();
-    return ok;
+#pragma unroll
+    for (int kk = 4; kk < 8; ++kk) mma_ts(lead, d, p + kk * 8, vd + kk * 128, idesc_o, 1);
+    return true;
   };
-  Walk walk(A, units, ctas);
-  Segment g;
-  while (walk.next(A, nqt, g)) {
-    const int nt = g.t1 - g.t0;
-    if (!wait_or_stop(B, &B.q_full[0], n_q[0]++ & 1)) return;
-    if (!g.split && !wait_or_stop(B, &B.q_full[1], n_q[1]++ & 1)) return;
+  Segments walk(B, segs);
+  while (const Segment *g = walk.next()) {
+    const int nt = __shfl_sync(0xffffffffu, g->t1 - g->t0, 0);
+    const bool split = __shfl_sync(0xffffffffu, g->split, 0) != 0;
+    walk.done(lane);
+    if (!wait_warp(B, &B.q_full[0], n_q[0]++ & 1)) return;
+    if (!split && !wait_warp(B, &B.q_full[1], n_q[1]++ & 1)) return;
     tc_fence_after();
-    if (!g.split) {  // both streams take every tile
+    if (!split) {  // both streams take every tile
       if (!ready(base)) return;
       scores(0, 0, base);
       scores(1, 1, base);
-      umma_commit(&B.empty[base % NS]);
+      commit(lead, &B.empty[base % NS]);
       for (int t = 0; t < nt; ++t) {
         const uint32_t gv = base + 2 * t + 1, gk = gv + 1;
-        if (!ready(gv) || !weights(0)) return;
-        values(0, gv, t > 0);
+        if (!ready(gv) || !values(0, gv, t > 0)) return;
         if (t + 1 < nt) {
           if (!ready(gk)) return;
           scores(0, 0, gk);
         } else {
-          umma_commit(&B.o_full[0]);
+          commit(lead, &B.o_full[0]);
         }
-        if (!weights(1)) return;
-        values(1, gv, t > 0);
-        umma_commit(&B.empty[gv % NS]);
+        if (!values(1, gv, t > 0)) return;
+        commit(lead, &B.empty[gv % NS]);
         if (t + 1 < nt) {
           scores(1, 1, gk);
-          umma_commit(&B.empty[gk % NS]);
+          commit(lead, &B.empty[gk % NS]);
         } else {
-          umma_commit(&B.o_full[1]);
+          commit(lead, &B.o_full[1]);
         }
       }
     } else {  // stream t % 2 takes tile t
       for (int t = 0; t < 2 && t < nt; ++t) {
         if (!ready(base + 2 * t)) return;
         scores(t, 0, base + 2 * t);
-        umma_commit(&B.empty[(base + 2 * t) % NS]);
+        commit(lead, &B.empty[(base + 2 * t) % NS]);
       }
       for (int t = 0; t < nt; ++t) {
         const uint32_t gv = base + 2 * t + 1, gk = base + 2 * t + 4;
         const int s = t & 1;
-        if (!ready(gv) || !weights(s)) return;
-        values(s, gv, t > 1);
-        umma_commit(&B.empty[gv % NS]);
+        if (!ready(gv) || !values(s, gv, t > 1)) return;
+        commit(lead, &B.empty[gv % NS]);
         if (t + 2 < nt) {
           if (!ready(gk)) return;
           scores(s, 0, gk);
-          umma_commit(&B.empty[gk % NS]);
+          commit(lead, &B.empty[gk % NS]);
         } else {
-          umma_commit(&B.o_full[s]);
+          commit(lead, &B.o_full[s]);
         }
       }
     }
@@ -354,79 +544,114 @@ __device__ void mma_role(const PagedAttnArgs &A, int nqt, int64_t units, int cta
 }
 
 // ------------------------------------------------------------------ softmax and results
-constexpr int kBarBoth = 1;  // named barrier of the two softmax warpgroups
+// Weights 2^(s scale - sub) of 32 columns of scores, rounded to T, to 16 TMEM columns (which lie among
+// scores taken already); their sums before the rounding are added to sum.
+template <typename T>
+__device__ __forceinline__ void weights32(const uint32_t (&w)[32], uint32_t tp, uint64_t scale2, uint64_t sub2, uint64_t (&sum)[2]) {
+  float pk[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float2 y = unpair(fma2(pair_bits(w[2 * e], w[2 * e + 1]), scale2, sub2));
+    const float y0 = exp2_fast(y.x), y1 = exp2_fast(y.y);
+    sum[e & 1] = add2(sum[e & 1], pair(y0, y1));
+    pk[e] = __uint_as_float(Pair<T>::pack(y0, y1));
+  }
+  tmem_st16(tp, pk);
+}
+// Half of a tile's weights are in TMEM: the products may take them.
+__device__ __forceinline__ void half_ready(uint64_t *bar) {
+  tmem_st_wait();
+  tc_fence_before();
+  mbar_arrive(bar);
+}
+// Columns 32k .. 32k+31 of a tile at the border of what the row sees (x <= last and (x >= from or
+// x < sink)), -inf where it sees nothing.  Such tiles are few: their loops stay rolled, for less code.
+__device__ __forceinline__ void edge32(uint32_t (&w)[32], uint32_t ts, int k, int last, int from, int sink) {
+  tmem_ld32_nowait(ts + 32 * k, w);
+  tmem_ld_wait();
+  tmem_values(w);
+  const uint32_t bits = seen_bits(last - 32 * k, from - 32 * k, sink - 32 * k);
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!(bits & (1u << x))) w[x] = 0xff800000u;
+}
+__device__ __forceinline__ float max32(const uint32_t (&w)[32]) {
+  float m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m[k] = max3(__uint_as_float(w[k]), __uint_as_float(w[k + 4]), __uint_as_float(w[k + 8]));
+    m[k] = max3(m[k], __uint_as_float(w[k + 12]), __uint_as_float(w[k + 16]));
+    m[k] = max3(m[k], __uint_as_float(w[k + 20]), __uint_as_float(w[k + 24]));
+  }
+  m[0] = max3(m[0], __uint_as_float(w[28]), __uint_as_float(w[29]));
+  m[1] = max3(m[1], __uint_as_float(w[30]), __uint_as_float(w[31]));
+  return max3(m[0], m[1], fmaxf(m[2], m[3]));
+}
 
+// Thread of row wt of stream st.
 template <typename T, int D>
-__device__ void softmax_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, uint8_t *smp, const Bars &B, uint32_t tmem,
-                             int wg, int wt) {
+__device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_t *smp, const Bars &B, uint32_t tmem, int st, int wt) {
   using C = Tc<D>;
   const PagedArgs &a = A.p;
   const uint32_t lanes = static_cast<uint32_t>(wt & ~31) << 16;  // TMEM lane of the warp's first row
-  const uint32_t ts = tmem + lanes + C::kS + wg * C::kStepS, tp = tmem + lanes + C::kP + wg * C::kStepP;
-  const uint32_t to[2] = {tmem + lanes + C::kO, tmem + lanes + C::kO + C::kStepO};
-  uint32_t n_s = 0, n_o = 0;
-  Walk walk(A, units, ctas);
-  Segment g;
-  bool ok = true;  // false once a wait gave up: what follows only keeps the warpgroups' barriers
-  while (walk.next(A, nqt, g)) {
-    ok = __all_sync(0xffffffffu, ok && !*B.stop);
-    const int64_t R = static_cast<int64_t>(g.rq.rows) * a.group;
-    const int64_t tile0 = static_cast<int64_t>(g.qt) * kItemRows + (g.split ? 0 : wg * 128);
-    const int base = g.rq.n - g.rq.rows;
+  const uint32_t ts = tmem + lanes + C::kS + st * C::kStepS, tp = tmem + lanes + C::kP + st * C::kStepP;
+  const uint32_t to0 = tmem + lanes + C::kO;
+  const uint32_t group = a.group;
+  uint32_t n_s = 0, n_o = 0, n_x = 0;
+  Segments walk(B, segs);
+  while (const Segment *g = walk.next()) {
+    const bool split = g->split;
+    const int R = g->r0 + g->n, tile0 = g->r0 + (split ? 0 : st * 128);  // the stream's rows: tile0 .. below R
     // query tile: 16 bytes a thread and step, consecutive threads along a row
-    if (ok && (wg == 0 || !g.split)) {
-      constexpr int CPR = D / 8;
-      uint8_t *qt = smp + wg * C::kTile;
+    if (st == 0 || !split) {
+      constexpr int CPR = D / 8, RPS = 128 / CPR;
+      const int c = wt % CPR;
+      const uint32_t qt = smem_u32(smp + st * C::kTile) + (c >> 3) * kAtom;
+      const T *src = static_cast<const T *>(a.q) + g->row0 * a.q_stride + g->h * a.group * D + c * 8;
 #pragma unroll 4
       for (int u = 0; u < CPR; ++u) {
-        const int x = u * 128 + wt, r = x / CPR, c = x % CPR;
-        const int64_t row = tile0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < R) {
-          const int i = static_cast<int>(row / a.group), e = static_cast<int>(row - static_cast<int64_t>(i) * a.group);
-          v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (g.rq.row0 + i) * a.q_stride +
-                                                    (g.h * a.group + e) * D + c * 8));
-        }
-        *reinterpret_cast<uint4 *>(qt + (c >> 3) * kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        const int r = u * RPS + wt / CPR, row = tile0 + r;
+        const uint32_t i = row / group, e = row - i * group;
+        cp_async16(qt + r * 128 + (((c & 7) ^ (r & 7)) << 4), row < R ? src + i * a.q_stride + e * D : a.q, row < R);
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       fence_proxy_async_shared();
-      mbar_arrive(&B.q_full[wg]);
+      mbar_arrive(&B.q_full[st]);
     }
     // what this thread's row sees: slots <= p, from f on or among the sinks; and the whole tile's rows
-    const int64_t row = tile0 + wt;
-    const bool valid = row < R;
-    const int p = valid ? base + static_cast<int>(row / a.group) : -1;
+    const int row = tile0 + wt;
+    const int p = row < R ? g->base + static_cast<int>(row / group) : -1;
     const int f = p >= 0 ? window_first(a, p) : 0;
-    const int p_low = base + static_cast<int>(tile0 / a.group);
-    const int f_high = window_first(a, max(0, base + static_cast<int>(((tile0 + 128 < R ? tile0 + 128 : R) - 1) / a.group)));
+    const int p_low = g->base + static_cast<int>(tile0 / group);
+    const int f_high = window_first(a, max(0, g->base + static_cast<int>((min(tile0 + 128, R) - 1) / group)));
+    const int step = split ? 2 : 1, t1 = g->t1;
     float ref = -INFINITY, l = 0.f;
-    const int step = g.split ? 2 : 1;
     bool any = false;
-    for (int t = g.t0 + (g.split ? wg : 0); t < g.t1 && ok; t += step) {
-      ok = wait_warp(B, &B.s_full[wg], n_s++ & 1);
-      if (!ok) break;
+#pragma unroll 1
+    for (int t = g->t0 + (split ? st : 0); t < t1; t += step) {
+      const int j0 = g->tile(t) * kTileSlots;
+      if (!wait_warp(B, &B.s_full[st], n_s++ & 1)) return;
       tc_fence_after();
+      const bool edge = !(j0 + kTileSlots - 1 <= p_low && (j0 >= f_high || j0 + kTileSlots <= a.n_sink));
       uint32_t w[4][32];
+      float m;
+      if (edge) {
+        m = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          edge32(w[0], ts, k, p - j0, f - j0, a.n_sink - j0);
+          m = fmaxf(m, max32(w[0]));
+        }
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32_nowait(ts + 32 * k, w[k]);
-      tmem_ld_wait();
-      const int j0 = g.tl.at(t) * kTileSlots;
-      if (!(j0 + kTileSlots - 1 <= p_low && (j0 >= f_high || j0 + kTileSlots <= a.n_sink))) {
-        const int lim = p - j0, from = f - j0, sink = a.n_sink - j0;  // visible: x <= lim and (x >= from or x < sink)
+        for (int k = 0; k < 4; ++k) tmem_ld32_nowait(ts + 32 * k, w[k]);
+        tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (!(k * 32 + x <= lim && (k * 32 + x >= from || k * 32 + x < sink))) w[k][x] = 0xff800000u;
+        for (int k = 0; k < 4; ++k) tmem_values(w[k]);
+        m = fmaxf(fmaxf(max32(w[0]), max32(w[1])), fmaxf(max32(w[2]), max32(w[3])));
       }
-      float mx[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        mx[k] = __uint_as_float(w[k][0]);
-#pragma unroll
-        for (int x = 1; x < 32; ++x) mx[k] = fmaxf(mx[k], __uint_as_float(w[k][x]));
-      }
-      const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2 - Head<T>::k;
+      m = m * a.scale_log2 - Head<T>::k;
       const bool move = m > ref + kMove || (ref == -INFINITY && m > -INFINITY);
       if (__any_sync(0xffffffffu, move)) {
         const float to_ref = move ? m : ref;
@@ -434,119 +659,123 @@ __device__ void softmax_role(const PagedAttnArgs &A, int nqt, int64_t units, int
         ref = to_ref;
         l *= scale;
         if (any) {  // the sums of the tiles before (complete: the scores of this tile came after them)
-          const uint32_t o = to[wg];
+          const uint32_t o = to0 + st * C::kStepO;
 #pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t x[32];
-            tmem_ld32_nowait(o + 32 * k, x);
-            tmem_ld_wait();
+          for (int k = 0; k < D / 16; ++k) {
+            float x[16];
+            tmem_ld16(o + 16 * k, x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * scale);
-            tmem_st32(o + 32 * k, x);
+            for (int e = 0; e < 16; ++e) x[e] *= scale;
+            tmem_st16(o + 16 * k, x);
           }
         }
       }
       any = true;
       const float sub = ref == -INFINITY ? 0.f : ref;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float x = exp2_fast(fmaf(__uint_as_float(w[k + (e >> 4)][2 * (e & 15)]), a.scale_log2, -sub));
-          const float y = exp2_fast(fmaf(__uint_as_float(w[k + (e >> 4)][2 * (e & 15) + 1]), a.scale_log2, -sub));
-          sum[e & 3] += x + y;
-          pk[e] = Pair<T>::pack(x, y);
+      const uint64_t scale2 = pair(a.scale_log2, a.scale_log2), sub2 = pair(-sub, -sub);
+      uint64_t sum[2] = {0, 0};
+      if (edge) {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          edge32(w[0], ts, k, p - j0, f - j0, a.n_sink - j0);
+          weights32<T>(w[0], tp + 16 * k, scale2, sub2, sum);
+          if (k & 1) half_ready(&B.p_full[2 * st + (k >> 1)]);
         }
-        tmem_st32(tp + 16 * k, pk);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          weights32<T>(w[k], tp + 16 * k, scale2, sub2, sum);
+          if (k & 1) half_ready(&B.p_full[2 * st + (k >> 1)]);
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&B.p_full[wg]);
+      const float2 sums = unpair(add2(sum[0], sum[1]));
+      l += sums.x + sums.y;
     }
-    if (ok && any) ok = wait_warp(B, &B.o_full[wg], n_o++ & 1);
+    if (any && !wait_warp(B, &B.o_full[st], n_o++ & 1)) return;
     tc_fence_after();
     float w0 = 1.f, w1 = 0.f;
-    if (g.split) {  // stream 1 hands its reference and sum over; stream 0 joins both and writes
-      float2 *xch = reinterpret_cast<float2 *>(smp + C::kTile);  // the second query tile is not used
-      if (wg == 1) xch[wt] = make_float2(ref, any ? l : 0.f);
-      tc_fence_before();
-      named_bar(kBarBoth, 256);
+    if (split) {  // stream 0 joins both streams' sums and writes; the second query tile carries (ref, l)
+      float2 *xch = reinterpret_cast<float2 *>(smp + C::kTile) + wt;
+      if (st == 1) {
+        *xch = make_float2(ref, l);
+        tc_fence_before();
+        mbar_arrive(B.x_ready);
+        if (!wait_warp(B, B.x_done, n_x++ & 1)) return;
+        tc_fence_after();
+        walk.done(wt & 31);
+        continue;
+      }
+      if (!wait_warp(B, B.x_ready, n_x++ & 1)) return;
       tc_fence_after();
-      if (wg == 0) {
-        const float2 x = xch[wt];
-        const float M = fmaxf(l == 0.f ? -INFINITY : ref, x.y == 0.f ? -INFINITY : x.x);
-        w0 = l == 0.f ? 0.f : exp2f(ref - M);
-        w1 = x.y == 0.f ? 0.f : exp2f(x.x - M);
-        l = (l == 0.f ? 0.f : w0 * l) + (x.y == 0.f ? 0.f : w1 * x.y);
-        ref = M;
-      }
+      const float2 x = *xch;
+      const float M = fmaxf(l == 0.f ? -INFINITY : ref, x.y == 0.f ? -INFINITY : x.x);
+      w0 = l == 0.f ? 0.f : exp2f(ref - M);
+      w1 = x.y == 0.f ? 0.f : exp2f(x.x - M);
+      l = (l == 0.f ? 0.f : w0 * l) + (x.y == 0.f ? 0.f : w1 * x.y);
+      ref = M;
     }
-    if (ok && (wg == 0 || !g.split)) {
-      const int slot = 2 * blockIdx.x + (g.u == share_begin(units, ctas, blockIdx.x) ? 0 : 1);
-      const int64_t part = static_cast<int64_t>(slot) * kItemRows + (g.split ? 0 : wg * 128) + wt;
-      const float inv = g.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const int i = valid ? static_cast<int>(row / a.group) : 0;
-      const int head = g.h * a.group + (valid ? static_cast<int>(row - static_cast<int64_t>(i) * a.group) : 0);
-      T *out = static_cast<T *>(A.out) + (g.rq.row0 + i) * A.out_stride + head * D;
-      bool bad = false;
-      const bool two = __any_sync(0xffffffffu, w1 != 0.f);
+    const bool valid = row < R, whole = g->whole;
+    // a block's parts: of the item that its share begins inside, and of the one that it ends inside
+    const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (g->t0 > 0 ? 0 : 1)) * kItemRows + (row - g->r0);
+    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+    const int i = valid ? row / group : 0, head = g->h * a.group + (valid ? row - i * a.group : 0);
+    T *out = static_cast<T *>(A.out) + (g->row0 + i) * A.out_stride + head * D;
+    const bool two = __any_sync(0xffffffffu, w1 != 0.f);
+    w0 = w0 == 0.f || l == 0.f ? 0.f : w0 * inv;
+    w1 *= inv;
+    bool bad = false;
 #pragma unroll 1
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t x[32];
-        tmem_ld32_nowait(to[g.split ? 0 : wg] + 32 * k, x);
-        tmem_ld_wait();
-        float o[32];
+    for (int k = 0; k < D / 32; ++k) {
+      uint32_t x[32], y[32];
+      tmem_ld32_nowait(to0 + (split ? 0 : st * C::kStepO) + 32 * k, x);
+      if (two) tmem_ld32_nowait(to0 + C::kStepO + 32 * k, y);
+      tmem_ld_wait();
+      tmem_values(x);
+      float o[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = w0 == 0.f ? 0.f : __uint_as_float(x[e]) * w0;
-        if (two) {
-          tmem_ld32_nowait(to[1] + 32 * k, x);
-          tmem_ld_wait();
+      for (int e = 0; e < 32; ++e) o[e] = w0 == 0.f ? 0.f : __uint_as_float(x[e]) * w0;
+      if (two) {
+        tmem_values(y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (w1 != 0.f) o[e] += __uint_as_float(x[e]) * w1;
-        }
-        if (!valid) continue;
-        if (g.whole) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            o[e] = l == 0.f ? 0.f : o[e] * inv;
-            bad |= !(fabsf(o[e]) <= 3.4e38f);
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4 *>(out + 32 * k + e) =
-                make_uint4(Pair<T>::pack(o[e], o[e + 1]), Pair<T>::pack(o[e + 2], o[e + 3]),
-                           Pair<T>::pack(o[e + 4], o[e + 5]), Pair<T>::pack(o[e + 6], o[e + 7]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(A.part_o + part * D + 32 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
+        for (int e = 0; e < 32; ++e)
+          if (w1 != 0.f) o[e] += __uint_as_float(y[e]) * w1;
       }
-      if (valid) {
-        if (g.whole)
-          store_lse(A, g.rq, g.h, static_cast<int>(row), ref, l);
-        else
-          A.part_ml[part] = make_float2(ref, l);
-      }
-      unsigned redo = __ballot_sync(0xffffffffu, bad);
-      while (redo) {
-        const int e = __ffs(redo) - 1;
-        redo &= redo - 1;
-        const int64_t r = tile0 + (wt & ~31) + e;
-        attend_row<T, D>(A, g.rq, g.b, static_cast<int>(r / a.group), g.h * a.group + static_cast<int>(r % a.group), wt & 31);
+      if (!valid) continue;
+      if (whole) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) bad |= !(fabsf(o[e]) <= 3.4e38f);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4 *>(out + 32 * k + e) =
+              make_uint4(Pair<T>::pack(o[e], o[e + 1]), Pair<T>::pack(o[e + 2], o[e + 3]),
+                         Pair<T>::pack(o[e + 4], o[e + 5]), Pair<T>::pack(o[e + 6], o[e + 7]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4 *>(A.part_o + part * D + 32 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
     }
     tc_fence_before();
-    if (g.split) named_bar(kBarBoth, 256);  // stream 1's sums and the exchange are read
+    if (split) mbar_arrive(B.x_done);  // stream 1's sums and its exchange are read
+    const Request rq = {g->len, g->row0, g->len - g->base};
+    if (valid) {
+      if (whole)
+        store_lse(A, rq, g->h, row, ref, l);
+      else
+        A.part_ml[part] = make_float2(ref, l);
+    }
+    const int b = g->b, h = g->h;
+    walk.done(wt & 31);
+    for (unsigned redo = __ballot_sync(0xffffffffu, bad); redo; redo &= redo - 1) {  // rows that are not finite
+      const uint32_t r = tile0 + (wt & ~31) + __ffs(redo) - 1;
+      attend_row<T, D>(A, rq, b, r / group, h * a.group + r % group, wt & 31);
+    }
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_constant__ PagedAttnArgs A, int nqt) {
+__global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_constant__ PagedAttnArgs A,
+                                                                const __grid_constant__ PoolMaps M, int box, int nqt) {
   using C = Tc<D>;
   extern __shared__ uint8_t sm_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -556,13 +785,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   B.empty = bars + C::kSlots;
   B.s_full = bars + 2 * C::kSlots;
   B.p_full = B.s_full + 2;
-  B.o_full = B.s_full + 4;
-  B.q_full = B.s_full + 6;
-  uint64_t *drain = B.s_full + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(B.s_full + 9);
+  B.o_full = B.s_full + 6;
+  B.q_full = B.s_full + 8;
+  B.seg_full = B.s_full + 10;
+  B.seg_empty = B.seg_full + kSegments;
+  B.x_ready = B.seg_empty + kSegments;
+  B.x_done = B.x_ready + 1;
+  uint64_t *drain = B.x_ready + 2;
+  static_assert((2 * C::kSlots + 10 + 2 * kSegments + 3) * 8 + 8 <= 320, "barriers");
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   int *stop = reinterpret_cast<int *>(tmem_slot + 1);
+  Segment *segs = reinterpret_cast<Segment *>(sm + C::kOffSeg);
   B.stop = stop;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&B.full[i], kLoaderThreads);
@@ -570,10 +805,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.p_full[i], 128);
+      mbar_init(&B.p_full[2 * i], 128);
+      mbar_init(&B.p_full[2 * i + 1], 128);
       mbar_init(&B.o_full[i], 1);
       mbar_init(&B.q_full[i], 128);
     }
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(&B.seg_full[i], 1);
+      mbar_init(&B.seg_empty[i], kSegmentReaders);
+    }
+    mbar_init(B.x_ready, 128);
+    mbar_init(B.x_done, 128);
     mbar_init(drain, 1);
     *stop = 0;
     fence_barrier_init();
@@ -585,7 +827,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
   const int64_t units = A.unit_start[A.p.n_requests * nqt];
@@ -593,15 +835,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   if (units > 0 && blockIdx.x < ctas) {
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      softmax_role<T, D>(A, nqt, units, ctas, sm, B, tmem, warp >> 2, tid & 127);
+      softmax_role<T, D>(A, segs, sm, B, tmem, warp >> 2, tid & 127);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
       if (warp >= 10) {
-        load_role<T, D>(A, nqt, units, ctas, smem_u32(sm + C::kOffRing), B, warp - 10, lane);
-      } else if (warp == 8 && lane == 0) {
-        mma_role<T, D>(A, nqt, units, ctas, smem_u32(sm), B, tmem);
-        umma_commit(drain);  // nothing of this block is in flight when its TMEM is freed
+        load_role<T, D>(A, M, box, segs, smem_u32(sm + C::kOffRing), B, warp - 10, lane);
+      } else if (warp == 8) {
+        mma_role<T, D>(segs, smem_u32(sm), B, tmem, lane);
+        __syncwarp();
+        commit(elect_lead(), drain);  // nothing of this block is in flight when its TMEM is freed
         mbar_wait(drain, 0);
+      } else if (lane == 0) {
+        segment_role(A, nqt, units, ctas, segs, B);
       }
     }
     __syncwarp();
@@ -613,10 +858,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
 }
 
 // ------------------------------------------------------------------ join
-// Block (x, y): rows 16y .. 16y+15 of the item that block x of the kernel before is the first to
+// Block (x, y): rows 32y .. 32y+31 of the item that block x of the kernel before is the first to
 // begin inside; and the rows before their requests' first slot.
 constexpr int kJoinManyThreads = 256;
-constexpr int kJoinManyRows = 16;
+constexpr int kJoinManyRows = 32;
+constexpr int kManyParts = 192;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinManyThreads) attention_join_many(const __grid_constant__ PagedAttnArgs A, int nqt) {
   const PagedArgs &a = A.p;
@@ -639,27 +885,57 @@ __global__ void __launch_bounds__(kJoinManyThreads) attention_join_many(const __
   if (units == 0 || g == 0 || g >= ctas) return;
   const int64_t here = share_begin(units, ctas, g), prev = share_begin(units, ctas, g - 1);
   const int i = A.cta_item[g], b = i / nqt, qt = i - b * nqt;
-  const int64_t start = A.unit_start[i], count = (A.unit_start[i + 1] - start) / a.n_kv_heads;
-  const int h = static_cast<int>((here - start) / count);
-  const int64_t begin = start + h * count;
-  if (here == begin || prev > begin) return;
-  int last = g;  // blocks g-1 .. last worked on it
-  while (last + 1 < ctas && share_begin(units, ctas, last + 1) < begin + count) ++last;
-  const int first = prev == begin ? 0 : 1;
+  const int64_t start = A.unit_start[i];
   const Request rq = request_of(a, b);
-  const int64_t left = static_cast<int64_t>(rq.rows) * a.group - static_cast<int64_t>(qt) * kItemRows;
-  const int r0 = blockIdx.y * kJoinManyRows;
-  const int n = static_cast<int>(left - r0 < kJoinManyRows ? left - r0 : kJoinManyRows);
+  const ItemRows ir = item_rows(a, rq, qt);
+  const int r0 = blockIdx.y * kJoinManyRows, n = min(ir.n - r0, kJoinManyRows);
   if (n <= 0) return;
-  join_rows<T, D, kJoinManyThreads, kJoinManyRows>(A, rq, b, h, qt * kItemRows + r0, n, last - g + 2, [&](int k) {
-    return static_cast<int64_t>(2 * (g - 1 + k) + (k == 0 ? first : 0)) * kItemRows + r0;
+  const ItemTiles tl = item_tiles(a, ir);
+  const uint32_t per = item_units(tl);
+  const int h = static_cast<uint32_t>(here - start) / per;
+  const int64_t begin = start + static_cast<int64_t>(h) * per;
+  if (here == begin || here - begin >= tl.count || prev > begin) return;
+  const int last = share_owner(units, ctas, begin + tl.count - 1);  // blocks g-1 .. last worked on it
+  join_rows<T, D, kJoinManyThreads, kJoinManyRows, kManyParts>(A, rq, b, h, ir.r0 + r0, n, last - g + 2, [&](int k) {
+    return static_cast<int64_t>(2 * (g - 1 + k) + (k == 0 ? 1 : 0)) * kItemRows + r0;
   });
 }
 
 // ------------------------------------------------------------------ host
-int many_blocks() { return num_sms() < kJoinParts ? num_sms() : kJoinParts; }
+int many_blocks() { return num_sms() < kManyParts - 1 ? num_sms() : kManyParts - 1; }
 int64_t item_count(int max_rows, int group) {
   return (static_cast<int64_t>(max_rows) * group + kItemRows - 1) / kItemRows;
+}
+
+// Slots of a TMA box: as many as always lie together in one page and one tile; 0: too few.
+int box_rows(int page_size) {
+  int b = kTileSlots;
+  while (page_size % b) b >>= 1;
+  return b >= 8 ? b : 0;
+}
+
+bool pool_map(CUtensorMap *m, const PagedArgs &a, const void *pool, bool bf16, int box) {
+  using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim), static_cast<cuuint64_t>(a.page_size),
+                              static_cast<cuuint64_t>(a.n_kv_heads), static_cast<cuuint64_t>(a.n_pages)};
+  const int64_t st[3] = {a.slot_stride, a.head_stride, a.page_stride};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] > 1 ? static_cast<cuuint64_t>(st[i]) * 2 : 16;
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, one[4] = {1, 1, 1, 1};
+  return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(pool), dims,
+                strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt, cudaStream_t s) {
@@ -673,7 +949,11 @@ template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt,
   }
   cudaError_t e = cudaFuncSetAttribute(attention_many<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
   if (e == cudaSuccess) e = launch_pdl(attention_plan, dim3(1), dim3(kPlanThreads), 0, s, A, nqt);
-  if (e == cudaSuccess) e = launch_pdl(attention_many<T, D>, dim3(A.n_ctas), dim3(kTcThreads), Tc<D>::kSmem, s, A, nqt);
+  PoolMaps M = {};
+  int box = box_rows(A.p.page_size);
+  const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  if (box && !(pool_map(&M.k, A.p, A.p.k, bf16, box) && pool_map(&M.v, A.p, A.p.v, bf16, box))) box = 0;
+  if (e == cudaSuccess) e = launch_pdl(attention_many<T, D>, dim3(A.n_ctas), dim3(kTcThreads), Tc<D>::kSmem, s, A, M, box, nqt);
   if (e == cudaSuccess)
     e = launch_pdl(attention_join_many<T, D>, dim3(A.n_ctas, kItemRows / kJoinManyRows), dim3(kJoinManyThreads), 0, s, A, nqt);
   return e;
@@ -691,7 +971,7 @@ size_t many_bytes(int n_requests, int max_rows, int group, int head_dim) {
 std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
   const int64_t nqt = item_count(a.max_rows, a.group);
-  if (nqt * a.n_requests > (1 << 30) || static_cast<int64_t>(a.max_rows) * a.group > (1 << 30))
+  if (nqt * a.n_requests > (1 << 30))
     return "too many rows for one call";
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = many_blocks();
