@@ -417,7 +417,7 @@ size_t bd_paged_workspace_bytes(const bd_paged_kv *kv, int n_requests, int max_r
     return 0;
   }
   // a batch made for many rows may hold few (and the other way round): the larger of the two
-  const size_t few = few_bytes(n_requests, kv->head_dim);
+  const size_t few = few_bytes(kv->head_dim);
   const size_t many = many_bytes(n_requests, max_rows, kv->n_q_heads / kv->n_kv_heads, kv->head_dim);
   return few > many ? few : many;
 }

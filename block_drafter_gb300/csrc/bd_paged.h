@@ -28,13 +28,25 @@ struct PagedAttnArgs {
   void *out;
   int64_t out_stride;
   float *lse;  // [n_rows][n_q_heads] or null
-  // workspace: the units before each request (few rows) or item (many rows), the item each block
-  // begins with (many rows), and the parts of items that several blocks work on
-  int64_t *unit_start;
-  int32_t *cta_item;
-  float *part_o;    // [2 * n_ctas][part rows][head_dim] unnormalised sums
-  float2 *part_ml;  // [2 * n_ctas][part rows] (reference in log2 units, row sum)
+  // workspace: where each block's share begins (many rows, long item lists only), the joins, and the
+  // parts of items that several blocks work on: of the item that block g's share begins inside
+  // (2g) and of the one that it ends inside (2g + 1)
+  int64_t *units;       // units before each item of the list, and in all
+  struct PagedShare *share;
+  struct PagedJoin *join;
+  float *part_o;        // [2 * n_ctas][part rows][head_dim] unnormalised sums
+  float2 *part_ml;      // [2 * n_ctas][part rows] (reference in log2 units, row sum)
   int n_ctas;
+};
+
+struct PagedShare {  // item a block's share begins in, and the units before that item
+  int64_t before;
+  int item, pad;
+};
+// Rows from .. from + n - 1 (of the request's rows * group) of KV head h, joined from the parts of
+// blocks g-1 .. g-2+np, g the place in the list; np = 0: none.
+struct PagedJoin {
+  int b, h, from, n, np, row0, len, rows;
 };
 
 // Query rows (of one KV head) a block of the few-rows attention takes.
@@ -65,7 +77,7 @@ struct PagedEvictArgs {
 };
 
 inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-size_t few_bytes(int n_requests, int head_dim);
+size_t few_bytes(int head_dim);
 size_t many_bytes(int n_requests, int max_rows, int group, int head_dim);
 std::string launch_attention_few(PagedAttnArgs a, void *workspace, int dtype, cudaStream_t s);
 std::string launch_attention_many(PagedAttnArgs a, void *workspace, int dtype, cudaStream_t s);

@@ -274,7 +274,7 @@ struct FewWarp {
   }
 };
 
-// unit_start[b] = units of the requests before b; all threads of the block.
+// start[b] = units of the requests before b; all threads of the block.
 template <int NT>
 __device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -325,9 +325,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   scan_requests<kFewThreads>(a, start, warp_sum_s);
   const int64_t units = start[a.n_requests];
   const int ctas = ctas_used(units, A.n_ctas), g = blockIdx.x;
-  if (g == 0)
-    for (int b = tid; b <= a.n_requests; b += kFewThreads) A.unit_start[b] = start[b];
-  if (g >= ctas) return;
+  for (int b = g; b < a.n_requests; b += gridDim.x)
+    if (start[b + 1] == start[b]) {  // rows without a slot
+      const Request rq = request_of(a, b);
+      empty_rows<T, D>(A, rq, rq.rows, tid, kFewThreads);
+    }
+  if (tid == 0) A.join[g].np = 0;
+  if (units == 0 || g >= ctas) return;
   const int64_t u0 = share_begin(units, ctas, g), u1 = share_begin(units, ctas, g + 1);
   uint8_t *mine = sm_raw + warp * Few<D>::kWarpBytes;
   for (int64_t u = u0; u < u1;) {
@@ -358,7 +362,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
       }
     }
     const bool whole = t0 == 0 && t1 == tl.count;
-    const int64_t slot = (2 * g + (u == u0 ? 0 : 1)) * kFewRows;
+    const int64_t slot = (2 * g + (t0 > 0 ? 0 : 1)) * kFewRows;
+    if (tid == 0 && t0 > 0 && share_begin(units, ctas, g - 1) <= u - t0)  // the first block to begin inside this head
+      A.join[g] = {b, h, 0, R, share_owner(units, ctas, u - t0 + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
     bool bad = false;
     if (tid == 0) bad_rows = 0u;
     __syncthreads();
@@ -399,57 +405,105 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   }
 }
 
-// One block per (request, KV head): joins the parts of a head that several blocks worked on, and
-// writes the rows of a request without slots.
+// ------------------------------------------------------------------ join
+// Block g: the join that block g of the few-rows kernel left, a head of which blocks g-1, g, ... each
+// worked on a part (one context of 4096 slots and 8 heads: 39 parts of 4 rows each).  All that bounds it
+// is round trips to L2, so nothing waits for one part at a time: a warp takes the references and sums of
+// a row's parts side by side and leaves their weights in shared memory; then the threads, as many groups
+// of them as fit, each add every kth part.
 constexpr int kJoinThreads = 512;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_constant__ PagedAttnArgs A) {
-  const PagedArgs &a = A.p;
-  const int h = blockIdx.x, b = blockIdx.y;
+  __shared__ unsigned bad_rows;
+  __shared__ float weight[kFewRows][kJoinParts];
+  __shared__ float2 row_ml[kFewRows];
+  __shared__ float4 sums[kJoinThreads];
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const int64_t begin = A.unit_start[b], units = A.unit_start[a.n_requests];
-  const Request rq = request_of(a, b);
-  if (rq.rows == 0) return;
-  const int count = tiles_of(a, rq).count;  // units of a head
-  int np = 0, g0 = 0, first = 0;
-  if (count > 0) {
-    const int ctas = ctas_used(units, A.n_ctas);
-    const int64_t u = begin + static_cast<int64_t>(h) * count;
-    g0 = share_owner(units, ctas, u);
-    np = share_owner(units, ctas, u + count - 1) - g0 + 1;
-    if (np == 1) return;
-    first = share_begin(units, ctas, g0) < u ? 1 : 0;  // the head began inside its first block
+  const PagedJoin j = A.join[g];
+  if (j.np == 0) return;
+  const Request rq = {j.len, j.row0, j.rows};
+  const int n = j.n;
+  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * kFewRows; };
+  if (tid == 0) bad_rows = 0u;
+  if (warp < n) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < j.np; i += 32) {
+      const float2 x = __ldcg(A.part_ml + slot(i) + warp);
+      const float mn = x.y == 0.f ? m : fmaxf(m, x.x);
+      l = (l == 0.f ? 0.f : l * exp2f(m - mn)) + (x.y == 0.f ? 0.f : x.y * exp2f(x.x - mn));
+      m = mn;
+      weight[warp][i] = x.y == 0.f ? -INFINITY : x.x;
+    }
+    const float M = warp_max(m);
+    const float L = warp_sum(l == 0.f ? 0.f : l * exp2f(m - M));
+    for (int i = lane; i < j.np; i += 32) {
+      const float x = weight[warp][i];
+      weight[warp][i] = x == -INFINITY ? 0.f : exp2f(x - M);
+    }
+    if (lane == 0) row_ml[warp] = make_float2(M, L);
   }
-  join_rows<T, D, kJoinThreads, kFewRows, kJoinParts>(A, rq, b, h, 0, rq.rows * a.group, np, [&](int i) {
-    return static_cast<int64_t>(2 * (g0 + i) + (i == 0 ? first : 0)) * kFewRows;
-  });
+  __syncthreads();
+  const int pieces = n * (D / 4);  // at most kJoinThreads
+  const int groups = kJoinThreads / pieces, k = tid / pieces, c = tid - k * pieces;
+  const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (k < groups) {
+#pragma unroll 4
+    for (int i = k; i < j.np; i += groups) {
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
+      const float w = weight[r][i];
+      if (w != 0.f) {
+        o.x += w * v.x;
+        o.y += w * v.y;
+        o.z += w * v.z;
+        o.w += w * v.w;
+      }
+    }
+  }
+  if (groups > 1) {
+    sums[tid] = o;
+    __syncthreads();
+    if (k == 0)
+      for (int i = 1; i < groups; ++i) {
+        const float4 v = sums[tid + i * pieces];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+  }
+  const bool bad = k == 0 && finish4<T>(A, rq, j.h, j.from + r, d, o, row_ml[r].x, row_ml[r].y);
+  if (bad) atomicOr(&bad_rows, 1u << r);
+  if (__syncthreads_or(bad)) redo_rows<T, D, kJoinThreads>(A, rq, j.b, j.h, j.from, n, bad_rows);
 }
+static_assert(kFewRows * 128 / 4 <= kJoinThreads, "a block's pieces");
 
 // ------------------------------------------------------------------ host
 static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts - 1; }
 
-size_t few_bytes(int n_requests, int head_dim) {
+size_t few_bytes(int head_dim) {
   const size_t parts = 2 * static_cast<size_t>(few_blocks()) * kFewRows;
-  return align256((static_cast<size_t>(n_requests) + 1) * 8) + align256(parts * head_dim * 4) + align256(parts * 8);
+  return align256(few_blocks() * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
 }
 
 template <typename T, int D>
 static cudaError_t launch(const PagedAttnArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
   auto kernel = a.max_rows * a.group <= 8 ? attention_few<T, D, true> : attention_few<T, D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
-  if (e == cudaSuccess) e = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Few<D>::kSmem, s, A);
-  if (e == cudaSuccess) e = launch_pdl(attention_join<T, D>, dim3(a.n_kv_heads, a.n_requests), dim3(kJoinThreads), 0, s, A);
-  return e;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Few<D>::kSmem, s, A);
+  return f == cudaSuccess ? launch_pdl(attention_join<T, D>, dim3(A.n_ctas), dim3(kJoinThreads), 0, s, A) : f;
 }
 
 std::string launch_attention_few(PagedAttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = few_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
-  A.unit_start = reinterpret_cast<int64_t *>(p);
-  p += align256((static_cast<size_t>(A.p.n_requests) + 1) * 8);
+  A.join = reinterpret_cast<PagedJoin *>(p);
+  p += align256(A.n_ctas * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);
   p += align256(parts * A.p.head_dim * 4);
   A.part_ml = reinterpret_cast<float2 *>(p);

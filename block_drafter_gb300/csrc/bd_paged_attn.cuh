@@ -123,78 +123,19 @@ __device__ __noinline__ void redo_rows(const PagedAttnArgs &A, const Request &rq
   __syncthreads();
 }
 
-// Joins np <= JP parts of n <= JR rows of KV head h, from row `from` of the request on: part i of
-// row r lies at slot(i) + r of part_o / part_ml.  A part's share of the result is a round trip to L2
-// away, so nothing here waits for one part at a time: a warp takes the references and row sums of a
-// row's parts side by side and leaves their weights in shared memory, and the threads, as many
-// groups of them as fit, then each add every kth part with eight loads in flight.  All threads of
-// the block; np = 0 writes empty rows.
-constexpr int kJoinParts = 320;  // parts of an item at most: the blocks of the kernel before, and one more
-template <typename T, int D, int NT, int JR, int JP, typename S>
-__device__ __forceinline__ void join_rows(const PagedAttnArgs &A, const Request &rq, int b, int h, int from, int n, int np, S slot) {
-  __shared__ unsigned bad_rows;
-  __shared__ float weight[JR][JP];
-  __shared__ float2 row_ml[JR];
-  __shared__ float4 sums[NT];
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (tid == 0) bad_rows = 0u;
-  for (int r = tid >> 5; r < n; r += NT / 32) {
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < np; i += 32) {
-      const float2 x = __ldcg(A.part_ml + slot(i) + r);
-      const float mn = x.y == 0.f ? m : fmaxf(m, x.x);
-      l = (l == 0.f ? 0.f : l * exp2f(m - mn)) + (x.y == 0.f ? 0.f : x.y * exp2f(x.x - mn));
-      m = mn;
-      weight[r][i] = x.y == 0.f ? -INFINITY : x.x;
-    }
-    const float M = warp_max(m);
-    const float L = warp_sum(l == 0.f ? 0.f : l * exp2f(m - M));
-    for (int i = lane; i < np; i += 32) {
-      const float x = weight[r][i];
-      weight[r][i] = x == -INFINITY ? 0.f : exp2f(x - M);
-    }
-    if (lane == 0) row_ml[r] = make_float2(M, L);
+constexpr int kJoinParts = 320;  // parts of an item at most: the blocks of a kernel, and one more
+
+// Rows of request rq that have no slot of their own or before them: zeros.  `step` threads, this one
+// the tid-th.
+template <typename T, int D>
+__device__ void empty_rows(const PagedAttnArgs &A, const Request &rq, int rows, int tid, int step) {
+  const int64_t per = static_cast<int64_t>(A.p.n_kv_heads) * A.p.group;
+  for (int64_t x = tid; x < rows * per * (D / 8); x += step) {
+    const int64_t hr = x / (D / 8), i = hr / per, head = hr - i * per;
+    T *out = static_cast<T *>(A.out) + (rq.row0 + i) * A.out_stride + head * D + (x - hr * (D / 8)) * 8;
+    *reinterpret_cast<uint4 *>(out) = make_uint4(0, 0, 0, 0);
+    if (A.lse && x == hr * (D / 8)) A.lse[(rq.row0 + i) * per + head] = -INFINITY;
   }
-  __syncthreads();
-  const int pieces = n * (D / 4);
-  const int groups = pieces < NT ? NT / pieces : 1;
-  bool bad = false;
-  for (int c0 = 0; c0 < pieces; c0 += NT) {
-    const int k = groups > 1 ? tid / pieces : 0, c = groups > 1 ? tid - k * pieces : c0 + tid;
-    const bool mine = k < groups && c < pieces;
-    const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mine) {
-#pragma unroll 8
-      for (int i = k; i < np; i += groups) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
-        const float w = weight[r][i];
-        if (w != 0.f) {
-          o.x += w * v.x;
-          o.y += w * v.y;
-          o.z += w * v.z;
-          o.w += w * v.w;
-        }
-      }
-    }
-    if (groups > 1) {
-      sums[tid] = o;
-      __syncthreads();
-      if (k > 0) continue;
-      for (int i = 1; i < groups; ++i) {
-        const float4 v = sums[tid + i * pieces];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
-      }
-    }
-    if (mine && finish4<T>(A, rq, h, from + r, d, o, row_ml[r].x, row_ml[r].y)) {
-      atomicOr(&bad_rows, 1u << r);
-      bad = true;
-    }
-  }
-  if (__syncthreads_or(bad)) redo_rows<T, D, NT>(A, rq, b, h, from, n, bad_rows);
 }
 
 }  // namespace bd

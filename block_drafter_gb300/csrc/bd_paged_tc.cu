@@ -19,8 +19,7 @@
 // tile of the same rows, joined at the end through TMEM.
 //
 // A call's units (key tiles of all items, and kItemCost for beginning and ending each) are split evenly
-// over one block an SM whatever lengths and masks are: attention_plan counts them, attention_many works,
-// attention_join_many joins the items that were split.  The reference of a row moves only when a score exceeds it by more than 2^8, so
+// over one block an SM whatever lengths and masks are; attention_join joins the items that were split.  The reference of a row moves only when a score exceeds it by more than 2^8, so
 // sums are rarely rescaled; weights round to 16 bits (2^-9 relative), as the result does.
 #include "bd_paged_attn.cuh"
 
@@ -54,7 +53,7 @@ template <int D> struct Tc {
   static constexpr uint32_t kOffRing = 2 * kTile;          // behind the two query tiles
   static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
   static constexpr uint32_t kOffSeg = kOffBar + 320;       // [kSegments] segments of 64 bytes
-  static constexpr size_t kSmem = 1024 + kOffSeg + kSegments * 64;
+  static constexpr size_t kSmem = 1024 + kOffSeg + kSegments * 64 + 128;  // and the share's beginning
   // TMEM columns of stream s.  With D = 128 the weights take the place of their scores: the products
   // have one shape, so the next scores are written after the weights have been read.
   static constexpr uint32_t kS = 0, kO = 256, kP = D == 128 ? 0 : 384;
@@ -199,53 +198,59 @@ __device__ __forceinline__ int many_ctas_used(int64_t units, int most) {
   return static_cast<int>(units < 1 ? 1 : units < most ? units : most);
 }
 
-// ------------------------------------------------------------------ plan
-// unit_start[i] = units before item list entry i = b * nqt + qt (every KV head of it), and the entry
-// each block's share begins in.  One block.
+// ------------------------------------------------------------------ shares
+// The item list: entry i = b * nqt + qt is rows 256 qt .. of request b, every KV head of it.
+__device__ __forceinline__ int list_units(const PagedArgs &a, int nqt, int i) {
+  const int b = i / nqt;
+  return item_units(item_tiles(a, item_rows(a, request_of(a, b), i - b * nqt)));
+}
+// Inclusive sum over the block (NT threads; two uses need a barrier between them), and its total.
+template <int NT> __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *warp_total, int64_t &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_total[warp] = x;
+  __syncthreads();
+  total = 0;
+#pragma unroll 1
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w == warp) x += total;
+    total += warp_total[w];
+  }
+  return x;
+}
+
+// Lists of up to kListEach entries a thread are summed up by every block itself; longer ones by this
+// kernel (one block).
+constexpr int kListEach = 3;
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) attention_plan(const __grid_constant__ PagedAttnArgs A, int nqt) {
   __shared__ int64_t warp_total[kPlanThreads / 32];
   const PagedArgs &a = A.p;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int N = a.n_requests * nqt;
+  const int tid = threadIdx.x, N = a.n_requests * nqt;
   pdl_wait();
   pdl_trigger();
   int64_t base = 0;
   for (int i0 = 0; i0 < N; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    int64_t x = 0;
-    if (i < N) {
-      const int b = i / nqt;
-      x = static_cast<int64_t>(item_units(item_tiles(a, item_rows(a, request_of(a, b), i - b * nqt)))) * a.n_kv_heads;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_total[warp] = x;
-    __syncthreads();
-    int64_t t = warp_total[lane];  // 32 warps
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
-    }
-    const int64_t before = __shfl_sync(0xffffffffu, t, warp > 0 ? warp - 1 : 0);
-    if (i < N) A.unit_start[i + 1] = base + x + (warp > 0 ? before : 0);
-    base += __shfl_sync(0xffffffffu, t, 31);
+    int64_t total;
+    const int64_t x = block_sum<kPlanThreads>(i < N ? static_cast<int64_t>(list_units(a, nqt, i)) * a.n_kv_heads : 0, warp_total, total);
+    if (i < N) A.units[i + 1] = base + x;
+    base += total;
     __syncthreads();
   }
-  if (tid == 0) A.unit_start[0] = 0;
+  if (tid == 0) A.units[0] = 0;
   __syncthreads();
-  const int64_t units = base;
-  const int ctas = many_ctas_used(units, A.n_ctas);
+  const int ctas = many_ctas_used(base, A.n_ctas);
   for (int i = tid; i < N; i += kPlanThreads) {
-    const int64_t s = A.unit_start[i], e = A.unit_start[i + 1];
+    const int64_t s = A.units[i], e = A.units[i + 1];
     if (s == e) continue;
-    int g = share_owner(units, ctas, s);
-    if (share_begin(units, ctas, g) < s) ++g;
-    for (; g < ctas && share_begin(units, ctas, g) < e; ++g) A.cta_item[g] = i;
+    int g = share_owner(base, ctas, s);
+    if (share_begin(base, ctas, g) < s) ++g;
+    for (; g < ctas && share_begin(base, ctas, g) < e; ++g) A.share[g] = {s, i, 0};
   }
 }
 
@@ -300,26 +305,32 @@ struct Segments {
   }
 };
 
-// One thread works them out.
-__device__ void segment_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, Segment *ring, const Bars &B) {
+// One thread works them out, from item i of the list on, which begins at unit `before`.
+__device__ void segment_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, int i, int64_t before, Segment *ring, const Bars &B) {
   const PagedArgs &a = A.p;
-  int64_t u = share_begin(units, ctas, blockIdx.x);
-  const int64_t end = share_begin(units, ctas, blockIdx.x + 1);
-  int i = A.cta_item[blockIdx.x];
+  const int g = blockIdx.x;
+  int64_t u = share_begin(units, ctas, g);
+  const int64_t end = share_begin(units, ctas, g + 1);
   for (uint32_t k = 0;; ++k) {
     Segment s = {};
     while (u < end && s.t0 == s.t1) {
-      while (A.unit_start[i + 1] <= u) ++i;
       s.b = i / nqt;
+      const int qt = i - s.b * nqt;
       const Request rq = request_of(a, s.b);
-      const ItemRows ir = item_rows(a, rq, i - s.b * nqt);
+      const ItemRows ir = item_rows(a, rq, qt);
       const ItemTiles tl = item_tiles(a, ir);
-      const uint32_t in = static_cast<uint32_t>(u - A.unit_start[i]), per = item_units(tl);  // below 2^31: checked by the host
-      s.h = in / per;
+      const int per = item_units(tl);
+      const int64_t all = static_cast<int64_t>(per) * a.n_kv_heads;
+      if (u >= before + all) {  // to the next item, past what the request does not fill
+        i = ir.n > 0 ? i + 1 : (s.b + 1) * nqt;
+        before += all;
+        continue;
+      }
+      const uint32_t in = static_cast<uint32_t>(u - before);  // below 2^31: checked by the host
+      s.h = in / static_cast<uint32_t>(per);
       const int from = in - s.h * per, to = end - u < per - from ? from + static_cast<int>(end - u) : per;
       s.t0 = min(from, tl.count);  // the units behind the tiles hold nothing
       s.t1 = min(to, tl.count);
-      u += to - from;
       s.row0 = rq.row0;
       s.base = rq.n - rq.rows;
       s.r0 = ir.r0;
@@ -331,6 +342,9 @@ __device__ void segment_role(const PagedAttnArgs &A, int nqt, int64_t units, int
       s.whole = s.t0 == 0 && s.t1 == tl.count;
       s.split = ir.n <= 128;
       s.len = rq.n;
+      if (s.t0 > 0 && s.t0 < s.t1 && share_begin(units, ctas, g - 1) <= u - from)  // the first block to begin inside it
+        A.join[g] = {s.b, s.h, ir.r0, ir.n, share_owner(units, ctas, u - from + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
+      u += to - from;
     }
     if (k >= kSegments && !wait_or_stop(B, &B.seg_empty[k % kSegments], ((k / kSegments) - 1) & 1)) return;
     ring[k % kSegments] = s;
@@ -796,6 +810,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   int *stop = reinterpret_cast<int *>(tmem_slot + 1);
   Segment *segs = reinterpret_cast<Segment *>(sm + C::kOffSeg);
+  PagedShare *share = reinterpret_cast<PagedShare *>(segs + kSegments);
+  int64_t *warp_total = reinterpret_cast<int64_t *>(share + 1);  // [warps]
   B.stop = stop;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
@@ -830,7 +846,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
-  const int64_t units = A.unit_start[A.p.n_requests * nqt];
+  // where this block's share begins: summed up here, or by attention_plan
+  const int N = A.p.n_requests * nqt;
+  int64_t units;
+  if (tid == 0) A.join[blockIdx.x].np = 0;
+  if (N <= kListEach * kTcThreads) {
+    int64_t x[kListEach], mine = 0;
+#pragma unroll
+    for (int k = 0; k < kListEach; ++k) {
+      const int i = tid * kListEach + k;
+      x[k] = i < N ? static_cast<int64_t>(list_units(A.p, nqt, i)) * A.p.n_kv_heads : 0;
+      mine += x[k];
+    }
+    int64_t before = block_sum<kTcThreads>(mine, warp_total, units) - mine;
+    const int64_t u = share_begin(units, many_ctas_used(units, A.n_ctas), blockIdx.x);
+#pragma unroll
+    for (int k = 0; k < kListEach; ++k) {
+      if (u >= before && u < before + x[k]) *share = {before, tid * kListEach + k, 0};
+      before += x[k];
+    }
+    __syncthreads();
+  } else {
+    units = A.units[N];
+    if (tid == 0 && blockIdx.x < many_ctas_used(units, A.n_ctas)) *share = A.share[blockIdx.x];
+    __syncthreads();
+  }
   const int ctas = many_ctas_used(units, A.n_ctas);
   if (units > 0 && blockIdx.x < ctas) {
     if (warp < 8) {
@@ -846,11 +886,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
         commit(elect_lead(), drain);  // nothing of this block is in flight when its TMEM is freed
         mbar_wait(drain, 0);
       } else if (lane == 0) {
-        segment_role(A, nqt, units, ctas, segs, B);
+        segment_role(A, nqt, units, ctas, share->item, share->before, segs, B);
       }
     }
     __syncwarp();
   }
+  if (warp >= 10)
+    for (int b = blockIdx.x; b < A.p.n_requests; b += gridDim.x) {  // rows before their requests' first slot
+      const Request rq = request_of(A.p, b);
+      empty_rows<T, D>(A, rq, max(0, rq.rows - rq.n), tid - 320, 64);
+    }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -858,51 +903,65 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
 }
 
 // ------------------------------------------------------------------ join
-// Block (x, y): rows 32y .. 32y+31 of the item that block x of the kernel before is the first to
-// begin inside; and the rows before their requests' first slot.
-constexpr int kJoinManyThreads = 256;
-constexpr int kJoinManyRows = 32;
-constexpr int kManyParts = 192;
+// Warp y of list place g: row y of the join that block g left.  The lanes hold the weights of up to 32
+// parts side by side (more are rare: they go round again), then add the parts, four columns (two with
+// D = 64) a lane.
+constexpr int kJoinWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinManyThreads) attention_join_many(const __grid_constant__ PagedAttnArgs A, int nqt) {
-  const PagedArgs &a = A.p;
-  const int g = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __grid_constant__ PagedAttnArgs A) {
+  constexpr int C = D / 32;
+  const int g = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.y == 0)
-    for (int b = g; b < a.n_requests; b += gridDim.x) {
-      const Request rq = request_of(a, b);
-      const int64_t per = static_cast<int64_t>(a.n_kv_heads) * a.group, none = max(0, rq.rows - rq.n) * per;
-      for (int64_t x = tid; x < none * (D / 8); x += kJoinManyThreads) {
-        const int64_t hr = x / (D / 8), i = hr / per, head = hr - i * per;
-        T *out = static_cast<T *>(A.out) + (rq.row0 + i) * A.out_stride + head * D + (x - hr * (D / 8)) * 8;
-        *reinterpret_cast<uint4 *>(out) = make_uint4(0, 0, 0, 0);
-        if (A.lse && x == hr * (D / 8)) A.lse[(rq.row0 + i) * per + head] = -INFINITY;
-      }
+  const PagedJoin j = A.join[g];
+  if (j.np == 0 || r >= j.n) return;
+  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * kItemRows + r; };
+  float M = -INFINITY, L = 0.f, o[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
+  for (int i0 = 0; i0 < j.np; i0 += 32) {
+    float2 x = make_float2(-INFINITY, 0.f);
+    if (i0 + lane < j.np) x = __ldcg(A.part_ml + slot(i0 + lane));
+    if (x.y == 0.f) x.x = -INFINITY;
+    const float m = fmaxf(M, warp_max(x.x));
+    const float back = M == -INFINITY ? 0.f : exp2f(M - m), w = x.y == 0.f ? 0.f : exp2f(x.x - m);
+    L = L * back + warp_sum(w * x.y);
+    M = m;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] *= back;
+    const int n = min(32, j.np - i0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float *v = A.part_o + slot(i0 + i) * D + C * lane;
+      float y[C];
+      if constexpr (C == 4)
+        *reinterpret_cast<float4 *>(y) = __ldcg(reinterpret_cast<const float4 *>(v));
+      else
+        *reinterpret_cast<float2 *>(y) = __ldcg(reinterpret_cast<const float2 *>(v));
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (wi != 0.f) o[c] += wi * y[c];
     }
-  const int64_t units = A.unit_start[a.n_requests * nqt];
-  const int ctas = many_ctas_used(units, A.n_ctas);
-  if (units == 0 || g == 0 || g >= ctas) return;
-  const int64_t here = share_begin(units, ctas, g), prev = share_begin(units, ctas, g - 1);
-  const int i = A.cta_item[g], b = i / nqt, qt = i - b * nqt;
-  const int64_t start = A.unit_start[i];
-  const Request rq = request_of(a, b);
-  const ItemRows ir = item_rows(a, rq, qt);
-  const int r0 = blockIdx.y * kJoinManyRows, n = min(ir.n - r0, kJoinManyRows);
-  if (n <= 0) return;
-  const ItemTiles tl = item_tiles(a, ir);
-  const uint32_t per = item_units(tl);
-  const int h = static_cast<uint32_t>(here - start) / per;
-  const int64_t begin = start + static_cast<int64_t>(h) * per;
-  if (here == begin || here - begin >= tl.count || prev > begin) return;
-  const int last = share_owner(units, ctas, begin + tl.count - 1);  // blocks g-1 .. last worked on it
-  join_rows<T, D, kJoinManyThreads, kJoinManyRows, kManyParts>(A, rq, b, h, ir.r0 + r0, n, last - g + 2, [&](int k) {
-    return static_cast<int64_t>(2 * (g - 1 + k) + (k == 0 ? 1 : 0)) * kItemRows + r0;
-  });
+  }
+  const Request rq = {j.len, j.row0, j.rows};
+  const uint32_t row = j.from + r, group = A.p.group, t = row / group;
+  const int head = j.h * A.p.group + row - t * group;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<T *>(A.out) + (rq.row0 + static_cast<int>(t)) * A.out_stride + head * D + C * lane);
+  bool bad = false;
+#pragma unroll
+  for (int c = 0; c < C; c += 2) {
+    const float y0 = o[c] * inv, y1 = o[c + 1] * inv;
+    bad |= !(fabsf(y0) <= 3.4e38f) || !(fabsf(y1) <= 3.4e38f);
+    out[c / 2] = Pair<T>::pack(y0, y1);
+  }
+  if (lane == 0) store_lse(A, rq, j.h, row, M, L);
+  if (__any_sync(0xffffffffu, bad)) attend_row<T, D>(A, rq, j.b, t, head, lane);
 }
 
 // ------------------------------------------------------------------ host
-int many_blocks() { return num_sms() < kManyParts - 1 ? num_sms() : kManyParts - 1; }
+int many_blocks() { return num_sms() < kJoinParts - 1 ? num_sms() : kJoinParts - 1; }
 int64_t item_count(int max_rows, int group) {
   return (static_cast<int64_t>(max_rows) * group + kItemRows - 1) / kItemRows;
 }
@@ -948,14 +1007,17 @@ template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt,
     checked.store(true, std::memory_order_relaxed);
   }
   cudaError_t e = cudaFuncSetAttribute(attention_many<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
-  if (e == cudaSuccess) e = launch_pdl(attention_plan, dim3(1), dim3(kPlanThreads), 0, s, A, nqt);
+  if (e == cudaSuccess && A.p.n_requests * nqt > kListEach * kTcThreads)
+    e = launch_pdl(attention_plan, dim3(1), dim3(kPlanThreads), 0, s, A, nqt);
   PoolMaps M = {};
   int box = box_rows(A.p.page_size);
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   if (box && !(pool_map(&M.k, A.p, A.p.k, bf16, box) && pool_map(&M.v, A.p, A.p.v, bf16, box))) box = 0;
   if (e == cudaSuccess) e = launch_pdl(attention_many<T, D>, dim3(A.n_ctas), dim3(kTcThreads), Tc<D>::kSmem, s, A, M, box, nqt);
-  if (e == cudaSuccess)
-    e = launch_pdl(attention_join_many<T, D>, dim3(A.n_ctas, kItemRows / kJoinManyRows), dim3(kJoinManyThreads), 0, s, A, nqt);
+  if (e == cudaSuccess) {
+    const int rows = A.p.max_rows * A.p.group, most = rows < kItemRows ? rows : kItemRows;
+    e = launch_pdl(attention_join_many<T, D>, dim3(A.n_ctas, (most + kJoinWarps - 1) / kJoinWarps), dim3(32 * kJoinWarps), 0, s, A);
+  }
   return e;
 }
 
@@ -964,8 +1026,8 @@ template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt,
 size_t many_bytes(int n_requests, int max_rows, int group, int head_dim) {
   if (static_cast<int64_t>(max_rows) * group <= kFewRows) return 0;
   const size_t parts = 2 * static_cast<size_t>(many_blocks()) * kItemRows;
-  return align256((static_cast<size_t>(n_requests) * item_count(max_rows, group) + 1) * 8) + align256(many_blocks() * 4) +
-         align256(parts * head_dim * 4) + align256(parts * 8);
+  return align256((static_cast<size_t>(n_requests) * item_count(max_rows, group) + 1) * 8) +
+         align256(many_blocks() * sizeof(PagedShare)) + align256(many_blocks() * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
 }
 
 std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, cudaStream_t s) {
@@ -976,10 +1038,12 @@ std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, c
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = many_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kItemRows;
-  A.unit_start = reinterpret_cast<int64_t *>(p);
+  A.units = reinterpret_cast<int64_t *>(p);
   p += align256((static_cast<size_t>(a.n_requests) * nqt + 1) * 8);
-  A.cta_item = reinterpret_cast<int32_t *>(p);
-  p += align256(A.n_ctas * 4);
+  A.share = reinterpret_cast<PagedShare *>(p);
+  p += align256(A.n_ctas * sizeof(PagedShare));
+  A.join = reinterpret_cast<PagedJoin *>(p);
+  p += align256(A.n_ctas * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);
   p += align256(parts * a.head_dim * 4);
   A.part_ml = reinterpret_cast<float2 *>(p);
