@@ -65,50 +65,167 @@ static std::string launch_append(PagedAppendArgs &A, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ accumulated weights
-// One warp per slot j: for each row that sees it and each query head, s = q.k over the lanes'
-// D/32 columns, then exp2(s - lse / ln 2).
+// out[j] = decay in[j] + sum over rows i and heads of 2^(scale log2(e) k_j.q_i - log2(e) lse_i).
+// Bound by K's bytes for a token or a block, by the tensor cores for many rows.  A warp owns 16 slots of
+// a request: their keys are the A operand of mma.sync m16n8k16 and stay in registers while the rows of
+// the KV head pass by, 8 at a time, as B; so a slot's weights are summed in the registers of four lanes,
+// without atomics, over all rows and heads of the warp.  Few slots give a block's eight warps fewer tiles
+// and split the KV heads among them (summed through shared memory in a fixed order).
+// The order of the D products of a score is free, so both operands take it as 16-byte pieces from
+// global memory: lane l holds pieces l%4, l%4 + 4, ... of its rows, two MMA steps each.
+constexpr int kWeightWarps = 8;
+
+template <typename T> __device__ __forceinline__ void mma_kq(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma_kq<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma_kq<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// P pieces of 16 bytes (every fourth from this lane's on) of a row, zeros where p is null.
+template <int P> __device__ __forceinline__ void load_pieces(uint4 (&v)[P], const void *p) {
+#pragma unroll
+  for (int c = 0; c < P; ++c) v[c] = p ? __ldg(static_cast<const uint4 *>(p) + 4 * c) : make_uint4(0, 0, 0, 0);
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_weights_kernel(const __grid_constant__ PagedWeightsArgs A) {
+__global__ void __launch_bounds__(32 * kWeightWarps, 2) paged_weights_kernel(const __grid_constant__ PagedWeightsArgs A, int head_split) {
+  constexpr int P = D / 32;  // pieces of a row per lane
+  __shared__ float part[kWeightWarps][16];
   const PagedArgs &a = A.p;
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y, quad = lane >> 2, kq = lane & 3;
+  const int tiles = kWeightWarps / head_split;           // slot tiles of the block
+  const int hs = warp / tiles;                           // this warp's KV heads: hs, hs + head_split, ...
+  const int j0 = (blockIdx.x * tiles + warp % tiles) * 16;
   pdl_wait();
   pdl_trigger();
   const Request rq = request_of(a, b);
-  if (j >= rq.n) return;
+  if (blockIdx.x * tiles * 16 >= rq.n) return;
   const int used = A.rows_used ? max(0, min(A.rows_used[b], rq.rows)) : rq.rows;
-  const int hq = a.n_kv_heads * a.group;
-  const int64_t off = slot_offset(a, a.page_table + static_cast<int64_t>(b) * a.table_width, j);
-  float sum = 0.f;
-  for (int h = 0; h < a.n_kv_heads && off >= 0; ++h) {
-    float k[C];
+  const int base = rq.n - rq.rows, G = a.group, hq = a.n_kv_heads * G;
+  // tokens i (slots base + i) that see some slot of the tile, and those that see all of it
+  const int j1 = min(j0 + 15, rq.n - 1);
+  const bool sinks = j0 < a.n_sink, all_sinks = j1 < a.n_sink;
+  int i_lo = max(0, j0 - base), i_hi = used;  // [i_lo, i_hi)
+  int f_lo = max(0, j1 - base), f_hi = used;
+  if (a.window > 0) {
+    auto behind = [&](int j) {  // the first token that does not see slot j any more, 0 .. used
+      const int64_t i = static_cast<int64_t>(j) + a.window - base;
+      return static_cast<int>(i < 0 ? 0 : i < used ? i : used);
+    };
+    if (!sinks) i_hi = behind(j1);
+    if (!all_sinks) f_hi = behind(j0);
+  }
+  float acc[2] = {0.f, 0.f};  // slots j0 + quad, + 8
+  if (j0 < rq.n && i_lo < i_hi) {
+    const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+    const T *K[2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) k[c] = to_f(static_cast<const T *>(a.k)[off + h * a.head_stride + c * 32 + lane]);
-    for (int i = max(0, j - (rq.n - rq.rows)); i < used; ++i) {
-      const int p = rq.n - rq.rows + i;
-      if (j >= a.n_sink && j < window_first(a, p)) break;
-      for (int g = 0; g < a.group; ++g) {
-        const int head = h * a.group + g;
-        const T *q = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + head * D;
-        float s = 0.f;
+    for (int x = 0; x < 2; ++x) {
+      const int j = j0 + quad + 8 * x;
+      const int64_t off = j < rq.n ? slot_offset(a, table, j) : -1;
+      K[x] = off < 0 ? nullptr : static_cast<const T *>(a.k) + off + kq * 8;
+    }
+    const int t0 = i_lo * G / 8, t1 = (i_hi * G + 7) / 8;  // row tiles
+    const int full0 = f_lo * G, full1 = f_hi * G;          // rows that see all of the tile's slots
+    const int R = i_hi * G;
+    uint4 k[2][P];
+    if (hs < a.n_kv_heads)
 #pragma unroll
-        for (int c = 0; c < C; ++c) s += k[c] * to_f(q[c * 32 + lane]);
-        const float lse = A.lse[static_cast<int64_t>(rq.row0 + i) * hq + head];
-        sum += exp2f(warp_sum(s) * a.scale_log2 - lse * (1.f / kLn2));
+      for (int x = 0; x < 2; ++x) load_pieces(k[x], K[x] ? K[x] + hs * a.head_stride : nullptr);
+    for (int h = hs; h < a.n_kv_heads; h += head_split) {
+      uint32_t kf[2 * P][4];
+#pragma unroll
+      for (int c = 0; c < P; ++c) {
+        const uint4 u = k[0][c], v = k[1][c];
+        kf[2 * c][0] = u.x, kf[2 * c][1] = v.x, kf[2 * c][2] = u.y, kf[2 * c][3] = v.y;
+        kf[2 * c + 1][0] = u.z, kf[2 * c + 1][1] = v.z, kf[2 * c + 1][2] = u.w, kf[2 * c + 1][3] = v.w;
+      }
+      if (h + head_split < a.n_kv_heads)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) load_pieces(k[x], K[x] ? K[x] + (h + head_split) * a.head_stride : nullptr);
+      // this lane's row of a tile: token i, head e of the group
+      const uint32_t r0 = t0 * 8 + quad;
+      int i = r0 / static_cast<uint32_t>(G), e = r0 - i * G;
+      const int di = 8 / G, de = 8 - di * G;
+      const T *q = static_cast<const T *>(a.q) + rq.row0 * a.q_stride + h * G * D + kq * 8;
+      const float *lse = A.lse + static_cast<int64_t>(rq.row0) * hq + h * G;
+      uint4 qn[P];
+      load_pieces(qn, i < i_hi ? q + i * a.q_stride + e * D : nullptr);
+      float ln = i < i_hi ? lse[static_cast<int64_t>(i) * hq + e] : INFINITY;  // no weight behind the last row
+      for (int t = t0; t < t1; ++t) {
+        uint4 qf[P];
+#pragma unroll
+        for (int c = 0; c < P; ++c) qf[c] = qn[c];
+        const float l = ln * (1.f / kLn2);
+        const int token = i;
+        i += di;
+        e += de;
+        if (e >= G) e -= G, ++i;
+        if (t + 1 < t1) {
+          load_pieces(qn, i < i_hi ? q + i * a.q_stride + e * D : nullptr);
+          ln = i < i_hi ? lse[static_cast<int64_t>(i) * hq + e] : INFINITY;
+        }
+        float c0[4] = {}, c1[4] = {};
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          mma_kq<T>(c0, kf[2 * c], qf[c].x, qf[c].y);
+          mma_kq<T>(c1, kf[2 * c + 1], qf[c].z, qf[c].w);
+        }
+        // columns of this lane: rows 2 kq and 2 kq + 1 of the tile
+        const float l0 = __shfl_sync(0xffffffffu, l, 8 * kq), l1 = __shfl_sync(0xffffffffu, l, 8 * kq + 4);
+        float w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w[x] = exp2_fast(fmaf(c0[x] + c1[x], a.scale_log2, -(x & 1 ? l1 : l0)));
+        if (t * 8 < full0 || t * 8 + 8 > full1) {
+          const int p0 = base + __shfl_sync(0xffffffffu, token, 8 * kq), p1 = base + __shfl_sync(0xffffffffu, token, 8 * kq + 4);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int p = x & 1 ? p1 : p0, j = j0 + quad + (x & 2 ? 8 : 0);
+            if (!(p >= 0 && j <= p && (j >= window_first(a, p) || j < a.n_sink)) || t * 8 + 2 * kq + (x & 1) >= R) w[x] = 0.f;
+          }
+        }
+        acc[0] += w[0] + w[1];
+        acc[1] += w[2] + w[3];
       }
     }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], 1);
+      acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], 2);
+    }
   }
-  if (lane == 0) {
-    const int64_t x = b * A.score_stride + j;
-    A.score_out[x] = (A.score_in ? A.decay * A.score_in[x] : 0.f) + sum;
+  if (kq == 0) {
+    part[warp][quad] = acc[0];
+    part[warp][quad + 8] = acc[1];
+  }
+  if (head_split > 1) __syncthreads(); else __syncwarp();
+  const int j = j0 + lane;
+  if (warp < tiles && lane < 16 && j < rq.n) {
+    float sum = 0.f;
+    for (int x = 0; x < head_split; ++x) sum += part[warp + x * tiles][lane];
+    const int64_t at = b * A.score_stride + j;
+    A.score_out[at] = (A.score_in ? A.decay * A.score_in[at] : 0.f) + sum;
   }
 }
 
 static std::string launch_weights(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  const dim3 grid((a.max_len + 7) / 8, a.n_requests);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, A); };
+  // Warps of their own for slot tiles first; while these are fewer than two blocks an SM hold, the KV
+  // heads are split (a token at 16 384 slots of one request: 8 heads in one warp 31 us, in eight 13 us).
+  int split = 1;
+  const int64_t tiles = static_cast<int64_t>(a.n_requests) * ((a.max_len + 15) / 16), want = 2ll * kWeightWarps * num_sms();
+  while (split < kWeightWarps && 2 * split <= a.n_kv_heads && tiles * split < want) split *= 2;
+  const int per = 16 * kWeightWarps / split;
+  const dim3 grid((a.max_len + per - 1) / per, a.n_requests);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(32 * kWeightWarps), 0, s, A, split); };
   cudaError_t e;
   if (dtype == BD_BF16)
     e = a.head_dim == 128 ? go(paged_weights_kernel<__nv_bfloat16, 128>) : go(paged_weights_kernel<__nv_bfloat16, 64>);
@@ -127,14 +244,20 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 
 constexpr int kSelThreads = 1024;
 
-// One block per request.  The score of the last slot that stays is found by radix selection,
-// eight bits of the key a pass: a histogram of the slots that match the bits found so far, then
-// the digit that holds the wanted rank.  A last pass in slot order keeps what is larger, and of
-// what is equal the first ones; ballots and the warps' counts give each kept slot its place.
+// One block per request.  The key of the last slot that stays is found by radix selection, eleven,
+// eleven and ten bits a pass: a histogram of the slots that match the bits found so far, then the digit
+// that holds the wanted rank.  Scores of one magnitude share their leading bits, so lanes with the same
+// digit count it together.  Then each warp, over a run of slots of its own, counts what stays -- what is
+// larger, and of what is equal the first ones -- and, knowing what stays before its run, places it.
+// Bound by the passes over the scores (L2) and the barriers between them.
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_constant__ PagedEvictArgs A) {
-  __shared__ int hist[256];
-  __shared__ int warp_cnt[2][kSelThreads / 32];
-  __shared__ uint32_t s_key;
+  __shared__ int hist[kBins];
+  __shared__ int2 warp_cnt[kSelWarps];  // a run's larger and equal slots; those before it
+  __shared__ int warp_sum_s[kSelWarps];
+  __shared__ uint32_t s_digit;
   __shared__ int s_need;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
   pdl_wait();
@@ -143,113 +266,156 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   const float *score = A.score + b * A.score_stride;
   float *score_out = A.score_out ? A.score_out + b * A.score_out_stride : nullptr;
   int32_t *kept = A.kept + static_cast<int64_t>(b) * A.budget;
-  const bool all = n <= A.budget;
-  // slots [lo, hi) compete; those outside stay
-  const int lo = all ? n : A.n_sink, hi = all ? n : n - A.n_recent;
-  int need = all ? 0 : A.budget - A.n_sink - A.n_recent;  // of them, how many stay
-  uint32_t key = 0;                                       // key of the last one that stays
-  if (need > 0) {
+  if (n <= A.budget) {
+    for (int j = tid; j < n; j += kSelThreads) {
+      kept[j] = j;
+      if (score_out && score_out != score) score_out[j] = score[j];
+    }
+    if (tid == 0) A.len_out[b] = n;
+    return;
+  }
+  // slots [lo, hi) compete for `need` places; those outside stay
+  const int lo = A.n_sink, hi = n - A.n_recent;
+  int need = A.budget - A.n_sink - A.n_recent;
+  const bool none = need == 0;
+  uint32_t key = 0xffffffffu;  // key of the last one that stays (none: no score has this one)
+  if (!none) {
     uint32_t mask = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int d = tid; d < 256; d += kSelThreads) hist[d] = 0;
+    key = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+      for (int d = tid; d < kBins; d += kSelThreads) hist[d] = 0;
       __syncthreads();
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
-        const uint32_t u = score_key(score[j]);
-        if ((u & mask) == key) atomicAdd(&hist[(u >> shift) & 255], 1);
+#pragma unroll 4
+      for (int j0 = lo; j0 < hi; j0 += kSelThreads) {
+        const int j = j0 + tid;
+        const uint32_t u = j < hi ? score_key(score[j]) : 0u;
+        const bool in = j < hi && (u & mask) == key;
+        const uint32_t digit = in ? (u >> shift) & (bins - 1) : kBins;
+        const unsigned same = __match_any_sync(0xffffffffu, digit);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
       }
       __syncthreads();
-      if (warp == 0) {  // lane l holds digits 255-8l .. 248-8l, largest first
-        int c[8], sum = 0;
+      // thread t holds digits bins-1-2t and bins-2-2t, the larger first
+      int c[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
-        int before = sum;
+      for (int x = 0; x < 2; ++x) c[x] = bins - 1 - 2 * tid - x >= 0 ? hist[bins - 1 - 2 * tid - x] : 0;
+      int sum = c[0] + c[1];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += x;
-        }
-        before -= sum;
-        if (before < need && before + sum >= need) {
-          int i = 0;
-          while (before + c[i] < need) before += c[i++];
-          s_key = key | static_cast<uint32_t>(255 - 8 * lane - i) << shift;
-          s_need = need - before;
-        }
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      if (lane == 31) warp_sum_s[warp] = sum;
+      __syncthreads();
+      int before = lane < warp ? warp_sum_s[lane] : 0;  // 32 warps: a lane each
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+      before += sum - c[0] - c[1];
+      if (before < need && before + c[0] + c[1] >= need) {
+        const int x = before + c[0] < need;
+        s_digit = bins - 1 - 2 * tid - x;
+        s_need = need - before - (x ? c[0] : 0);
       }
       __syncthreads();
-      key = s_key;
+      key |= s_digit << shift;
       need = s_need;
-      mask |= 255u << shift;
-      __syncthreads();
+      mask |= (bins - 1u) << shift;
     }
   }
   // need: how many of the slots whose key is `key` stay (the first ones)
-  int placed = 0, ties = 0;
-  const bool some = !all && A.budget > A.n_sink + A.n_recent;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const float x = j < n ? score[j] : 0.f;
-    const bool in = j >= lo && j < hi;
-    const uint32_t u = in && some ? score_key(x) : 0u;
-    const bool tie = in && some && u == key;
-    const unsigned tie_bits = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) warp_cnt[0][warp] = __popc(tie_bits);
-    __syncthreads();
-    int ties_before = ties + __popc(tie_bits & ((1u << lane) - 1));
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      const int c = warp_cnt[0][w];
-      if (w < warp) ties_before += c;
-      ties += c;
-    }
-    const bool keep = j < n && (!in || (some && (u > key || (tie && ties_before < need))));
-    const unsigned keep_bits = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) warp_cnt[1][warp] = __popc(keep_bits);
-    __syncthreads();
-    int place = placed + __popc(keep_bits & ((1u << lane) - 1));
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      const int c = warp_cnt[1][w];
-      if (w < warp) place += c;
-      placed += c;
-    }
+  const int run = (n + kSelThreads - 1) / kSelThreads * 32, j_lo = min(n, warp * run), j_hi = min(n, j_lo + run);
+  int2 cnt = make_int2(0, 0);
+#pragma unroll 4
+  for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
+    const int j = j0 + lane;
+    const bool in = j < j_hi && j >= lo && j < hi;
+    const uint32_t u = in ? score_key(score[j]) : 0u;
+    cnt.x += __popc(__ballot_sync(0xffffffffu, j < j_hi && (!in || u > key)));
+    cnt.y += __popc(__ballot_sync(0xffffffffu, in && u == key));
+  }
+  if (lane == 0) warp_cnt[warp] = cnt;
+  __syncthreads();
+  int2 at = lane < warp ? warp_cnt[lane] : make_int2(0, 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    at.x += __shfl_xor_sync(0xffffffffu, at.x, o);
+    at.y += __shfl_xor_sync(0xffffffffu, at.y, o);
+  }
+  int larger = at.x, equal = at.y;  // before this run
+  if (none) need = 0;
+  const bool in_place = score_out == score;
+#pragma unroll 1
+  for (int x = 0; x < run; x += 32) {
+    const int j = j_lo + x + lane;
+    const bool here = j < j_hi, in = here && j >= lo && j < hi;
+    const float v = here ? score[j] : 0.f;
+    const uint32_t u = in ? score_key(v) : 0u;
+    const unsigned below = (1u << lane) - 1;
+    const unsigned gt = __ballot_sync(0xffffffffu, here && (!in || u > key)), eq = __ballot_sync(0xffffffffu, in && u == key);
+    const int e = equal + __popc(eq & below), place = larger + __popc(gt & below) + min(e, need);
+    const bool keep = here && (!in || u > key || (u == key && e < need));
+    larger += __popc(gt);
+    equal += __popc(eq);
     if (keep) {
       kept[place] = j;
-      if (score_out) score_out[place] = x;
+      if (score_out && !in_place) score_out[place] = v;
     }
   }
-  if (score_out == score)  // slots filled later start from zero
-    for (int j = placed + tid; j < n; j += kSelThreads) score_out[j] = 0.f;
-  __syncthreads();
-  if (tid == 0) A.len_out[b] = placed;
+  if (in_place) {
+    // score i comes from kept[i] >= i: a block of them is written when all of it has been read, and the
+    // blocks behind it read behind what it wrote
+    __syncthreads();
+    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+      const int i = i0 + tid;
+      const float v = i < A.budget ? score[kept[i]] : 0.f;
+      __syncthreads();
+      if (i < n) score_out[i] = v;  // behind the kept ones zero: slots filled later start from there
+    }
+  }
+  if (tid == 0) A.len_out[b] = A.budget;
 }
 
 // Moves the kept slots.  Slot i's row of one pool and KV head is D contiguous values; a thread
-// moves 16 bytes of it.  To other pages every block takes kMoveRows slots of its own.
+// moves 16 bytes of it.  To other pages every block takes kMoveRows slots of its own, each thread its
+// pieces side by side: slot, page and piece are three round trips, whatever their number.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 64;
+constexpr int kMoveEach = 8;  // 16-byte pieces of a thread
 
 __device__ __forceinline__ int64_t dst_offset(const PagedEvictArgs &A, int b, int i) {
   if (!A.dst_table) return slot_offset(A.p, A.p.page_table + static_cast<int64_t>(b) * A.p.table_width, i);
   return slot_offset(A.p, A.dst_table + static_cast<int64_t>(b) * A.dst_width, i);
 }
 
+template <int CPR>  // pieces of a row
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_constant__ PagedEvictArgs A) {
   const PagedArgs &a = A.p;
   const int b = blockIdx.z, h = blockIdx.y >> 1;
   uint16_t *pool = static_cast<uint16_t *>(const_cast<void *>(blockIdx.y & 1 ? a.v : a.k)) + h * a.head_stride;
-  const int cpr = a.head_dim / 8;
   pdl_wait();
   pdl_trigger();
   const int n = min(A.len_out[b], A.budget);
   const int32_t *kept = A.kept + static_cast<int64_t>(b) * A.budget;
   const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
-  const int i0 = blockIdx.x * kMoveRows;
-  for (int c = threadIdx.x; c < kMoveRows * cpr; c += kMoveThreads) {
-    const int i = i0 + c / cpr, x = (c % cpr) * 8;
-    if (i >= n) break;
-    const int64_t src = slot_offset(a, table, kept[i]), dst = dst_offset(A, b, i);
-    if (src >= 0 && dst >= 0)
-      *reinterpret_cast<uint4 *>(pool + dst + x) = *reinterpret_cast<const uint4 *>(pool + src + x);
+  constexpr int STEP = kMoveThreads / CPR;
+  const int i0 = blockIdx.x * STEP * kMoveEach + threadIdx.x / CPR, x = (threadIdx.x % CPR) * 8;
+  if (blockIdx.x * STEP * kMoveEach >= n) return;
+  int j[kMoveEach];
+#pragma unroll
+  for (int u = 0; u < kMoveEach; ++u) j[u] = kept[min(i0 + u * STEP, n - 1)];
+  int64_t src[kMoveEach], dst[kMoveEach];
+#pragma unroll
+  for (int u = 0; u < kMoveEach; ++u) {
+    src[u] = slot_offset(a, table, j[u]);
+    dst[u] = i0 + u * STEP < n ? dst_offset(A, b, i0 + u * STEP) : -1;
   }
+  uint4 v[kMoveEach];
+#pragma unroll
+  for (int u = 0; u < kMoveEach; ++u)
+    if (src[u] >= 0 && dst[u] >= 0) v[u] = *reinterpret_cast<const uint4 *>(pool + src[u] + x);
+#pragma unroll
+  for (int u = 0; u < kMoveEach; ++u)
+    if (src[u] >= 0 && dst[u] >= 0) *reinterpret_cast<uint4 *>(pool + dst[u] + x) = v[u];
 }
 
 // In place, one block per (request, KV head, pool) goes up through the slots in chunks of
@@ -301,8 +467,9 @@ static std::string launch_evict(const PagedEvictArgs &A, cudaStream_t s) {
   if (e == cudaSuccess) {
     const int most = A.budget < a.max_len ? A.budget : a.max_len;
     if (A.dst_table) {
-      const dim3 grid((most + kMoveRows - 1) / kMoveRows, 2 * a.n_kv_heads, a.n_requests);
-      if (most > 0) e = launch_pdl(paged_move_kernel, grid, dim3(kMoveThreads), 0, s, A);
+      const int rows = kMoveThreads * kMoveEach / (a.head_dim / 8);  // of a block
+      const dim3 grid((most + rows - 1) / rows, 2 * a.n_kv_heads, a.n_requests);
+      if (most > 0) e = launch_pdl(a.head_dim == 128 ? paged_move_kernel<16> : paged_move_kernel<8>, grid, dim3(kMoveThreads), 0, s, A);
     } else if (A.budget < a.max_len) {  // else nothing can leave
       e = launch_pdl(paged_move_in_place_kernel, dim3(2 * a.n_kv_heads, a.n_requests), dim3(kInThreads), 0, s, A);
     }
@@ -482,6 +649,8 @@ bd_status bd_paged_weights(const bd_paged_kv *kv, const bd_paged_batch *batch, c
     if (!lse || misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged weights: lse must be given");
   }
   if (misaligned(rows_used, 4)) return refuse(BD_ERR_INVALID_ARG, "paged weights: rows_used misaligned");
+  if (static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30))
+    return refuse(BD_ERR_UNSUPPORTED, "paged weights: max_rows * n_q_heads too large");
   if (!std::isfinite(decay)) return refuse(BD_ERR_INVALID_ARG, "paged weights: decay must be finite");
   if (!score_out || misaligned(score_out, 4) || misaligned(score_in, 4) || score_stride < batch->max_len)
     return refuse(BD_ERR_INVALID_ARG, "paged weights: score_out must be given, with rows of at least max_len entries");
