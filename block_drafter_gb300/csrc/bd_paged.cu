@@ -1,7 +1,8 @@
 // Paged K/V cache: the entry points' checks, and the kernels of the append, the accumulated
 // attention weights and the eviction.
-#include "bd_paged_device.cuh"
+#include "bd_paged_attn.cuh"
 
+#include <climits>
 #include <cmath>
 
 namespace bd {
@@ -14,6 +15,7 @@ BD_DEFINE_ERROR_TAKER(take_error_word_paged)
 // row ranges against the block's.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 8;
+constexpr int kAppendEach = 4;  // pieces of a thread in flight
 
 struct PagedAppendArgs {
   PagedArgs p;
@@ -45,15 +47,25 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
   }
   __syncthreads();
   const int per_head = a.head_dim / 8, per_side = a.n_kv_heads * per_head, per_row = 2 * per_side;
-  for (int c = threadIdx.x; c < (r1 - r0) * per_row; c += kAppendThreads) {
-    const int r = c / per_row, u = c - r * per_row;
-    if (off[r] < 0) continue;
-    const bool v = u >= per_side;
-    const int w = v ? u - per_side : u, h = w / per_head, x = (w - h * per_head) * 8;
-    const uint16_t *src = static_cast<const uint16_t *>(v ? A.v_new : A.k_new) +
-                          (r0 + r) * (v ? A.v_stride : A.k_stride) + w * 8;
-    uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(v ? a.v : a.k)) + off[r] + h * a.head_stride + x;
-    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src);
+  const int pieces = (r1 - r0) * per_row;
+  for (int c0 = threadIdx.x; c0 < pieces; c0 += kAppendEach * kAppendThreads) {
+    uint4 v[kAppendEach];
+    int64_t to[kAppendEach];
+    bool k[kAppendEach];
+#pragma unroll
+    for (int u = 0; u < kAppendEach; ++u) {
+      const int c = c0 + u * kAppendThreads, r = c / per_row, x = c - r * per_row;
+      to[u] = -1;
+      if (c >= pieces || off[r] < 0) continue;
+      k[u] = x < per_side;
+      const int w = k[u] ? x : x - per_side, h = w / per_head;
+      v[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(k[u] ? A.k_new : A.v_new) +
+                                                   (r0 + r) * (k[u] ? A.k_stride : A.v_stride) + w * 8));
+      to[u] = off[r] + h * a.head_stride + (w - h * per_head) * 8;
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendEach; ++u)
+      if (to[u] >= 0) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(const_cast<void *>(k[u] ? a.k : a.v)) + to[u]) = v[u];
   }
 }
 
@@ -69,10 +81,9 @@ static std::string launch_append(PagedAppendArgs &A, cudaStream_t s) {
 // Bound by K's bytes for a token or a block, by the tensor cores for many rows.  A warp owns 16 slots of
 // a request: their keys are the A operand of mma.sync m16n8k16 and stay in registers while the rows of
 // the KV head pass by, 8 at a time, as B; so a slot's weights are summed in the registers of four lanes,
-// without atomics, over all rows and heads of the warp.  Few slots give a block's eight warps fewer tiles
-// and split the KV heads among them (summed through shared memory in a fixed order).
-// The order of the D products of a score is free, so both operands take it as 16-byte pieces from
-// global memory: lane l holds pieces l%4, l%4 + 4, ... of its rows, two MMA steps each.
+// without atomics, over all rows and heads of the warp.
+// The order of the D products of a score is free, so both operands are taken as 16-byte pieces: lane l
+// holds pieces l%4, l%4 + 4, ... of its rows, two MMA steps each.
 constexpr int kWeightWarps = 8;
 
 template <typename T> __device__ __forceinline__ void mma_kq(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -89,148 +100,293 @@ __device__ __forceinline__ void mma_kq<__half>(float (&c)[4], const uint32_t (&a
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// P pieces of 16 bytes (every fourth from this lane's on) of a row, zeros where p is null.
-template <int P> __device__ __forceinline__ void load_pieces(uint4 (&v)[P], const void *p) {
-#pragma unroll
-  for (int c = 0; c < P; ++c) v[c] = p ? __ldg(static_cast<const uint4 *>(p) + 4 * c) : make_uint4(0, 0, 0, 0);
+// A tile of 16 slots of a request, and which tokens (of slot base + i) it concerns.
+struct WeightTile {
+  Request rq;
+  int b, j0, base;
+  int i_lo, i_hi;    // tokens that see some of its slots
+  int f_lo, f_hi;    // rows that see all of them, f_lo to f_hi - 1
+  int64_t q0;        // this lane's row of the first row tile: element offset in q (KV head 0),
+  int lse0, i0, e0;  //   offset in lse from the request's first row, token, head of the group
+};
+__device__ __forceinline__ WeightTile weight_tile(const PagedWeightsArgs &A, int b, int j0, int quad, int kq) {
+  const PagedArgs &a = A.p;
+  WeightTile t;
+  t.rq = request_of(a, b);
+  t.b = b;
+  t.j0 = j0;
+  t.base = t.rq.n - t.rq.rows;
+  const int used = A.rows_used ? max(0, min(__ldg(A.rows_used + b), t.rq.rows)) : t.rq.rows;
+  const int j1 = min(j0 + 15, t.rq.n - 1);
+  t.i_lo = max(0, j0 - t.base);
+  t.f_lo = max(0, j1 - t.base);
+  t.i_hi = t.f_hi = used;
+  if (a.window > 0) {
+    auto behind = [&](int j) {  // the first token that does not see slot j any more, 0 .. used
+      const int64_t i = static_cast<int64_t>(j) + a.window - t.base;
+      return static_cast<int>(i < 0 ? 0 : i < used ? i : used);
+    };
+    if (j0 >= a.n_sink) t.i_hi = behind(j1);
+    if (j1 >= a.n_sink) t.f_hi = behind(j0);
+  }
+  if (t.f_hi == t.i_hi) t.f_hi = INT_MAX;  // rows behind the last count nothing anyway
+  else t.f_hi *= a.group;
+  t.f_lo *= a.group;
+  const uint32_t r0 = t.i_lo * a.group / 8 * 8 + quad;
+  t.i0 = r0 / static_cast<uint32_t>(a.group);
+  t.e0 = r0 - t.i0 * a.group;
+  t.q0 = (t.rq.row0 + t.i0) * a.q_stride + t.e0 * a.head_dim + kq * 8;
+  t.lse0 = t.i0 * a.n_kv_heads * a.group + t.e0;
+  return t;
 }
+
+// How a lane steps from a row tile to the next: 8 rows are di tokens and de heads on, or one token more
+// and a group less.
+struct RowStep {
+  int di, de, dl, wrap_l;
+  int64_t dq, wrap_q;
+};
+
+// Weights a tile's slots (quad, quad + 8) get from the rows of KV head h, its keys in kf: added to acc.
+template <typename T, int D>
+__device__ __forceinline__ void tile_weights(const PagedWeightsArgs &A, const WeightTile &w, const RowStep &rs, int h,
+                                             const uint32_t (&kf)[D / 16][4], float (&acc)[2], int quad, int kq) {
+  constexpr int P = D / 32;
+  const PagedArgs &a = A.p;
+  const int G = a.group;
+  const int t0 = w.i_lo * G / 8, t1 = (w.i_hi * G + 7) / 8;  // row tiles of 8
+  const T *q = static_cast<const T *>(a.q) + w.q0 + h * G * D;
+  const float *lse = A.lse + static_cast<int64_t>(w.rq.row0) * a.n_kv_heads * G + w.lse0 + h * G;
+  int i = w.i0, e = w.e0;
+  uint4 qn[P];
+  float ln = INFINITY;  // no weight behind the last row
+#pragma unroll
+  for (int c = 0; c < P; ++c) qn[c] = make_uint4(0, 0, 0, 0);
+  auto fetch = [&]() {
+    if (i < w.i_hi) {
+      ln = __ldg(lse);
+#pragma unroll
+      for (int c = 0; c < P; ++c) qn[c] = __ldg(reinterpret_cast<const uint4 *>(q) + 4 * c);
+    } else {
+      ln = INFINITY;
+    }
+  };
+  fetch();
+#pragma unroll 2
+  for (int t = t0; t < t1; ++t) {
+    float c0[4] = {}, c1[4] = {};
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+      mma_kq<T>(c0, kf[2 * c], qn[c].x, qn[c].y);
+      mma_kq<T>(c1, kf[2 * c + 1], qn[c].z, qn[c].w);
+    }
+    const float l = ln * (1.f / kLn2);
+    const int token = i;
+    i += rs.di;
+    e += rs.de;
+    q += rs.dq;
+    lse += rs.dl;
+    if (e >= G) {
+      e -= G;
+      ++i;
+      q += rs.wrap_q;
+      lse += rs.wrap_l;
+    }
+    if (t + 1 < t1) fetch();
+    // columns of this lane: rows 2 kq and 2 kq + 1 of the row tile
+    const float l0 = __shfl_sync(0xffffffffu, l, 8 * kq), l1 = __shfl_sync(0xffffffffu, l, 8 * kq + 4);
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float lx = x & 1 ? l1 : l0;
+      v[x] = lx == INFINITY ? 0.f : exp2_fast(fmaf(c0[x] + c1[x], a.scale_log2, -lx));
+    }
+    if (t * 8 < w.f_lo || t * 8 + 8 > w.f_hi) {
+      const int p0 = w.base + __shfl_sync(0xffffffffu, token, 8 * kq), p1 = w.base + __shfl_sync(0xffffffffu, token, 8 * kq + 4);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int p = x & 1 ? p1 : p0, j = w.j0 + quad + (x & 2 ? 8 : 0);
+        if (!(p >= 0 && j <= p && (j >= window_first(a, p) || j < a.n_sink))) v[x] = 0.f;
+      }
+    }
+    acc[0] += v[0] + v[1];
+    acc[1] += v[2] + v[3];
+  }
+}
+
+// Blocks of the weights kernel: two on every SM.  Each of its teams of head_split warps takes every
+// n_teams-th slot tile of the call's list (all requests' tiles in order); the tile's KV heads hs,
+// hs + head_split, ... are warp hs's.  A warp's keys -- one KV head of one tile a stage -- come by cp.async
+// into its own ring, kStages - 1 ahead across heads and tiles.
+template <int D> struct Weights {
+  static constexpr int kStage = 16 * 2 * D;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kSmem = kWeightWarps * kStages * kStage;
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kWeightWarps, 2) paged_weights_kernel(const __grid_constant__ PagedWeightsArgs A, int head_split) {
-  constexpr int P = D / 32;  // pieces of a row per lane
-  __shared__ float part[kWeightWarps][16];
+  using W = Weights<D>;
+  constexpr int CPR = D / 8, RPI = 32 / CPR, P = D / 32;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  __shared__ int tiles_before[BD_PAGED_MAX_REQUESTS + 1];
+  __shared__ float part[2][kWeightWarps][16];
+  __shared__ int warp_total[kWeightWarps];
   const PagedArgs &a = A.p;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y, quad = lane >> 2, kq = lane & 3;
-  const int tiles = kWeightWarps / head_split;           // slot tiles of the block
-  const int hs = warp / tiles;                           // this warp's KV heads: hs, hs + head_split, ...
-  const int j0 = (blockIdx.x * tiles + warp % tiles) * 16;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = lane >> 2, kq = lane & 3;
   pdl_wait();
   pdl_trigger();
-  const Request rq = request_of(a, b);
-  if (blockIdx.x * tiles * 16 >= rq.n) return;
-  const int used = A.rows_used ? max(0, min(A.rows_used[b], rq.rows)) : rq.rows;
-  const int base = rq.n - rq.rows, G = a.group, hq = a.n_kv_heads * G;
-  // tokens i (slots base + i) that see some slot of the tile, and those that see all of it
-  const int j1 = min(j0 + 15, rq.n - 1);
-  const bool sinks = j0 < a.n_sink, all_sinks = j1 < a.n_sink;
-  int i_lo = max(0, j0 - base), i_hi = used;  // [i_lo, i_hi)
-  int f_lo = max(0, j1 - base), f_hi = used;
-  if (a.window > 0) {
-    auto behind = [&](int j) {  // the first token that does not see slot j any more, 0 .. used
-      const int64_t i = static_cast<int64_t>(j) + a.window - base;
-      return static_cast<int>(i < 0 ? 0 : i < used ? i : used);
-    };
-    if (!sinks) i_hi = behind(j1);
-    if (!all_sinks) f_hi = behind(j0);
+  {  // tiles of the requests before each
+    int before = 0;
+    for (int b0 = 0; b0 < a.n_requests; b0 += 32 * kWeightWarps) {
+      const int b = b0 + tid;
+      int x = b < a.n_requests ? (request_len(a, b) + 15) / 16 : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_total[warp] = x;
+      __syncthreads();
+      int all = 0;
+      for (int w = 0; w < kWeightWarps; ++w) {
+        if (w == warp) x += all;
+        all += warp_total[w];
+      }
+      if (b < a.n_requests) tiles_before[b + 1] = before + x;
+      before += all;
+      __syncthreads();
+    }
+    if (tid == 0) tiles_before[0] = 0;
+    __syncthreads();
   }
-  float acc[2] = {0.f, 0.f};  // slots j0 + quad, + 8
-  if (j0 < rq.n && i_lo < i_hi) {
-    const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
-    const T *K[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int j = j0 + quad + 8 * x;
-      const int64_t off = j < rq.n ? slot_offset(a, table, j) : -1;
-      K[x] = off < 0 ? nullptr : static_cast<const T *>(a.k) + off + kq * 8;
+  const int n_tiles = tiles_before[a.n_requests];
+  const int teams = kWeightWarps / head_split, n_teams = teams * gridDim.x;
+  const int hs = warp / teams, heads = hs < a.n_kv_heads ? (a.n_kv_heads - hs + head_split - 1) / head_split : 0;
+  const int first = blockIdx.x + (warp % teams) * gridDim.x;  // a block's teams lie far apart in the list
+  auto tile_at = [&](int t) {
+    int lo = 0, hi = a.n_requests;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tiles_before[mid] <= t) lo = mid; else hi = mid;
     }
-    const int t0 = i_lo * G / 8, t1 = (i_hi * G + 7) / 8;  // row tiles
-    const int full0 = f_lo * G, full1 = f_hi * G;          // rows that see all of the tile's slots
-    const int R = i_hi * G;
-    uint4 k[2][P];
-    if (hs < a.n_kv_heads)
+    return weight_tile(A, lo, (t - tiles_before[lo]) * 16, quad, kq);
+  };
+  RowStep rs;
+  rs.di = 8 / a.group;
+  rs.de = 8 - rs.di * a.group;
+  rs.dl = rs.di * a.n_kv_heads * a.group + rs.de;
+  rs.wrap_l = (a.n_kv_heads - 1) * a.group;
+  rs.dq = rs.di * a.q_stride + rs.de * D;
+  rs.wrap_q = a.q_stride - a.group * D;
+  const uint32_t mine = smem_u32(ring) + warp * W::kStages * W::kStage;
+  // the copies run ahead of the products: their own place in the list
+  int ct = first, ch = 0;
+  int64_t off[16 / RPI];  // of the rows this lane copies, -1: none
+  bool any = false;       // some row sees some of the tile
+  auto open = [&]() {
+    if (ct >= n_tiles) return;
+    const WeightTile w = tile_at(ct);
+    any = w.i_lo < w.i_hi && heads > 0;
+    const int j = w.j0 + (lane & 15);
+    const int64_t o = any && j < w.rq.n ? slot_offset(a, a.page_table + static_cast<int64_t>(w.b) * a.table_width, j) : -1;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) load_pieces(k[x], K[x] ? K[x] + hs * a.head_stride : nullptr);
-    for (int h = hs; h < a.n_kv_heads; h += head_split) {
-      uint32_t kf[2 * P][4];
+    for (int u = 0; u < 16 / RPI; ++u) {
+      off[u] = __shfl_sync(0xffffffffu, o, u * RPI + lane / CPR);
+      if (off[u] >= 0) off[u] += lane % CPR * 8;
+    }
+  };
+  auto copy = [&](int stage) {  // one KV head of one tile
+    while (ct < n_tiles && !any) {  // tiles nobody sees
+      ct += n_teams;
+      open();
+    }
+    if (ct < n_tiles) {
+      const T *K = static_cast<const T *>(a.k) + (hs + ch * head_split) * a.head_stride;
+      const uint32_t dst = mine + stage * W::kStage;
+      const int c = lane % CPR;
 #pragma unroll
-      for (int c = 0; c < P; ++c) {
-        const uint4 u = k[0][c], v = k[1][c];
-        kf[2 * c][0] = u.x, kf[2 * c][1] = v.x, kf[2 * c][2] = u.y, kf[2 * c][3] = v.y;
-        kf[2 * c + 1][0] = u.z, kf[2 * c + 1][1] = v.z, kf[2 * c + 1][2] = u.w, kf[2 * c + 1][3] = v.w;
+      for (int u = 0; u < 16 / RPI; ++u) {
+        const int r = u * RPI + lane / CPR;
+        cp_async16(dst + r * 2 * D + ((c ^ (r & 7)) << 4), K + (off[u] < 0 ? 0 : off[u]), off[u] >= 0);
       }
-      if (h + head_split < a.n_kv_heads)
+      if (++ch == heads) {
+        ch = 0;
+        ct += n_teams;
+        open();
+      }
+    }
+    cp_async_commit();
+  };
+  open();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) load_pieces(k[x], K[x] ? K[x] + (h + head_split) * a.head_stride : nullptr);
-      // this lane's row of a tile: token i, head e of the group
-      const uint32_t r0 = t0 * 8 + quad;
-      int i = r0 / static_cast<uint32_t>(G), e = r0 - i * G;
-      const int di = 8 / G, de = 8 - di * G;
-      const T *q = static_cast<const T *>(a.q) + rq.row0 * a.q_stride + h * G * D + kq * 8;
-      const float *lse = A.lse + static_cast<int64_t>(rq.row0) * hq + h * G;
-      uint4 qn[P];
-      load_pieces(qn, i < i_hi ? q + i * a.q_stride + e * D : nullptr);
-      float ln = i < i_hi ? lse[static_cast<int64_t>(i) * hq + e] : INFINITY;  // no weight behind the last row
-      for (int t = t0; t < t1; ++t) {
-        uint4 qf[P];
+  for (int st = 0; st < W::kStages - 1; ++st) copy(st);
+  int stage = 0, turn = 0;
+  for (int t = first; t < n_tiles; t += n_teams) {
+    const WeightTile w = tile_at(t);
+    float acc[2] = {0.f, 0.f};  // slots j0 + quad, + 8
+    if (w.i_lo < w.i_hi)
+      for (int x = 0; x < heads; ++x) {
+        cp_async_wait<W::kStages - 2>();
+        __syncwarp();
+        copy(stage == 0 ? W::kStages - 1 : stage - 1);
+        uint32_t kf[2 * P][4];
 #pragma unroll
-        for (int c = 0; c < P; ++c) qf[c] = qn[c];
-        const float l = ln * (1.f / kLn2);
-        const int token = i;
-        i += di;
-        e += de;
-        if (e >= G) e -= G, ++i;
-        if (t + 1 < t1) {
-          load_pieces(qn, i < i_hi ? q + i * a.q_stride + e * D : nullptr);
-          ln = i < i_hi ? lse[static_cast<int64_t>(i) * hq + e] : INFINITY;
-        }
-        float c0[4] = {}, c1[4] = {};
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int c = 0; c < P; ++c) {
-          mma_kq<T>(c0, kf[2 * c], qf[c].x, qf[c].y);
-          mma_kq<T>(c1, kf[2 * c + 1], qf[c].z, qf[c].w);
-        }
-        // columns of this lane: rows 2 kq and 2 kq + 1 of the tile
-        const float l0 = __shfl_sync(0xffffffffu, l, 8 * kq), l1 = __shfl_sync(0xffffffffu, l, 8 * kq + 4);
-        float w[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) w[x] = exp2_fast(fmaf(c0[x] + c1[x], a.scale_log2, -(x & 1 ? l1 : l0)));
-        if (t * 8 < full0 || t * 8 + 8 > full1) {
-          const int p0 = base + __shfl_sync(0xffffffffu, token, 8 * kq), p1 = base + __shfl_sync(0xffffffffu, token, 8 * kq + 4);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int p = x & 1 ? p1 : p0, j = j0 + quad + (x & 2 ? 8 : 0);
-            if (!(p >= 0 && j <= p && (j >= window_first(a, p) || j < a.n_sink)) || t * 8 + 2 * kq + (x & 1) >= R) w[x] = 0.f;
+          for (int c = 0; c < P; ++c) {
+            uint4 v;
+            const uint32_t at = mine + stage * W::kStage + (quad + 8 * r) * 2 * D + (((4 * c + kq) ^ quad) << 4);
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+            kf[2 * c][r] = v.x, kf[2 * c][r + 2] = v.y, kf[2 * c + 1][r] = v.z, kf[2 * c + 1][r + 2] = v.w;
           }
-        }
-        acc[0] += w[0] + w[1];
-        acc[1] += w[2] + w[3];
+        tile_weights<T, D>(A, w, rs, hs + x * head_split, kf, acc, quad, kq);
+        __syncwarp();
+        stage = stage + 1 == W::kStages ? 0 : stage + 1;
       }
-    }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], 1);
       acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], 2);
     }
+    if (kq == 0) {
+      part[turn][warp][quad] = acc[0];
+      part[turn][warp][quad + 8] = acc[1];
+    }
+    // a team's warps meet once a tile; two sets of sums keep a fast one from the next tile's
+    if (head_split == 1)
+      __syncwarp();
+    else
+      named_bar(1 + warp % teams, 32 * head_split);
+    const int j = w.j0 + lane;
+    if (warp < teams && lane < 16 && j < w.rq.n) {
+      float sum = 0.f;
+      for (int x = 0; x < head_split; ++x) sum += part[turn][warp + x * teams][lane];
+      const int64_t at = w.b * A.score_stride + j;
+      A.score_out[at] = (A.score_in ? A.decay * A.score_in[at] : 0.f) + sum;
+    }
+    turn ^= 1;
+    if (head_split == 1) __syncwarp();
   }
-  if (kq == 0) {
-    part[warp][quad] = acc[0];
-    part[warp][quad + 8] = acc[1];
-  }
-  if (head_split > 1) __syncthreads(); else __syncwarp();
-  const int j = j0 + lane;
-  if (warp < tiles && lane < 16 && j < rq.n) {
-    float sum = 0.f;
-    for (int x = 0; x < head_split; ++x) sum += part[warp + x * tiles][lane];
-    const int64_t at = b * A.score_stride + j;
-    A.score_out[at] = (A.score_in ? A.decay * A.score_in[at] : 0.f) + sum;
-  }
+  cp_async_wait<0>();
 }
 
+template <typename T, int D> static cudaError_t launch_weights_t(const PagedWeightsArgs &A, int split, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(paged_weights_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Weights<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_weights_kernel<T, D>, dim3(2 * num_sms()), dim3(32 * kWeightWarps), Weights<D>::kSmem, s, A, split);
+}
 static std::string launch_weights(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  // Warps of their own for slot tiles first; while these are fewer than two blocks an SM hold, the KV
-  // heads are split (a token at 16 384 slots of one request: 8 heads in one warp 31 us, in eight 13 us).
+  // Warps work on tiles of their own while there are enough; else they split the KV heads of one.
   int split = 1;
-  const int64_t tiles = static_cast<int64_t>(a.n_requests) * ((a.max_len + 15) / 16), want = 2ll * kWeightWarps * num_sms();
+  const int64_t tiles = static_cast<int64_t>(a.n_requests) * ((a.max_len + 15) / 16), want = 4ll * kWeightWarps * num_sms();
   while (split < kWeightWarps && 2 * split <= a.n_kv_heads && tiles * split < want) split *= 2;
-  const int per = 16 * kWeightWarps / split;
-  const dim3 grid((a.max_len + per - 1) / per, a.n_requests);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(32 * kWeightWarps), 0, s, A, split); };
   cudaError_t e;
   if (dtype == BD_BF16)
-    e = a.head_dim == 128 ? go(paged_weights_kernel<__nv_bfloat16, 128>) : go(paged_weights_kernel<__nv_bfloat16, 64>);
+    e = a.head_dim == 128 ? launch_weights_t<__nv_bfloat16, 128>(A, split, s) : launch_weights_t<__nv_bfloat16, 64>(A, split, s);
   else
-    e = a.head_dim == 128 ? go(paged_weights_kernel<__half, 128>) : go(paged_weights_kernel<__half, 64>);
+    e = a.head_dim == 128 ? launch_weights_t<__half, 128>(A, split, s) : launch_weights_t<__half, 64>(A, split, s);
   return e == cudaSuccess ? std::string() : std::string("paged weights: ") + cudaGetErrorString(e);
 }
 
@@ -242,36 +398,48 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// One cluster of eight blocks per request.  The key of the last slot that stays is found by radix
+// selection, eleven, eleven and ten bits a pass: a histogram of the slots that match the bits found so
+// far -- each block of its share of the slots, summed over the cluster through distributed shared
+// memory -- then the digit that holds the wanted rank.  Then each warp, over a run of slots of its own,
+// counts what stays -- what is larger, and of what is equal the first ones -- and, knowing what stays
+// before its run, places it.  Bound by the round trips of its passes and barriers; on one block, by that
+// SM's instructions (32 768 slots: 57 us).
 constexpr int kSelThreads = 1024;
-
-// One block per request.  The key of the last slot that stays is found by radix selection, eleven,
-// eleven and ten bits a pass: a histogram of the slots that match the bits found so far, then the digit
-// that holds the wanted rank.  Scores of one magnitude share their leading bits, so lanes with the same
-// digit count it together.  Then each warp, over a run of slots of its own, counts what stays -- what is
-// larger, and of what is equal the first ones -- and, knowing what stays before its run, places it.
-// Bound by the passes over the scores (L2) and the barriers between them.
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBlocks = 8;
 constexpr int kBins = 2048;
 
+__device__ __forceinline__ int2 ld_cluster_i2(uint32_t addr) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_constant__ PagedEvictArgs A) {
-  __shared__ int hist[kBins];
-  __shared__ int2 warp_cnt[kSelWarps];  // a run's larger and equal slots; those before it
+  __shared__ __align__(16) int hist[2][kBins];  // two: a block may clear one while others still read its last
+  __shared__ int2 warp_cnt[kSelWarps];          // a run's slots that stay beside ties, and its ties
+  __shared__ __align__(8) int2 block_cnt;
   __shared__ int warp_sum_s[kSelWarps];
   __shared__ uint32_t s_digit;
   __shared__ int s_need;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
+  const int rank = blockIdx.x, ct = rank * kSelThreads + tid;  // thread of the cluster
+  constexpr int CT = kSelBlocks * kSelThreads;
   pdl_wait();
   pdl_trigger();
   const int n = request_len(A.p, b);
   const float *score = A.score + b * A.score_stride;
   float *score_out = A.score_out ? A.score_out + b * A.score_out_stride : nullptr;
   int32_t *kept = A.kept + static_cast<int64_t>(b) * A.budget;
-  if (n <= A.budget) {
-    for (int j = tid; j < n; j += kSelThreads) {
+  const bool in_place = score_out == score;
+  if (n <= A.budget) {  // the whole cluster
+    for (int j = ct; j < n; j += CT) {
       kept[j] = j;
-      if (score_out && score_out != score) score_out[j] = score[j];
+      if (score_out && !in_place) score_out[j] = score[j];
     }
-    if (tid == 0) A.len_out[b] = n;
+    cluster_sync();  // every block has read the length: it may be replaced
+    if (ct == 0) A.len_out[b] = n;
     return;
   }
   // slots [lo, hi) compete for `need` places; those outside stay
@@ -284,22 +452,26 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
     key = 0;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-      for (int d = tid; d < kBins; d += kSelThreads) hist[d] = 0;
+      int *h = hist[pass & 1];
+      for (int d = tid; d < kBins; d += kSelThreads) h[d] = 0;
       __syncthreads();
 #pragma unroll 4
-      for (int j0 = lo; j0 < hi; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        const uint32_t u = j < hi ? score_key(score[j]) : 0u;
-        const bool in = j < hi && (u & mask) == key;
-        const uint32_t digit = in ? (u >> shift) & (bins - 1) : kBins;
-        const unsigned same = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+      for (int j = lo + ct; j < hi; j += CT) {
+        const uint32_t u = score_key(score[j]);
+        if ((u & mask) == key) atomicAdd(&h[(u >> shift) & (bins - 1)], 1);
       }
-      __syncthreads();
-      // thread t holds digits bins-1-2t and bins-2-2t, the larger first
-      int c[2];
+      cluster_sync();
+      // thread t holds digits bins-1-2t and bins-2-2t, the larger first, of all blocks
+      int c[2] = {0, 0};
+      if (2 * tid < bins) {
+        const uint32_t at = smem_u32(h + bins - 2 - 2 * tid);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) c[x] = bins - 1 - 2 * tid - x >= 0 ? hist[bins - 1 - 2 * tid - x] : 0;
+        for (int r = 0; r < kSelBlocks; ++r) {
+          const int2 v = ld_cluster_i2(cluster_map(at, r));
+          c[0] += v.y;
+          c[1] += v.x;
+        }
+      }
       int sum = c[0] + c[1];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -324,7 +496,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
     }
   }
   // need: how many of the slots whose key is `key` stay (the first ones)
-  const int run = (n + kSelThreads - 1) / kSelThreads * 32, j_lo = min(n, warp * run), j_hi = min(n, j_lo + run);
+  const int run = (n + CT - 1) / CT * 32, j_lo = min(n, (rank * kSelWarps + warp) * run), j_hi = min(n, j_lo + run);
   int2 cnt = make_int2(0, 0);
 #pragma unroll 4
   for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
@@ -337,6 +509,21 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   if (lane == 0) warp_cnt[warp] = cnt;
   __syncthreads();
   int2 at = lane < warp ? warp_cnt[lane] : make_int2(0, 0);
+  if (warp == 0) {
+    int2 all = warp_cnt[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all.x += __shfl_xor_sync(0xffffffffu, all.x, o);
+      all.y += __shfl_xor_sync(0xffffffffu, all.y, o);
+    }
+    if (lane == 0) block_cnt = all;
+  }
+  cluster_sync();
+  if (lane < rank) {  // the blocks before this one, a lane each
+    const int2 v = ld_cluster_i2(cluster_map(smem_u32(&block_cnt), lane));
+    at.x += v.x;
+    at.y += v.y;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     at.x += __shfl_xor_sync(0xffffffffu, at.x, o);
@@ -344,10 +531,9 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   }
   int larger = at.x, equal = at.y;  // before this run
   if (none) need = 0;
-  const bool in_place = score_out == score;
 #pragma unroll 1
-  for (int x = 0; x < run; x += 32) {
-    const int j = j_lo + x + lane;
+  for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
+    const int j = j0 + lane;
     const bool here = j < j_hi, in = here && j >= lo && j < hi;
     const float v = here ? score[j] : 0.f;
     const uint32_t u = in ? score_key(v) : 0u;
@@ -362,25 +548,25 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
       if (score_out && !in_place) score_out[place] = v;
     }
   }
-  if (in_place) {
-    // score i comes from kept[i] >= i: a block of them is written when all of it has been read, and the
-    // blocks behind it read behind what it wrote
-    __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const float v = i < A.budget ? score[kept[i]] : 0.f;
-      __syncthreads();
+  cluster_sync();  // kept[] is complete, every block's shared memory and the length are read
+  if (in_place)
+    // score i comes from kept[i] >= i: a step of them is written when all of it has been read, and the
+    // steps behind it read behind what it wrote
+    for (int i0 = 0; i0 < n; i0 += CT) {
+      const int i = i0 + ct;
+      const float v = i < A.budget ? score[__ldcg(kept + i)] : 0.f;
+      cluster_sync();
       if (i < n) score_out[i] = v;  // behind the kept ones zero: slots filled later start from there
     }
-  }
-  if (tid == 0) A.len_out[b] = A.budget;
+  if (ct == 0) A.len_out[b] = A.budget;
 }
 
-// Moves the kept slots.  Slot i's row of one pool and KV head is D contiguous values; a thread
-// moves 16 bytes of it.  To other pages every block takes kMoveRows slots of its own, each thread its
-// pieces side by side: slot, page and piece are three round trips, whatever their number.
+// Moves the kept slots.  Slot i's row of one pool and KV head is D contiguous values; a thread moves 16
+// bytes of it.  To other pages a block takes kMoveRows slots: it finds their places once, for `each` of
+// the 2 Hkv row sets (pool and KV head), and has the next set's rows on the way while it writes one's.
+// Bound by the bytes, read and written once.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveEach = 8;  // 16-byte pieces of a thread
+constexpr int kMoveEach = 4;  // 16-byte pieces of a thread and row set
 
 __device__ __forceinline__ int64_t dst_offset(const PagedEvictArgs &A, int b, int i) {
   if (!A.dst_table) return slot_offset(A.p, A.p.page_table + static_cast<int64_t>(b) * A.p.table_width, i);
@@ -388,18 +574,17 @@ __device__ __forceinline__ int64_t dst_offset(const PagedEvictArgs &A, int b, in
 }
 
 template <int CPR>  // pieces of a row
-__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_constant__ PagedEvictArgs A) {
+__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_constant__ PagedEvictArgs A, int each) {
   const PagedArgs &a = A.p;
-  const int b = blockIdx.z, h = blockIdx.y >> 1;
-  uint16_t *pool = static_cast<uint16_t *>(const_cast<void *>(blockIdx.y & 1 ? a.v : a.k)) + h * a.head_stride;
+  const int b = blockIdx.z;
   pdl_wait();
   pdl_trigger();
   const int n = min(A.len_out[b], A.budget);
+  constexpr int STEP = kMoveThreads / CPR, ROWS = STEP * kMoveEach;
+  const int i0 = blockIdx.x * ROWS + threadIdx.x / CPR, x = (threadIdx.x % CPR) * 8;
+  if (static_cast<int>(blockIdx.x) * ROWS >= n) return;
   const int32_t *kept = A.kept + static_cast<int64_t>(b) * A.budget;
   const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
-  constexpr int STEP = kMoveThreads / CPR;
-  const int i0 = blockIdx.x * STEP * kMoveEach + threadIdx.x / CPR, x = (threadIdx.x % CPR) * 8;
-  if (blockIdx.x * STEP * kMoveEach >= n) return;
   int j[kMoveEach];
 #pragma unroll
   for (int u = 0; u < kMoveEach; ++u) j[u] = kept[min(i0 + u * STEP, n - 1)];
@@ -408,14 +593,28 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_c
   for (int u = 0; u < kMoveEach; ++u) {
     src[u] = slot_offset(a, table, j[u]);
     dst[u] = i0 + u * STEP < n ? dst_offset(A, b, i0 + u * STEP) : -1;
+    if (src[u] < 0) dst[u] = -1;
   }
+  const int s0 = blockIdx.y * each, s1 = min(2 * a.n_kv_heads, s0 + each);
+  auto base = [&](int s) {
+    return static_cast<uint16_t *>(const_cast<void *>(s & 1 ? a.v : a.k)) + (s >> 1) * a.head_stride + x;
+  };
   uint4 v[kMoveEach];
+  auto load = [&](int s) {
 #pragma unroll
-  for (int u = 0; u < kMoveEach; ++u)
-    if (src[u] >= 0 && dst[u] >= 0) v[u] = *reinterpret_cast<const uint4 *>(pool + src[u] + x);
+    for (int u = 0; u < kMoveEach; ++u)
+      if (dst[u] >= 0) v[u] = __ldcs(reinterpret_cast<const uint4 *>(base(s) + src[u]));
+  };
+  load(s0);
+  for (int s = s0; s < s1; ++s) {
+    uint4 w[kMoveEach];
 #pragma unroll
-  for (int u = 0; u < kMoveEach; ++u)
-    if (src[u] >= 0 && dst[u] >= 0) *reinterpret_cast<uint4 *>(pool + dst[u] + x) = v[u];
+    for (int u = 0; u < kMoveEach; ++u) w[u] = v[u];
+    if (s + 1 < s1) load(s + 1);
+#pragma unroll
+    for (int u = 0; u < kMoveEach; ++u)
+      if (dst[u] >= 0) *reinterpret_cast<uint4 *>(base(s) + dst[u]) = w[u];
+  }
 }
 
 // In place, one block per (request, KV head, pool) goes up through the slots in chunks of
@@ -463,13 +662,17 @@ __global__ void __launch_bounds__(kInThreads) paged_move_in_place_kernel(const _
 
 static std::string launch_evict(const PagedEvictArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  cudaError_t e = launch_pdl(paged_select_kernel, dim3(a.n_requests), dim3(kSelThreads), 0, s, A);
+  cudaError_t e = launch_pdl_cluster(paged_select_kernel, dim3(kSelBlocks, a.n_requests), dim3(kSelThreads), 0, s, kSelBlocks, A);
   if (e == cudaSuccess) {
     const int most = A.budget < a.max_len ? A.budget : a.max_len;
     if (A.dst_table) {
-      const int rows = kMoveThreads * kMoveEach / (a.head_dim / 8);  // of a block
-      const dim3 grid((most + rows - 1) / rows, 2 * a.n_kv_heads, a.n_requests);
-      if (most > 0) e = launch_pdl(a.head_dim == 128 ? paged_move_kernel<16> : paged_move_kernel<8>, grid, dim3(kMoveThreads), 0, s, A);
+      const int rows = kMoveThreads * kMoveEach / (a.head_dim / 8), blocks = (most + rows - 1) / rows, sets = 2 * a.n_kv_heads;
+      // as many row sets a block as leave eight blocks an SM
+      int each = 1;
+      while (2 * each <= sets && static_cast<int64_t>(blocks) * a.n_requests * (sets / (2 * each)) >= 8 * num_sms()) each *= 2;
+      const dim3 grid(blocks, (sets + each - 1) / each, a.n_requests);
+      if (most > 0)
+        e = launch_pdl(a.head_dim == 128 ? paged_move_kernel<16> : paged_move_kernel<8>, grid, dim3(kMoveThreads), 0, s, A, each);
     } else if (A.budget < a.max_len) {  // else nothing can leave
       e = launch_pdl(paged_move_in_place_kernel, dim3(2 * a.n_kv_heads, a.n_requests), dim3(kInThreads), 0, s, A);
     }
@@ -649,8 +852,9 @@ bd_status bd_paged_weights(const bd_paged_kv *kv, const bd_paged_batch *batch, c
     if (!lse || misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged weights: lse must be given");
   }
   if (misaligned(rows_used, 4)) return refuse(BD_ERR_INVALID_ARG, "paged weights: rows_used misaligned");
-  if (static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30))
-    return refuse(BD_ERR_UNSUPPORTED, "paged weights: max_rows * n_q_heads too large");
+  if (static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30) ||
+      static_cast<int64_t>(batch->n_requests) * (batch->max_len / 16 + 1) >= (1ll << 30))
+    return refuse(BD_ERR_UNSUPPORTED, "paged weights: max_rows * n_q_heads or n_requests * max_len too large");
   if (!std::isfinite(decay)) return refuse(BD_ERR_INVALID_ARG, "paged weights: decay must be finite");
   if (!score_out || misaligned(score_out, 4) || misaligned(score_in, 4) || score_stride < batch->max_len)
     return refuse(BD_ERR_INVALID_ARG, "paged weights: score_out must be given, with rows of at least max_len entries");
