@@ -82,7 +82,11 @@ size_t many_bytes(int n_requests, int max_rows, int group, int head_dim);
 std::string launch_attention_few(PagedAttnArgs a, void *workspace, int dtype, cudaStream_t s);
 std::string launch_attention_many(PagedAttnArgs a, void *workspace, int dtype, cudaStream_t s);
 
+bool weights_many_takes(const PagedArgs &a);
+std::string launch_weights_many(const PagedWeightsArgs &A, int dtype, cudaStream_t s);
+
 unsigned take_error_word_paged();
+unsigned take_error_word_paged_wt();
 unsigned take_error_word_paged_attn();
 unsigned take_error_word_paged_tc();
 

@@ -471,3 +471,58 @@ def test_python_checks():
         t = c.cache.batch(c.table, c.lend, c.startd, 3, 2, 50, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
         c.cache.attention(t, c.qd, out)
     assert isinstance(c.cache, PagedCache)
+
+
+@pytest.mark.parametrize("rows,group,hkv,window,n_sink,d,dtype", [
+    (16, 4, 8, 0, 0, 128, "bf16"), (64, 4, 2, 0, 0, 128, "fp16"), (100, 1, 3, 0, 0, 64, "bf16"), (65, 2, 1, 40, 3, 64, "fp16"),
+    (33, 8, 9, 100, 130, 128, "bf16"), (129, 16, 1, 1, 0, 128, "bf16"), (70, 3, 2, 50, 4, 128, "bf16"), (8, 128, 2, 0, 0, 64, "fp16"),
+    (300, 4, 1, 129, 1, 64, "bf16")])
+@pytest.mark.parametrize("page", [8, 33, 64])
+def test_weights_of_many_rows(rows, group, hkv, window, n_sink, d, dtype, page):
+    """The row counts from which the tensor-core form takes over, and the forms that it leaves."""
+    c = PagedCase((rows + 260, 257, max(1, rows - 5)), (rows, min(rows, 40), rows), hkv=hkv, group=group, d=d, dtype=dtype, page=page,
+                  window=window, n_sink=n_sink, lead=1, seed=rows).build()
+    _, lse = c.attend()
+    used = (rows, 0, max(1, rows - 7))
+    score = torch.full((3, c.max_len), -7.0, device="cuda")
+    c.cache.weights(c.batch, c.qd, lse, score, rows_used=torch.tensor(used, dtype=torch.int32, device="cuda"), window=window, n_sink=n_sink)
+    sync()
+    got, lse = score.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, (n, r) in enumerate(zip(c.lens, c.rows)):
+        s = slice(c.starts[b], c.starts[b] + r)
+        w = P.weights(c.qf[s], c.k[b], lse[s], used[b], window, n_sink, c.scale)
+        _, _, _, size = P.attention(c.qf[s], c.k[b], c.v[b], window, n_sink, c.scale)
+        S = size.max()      # the tolerance of test_weights_match_the_oracle
+        ds = c.d * 2.0 ** -23 * S + (2 * S + np.log(n + 1) + 8) * 2.0 ** -22
+        tol = (1.01 * ds + (r * hkv * group + 32) * 2.0 ** -23) * w + 2.0 ** -100
+        assert (np.abs(got[b, :n] - w) <= tol).all(), b
+        assert (got[b, n:] == -7.0).all()
+
+
+@pytest.mark.parametrize("rows", [2, 40])
+def test_weights_of_hidden_garbage(rows):
+    """NaN keys in a slot, NaN in a row that does not count: other slots and rows stand."""
+    case = PagedCase((300,), (rows,), hkv=2).build()
+    _, lse = case.attend()
+    clean, score = (torch.zeros(1, 300, device="cuda") for _ in range(2))
+    used = torch.tensor([rows - 1], dtype=torch.int32, device="cuda")
+    case.cache.weights(case.batch, case.qd, lse, clean, rows_used=used)
+    case.kd[case.table[0, 3].item(), :, 5] = float("nan")     # slot 53, seen by every row
+    case.qd[rows - 1] = float("nan")
+    lse[rows - 1] = float("nan")
+    case.cache.weights(case.batch, case.qd, lse, score, rows_used=used)
+    sync()
+    assert torch.isnan(score[0, 53])
+    keep = torch.arange(300, device="cuda") != 53
+    assert torch.equal(score[0, keep], clean[0, keep])
+
+
+def test_a_long_list_of_items_is_planned_apart():
+    """More requests and row tiles than a block of the tensor-core attention sums up by itself."""
+    rows = [1] * 130
+    rows[7], rows[60], rows[129] = 600, 90, 300
+    lens = [r + (i * 37) % 190 for i, r in enumerate(rows)]
+    c = PagedCase(tuple(lens), tuple(rows), hkv=1, group=8, d=64).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
