@@ -400,16 +400,18 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One cluster of eight blocks per request.  The key of the last slot that stays is found by radix
-// selection, eleven, eleven and ten bits a pass: a histogram of the slots that match the bits found so
-// far -- each block of its share of the slots, summed over the cluster through distributed shared
-// memory -- then the digit that holds the wanted rank.  Then each warp, over a run of slots of its own,
-// counts what stays -- what is larger, and of what is equal the first ones -- and, knowing what stays
-// before its run, places it.  Bound by the round trips of its passes and barriers; on one block, by that
-// SM's instructions (32 768 slots: 57 us).
+// One cluster of blocks per request (one block up to kSelSmall slots, else eight).  Every warp has a run
+// of slots of its own, in registers as far as they reach.  The key of the last slot that stays is found
+// by radix selection, eleven, eleven and ten bits a pass: a histogram of the slots that match the bits
+// found so far -- each block of its slots, summed over the cluster through distributed shared memory --
+// then the digit that holds the wanted rank.  Then each warp counts what stays of its run -- what is
+// larger, and of what is equal the first ones -- and, knowing what stays before its run, places it.
+// Bound by the round trips of its passes and barriers.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBlocks = 8;
+constexpr int kSelSmall = 8192;
+constexpr int kSelEach = 8;  // slots of a thread in registers
 constexpr int kBins = 2048;
 
 __device__ __forceinline__ int2 ld_cluster_i2(uint32_t addr) {
@@ -426,8 +428,10 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   __shared__ uint32_t s_digit;
   __shared__ int s_need;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
-  const int rank = blockIdx.x, ct = rank * kSelThreads + tid;  // thread of the cluster
-  constexpr int CT = kSelBlocks * kSelThreads;
+  const int blocks = gridDim.x, rank = blockIdx.x, ct = rank * kSelThreads + tid, CT = blocks * kSelThreads;  // of the cluster
+  auto meet = [&]() {
+    if (blocks > 1) cluster_sync(); else __syncthreads();
+  };
   pdl_wait();
   pdl_trigger();
   const int n = request_len(A.p, b);
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
       kept[j] = j;
       if (score_out && !in_place) score_out[j] = score[j];
     }
-    cluster_sync();  // every block has read the length: it may be replaced
+    meet();  // every thread has read the length: it may be replaced
     if (ct == 0) A.len_out[b] = n;
     return;
   }
@@ -448,6 +452,12 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   const int lo = A.n_sink, hi = n - A.n_recent;
   int need = A.budget - A.n_sink - A.n_recent;
   const bool none = need == 0;
+  // the warp's run: steps of 32 slots from j_lo on
+  const int steps = (n + CT - 1) / CT, j_lo = (rank * kSelWarps + warp) * steps * 32 + lane;
+  float held[kSelEach];
+#pragma unroll
+  for (int k = 0; k < kSelEach; ++k) held[k] = k < steps && j_lo + 32 * k < n ? score[j_lo + 32 * k] : 0.f;
+  auto value = [&](int k, int j) { return j < n ? score[j] : 0.f; };  // beyond what is held
   uint32_t key = 0xffffffffu;  // key of the last one that stays (none: no score has this one)
   if (!none) {
     uint32_t mask = 0;
@@ -457,21 +467,30 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
       int *h = hist[pass & 1];
       for (int d = tid; d < kBins; d += kSelThreads) h[d] = 0;
       __syncthreads();
+      auto count = [&](int j, float v) {
+        const uint32_t u = score_key(v);
+        if (j >= lo && j < hi && (u & mask) == key) atomicAdd(&h[(u >> shift) & (bins - 1)], 1);
+      };
+#pragma unroll
+      for (int k = 0; k < kSelEach; ++k)
+        if (k < steps) count(j_lo + 32 * k, held[k]);
 #pragma unroll 4
-      for (int j = lo + ct; j < hi; j += CT) {
-        const uint32_t u = score_key(score[j]);
-        if ((u & mask) == key) atomicAdd(&h[(u >> shift) & (bins - 1)], 1);
-      }
-      cluster_sync();
+      for (int k = kSelEach; k < steps; ++k) count(j_lo + 32 * k, value(k, j_lo + 32 * k));
+      meet();
       // thread t holds digits bins-1-2t and bins-2-2t, the larger first, of all blocks
       int c[2] = {0, 0};
       if (2 * tid < bins) {
-        const uint32_t at = smem_u32(h + bins - 2 - 2 * tid);
+        if (blocks == 1) {
+          c[0] = h[bins - 1 - 2 * tid];
+          c[1] = h[bins - 2 - 2 * tid];
+        } else {
+          const uint32_t at = smem_u32(h + bins - 2 - 2 * tid);
 #pragma unroll
-        for (int r = 0; r < kSelBlocks; ++r) {
-          const int2 v = ld_cluster_i2(cluster_map(at, r));
-          c[0] += v.y;
-          c[1] += v.x;
+          for (int r = 0; r < kSelBlocks; ++r) {
+            const int2 v = ld_cluster_i2(cluster_map(at, r));
+            c[0] += v.y;
+            c[1] += v.x;
+          }
         }
       }
       int sum = c[0] + c[1];
@@ -498,33 +517,37 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
     }
   }
   // need: how many of the slots whose key is `key` stay (the first ones)
-  const int run = (n + CT - 1) / CT * 32, j_lo = min(n, (rank * kSelWarps + warp) * run), j_hi = min(n, j_lo + run);
   int2 cnt = make_int2(0, 0);
-#pragma unroll 4
-  for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
-    const int j = j0 + lane;
-    const bool in = j < j_hi && j >= lo && j < hi;
-    const uint32_t u = in ? score_key(score[j]) : 0u;
-    cnt.x += __popc(__ballot_sync(0xffffffffu, j < j_hi && (!in || u > key)));
+  auto tally = [&](int j, float v) {
+    const bool in = j >= lo && j < hi;
+    const uint32_t u = score_key(v);
+    cnt.x += __popc(__ballot_sync(0xffffffffu, j < n && (!in || u > key)));
     cnt.y += __popc(__ballot_sync(0xffffffffu, in && u == key));
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kSelEach; ++k)
+    if (k < steps) tally(j_lo + 32 * k, held[k]);
+#pragma unroll 4
+  for (int k = kSelEach; k < steps; ++k) tally(j_lo + 32 * k, value(k, j_lo + 32 * k));
   if (lane == 0) warp_cnt[warp] = cnt;
   __syncthreads();
   int2 at = lane < warp ? warp_cnt[lane] : make_int2(0, 0);
-  if (warp == 0) {
-    int2 all = warp_cnt[lane];
+  if (blocks > 1) {
+    if (warp == 0) {
+      int2 all = warp_cnt[lane];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      all.x += __shfl_xor_sync(0xffffffffu, all.x, o);
-      all.y += __shfl_xor_sync(0xffffffffu, all.y, o);
+      for (int o = 16; o > 0; o >>= 1) {
+        all.x += __shfl_xor_sync(0xffffffffu, all.x, o);
+        all.y += __shfl_xor_sync(0xffffffffu, all.y, o);
+      }
+      if (lane == 0) block_cnt = all;
     }
-    if (lane == 0) block_cnt = all;
-  }
-  cluster_sync();
-  if (lane < rank) {  // the blocks before this one, a lane each
-    const int2 v = ld_cluster_i2(cluster_map(smem_u32(&block_cnt), lane));
-    at.x += v.x;
-    at.y += v.y;
+    cluster_sync();
+    if (lane < rank) {  // the blocks before this one, a lane each
+      const int2 v = ld_cluster_i2(cluster_map(smem_u32(&block_cnt), lane));
+      at.x += v.x;
+      at.y += v.y;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -533,31 +556,33 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   }
   int larger = at.x, equal = at.y;  // before this run
   if (none) need = 0;
-#pragma unroll 1
-  for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
-    const int j = j0 + lane;
-    const bool here = j < j_hi, in = here && j >= lo && j < hi;
-    const float v = here ? score[j] : 0.f;
-    const uint32_t u = in ? score_key(v) : 0u;
+  auto place = [&](int j, float v) {
+    const bool here = j < n, in = j >= lo && j < hi;
+    const uint32_t u = score_key(v);
     const unsigned below = (1u << lane) - 1;
     const unsigned gt = __ballot_sync(0xffffffffu, here && (!in || u > key)), eq = __ballot_sync(0xffffffffu, in && u == key);
-    const int e = equal + __popc(eq & below), place = larger + __popc(gt & below) + min(e, need);
+    const int e = equal + __popc(eq & below), to = larger + __popc(gt & below) + min(e, need);
     const bool keep = here && (!in || u > key || (u == key && e < need));
     larger += __popc(gt);
     equal += __popc(eq);
     if (keep) {
-      kept[place] = j;
-      if (score_out && !in_place) score_out[place] = v;
+      kept[to] = j;
+      if (score_out && !in_place) score_out[to] = v;
     }
-  }
-  cluster_sync();  // kept[] is complete, every block's shared memory and the length are read
+  };
+#pragma unroll
+  for (int k = 0; k < kSelEach; ++k)
+    if (k < steps) place(j_lo + 32 * k, held[k]);
+#pragma unroll 1
+  for (int k = kSelEach; k < steps; ++k) place(j_lo + 32 * k, value(k, j_lo + 32 * k));
+  meet();  // kept[] is complete, every block's shared memory and the length are read
   if (in_place)
     // score i comes from kept[i] >= i: a step of them is written when all of it has been read, and the
     // steps behind it read behind what it wrote
     for (int i0 = 0; i0 < n; i0 += CT) {
       const int i = i0 + ct;
-      const float v = i < A.budget ? score[__ldcg(kept + i)] : 0.f;
-      cluster_sync();
+      const float v = i < A.budget ? __ldcg(score + __ldcg(kept + i)) : 0.f;
+      meet();
       if (i < n) score_out[i] = v;  // behind the kept ones zero: slots filled later start from there
     }
   if (ct == 0) A.len_out[b] = A.budget;
@@ -664,7 +689,10 @@ __global__ void __launch_bounds__(kInThreads) paged_move_in_place_kernel(const _
 
 static std::string launch_evict(const PagedEvictArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  cudaError_t e = launch_pdl_cluster(paged_select_kernel, dim3(kSelBlocks, a.n_requests), dim3(kSelThreads), 0, s, kSelBlocks, A);
+  // a barrier of eight blocks costs about a microsecond: fewer slots are one block's (4096: 19 us with
+  // eight, 13 us with one)
+  const int sel = a.max_len <= kSelSmall ? 1 : kSelBlocks;
+  cudaError_t e = launch_pdl_cluster(paged_select_kernel, dim3(sel, a.n_requests), dim3(kSelThreads), 0, s, sel, A);
   if (e == cudaSuccess) {
     const int most = A.budget < a.max_len ? A.budget : a.max_len;
     if (A.dst_table) {
