@@ -275,14 +275,19 @@ struct FewWarp {
 };
 
 // start[b] = units of the requests before b; all threads of the block.
+// The first NT requests' sizes are kept in `first`.
 template <int NT>
-__device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s) {
+__device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s, Request *first) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t base = 0;
   for (int b0 = 0; b0 < a.n_requests; b0 += NT) {
     const int b = b0 + tid;
     int64_t v = 0;
-    if (b < a.n_requests) v = static_cast<int64_t>(tiles_of(a, request_of(a, b)).count) * a.n_kv_heads;
+    if (b < a.n_requests) {
+      const Request rq = request_of(a, b);
+      if (b0 == 0) first[tid] = rq;
+      v = static_cast<int64_t>(tiles_of(a, rq).count) * a.n_kv_heads;
+    }
     int64_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -316,13 +321,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ int64_t start[BD_PAGED_MAX_REQUESTS + 1];
   __shared__ int64_t warp_sum_s[kFewWarps];
+  __shared__ Request first[kFewThreads];
   __shared__ float2 ml[kFewWarps][kFewRows];
   __shared__ unsigned bad_rows;
   const PagedArgs &a = A.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  scan_requests<kFewThreads>(a, start, warp_sum_s);
+  scan_requests<kFewThreads>(a, start, warp_sum_s, first);
   const int64_t units = start[a.n_requests];
   const int ctas = ctas_used(units, A.n_ctas), g = blockIdx.x;
   for (int b = g; b < a.n_requests; b += gridDim.x)
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   uint8_t *mine = sm_raw + warp * Few<D>::kWarpBytes;
   for (int64_t u = u0; u < u1;) {
     const int b = request_at(start, a.n_requests, u);
-    const Request rq = request_of(a, b);
+    const Request rq = b < kFewThreads ? first[b] : request_of(a, b);
     const Tiles tl = tiles_of(a, rq);
     const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
     const int h = in / static_cast<uint32_t>(tl.count), t0 = in - h * tl.count;
@@ -412,6 +418,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
 // a row's parts side by side and leaves their weights in shared memory; then the threads, as many groups
 // of them as fit, each add every kth part.
 constexpr int kJoinThreads = 512;
+constexpr int kJoinHeld = 10;  // parts of a thread in registers
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_constant__ PagedAttnArgs A) {
   __shared__ unsigned bad_rows;
@@ -426,6 +433,16 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
   const Request rq = {j.len, j.row0, j.rows};
   const int n = j.n;
   auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * kFewRows; };
+  const int pieces = n * (D / 4);  // at most kJoinThreads
+  const int groups = kJoinThreads / pieces, k = tid / pieces, c = tid - k * pieces;
+  const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
+  // this thread's first parts are on their way while the weights are worked out
+  float4 held[kJoinHeld];
+#pragma unroll
+  for (int x = 0; x < kJoinHeld; ++x) {
+    const int i = k + x * groups;
+    if (k < groups && i < j.np) held[x] = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
+  }
   if (tid == 0) bad_rows = 0u;
   if (warp < n) {
     float m = -INFINITY, l = 0.f;
@@ -445,22 +462,23 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
     if (lane == 0) row_ml[warp] = make_float2(M, L);
   }
   __syncthreads();
-  const int pieces = n * (D / 4);  // at most kJoinThreads
-  const int groups = kJoinThreads / pieces, k = tid / pieces, c = tid - k * pieces;
-  const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (k < groups) {
-#pragma unroll 4
-    for (int i = k; i < j.np; i += groups) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
-      const float w = weight[r][i];
-      if (w != 0.f) {
-        o.x += w * v.x;
-        o.y += w * v.y;
-        o.z += w * v.z;
-        o.w += w * v.w;
-      }
+  auto add = [&](int i, const float4 &v) {
+    const float w = weight[r][i];
+    if (w != 0.f) {
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
     }
+  };
+  if (k < groups) {
+#pragma unroll
+    for (int x = 0; x < kJoinHeld; ++x)
+      if (k + x * groups < j.np) add(k + x * groups, held[x]);
+#pragma unroll 4
+    for (int i = k + kJoinHeld * groups; i < j.np; i += groups)
+      add(i, __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d)));
   }
   if (groups > 1) {
     sums[tid] = o;

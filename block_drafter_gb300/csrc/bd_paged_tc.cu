@@ -805,6 +805,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
 // parts side by side (more are rare: they go round again), then add the parts, four columns (two with
 // D = 64) a lane.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinHeld = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __grid_constant__ PagedAttnArgs A) {
   constexpr int C = D / 32;
@@ -818,6 +819,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __g
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.f;
   for (int i0 = 0; i0 < j.np; i0 += 32) {
+    const int n = min(32, j.np - i0);
+    auto part = [&](int i, float (&y)[C]) {
+      const float *v = A.part_o + slot(i0 + i) * D + C * lane;
+      if constexpr (C == 4)
+        *reinterpret_cast<float4 *>(y) = __ldcg(reinterpret_cast<const float4 *>(v));
+      else
+        *reinterpret_cast<float2 *>(y) = __ldcg(reinterpret_cast<const float2 *>(v));
+    };
+    float held[kJoinHeld][C];  // the first parts are on their way while the weights are worked out
+#pragma unroll
+    for (int i = 0; i < kJoinHeld; ++i)
+      if (i < n) part(i, held[i]);
     float2 x = make_float2(-INFINITY, 0.f);
     if (i0 + lane < j.np) x = __ldcg(A.part_ml + slot(i0 + lane));
     if (x.y == 0.f) x.x = -INFINITY;
@@ -827,19 +840,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __g
     M = m;
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] *= back;
-    const int n = min(32, j.np - i0);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float *v = A.part_o + slot(i0 + i) * D + C * lane;
-      float y[C];
-      if constexpr (C == 4)
-        *reinterpret_cast<float4 *>(y) = __ldcg(reinterpret_cast<const float4 *>(v));
-      else
-        *reinterpret_cast<float2 *>(y) = __ldcg(reinterpret_cast<const float2 *>(v));
+    auto add = [&](int i, const float (&y)[C]) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
       for (int c = 0; c < C; ++c)
         if (wi != 0.f) o[c] += wi * y[c];
+    };
+#pragma unroll
+    for (int i = 0; i < kJoinHeld; ++i)
+      if (i < n) add(i, held[i]);
+#pragma unroll 4
+    for (int i = kJoinHeld; i < n; ++i) {
+      float y[C];
+      part(i, y);
+      add(i, y);
     }
   }
   const Request rq = {j.len, j.row0, j.rows};
