@@ -509,22 +509,33 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
   const uint32_t ts = tmem + lanes + C::kS + st * C::kStepS, tp = tmem + lanes + C::kP + st * C::kStepP;
   const uint32_t to0 = tmem + lanes + C::kO;
   const uint32_t group = a.group;
+  // A warp's 32 rows of its stream's query tile are its own: it fills them, and passes its results through
+  // them on their way to whole rows in global memory.  Lane: piece c of rows r_first, r_first + RPI, ...
+  constexpr int CPR = D / 8, RPI = 32 / CPR;
+  const int lane = wt & 31, c = lane % CPR, r_first = (wt & ~31) + lane / CPR;
+  const uint32_t qt = smem_u32(smp + st * C::kTile) + (c >> 3) * kAtom;
+  const uint32_t step_e = RPI % group;
+  const int64_t step_q = RPI / group * a.q_stride + step_e * D;
   uint32_t n_s = 0, n_o = 0, n_x = 0;
   Segments walk(B, segs);
   while (const Segment *g = walk.next()) {
     const bool split = g->split;
     const int R = g->r0 + g->n, tile0 = g->r0 + (split ? 0 : st * 128);  // the stream's rows: tile0 .. below R
-    // query tile: 16 bytes a thread and step, consecutive threads along a row
+    // query tile: every warp the rows of its own 32, consecutive lanes along a row
     if (st == 0 || !split) {
-      constexpr int CPR = D / 8, RPS = 128 / CPR;
-      const int c = wt % CPR;
-      const uint32_t qt = smem_u32(smp + st * C::kTile) + (c >> 3) * kAtom;
       const T *src = static_cast<const T *>(a.q) + g->row0 * a.q_stride + g->h * a.group * D + c * 8;
+      uint32_t i = (tile0 + r_first) / group, e = tile0 + r_first - i * group;
+      int64_t at = i * a.q_stride + e * D;
 #pragma unroll 4
-      for (int u = 0; u < CPR; ++u) {
-        const int r = u * RPS + wt / CPR, row = tile0 + r;
-        const uint32_t i = row / group, e = row - i * group;
-        cp_async16(qt + r * 128 + (((c & 7) ^ (r & 7)) << 4), row < R ? src + i * a.q_stride + e * D : a.q, row < R);
+      for (int r = r_first; r < r_first + 32; r += RPI) {
+        const bool in = tile0 + r < R;
+        cp_async16(qt + r * 128 + (((c & 7) ^ (r & 7)) << 4), in ? src + at : a.q, in);
+        e += step_e;
+        at += step_q;
+        if (e >= group) {
+          e -= group;
+          at += a.q_stride - a.group * D;
+        }
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -627,46 +638,77 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
       ref = M;
     }
     const bool valid = row < R, whole = g->whole;
-    // a block's parts: of the item that its share begins inside, and of the one that it ends inside
-    const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (g->t0 > 0 ? 0 : 1)) * kItemRows + (row - g->r0);
-    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-    const int i = valid ? row / group : 0, head = g->h * a.group + (valid ? row - i * a.group : 0);
-    T *out = static_cast<T *>(A.out) + (g->row0 + i) * A.out_stride + head * D;
     const bool two = __any_sync(0xffffffffu, w1 != 0.f);
-    w0 = w0 == 0.f || l == 0.f ? 0.f : w0 * inv;
-    w1 *= inv;
-    bool bad = false;
-#pragma unroll 1
-    for (int k = 0; k < D / 32; ++k) {
-      uint32_t x[32], y[32];
-      tmem_ld32_nowait(to0 + (split ? 0 : st * C::kStepO) + 32 * k, x);
-      if (two) tmem_ld32_nowait(to0 + C::kStepO + 32 * k, y);
-      tmem_ld_wait();
-      tmem_values(x);
-      float o[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = w0 == 0.f ? 0.f : __uint_as_float(x[e]) * w0;
-      if (two) {
-        tmem_values(y);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (w1 != 0.f) o[e] += __uint_as_float(y[e]) * w1;
-      }
-      if (!valid) continue;
-      if (whole) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) bad |= !(fabsf(o[e]) <= 3.4e38f);
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4 *>(out + 32 * k + e) =
-              make_uint4(Pair<T>::pack(o[e], o[e + 1]), Pair<T>::pack(o[e + 2], o[e + 3]),
-                         Pair<T>::pack(o[e + 4], o[e + 5]), Pair<T>::pack(o[e + 6], o[e + 7]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4 *>(A.part_o + part * D + 32 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-      }
+    {
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      w0 = w0 == 0.f || l == 0.f ? 0.f : w0 * inv;
+      w1 *= inv;
     }
+    bool bad = false;
+    const uint32_t own = smem_u32(smp + st * C::kTile) + wt * 128;  // this row in the tile
+    T *out = static_cast<T *>(A.out) + g->row0 * A.out_stride + g->h * a.group * D + c * 8;
+    // a block's parts: of the item that its share begins inside, and of the one that it ends inside
+    float *part = A.part_o + (static_cast<int64_t>(2 * blockIdx.x + (g->t0 > 0 ? 0 : 1)) * kItemRows + (tile0 - g->r0)) * D;
+    // 16-bit results fill the rows once, 32-bit parts take the two halves of D in turn
+#pragma unroll 1
+    for (int turn = 0; turn < (whole ? 1 : 2); ++turn) {
+#pragma unroll 1
+      for (int k = 0; k < (whole ? D : D / 2); k += 16) {  // 16 columns
+        float o[16];
+        tmem_ld16(to0 + (split ? 0 : st * C::kStepO) + turn * (D / 2) + k, o);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = w0 == 0.f ? 0.f : o[x] * w0;
+        if (two) {
+          float y[16];
+          tmem_ld16(to0 + C::kStepO + turn * (D / 2) + k, y);
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            if (w1 != 0.f) o[x] += y[x] * w1;
+        }
+        const uint32_t word = whole ? k / 2 : k;  // 4-byte words before these columns
+        uint32_t v[16];
+        if (whole) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) bad |= !(fabsf(o[x]) <= 3.4e38f);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = Pair<T>::pack(o[2 * x], o[2 * x + 1]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(o[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x < 2 || !whole) {
+            const uint32_t piece = word / 4 + x;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(own + (piece >> 3) * kAtom + (((piece & 7) ^ (wt & 7)) << 4)),
+                         "r"(v[4 * x]), "r"(v[4 * x + 1]), "r"(v[4 * x + 2]), "r"(v[4 * x + 3])
+                         : "memory");
+          }
+      }
+      __syncwarp();
+      uint32_t i = (tile0 + r_first) / group, e = tile0 + r_first - i * group;
+      int64_t at = i * A.out_stride + e * D;
+#pragma unroll 4
+      for (int r = r_first; r < r_first + 32; r += RPI) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(qt + r * 128 + (((c & 7) ^ (r & 7)) << 4)) : "memory");
+        if (tile0 + r < R) {
+          if (whole)
+            *reinterpret_cast<uint4 *>(out + at) = v;
+          else
+            *reinterpret_cast<uint4 *>(part + r * D + turn * (D / 2) + 4 * c) = v;
+        }
+        e += step_e;
+        at += RPI / group * A.out_stride + step_e * D;
+        if (e >= group) {
+          e -= group;
+          at += A.out_stride - a.group * D;
+        }
+      }
+      __syncwarp();
+    }
+    bad = bad && valid;
     tc_fence_before();
     if (split) mbar_arrive(B.x_done);  // stream 1's sums and its exchange are read
     const Request rq = {g->len, g->row0, g->len - g->base};
@@ -674,7 +716,7 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
       if (whole)
         store_lse(A, rq, g->h, row, ref, l);
       else
-        A.part_ml[part] = make_float2(ref, l);
+        A.part_ml[static_cast<int64_t>(2 * blockIdx.x + (g->t0 > 0 ? 0 : 1)) * kItemRows + (row - g->r0)] = make_float2(ref, l);
     }
     const int b = g->b, h = g->h;
     walk.done(wt & 31);
