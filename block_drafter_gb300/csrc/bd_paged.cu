@@ -10,12 +10,12 @@ namespace bd {
 BD_DEFINE_ERROR_TAKER(take_error_word_paged)
 
 // ------------------------------------------------------------------ append
-// Copies each row's keys and values into its slot, 16 bytes a thread.  A block takes rows_per_cta
-// consecutive rows and first finds the request of each: every thread tests some of the requests'
-// row ranges against the block's.
+// Copies each row's keys and values into its slot.  A block takes rows_per_cta consecutive rows; the first
+// kAppendEach 16-byte pieces of every thread are on their way while it finds the rows' requests -- every
+// thread tests some of the requests' row ranges against the block's -- and slots.  Bound by the bytes.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 8;
-constexpr int kAppendEach = 4;  // pieces of a thread in flight
+constexpr int kAppendRows = 4;
+constexpr int kAppendEach = 4;
 
 struct PagedAppendArgs {
   PagedArgs p;
@@ -27,45 +27,50 @@ struct PagedAppendArgs {
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs A) {
   const PagedArgs &a = A.p;
   __shared__ int64_t off[kAppendRows];  // element offset of the row's slot, -1: not stored
+  __shared__ int2 place[kAppendRows];   // the row's request and slot (negative: none)
   const int r0 = blockIdx.x * A.rows_per_cta, r1 = min(a.n_rows, r0 + A.rows_per_cta);
-  if (threadIdx.x < kAppendRows) off[threadIdx.x] = -1;
+  const uint32_t per_head = a.head_dim / 8, per_side = a.n_kv_heads * per_head, per_row = 2 * per_side;
+  const int pieces = (r1 - r0) * per_row;
+  if (threadIdx.x < kAppendRows) place[threadIdx.x] = make_int2(0, -1);
   pdl_wait();
   pdl_trigger();
+  uint4 v[kAppendEach];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int u = 0; u < kAppendEach; ++u) {
+      const uint32_t c = c0 + u * kAppendThreads, r = c / per_row, x = c - r * per_row;
+      if (c >= pieces) continue;
+      const void *row = x < per_side ? static_cast<const uint16_t *>(A.k_new) + (r0 + r) * A.k_stride + x * 8
+                                     : static_cast<const uint16_t *>(A.v_new) + (r0 + r) * A.v_stride + (x - per_side) * 8;
+      v[u] = __ldcs(static_cast<const uint4 *>(row));
+    }
+  };
+  load(threadIdx.x);
   __syncthreads();
   for (int b = threadIdx.x; b < a.n_requests; b += kAppendThreads) {
-    const int s = a.row_start[b], e = a.row_start[b + 1];
+    const int s = a.row_start[b], e = a.row_start[b + 1], n = request_len(a, b);
     if (s < 0 || e < s || e > a.n_rows || e - s > a.max_rows) {
       atomicOr(&g_error_word, DEVERR_BAD_INDEX);
       continue;
     }
-    if (s >= r1 || e <= r0) continue;
-    const int n = request_len(a, b);
-    for (int r = max(s, r0); r < min(e, r1); ++r) {
-      const int p = n - (e - r);
-      off[r - r0] = p < 0 ? -1 : slot_offset(a, a.page_table + static_cast<int64_t>(b) * a.table_width, p);
-    }
+    for (int r = max(s, r0); r < min(e, r1); ++r) place[r - r0] = make_int2(b, n - (e - r));
   }
   __syncthreads();
-  const int per_head = a.head_dim / 8, per_side = a.n_kv_heads * per_head, per_row = 2 * per_side;
-  const int pieces = (r1 - r0) * per_row;
+  if (threadIdx.x < kAppendRows) {
+    const int2 p = place[threadIdx.x];
+    off[threadIdx.x] = p.y < 0 ? -1 : slot_offset(a, a.page_table + static_cast<int64_t>(p.x) * a.table_width, p.y);
+  }
+  __syncthreads();
   for (int c0 = threadIdx.x; c0 < pieces; c0 += kAppendEach * kAppendThreads) {
-    uint4 v[kAppendEach];
-    int64_t to[kAppendEach];
-    bool k[kAppendEach];
+    if (c0 != static_cast<int>(threadIdx.x)) load(c0);
 #pragma unroll
     for (int u = 0; u < kAppendEach; ++u) {
-      const int c = c0 + u * kAppendThreads, r = c / per_row, x = c - r * per_row;
-      to[u] = -1;
+      const uint32_t c = c0 + u * kAppendThreads, r = c / per_row, x = c - r * per_row;
       if (c >= pieces || off[r] < 0) continue;
-      k[u] = x < per_side;
-      const int w = k[u] ? x : x - per_side, h = w / per_head;
-      v[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(k[u] ? A.k_new : A.v_new) +
-                                                   (r0 + r) * (k[u] ? A.k_stride : A.v_stride) + w * 8));
-      to[u] = off[r] + h * a.head_stride + (w - h * per_head) * 8;
+      const uint32_t w = x < per_side ? x : x - per_side, h = w / per_head;
+      uint16_t *to = static_cast<uint16_t *>(const_cast<void *>(x < per_side ? a.k : a.v));
+      *reinterpret_cast<uint4 *>(to + off[r] + h * a.head_stride + (w - h * per_head) * 8) = v[u];
     }
-#pragma unroll
-    for (int u = 0; u < kAppendEach; ++u)
-      if (to[u] >= 0) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(const_cast<void *>(k[u] ? a.k : a.v)) + to[u]) = v[u];
   }
 }
 
