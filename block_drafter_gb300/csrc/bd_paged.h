@@ -37,6 +37,7 @@ struct PagedAttnArgs {
   float *part_o;        // [2 * n_ctas][part rows][head_dim] unnormalised sums
   float2 *part_ml;      // [2 * n_ctas][part rows] (reference in log2 units, row sum)
   int n_ctas;
+  bool whole;           // every item is one block's: no shares, no joins
 };
 
 struct PagedShare {  // item a block's share begins in, and the units before that item
@@ -76,6 +77,11 @@ struct PagedEvictArgs {
   int64_t score_out_stride;
 };
 
+// Bound on the slots that any rows of one request see.
+inline int64_t visible_slots(const PagedArgs &a) {
+  const int64_t seen = a.window > 0 ? static_cast<int64_t>(a.window) + a.max_rows + a.n_sink : a.max_len;
+  return seen < a.max_len ? seen : a.max_len;
+}
 inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 size_t few_bytes(int head_dim);
 size_t many_bytes(int n_requests, int max_rows, int group, int head_dim);

@@ -55,11 +55,12 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq)
   return t;
 }
 
-__device__ __forceinline__ int ctas_used(int64_t units, int most) {
-  const int64_t c = (units + kFewWarps - 1) >> 2;  // at least a unit for each of the four warps
+// Blocks that work: a unit for each of their four warps, but as many as there are heads (a block takes
+// its heads one after the other, about 2.5 us each).
+__device__ __forceinline__ int ctas_used(int64_t units, int heads, int most) {
+  const int64_t quarter = (units + kFewWarps - 1) >> 2, c = quarter > heads ? quarter : units < heads ? units : heads;
   return c < 1 ? 1 : static_cast<int>(c < most ? c : most);
 }
-
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -328,25 +329,49 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  scan_requests<kFewThreads>(a, start, warp_sum_s, first);
-  const int64_t units = start[a.n_requests];
-  const int ctas = ctas_used(units, A.n_ctas), g = blockIdx.x;
-  for (int b = g; b < a.n_requests; b += gridDim.x)
-    if (start[b + 1] == start[b]) {  // rows without a slot
-      const Request rq = request_of(a, b);
-      empty_rows<T, D>(A, rq, rq.rows, tid, kFewThreads);
-    }
-  if (tid == 0) A.join[g].np = 0;
-  if (units == 0 || g >= ctas) return;
-  const int64_t u0 = share_begin(units, ctas, g), u1 = share_begin(units, ctas, g + 1);
+  const int g = blockIdx.x;
+  int64_t units = 0, u = 0, u1 = 1;
+  int ctas = 1;
+  if (!A.whole) {
+    scan_requests<kFewThreads>(a, start, warp_sum_s, first);
+    units = start[a.n_requests];
+    ctas = ctas_used(units, a.n_requests * a.n_kv_heads, A.n_ctas);
+    for (int b = g; b < a.n_requests; b += gridDim.x)
+      if (start[b + 1] == start[b]) {  // rows without a slot
+        const Request rq = request_of(a, b);
+        empty_rows<T, D>(A, rq, rq.rows, tid, kFewThreads);
+      }
+    if (tid == 0) A.join[g].np = 0;
+    if (units == 0 || g >= ctas) return;
+    u = share_begin(units, ctas, g);
+    u1 = share_begin(units, ctas, g + 1);
+  }
   uint8_t *mine = sm_raw + warp * Few<D>::kWarpBytes;
-  for (int64_t u = u0; u < u1;) {
-    const int b = request_at(start, a.n_requests, u);
-    const Request rq = b < kFewThreads ? first[b] : request_of(a, b);
-    const Tiles tl = tiles_of(a, rq);
-    const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
-    const int h = in / static_cast<uint32_t>(tl.count), t0 = in - h * tl.count;
-    const int t1 = static_cast<int>(u1 - u < tl.count - t0 ? t0 + (u1 - u) : tl.count);
+  while (u < u1) {
+    int b, h, t0, t1;
+    Request rq;
+    Tiles tl;
+    if (A.whole) {  // one head, all of it
+      b = g / a.n_kv_heads;
+      h = g - b * a.n_kv_heads;
+      rq = request_of(a, b);
+      tl = tiles_of(a, rq);
+      t0 = 0;
+      t1 = tl.count;
+      u1 = t1;
+      if (t1 == 0) {
+        if (h == 0) empty_rows<T, D>(A, rq, rq.rows, tid, kFewThreads);
+        return;
+      }
+    } else {
+      b = request_at(start, a.n_requests, u);
+      rq = b < kFewThreads ? first[b] : request_of(a, b);
+      tl = tiles_of(a, rq);
+      const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
+      h = in / static_cast<uint32_t>(tl.count);
+      t0 = in - h * tl.count;
+      t1 = static_cast<int>(u1 - u < tl.count - t0 ? t0 + (u1 - u) : tl.count);
+    }
     const int R = rq.rows * a.group;
     {
       FewWarp<T, D, HALF> w;
@@ -412,27 +437,28 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
 }
 
 // ------------------------------------------------------------------ join
-// Block g: the join that block g of the few-rows kernel left, a head of which blocks g-1, g, ... each
-// worked on a part (one context of 4096 slots and 8 heads: 39 parts of 4 rows each).  All that bounds it
+// Block (g, y): rows 4y .. 4y+3 of the join that block g of the few-rows kernel left, a head of which
+// blocks g-1, g, ... each worked on a part (one context of 4096 slots and 8 heads: 39 parts).  All that bounds it
 // is round trips to L2, so nothing waits for one part at a time: a warp takes the references and sums of
 // a row's parts side by side and leaves their weights in shared memory; then the threads, as many groups
 // of them as fit, each add every kth part.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinHeld = 10;  // parts of a thread in registers
+constexpr int kJoinRows = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_constant__ PagedAttnArgs A) {
   __shared__ unsigned bad_rows;
-  __shared__ float weight[kFewRows][kJoinParts];
-  __shared__ float2 row_ml[kFewRows];
+  __shared__ float weight[kJoinRows][kJoinParts];
+  __shared__ float2 row_ml[kJoinRows];
   __shared__ float4 sums[kJoinThreads];
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
   const PagedJoin j = A.join[g];
-  if (j.np == 0) return;
+  const int r0 = blockIdx.y * kJoinRows, n = min(j.n - r0, kJoinRows);
+  if (j.np == 0 || n <= 0) return;
   const Request rq = {j.len, j.row0, j.rows};
-  const int n = j.n;
-  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * kFewRows; };
+  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * kFewRows + r0; };
   const int pieces = n * (D / 4);  // at most kJoinThreads
   const int groups = kJoinThreads / pieces, k = tid / pieces, c = tid - k * pieces;
   const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
@@ -492,13 +518,18 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
         o.w += v.w;
       }
   }
-  const bool bad = k == 0 && finish4<T>(A, rq, j.h, j.from + r, d, o, row_ml[r].x, row_ml[r].y);
+  const bool bad = k == 0 && finish4<T>(A, rq, j.h, j.from + r0 + r, d, o, row_ml[r].x, row_ml[r].y);
   if (bad) atomicOr(&bad_rows, 1u << r);
-  if (__syncthreads_or(bad)) redo_rows<T, D, kJoinThreads>(A, rq, j.b, j.h, j.from, n, bad_rows);
+  if (__syncthreads_or(bad)) redo_rows<T, D, kJoinThreads>(A, rq, j.b, j.h, j.from + r0, n, bad_rows);
 }
-static_assert(kFewRows * 128 / 4 <= kJoinThreads, "a block's pieces");
+static_assert(kJoinRows * 128 / 4 <= kJoinThreads, "a block's pieces");
 
 // ------------------------------------------------------------------ host
+// Up to this many slots a head is not split but one block's, whose warps take eight units of it at most:
+// that saves summing up the lengths and the joining launch (8 requests x 8 heads of 512 slots:
+// @WHOLE@ us, split @SPLIT@ us).
+constexpr int kWholeSlots = 512;
+
 static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts - 1; }
 
 size_t few_bytes(int head_dim) {
@@ -509,17 +540,21 @@ size_t few_bytes(int head_dim) {
 template <typename T, int D>
 static cudaError_t launch(const PagedAttnArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  auto kernel = a.max_rows * a.group <= 8 ? attention_few<T, D, true> : attention_few<T, D, false>;
+  const int rows = a.max_rows * a.group;
+  auto kernel = rows <= 8 ? attention_few<T, D, true> : attention_few<T, D, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
   if (e != cudaSuccess) return e;
+  if (A.whole) return launch_pdl(kernel, dim3(a.n_requests * a.n_kv_heads), dim3(kFewThreads), Few<D>::kSmem, s, A);
   const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Few<D>::kSmem, s, A);
-  return f == cudaSuccess ? launch_pdl(attention_join<T, D>, dim3(A.n_ctas), dim3(kJoinThreads), 0, s, A) : f;
+  if (f != cudaSuccess) return f;
+  return launch_pdl(attention_join<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
 }
 
 std::string launch_attention_few(PagedAttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = few_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
+  A.whole = visible_slots(A.p) <= kWholeSlots;
   A.join = reinterpret_cast<PagedJoin *>(p);
   p += align256(A.n_ctas * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);

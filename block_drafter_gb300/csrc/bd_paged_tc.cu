@@ -51,7 +51,8 @@ template <int D> struct Tc {
   static constexpr uint32_t kOffRing = 2 * kTile;          // behind the two query tiles
   static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
   static constexpr uint32_t kOffSeg = kOffBar + 320;       // [kSegments] segments of 64 bytes
-  static constexpr size_t kSmem = 1024 + kOffSeg + kSegments * 64 + 128;  // and the share's beginning
+  static constexpr size_t kSmem = 1024 + kOffSeg + kSegments * 64 + 128;  // and the walk
+  static_assert(32 + 8 * kTcThreads / 32 <= 128, "the walk and the warps' totals");
   // TMEM columns of stream s.  With D = 128 the weights take the place of their scores: the products
   // have one shape, so the next scores are written after the weights have been read.
   static constexpr uint32_t kS = 0, kO = 256, kP = D == 128 ? 0 : 384;
@@ -203,47 +204,63 @@ struct Segments {
   }
 };
 
-// One thread works them out, from item i of the list on, which begins at unit `before`.
-__device__ void segment_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, int i, int64_t before, Segment *ring, const Bars &B) {
+// Where a block is in its share: unit u of u .. end, item i of the list, the units before it.
+struct SegmentWalk {
+  int64_t u, end, before;
+  int i;
+};
+// The block's next segment; t0 == t1: none.
+__device__ __forceinline__ void next_segment(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, SegmentWalk &w, Segment &s) {
   const PagedArgs &a = A.p;
-  const int g = blockIdx.x;
-  int64_t u = share_begin(units, ctas, g);
-  const int64_t end = share_begin(units, ctas, g + 1);
-  for (uint32_t k = 0;; ++k) {
-    Segment s = {};
-    while (u < end && s.t0 == s.t1) {
-      s.b = i / nqt;
-      const int qt = i - s.b * nqt;
-      const Request rq = request_of(a, s.b);
-      const ItemRows ir = item_rows(a, rq, qt);
-      const ItemTiles tl = item_tiles(a, ir);
+  s.t0 = s.t1 = 0;
+  while (w.u < w.end && s.t0 == s.t1) {
+    s.b = w.i / nqt;
+    const int qt = w.i - s.b * nqt;
+    const Request rq = request_of(a, s.b);
+    const ItemRows ir = item_rows(a, rq, qt);
+    const ItemTiles tl = item_tiles(a, ir);
+    int from = 0, to = tl.count;
+    if (A.whole) {  // w.before is the KV head
+      s.h = static_cast<int>(w.before);
+      w.u = w.end;
+    } else {
       const int per = item_units(tl);
       const int64_t all = static_cast<int64_t>(per) * a.n_kv_heads;
-      if (u >= before + all) {  // to the next item, past what the request does not fill
-        i = ir.n > 0 ? i + 1 : (s.b + 1) * nqt;
-        before += all;
+      if (w.u >= w.before + all) {  // to the next item, past what the request does not fill
+        w.i = ir.n > 0 ? w.i + 1 : (s.b + 1) * nqt;
+        w.before += all;
         continue;
       }
-      const uint32_t in = static_cast<uint32_t>(u - before);  // below 2^31: checked by the host
+      const uint32_t in = static_cast<uint32_t>(w.u - w.before);  // below 2^31: checked by the host
       s.h = in / static_cast<uint32_t>(per);
-      const int from = in - s.h * per, to = end - u < per - from ? from + static_cast<int>(end - u) : per;
-      s.t0 = min(from, tl.count);  // the units behind the tiles hold nothing
-      s.t1 = min(to, tl.count);
-      s.row0 = rq.row0;
-      s.base = rq.n - rq.rows;
-      s.r0 = ir.r0;
-      s.n = ir.n;
-      s.p_low = ir.p_low;
-      s.p_high = ir.p_high;
-      s.sinks = tl.sinks;
-      s.first = tl.first;
-      s.whole = s.t0 == 0 && s.t1 == tl.count;
-      s.split = ir.n <= 128;
-      s.len = rq.n;
-      if (s.t0 > 0 && s.t0 < s.t1 && share_begin(units, ctas, g - 1) <= u - from)  // the first block to begin inside it
-        A.join[g] = {s.b, s.h, ir.r0, ir.n, share_owner(units, ctas, u - from + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
-      u += to - from;
+      from = in - s.h * per;
+      to = w.end - w.u < per - from ? from + static_cast<int>(w.end - w.u) : per;
+      if (from > 0 && from < tl.count && share_begin(units, ctas, blockIdx.x - 1) <= w.u - from)  // the first block to begin inside it
+        A.join[blockIdx.x] = {s.b, s.h, ir.r0, ir.n, share_owner(units, ctas, w.u - from + tl.count - 1) - static_cast<int>(blockIdx.x) + 2,
+                              rq.row0, rq.n, rq.rows};
+      w.u += to - from;
     }
+    s.t0 = min(from, tl.count);  // the units behind the tiles hold nothing
+    s.t1 = min(to, tl.count);
+    s.row0 = rq.row0;
+    s.base = rq.n - rq.rows;
+    s.r0 = ir.r0;
+    s.n = ir.n;
+    s.p_low = ir.p_low;
+    s.p_high = ir.p_high;
+    s.sinks = tl.sinks;
+    s.first = tl.first;
+    s.whole = s.t0 == 0 && s.t1 == tl.count;
+    s.split = ir.n <= 128;
+    s.len = rq.n;
+  }
+}
+
+// One thread works them out.
+__device__ void segment_role(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, SegmentWalk w, Segment *ring, const Bars &B) {
+  for (uint32_t k = 0;; ++k) {
+    Segment s = {};
+    next_segment(A, nqt, units, ctas, w, s);
     if (k >= kSegments && !wait_or_stop(B, &B.seg_empty[k % kSegments], ((k / kSegments) - 1) & 1)) return;
     ring[k % kSegments] = s;
     mbar_arrive(&B.seg_full[k % kSegments]);
@@ -750,8 +767,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   int *stop = reinterpret_cast<int *>(tmem_slot + 1);
   Segment *segs = reinterpret_cast<Segment *>(sm + C::kOffSeg);
-  PagedShare *share = reinterpret_cast<PagedShare *>(segs + kSegments);
-  int64_t *warp_total = reinterpret_cast<int64_t *>(share + 1);  // [warps]
+  SegmentWalk *walk = reinterpret_cast<SegmentWalk *>(segs + kSegments);
+  int64_t *warp_total = reinterpret_cast<int64_t *>(walk + 1);  // [warps]
   B.stop = stop;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
@@ -786,32 +803,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
-  // where this block's share begins: summed up here, or by attention_plan
+  // the block's work: an item of its own, or a share, whose beginning is summed up here or by
+  // attention_plan
   const int N = A.p.n_requests * nqt;
-  int64_t units;
-  if (tid == 0) A.join[blockIdx.x].np = 0;
-  if (N <= kListEach * kTcThreads) {
-    int64_t x[kListEach], mine = 0;
-#pragma unroll
-    for (int k = 0; k < kListEach; ++k) {
-      const int i = tid * kListEach + k;
-      x[k] = i < N ? static_cast<int64_t>(list_units(A.p, nqt, i)) * A.p.n_kv_heads : 0;
-      mine += x[k];
+  int64_t units = 1;
+  if (A.whole) {
+    if (tid == 0) {
+      const int i = blockIdx.x / A.p.n_kv_heads;
+      *walk = {0, 1, static_cast<int64_t>(blockIdx.x) - static_cast<int64_t>(i) * A.p.n_kv_heads, i};
     }
-    int64_t before = block_sum<kTcThreads>(mine, warp_total, units) - mine;
-    const int64_t u = share_begin(units, many_ctas_used(units, A.n_ctas), blockIdx.x);
-#pragma unroll
-    for (int k = 0; k < kListEach; ++k) {
-      if (u >= before && u < before + x[k]) *share = {before, tid * kListEach + k, 0};
-      before += x[k];
-    }
-    __syncthreads();
   } else {
-    units = A.units[N];
-    if (tid == 0 && blockIdx.x < many_ctas_used(units, A.n_ctas)) *share = A.share[blockIdx.x];
-    __syncthreads();
+    if (tid == 0) A.join[blockIdx.x].np = 0;
+    int64_t u = 0;
+    int ctas = 1;
+    if (N <= kListEach * kTcThreads) {
+      int64_t x[kListEach], mine = 0;
+#pragma unroll
+      for (int k = 0; k < kListEach; ++k) {
+        const int i = tid * kListEach + k;
+        x[k] = i < N ? static_cast<int64_t>(list_units(A.p, nqt, i)) * A.p.n_kv_heads : 0;
+        mine += x[k];
+      }
+      int64_t before = block_sum<kTcThreads>(mine, warp_total, units) - mine;
+      ctas = many_ctas_used(units, A.n_ctas);
+      u = share_begin(units, ctas, blockIdx.x);
+#pragma unroll
+      for (int k = 0; k < kListEach; ++k) {
+        if (u >= before && u < before + x[k]) {
+          *walk = {u, share_begin(units, ctas, blockIdx.x + 1), before, tid * kListEach + k};
+        }
+        before += x[k];
+      }
+    } else {
+      units = A.units[N];
+      ctas = many_ctas_used(units, A.n_ctas);
+      if (tid == 0 && blockIdx.x < ctas) {
+        const PagedShare sh = A.share[blockIdx.x];
+        *walk = {share_begin(units, ctas, blockIdx.x), share_begin(units, ctas, blockIdx.x + 1), sh.before, sh.item};
+      }
+    }
   }
-  const int ctas = many_ctas_used(units, A.n_ctas);
+  __syncthreads();
+  const int ctas = A.whole ? static_cast<int>(gridDim.x) : many_ctas_used(units, A.n_ctas);
   if (units > 0 && blockIdx.x < ctas) {
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -826,7 +859,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
         commit(elect_lead(), drain);  // nothing of this block is in flight when its TMEM is freed
         mbar_wait(drain, 0);
       } else if (lane == 0) {
-        segment_role(A, nqt, units, ctas, share->item, share->before, segs, B);
+        segment_role(A, nqt, units, ctas, *walk, segs, B);
       }
     }
     __syncwarp();
@@ -916,6 +949,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __g
 
 // ------------------------------------------------------------------ host
 int many_blocks() { return num_sms() < kJoinParts - 1 ? num_sms() : kJoinParts - 1; }
+// A call of no more items than blocks, each of few tiles, is not shared out: every item and KV head is one
+// block's, which needs neither the list nor the joining launch (1 request, 8 heads, 512 rows: @MWHOLE@ us,
+// shared @MSPLIT@ us).
+constexpr int kWholeTiles = 8;
+
 int64_t item_count(int max_rows, int group) {
   return (static_cast<int64_t>(max_rows) * group + kItemRows - 1) / kItemRows;
 }
@@ -930,14 +968,15 @@ template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt,
     checked.store(true, std::memory_order_relaxed);
   }
   cudaError_t e = cudaFuncSetAttribute(attention_many<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
-  if (e == cudaSuccess && A.p.n_requests * nqt > kListEach * kTcThreads)
+  if (e == cudaSuccess && !A.whole && A.p.n_requests * nqt > kListEach * kTcThreads)
     e = launch_pdl(attention_plan, dim3(1), dim3(kPlanThreads), 0, s, A, nqt);
   PoolMaps M = {};
   int box = box_rows(A.p.page_size);
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   if (box && !(pool_map(&M.k, A.p, A.p.k, bf16, box) && pool_map(&M.v, A.p, A.p.v, bf16, box))) box = 0;
-  if (e == cudaSuccess) e = launch_pdl(attention_many<T, D>, dim3(A.n_ctas), dim3(kTcThreads), Tc<D>::kSmem, s, A, M, box, nqt);
-  if (e == cudaSuccess) {
+  const int blocks = A.whole ? A.p.n_requests * nqt * A.p.n_kv_heads : A.n_ctas;
+  if (e == cudaSuccess) e = launch_pdl(attention_many<T, D>, dim3(blocks), dim3(kTcThreads), Tc<D>::kSmem, s, A, M, box, nqt);
+  if (e == cudaSuccess && !A.whole) {
     const int rows = A.p.max_rows * A.p.group, most = rows < kItemRows ? rows : kItemRows;
     e = launch_pdl(attention_join_many<T, D>, dim3(A.n_ctas, (most + kJoinWarps - 1) / kJoinWarps), dim3(32 * kJoinWarps), 0, s, A);
   }
@@ -961,6 +1000,8 @@ std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, c
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = many_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kItemRows;
+  const int64_t seen = a.window > 0 ? a.window + kItemRows / a.group + 1ll + a.n_sink : a.max_len;  // by one item
+  A.whole = nqt * a.n_requests * a.n_kv_heads <= A.n_ctas && (seen < a.max_len ? seen : a.max_len) <= kWholeTiles * kTileSlots;
   A.units = reinterpret_cast<int64_t *>(p);
   p += align256((static_cast<size_t>(a.n_requests) * nqt + 1) * 8);
   A.share = reinterpret_cast<PagedShare *>(p);
