@@ -381,10 +381,9 @@ template <typename T, int D> static cudaError_t launch_weights_t(const PagedWeig
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_weights_kernel<T, D>, dim3(2 * num_sms()), dim3(32 * kWeightWarps), Weights<D>::kSmem, s, A, split);
 }
-constexpr int kWeightsMany = 64;  // rows of a KV head from which the tensor cores' 128-wide tiles pay
 static std::string launch_weights(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  if (a.max_rows * a.group >= kWeightsMany && weights_many_takes(a)) return launch_weights_many(A, dtype, s);
+  if (weights_many_takes(a)) return launch_weights_many(A, dtype, s);
   // Warps work on tiles of their own while there are enough; else they split the KV heads of one.
   int split = 1;
   const int64_t tiles = static_cast<int64_t>(a.n_requests) * ((a.max_len + 15) / 16), want = 4ll * kWeightWarps * num_sms();
