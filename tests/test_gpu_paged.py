@@ -526,3 +526,15 @@ def test_a_long_list_of_items_is_planned_apart():
     out, lse = c.attend()
     sync()
     c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 300])
+def test_rows_that_see_garbage_show_it_and_others_do_not(rows):
+    """NaN among the visible values of every row (no hidden garbage): the affected column alone."""
+    c = PagedCase((700,), (rows,), hkv=2, group=2).build()
+    c.vd[c.table[0, 2].item(), 1, 9, 5] = float("nan")        # slot 41, KV head 1
+    out, lse = c.attend()
+    sync()
+    bad = torch.zeros(c.n_rows, 4, c.d, dtype=torch.bool, device="cuda")
+    bad[:, 2:, 5] = True
+    assert torch.equal(torch.isnan(out), bad) and torch.isfinite(lse).all()
