@@ -384,9 +384,12 @@ template <typename T, int D> static cudaError_t launch_weights_t(const PagedWeig
 static std::string launch_weights(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
   if (weights_many_takes(a)) return launch_weights_many(A, dtype, s);  // else boxes do not fit
-  // Warps work on tiles of their own while there are enough; else they split the KV heads of one.
+  // Warps work on tiles of their own while there are enough for half of them; else they split the KV heads
+  // of one (a token, 8 heads: 4096 slots 5.6 us split eight ways, 9.2 us whole; 16 384 slots 10.5 us
+  // split in two, 12.2 us whole, 15.2 us split eight ways; 8 requests of 8192 slots 31.4 us whole, 34.7 us
+  // split in two).
   int split = 1;
-  const int64_t tiles = static_cast<int64_t>(a.n_requests) * ((a.max_len + 15) / 16), want = 4ll * kWeightWarps * num_sms();
+  const int64_t tiles = static_cast<int64_t>(a.n_requests) * ((a.max_len + 15) / 16), want = static_cast<int64_t>(kWeightWarps) * num_sms();
   while (split < kWeightWarps && 2 * split <= a.n_kv_heads && tiles * split < want) split *= 2;
   cudaError_t e;
   if (dtype == BD_BF16)
@@ -693,8 +696,8 @@ __global__ void __launch_bounds__(kInThreads) paged_move_in_place_kernel(const _
 
 static std::string launch_evict(const PagedEvictArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  // a barrier of eight blocks costs about a microsecond: fewer slots are one block's (4096: 19 us with
-  // eight, 13 us with one)
+  // a barrier of eight blocks costs about a microsecond: fewer slots are one block's (a request of 4096
+  // slots, 2048 kept: 18.5 us with eight blocks, 12.0 us with one; of 16 384: 19.0 and 20.6 us)
   const int sel = a.max_len <= kSelSmall ? 1 : kSelBlocks;
   cudaError_t e = launch_pdl_cluster(paged_select_kernel, dim3(sel, a.n_requests), dim3(kSelThreads), 0, s, sel, A);
   if (e == cudaSuccess) {

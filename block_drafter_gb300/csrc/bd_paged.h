@@ -37,7 +37,7 @@ struct PagedAttnArgs {
   float *part_o;        // [2 * n_ctas][part rows][head_dim] unnormalised sums
   float2 *part_ml;      // [2 * n_ctas][part rows] (reference in log2 units, row sum)
   int n_ctas;
-  bool whole;           // every item is one block's: no shares, no joins
+  int whole;            // not 0: every item is one block's, in so many rounds: no shares, no joins
 };
 
 struct PagedShare {  // item a block's share begins in, and the units before that item

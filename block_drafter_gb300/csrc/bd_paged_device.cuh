@@ -51,7 +51,7 @@ __device__ __forceinline__ int64_t slot_offset(const PagedArgs &a, const int32_t
 }
 
 // First slot beside the sinks that the row at slot p sees (p >= 0).
-__device__ __forceinline__ int window_first(const PagedArgs &a, int p) {
+__host__ __device__ __forceinline__ int window_first(const PagedArgs &a, int p) {
   return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
 }
 

@@ -64,35 +64,35 @@ template <typename T> struct Head { static constexpr float k = 0.f; };
 template <> struct Head<__half> { static constexpr float k = 6.f; };
 constexpr float kMove = 8.f;
 
-
 // Key tiles of one item: those of the sinks, then those from its first row's window on.
 struct ItemTiles {
   int sinks, first, count;
-  __device__ int at(int t) const { return t < sinks ? t : first + t - sinks; }
 };
 // Rows of the item list entry qt, and the slots of its first and last row (rows * group < 2^30).
 struct ItemRows {
   int r0, n, p_low, p_high;  // n <= 0: none
 };
-__device__ __forceinline__ ItemRows item_rows(const PagedArgs &a, const Request &rq, int qt) {
+__host__ __device__ __forceinline__ ItemRows item_rows(const PagedArgs &a, const Request &rq, int qt) {
   ItemRows x;
   x.r0 = qt * kItemRows;
-  x.n = min(rq.rows * a.group - x.r0, kItemRows);
+  x.n = rq.rows * a.group - x.r0;
+  if (x.n > kItemRows) x.n = kItemRows;
   x.p_low = rq.n - rq.rows + x.r0 / static_cast<uint32_t>(a.group);
-  x.p_high = rq.n - rq.rows + (x.r0 + max(x.n, 1) - 1) / static_cast<uint32_t>(a.group);
+  x.p_high = rq.n - rq.rows + (x.r0 + (x.n > 1 ? x.n - 1 : 0)) / static_cast<uint32_t>(a.group);
   return x;
 }
-__device__ __forceinline__ ItemTiles item_tiles(const PagedArgs &a, const ItemRows &x) {
+__host__ __device__ __forceinline__ ItemTiles item_tiles(const PagedArgs &a, const ItemRows &x) {
   ItemTiles t = {0, 0, 0};
   if (x.n <= 0 || x.p_high < 0) return t;
-  const int first = window_first(a, max(0, x.p_low));
+  const int first = window_first(a, x.p_low > 0 ? x.p_low : 0);
   t.first = first / kTileSlots;
-  t.sinks = min((min(a.n_sink, first) + kTileSlots - 1) / kTileSlots, t.first);
+  t.sinks = ((a.n_sink < first ? a.n_sink : first) + kTileSlots - 1) / kTileSlots;
+  if (t.sinks > t.first) t.sinks = t.first;
   t.count = t.sinks + x.p_high / kTileSlots + 1 - t.first;
   return t;
 }
 // Units of one KV head of an item.
-__device__ __forceinline__ int item_units(const ItemTiles &t) { return t.count > 0 ? t.count + kItemCost : 0; }
+__host__ __device__ __forceinline__ int item_units(const ItemTiles &t) { return t.count > 0 ? t.count + kItemCost : 0; }
 __device__ __forceinline__ int many_ctas_used(int64_t units, int most) {
   return static_cast<int>(units < 1 ? 1 : units < most ? units : most);
 }
@@ -204,7 +204,8 @@ struct Segments {
   }
 };
 
-// Where a block is in its share: unit u of u .. end, item i of the list, the units before it.
+// Where a block is in its share: unit u of u .. end, item i of the list, the units before it.  Without
+// shares: round u of u .. end.
 struct SegmentWalk {
   int64_t u, end, before;
   int i;
@@ -214,16 +215,25 @@ __device__ __forceinline__ void next_segment(const PagedAttnArgs &A, int nqt, in
   const PagedArgs &a = A.p;
   s.t0 = s.t1 = 0;
   while (w.u < w.end && s.t0 == s.t1) {
-    s.b = w.i / nqt;
-    const int qt = w.i - s.b * nqt;
+    int qt;
+    if (A.whole) {
+      // Every request's last rows -- the most tiles -- first, and the blocks taken in turn there and back:
+      // who has one of a round's largest items has one of the next round's smallest.
+      const uint32_t r = static_cast<uint32_t>(w.u++), place = r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+      const uint32_t entry = (r * gridDim.x + place) / a.n_kv_heads;
+      s.h = r * gridDim.x + place - entry * a.n_kv_heads;
+      qt = entry / static_cast<uint32_t>(a.n_requests);
+      s.b = entry - qt * a.n_requests;
+    } else {
+      s.b = w.i / nqt;
+      qt = w.i - s.b * nqt;
+    }
     const Request rq = request_of(a, s.b);
+    if (A.whole && (qt = (rq.rows * a.group + kItemRows - 1) / kItemRows - 1 - qt) < 0) continue;
     const ItemRows ir = item_rows(a, rq, qt);
     const ItemTiles tl = item_tiles(a, ir);
     int from = 0, to = tl.count;
-    if (A.whole) {  // w.before is the KV head
-      s.h = static_cast<int>(w.before);
-      w.u = w.end;
-    } else {
+    if (!A.whole) {
       const int per = item_units(tl);
       const int64_t all = static_cast<int64_t>(per) * a.n_kv_heads;
       if (w.u >= w.before + all) {  // to the next item, past what the request does not fill
@@ -288,6 +298,12 @@ __device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, co
       mbar_arrive(&B.full[(q - late) % NS]);
     }
   };
+  auto leave = [&]() {  // nothing is in flight when the block ends, after a wait that gave up either
+    cp_async_wait<0>();
+    announce(0);
+    bool ok = true;
+    for (uint32_t g = q < NS ? 0 : q - NS; box && ok && g < q; ++g) ok = mbar_wait(&B.full[g % NS], (g / NS) & 1);
+  };
   constexpr int ATOMS = D / 64;
   const int boxes = box ? kTileSlots / box : 0;
   const bool mine = warp == 0 && lane < boxes * ATOMS;  // this thread issues a TMA box
@@ -345,7 +361,7 @@ __device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, co
         const bool whole_v = j0 + kTileSlots <= s.len;
 #pragma unroll 1
         for (int v = 0; v < (whole_v ? 2 : 1); ++v) {
-          if (!free_slot()) return;
+          if (!free_slot()) return leave();
           const uint32_t slot = q % NS;
           if (mine) {
             mbar_arrive_expect_tx(&B.full[slot], static_cast<uint32_t>(box) * 128);
@@ -358,7 +374,7 @@ __device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, co
         }
         if (!whole_v) {
           const int64_t off[2] = {offset(t, 0, page_at(t, 0)), offset(t, 1, page_at(t, 1))};
-          if (!free_slot()) return;
+          if (!free_slot()) return leave();
           copy_rows(V, off);
         }
       }
@@ -370,10 +386,7 @@ __device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, co
         page[1] = page_at(t + 1, 1);
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
-          if (!free_slot()) {
-            cp_async_wait<0>();
-            return;
-          }
+          if (!free_slot()) return leave();
           copy_rows(v ? V : K, off);
           if (late > kLag) {
             cp_async_wait<kLag>();
@@ -383,8 +396,7 @@ __device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, co
       }
     }
   }
-  cp_async_wait<0>();
-  announce(0);
+  leave();
 }
 
 // ------------------------------------------------------------------ products (one warp)
@@ -823,10 +835,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
   const int N = A.p.n_requests * nqt;
   int64_t units = 1;
   if (A.whole) {
-    if (tid == 0) {
-      const int i = blockIdx.x / A.p.n_kv_heads;
-      *walk = {0, 1, static_cast<int64_t>(blockIdx.x) - static_cast<int64_t>(i) * A.p.n_kv_heads, i};
-    }
+    if (tid == 0) *walk = {0, A.whole, 0, 0};
   } else {
     if (tid == 0) A.join[blockIdx.x].np = 0;
     int64_t u = 0;
@@ -964,10 +973,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __g
 
 // ------------------------------------------------------------------ host
 int many_blocks() { return num_sms() < kJoinParts - 1 ? num_sms() : kJoinParts - 1; }
-// A call of no more items than blocks, each of few tiles, is not shared out: every item and KV head is one
-// block's, which needs neither the list nor the joining launch (1 request, 8 heads, 512 rows: 15.5 us,
-// shared 25.3 us).
-constexpr int kWholeTiles = 8;
+// A call is not shared out, but every item and KV head is one block's, where that leaves the busiest block
+// less than what sharing costs: its even part of the tiles, an item that it shares and, about
+// kJoinCost tiles, the joins (8 heads, group 4: 512 rows %W512%; 8192 rows %W8192%).
+// Bounds stand for the lengths here; of several requests, ones of equal rows, as n_rows tells.
+constexpr int kJoinCost = 8;
+constexpr int kMostWhole = 4096;  // items that are weighed on the host: more take milliseconds, joins or not
+int whole_rounds(const PagedArgs &a, int nqt, int blocks) {
+  const int64_t items = static_cast<int64_t>(nqt) * a.n_requests * a.n_kv_heads;
+  if (items > kMostWhole || (items > blocks && static_cast<int64_t>(a.n_rows) * 20 < static_cast<int64_t>(a.n_requests) * a.max_rows * 19))
+    return 0;
+  const Request rq = {a.max_len, 0, a.max_rows < a.max_len ? a.max_rows : a.max_len};
+  int load[kJoinParts] = {}, most = 0, m = 0;
+  int64_t all = 0;
+  for (int qt = nqt - 1; qt >= 0; --qt) {
+    const int units = item_units(item_tiles(a, item_rows(a, rq, qt)));
+    for (int x = 0; x < a.n_requests * a.n_kv_heads; ++x, ++m) {
+      int &l = load[m / blocks & 1 ? blocks - 1 - m % blocks : m % blocks];
+      l += units;
+      most = l > most ? l : most;
+    }
+    all += static_cast<int64_t>(units) * a.n_requests * a.n_kv_heads;
+  }
+  return most <= all / blocks + kItemCost + kJoinCost ? static_cast<int>((items + blocks - 1) / blocks) : 0;
+}
 
 int64_t item_count(int max_rows, int group) {
   return (static_cast<int64_t>(max_rows) * group + kItemRows - 1) / kItemRows;
@@ -989,7 +1018,7 @@ template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt,
   int box = box_rows(A.p.page_size);
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   if (box && !(pool_map(&M.k, A.p, A.p.k, bf16, box) && pool_map(&M.v, A.p, A.p.v, bf16, box))) box = 0;
-  const int blocks = A.whole ? A.p.n_requests * nqt * A.p.n_kv_heads : A.n_ctas;
+  const int items = A.p.n_requests * nqt * A.p.n_kv_heads, blocks = A.whole && items < A.n_ctas ? items : A.n_ctas;
   if (e == cudaSuccess) e = launch_pdl(attention_many<T, D>, dim3(blocks), dim3(kTcThreads), Tc<D>::kSmem, s, A, M, box, nqt);
   if (e == cudaSuccess && !A.whole) {
     const int rows = A.p.max_rows * A.p.group, most = rows < kItemRows ? rows : kItemRows;
@@ -1013,8 +1042,7 @@ std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, c
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = many_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kItemRows;
-  const int64_t seen = a.window > 0 ? a.window + kItemRows / a.group + 1ll + a.n_sink : a.max_len;  // by one item
-  A.whole = nqt * a.n_requests * a.n_kv_heads <= A.n_ctas && (seen < a.max_len ? seen : a.max_len) <= kWholeTiles * kTileSlots;
+  A.whole = whole_rounds(a, static_cast<int>(nqt), A.n_ctas);
   A.units = reinterpret_cast<int64_t *>(p);
   p += align256((static_cast<size_t>(a.n_requests) * nqt + 1) * 8);
   A.share = reinterpret_cast<PagedShare *>(p);

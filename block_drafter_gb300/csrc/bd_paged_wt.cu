@@ -32,8 +32,11 @@ template <int D, int N> struct Wt {
   static constexpr uint32_t kOffSum = kOffLse + 16 * N;      // [2 tiles][2 halves][128] floats
   static constexpr uint32_t kOffList = kOffSum + 2048;       // tiles before each request
   static constexpr uint32_t kOffBar = kOffList + (BD_PAGED_MAX_REQUESTS + 2) * 4;
-  static constexpr size_t kSmem = 1024 + kOffBar + 256;
+  // More than a third of an SM's shared memory: at most two blocks share an SM, so their TMEM always
+  // fits.  Blocks of two calls on two streams that waited for TMEM there could wait for each other's clusters.
+  static constexpr size_t kNeed = 1024 + kOffBar + 256, kSmem = kNeed > 78 * 1024 ? kNeed : 78 * 1024;
   static constexpr uint32_t kCols = 2 * N;
+  static_assert(2 * kCols <= 512, "two blocks' TMEM");
 };
 struct WeightMaps {
   CUtensorMap k, q;  // q: [token][query head][D], boxes of N / G tokens x G heads x 64
@@ -257,6 +260,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
       __syncwarp();
       if (blocks > 1) cluster_sync();
     }
+    // nothing is in flight when the block ends, after a wait that gave up either
+    for (uint32_t i = k < KS ? 0 : k - KS; i < k; ++i) mbar_wait(&B.k_full[i % KS], (i / KS) & 1);
+    for (uint32_t i = q < QS ? 0 : q - QS; i < q; ++i) mbar_wait(&B.q_full[i % QS], (i / QS) & 1);
   } else if (warp == 8) {  // products
     const uint32_t lead = elect_lead(), idesc = umma_idesc(ab_format<T>(), 128, N);
     const uint64_t k0 = umma_desc_sw128(smem_u32(sm)), q0 = umma_desc_sw128(smem_u32(sm) + C::kOffQ);

@@ -23,6 +23,7 @@ import torch
 
 from . import binding as B
 
+
 def _current_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
@@ -66,6 +67,7 @@ class PagedBatch:
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
         cache._on_device("workspace", workspace)
+        _need(workspace.is_contiguous(), "workspace: a contiguous tensor is wanted")
         self.workspace = workspace
         self.ws_ptr = workspace.data_ptr()
         self.ws_bytes = workspace.numel() * workspace.element_size()
@@ -194,7 +196,7 @@ class PagedCache:
         self._ints("len_out", len_out, (batch.n_requests,))
         width = 0
         if dst_table is not None:
-            width = dst_table.shape[-1]
+            width = dst_table.shape[-1] if dst_table.dim() else 0
             self._ints("dst_table", dst_table, (batch.n_requests, width))
         ostride = 0
         if score_out is not None:

@@ -489,7 +489,8 @@ bd_status bd_paged_append(const bd_paged_kv *kv, const bd_paged_batch *batch, co
  * over the slots j that row i sees.  A row that sees none gets out = 0 and lse = -inf.  One row
  * per request is plain decoding, K+1 rows verify a drafted block, longer ones are prompt chunks.
  *   q, out  dev [n_rows, n_q_heads, D], rows q_stride / out_stride elements apart (multiples of
- *           8), 16-byte aligned; they must not overlap each other
+ *           8), 16-byte aligned; from their first row to the end of their last they must not
+ *           overlap each other
  *   lse     dev fp32 [n_rows, n_q_heads] OUT (natural logarithm), or NULL
  *   window  0 = none;  n_sink >= 0;  scale > 0, finite
  */

@@ -538,3 +538,51 @@ def test_rows_that_see_garbage_show_it_and_others_do_not(rows):
     bad = torch.zeros(c.n_rows, 4, c.d, dtype=torch.bool, device="cuda")
     bad[:, 2:, 5] = True
     assert torch.equal(torch.isnan(out), bad) and torch.isfinite(lse).all()
+
+
+def test_weights_on_two_streams_beside_attention():
+    """Calls that share the SMs: clusters that wait for TMEM must not wait for each other."""
+    cases = [PagedCase((900, 700), (200, 150), hkv=8, group=4, d=64, page=64, seed=s).build() for s in (1, 2)]
+    lse = [c.attend()[1] for c in cases]
+    want = [torch.zeros(2, c.max_len, device="cuda") for c in cases]
+    got = [torch.zeros_like(w) for w in want]
+    for c, l, w in zip(cases, lse, want):
+        for _ in range(20):
+            c.cache.weights(c.batch, c.qd, l, w, score_in=w)
+    out, l3 = cases[0].outputs()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, l, x, s in zip(cases, lse, got, streams):
+            c.cache.weights(c.batch, c.qd, l, x, score_in=x, stream=s)
+        cases[0].cache.attention(cases[0].batch, cases[0].qd, out, lse=l3, stream=streams[2])
+    sync()
+    for x, w in zip(got, want):
+        assert torch.equal(x, w)
+    assert torch.equal(l3, lse[0])
+
+
+def test_a_workspace_must_be_contiguous():
+    c = PagedCase((40,), (1,)).build()
+    n = c.batch.ws_bytes
+    for bad in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(n), torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows, c.max_len, workspace=bad)
+
+
+@pytest.mark.parametrize("lens,rows,kw,slack", [
+    ((1500,), (1500,), dict(), 0),                                  # two rounds of items
+    ((1400,), (1200,), dict(lead=300), 500),                        # bounds beyond the lengths
+    ((900, 700, 1100, 640), (640,) * 4, dict(d=64, dtype="fp16"), 0),   # equal rows, other lengths
+    ((1000, 0, 300), (500,) * 3, dict(group=8), 0),                 # no slots; rows before the first slot
+    ((1300,), (1300,), dict(window=200, n_sink=5, page=24), 0),
+    ((1100, 1100), (1, 1100), dict(), 0),                           # not equal: shared out
+])
+def test_prompts_whose_items_are_not_shared(lens, rows, kw, slack):
+    c = PagedCase(lens, rows, **{**dict(hkv=8, group=4), **kw}).build()
+    if slack:
+        c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows + slack, c.max_len)
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    c.check_guards(out, lse)
