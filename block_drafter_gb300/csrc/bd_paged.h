@@ -38,6 +38,7 @@ struct PagedAttnArgs {
   float2 *part_ml;      // [2 * n_ctas][part rows] (reference in log2 units, row sum)
   int n_ctas;
   int whole;            // not 0: every item is one block's, in so many rounds: no shares, no joins
+  int item_rows;        // rows of an item (many rows)
 };
 
 struct PagedShare {  // item a block's share begins in, and the units before that item

@@ -72,11 +72,11 @@ struct ItemTiles {
 struct ItemRows {
   int r0, n, p_low, p_high;  // n <= 0: none
 };
-__host__ __device__ __forceinline__ ItemRows item_rows(const PagedArgs &a, const Request &rq, int qt) {
+__host__ __device__ __forceinline__ ItemRows item_rows(const PagedArgs &a, const Request &rq, int qt, int rows) {
   ItemRows x;
-  x.r0 = qt * kItemRows;
+  x.r0 = qt * rows;
   x.n = rq.rows * a.group - x.r0;
-  if (x.n > kItemRows) x.n = kItemRows;
+  if (x.n > rows) x.n = rows;
   x.p_low = rq.n - rq.rows + x.r0 / static_cast<uint32_t>(a.group);
   x.p_high = rq.n - rq.rows + (x.r0 + (x.n > 1 ? x.n - 1 : 0)) / static_cast<uint32_t>(a.group);
   return x;
@@ -101,7 +101,7 @@ __device__ __forceinline__ int many_ctas_used(int64_t units, int most) {
 // The item list: entry i = b * nqt + qt is rows 256 qt .. of request b, every KV head of it.
 __device__ __forceinline__ int list_units(const PagedArgs &a, int nqt, int i) {
   const int b = i / nqt;
-  return item_units(item_tiles(a, item_rows(a, request_of(a, b), i - b * nqt)));
+  return item_units(item_tiles(a, item_rows(a, request_of(a, b), i - b * nqt, kItemRows)));
 }
 // Inclusive sum over the block (NT threads; two uses need a barrier between them), and its total.
 template <int NT> __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *warp_total, int64_t &total) {
@@ -229,8 +229,8 @@ __device__ __forceinline__ void next_segment(const PagedAttnArgs &A, int nqt, in
       qt = w.i - s.b * nqt;
     }
     const Request rq = request_of(a, s.b);
-    if (A.whole && (qt = (rq.rows * a.group + kItemRows - 1) / kItemRows - 1 - qt) < 0) continue;
-    const ItemRows ir = item_rows(a, rq, qt);
+    if (A.whole && (qt = (rq.rows * a.group + A.item_rows - 1) / A.item_rows - 1 - qt) < 0) continue;
+    const ItemRows ir = item_rows(a, rq, qt, A.item_rows);
     const ItemTiles tl = item_tiles(a, ir);
     int from = 0, to = tl.count;
     if (!A.whole) {
@@ -979,27 +979,50 @@ int many_blocks() { return num_sms() < kJoinParts - 1 ? num_sms() : kJoinParts -
 // Bounds stand for the lengths here; of several requests, ones of equal rows, as n_rows tells.
 constexpr int kJoinCost = 8;
 constexpr int kMostWhole = 4096;  // items that are weighed on the host: more take milliseconds, joins or not
-int whole_rounds(const PagedArgs &a, int nqt, int blocks) {
-  const int64_t items = static_cast<int64_t>(nqt) * a.n_requests * a.n_kv_heads;
-  if (items > kMostWhole || (items > blocks && static_cast<int64_t>(a.n_rows) * 20 < static_cast<int64_t>(a.n_requests) * a.max_rows * 19))
-    return 0;
+int64_t item_count(int max_rows, int group, int rows) {
+  return (static_cast<int64_t>(max_rows) * group + rows - 1) / rows;
+}
+struct WholeLoad {
+  int most, even;  // the busiest block's units; an even part of them
+};
+WholeLoad whole_load(const PagedArgs &a, int rows, int blocks) {
   const Request rq = {a.max_len, 0, a.max_rows < a.max_len ? a.max_rows : a.max_len};
-  int load[kJoinParts] = {}, most = 0, m = 0;
+  const int per = a.n_requests * a.n_kv_heads;
+  int load[kJoinParts] = {}, most = 0, at = 0;
   int64_t all = 0;
-  for (int qt = nqt - 1; qt >= 0; --qt) {
-    const int units = item_units(item_tiles(a, item_rows(a, rq, qt)));
-    for (int x = 0; x < a.n_requests * a.n_kv_heads; ++x, ++m) {
-      int &l = load[m / blocks & 1 ? blocks - 1 - m % blocks : m % blocks];
+  bool back = false;
+  for (int64_t qt = item_count(a.max_rows, a.group, rows) - 1; qt >= 0; --qt) {
+    const ItemTiles t = item_tiles(a, item_rows(a, rq, static_cast<int>(qt), rows));
+    const int units = rows == kItemRows ? item_units(t) : (t.count + 1) / 2 + kItemCost;  // two streams share the tiles
+    for (int x = 0; x < per; ++x) {
+      int &l = load[back ? blocks - 1 - at : at];
       l += units;
       most = l > most ? l : most;
+      if (++at == blocks) at = 0, back = !back;
     }
-    all += static_cast<int64_t>(units) * a.n_requests * a.n_kv_heads;
+    all += static_cast<int64_t>(units) * per;
   }
-  return most <= all / blocks + kItemCost + kJoinCost ? static_cast<int>((items + blocks - 1) / blocks) : 0;
+  return {most, static_cast<int>(all / blocks)};
 }
-
-int64_t item_count(int max_rows, int group) {
-  return (static_cast<int64_t>(max_rows) * group + kItemRows - 1) / kItemRows;
+// Sets A.whole and A.item_rows.
+void plan_whole(PagedAttnArgs &A) {
+  const PagedArgs &a = A.p;
+  const int blocks = A.n_ctas;
+  const int64_t items = item_count(a.max_rows, a.group, kItemRows) * a.n_requests * a.n_kv_heads;
+  A.whole = 0;
+  A.item_rows = kItemRows;
+  if (items > kMostWhole || (items > blocks && static_cast<int64_t>(a.n_rows) * 20 < static_cast<int64_t>(a.n_requests) * a.max_rows * 19))
+    return;
+  const WholeLoad w = whole_load(a, kItemRows, blocks);
+  int best = w.even + kItemCost + kJoinCost;
+  auto take = [&](int most, int rows) {
+    if (most > best) return;
+    best = most;
+    A.item_rows = rows;
+    A.whole = static_cast<int>((item_count(a.max_rows, a.group, rows) * a.n_requests * a.n_kv_heads + blocks - 1) / blocks);
+  };
+  take(w.most, kItemRows);
+  if (items <= blocks) take(whole_load(a, kItemRows / 2, blocks).most, kItemRows / 2);
 }
 
 template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt, cudaStream_t s) {
@@ -1032,19 +1055,19 @@ template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt,
 size_t many_bytes(int n_requests, int max_rows, int group, int head_dim) {
   if (static_cast<int64_t>(max_rows) * group <= kFewRows) return 0;
   const size_t parts = 2 * static_cast<size_t>(many_blocks()) * kItemRows;
-  return align256((static_cast<size_t>(n_requests) * item_count(max_rows, group) + 1) * 8) +
+  return align256((static_cast<size_t>(n_requests) * item_count(max_rows, group, kItemRows) + 1) * 8) +
          align256(many_blocks() * sizeof(PagedShare)) + align256(many_blocks() * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
 }
 
 std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  const int64_t nqt = item_count(a.max_rows, a.group);
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = many_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kItemRows;
-  A.whole = whole_rounds(a, static_cast<int>(nqt), A.n_ctas);
+  plan_whole(A);
+  const int64_t nqt = item_count(a.max_rows, a.group, A.item_rows);
   A.units = reinterpret_cast<int64_t *>(p);
-  p += align256((static_cast<size_t>(a.n_requests) * nqt + 1) * 8);
+  p += align256((static_cast<size_t>(a.n_requests) * item_count(a.max_rows, a.group, kItemRows) + 1) * 8);
   A.share = reinterpret_cast<PagedShare *>(p);
   p += align256(A.n_ctas * sizeof(PagedShare));
   A.join = reinterpret_cast<PagedJoin *>(p);
