@@ -37,7 +37,8 @@ struct PagedAttnArgs {
   float *part_o;        // [2 * n_ctas][part rows][head_dim] unnormalised sums
   float2 *part_ml;      // [2 * n_ctas][part rows] (reference in log2 units, row sum)
   int n_ctas;
-  int whole;            // not 0: every item is one block's, in so many rounds: no shares, no joins
+  int whole;            // not 0: no shares, no joins.  Many rows: every item is one block's, in so many
+                        // rounds; few rows: a head is a cluster's of so many blocks
   int item_rows;        // rows of an item (many rows)
 };
 

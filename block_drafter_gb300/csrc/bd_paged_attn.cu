@@ -55,6 +55,8 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq)
   return t;
 }
 
+constexpr int kMostCluster = 16;
+
 // Blocks that work: a unit for each of their four warps, but as many as there are heads (a block takes
 // its heads one after the other, about 2.5 us each).
 __device__ __forceinline__ int ctas_used(int64_t units, int heads, int most) {
@@ -137,7 +139,7 @@ struct FewWarp {
     // page of slot lane % 16 of tile t (the load alone: several go out side by side), then the
     // slot's offset, -1 for a slot no row sees
     const int f_low = window_first(a, max(0, p_low));
-    auto page_of = [&](int t) { return __ldg(table + min(tl.at(min(t, t1 - 1)) * kUnit + (lane & 15), rq.n - 1) / a.page_size); };
+    auto page_of = [&](int t) { return __ldg(table + min(tl.at(max(min(t, t1 - 1), 0)) * kUnit + (lane & 15), rq.n - 1) / a.page_size); };
     auto offset = [&](int t, int page) -> int64_t {
       const int j = tl.at(t) * kUnit + (lane & 15);
       if (t >= t1 || j >= rq.n || (j >= a.n_sink && j < f_low)) return -1;
@@ -324,6 +326,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
   __shared__ int64_t warp_sum_s[kFewWarps];
   __shared__ Request first[kFewThreads];
   __shared__ float2 ml[kFewWarps][kFewRows];
+  __shared__ __align__(8) float2 block_ml[kFewRows];  // of a cluster's block, its sums in place of its first warp's
   __shared__ unsigned bad_rows;
   const PagedArgs &a = A.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -347,20 +350,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
     u1 = share_begin(units, ctas, g + 1);
   }
   uint8_t *mine = sm_raw + warp * Few<D>::kWarpBytes;
-  while (u < u1) {
+  do {
     int b, h, t0, t1;
     Request rq;
     Tiles tl;
-    if (A.whole) {  // one head, all of it
-      b = g / a.n_kv_heads;
-      h = g - b * a.n_kv_heads;
+    if (A.whole) {  // one head, or a cluster's block's part of one
+      const int item = g / static_cast<uint32_t>(A.whole), rank = g - item * A.whole;
+      b = item / a.n_kv_heads;
+      h = item - b * a.n_kv_heads;
       rq = request_of(a, b);
       tl = tiles_of(a, rq);
-      t0 = 0;
-      t1 = tl.count;
+      t0 = tl.count * rank / A.whole;
+      t1 = tl.count * (rank + 1) / A.whole;
+      u = t0;
       u1 = t1;
-      if (t1 == 0) {
-        if (h == 0) empty_rows<T, D>(A, rq, rq.rows, tid, kFewThreads);
+      if (tl.count == 0) {
+        if (h == 0 && rank == 0) empty_rows<T, D>(A, rq, rq.rows, tid, kFewThreads);
         return;
       }
     } else {
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
     }
     const bool whole = t0 == 0 && t1 == tl.count;
     const int64_t slot = (2 * g + (t0 > 0 ? 0 : 1)) * kFewRows;
-    if (tid == 0 && t0 > 0 && share_begin(units, ctas, g - 1) <= u - t0)  // the first block to begin inside this head
+    if (tid == 0 && !A.whole && t0 > 0 && share_begin(units, ctas, g - 1) <= u - t0)  // the first block to begin inside this head
       A.join[g] = {b, h, 0, R, share_owner(units, ctas, u - t0 + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
     bool bad = false;
     if (tid == 0) bad_rows = 0u;
@@ -421,7 +426,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
           o.w += w * v.w;
         }
       }
-      if (whole) {
+      if (A.whole > 1) {
+        *reinterpret_cast<float4 *>(sm_raw + (r * D + d) * 4) = o;
+        if (d == 0) block_ml[r] = make_float2(M, L);
+      } else if (whole) {
         if (finish4<T>(A, rq, h, r, d, o, M, L)) {
           atomicOr(&bad_rows, 1u << r);
           bad = true;
@@ -431,9 +439,43 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
         if (d == 0) A.part_ml[slot + r] = make_float2(M, L);
       }
     }
+    if (A.whole > 1) {  // the blocks' parts: a warp takes every kth row
+      __syncwarp();
+      cluster_sync();
+      const int rank = g % static_cast<uint32_t>(A.whole), d = lane * 4;
+      for (int r = rank + A.whole * warp; r < R; r += A.whole * kFewWarps) {
+        float4 v[kMostCluster];
+        const uint32_t at = smem_u32(sm_raw) + (r * D + d % D) * 4;
+#pragma unroll
+        for (int i = 0; i < kMostCluster; ++i)
+          if (i < A.whole) v[i] = ld_cluster_f4(cluster_map(at, i));
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (lane < A.whole) {
+          const uint32_t y = cluster_map(smem_u32(block_ml + r), lane);
+          x = make_float2(ld_cluster_f32(y), ld_cluster_f32(y + 4));
+        }
+        const float M = warp_max(x.y == 0.f ? -INFINITY : x.x), w = x.y == 0.f ? 0.f : exp2f(x.x - M), L = warp_sum(w * x.y);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kMostCluster; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          if (wi != 0.f) {
+            o.x += wi * v[i].x;
+            o.y += wi * v[i].y;
+            o.z += wi * v[i].z;
+            o.w += wi * v[i].w;
+          }
+        }
+        const bool off = d < D && finish4<T>(A, rq, h, r, d, o, M, L);
+        if (__any_sync(0xffffffffu, off)) attend_row<T, D>(A, rq, b, r / a.group, h * a.group + r % a.group, lane);
+      }
+      __syncwarp();
+      cluster_sync();  // every block's sums are read
+      return;
+    }
     if (__syncthreads_or(bad)) redo_rows<T, D, kFewThreads>(A, rq, b, h, 0, R, bad_rows);
     u += t1 - t0;
-  }
+  } while (u < u1);
 }
 
 // ------------------------------------------------------------------ join
@@ -525,10 +567,21 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
 static_assert(kJoinRows * 128 / 4 <= kJoinThreads, "a block's pieces");
 
 // ------------------------------------------------------------------ host
-// Up to this many slots a head is not split but one block's, whose warps take eight units of it at most:
-// that saves summing up the lengths and the joining launch (8 requests x 8 heads of 512 slots:
-// 9.3 us, split 13.1 us).
+// A head of few slots is not split but one block's, whose warps take eight units of it at most: that saves
+// summing up the lengths and the joining launch (8 requests x 8 heads of 512 slots: 9.3 us, shared out 13.1 us).
 constexpr int kWholeSlots = 512;
+// Where there are fewer heads than blocks, a head is a cluster's, whose blocks join their parts through distributed
+// shared memory: as many blocks as are left and kBlockSlots slots for each (8 heads of 512 slots: eight
+// blocks 5.8 us, four 6.5 us, one 9.1 us; of 128 slots: one 4.9 us, two 5.8 us).
+// Clusters of more than kEasyCluster blocks take most of a GPC, eight of them at a time (2 requests of 4096
+// slots, 16 heads: eight blocks each 12.7 us, sixteen 17.6 us).
+constexpr int kBlockSlots = 64, kEasyCluster = 8, kWideClusters = 8;
+// Up to this many slots a block (one request, 8 heads, 16 blocks each: 4096 slots 9.0 us, shared out 12.2 us; 16 384
+// slots 20.7 and 22.5 us; 32 768 slots 34.2 and 31.9 us).  max_len only bounds the lengths, and a cluster is as
+// slow as its longest head (16 ragged requests, a block up to 16 384 slots: 236 and 184 us); a window
+// leaves heads alike, so there it may be more (8 requests, 8 heads: a window of 4096 27.1 and 33.9 us, of 8192
+// 44.1 and 52.0 us).
+constexpr int kClusterSlots = 1088, kClusterWindow = 2176;
 
 static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts - 1; }
 
@@ -544,7 +597,12 @@ static cudaError_t launch(const PagedAttnArgs &A, cudaStream_t s) {
   auto kernel = rows <= 8 ? attention_few<T, D, true> : attention_few<T, D, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
   if (e != cudaSuccess) return e;
-  if (A.whole) return launch_pdl(kernel, dim3(a.n_requests * a.n_kv_heads), dim3(kFewThreads), Few<D>::kSmem, s, A);
+  if (A.whole == 1) return launch_pdl(kernel, dim3(a.n_requests * a.n_kv_heads), dim3(kFewThreads), Few<D>::kSmem, s, A);
+  if (A.whole > 1) {
+    const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (c != cudaSuccess) return c;
+    return launch_pdl_cluster(kernel, dim3(a.n_requests * a.n_kv_heads * A.whole), dim3(kFewThreads), Few<D>::kSmem, s, A.whole, A);
+  }
   const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Few<D>::kSmem, s, A);
   if (f != cudaSuccess) return f;
   return launch_pdl(attention_join<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
@@ -554,7 +612,13 @@ std::string launch_attention_few(PagedAttnArgs A, void *workspace, int dtype, cu
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = few_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
-  A.whole = visible_slots(A.p) <= kWholeSlots;
+  const int64_t seen = visible_slots(A.p), heads = static_cast<int64_t>(A.p.n_requests) * A.p.n_kv_heads;
+  int blocks = 1;
+  while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && 2 * blocks * heads <= A.n_ctas &&
+         (2 * blocks <= kEasyCluster || heads <= kWideClusters))
+    blocks *= 2;
+  const int64_t most = blocks == 1 ? kWholeSlots : blocks * (seen < A.p.max_len ? kClusterWindow : kClusterSlots);
+  A.whole = seen <= most ? blocks : 0;
   A.join = reinterpret_cast<PagedJoin *>(p);
   p += align256(A.n_ctas * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);

@@ -586,3 +586,42 @@ def test_prompts_whose_items_are_not_shared(lens, rows, kw, slack):
     sync()
     c.check_attention(out, lse)
     c.check_guards(out, lse)
+
+
+@pytest.mark.parametrize("n,rows,group,d,dtype", [(40, 1, 1, 64, "bf16"), (44, 2, 2, 128, "fp16"), (21, 5, 3, 64, "fp16")])
+def test_few_rows_of_many_heads_share_the_blocks(n, rows, group, d, dtype):
+    lens = tuple((i * 389) % 900 + (i % 3) for i in range(n))
+    c = PagedCase(lens, tuple((i % rows) + 1 for i in range(n)), hkv=8, group=group, d=d, dtype=dtype).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    c.check_guards(out, lse)
+
+
+@pytest.mark.parametrize("lens,rows,kw", [
+    ((4100,), (1,), dict(hkv=8)),                                        # sixteen blocks a head
+    ((2300, 3, 0, 17), (2, 4, 1, 4), dict(hkv=4)),                       # fewer units than blocks, no slot
+    ((1900, 1200), (5, 4), dict(hkv=5, group=3, d=64, dtype="fp16")),    # up to 15 rows, eight blocks a head
+    ((9000, 700, 5000), (1, 1, 1), dict(hkv=8, window=1500, n_sink=3, page=24)),
+])
+def test_few_rows_of_few_heads_are_a_clusters(lens, rows, kw):
+    c = PagedCase(lens, rows, **kw).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    again, lse2 = c.attend()
+    sync()
+    assert torch.equal(again[c.starts[0]:c.starts[-1]], out[c.starts[0]:c.starts[-1]]) and torch.equal(lse2, lse)
+
+
+def test_hidden_garbage_of_a_clusters_head():
+    c = PagedCase((3000, 2000), (4, 4), hkv=2, group=2, window=700).build()
+    want, wl = c.attend()
+    for b, n in enumerate(c.lens):      # slots that the later rows see no more, and those that the first do not yet
+        for j in list(range(n - 704, n - 700)) + list(range(n - 3, n)):
+            c.vd[c.table[b, j // c.page].item(), :, j % c.page] = float("inf")
+    out, lse = c.attend()
+    sync()
+    assert torch.equal(lse, wl)
+    bad = torch.isfinite(out).logical_not().flatten(1).any(1)
+    assert bad.tolist() == [True] * 8   # each row sees one of them or more
