@@ -37,8 +37,9 @@ struct PagedAttnArgs {
   float *part_o;        // [2 * n_ctas][part rows][head_dim] unnormalised sums
   float2 *part_ml;      // [2 * n_ctas][part rows] (reference in log2 units, row sum)
   int n_ctas;
-  int whole;            // not 0: no shares, no joins.  Many rows: every item is one block's, in so many
-                        // rounds; few rows: a head is a cluster's of so many blocks
+  int whole;            // not 0: no shares, no joins, but every item (few rows: every KV head) is a cluster's,
+                        // in so many rounds
+  int cluster;          // blocks of it: 1 .. kMostCluster
   int item_rows;        // rows of an item (many rows)
 };
 
@@ -51,6 +52,8 @@ struct PagedShare {  // item a block's share begins in, and the units before tha
 struct PagedJoin {
   int b, h, from, n, np, row0, len, rows;
 };
+
+constexpr int kMostCluster = 16;
 
 // Query rows (of one KV head) a block of the few-rows attention takes.
 constexpr int kFewRows = 16;
@@ -84,6 +87,36 @@ inline int64_t visible_slots(const PagedArgs &a) {
   const int64_t seen = a.window > 0 ? static_cast<int64_t>(a.window) + a.max_rows + a.n_sink : a.max_len;
   return seen < a.max_len ? seen : a.max_len;
 }
+// Clusters of `size` blocks of a kernel that the device holds at once.
+template <typename... KArgs> int clusters_at_once(void (*kernel)(KArgs...), int threads, size_t smem, int size) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(size);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess &&
+                  cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                  cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess;
+  return ok ? n : 0;
+}
+// The same of 2, 4, 8 and 16 blocks, asked once.
+template <typename... KArgs> struct ClustersAtOnce {
+  int n[5];
+  ClustersAtOnce(void (*kernel)(KArgs...), int threads, size_t smem) {
+    for (int x = 0; x < 5; ++x) n[x] = x ? clusters_at_once(kernel, threads, smem, 1 << x) : 1 << 30;
+  }
+  int of(int size) const {
+    int x = 0;
+    while (1 << x < size) ++x;
+    return n[x];
+  }
+};
 inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 size_t few_bytes(int head_dim);
 size_t many_bytes(int n_requests, int max_rows, int group, int head_dim);

@@ -55,8 +55,6 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq)
   return t;
 }
 
-constexpr int kMostCluster = 16;
-
 // Blocks that work: a unit for each of their four warps, but as many as there are heads (a block takes
 // its heads one after the other, about 2.5 us each).
 __device__ __forceinline__ int ctas_used(int64_t units, int heads, int most) {
@@ -355,13 +353,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
     Request rq;
     Tiles tl;
     if (A.whole) {  // one head, or a cluster's block's part of one
-      const int item = g / static_cast<uint32_t>(A.whole), rank = g - item * A.whole;
+      const int item = g / static_cast<uint32_t>(A.cluster), rank = g - item * A.cluster;
       b = item / a.n_kv_heads;
       h = item - b * a.n_kv_heads;
       rq = request_of(a, b);
       tl = tiles_of(a, rq);
-      t0 = tl.count * rank / A.whole;
-      t1 = tl.count * (rank + 1) / A.whole;
+      t0 = tl.count * rank / A.cluster;
+      t1 = tl.count * (rank + 1) / A.cluster;
       u = t0;
       u1 = t1;
       if (tl.count == 0) {
@@ -426,7 +424,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
           o.w += w * v.w;
         }
       }
-      if (A.whole > 1) {
+      if (A.cluster > 1) {
         *reinterpret_cast<float4 *>(sm_raw + (r * D + d) * 4) = o;
         if (d == 0) block_ml[r] = make_float2(M, L);
       } else if (whole) {
@@ -439,18 +437,18 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
         if (d == 0) A.part_ml[slot + r] = make_float2(M, L);
       }
     }
-    if (A.whole > 1) {  // the blocks' parts: a warp takes every kth row
+    if (A.cluster > 1) {  // the blocks' parts: a warp takes every kth row
       __syncwarp();
       cluster_sync();
-      const int rank = g % static_cast<uint32_t>(A.whole), d = lane * 4;
-      for (int r = rank + A.whole * warp; r < R; r += A.whole * kFewWarps) {
+      const int rank = g % static_cast<uint32_t>(A.cluster), d = lane * 4;
+      for (int r = rank + A.cluster * warp; r < R; r += A.cluster * kFewWarps) {
         float4 v[kMostCluster];
         const uint32_t at = smem_u32(sm_raw) + (r * D + d % D) * 4;
 #pragma unroll
         for (int i = 0; i < kMostCluster; ++i)
-          if (i < A.whole) v[i] = ld_cluster_f4(cluster_map(at, i));
+          if (i < A.cluster) v[i] = ld_cluster_f4(cluster_map(at, i));
         float2 x = make_float2(-INFINITY, 0.f);
-        if (lane < A.whole) {
+        if (lane < A.cluster) {
           const uint32_t y = cluster_map(smem_u32(block_ml + r), lane);
           x = make_float2(ld_cluster_f32(y), ld_cluster_f32(y + 4));
         }
@@ -573,9 +571,9 @@ constexpr int kWholeSlots = 512;
 // Where there are fewer heads than blocks, a head is a cluster's, whose blocks join their parts through distributed
 // shared memory: as many blocks as are left and kBlockSlots slots for each (8 heads of 512 slots: eight
 // blocks 5.8 us, four 6.5 us, one 9.1 us; of 128 slots: one 4.9 us, two 5.8 us).
-// Clusters of more than kEasyCluster blocks take most of a GPC, eight of them at a time (2 requests of 4096
-// slots, 16 heads: eight blocks each 12.7 us, sixteen 17.6 us).
-constexpr int kBlockSlots = 64, kEasyCluster = 8, kWideClusters = 8;
+// More heads than the device holds clusters at once would go in turns (2 requests of 4096 slots, 16 heads, of which
+// it holds 14 clusters of sixteen: eight blocks each 12.7 us, sixteen 17.6 us).
+constexpr int kBlockSlots = 64;
 // Up to this many slots a block (one request, 8 heads, 16 blocks each: 4096 slots 9.0 us, shared out 12.2 us; 16 384
 // slots 20.7 and 22.5 us; 32 768 slots 34.2 and 31.9 us).  max_len only bounds the lengths, and a cluster is as
 // slow as its longest head (16 ragged requests, a block up to 16 384 slots: 236 and 184 us); a window
@@ -590,35 +588,33 @@ size_t few_bytes(int head_dim) {
   return align256(few_blocks() * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
 }
 
-template <typename T, int D>
-static cudaError_t launch(const PagedAttnArgs &A, cudaStream_t s) {
+template <typename T, int D, bool HALF> static cudaError_t launch(PagedAttnArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  const int rows = a.max_rows * a.group;
-  auto kernel = rows <= 8 ? attention_few<T, D, true> : attention_few<T, D, false>;
+  auto kernel = attention_few<T, D, HALF>;
+  static const ClustersAtOnce fit(kernel, kFewThreads, Few<D>::kSmem);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
   if (e != cudaSuccess) return e;
-  if (A.whole == 1) return launch_pdl(kernel, dim3(a.n_requests * a.n_kv_heads), dim3(kFewThreads), Few<D>::kSmem, s, A);
-  if (A.whole > 1) {
-    const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (c != cudaSuccess) return c;
-    return launch_pdl_cluster(kernel, dim3(a.n_requests * a.n_kv_heads * A.whole), dim3(kFewThreads), Few<D>::kSmem, s, A.whole, A);
-  }
+  const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
+  int blocks = 1;
+  while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
+  const int64_t most = blocks == 1 ? kWholeSlots : blocks * (seen < a.max_len ? kClusterWindow : kClusterSlots);
+  A.whole = seen <= most;
+  A.cluster = A.whole ? blocks : 1;
+  if (A.whole)
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(heads * blocks)), dim3(kFewThreads), Few<D>::kSmem, s, blocks, A);
   const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Few<D>::kSmem, s, A);
   if (f != cudaSuccess) return f;
+  const int rows = a.max_rows * a.group;
   return launch_pdl(attention_join<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
+}
+template <typename T, int D> static cudaError_t launch(PagedAttnArgs &A, cudaStream_t s) {
+  return A.p.max_rows * A.p.group <= 8 ? launch<T, D, true>(A, s) : launch<T, D, false>(A, s);
 }
 
 std::string launch_attention_few(PagedAttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = few_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows;
-  const int64_t seen = visible_slots(A.p), heads = static_cast<int64_t>(A.p.n_requests) * A.p.n_kv_heads;
-  int blocks = 1;
-  while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && 2 * blocks * heads <= A.n_ctas &&
-         (2 * blocks <= kEasyCluster || heads <= kWideClusters))
-    blocks *= 2;
-  const int64_t most = blocks == 1 ? kWholeSlots : blocks * (seen < A.p.max_len ? kClusterWindow : kClusterSlots);
-  A.whole = seen <= most ? blocks : 0;
   A.join = reinterpret_cast<PagedJoin *>(p);
   p += align256(A.n_ctas * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);

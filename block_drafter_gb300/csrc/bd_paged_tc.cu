@@ -50,6 +50,8 @@ template <int D> struct Tc {
   static constexpr int kSlots = D == 128 ? 5 : 8;          // ring tiles
   static constexpr uint32_t kOffRing = 2 * kTile;          // behind the two query tiles
   static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
+  static constexpr uint32_t kOffPart = kOffRing + kItemRows * D * 4;  // (reference, sum) of a cluster's block's part
+  static_assert(kOffPart + kItemRows * 8 <= kOffBar, "a part lies in the ring");
   static constexpr uint32_t kOffSeg = kOffBar + 320;       // [kSegments] segments of 64 bytes
   static constexpr size_t kSmem = 1024 + kOffSeg + kSegments * 64 + 128;  // and the walk
   static_assert(32 + 8 * kTcThreads / 32 <= 128, "the walk and the warps' totals");
@@ -210,6 +212,18 @@ struct SegmentWalk {
   int64_t u, end, before;
   int i;
 };
+// Place `place` of the items of a call that is not shared out -- the requests' last rows first, which have the most
+// tiles -- is of request b and KV head h; returns how many row tiles of 256 (128) rows lie behind its.
+__device__ __forceinline__ int whole_entry(const PagedArgs &a, uint32_t place, int &b, int &h) {
+  const uint32_t entry = place / a.n_kv_heads, back = entry / static_cast<uint32_t>(a.n_requests);
+  h = place - entry * a.n_kv_heads;
+  b = entry - back * a.n_requests;
+  return static_cast<int>(back);
+}
+// That row tile's number; below 0: there is none.
+__device__ __forceinline__ int whole_tile(const PagedAttnArgs &A, const Request &rq, int back) {
+  return (rq.rows * A.p.group + A.item_rows - 1) / A.item_rows - 1 - back;
+}
 // The block's next segment; t0 == t1: none.
 __device__ __forceinline__ void next_segment(const PagedAttnArgs &A, int nqt, int64_t units, int ctas, SegmentWalk &w, Segment &s) {
   const PagedArgs &a = A.p;
@@ -217,23 +231,24 @@ __device__ __forceinline__ void next_segment(const PagedAttnArgs &A, int nqt, in
   while (w.u < w.end && s.t0 == s.t1) {
     int qt;
     if (A.whole) {
-      // Every request's last rows -- the most tiles -- first, and the blocks taken in turn there and back:
-      // who has one of a round's largest items has one of the next round's smallest.
-      const uint32_t r = static_cast<uint32_t>(w.u++), place = r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-      const uint32_t entry = (r * gridDim.x + place) / a.n_kv_heads;
-      s.h = r * gridDim.x + place - entry * a.n_kv_heads;
-      qt = entry / static_cast<uint32_t>(a.n_requests);
-      s.b = entry - qt * a.n_requests;
+      // the clusters are taken in turn there and back: who has one of a round's largest items has one of the
+      // next round's smallest
+      const uint32_t r = static_cast<uint32_t>(w.u++), n = gridDim.x / A.cluster, k = blockIdx.x / A.cluster;
+      qt = whole_entry(a, r * n + (r & 1 ? n - 1 - k : k), s.b, s.h);
     } else {
       s.b = w.i / nqt;
       qt = w.i - s.b * nqt;
     }
     const Request rq = request_of(a, s.b);
-    if (A.whole && (qt = (rq.rows * a.group + A.item_rows - 1) / A.item_rows - 1 - qt) < 0) continue;
+    if (A.whole && (qt = whole_tile(A, rq, qt)) < 0) continue;
     const ItemRows ir = item_rows(a, rq, qt, A.item_rows);
     const ItemTiles tl = item_tiles(a, ir);
     int from = 0, to = tl.count;
-    if (!A.whole) {
+    if (A.cluster > 1) {  // an even part
+      const int rank = blockIdx.x % A.cluster;
+      from = tl.count * rank / A.cluster;
+      to = tl.count * (rank + 1) / A.cluster;
+    } else if (!A.whole) {
       const int per = item_units(tl);
       const int64_t all = static_cast<int64_t>(per) * a.n_kv_heads;
       if (w.u >= w.before + all) {  // to the next item, past what the request does not fill
@@ -260,7 +275,7 @@ __device__ __forceinline__ void next_segment(const PagedAttnArgs &A, int nqt, in
     s.p_high = ir.p_high;
     s.sinks = tl.sinks;
     s.first = tl.first;
-    s.whole = s.t0 == 0 && s.t1 == tl.count;
+    s.whole = s.t0 == 0 && s.t1 == tl.count && A.cluster == 1;
     s.split = ir.n <= 128;
     s.len = rq.n;
   }
@@ -659,6 +674,8 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
       l += sums.x + sums.y;
     }
     if (any && !wait_warp(B, &B.o_full[st], n_o++ & 1)) return;
+    // a cluster's block leaves its part in the ring, which the other stream's products must have read too
+    if (A.cluster > 1 && !split && !wait_warp(B, &B.o_full[st ^ 1], 0)) return;
     tc_fence_after();
     float w0 = 1.f, w1 = 0.f;
     if (split) {  // stream 0 joins both streams' sums and writes; the second query tile carries (ref, l)
@@ -692,7 +709,9 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
     const uint32_t own = smem_u32(smp + st * C::kTile) + wt * 128;  // this row in the tile
     T *out = static_cast<T *>(A.out) + g->row0 * A.out_stride + g->h * a.group * D + c * 8;
     // a block's parts: of the item that its share begins inside, and of the one that it ends inside
-    float *part = A.part_o + (static_cast<int64_t>(2 * blockIdx.x + (g->t0 > 0 ? 0 : 1)) * kItemRows + (tile0 - g->r0)) * D;
+    const int64_t slot = static_cast<int64_t>(2 * blockIdx.x + (g->t0 > 0 ? 0 : 1)) * kItemRows;
+    float *part = (A.cluster > 1 ? reinterpret_cast<float *>(smp + C::kOffRing) : A.part_o + slot * D) + (tile0 - g->r0) * D;
+    float2 *part_ml = A.cluster > 1 ? reinterpret_cast<float2 *>(smp + C::kOffPart) : A.part_ml + slot;
     // 16-bit results fill the rows once, 32-bit parts take the two halves of D in turn
 #pragma unroll 1
     for (int turn = 0; turn < (whole ? 1 : 2); ++turn) {
@@ -760,7 +779,7 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
       if (whole)
         store_lse(A, rq, g->h, row, ref, l);
       else
-        A.part_ml[static_cast<int64_t>(2 * blockIdx.x + (g->t0 > 0 ? 0 : 1)) * kItemRows + (row - g->r0)] = make_float2(ref, l);
+        part_ml[row - g->r0] = make_float2(ref, l);
     }
     const int b = g->b, h = g->h;
     walk.done(wt & 31);
@@ -769,6 +788,86 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
       attend_row<T, D>(A, rq, b, r / group, h * a.group + r % group, wt & 31);
     }
   }
+}
+
+// The parts of a cluster's blocks, which each block left in its ring, joined: a warp takes every kth row.  The
+// softmax warps of all blocks; the others only pass the two barriers.
+template <typename T, int D>
+__device__ __noinline__ void cluster_join(const PagedAttnArgs &A, uint8_t *smp, int warp, int lane) {
+  using C = Tc<D>;
+  const int rank = blockIdx.x % A.cluster;
+  int b, h;
+  const int back = whole_entry(A.p, blockIdx.x / A.cluster, b, h);
+  const Request rq = request_of(A.p, b);
+  const ItemRows ir = item_rows(A.p, rq, max(0, whole_tile(A, rq, back)), A.item_rows);
+  const ItemTiles tl = item_tiles(A.p, ir);
+  if (tl.count * rank / A.cluster == tl.count * (rank + 1) / A.cluster)  // this block had no tile
+    for (int r = threadIdx.x; r < kItemRows; r += 256)
+      reinterpret_cast<float2 *>(smp + C::kOffPart)[r] = make_float2(-INFINITY, 0.f);
+  __syncwarp();
+  cluster_sync();
+  if (whole_tile(A, rq, back) >= 0 && tl.count > 0) {
+    const int d = lane * 4;
+    const uint32_t part = smem_u32(smp + C::kOffRing), ml = smem_u32(smp + C::kOffPart);
+    constexpr int kRows = 4, kBlocks = 4;  // rows and blocks whose parts are on their way together
+    const int step = A.cluster * 8;        // between a warp's rows
+    for (int r0 = rank + A.cluster * warp; r0 < ir.n; r0 += kRows * step) {
+      float2 x[kRows];
+      float M[kRows], w[kRows], L[kRows];
+      float4 o[kRows];
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) {
+        const int r = r0 + q * step;
+        x[q] = make_float2(-INFINITY, 0.f);
+        o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane < A.cluster && r < ir.n) {
+          const uint32_t y = cluster_map(ml + r * 8, lane);
+          x[q] = make_float2(ld_cluster_f32(y), ld_cluster_f32(y + 4));
+        }
+      }
+#pragma unroll 1
+      for (int i0 = 0; i0 < A.cluster; i0 += kBlocks) {
+        float4 v[kBlocks][kRows];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+          if (i0 + i < A.cluster) {
+            const uint32_t at = cluster_map(part + d % D * 4, i0 + i);
+#pragma unroll
+            for (int q = 0; q < kRows; ++q)
+              if (r0 + q * step < ir.n) v[i][q] = ld_cluster_f4(at + (r0 + q * step) * D * 4);
+          }
+        if (i0 == 0) {
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) {
+            M[q] = warp_max(x[q].y == 0.f ? -INFINITY : x[q].x);
+            w[q] = x[q].y == 0.f ? 0.f : exp2f(x[q].x - M[q]);
+            L[q] = warp_sum(w[q] * x[q].y);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) {
+            const float wi = __shfl_sync(0xffffffffu, w[q], i0 + i);
+            if (wi != 0.f) {
+              o[q].x += wi * v[i][q].x;
+              o[q].y += wi * v[i][q].y;
+              o[q].z += wi * v[i][q].z;
+              o[q].w += wi * v[i][q].w;
+            }
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) {
+        const int r = r0 + q * step;
+        if (r >= ir.n) break;
+        const bool off = d < D && finish4<T>(A, rq, h, ir.r0 + r, d, o[q], M[q], L[q]);
+        if (__any_sync(0xffffffffu, off)) attend_row<T, D>(A, rq, b, (ir.r0 + r) / A.p.group, h * A.p.group + (ir.r0 + r) % A.p.group, lane);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // every block's part is read
 }
 
 template <typename T, int D>
@@ -873,6 +972,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
       softmax_role<T, D>(A, segs, sm, B, tmem, warp >> 2, tid & 127);
+      if (A.cluster > 1) cluster_join<T, D>(A, sm, warp, lane);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
       if (warp >= 10) {
@@ -884,6 +984,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_many(const __grid_con
         mbar_wait(drain, 0);
       } else if (lane == 0) {
         segment_role(A, nqt, units, ctas, *walk, segs, B);
+      }
+      if (A.cluster > 1) {  // cluster_join's barriers
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
       }
     }
     __syncwarp();
@@ -975,9 +1080,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __g
 int many_blocks() { return num_sms() < kJoinParts - 1 ? num_sms() : kJoinParts - 1; }
 // A call is not shared out, but every item and KV head is one block's, where that leaves the busiest block
 // less than what sharing costs: its even part of the tiles, an item that it shares and, about
-// kJoinCost tiles, the joins (8 heads, group 4: 512 rows %W512%; 8192 rows %W8192%).
+// kJoinCost tiles, the joins (8 heads, group 4: 512 rows 12.4 us in items of 128 rows, 14.6 us of 256, shared out
+// 25.3 us; 8192 rows 376 us, shared out 410 us).  Items of 128 rows, whose tiles the two streams share, where there
+// are blocks for them.
 // Bounds stand for the lengths here; of several requests, ones of equal rows, as n_rows tells.
 constexpr int kJoinCost = 8;
+// An item may also be a cluster's, whose blocks join their parts through distributed shared memory, for about
+// kClusterCost tiles more than a whole item, up to kClusterTiles tiles a block (16 rows, 8 heads, group 4: 2048
+// slots, eight blocks an item 16.8 us, one 25.0 us; 8 requests of 4096 slots, two blocks 38.2 us, shared out 43.6 us,
+// of 1024 slots, two blocks 21.2 us, one 17.8 us; 16 384 slots, eight blocks 33.1 us, shared out 29.4 us).
+constexpr int kClusterCost = 5, kClusterTiles = 8;
 constexpr int kMostWhole = 4096;  // items that are weighed on the host: more take milliseconds, joins or not
 int64_t item_count(int max_rows, int group, int rows) {
   return (static_cast<int64_t>(max_rows) * group + rows - 1) / rows;
@@ -987,13 +1099,14 @@ struct WholeLoad {
 };
 WholeLoad whole_load(const PagedArgs &a, int rows, int blocks) {
   const Request rq = {a.max_len, 0, a.max_rows < a.max_len ? a.max_rows : a.max_len};
+  const bool shared = rows < kItemRows || a.max_rows * a.group <= kItemRows / 2;  // by the two streams
   const int per = a.n_requests * a.n_kv_heads;
   int load[kJoinParts] = {}, most = 0, at = 0;
   int64_t all = 0;
   bool back = false;
   for (int64_t qt = item_count(a.max_rows, a.group, rows) - 1; qt >= 0; --qt) {
     const ItemTiles t = item_tiles(a, item_rows(a, rq, static_cast<int>(qt), rows));
-    const int units = rows == kItemRows ? item_units(t) : (t.count + 1) / 2 + kItemCost;  // two streams share the tiles
+    const int units = shared ? (t.count + 1) / 2 + kItemCost : item_units(t);
     for (int x = 0; x < per; ++x) {
       int &l = load[back ? blocks - 1 - at : at];
       l += units;
@@ -1004,28 +1117,49 @@ WholeLoad whole_load(const PagedArgs &a, int rows, int blocks) {
   }
   return {most, static_cast<int>(all / blocks)};
 }
-// Sets A.whole and A.item_rows.
-void plan_whole(PagedAttnArgs &A) {
+// Sets A.whole, A.cluster and A.item_rows.
+template <typename Fit> void plan_whole(PagedAttnArgs &A, const Fit &fit) {
   const PagedArgs &a = A.p;
   const int blocks = A.n_ctas;
   const int64_t items = item_count(a.max_rows, a.group, kItemRows) * a.n_requests * a.n_kv_heads;
   A.whole = 0;
+  A.cluster = 1;
   A.item_rows = kItemRows;
   if (items > kMostWhole || (items > blocks && static_cast<int64_t>(a.n_rows) * 20 < static_cast<int64_t>(a.n_requests) * a.max_rows * 19))
     return;
   const WholeLoad w = whole_load(a, kItemRows, blocks);
   int best = w.even + kItemCost + kJoinCost;
-  auto take = [&](int most, int rows) {
+  auto take = [&](int most, int rows, int cluster) {
     if (most > best) return;
     best = most;
     A.item_rows = rows;
+    A.cluster = cluster;
     A.whole = static_cast<int>((item_count(a.max_rows, a.group, rows) * a.n_requests * a.n_kv_heads + blocks - 1) / blocks);
   };
-  take(w.most, kItemRows);
-  if (items <= blocks) take(whole_load(a, kItemRows / 2, blocks).most, kItemRows / 2);
+  // items of a cluster each: the most blocks of which the device holds a cluster for each
+  auto spread = [&](int rows) {
+    const int64_t n = item_count(a.max_rows, a.group, rows) * a.n_requests * a.n_kv_heads;
+    int size = kMostCluster;
+    while (size > 1 && n > fit.of(size)) size /= 2;
+    if (size == 1) return;
+    const Request rq = {a.max_len, 0, a.max_rows < a.max_len ? a.max_rows : a.max_len};
+    const int last = static_cast<int>(item_count(a.max_rows, a.group, rows)) - 1;
+    const int tiles = (item_tiles(a, item_rows(a, rq, last, rows)).count + size - 1) / size;
+    const int units = rows == kItemRows && a.max_rows * a.group > kItemRows / 2 ? tiles : (tiles + 1) / 2;
+    if (units <= kClusterTiles) take(units + kItemCost + kClusterCost, rows, size);
+  };
+  take(w.most, kItemRows, 1);
+  if (items <= blocks) {
+    take(whole_load(a, kItemRows / 2, blocks).most, kItemRows / 2, 1);
+    spread(kItemRows);
+    if (a.max_rows * a.group > kItemRows / 2) spread(kItemRows / 2);
+  }
 }
 
-template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt, cudaStream_t s) {
+template <typename T, int D> cudaError_t launch(PagedAttnArgs &A, cudaStream_t s) {
+  static const ClustersAtOnce fit(attention_many<T, D>, kTcThreads, Tc<D>::kSmem);
+  plan_whole(A, fit);
+  const int nqt = static_cast<int>(item_count(A.p.max_rows, A.p.group, A.item_rows));
   static std::atomic<bool> checked{false};  // the register split fits what the compiler gave the block
   if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes at;
@@ -1041,8 +1175,9 @@ template <typename T, int D> cudaError_t launch(const PagedAttnArgs &A, int nqt,
   int box = box_rows(A.p.page_size);
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   if (box && !(pool_map(&M.k, A.p, A.p.k, bf16, box) && pool_map(&M.v, A.p, A.p.v, bf16, box))) box = 0;
-  const int items = A.p.n_requests * nqt * A.p.n_kv_heads, blocks = A.whole && items < A.n_ctas ? items : A.n_ctas;
-  if (e == cudaSuccess) e = launch_pdl(attention_many<T, D>, dim3(blocks), dim3(kTcThreads), Tc<D>::kSmem, s, A, M, box, nqt);
+  const int items = A.p.n_requests * nqt * A.p.n_kv_heads, blocks = A.whole && items * A.cluster < A.n_ctas ? items * A.cluster : A.n_ctas;
+  if (e == cudaSuccess)
+    e = launch_pdl_cluster(attention_many<T, D>, dim3(blocks), dim3(kTcThreads), Tc<D>::kSmem, s, A.cluster, A, M, box, nqt);
   if (e == cudaSuccess && !A.whole) {
     const int rows = A.p.max_rows * A.p.group, most = rows < kItemRows ? rows : kItemRows;
     e = launch_pdl(attention_join_many<T, D>, dim3(A.n_ctas, (most + kJoinWarps - 1) / kJoinWarps), dim3(32 * kJoinWarps), 0, s, A);
@@ -1064,8 +1199,6 @@ std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, c
   uint8_t *p = static_cast<uint8_t *>(workspace);
   A.n_ctas = many_blocks();
   const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kItemRows;
-  plan_whole(A);
-  const int64_t nqt = item_count(a.max_rows, a.group, A.item_rows);
   A.units = reinterpret_cast<int64_t *>(p);
   p += align256((static_cast<size_t>(a.n_requests) * item_count(a.max_rows, a.group, kItemRows) + 1) * 8);
   A.share = reinterpret_cast<PagedShare *>(p);
@@ -1077,10 +1210,9 @@ std::string launch_attention_many(PagedAttnArgs A, void *workspace, int dtype, c
   A.part_ml = reinterpret_cast<float2 *>(p);
   cudaError_t e;
   if (dtype == BD_BF16)
-    e = a.head_dim == 128 ? launch<__nv_bfloat16, 128>(A, static_cast<int>(nqt), s)
-                          : launch<__nv_bfloat16, 64>(A, static_cast<int>(nqt), s);
+    e = a.head_dim == 128 ? launch<__nv_bfloat16, 128>(A, s) : launch<__nv_bfloat16, 64>(A, s);
   else
-    e = a.head_dim == 128 ? launch<__half, 128>(A, static_cast<int>(nqt), s) : launch<__half, 64>(A, static_cast<int>(nqt), s);
+    e = a.head_dim == 128 ? launch<__half, 128>(A, s) : launch<__half, 64>(A, s);
   return e == cudaSuccess ? std::string() : std::string("paged attention: ") + cudaGetErrorString(e);
 }
 

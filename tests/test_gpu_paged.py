@@ -625,3 +625,36 @@ def test_hidden_garbage_of_a_clusters_head():
     assert torch.equal(lse, wl)
     bad = torch.isfinite(out).logical_not().flatten(1).any(1)
     assert bad.tolist() == [True] * 8   # each row sees one of them or more
+
+
+@pytest.mark.parametrize("lens,rows,kw", [
+    ((4100,), (16,), dict(hkv=8)),                                           # eight blocks an item, shared streams
+    ((2600,), (33,), dict(hkv=4, group=5, page=33)),                         # 165 rows: items of 128
+    ((2000, 30, 0, 5), (20, 9, 3, 9), dict(hkv=3, group=7, d=64, dtype="fp16")),   # no tile for most blocks, no slot
+    ((3000,), (300,), dict(hkv=2, group=1, dtype="fp16")),
+    ((5000, 900), (40, 200), dict(hkv=2, group=2, window=1100, n_sink=4, page=24)),
+    ((129, 257), (128, 128), dict(hkv=1, group=2, d=64)),
+    ((6000,), (256,), dict(hkv=1, group=1, page=64)),                        # two streams, sixteen blocks
+])
+def test_items_of_a_cluster(lens, rows, kw):
+    c = PagedCase(lens, rows, lead=2, **kw).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    c.check_guards(out, lse)
+    again, lse2 = c.attend()
+    sync()
+    s = slice(c.starts[0], c.starts[-1])
+    assert torch.equal(again[s], out[s]) and torch.equal(lse2, lse)
+
+
+def test_hidden_garbage_of_a_clusters_item():
+    """Infinities among the last slots, which all rows but the request's last do not see."""
+    c = PagedCase((3001,), (30,), hkv=2, group=4).build()
+    want, wl = c.attend()
+    c.vd[c.table[0, 3000 // c.page].item(), :, 3000 % c.page] = float("inf")
+    out, lse = c.attend()
+    sync()
+    assert torch.equal(lse, wl) and not torch.isfinite(out[29]).any()
+    c.check_attention(torch.where(torch.isfinite(out), out, want), lse)
+    assert torch.isfinite(out[:29]).all()
