@@ -6,17 +6,19 @@
 //
 // attention_few: calls whose rows of one KV head (rows x group) are at most kFewRows = 16 --
 // decoding and short blocks.  Bound by the bytes of K and V, so it is built to keep loads in
-// flight.  The work of a call is a list of units of 16 slots, ordered by request, KV head and
+// flight (16 ragged requests of up to 32 768 slots: 184 us, 6.5 TB/s).  Long calls are a list of units
+// of 16 slots, ordered by request, KV head and
 // slot; the blocks (two an SM) take equal shares of it whatever the lengths are, so that one long
-// request spreads over all SMs and short ones share a block.  Inside a block every warp works alone:
-// it takes every fourth unit of the block's share, copies the unit's K and V rows page by page into
+// request spreads over all SMs and short ones share a block.  Shorter ones, bound by their start and the
+// joining launch, give each head to a cluster instead (kClusterSlots).  Inside a block every warp works alone:
+// it takes every fourth unit of the block's part, copies the unit's K and V rows page by page into
 // its own shared memory with cp.async (kStages units deep, no barrier between warps), and feeds
 // mma.sync m16n8k16 from there (the tensor work is small: tcgen05's 128-row tiles would be 7/8
 // padding).  The warps join at the end of each (request, KV head); heads that several blocks worked
 // on are joined by attention_join from fp32 parts in the workspace.
 //
 // The weights enter the second product as a 16-bit high part and a 16-bit rest: the rounding to
-// 16 bits (2^-9 relative, as large as the output's own) then disappears from the result.  With at
+// 16 bits (2^-8 relative in bf16, as large as the output's own) then disappears from the result.  With at
 // most 8 rows the rest takes the idle upper 8 rows of the product and costs nothing.
 #include "bd_paged_attn.cuh"
 

@@ -12,7 +12,9 @@
 // exponentials and the tensor cores alike (a 128 x 128 tile: 512 cycles each on an SM).
 //   warps 0-3, 4-7  take the row tiles in turn, each from its half of TMEM (N columns)
 //   warp 8          issues the MMAs;  warp 9  brings K and Q by TMA
-// Two blocks on an SM hide each other's start.
+// Two blocks on an SM hide each other's start.  Measured: a token of each of 8 requests of up to 16 384
+// slots 24.4 us, 5.0 TB/s; 64 rows of 2 requests through a window of 4096 12.8 us, half of it the start: mask, list
+// and first tiles.
 #include "bd_paged_tc.cuh"
 
 namespace bd {
@@ -404,8 +406,8 @@ template <typename T, int D, int N> cudaError_t launch(const PagedWeightsArgs &A
   const cudaError_t e = cudaFuncSetAttribute(paged_weights_many<T, D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wt<D, N>::kSmem);
   if (e != cudaSuccess) return e;
   // Blocks that share the KV heads of a tile: as many as make the longest block's work -- its tiles times
-  // their heads, and about one more for each, three where blocks meet -- the shortest (one request of 16 384 slots, 129 tiles, 8
-  // heads: two blocks 9.3 us, four 15.5 us).
+  // their heads, and about one more for each, three where blocks meet -- the shortest (one request of
+  // 16 384 slots, 129 tiles, 8 heads: two blocks 9.3 us, four 15.5 us).
   const int64_t most = (a.max_len + kTileSlots - 1) / kTileSlots * static_cast<int64_t>(a.n_requests);
   const int64_t tiles = (visible_slots(a) / kTileSlots + 1) * a.n_requests;
   int blocks = 1;
