@@ -13,7 +13,7 @@
 //   warps 0-3, 4-7  take the row tiles in turn, each from its half of TMEM (N columns)
 //   warp 8          issues the MMAs;  warp 9  brings K and Q by TMA
 // Two blocks on an SM hide each other's start.  Measured: a token of each of 8 requests of up to 16 384
-// slots 24.4 us, 5.0 TB/s; 64 rows of 2 requests through a window of 4096 12.8 us, half of it the start: mask, list
+// slots 24.4 us, 5.0 TB/s; 64 rows of 2 requests through a window of 4096 12.6 us, half of it the start: list, page ids
 // and first tiles.
 #include "bd_paged_tc.cuh"
 
@@ -76,7 +76,7 @@ __device__ __forceinline__ int rows_used(const PagedWeightsArgs &A, const Reques
   return A.rows_used ? max(0, min(__ldg(A.rows_used + b), rq.rows)) : rq.rows;
 }
 // The request's tiles that are gone through: without a window all of them, else the sinks' and those from
-// the first row's window to the last row's slot.
+// the first row's window to the last row's slot; the slots between and behind them are shared out among those.
 struct TileList {
   int sinks, first, count;
   __device__ int at(int t) const { return t < sinks ? t : first + t - sinks; }
@@ -86,7 +86,7 @@ __device__ __forceinline__ TileList tile_list(const PagedWeightsArgs &A, const R
   TileList t = {0, 0, (rq.n + kTileSlots - 1) / kTileSlots};
   if (a.window == 0) return t;
   const int base = rq.n - rq.rows, last = base + rows_used(A, rq, b) - 1;  // the last row's slot
-  if (last < max(0, base)) return {0, 0, 0};
+  if (last < max(0, base)) return t;  // no row that sees any
   const int first = window_first(a, max(0, base));
   t.first = first / kTileSlots;
   t.sinks = min((min(a.n_sink, first) + kTileSlots - 1) / kTileSlots, t.first);
@@ -145,6 +145,28 @@ template <typename F> __device__ __forceinline__ int sum_up(const PagedArgs &a, 
   return n;
 }
 
+// The `place`th tile's part of the request's slots that no row sees: their scores only decay.  Thread wt of half
+// `half` takes one slot of every other tile of them.
+__device__ __forceinline__ void unseen_slots(const PagedWeightsArgs &A, const Request &rq, int b, int place, int half, int wt) {
+  const TileList l = tile_list(A, rq, b);
+  const int behind = l.first + l.count - l.sinks;  // first tile behind the seen ones
+  const int gap = l.first - l.sinks, all = gap + (rq.n + kTileSlots - 1) / kTileSlots - behind;
+  const int x1 = static_cast<int>(static_cast<int64_t>(all) * (place + 1) / l.count);
+  for (int x0 = static_cast<int>(static_cast<int64_t>(all) * place / l.count) + half; x0 < x1; x0 += 8) {
+    float v[4];
+    int64_t at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = x0 + 2 * k, j = (x < gap ? l.sinks + x : behind + x - gap) * kTileSlots + wt;
+      at[k] = x < x1 && j < rq.n ? b * A.score_stride + j : -1;
+      v[k] = at[k] >= 0 && A.score_in ? A.decay * A.score_in[at[k]] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at[k] >= 0) A.score_out[at[k]] = v[k];
+  }
+}
+
 template <typename T, int D, int N>
 __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_constant__ PagedWeightsArgs A,
                                                                   const __grid_constant__ WeightMaps M, int box, int blocks) {
@@ -195,20 +217,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
   if (warp == 8) {
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
-  }
-  if (a.window > 0) {  // slots behind every window: a warp each 128 of them
-    const int all = sum_up(a, before, warp_total, [&](int b) { return (request_len(a, b) + kTileSlots - 1) / kTileSlots; });
-    for (int index = blockIdx.x * (kThreads / 32) + warp; index < all; index += gridDim.x * (kThreads / 32)) {
-      const int b = request_at(before, a.n_requests, index), t = index - before[b];
-      const Request rq = request_of(a, b);
-      const TileList l = tile_list(A, rq, b);
-      if (t < l.sinks || (t >= l.first && t < l.first + l.count - l.sinks)) continue;
-      for (int j = t * kTileSlots + lane; j < min(rq.n, (t + 1) * kTileSlots); j += 32) {
-        const int64_t at = b * A.score_stride + j;
-        A.score_out[at] = A.score_in ? A.decay * A.score_in[at] : 0.f;
-      }
-    }
-    __syncthreads();
   }
   const int n_tiles = sum_up(a, before, warp_total, [&](int b) {
     return a.window > 0 ? tile_list(A, request_of(a, b), b).count : (request_len(a, b) + kTileSlots - 1) / kTileSlots;
@@ -308,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
       const SlotTile t = slot_tile<N>(A, before, index);
       const int j = t.j0 + wt;
       float sum = 0.f;
+      if (a.window > 0 && rank == 0) unseen_slots(A, t.rq, t.b, index - before[t.b], half, wt);  // while the keys come
       if (t.nt > 0) {
         // rows that see this thread's slot, and those that see all of the tile's
         const int lo = max(0, j - t.base) * G, hi = a.window > 0 && j >= a.n_sink ? row_behind(a, t, j) : t.used * G;
