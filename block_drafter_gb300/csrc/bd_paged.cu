@@ -15,7 +15,7 @@ BD_DEFINE_ERROR_TAKER(take_error_word_paged)
 // thread tests some of the requests' row ranges against the block's -- and slots.  Bound by the bytes
 // (23 700 rows of 8 heads 33.4 us, 5.8 TB/s read and written), of few rows by the launch (2.5 us).
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 4;
+constexpr int kAppendRows = 32;
 constexpr int kAppendEach = 4;
 
 struct PagedAppendArgs {
@@ -76,7 +76,13 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 }
 
 static std::string launch_append(PagedAppendArgs &A, cudaStream_t s) {
-  A.rows_per_cta = A.p.n_rows > 8 * num_sms() ? kAppendRows : 1;
+  // as many rows as its threads' first pieces cover, while two blocks an SM are left (22 000 rows of one head of
+  // 128 in blocks of four 11.8 us, of thirty-two 6.3 us)
+  const int pieces = 2 * A.p.n_kv_heads * A.p.head_dim / 8;
+  A.rows_per_cta = 1;
+  while (2 * A.rows_per_cta <= kAppendRows && 2 * A.rows_per_cta * pieces <= kAppendEach * kAppendThreads &&
+         A.p.n_rows >= 4 * A.rows_per_cta * num_sms())
+    A.rows_per_cta *= 2;
   const int grid = (A.p.n_rows + A.rows_per_cta - 1) / A.rows_per_cta;
   const cudaError_t e = launch_pdl(paged_append_kernel, dim3(grid), dim3(kAppendThreads), 0, s, A);
   return e == cudaSuccess ? std::string() : std::string("paged append: ") + cudaGetErrorString(e);
@@ -84,7 +90,8 @@ static std::string launch_append(PagedAppendArgs &A, cudaStream_t s) {
 
 // ------------------------------------------------------------------ accumulated weights
 // out[j] = decay in[j] + sum over rows i and heads of 2^(scale log2(e) k_j.q_i - log2(e) lse_i).
-// Bound by K's bytes for a token or a block, by the tensor cores for many rows.  A warp owns 16 slots of
+// For pages whose slots make no TMA boxes; others go to the persistent kernel (8 requests of 8192 slots, 16 rows
+// of group 3: 29 us there, 79 us here).  A warp owns 16 slots of
 // a request: their keys are the A operand of mma.sync m16n8k16 and stay in registers while the rows of
 // the KV head pass by, 8 at a time, as B; so a slot's weights are summed in the registers of four lanes,
 // without atomics, over all rows and heads of the warp.
@@ -384,7 +391,7 @@ template <typename T, int D> static cudaError_t launch_weights_t(const PagedWeig
 }
 static std::string launch_weights(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;
-  if (weights_many_takes(a)) return launch_weights_many(A, dtype, s);  // else boxes do not fit
+  if (weights_many_takes(a)) return launch_weights_many(A, dtype, s);  // else pages make no boxes
   // Warps work on tiles of their own while there are enough for half of them; else they split the KV heads
   // of one (a token, 8 heads: 4096 slots 5.6 us split eight ways, 9.2 us whole; 16 384 slots 10.5 us
   // split in two, 12.2 us whole, 15.2 us split eight ways; 8 requests of 8192 slots 31.4 us whole, 34.7 us

@@ -1,5 +1,4 @@
-// Accumulated attention weights (bd_paged_weights) on the tensor cores, for pages and head groups that make
-// whole boxes.
+// Accumulated attention weights (bd_paged_weights) on the tensor cores, for pages that make whole boxes.
 //
 // S^T = K Q^T with the slots on the MMA's M side: a thread owns one slot -- one TMEM lane -- and adds up
 // its weights 2^(scale log2(e) s - log2(e) lse) over the columns, which are the rows, in a register.  So
@@ -7,7 +6,7 @@
 // The work is tiles of 128 slots of all requests.  A cluster takes every kth of them (one block where
 // there are enough tiles; else its blocks share the KV heads and add their sums through distributed
 // shared memory, in rank order) and passes, KV head by KV head, over the rows that see the tile, N at a
-// time: N = 16 for a token, 64 for a block, 128 for prompt rows, so that a call of few rows is bound by
+// time (as many whole tokens as fit): N = 16 for a token, 64 for a block, 128 for prompt rows, so that a call of few rows is bound by
 // K's bytes, which stream through a ring across heads and tiles, and one of many rows by the
 // exponentials and the tensor cores alike (a 128 x 128 tile: 512 cycles each on an SM).
 //   warps 0-3, 4-7  take the row tiles in turn, each from its half of TMEM (N columns)
@@ -102,7 +101,8 @@ __device__ __forceinline__ int request_at(const int *before, int n, int index) {
   }
   return lo;
 }
-template <int N> __device__ __forceinline__ SlotTile slot_tile(const PagedWeightsArgs &A, const int *before, int index) {
+// Tile `index` of the list; NR rows make a row tile.
+__device__ __forceinline__ SlotTile slot_tile(const PagedWeightsArgs &A, const int *before, int index, int NR) {
   const PagedArgs &a = A.p;
   SlotTile t;
   t.b = request_at(before, a.n_requests, index);
@@ -113,8 +113,8 @@ template <int N> __device__ __forceinline__ SlotTile slot_tile(const PagedWeight
   t.used = rows_used(A, t.rq, t.b);
   const int r_lo = max(0, t.j0 - t.base) * a.group;
   t.r_hi = a.window > 0 && t.j0 >= a.n_sink ? row_behind(a, t, t.j1) : t.used * a.group;
-  t.t0 = r_lo / N;
-  t.nt = r_lo < t.r_hi ? (t.r_hi + N - 1) / N - t.t0 : 0;
+  t.t0 = r_lo / NR;
+  t.nt = r_lo < t.r_hi ? (t.r_hi + NR - 1) / NR - t.t0 : 0;
   return t;
 }
 // before[b] = sum of count(0) .. count(b - 1); returns the sum of all.  All threads.
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
   const PagedArgs &a = A.p;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = blockIdx.x % blocks, cluster = blockIdx.x / blocks, clusters = gridDim.x / blocks;
-  const int G = a.group, hq = a.n_kv_heads * G;
+  const int G = a.group, hq = a.n_kv_heads * G, tokens = N / G, NR = tokens * G;  // of a row tile
   const int heads = (a.n_kv_heads - rank + blocks - 1) / blocks;  // KV heads rank, rank + blocks, ...
   float *sums = reinterpret_cast<float *>(sm + C::kOffSum);
   int *before = reinterpret_cast<int *>(sm + C::kOffList);
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
     uint32_t q = 0, k = 0;
     bool ok = true;
     for (int index = cluster; index < n_tiles; index += clusters) {
-      const SlotTile t = slot_tile<N>(A, before, index);
+      const SlotTile t = slot_tile(A, before, index, NR);
       if (t.nt == 0) continue;
       const int j = t.j0 + bx;
       int page = a.n_pages;  // beyond the pool: zeros
@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
           const uint32_t slot = q % QS;
           ok = q < QS || wait_all(B, &B.q_empty[slot], ((q / QS) - 1) & 1);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&B.q_full[slot], C::kQ);
+          if (lane == 0) mbar_arrive_expect_tx(&B.q_full[slot], NR * 128 * ATOMS);
           __syncwarp();
           if (lane < ATOMS)
             tma_load_3d(smem_u32(sm) + C::kOffQ + slot * C::kQ + lane * C::kQAtom, &M.q, &B.q_full[slot], lane * 64, h * G,
-                        t.rq.row0 + (t.t0 + r) * N / G);
+                        t.rq.row0 + (t.t0 + r) * tokens);
         }
       }
       __syncwarp();
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
     uint32_t q = 0, k = 0;
     bool ok = true;
     for (int index = cluster; index < n_tiles; index += clusters) {
-      const SlotTile t = slot_tile<N>(A, before, index);
+      const SlotTile t = slot_tile(A, before, index, NR);
       if (t.nt == 0) continue;
       for (int x = 0; x < heads && ok; ++x, ++k) {
         ok = wait_all(B, &B.k_full[k % KS], (k / KS) & 1);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
     uint32_t q = 0, turn = 0, n_s = 0;  // row tiles so far, sums' buffer, this half's row tiles
     bool ok = true;                     // false once a wait gave up: what follows only keeps the barriers
     for (int index = cluster; index < n_tiles; index += clusters) {
-      const SlotTile t = slot_tile<N>(A, before, index);
+      const SlotTile t = slot_tile(A, before, index, NR);
       const int j = t.j0 + wt;
       float sum = 0.f;
       if (a.window > 0 && rank == 0) unseen_slots(A, t.rq, t.b, index - before[t.b], half, wt);  // while the keys come
@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
         const int all_hi = a.window > 0 && t.j1 >= a.n_sink ? row_behind(a, t, t.j0) : t.used * G;
         const float *lse = A.lse + static_cast<int64_t>(t.rq.row0) * hq;
         auto column = [&](int x, int r) {  // -log2(e) lse of this thread's column of row tile r, KV head number x
-          const int row = (t.t0 + r) * N + wt, i = row / static_cast<uint32_t>(G), e = row - i * G;
-          return wt < N && x < heads && row < t.r_hi ? __ldg(lse + static_cast<int64_t>(i) * hq + (rank + x * blocks) * G + e) * (-1.f / kLn2)
+          const int row = (t.t0 + r) * NR + wt, i = row / static_cast<uint32_t>(G), e = row - i * G;
+          return wt < NR && x < heads && row < t.r_hi ? __ldg(lse + static_cast<int64_t>(i) * hq + (rank + x * blocks) * G + e) * (-1.f / kLn2)
                                                      : -INFINITY;
         };
         uint64_t acc[2] = {0, 0};
@@ -338,13 +338,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
           float *l_s = lse_s + (n_s & 1) * N;
           if (wt < N) l_s[wt] = next;
           named_bar(1 + half, 128);
-          const int r0 = (t.t0 + r) * N;
+          const int r0 = (t.t0 + r) * NR;
           for (r += 2; r >= t.nt && x < heads; r -= t.nt) ++x;
           next = column(x, r);
           ok = ok && wait_all(B, &B.s_full[half], n_s & 1);
           ++n_s;
           tc_fence_after();
-          const bool edge = r0 < all_lo || r0 + N > all_hi;
+          const bool edge = r0 < all_lo || r0 + N > all_hi || NR < N;  // columns from NR on are no rows
+          const int end = min(hi, r0 + NR);
 #pragma unroll 1
           for (int k = 0; k < N; k += CW) {
             uint32_t w[CW];
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
                 acc[1] = add2(acc[1], pair(exp2_fast(y1.x), exp2_fast(y1.y)));
               }
             } else {  // a hidden column adds nothing, whatever its row and lse hold
-              const uint32_t bits = seen_bits(hi - 1 - r0 - k, lo - r0 - k, 0);
+              const uint32_t bits = seen_bits(end - 1 - r0 - k, lo - r0 - k, 0);
 #pragma unroll
               for (int c = 0; c < CW; ++c) {
                 const float y = exp2_fast(fmaf(__uint_as_float(w[c]), a.scale_log2, l_s[k + c]));
@@ -442,8 +443,8 @@ int row_tile(const PagedArgs &a) {
 
 }  // namespace
 
-// Whether the kernel above takes the call: pages and head groups must make whole boxes.
-bool weights_many_takes(const PagedArgs &a) { return a.max_rows > 0 && box_rows(a.page_size) > 0 && row_tile(a) % a.group == 0; }
+// Whether the kernel above takes the call: pages must make whole boxes.
+bool weights_many_takes(const PagedArgs &a) { return a.max_rows > 0 && box_rows(a.page_size) > 0; }
 
 std::string launch_weights_many(const PagedWeightsArgs &A, int dtype, cudaStream_t s) {
   const PagedArgs &a = A.p;

@@ -658,3 +658,10 @@ def test_hidden_garbage_of_a_clusters_item():
     assert torch.equal(lse, wl) and not torch.isfinite(out[29]).any()
     c.check_attention(torch.where(torch.isfinite(out), out, want), lse)
     assert torch.isfinite(out[:29]).all()
+
+
+@pytest.mark.parametrize("rows,group,hkv,window,n_sink,d,dtype", [
+    (3, 5, 8, 0, 0, 128, "bf16"), (1, 11, 3, 90, 2, 64, "fp16"), (12, 5, 2, 0, 0, 64, "bf16"), (1, 48, 2, 0, 0, 128, "fp16"),
+    (9, 7, 9, 60, 3, 128, "fp16"), (200, 7, 1, 0, 0, 128, "bf16"), (2, 100, 1, 0, 0, 64, "bf16")])
+def test_weights_of_groups_that_do_not_fill_a_row_tile(rows, group, hkv, window, n_sink, d, dtype):
+    test_weights_of_many_rows(rows, group, hkv, window, n_sink, d, dtype, 16)
