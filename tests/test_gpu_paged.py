@@ -665,3 +665,12 @@ def test_hidden_garbage_of_a_clusters_item():
     (9, 7, 9, 60, 3, 128, "fp16"), (200, 7, 1, 0, 0, 128, "bf16"), (2, 100, 1, 0, 0, 64, "bf16")])
 def test_weights_of_groups_that_do_not_fill_a_row_tile(rows, group, hkv, window, n_sink, d, dtype):
     test_weights_of_many_rows(rows, group, hkv, window, n_sink, d, dtype, 16)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("lens,budget,sink,recent,page,kind", [
+    ((20000, 9000, 300), 8191, 4, 512, 16, "normal"), ((8193,), 100, 0, 0, 64, "ties"), ((16383, 12345), 12345, 3, 0, 33, "odd"),
+    ((70001, 66000), 5000, 1, 4000, 256, "same"), ((70001,), 65999, 0, 17, 64, "normal")])
+def test_eviction_of_long_requests(lens, budget, sink, recent, page, kind, in_place):
+    """Selections by eight blocks, and of more slots than their registers hold."""
+    test_eviction_keeps_what_the_oracle_keeps(lens, budget, sink, recent, page, kind, in_place)
