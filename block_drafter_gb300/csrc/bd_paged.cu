@@ -421,7 +421,7 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 // found so far -- each block of its slots, summed over the cluster through distributed shared memory --
 // then the digit that holds the wanted rank; it is done early where all slots of that digit stay.  Then each warp counts what stays of its run -- what is
 // larger, and of what is equal the first ones -- and, knowing what stays before its run, places it.
-// Bound by the round trips of its passes and barriers (a request of 4096 slots, 2048 kept: 12 us with
+// Bound by the round trips of its passes and barriers (a request of 4096 slots, 2048 kept: 11.3 us with
 // the move).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
 // Moves the kept slots.  Slot i's row of one pool and KV head is D contiguous values; a thread moves 16
 // bytes of it.  To other pages a block takes kMoveRows slots: it finds their places once, for `each` of
 // the 2 Hkv row sets (pool and KV head), and has the next set's rows on the way while it writes one's.
-// Bound by the bytes, read and written once (8 requests, up to 8192 slots kept: 102 us with the selection, 5.2 TB/s).
+// Bound by the bytes, read and written once (8 requests, up to 8192 slots kept: 101 us with the selection, 5.3 TB/s).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveEach = 4;  // 16-byte pieces of a thread and row set
 
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kInThreads) paged_move_in_place_kernel(const _
 static std::string launch_evict(const PagedEvictArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.p;
   // a barrier of eight blocks costs about a microsecond: fewer slots are one block's (a request of 4096
-  // slots, 2048 kept: 18.5 us with eight blocks, 12.0 us with one; of 16 384: 19.0 and 20.6 us)
+  // slots, 2048 kept: 16.3 us with eight blocks, 11.4 us with one; of 16 384: 16.0 and 18.8 us)
   const int sel = a.max_len <= kSelSmall ? 1 : kSelBlocks;
   cudaError_t e = launch_pdl_cluster(paged_select_kernel, dim3(sel, a.n_requests), dim3(kSelThreads), 0, s, sel, A);
   if (e == cudaSuccess) {
