@@ -117,6 +117,10 @@ template <typename... KArgs> struct ClustersAtOnce {
     return n[x];
   }
 };
+// Before a launch of clusters of `size` blocks: more than eight ask the function's leave, on every device.
+template <typename... KArgs> cudaError_t allow_cluster(void (*kernel)(KArgs...), int size) {
+  return size <= 8 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
 inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 size_t few_bytes(int head_dim);
 size_t many_bytes(int n_requests, int max_rows, int group, int head_dim);

@@ -602,8 +602,11 @@ template <typename T, int D, bool HALF> static cudaError_t launch(PagedAttnArgs 
   const int64_t most = blocks == 1 ? kWholeSlots : blocks * (seen < a.max_len ? kClusterWindow : kClusterSlots);
   A.whole = seen <= most;
   A.cluster = A.whole ? blocks : 1;
-  if (A.whole)
+  if (A.whole) {
+    const cudaError_t c = allow_cluster(kernel, blocks);
+    if (c != cudaSuccess) return c;
     return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(heads * blocks)), dim3(kFewThreads), Few<D>::kSmem, s, blocks, A);
+  }
   const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Few<D>::kSmem, s, A);
   if (f != cudaSuccess) return f;
   const int rows = a.max_rows * a.group;

@@ -1187,6 +1187,7 @@ template <typename T, int D> cudaError_t launch(PagedAttnArgs &A, cudaStream_t s
   if (box && !(pool_map(&M.k, A.p, A.p.k, bf16, box) && pool_map(&M.v, A.p, A.p.v, bf16, box))) box = 0;
   const int items = A.p.n_requests * nqt * A.p.n_kv_heads;
   const int blocks = A.whole && items * A.cluster < A.n_ctas ? items * A.cluster : A.n_ctas;
+  if (e == cudaSuccess) e = allow_cluster(attention_many<T, D>, A.cluster);
   if (e == cudaSuccess)
     e = launch_pdl_cluster(attention_many<T, D>, dim3(blocks), dim3(kTcThreads), Tc<D>::kSmem, s, A.cluster, A, M, box, nqt);
   if (e == cudaSuccess && !A.whole) {
