@@ -576,12 +576,12 @@ constexpr int kWholeSlots = 512;
 // More heads than the device holds clusters at once would go in turns (2 requests of 4096 slots, 16 heads, of which
 // it holds 14 clusters of sixteen: eight blocks each 12.7 us, sixteen 17.6 us).
 constexpr int kBlockSlots = 64;
-// Up to this many slots a block (one request, 8 heads, 16 blocks each: 4096 slots 9.0 us, shared out 12.2 us; 16 384
-// slots 20.7 and 22.5 us; 32 768 slots 34.2 and 31.9 us).  max_len only bounds the lengths, and a cluster is as
-// slow as its longest head (16 ragged requests, a block up to 16 384 slots: 236 and 184 us); a window
-// leaves heads alike, so there it may be more (8 requests, 8 heads: a window of 4096 27.1 and 33.9 us, of 8192
-// 44.1 and 52.0 us).
-constexpr int kClusterSlots = 1088, kClusterWindow = 2176;
+// Up to kClusterSlots slots a block: max_len only bounds the lengths, and a cluster is as slow as its longest head (16
+// ragged requests, a block up to 16 384 slots: 236 us, shared out 184 us).  A window and a call of one request leave the
+// heads alike, there it may be kClusterAlike (8 requests, 8 heads: a window of 4096 27.1 and 33.9 us, of 8192 44.1 and
+// 52.0 us; one request, 8 heads, 16 blocks each: 4096 slots 9.0 and 12.2 us whatever max_len says, 16 384 slots
+// 20.7 and 22.5 us, 32 768 slots 34.2 and 31.9 us).
+constexpr int kClusterSlots = 1088, kClusterAlike = 2176;
 
 static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts - 1; }
 
@@ -599,7 +599,8 @@ template <typename T, int D, bool HALF> static cudaError_t launch(PagedAttnArgs 
   const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
   int blocks = 1;
   while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
-  const int64_t most = blocks == 1 ? kWholeSlots : blocks * (seen < a.max_len ? kClusterWindow : kClusterSlots);
+  const bool alike = seen < a.max_len || a.n_requests == 1;
+  const int64_t most = blocks == 1 ? kWholeSlots : blocks * (alike ? kClusterAlike : kClusterSlots);
   A.whole = seen <= most;
   A.cluster = A.whole ? blocks : 1;
   if (A.whole) {

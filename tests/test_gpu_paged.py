@@ -674,3 +674,16 @@ def test_weights_of_groups_that_do_not_fill_a_row_tile(rows, group, hkv, window,
 def test_eviction_of_long_requests(lens, budget, sink, recent, page, kind, in_place):
     """Selections by eight blocks, and of more slots than their registers hold."""
     test_eviction_keeps_what_the_oracle_keeps(lens, budget, sink, recent, page, kind, in_place)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_a_short_request_under_a_large_bound(rows):
+    """A batch made for long contexts, as a captured step has it, with few slots yet."""
+    c = PagedCase((70,), (rows,), hkv=8, page=64).build()
+    table = torch.zeros(1, 512, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    for max_len in (600, 5000, 32768):
+        c.batch = c.cache.batch(table, c.lend, c.startd, c.n_rows, c.max_rows, max_len)
+        out, lse = c.attend()
+        sync()
+        c.check_attention(out, lse)
