@@ -117,6 +117,7 @@ __device__ __forceinline__ void mma_kq<__half>(float (&c)[4], const uint32_t (&a
 struct WeightTile {
   Request rq;
   int b, j0, base;
+  int last;          // slot of the last token that counts
   int i_lo, i_hi;    // tokens that see some of its slots
   int f_lo, f_hi;    // rows that see all of them, f_lo to f_hi - 1
   int64_t q0;        // this lane's row of the first row tile: element offset in q (KV head 0),
@@ -131,6 +132,7 @@ __device__ __forceinline__ WeightTile weight_tile(const PagedWeightsArgs &A, int
   t.base = t.rq.n - t.rq.rows;
   const int used = A.rows_used ? max(0, min(__ldg(A.rows_used + b), t.rq.rows)) : t.rq.rows;
   const int j1 = min(j0 + 15, t.rq.n - 1);
+  t.last = t.base + used - 1;
   t.i_lo = max(0, j0 - t.base);
   t.f_lo = max(0, j1 - t.base);
   t.i_hi = t.f_hi = used;
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWeightWarps, 2) paged_weights_kernel(con
     const WeightTile w = tile_at(ct);
     any = w.i_lo < w.i_hi && heads > 0;
     const int j = w.j0 + (lane & 15);
-    const int64_t o = any && j < w.rq.n ? slot_offset(a, a.page_table + static_cast<int64_t>(w.b) * a.table_width, j) : -1;
+    const int64_t o = any && any_seen(a, j, 1, window_first(a, max(0, w.base)), w.last) ? slot_offset(a, a.page_table + static_cast<int64_t>(w.b) * a.table_width, j) : -1;
 #pragma unroll
     for (int u = 0; u < 16 / RPI; ++u) {
       off[u] = __shfl_sync(0xffffffffu, o, u * RPI + lane / CPR);

@@ -30,14 +30,16 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Whether one of slots [from, to) holds a value that is not finite (KV head at V); one warp.
+// Whether one of slots [from, to) holds a value that is not finite (KV head at V); one warp.  The slots are hidden from
+// the row: a page that is none of the pool holds nothing, and is reported only by rows that see it.
 template <typename T, int D>
 __device__ __noinline__ bool holds_garbage(const PagedArgs &a, const T *V, const int32_t *table, int from, int to, int lane) {
   constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;  // all ones: infinity or NaN
   bool bad = false;
   for (int j = from + lane; j < to; j += 32) {
-    const int64_t off = slot_offset(a, table, j);
-    if (off < 0) continue;
+    const int page = __ldg(table + j / a.page_size);
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) continue;
+    const int64_t off = page_offset(a, page, j);
 #pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {
       const uint4 w = __ldg(reinterpret_cast<const uint4 *>(V + off) + c);

@@ -50,6 +50,13 @@ __device__ __forceinline__ int64_t slot_offset(const PagedArgs &a, const int32_t
   return page_offset(a, __ldg(table_row + j / a.page_size), j);
 }
 
+// Whether some of slots j .. j + n - 1 are seen by rows whose first slot beside the sinks is f_low and whose last is
+// p_high.  The page of slots that no row sees is not looked at: behind a window it may be given back, its
+// entry no page of the pool.
+__device__ __forceinline__ bool any_seen(const PagedArgs &a, int j, int n, int f_low, int p_high) {
+  return j <= p_high && (j + n > f_low || j < a.n_sink);
+}
+
 // First slot beside the sinks that the row at slot p sees (p >= 0).
 __host__ __device__ __forceinline__ int window_first(const PagedArgs &a, int p) {
   return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;

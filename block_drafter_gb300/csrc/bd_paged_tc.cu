@@ -342,14 +342,15 @@ __device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, co
     const int f_low = window_first(a, max(0, s.p_low)), p_high = s.p_high;
     auto slot_of = [&](int t, int k) { return s.tile(min(t, s.t1 - 1)) * kTileSlots + warp * 64 + k * 32 + lane; };
     auto page_at = [&](int t, int k) { return __ldg(table + min(slot_of(t, k), p_high) / a.page_size); };
-    // page of this thread's box of tile t; beyond the pool (zeros) where it holds no slot of the request
+    // page of this thread's box of tile t; beyond the pool (zeros) where no row of the item sees a slot of it
+    auto box_seen = [&](int j) { return mine && any_seen(a, j, box, f_low, p_high); };
     auto box_page = [&](int t) {
       const int j = s.tile(min(t, s.t1 - 1)) * kTileSlots + bx;
-      return mine && j < s.len ? __ldg(table + j / a.page_size) : a.n_pages;
+      return box_seen(j) ? __ldg(table + j / a.page_size) : a.n_pages;
     };
     auto offset = [&](int t, int k, int page) {
       const int j = slot_of(t, k);
-      return j <= p_high && (j >= f_low || j < a.n_sink) ? page_offset(a, page, j) : static_cast<int64_t>(-1);
+      return any_seen(a, j, 1, f_low, p_high) ? page_offset(a, page, j) : static_cast<int64_t>(-1);
     };
     auto free_slot = [&]() {  // the ring tile of group q
       return q < NS || wait_warp(B, &B.empty[q % NS], ((q / NS) - 1) & 1);
@@ -374,7 +375,7 @@ __device__ void load_role(const PagedAttnArgs &A, const PoolMaps &M, int box, co
         int pg = next;
         next = box_page(t + 1);
         if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) {
-          if (mine && j0 + bx < s.len) atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+          if (box_seen(j0 + bx)) atomicOr(&g_error_word, DEVERR_BAD_INDEX);
           pg = a.n_pages;
         }
         if (late) {

@@ -237,8 +237,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_weights_many(const __grid_c
       const SlotTile t = slot_tile(A, before, index, NR);
       if (t.nt == 0) continue;
       const int j = t.j0 + bx;
-      int page = a.n_pages;  // beyond the pool: zeros
-      if (mine && j < t.rq.n) {
+      // beyond the pool (zeros): boxes of which no row that counts sees a slot
+      int page = a.n_pages;
+      if (mine && any_seen(a, j, box, window_first(a, max(0, t.base)), t.base + t.used - 1)) {
         page = __ldg(a.page_table + static_cast<int64_t>(t.b) * a.table_width + j / a.page_size);
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
           page = a.n_pages;

@@ -426,15 +426,16 @@ bd_status bd_lm_head_argmax_noalloc(const bd_config *cfg, const bd_weights *w,
  *
  * Values.  q, k, v and out have the pool's type; products accumulate in fp32, softmax statistics,
  * lse and accumulated weights are fp32.  A slot that no row of the call sees is never used,
- * whatever its page holds; a slot that a row does not see does not reach that row's results,
- * even if it holds infinities or NaN.  A value that is not finite in a slot that a row does see
+ * whatever its page holds, and an entry of page_table none of whose slots a row sees may be any
+ * number (pages behind a window may be given back); a slot that a row does not see does not reach
+ * that row's results, even if it holds infinities or NaN.  A value that is not finite in a slot that a row does see
  * makes that column of the row's out infinite or NaN.
  *
  * Lengths and page ids live on the device and are checked there: a request whose rows are not
  * 0 <= row_start[b] <= row_start[b+1] <= n_rows with at most max_rows rows takes no part; one
  * whose seq_len is negative or beyond max_len or its page_table row counts as empty; a page id
- * outside the pool is not followed (the slot's values count as zero and nothing is stored
- * there).  Each sets the device error word (bd_sync_status: BD_ERR_INVALID_ARG), and that
+ * outside the pool, of a slot that a row sees or is stored in or an eviction keeps, is not followed
+ * (the slot's values count as zero and nothing is stored there).  Each sets the device error word (bd_sync_status: BD_ERR_INVALID_ARG), and that
  * request's results are unspecified.  Rows outside every request are left as they were.
  *
  * Tensors belong to the current device.  Errors: BD_ERR_INVALID_ARG (NULL, misaligned or

@@ -687,3 +687,59 @@ def test_a_short_request_under_a_large_bound(rows):
         out, lse = c.attend()
         sync()
         c.check_attention(out, lse)
+
+
+def _give_back_unseen_pages(c):
+    """Page-table entries of pages no slot of which a row sees: as a program leaves them behind a window."""
+    given = 0
+    for b, (n, r) in enumerate(zip(c.lens, c.rows)):
+        seen = P.visible(n, r, c.window, c.n_sink).any(0)
+        for i in range(-(-n // c.page)):
+            if not seen[i * c.page:(i + 1) * c.page].any():
+                c.table[b, i] = (-1, 2 ** 30, c.kd.shape[0])[i % 3]
+                given += 1
+    assert given > 0
+
+
+@pytest.mark.parametrize("page", [8, 16, 33, 64])
+@pytest.mark.parametrize("rows,kw", [
+    (1, dict()), (4, dict(hkv=1)), (16, dict()), (40, dict(d=64, dtype="fp16")), (150, dict(group=2)), (9, dict(group=40, hkv=1))])
+def test_pages_that_no_row_sees_may_be_given_back(rows, kw, page):
+    c = PagedCase((1000, 701), (rows, max(1, rows - 1)), page=page, window=200, n_sink=3, **kw).build()
+    want, wl = c.attend()
+    ws = torch.zeros(2, c.max_len, device="cuda")
+    c.cache.weights(c.batch, c.qd, wl, ws, window=c.window, n_sink=c.n_sink)
+    sync()
+    _give_back_unseen_pages(c)
+    out, lse = c.attend()
+    sync()                                  # nothing is reported
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    score = torch.zeros_like(ws)
+    c.cache.weights(c.batch, c.qd, lse, score, window=c.window, n_sink=c.n_sink)
+    sync()
+    assert torch.equal(score, ws)
+    # rows done again for an infinity among the values they do not see look past such pages, too
+    c.vd[c.table[0, 999 // page].item(), :, 999 % page] = float("inf")
+    out, _ = c.attend()
+    sync()
+    assert torch.isfinite(out[:rows - 1]).all() and not torch.isfinite(out[rows - 1]).any()
+
+
+@pytest.mark.parametrize("rows", [1, 16, 150])
+@pytest.mark.parametrize("page", [16, 33])
+def test_a_seen_page_outside_the_pool_is_still_reported(rows, page):
+    from block_drafter_gb300 import binding as B
+    c = PagedCase((1000,), (rows,), page=page, window=200, n_sink=3).build()
+    _, lse = c.attend()
+    score = torch.zeros(1, c.max_len, device="cuda")
+    sync()
+    for slot in (0, 1000 - rows - 199, 999):            # a sink, the first row's window's first slot, the last slot
+        keep = c.table[0, slot // page].item()
+        c.table[0, slot // page] = -1
+        for call in (lambda: c.attend(), lambda: c.cache.weights(c.batch, c.qd, lse, score, window=200, n_sink=3)):
+            call()
+            with pytest.raises(B.BdError):
+                B.sync_status()
+        c.table[0, slot // page] = keep
+    c.attend()
+    sync()
