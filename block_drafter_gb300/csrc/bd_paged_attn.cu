@@ -417,8 +417,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
 #pragma unroll
       for (int i = 0; i < kFewWarps; ++i) {
         const float4 v = *reinterpret_cast<const float4 *>(sm_raw + i * Few<D>::kWarpBytes + (r * D + d) * 4);
-        const float w = x[i].y == 0.f ? 0.f : exp2f(x[i].x - M);
-        if (w != 0.f) {
+        if (x[i].y != 0.f) {  // a weight of zero counts: it keeps a visible infinity or NaN
+          const float w = exp2f(x[i].x - M);
           L += w * x[i].y;
           o.x += w * v.x;
           o.y += w * v.y;
@@ -455,11 +455,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few(const __grid_con
           x = make_float2(ld_cluster_f32(y), ld_cluster_f32(y + 4));
         }
         const float M = warp_max(x.y == 0.f ? -INFINITY : x.x), w = x.y == 0.f ? 0.f : exp2f(x.x - M), L = warp_sum(w * x.y);
+        const unsigned seen = __ballot_sync(0xffffffffu, x.y != 0.f);  // blocks that saw a slot
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kMostCluster; ++i) {
           const float wi = __shfl_sync(0xffffffffu, w, i);
-          if (wi != 0.f) {
+          if (seen >> i & 1) {
             o.x += wi * v[i].x;
             o.y += wi * v[i].y;
             o.z += wi * v[i].z;
@@ -519,13 +520,13 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
       const float mn = x.y == 0.f ? m : fmaxf(m, x.x);
       l = (l == 0.f ? 0.f : l * exp2f(m - mn)) + (x.y == 0.f ? 0.f : x.y * exp2f(x.x - mn));
       m = mn;
-      weight[warp][i] = x.y == 0.f ? -INFINITY : x.x;
+      weight[warp][i] = x.y == 0.f ? INFINITY : x.x;  // infinity: a part that saw no slot
     }
     const float M = warp_max(m);
     const float L = warp_sum(l == 0.f ? 0.f : l * exp2f(m - M));
     for (int i = lane; i < j.np; i += 32) {
       const float x = weight[warp][i];
-      weight[warp][i] = x == -INFINITY ? 0.f : exp2f(x - M);
+      weight[warp][i] = x == INFINITY ? -1.f : exp2f(x - M);
     }
     if (lane == 0) row_ml[warp] = make_float2(M, L);
   }
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join(const __grid_cons
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](int i, const float4 &v) {
     const float w = weight[r][i];
-    if (w != 0.f) {
+    if (!(w < 0.f)) {  // a weight of zero counts: it keeps a visible infinity or NaN
       o.x += w * v.x;
       o.y += w * v.y;
       o.z += w * v.z;

@@ -689,6 +689,7 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
     if (A.cluster > 1 && !split && !wait_warp(B, &B.o_full[st ^ 1], 0)) return;
     tc_fence_after();
     float w0 = 1.f, w1 = 0.f;
+    bool has0 = l != 0.f, has1 = false;  // the streams that saw a slot; a weight of zero keeps a visible infinity or NaN
     if (split) {  // stream 0 joins both streams' sums and writes; the second query tile carries (ref, l)
       float2 *xch = reinterpret_cast<float2 *>(smp + C::kTile) + wt;
       if (st == 1) {
@@ -703,17 +704,18 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
       if (!wait_warp(B, B.x_ready, n_x++ & 1)) return;
       tc_fence_after();
       const float2 x = *xch;
-      const float M = fmaxf(l == 0.f ? -INFINITY : ref, x.y == 0.f ? -INFINITY : x.x);
-      w0 = l == 0.f ? 0.f : exp2f(ref - M);
-      w1 = x.y == 0.f ? 0.f : exp2f(x.x - M);
-      l = (l == 0.f ? 0.f : w0 * l) + (x.y == 0.f ? 0.f : w1 * x.y);
+      has1 = x.y != 0.f;
+      const float M = fmaxf(has0 ? ref : -INFINITY, has1 ? x.x : -INFINITY);
+      w0 = has0 ? exp2f(ref - M) : 0.f;
+      w1 = has1 ? exp2f(x.x - M) : 0.f;
+      l = (has0 ? w0 * l : 0.f) + (has1 ? w1 * x.y : 0.f);
       ref = M;
     }
     const bool valid = row < R, whole = g->whole;
-    const bool two = __any_sync(0xffffffffu, w1 != 0.f);
+    const bool two = __any_sync(0xffffffffu, has1);
     {
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      w0 = w0 == 0.f || l == 0.f ? 0.f : w0 * inv;
+      w0 *= inv;
       w1 *= inv;
     }
     bool bad = false;
@@ -731,13 +733,13 @@ __device__ void softmax_role(const PagedAttnArgs &A, const Segment *segs, uint8_
         float o[16];
         tmem_ld16(to0 + (split ? 0 : st * C::kStepO) + turn * (D / 2) + k, o);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) o[x] = w0 == 0.f ? 0.f : o[x] * w0;
+        for (int x = 0; x < 16; ++x) o[x] = has0 ? o[x] * w0 : 0.f;
         if (two) {
           float y[16];
           tmem_ld16(to0 + C::kStepO + turn * (D / 2) + k, y);
 #pragma unroll
           for (int x = 0; x < 16; ++x)
-            if (w1 != 0.f) o[x] += y[x] * w1;
+            if (has1) o[x] += y[x] * w1;
         }
         const uint32_t word = whole ? k / 2 : k;  // 4-byte words before these columns
         uint32_t v[16];
@@ -825,6 +827,7 @@ __device__ __noinline__ void cluster_join(const PagedAttnArgs &A, uint8_t *smp, 
     for (int r0 = rank + A.cluster * warp; r0 < ir.n; r0 += kRows * step) {
       float2 x[kRows];
       float M[kRows], w[kRows], L[kRows];
+      unsigned seen[kRows];  // blocks that saw a slot; a weight of zero keeps a visible infinity or NaN
       float4 o[kRows];
 #pragma unroll
       for (int q = 0; q < kRows; ++q) {
@@ -850,6 +853,7 @@ __device__ __noinline__ void cluster_join(const PagedAttnArgs &A, uint8_t *smp, 
         if (i0 == 0) {
 #pragma unroll
           for (int q = 0; q < kRows; ++q) {
+            seen[q] = __ballot_sync(0xffffffffu, x[q].y != 0.f);
             M[q] = warp_max(x[q].y == 0.f ? -INFINITY : x[q].x);
             w[q] = x[q].y == 0.f ? 0.f : exp2f(x[q].x - M[q]);
             L[q] = warp_sum(w[q] * x[q].y);
@@ -860,7 +864,7 @@ __device__ __noinline__ void cluster_join(const PagedAttnArgs &A, uint8_t *smp, 
 #pragma unroll
           for (int q = 0; q < kRows; ++q) {
             const float wi = __shfl_sync(0xffffffffu, w[q], i0 + i);
-            if (wi != 0.f) {
+            if (seen[q] >> (i0 + i) & 1) {
               o[q].x += wi * v[i][q].x;
               o[q].y += wi * v[i][q].y;
               o[q].z += wi * v[i][q].z;
@@ -1050,6 +1054,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __g
     if (i0 + lane < j.np) x = __ldcg(A.part_ml + slot(i0 + lane));
     if (x.y == 0.f) x.x = -INFINITY;
     const float m = fmaxf(M, warp_max(x.x));
+    const unsigned seen = __ballot_sync(0xffffffffu, x.y != 0.f);  // parts that saw a slot; a weight of zero keeps a visible infinity or NaN
     const float back = M == -INFINITY ? 0.f : exp2f(M - m), w = x.y == 0.f ? 0.f : exp2f(x.x - m);
     L = L * back + warp_sum(w * x.y);
     M = m;
@@ -1059,7 +1064,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_many(const __g
       const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (wi != 0.f) o[c] += wi * y[c];
+        if (seen >> i & 1) o[c] += wi * y[c];
     };
 #pragma unroll
     for (int i = 0; i < kJoinHeld; ++i)

@@ -743,3 +743,34 @@ def test_a_seen_page_outside_the_pool_is_still_reported(rows, page):
         c.table[0, slot // page] = keep
     c.attend()
     sync()
+
+
+@pytest.mark.parametrize("lens,rows,kw,bound", [
+    ((300,), (1,), dict(), 0),                                       # a head is one block's: its four warps
+    ((4100,), (1,), dict(hkv=8), 0),                                 # a cluster's
+    ((3000, 5000, 4000), (1, 1, 1), dict(hkv=8), 40000),             # shared out, joined by a launch
+    ((3000, 5000, 4000), (4, 3, 4), dict(hkv=8, dtype="fp16"), 40000),
+    ((700,), (16,), dict(), 0),                                      # a block of rows: the two streams
+    ((4100,), (16,), dict(hkv=8), 0),                                # a cluster's item
+    ((4100,), (150,), dict(group=2, d=64, dtype="fp16"), 0),
+    ((3000, 5000, 4000), (16, 9, 16), dict(hkv=8), 40000),           # items shared out
+])
+def test_a_visible_nan_beside_a_slot_that_outweighs_it_shows(lens, rows, kw, bound):
+    """One key outweighs every other by more than any exponent holds; NaN values far from it, each in a column of
+    its own, still make that column NaN, whichever warp, stream or block has them."""
+    c = PagedCase(lens, rows, spare=-(-bound // 16), **kw).build()
+    if bound:
+        c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows, bound)
+    c.qd.fill_(1.0)
+    bad = np.zeros((c.n_rows, c.hkv * c.group, c.d), bool)
+    for b, (n, r) in enumerate(zip(lens, rows)):
+        at = lambda j: (c.table[b, j // c.page].item(), slice(None), j % c.page)
+        c.kd[at(n // 2)] = 32.0                # scale q.k = 32 sqrt(D): 256 and more beyond the others' few
+        see = P.visible(n, r, 0, 0)
+        for col, j in enumerate(range(n - 1, -1, -(n // 48 + 1))):
+            if j != n // 2:
+                c.vd[at(j)][:, col] = float("nan")
+                bad[c.starts[b]:c.starts[b] + r, :, col] = see[:, j, None]
+    out, lse = c.attend()
+    sync()
+    assert bad.any() and np.array_equal(torch.isnan(out).cpu().numpy(), bad) and torch.isfinite(lse).all()
