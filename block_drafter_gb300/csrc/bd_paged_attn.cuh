@@ -61,6 +61,7 @@ __device__ __noinline__ bool holds_garbage(const PagedArgs &a, const T *V, const
 template <typename T, int D>
 __device__ __noinline__ void attend_row(const PagedAttnArgs &A, const Request &rq, int b, int i, int head, int lane) {
   const PagedArgs &a = A.p;
+  __syncwarp();  // other lanes of the warp have stored this row: their values before these
   const int row = rq.row0 + i, p = rq.n - rq.rows + i;
   const T *q = static_cast<const T *>(a.q) + row * a.q_stride + head * D;
   constexpr int C = D / 32;  // columns of a lane

@@ -774,3 +774,31 @@ def test_a_visible_nan_beside_a_slot_that_outweighs_it_shows(lens, rows, kw, bou
     out, lse = c.attend()
     sync()
     assert bad.any() and np.array_equal(torch.isnan(out).cpu().numpy(), bad) and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("rows,window,kw,launches", [
+    (4, 700, dict(group=2, hkv=2), 1),              # few rows: a head is a cluster's
+    (4, 700, dict(group=2, hkv=64), 2),             # shared out, joined by a launch
+    (16, 700, dict(group=4, hkv=2), 1),             # an item is a cluster's
+    (17, 2600, dict(group=1, hkv=51), 2),           # items shared out
+])
+@pytest.mark.parametrize("hit", ["last", "first"])
+def test_rows_done_again_hold_what_they_see_alone(rows, window, kw, launches, hit):
+    """Infinities in a slot that one row alone sees, the last row's own or the first one of the first row's window: that row
+    shows them, and every other one, done again, agrees with the oracle and keeps its lse."""
+    from block_drafter_gb300 import binding as B
+    c = PagedCase((3000, 2900, 3100), (rows,) * 3, window=window, **kw).build()
+    before = B.kernel_launches()
+    want, wl = c.attend()
+    assert B.kernel_launches() - before == launches
+    mine = []
+    for b, n in enumerate(c.lens):
+        j = n - 1 if hit == "last" else n - rows - window + 1
+        c.vd[c.table[b, j // c.page].item(), :, j % c.page] = float("inf")
+        mine.append(c.starts[b] + (rows - 1 if hit == "last" else 0))
+    out, lse = c.attend()
+    sync()
+    assert torch.equal(lse, wl)
+    fine = torch.isfinite(out).flatten(1)
+    assert [i for i in range(c.n_rows) if not fine[i].any()] == mine and fine.all(1).sum().item() == c.n_rows - 3
+    c.check_attention(torch.where(torch.isfinite(out), out, want), lse)
