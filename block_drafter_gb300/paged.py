@@ -34,6 +34,16 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream
 _TYPES = {torch.bfloat16: B.BF16, torch.float16: B.F16, torch.float32: B.F32}
 
 
+def _stream_of(handle: int, device: torch.device) -> torch.cuda.Stream:
+    # 0 and 1 are the default stream's handles; an ExternalStream of 0 would be a new stream
+    return torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)
+
+
+def _capturing(stream: torch.cuda.Stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _need(ok: bool, msg: str):
     if not ok:
         raise ValueError(msg)
@@ -64,13 +74,28 @@ class PagedBatch:
                                    page_table.data_ptr(), seq_len.data_ptr(),
                                    None if row_start is None else row_start.data_ptr())
         nbytes = B.paged_workspace_bytes(cache.struct, n, int(max_rows))
+        # Streams that the batch's own workspace is known to; None: the caller's workspace.
+        self.streams = None
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+            self.home = _current_stream(cache.index)
+            self.streams = {self.home}
         cache._on_device("workspace", workspace)
         _need(workspace.is_contiguous(), "workspace: a contiguous tensor is wanted")
         self.workspace = workspace
         self.ws_ptr = workspace.data_ptr()
         self.ws_bytes = workspace.numel() * workspace.element_size()
+
+    def _use_on(self, handle: int):
+        """First use of the batch's own workspace on a stream other than the one it was allocated on: what that one
+        has queued comes first (its memory may have been something else's), and the memory goes to no other use
+        before the stream's calls are done.  In a capture there is nothing to wait for that it could hold."""
+        device = self.workspace.device
+        home, other = (_stream_of(h, device) for h in (self.home, handle))
+        if not (_capturing(other) or _capturing(home)):
+            other.wait_stream(home)
+        self.workspace.record_stream(other)
+        self.streams.add(handle)
 
 
 class PagedCache:
@@ -128,9 +153,12 @@ class PagedCache:
         if lse.get_device() != self.index:
             self._on_device("lse", lse)
 
-    def _call(self, fn, *args, stream):
-        """The library's call on the pools' device, on the given stream or that device's current one."""
-        stream = _current_stream(self.index) if stream is None else getattr(stream, "cuda_stream", stream)
+    def _handle(self, stream) -> int:
+        """The given stream's handle, or that of the pools' device's current one."""
+        return _current_stream(self.index) if stream is None else getattr(stream, "cuda_stream", stream)
+
+    def _call(self, fn, *args, stream: int):
+        """The library's call on the pools' device."""
         if torch.cuda.current_device() == self.index:
             fn(self.struct, *args, stream)
         else:
@@ -141,14 +169,17 @@ class PagedCache:
               n_rows: int, max_rows: int, max_len: int, workspace: Optional[torch.Tensor] = None) -> PagedBatch:
         """page_table int32 [requests, pages], seq_len int32 [requests] (this step's rows counted),
         row_start int32 [requests + 1]; max_rows and max_len bound every request's rows and length.
-        workspace: a uint8 tensor to share between batches used in order on one stream."""
+        workspace: a uint8 tensor to share between batches used in order on one stream.  Without one the batch
+        allocates its own, which it keeps from other uses until its calls are done, on whatever streams they ran;
+        a stream given by its handle must outlive the batch.  Captured calls hold the addresses of the batch's
+        arrays and of its workspace: keep the batch as long as their graphs are replayed."""
         return PagedBatch(self, page_table, seq_len, row_start, n_rows, max_rows, max_len, workspace)
 
     def append(self, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
         """Stores the rows' keys and values ([n_rows, KV heads, D]) in their slots."""
         ks = self._rows("k_new", k_new, batch.kv_shape)
         vs = self._rows("v_new", v_new, batch.kv_shape)
-        self._call(B.paged_append, batch.struct, k_new.data_ptr(), ks, v_new.data_ptr(), vs, stream=stream)
+        self._call(B.paged_append, batch.struct, k_new.data_ptr(), ks, v_new.data_ptr(), vs, stream=self._handle(stream))
 
     def attention(self, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
                   window: int = 0, n_sink: int = 0, scale: Optional[float] = None, stream=None):
@@ -159,6 +190,9 @@ class PagedCache:
         os = self._rows("out", out, batch.q_shape)
         if lse is not None:
             self._lse(lse, batch)
+        stream = self._handle(stream)
+        if batch.streams is not None and stream not in batch.streams:
+            batch._use_on(stream)
         self._call(B.paged_attention, batch.struct, q.data_ptr(), qs, out.data_ptr(), os,
                    None if lse is None else lse.data_ptr(), window, n_sink,
                    self.scale if scale is None else scale, batch.ws_ptr, batch.ws_bytes, stream=stream)
@@ -180,7 +214,7 @@ class PagedCache:
         self._call(B.paged_weights, batch.struct, q.data_ptr(), qs, lse.data_ptr(),
                    None if rows_used is None else rows_used.data_ptr(), window, n_sink,
                    self.scale if scale is None else scale, decay,
-                   None if score_in is None else score_in.data_ptr(), score_out.data_ptr(), stride, stream=stream)
+                   None if score_in is None else score_in.data_ptr(), score_out.data_ptr(), stride, stream=self._handle(stream))
 
     def evict(self, batch: PagedBatch, score: torch.Tensor, budget: int, kept: torch.Tensor, len_out: torch.Tensor,
               n_sink: int = 0, n_recent: int = 0, dst_table: Optional[torch.Tensor] = None,
@@ -203,4 +237,4 @@ class PagedCache:
             ostride = self._floats("score_out", score_out, batch.n_requests, min(budget, batch.max_len))
         self._call(B.paged_evict, batch.struct, score.data_ptr(), stride, budget, n_sink, n_recent,
                    None if dst_table is None else dst_table.data_ptr(), width, kept.data_ptr(),
-                   len_out.data_ptr(), None if score_out is None else score_out.data_ptr(), ostride, stream=stream)
+                   len_out.data_ptr(), None if score_out is None else score_out.data_ptr(), ostride, stream=self._handle(stream))

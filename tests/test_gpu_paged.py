@@ -802,3 +802,58 @@ def test_rows_done_again_hold_what_they_see_alone(rows, window, kw, launches, hi
     fine = torch.isfinite(out).flatten(1)
     assert [i for i in range(c.n_rows) if not fine[i].any()] == mine and fine.all(1).sum().item() == c.n_rows - 3
     c.check_attention(torch.where(torch.isfinite(out), out, want), lse)
+
+
+def test_a_batchs_workspace_waits_for_the_streams_it_is_used_on():
+    c = PagedCase((700, 300), (40, 60)).build()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for how in ("given", "current"):
+        c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows, c.max_len)
+        out, lse = c.outputs()
+        torch.cuda.synchronize()
+        s, n, place = torch.cuda.Stream(), c.batch.ws_bytes, c.batch.ws_ptr
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)      # about 0.1 s
+            if how == "current":
+                c.cache.attention(c.batch, c.qd, out, lse=lse)
+        if how == "given":
+            c.cache.attention(c.batch, c.qd, out, lse=lse, stream=s)
+        c.batch = None                          # its call has not begun
+        other = torch.empty(n, dtype=torch.uint8, device="cuda")
+        assert other.data_ptr() != place
+        other.fill_(255)
+        sync()
+        torch.cuda.synchronize()
+        c.check_attention(out, lse)
+        del other
+        torch.cuda.empty_cache()
+
+
+def test_a_batchs_workspace_waits_for_the_stream_it_was_allocated_on():
+    import time
+    c = PagedCase((700, 300), (40, 60)).build()
+    out, lse = c.outputs()
+    s, home, done = torch.cuda.Stream(), torch.cuda.Event(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1_000_000_000)            # about 0.5 s: what the memory was before may still be in use
+    home.record()
+    c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows, c.max_len)
+    c.cache.attention(c.batch, c.qd, out, lse=lse, stream=s)
+    done.record(s)
+    time.sleep(0.05)
+    early = done.query()
+    assert home.query() or not early
+    torch.cuda.synchronize()
+    sync()
+    c.check_attention(out, lse)
+    # a batch made before, captured and replayed on streams of its own
+    graph = torch.cuda.CUDAGraph()
+    c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows, c.max_len)
+    o2, l2 = c.outputs()
+    with torch.cuda.graph(graph):
+        c.cache.attention(c.batch, c.qd, o2, lse=l2)
+    with torch.cuda.stream(s):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
