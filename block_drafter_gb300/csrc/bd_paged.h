@@ -4,6 +4,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "bd_internal.h"
@@ -87,7 +88,7 @@ inline int64_t visible_slots(const PagedArgs &a) {
   const int64_t seen = a.window > 0 ? static_cast<int64_t>(a.window) + a.max_rows + a.n_sink : a.max_len;
   return seen < a.max_len ? seen : a.max_len;
 }
-// Clusters of `size` blocks of a kernel that the device holds at once.
+// Clusters of `size` blocks of a kernel that the current device holds at once; below 0: no answer.
 template <typename... KArgs> int clusters_at_once(void (*kernel)(KArgs...), int threads, size_t smem, int size) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size);
@@ -103,19 +104,33 @@ template <typename... KArgs> int clusters_at_once(void (*kernel)(KArgs...), int 
   const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess &&
                   cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
                   cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess;
-  return ok ? n : 0;
+  if (!ok) cudaGetLastError();  // the caller does without clusters: the error is not the next call's
+  return ok ? n : -1;
 }
-// The same of 2, 4, 8 and 16 blocks, asked once.
-template <typename... KArgs> struct ClustersAtOnce {
-  int n[5];
-  ClustersAtOnce(void (*kernel)(KArgs...), int threads, size_t smem) {
-    for (int x = 0; x < 5; ++x) n[x] = x ? clusters_at_once(kernel, threads, smem, 1 << x) : 1 << 30;
-  }
+// The same of 2, 4, 8 and 16 blocks, asked once on each device; a question that failed is asked again.
+template <typename... KArgs> class ClustersAtOnce {
+ public:
+  ClustersAtOnce(void (*kernel)(KArgs...), int threads, size_t smem) : kernel_(kernel), threads_(threads), smem_(smem) {}
   int of(int size) const {
-    int x = 0;
-    while (1 << x < size) ++x;
-    return n[x];
+    if (size <= 1) return 1 << 30;
+    int device = 0, x = 0;
+    while (2 << x < size) ++x;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0) return 0;
+    std::atomic<int> *kept = device < kDevices ? &n_[device][x] : nullptr;
+    int n = kept ? kept->load(std::memory_order_relaxed) - 1 : -1;
+    if (n < 0) {
+      n = clusters_at_once(kernel_, threads_, smem_, size);
+      if (n >= 0 && kept) kept->store(n + 1, std::memory_order_relaxed);
+    }
+    return n < 0 ? 0 : n;
   }
+
+ private:
+  static constexpr int kDevices = 64;
+  void (*kernel_)(KArgs...);
+  int threads_;
+  size_t smem_;
+  mutable std::atomic<int> n_[kDevices][4] = {};  // and one; 0: not asked yet
 };
 // Before a launch of clusters of `size` blocks: more than eight ask the function's leave, on every device.
 template <typename... KArgs> cudaError_t allow_cluster(void (*kernel)(KArgs...), int size) {

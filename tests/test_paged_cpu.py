@@ -148,3 +148,46 @@ def test_python_checks_come_before_the_device(B):
     f = k.float()
     with pytest.raises(B.BdError, match="dtype"):
         PagedCache(f, f.clone(), n_q_heads=4)
+
+
+# ------------------------------------------------------------------ launch plans
+_CLUSTERS = r'''
+#include <cuda_runtime.h>
+static int device = 0, asked = 0;
+static bool fails = true;
+extern "C" cudaError_t cudaGetDevice(int *d) { *d = device; return cudaSuccess; }
+extern "C" cudaError_t cudaGetLastError() { return cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(void (*)(int), cudaFuncAttribute, int) { return cudaSuccess; }
+cudaError_t cudaOccupancyMaxActiveClusters(int *n, void (*)(int), const cudaLaunchConfig_t *c) {
+  ++asked;
+  *n = (device ? 100 : 10) / static_cast<int>(c->gridDim.x);
+  return fails ? cudaErrorUnknown : cudaSuccess;
+}
+#include "bd_paged.h"
+static void kernel(int) {}
+int main() {
+  const bd::ClustersAtOnce fit(kernel, 128, 1024);
+  if (fit.of(4) != 0) return 1;                    // no answer: no clusters
+  fails = false;
+  if (fit.of(4) != 2 || fit.of(2) != 5) return 2;  // asked again
+  device = 1;
+  if (fit.of(4) != 25 || fit.of(16) != 6) return 3;
+  device = 0;
+  const int before = asked;
+  if (fit.of(4) != 2 || fit.of(2) != 5 || asked != before) return 4;  // kept
+  return fit.of(1) < 1000;
+}
+'''
+
+
+def test_cluster_counts_are_each_devices_own_and_failed_questions_are_asked_again(tmp_path):
+    import os
+    import subprocess
+    from block_drafter_gb300 import builder
+    src, exe = tmp_path / "clusters.cpp", tmp_path / "clusters"
+    src.write_text(_CLUSTERS)
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    p = subprocess.run(["g++", "-std=c++17", "-O1", f"-I{builder.CSRC}", f"-I{builder.INCLUDE}", f"-I{cuda}", str(src), "-o", str(exe)],
+                       capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
+    assert subprocess.run([str(exe)]).returncode == 0
