@@ -1199,8 +1199,7 @@ bd_status bd_sync_status(void *stream_) {
   if (e != cudaSuccess) return fail(BD_ERR_CUDA, std::string("stream: ") + cudaGetErrorString(e));
   const unsigned word = take_error_word_gemm() | take_error_word_att() | take_error_word_small() |
                         take_error_word_pack() | take_error_word_head8() | take_error_word_bridge() |
-                        take_error_word_paged() | take_error_word_paged_attn() | take_error_word_paged_tc() |
-                        take_error_word_paged_wt();
+                        take_error_words_paged();
   if (word & DEVERR_TIMEOUT) return fail(BD_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up");
   if (word & DEVERR_BAD_INDEX)
     return fail(BD_ERR_INVALID_ARG, "a device-side index (token id, request or position) was out of range");

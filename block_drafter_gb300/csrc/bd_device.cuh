@@ -17,10 +17,9 @@ namespace bd {
 static __device__ unsigned g_error_word = 0;
 #define BD_DEFINE_ERROR_TAKER(name)                                          \
   unsigned name() {                                                          \
-    unsigned v = 0, z = 0;                                                   \
-    if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof v) != cudaSuccess) return 0; \
-    cudaMemcpyToSymbol(g_error_word, &z, sizeof z);                          \
-    return v;                                                                \
+    return take_if_set(                                                      \
+        [](unsigned &v) { return cudaMemcpyFromSymbol(&v, g_error_word, sizeof v) == cudaSuccess; }, \
+        [](unsigned z) { cudaMemcpyToSymbol(g_error_word, &z, sizeof z); }); \
   }
 
 // fp32 -> fp16 for an activation operand; a value beyond +-65504 (or not finite) would

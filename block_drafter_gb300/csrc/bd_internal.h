@@ -16,6 +16,14 @@ namespace bd {
 // DEVERR_RANGE: a weight beyond the fp16 range met the packed image's fp16 conversion;
 // DEVERR_F16: an activation beyond the fp16 range (or not finite) met an fp16 operand store.
 enum : unsigned { DEVERR_TIMEOUT = 1u, DEVERR_BAD_INDEX = 2u, DEVERR_RANGE = 4u, DEVERR_F16 = 8u };
+// One translation unit's word: read, and cleared only where it is set.  Each is a blocking copy of a
+// few microseconds, and a status call takes the words of all units.
+template <typename Read, typename Write> unsigned take_if_set(Read read, Write write) {
+  unsigned v = 0;
+  if (!read(v)) return 0;
+  if (v) write(0u);
+  return v;
+}
 
 // ------------------------------------------------------------------ GEMM
 // D[tok, out] = X[tok, :] . W[out, :]  computed swap-AB on tcgen05: weight rows fill the

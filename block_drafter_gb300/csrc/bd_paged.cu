@@ -9,6 +9,12 @@ namespace bd {
 
 BD_DEFINE_ERROR_TAKER(take_error_word_paged)
 
+static std::atomic<bool> paged_used{false};  // some call of this file has launched, or been captured
+unsigned take_error_words_paged() {
+  if (!paged_used.load(std::memory_order_acquire)) return 0;
+  return take_error_word_paged() | take_error_word_paged_attn() | take_error_word_paged_tc() | take_error_word_paged_wt();
+}
+
 // ------------------------------------------------------------------ append
 // Copies each row's keys and values into its slot.  A block takes rows_per_cta consecutive rows; the first
 // kAppendEach 16-byte pieces of every thread are on their way while it finds the rows' requests -- every
@@ -803,6 +809,7 @@ bd_status check_mask(int window, int n_sink, float scale) {
 }
 
 PagedArgs args_of(const bd_paged_kv *c, const bd_paged_batch *t) {
+  paged_used.store(true, std::memory_order_release);
   PagedArgs a = {};
   a.k = c->k;
   a.v = c->v;

@@ -145,7 +145,8 @@ std::string launch_attention_many(PagedAttnArgs a, void *workspace, int dtype, c
 bool weights_many_takes(const PagedArgs &a);
 std::string launch_weights_many(const PagedWeightsArgs &A, int dtype, cudaStream_t s);
 
-unsigned take_error_word_paged();
+// The error words of the paged-cache kernels together; not read (a blocking copy each) before the first call of theirs.
+unsigned take_error_words_paged();
 unsigned take_error_word_paged_wt();
 unsigned take_error_word_paged_attn();
 unsigned take_error_word_paged_tc();

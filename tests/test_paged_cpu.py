@@ -180,14 +180,38 @@ int main() {
 '''
 
 
-def test_cluster_counts_are_each_devices_own_and_failed_questions_are_asked_again(tmp_path):
+def _run_host_program(tmp_path, text):
     import os
     import subprocess
     from block_drafter_gb300 import builder
-    src, exe = tmp_path / "clusters.cpp", tmp_path / "clusters"
-    src.write_text(_CLUSTERS)
+    src, exe = tmp_path / "host.cpp", tmp_path / "host"
+    src.write_text(text)
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     p = subprocess.run(["g++", "-std=c++17", "-O1", f"-I{builder.CSRC}", f"-I{builder.INCLUDE}", f"-I{cuda}", str(src), "-o", str(exe)],
                        capture_output=True, text=True)
     assert p.returncode == 0, p.stderr
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_cluster_counts_are_each_devices_own_and_failed_questions_are_asked_again(tmp_path):
+    _run_host_program(tmp_path, _CLUSTERS)
+
+
+_WORDS = r'''
+#include "bd_internal.h"
+int main() {
+  unsigned word = 0;
+  int copies = 0;
+  auto read = [&](unsigned &v) { ++copies; v = word; return true; };
+  auto write = [&](unsigned v) { ++copies; word = v; };
+  if (bd::take_if_set(read, write) != 0 || copies != 1) return 1;  // nothing set: one copy
+  word = 6;
+  if (bd::take_if_set(read, write) != 6 || word != 0 || copies != 3) return 2;
+  word = 2;
+  return bd::take_if_set([](unsigned &) { return false; }, write) != 0 || word != 2;  // not read: kept
+}
+'''
+
+
+def test_a_status_call_copies_an_error_word_back_only_where_it_was_set(tmp_path):
+    _run_host_program(tmp_path, _WORDS)
