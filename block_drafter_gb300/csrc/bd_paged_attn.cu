@@ -577,12 +577,25 @@ constexpr int kWholeSlots = 512;
 // More heads than the device holds clusters at once would go in turns (2 requests of 4096 slots, 16 heads, of which
 // it holds 14 clusters of sixteen: eight blocks each 12.7 us, sixteen 17.6 us).
 constexpr int kBlockSlots = 64;
-// Up to kClusterSlots slots a block: max_len only bounds the lengths, and a cluster is as slow as its longest head (16
-// ragged requests, a block up to 16 384 slots: 236 us, shared out 184 us).  A window and a call of one request leave the
-// heads alike, there it may be kClusterAlike (8 requests, 8 heads: a window of 4096 27.1 and 33.9 us, of 8192 44.1 and
-// 52.0 us; one request, 8 heads, 16 blocks each: 4096 slots 9.0 and 12.2 us whatever max_len says, 16 384 slots
-// 20.7 and 22.5 us, 32 768 slots 34.2 and 31.9 us).
-constexpr int kClusterSlots = 1088, kClusterAlike = 2176;
+// What a block of a cluster goes through alone is weighed against an even share of the call, the joining launch and its
+// parts (a head is at most n_ctas / heads parts), all in slots of a block (us of a cluster of sixteen / shared out; one
+// request, group 4, D = 128):
+//   KV heads     4096       16 384      20 480      24 576      28 672      32 768
+//   1         7.5/10.9   16.8/21.3   19.8/24.5   22.6/24.7   25.5/25.0   28.3/25.5
+//   2         7.8/12.7   16.8/19.0   19.8/20.0   22.6/20.3   25.6/20.9   28.4/21.9
+//   4         8.3/14.0   17.1/19.2   20.1/20.7   22.9/21.7   25.8/22.8   28.8/23.9
+//   8         9.8/14.5   20.3/21.9   23.9/24.7   27.3/27.3   30.9/29.4   34.2/32.0
+// The rule shares out from 23 777, 19 729, 19 281 and 24 193 slots on; both take as long at about 27 500, 20 300, 20 900 and
+// 24 600 (group 1: 20 900, 16 400 and 24 600 of 1, 2 and 8 heads; group 16: 22 000, 16 800 and 18 000; D = 64 within a
+// tenth of group 4).  It goes by the bound max_len: a shorter request under a larger bound takes the second figure.
+// Where clusters give every SM a block, shares have no more of the device: up to kClusterFilled slots a block (windows, 8
+// heads: 5 requests, 8192 slots, 4 blocks a head 34.9/37.9; 10 requests, 4096 slots, 2 blocks 34.8/38.5; 19
+// requests 51.0/57.7).
+// All of this holds for heads that are alike, as a window or a call of one request makes them.  Else a cluster is as slow as
+// its longest head, and max_len only bounds it: up to kClusterSlots slots a block (8 requests of 16 384 slots and one head
+// 20.4/22.5, 2 requests of 8 heads 34.1/31.3; 16 ragged requests, a block up to 16 384 slots: 236/184).
+constexpr int kClusterSlots = 1088, kClusterFilled = 2176;
+constexpr int kJoinSlots = 800, kPartSlots = 2;
 
 static int few_blocks() { return few_ctas() < kJoinParts ? few_ctas() : kJoinParts - 1; }
 
@@ -601,8 +614,13 @@ template <typename T, int D, bool HALF> static cudaError_t launch(PagedAttnArgs 
   int blocks = 1;
   while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
   const bool alike = seen < a.max_len || a.n_requests == 1;
-  const int64_t most = blocks == 1 ? kWholeSlots : blocks * (alike ? kClusterAlike : kClusterSlots);
-  A.whole = seen <= most;
+  const int64_t each = (seen + blocks - 1) / blocks, share = heads * seen / A.n_ctas;  // a block's slots, either way
+  if (blocks == 1)
+    A.whole = seen <= kWholeSlots;
+  else if (alike)
+    A.whole = each <= share + kJoinSlots + kPartSlots * A.n_ctas / heads || (heads * blocks >= num_sms() && each <= kClusterFilled);
+  else
+    A.whole = each <= kClusterSlots;
   A.cluster = A.whole ? blocks : 1;
   if (A.whole) {
     const cudaError_t c = allow_cluster(kernel, blocks);

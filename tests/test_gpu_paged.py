@@ -857,3 +857,30 @@ def test_a_batchs_workspace_waits_for_the_stream_it_was_allocated_on():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("requests,hkv,bound,window,launches", [
+    (1, 1, 16384, 0, 1), (1, 1, 32768, 0, 2), (1, 2, 16384, 0, 1), (1, 2, 32768, 0, 2), (1, 4, 16384, 0, 1), (1, 4, 32768, 0, 2),
+    (1, 8, 16384, 0, 1), (1, 8, 32768, 0, 2), (1, 16, 4096, 0, 1), (1, 16, 16384, 0, 2),
+    (5, 8, 32768, 8192, 1), (10, 8, 32768, 4096, 1), (19, 8, 32768, 4096, 1), (2, 1, 32768, 32000, 2), (8, 1, 16384, 0, 1), (2, 8, 16384, 0, 2)])
+def test_a_token_is_shared_out_where_that_was_faster(requests, hkv, bound, window, launches):
+    """A cluster a head is one launch, equal shares and their joins are two; which was measured to be faster at the bound."""
+    from block_drafter_gb300 import binding as B
+    c = PagedCase(tuple(40 + 30 * b for b in range(requests)), (1,) * requests, hkv=hkv, window=window, spare=-(-bound // 16)).build()
+    c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, 1, bound)
+    before = B.kernel_launches()
+    out, lse = c.attend()
+    assert B.kernel_launches() - before == launches
+    sync()
+    c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("lens,rows,kw", [
+    ((32768,), (1,), dict(hkv=1)), ((20011,), (1,), dict(hkv=1, group=16, d=64)), ((12001, 30000), (2, 1), dict(hkv=1, dtype="fp16")),
+    ((32768,), (1,), dict(hkv=2, page=64)), ((17000,), (4,), dict(hkv=2, d=64, page=33)), ((19999,), (60,), dict(hkv=1)),
+    ((23000,), (16,), dict(hkv=2, dtype="fp16", page=64))])
+def test_few_heads_over_long_requests(lens, rows, kw):
+    c = PagedCase(lens, rows, **kw).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
