@@ -683,6 +683,7 @@ constexpr int kInRegs = 8;  // 16-byte pieces of a chunk per thread
 __global__ void __launch_bounds__(kInThreads) paged_move_in_place_kernel(const __grid_constant__ PagedEvictArgs A) {
   const PagedArgs &a = A.p;
   const int b = blockIdx.y, h = blockIdx.x >> 1;
+  if ((blockIdx.x & 1) && a.k == a.v) return;  // one pool for both: moved once, for two blocks would not keep in step
   uint16_t *pool = static_cast<uint16_t *>(const_cast<void *>(blockIdx.x & 1 ? a.v : a.k)) + h * a.head_stride;
   const int cpr = a.head_dim / 8;
   const int chunk = kInThreads * kInRegs / cpr;  // rows
@@ -774,6 +775,9 @@ bd_status check_kv(const bd_paged_kv *c) {
   return BD_OK;
 }
 
+// Whether a slot's keys and values lie in one another but are not the same: no call can store them.
+bool pools_mixed(const bd_paged_kv *c) { return c->k != c->v && overlap(c->k, 2 * c->head_dim, c->v, 2 * c->head_dim); }
+
 bd_status check_batch(const bd_paged_kv *c, const bd_paged_batch *t, bool rows) {
   if (bd_status st = check_kv(c)) return st;
   if (!t) return refuse(BD_ERR_INVALID_ARG, "paged batch is NULL");
@@ -859,6 +863,8 @@ bd_status bd_paged_append(const bd_paged_kv *kv, const bd_paged_batch *batch, co
   const int64_t width = static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim;
   if (bd_status st = check_rows(k_new, k_stride, width, batch->n_rows, "k_new")) return st;
   if (bd_status st = check_rows(v_new, v_stride, width, batch->n_rows, "v_new")) return st;
+  if (pools_mixed(kv) || (kv->k == kv->v && (k_new != v_new || k_stride != v_stride)))
+    return refuse(BD_ERR_INVALID_ARG, "paged append: k and v are one pool, which takes the same rows as keys and values only");
   PagedAppendArgs A = {};
   A.p = args_of(kv, batch);
   A.k_new = k_new;
@@ -944,6 +950,7 @@ bd_status bd_paged_evict(const bd_paged_kv *kv, const bd_paged_batch *batch, con
   if (bd_status st = check_batch(kv, batch, false)) return st;
   if (budget < 1 || n_sink < 0 || n_recent < 0 || static_cast<int64_t>(n_sink) + n_recent > budget)
     return refuse(BD_ERR_INVALID_ARG, "paged eviction: budget must be >= 1 and hold n_sink + n_recent");
+  if (pools_mixed(kv)) return refuse(BD_ERR_INVALID_ARG, "paged eviction: the slots of k and v overlap");
   const int most = budget < batch->max_len ? budget : batch->max_len;
   if (!score || misaligned(score, 4) || score_stride < batch->max_len)
     return refuse(BD_ERR_INVALID_ARG, "paged eviction: score must be given, with rows of at least max_len entries");

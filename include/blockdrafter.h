@@ -457,7 +457,8 @@ typedef struct {
   int64_t page_stride;        /* elements between pages, KV heads and slots of the pool (each a   */
   int64_t head_stride;        /*   multiple of 8; the D values of a slot are contiguous); the     */
   int64_t slot_stride;        /*   same for k and v                                               */
-  void *k, *v;                /* dev pools, 16-byte aligned                                       */
+  void *k, *v;                /* dev pools, 16-byte aligned; both may be one pool (v = k): it is     */
+                              /*   then appended to with v_new = k_new                            */
 } bd_paged_kv;
 
 typedef struct {

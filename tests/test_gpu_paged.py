@@ -884,3 +884,33 @@ def test_few_heads_over_long_requests(lens, rows, kw):
     out, lse = c.attend()
     sync()
     c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_keys_and_values_in_one_pool(in_place):
+    """One pool for both: a row is its key and its value; long in-place moves keep their slots."""
+    lens, budget, page = (20000, 9000), 8000, 16
+    c = PagedCase(lens, (3, 70), page=page, hkv=4, d=64).build()
+    x = c.kd.clone() if in_place else torch.cat([c.kd, torch.full((1000,) + c.kd.shape[1:], float("nan"), dtype=c.kd.dtype, device="cuda")])
+    c.cache = type(c.cache)(x, x, n_q_heads=c.hkv * c.group)
+    c.batch = c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows, c.max_len)
+    new = torch.randn(c.n_rows, c.hkv, c.d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    rows = new.cuda()
+    c.cache.append(c.batch, rows, rows)
+    for b, (n, r) in enumerate(zip(c.lens, c.rows)):
+        c.k[b][n - r:] = new[c.starts[b]:c.starts[b] + r].double().numpy()
+    c.v = c.k
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    score = torch.rand(2, max(lens), device="cuda")
+    kept = torch.zeros(2, budget, dtype=torch.int32, device="cuda")
+    new_len = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dst = None if in_place else (c.kd.shape[0] + torch.arange(1000, device="cuda", dtype=torch.int32)).view(2, 500)
+    c.cache.evict(c.batch, score, budget, kept, new_len, dst_table=dst)
+    sync()
+    table = c.table if in_place else dst
+    for b in range(2):
+        i = torch.arange(budget, device="cuda")
+        got = x[table[b].long()[i // page], :, i % page]
+        assert new_len[b].item() == budget and torch.equal(got.double().cpu(), torch.from_numpy(c.k[b])[kept[b].cpu().long()])

@@ -132,6 +132,19 @@ def test_bad_append_weights_and_eviction_arguments_are_refused(B):
         assert evict(**kw) == -1 and msg in L.bd_last_error(), kw
 
 
+def test_pools_whose_slots_overlap_are_not_stored_to(B):
+    L, bt = B.lib(), _batch(B)
+    evict = lambda kv: L.bd_paged_evict(kv, bt, 0x70000, 100, 50, 1, 1, None, 0, 0x80000, 0x90000, None, 0, None)
+    for off in (-240, -16, 16, 240):                     # a slot of 128 values: 256 bytes
+        kv = _kv(B, v=0x10000 + off)
+        for k, v in ((0x40000, 0x50000), (0x40000, 0x40000)):
+            assert L.bd_paged_append(kv, bt, k, 256, v, 256, None) == -1 and b"one pool" in L.bd_last_error()
+        assert evict(kv) == -1 and b"overlap" in L.bd_last_error()
+    one = _kv(B, v=0x10000)                              # one pool takes one set of rows
+    assert L.bd_paged_append(one, bt, 0x40000, 256, 0x50000, 256, None) == -1 and b"one pool" in L.bd_last_error()
+    assert L.bd_paged_append(one, bt, 0x40000, 256, 0x40000, 264, None) == -1 and b"one pool" in L.bd_last_error()
+
+
 def test_python_checks_come_before_the_device(B):
     from block_drafter_gb300.paged import PagedCache
     k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
