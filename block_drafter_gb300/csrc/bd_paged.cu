@@ -960,14 +960,18 @@ bd_status bd_paged_evict(const bd_paged_kv *kv, const bd_paged_batch *batch, con
     return refuse(BD_ERR_INVALID_ARG, "paged eviction: dst_table's rows must hold min(budget, max_len) slots");
   if (dst_table == batch->page_table && dst_table)
     return refuse(BD_ERR_INVALID_ARG, "paged eviction: dst_table is page_table (NULL moves in place)");
+  const int64_t ints = batch->n_requests * 4ll, kept = ints * budget, in = ((batch->n_requests - 1) * score_stride + batch->max_len) * 4;
+  const int64_t out = score_out ? ((batch->n_requests - 1) * score_out_stride + most) * 4 : 0;
   if (score_out) {
     if (misaligned(score_out, 4) || score_out_stride < most)
       return refuse(BD_ERR_INVALID_ARG, "paged eviction: score_out's rows must hold min(budget, max_len) entries");
-    const int64_t in = ((batch->n_requests - 1) * score_stride + batch->max_len) * 4;
-    const int64_t out = ((batch->n_requests - 1) * score_out_stride + most) * 4;
     if (score_out == score ? score_out_stride != score_stride : overlap(score, in, score_out, out))
       return refuse(BD_ERR_INVALID_ARG, "paged eviction: score_out must be score (same stride) or not overlap it");
   }
+  if ((len_out != batch->seq_len && overlap(len_out, ints, batch->seq_len, ints)) || overlap(kept_out, kept, batch->seq_len, ints) ||
+      overlap(kept_out, kept, len_out, ints) || overlap(kept_out, kept, score, in) || overlap(kept_out, kept, score_out, out) ||
+      overlap(len_out, ints, score, in) || overlap(len_out, ints, score_out, out))
+    return refuse(BD_ERR_INVALID_ARG, "paged eviction: kept_out, len_out (but for seq_len itself), seq_len, score and score_out overlap");
   PagedEvictArgs A = {};
   A.p = args_of(kv, batch);
   A.score = score;

@@ -534,7 +534,8 @@ bd_status bd_paged_weights(const bd_paged_kv *kv, const bd_paged_batch *batch, c
  *              request of the call reads; or NULL: in place, in the pages of page_table, of which
  *              a request that loses slots must not share any it moves slots in
  *   kept_out   dev int32 [n_requests, budget] OUT (ascending)
- *   len_out    dev int32 [n_requests] OUT; may be seq_len itself
+ *   len_out    dev int32 [n_requests] OUT; may be seq_len itself; kept_out, len_out and the scores do
+ *              not overlap otherwise
  *   score_out  dev fp32 [n_requests, score_out_stride] OUT (score_out_stride >= min(budget,
  *              max_len)); or NULL; may be score itself, with the same stride
  */

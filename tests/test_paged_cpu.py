@@ -132,6 +132,17 @@ def test_bad_append_weights_and_eviction_arguments_are_refused(B):
         assert evict(**kw) == -1 and msg in L.bd_last_error(), kw
 
 
+def test_an_evictions_outputs_do_not_overlap(B):
+    L, kv, bt = B.lib(), _kv(B), _batch(B)               # 2 requests, seq_len at 0x31000; 400 bytes of scores each
+    for kept, n, so, sos in ((0x80000, 0x31004, None, 0),            # the lengths, shifted
+                             (0x80000, 0x30ffc, None, 0), (0x80000, 0x80000, None, 0), (0x80000, 0x8018c, None, 0),
+                             (0x31000 - 396, 0x90000, None, 0),      # the last kept slot is the first length
+                             (0x70100, 0x90000, None, 0), (0x80000, 0x70004, None, 0),
+                             (0x80000, 0x90000, 0x80100, 50), (0x80000, 0xa0004, 0xa0000, 50)):
+        assert L.bd_paged_evict(kv, bt, 0x70000, 100, 50, 1, 1, None, 0, kept, n, so, sos, None) == -1, hex(kept)
+        assert b"overlap" in L.bd_last_error()
+
+
 def test_pools_whose_slots_overlap_are_not_stored_to(B):
     L, bt = B.lib(), _batch(B)
     evict = lambda kv: L.bd_paged_evict(kv, bt, 0x70000, 100, 50, 1, 1, None, 0, 0x80000, 0x90000, None, 0, None)
