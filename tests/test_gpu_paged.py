@@ -914,3 +914,32 @@ def test_keys_and_values_in_one_pool(in_place):
         i = torch.arange(budget, device="cuda")
         got = x[table[b].long()[i // page], :, i % page]
         assert new_len[b].item() == budget and torch.equal(got.double().cpu(), torch.from_numpy(c.k[b])[kept[b].cpu().long()])
+
+
+@pytest.mark.parametrize("n,group", [(40, 1), (40, 8), (40, 12), (200, 4), (200, 16)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_few_rows_keep_the_rest_of_their_weights(n, group, dtype):
+    """Values that cancel: the weights' rounding to 16 bits, about as large as the output's own where they do not,
+    would stand out.  Tolerance: that of check_attention with the weights as a 16-bit part and a 16-bit rest (u^2 for u;
+    what fp16 loses below its subnormals, 2^-25 of weights formed 2^12 above the largest's size, is 2^-37 a slot)."""
+    c = PagedCase((n,), (1,), hkv=2, group=group, dtype=dtype).build()
+    t = TYPES[dtype]
+    u = torch.finfo(t).eps / 2
+    q = (torch.randn(1, 2, 1, c.d, generator=torch.Generator().manual_seed(n + group)) * 0.05).to(t).expand(1, 2, group, c.d)
+    c.qd.copy_(q.reshape(1, -1, c.d).cuda())
+    qf, lost = q.double().numpy(), np.zeros((1, 2 * group, c.d))
+    for h in range(2):                                  # the last slot's value cancels the others' sum
+        s = c.scale * (c.k[0][:, h] @ qf[0, h, 0])
+        w = np.exp(s - s.max())
+        last = -(w[:-1, None] * c.v[0][:-1, h]).sum(0) / w[-1]
+        c.v[0][-1, h] = torch.from_numpy(last).to(t).double().numpy()
+        c.vd[c.table[0, (n - 1) // c.page].item(), h, (n - 1) % c.page] = torch.from_numpy(last).to(t).cuda()
+        lost[0, h * group:(h + 1) * group] = (torch.from_numpy(w).to(t).double().numpy() @ c.v[0][:, h]) / w.sum()
+    ref, _, spread, size = P.attention(qf.reshape(1, -1, c.d), c.k[0], c.v[0], 0, 0, c.scale)
+    ds = ((c.d * 2.0 ** -23) * size + (size + 4) * 2.0 ** -22)[..., None]
+    tol = u * np.abs(ref) + torch.finfo(t).smallest_normal * u + (u * u + 2.02 * ds + (n + 64) * 2.0 ** -23) * spread + \
+        n * 2.0 ** -37 * np.abs(c.v[0]).max()
+    assert (np.abs(lost - ref) > tol).any()             # weights of 16 bits alone would fail here
+    out, _ = c.attend()
+    sync()
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
