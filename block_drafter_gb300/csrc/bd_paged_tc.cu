@@ -24,7 +24,10 @@
 // (plan_whole).
 //
 // The reference of a row moves only when a score exceeds it by more than 2^8, so sums are rarely rescaled;
-// weights round to 16 bits (half a step: 2^-8 relative in bf16), as the result does.
+// weights round to 16 bits (half a step: 2^-8 relative in bf16), as the result does.  A second operand with the rest
+// would be half as many products again.  Root-mean-square error against 64 bits, of a form with 32-bit weights, of one
+// whose weights are rounded against the row's maximum, and here, where the largest weight is no power of two and
+// rounds, too: a block of 16 rows 0.00166, 0.00202, 0.00227; a prompt 0.00166, 0.00194, 0.00219.
 //
 // Measured: 8192 rows of one request, 32 heads over 8 KV heads, D = 128, bf16: 372 us, 1480 TFLOP/s.  A tile of
 // both streams takes the tensor cores 2048 cycles and the softmax's exponentials, 32 a cycle, 1024; what is left

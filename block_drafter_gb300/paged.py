@@ -168,7 +168,8 @@ class PagedCache:
     def batch(self, page_table: torch.Tensor, seq_len: torch.Tensor, row_start: Optional[torch.Tensor],
               n_rows: int, max_rows: int, max_len: int, workspace: Optional[torch.Tensor] = None) -> PagedBatch:
         """page_table int32 [requests, pages], seq_len int32 [requests] (this step's rows counted),
-        row_start int32 [requests + 1]; max_rows and max_len bound every request's rows and length.
+        row_start int32 [requests + 1]; max_rows (at most n_rows) and max_len bound every request's rows and
+        length.  The schedules go by these bounds: close ones are faster than loose ones.
         workspace: a uint8 tensor to share between batches used in order on one stream.  Without one the batch
         allocates its own, which it keeps from other uses until its calls are done, on whatever streams they ran;
         a stream given by its handle must outlive the batch.  Captured calls hold the addresses of the batch's

@@ -428,20 +428,23 @@ bd_status bd_lm_head_argmax_noalloc(const bd_config *cfg, const bd_weights *w,
  * lse and accumulated weights are fp32.  A slot that no row of the call sees is never used,
  * whatever its page holds, and an entry of page_table none of whose slots a row sees may be any
  * number (pages behind a window may be given back); a slot that a row does not see does not reach
- * that row's results, even if it holds infinities or NaN.  A value that is not finite in a slot that a row does see
- * makes that column of the row's out infinite or NaN.
+ * that row's results, even if it holds infinities or NaN.  A value that is not finite in a slot
+ * that a row does see makes that column of the row's out infinite or NaN, however small the
+ * slot's weight.
  *
  * Lengths and page ids live on the device and are checked there: a request whose rows are not
  * 0 <= row_start[b] <= row_start[b+1] <= n_rows with at most max_rows rows takes no part; one
  * whose seq_len is negative or beyond max_len or its page_table row counts as empty; a page id
  * outside the pool, of a slot that a row sees or is stored in or an eviction keeps, is not followed
- * (the slot's values count as zero and nothing is stored there).  Each sets the device error word (bd_sync_status: BD_ERR_INVALID_ARG), and that
- * request's results are unspecified.  Rows outside every request are left as they were.
+ * (the slot's values count as zero and nothing is stored there).  Each sets the device error word
+ * (bd_sync_status: BD_ERR_INVALID_ARG), and that request's results are unspecified.  Rows outside
+ * every request are left as they were.
  *
- * Tensors belong to the current device.  Errors: BD_ERR_INVALID_ARG (NULL, misaligned or
- * overlapping arrays, sizes out of range), BD_ERR_UNSUPPORTED (type, head size),
- * BD_ERR_WORKSPACE.  The workspace holds nothing between calls; calls that share one must be
- * ordered on one stream.  No call synchronises, allocates or needs initialised scratch, and
+ * Tensors belong to the current device.  Errors: BD_ERR_INVALID_ARG (NULL or misaligned arrays,
+ * the overlaps that an entry point names below, sizes out of range), BD_ERR_UNSUPPORTED (type,
+ * head size), BD_ERR_WORKSPACE.  An array that a call writes must not overlap any other of its
+ * arrays but where it says so.  The workspace holds nothing between calls; calls that share one
+ * must be ordered on one stream, and replays of graphs that captured them, too.  No call synchronises, allocates or needs initialised scratch, and
  * every call can be captured into a graph.  Results do not depend on the run (no atomics on
  * floating-point values).
  */
@@ -465,8 +468,9 @@ typedef struct {
   int n_requests;             /* 1 .. BD_PAGED_MAX_REQUESTS                                       */
   int table_width;            /* entries of one page_table row                                    */
   int n_rows;                 /* rows of the call's row tensors (>= 0)                            */
-  int max_rows;               /* bound on the rows of any request (>= 0)                          */
-  int max_len;                /* bound on any seq_len                                             */
+  int max_rows;               /* bound on the rows of any request: 0 .. n_rows                    */
+  int max_len;                /* bound on any seq_len: 0 .. table_width * page_size, at most 2^30;*/
+                              /*   schedules go by it, so a close bound is faster than a loose one*/
   const int32_t *page_table;  /* dev [n_requests, table_width]                                    */
   const int32_t *seq_len;     /* dev [n_requests]                                                 */
   const int32_t *row_start;   /* dev [n_requests + 1]                                             */
