@@ -27,7 +27,9 @@ EXPORTS = ("bd_abi_version", "bd_workspace_bytes", "bd_ctx_kv_materialize", "bd_
            "bd_packed_bytes", "bd_pack_weights", "bd_lm_head_argmax_noalloc", "bd_lm_head_topk",
            "bd_refine_tail", "bd_head_fp8_bytes", "bd_pack_head_fp8", "bd_lm_head_topk_fp8",
            "bd_selftest_wait", "bd_set_timing_events", "bd_paged_workspace_bytes", "bd_paged_append",
-           "bd_paged_attention", "bd_paged_weights", "bd_paged_evict")
+           "bd_paged_attention", "bd_paged_weights", "bd_paged_evict", "bd_paged_plan",
+           "bd_paged4_workspace_bytes", "bd_paged4_append", "bd_paged4_attention",
+           "bd_head_norm_rope", "bd_token_logprobs")
 
 TOPK_MAX = 16
 
@@ -87,6 +89,32 @@ class PagedBatch(C.Structure):
                 ("max_rows", C.c_int), ("max_len", C.c_int), ("page_table", C.c_void_p),
                 ("seq_len", C.c_void_p), ("row_start", C.c_void_p)]
 
+
+class PagedPages(C.Structure):
+    _fields_ = [("n_requests", C.c_int), ("table_width", C.c_int), ("page_size", C.c_int),
+                ("n_free", C.c_int), ("page_table", C.c_void_p), ("held", C.c_void_p),
+                ("held_out", C.c_void_p), ("free_pages", C.c_void_p), ("free_count", C.c_void_p),
+                ("free_count_out", C.c_void_p)]
+
+
+class Paged4Kv(C.Structure):
+    _fields_ = [("n_q_heads", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("dtype", C.c_int), ("page_size", C.c_int), ("n_pages", C.c_int),
+                ("k_exp", C.c_int), ("v_exp", C.c_int), ("page_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("slot_stride", C.c_int64),
+                ("scale_page_stride", C.c_int64), ("scale_head_stride", C.c_int64),
+                ("scale_slot_stride", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
+class HeadRope(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("head_dim", C.c_int), ("rotary_dim", C.c_int),
+                ("interleaved", C.c_int), ("n_q_heads", C.c_int), ("n_kv_heads", C.c_int),
+                ("eps", C.c_float), ("q_gain", C.c_void_p), ("k_gain", C.c_void_p),
+                ("turns", C.c_void_p)]
+
+
+LOGPROB_TOP_MAX, LOGPROB_GIVEN_MAX = 32, 64
 
 _lib = None
 
@@ -151,6 +179,20 @@ def lib() -> C.CDLL:
         L.bd_paged_weights.argtypes = [kvp, btp, vp, i64, vp, vp, i, i, f, f, vp, vp, i64, vp]
         L.bd_paged_evict.restype = i
         L.bd_paged_evict.argtypes = [kvp, btp, vp, i64, i, i, i, vp, i, vp, vp, vp, i64, vp]
+        L.bd_paged_plan.restype = i
+        L.bd_paged_plan.argtypes = [C.POINTER(PagedPages), vp, vp, i, i, vp, vp, vp, vp, vp, vp, vp]
+        kv4 = C.POINTER(Paged4Kv)
+        L.bd_paged4_workspace_bytes.restype = sz
+        L.bd_paged4_workspace_bytes.argtypes = [kv4, i, i, i]
+        L.bd_paged4_append.restype = i
+        L.bd_paged4_append.argtypes = [kv4, btp, vp, i64, vp, i64, vp, vp, vp]
+        L.bd_paged4_attention.restype = i
+        L.bd_paged4_attention.argtypes = [kv4, btp, vp, i64, vp, i64, vp, i, i, f, vp, sz, vp]
+        L.bd_head_norm_rope.restype = i
+        L.bd_head_norm_rope.argtypes = [C.POINTER(HeadRope), i, vp, vp, i64, vp, i64, vp, i64, vp,
+                                        i64, vp]
+        L.bd_token_logprobs.restype = i
+        L.bd_token_logprobs.argtypes = [vp, i64, i, i, i, f, vp, i, vp, vp, vp, i, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -372,6 +414,47 @@ def paged_evict(kv: PagedKv, batch: PagedBatch, score: int, score_stride: int, b
                 len_out: int, score_out: Optional[int], score_out_stride: int, stream: int):
     _check(lib().bd_paged_evict(kv, batch, score, score_stride, budget, n_sink, n_recent, dst_table,
                                 dst_width, kept, len_out, score_out, score_out_stride, stream))
+
+
+def paged_plan(pages: PagedPages, length: int, n_new: int, give_back: int, n_rows: int, seq_len: int,
+               row_start: int, row_request: Optional[int], row_pos: int, slot_map: int,
+               n_short: Optional[int], stream: int):
+    _check(lib().bd_paged_plan(pages, length, n_new, give_back, n_rows, seq_len, row_start,
+                               row_request, row_pos, slot_map, n_short, stream))
+
+
+def paged4_workspace_bytes(kv: Paged4Kv, n_requests: int, max_rows: int, max_len: int) -> int:
+    n = lib().bd_paged4_workspace_bytes(C.byref(kv), n_requests, max_rows, max_len)
+    if n == 0:
+        raise BdError(-1, lib().bd_last_error().decode())
+    return n
+
+
+def paged4_append(kv: Paged4Kv, batch: PagedBatch, k_new: int, k_stride: int, v_new: int,
+                  v_stride: int, k_held: Optional[int], v_held: Optional[int], stream: int):
+    _check(lib().bd_paged4_append(kv, batch, k_new, k_stride, v_new, v_stride, k_held, v_held, stream))
+
+
+def paged4_attention(kv: Paged4Kv, batch: PagedBatch, q: int, q_stride: int, out: int,
+                     out_stride: int, lse: Optional[int], window: int, n_sink: int, scale: float,
+                     workspace: int, workspace_nbytes: int, stream: int):
+    _check(lib().bd_paged4_attention(kv, batch, q, q_stride, out, out_stride, lse, window, n_sink,
+                                     scale, workspace, workspace_nbytes, stream))
+
+
+def head_norm_rope(c: HeadRope, n_rows: int, pos: int, q: int, q_stride: int, k: int, k_stride: int,
+                   q_out: int, q_out_stride: int, k_out: int, k_out_stride: int, stream: int):
+    _check(lib().bd_head_norm_rope(c, n_rows, pos, q, q_stride, k, k_stride, q_out, q_out_stride,
+                                   k_out, k_out_stride, stream))
+
+
+def token_logprobs(logits: int, row_stride: int, dtype: int, rows: int, vocab: int,
+                   temperature: float, tokens: Optional[int], n_given: int, logprob: Optional[int],
+                   entropy: Optional[int], lse: Optional[int], top_k: int, top_ids: Optional[int],
+                   top_logprob: Optional[int], stream: int):
+    _check(lib().bd_token_logprobs(logits, row_stride, dtype, rows, vocab, temperature, tokens,
+                                   n_given, logprob, entropy, lse, top_k, top_ids, top_logprob,
+                                   stream))
 
 
 TIME_KINDS = {"qkv": 1, "attention": 2, "wo": 3, "gate_up": 4, "down": 5, "bridge": 6, "head": 7}

@@ -1199,7 +1199,7 @@ bd_status bd_sync_status(void *stream_) {
   if (e != cudaSuccess) return fail(BD_ERR_CUDA, std::string("stream: ") + cudaGetErrorString(e));
   const unsigned word = take_error_word_gemm() | take_error_word_att() | take_error_word_small() |
                         take_error_word_pack() | take_error_word_head8() | take_error_word_bridge() |
-                        take_error_words_paged();
+                        take_error_words_paged() | take_error_words_target();
   if (word & DEVERR_TIMEOUT) return fail(BD_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up");
   if (word & DEVERR_BAD_INDEX)
     return fail(BD_ERR_INVALID_ARG, "a device-side index (token id, request or position) was out of range");
@@ -1208,6 +1208,8 @@ bd_status bd_sync_status(void *stream_) {
   if (word & DEVERR_F16)
     return fail(BD_ERR_RANGE, "an activation stored as an fp16 operand was beyond the fp16 range "
                               "(|x| > 65504) or not finite");
+  if (word & DEVERR_4BIT)
+    return fail(BD_ERR_RANGE, "a key or value was beyond the 4-bit cache's range (|x| > 2688 * 2^exp) or not finite");
   return BD_OK;
 }
 

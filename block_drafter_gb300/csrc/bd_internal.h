@@ -14,8 +14,9 @@ namespace bd {
 
 // Device error word flags (set by kernels, read and cleared by bd_sync_status()).
 // DEVERR_RANGE: a weight beyond the fp16 range met the packed image's fp16 conversion;
-// DEVERR_F16: an activation beyond the fp16 range (or not finite) met an fp16 operand store.
-enum : unsigned { DEVERR_TIMEOUT = 1u, DEVERR_BAD_INDEX = 2u, DEVERR_RANGE = 4u, DEVERR_F16 = 8u };
+// DEVERR_F16: an activation beyond the fp16 range (or not finite) met an fp16 operand store;
+// DEVERR_4BIT: a key or value beyond the 4-bit cache's range (or not finite) was appended.
+enum : unsigned { DEVERR_TIMEOUT = 1u, DEVERR_BAD_INDEX = 2u, DEVERR_RANGE = 4u, DEVERR_F16 = 8u, DEVERR_4BIT = 16u };
 // One translation unit's word: read, and cleared only where it is set.  Each is a blocking copy of a
 // few microseconds, and a status call takes the words of all units.
 template <typename Read, typename Write> unsigned take_if_set(Read read, Write write) {

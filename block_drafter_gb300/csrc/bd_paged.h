@@ -151,4 +151,12 @@ unsigned take_error_word_paged_wt();
 unsigned take_error_word_paged_attn();
 unsigned take_error_word_paged_tc();
 
+// The same of the kernels of a step's tables, 4-bit cache and target rows; set before their first launch or capture.
+void use_target_kernels();
+unsigned take_error_words_target();
+unsigned take_error_word_paged_plan();
+unsigned take_error_word_paged4();
+unsigned take_error_word_paged4_attn();
+unsigned take_error_word_logprobs();
+
 }  // namespace bd

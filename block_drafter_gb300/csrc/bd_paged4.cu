@@ -1,0 +1,429 @@
+// Paged K/V cache in 4 bits: the entry points' checks, the append, and the 16-bit copy that calls of many
+// rows read.
+#include "bd_paged4.cuh"
+
+#include "bd_checks.h"
+#include "bd_paged_attn.cuh"
+
+namespace bd {
+
+BD_DEFINE_ERROR_TAKER(take_error_word_paged4)
+
+// ------------------------------------------------------------------ append
+// A thread takes groups of 16 values (32 bytes in, 9 out), kAppend4Each of them on their way while the block finds
+// its rows' requests and slots.  The codes are exact without a division: x / s is formed as x (1/s), off by about
+// 2^-23, and rounded to fp16's 11 bits before it is rounded to a code.  A border between two codes is a middle g
+// (3 bits) times s (4 bits): a value of at most 11 bits that is not g s is off it by more than 2^-12, further than
+// either error, and one that is becomes g itself, the tie.  Bound by the bytes.
+namespace {
+
+constexpr int kAppend4Threads = 256;
+constexpr int kAppend4Rows = 32;
+constexpr int kAppend4Each = 2;
+
+struct Paged4AppendArgs {
+  Paged4Args c;
+  const uint16_t *k_new, *v_new;
+  int64_t k_stride, v_stride;
+  uint16_t *k_held, *v_held;
+  int rows_per_cta;
+};
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(byte)));
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(d)));
+}
+
+struct Group4 {
+  uint32_t codes[2], scale;
+};
+// 16 values (two a word) to their codes and scale; down: 2^-exp.
+template <typename T> __device__ __forceinline__ Group4 encode16(const uint32_t (&w)[8], float down, bool &bad) {
+  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+  const float most = Pair<T>::unpack(top).x * down;
+  Group4 g = {{0, 0}, 0};
+  if (top >= kInf) {
+    bad = true;
+    return g;
+  }
+  bad |= most > 2688.f;
+  g.scale = e4m3x2(__fdiv_rn(most, 6.f), 0.f) & 0xffu;
+  const float s = e4m3_value(g.scale);
+  if (s == 0.f) {
+    g.scale = 0;
+    return g;
+  }
+  const float f = __frcp_rn(s) * down;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = Pair<T>::unpack(w[i]);
+    const float2 y = Pair<__half>::unpack(Pair<__half>::pack(x.x * f, x.y * f));
+    g.codes[i / 4] |= e2m1_codes(y.x, y.y) << (i % 4 * 8);
+  }
+  return g;
+}
+
+// The values that a group stands for, in T (exact: 2 bits times 4).
+template <typename T> __device__ __forceinline__ void decode16(const Group4 &g, float up, uint32_t (&w)[8]) {
+  const float s = e4m3_value(g.scale) * up;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t p[4];
+    e2m1_pairs(g.codes[i], p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = Pair<__half>::unpack(p[j]);
+      w[i * 4 + j] = Pair<T>::pack(x.x * s, x.y * s);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAppend4Threads) paged4_append_kernel(const __grid_constant__ Paged4AppendArgs A) {
+  const PagedArgs &a = A.c.p;
+  __shared__ Place4 place[kAppend4Rows];  // of the row's slot, code -1: not stored
+  __shared__ int2 slot[kAppend4Rows];     // the row's request and slot (negative: none)
+  const int r0 = blockIdx.x * A.rows_per_cta, r1 = min(a.n_rows, r0 + A.rows_per_cta);
+  const uint32_t per_head = a.head_dim / 16, per_side = a.n_kv_heads * per_head, per_row = 2 * per_side;
+  const int groups = (r1 - r0) * per_row;
+  if (threadIdx.x < kAppend4Rows) slot[threadIdx.x] = make_int2(0, -1);
+  pdl_wait();
+  pdl_trigger();
+  uint4 v[kAppend4Each][2];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int u = 0; u < kAppend4Each; ++u) {
+      const uint32_t c = c0 + u * kAppend4Threads, r = c / per_row, x = c - r * per_row;
+      if (static_cast<int>(c) >= groups) continue;
+      const uint4 *src = reinterpret_cast<const uint4 *>(x < per_side ? A.k_new + (r0 + r) * A.k_stride + x * 16
+                                                                      : A.v_new + (r0 + r) * A.v_stride + (x - per_side) * 16);
+      v[u][0] = __ldcs(src);
+      v[u][1] = __ldcs(src + 1);
+    }
+  };
+  load(threadIdx.x);
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.n_requests; b += kAppend4Threads) {
+    const int s = a.row_start[b], e = a.row_start[b + 1], n = request_len(a, b);
+    if (s < 0 || e < s || e > a.n_rows || e - s > a.max_rows) {
+      atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+      continue;
+    }
+    for (int r = max(s, r0); r < min(e, r1); ++r) slot[r - r0] = make_int2(b, n - (e - r));
+  }
+  __syncthreads();
+  if (threadIdx.x < kAppend4Rows) {
+    const int2 p = slot[threadIdx.x];
+    Place4 at = {-1, -1};
+    if (p.y >= 0) at = place4(A.c, __ldg(a.page_table + static_cast<int64_t>(p.x) * a.table_width + p.y / a.page_size), p.y);
+    place[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const float k_down = pow2(-A.c.k_exp), v_down = pow2(-A.c.v_exp), k_up = pow2(A.c.k_exp), v_up = pow2(A.c.v_exp);
+  for (int c0 = threadIdx.x; c0 < groups; c0 += kAppend4Each * kAppend4Threads) {
+    if (c0 != static_cast<int>(threadIdx.x)) load(c0);
+#pragma unroll
+    for (int u = 0; u < kAppend4Each; ++u) {
+      const uint32_t c = c0 + u * kAppend4Threads, r = c / per_row, x = c - r * per_row;
+      if (static_cast<int>(c) >= groups) continue;
+      const Place4 to = place[r];
+      if (to.code < 0) continue;
+      const bool key = x < per_side;
+      const uint32_t w = key ? x : x - per_side, h = w / per_head, i = w - h * per_head;
+      const uint32_t in[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+      bool bad = false;
+      const Group4 g = encode16<T>(in, key ? k_down : v_down, bad);
+      if (bad) atomicOr(&g_error_word, DEVERR_4BIT);
+      uint8_t *codes = static_cast<uint8_t *>(const_cast<void *>(key ? a.k : a.v));
+      uint8_t *scales = static_cast<uint8_t *>(const_cast<void *>(key ? A.c.k_scale : A.c.v_scale));
+      *reinterpret_cast<uint2 *>(codes + to.code + h * a.head_stride + i * 8) = make_uint2(g.codes[0], g.codes[1]);
+      scales[to.scale + h * A.c.scale_head_stride + i] = static_cast<uint8_t>(g.scale);
+      uint16_t *held = key ? A.k_held : A.v_held;
+      if (held) {
+        uint32_t o[8];
+        decode16<T>(g, key ? k_up : v_up, o);
+        uint4 *dst = reinterpret_cast<uint4 *>(held + (static_cast<int64_t>(r0 + r) * per_side + w) * 16);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+  }
+}
+
+std::string launch_append4(Paged4AppendArgs &A, int dtype, cudaStream_t s) {
+  // as many rows as its threads' first groups cover, while two blocks an SM are left
+  const int groups = 2 * A.c.p.n_kv_heads * A.c.p.head_dim / 16;
+  A.rows_per_cta = 1;
+  while (2 * A.rows_per_cta <= kAppend4Rows && 2 * A.rows_per_cta * groups <= kAppend4Each * kAppend4Threads &&
+         A.c.p.n_rows >= 4 * A.rows_per_cta * num_sms())
+    A.rows_per_cta *= 2;
+  const int grid = (A.c.p.n_rows + A.rows_per_cta - 1) / A.rows_per_cta;
+  const cudaError_t e = launch_pdl(dtype == BD_BF16 ? paged4_append_kernel<__nv_bfloat16> : paged4_append_kernel<__half>, dim3(grid),
+                                   dim3(kAppend4Threads), 0, s, A);
+  return e == cudaSuccess ? std::string() : std::string("paged 4-bit append: ") + cudaGetErrorString(e);
+}
+
+// ------------------------------------------------------------------ the 16-bit copy
+// Calls of many rows use each slot often (a prompt of 8192 rows and group 4 reads every tile 128 times): its values are
+// worked out once into pages of kWideSlots slots of a pool in the workspace, which the 16-bit attention reads.
+// A block takes the keys or values of one head's kWideSlots slots, a thread 32 codes at a time.
+constexpr int kWideSlots = 128;
+constexpr int kWideThreads = 256;
+
+struct WidenArgs {
+  Paged4Args c;
+  uint16_t *k, *v;      // [requests * pages][KV heads][kWideSlots][D]
+  int32_t *table;       // [requests][pages]
+  int pages;            // of a request
+};
+
+template <typename T, int D> __global__ void __launch_bounds__(kWideThreads) paged4_widen_kernel(const __grid_constant__ WidenArgs A) {
+  constexpr int P = D / 32;  // 16-byte pieces of a slot's codes
+  const PagedArgs &a = A.c.p;
+  const int page = blockIdx.x, b = blockIdx.z, h = blockIdx.y >> 1, side = blockIdx.y & 1;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0 && blockIdx.y == 0) A.table[b * A.pages + page] = b * A.pages + page;
+  const Request rq = request_of(a, b);
+  const int j0 = page * kWideSlots, f_low = window_first(a, max(0, rq.n - rq.rows));
+  if (rq.rows == 0 || j0 >= rq.n || !any_seen(a, j0, kWideSlots, f_low, rq.n - 1)) return;
+  const uint8_t *codes = static_cast<const uint8_t *>(side ? a.v : a.k) + h * a.head_stride;
+  const uint8_t *scales = static_cast<const uint8_t *>(side ? A.c.v_scale : A.c.k_scale) + h * A.c.scale_head_stride;
+  uint16_t *dst = (side ? A.v : A.k) + ((static_cast<int64_t>(b) * A.pages + page) * a.n_kv_heads + h) * kWideSlots * D;
+  const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+  const float up = pow2(side ? A.c.v_exp : A.c.k_exp);
+#pragma unroll
+  for (int u = 0; u < kWideSlots * P / kWideThreads; ++u) {
+    const int x = u * kWideThreads + threadIdx.x, r = x / P, i = x - r * P, j = j0 + r;
+    Place4 at = {-1, -1};  // slots that no row sees are zeros: no value of a tile is not finite
+    if (j < rq.n && any_seen(a, j, 1, f_low, rq.n - 1)) at = place4(A.c, __ldg(table + j / a.page_size), j);
+    Group4 g[2] = {};
+    if (at.code >= 0) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(codes + at.code) + i);
+      const uint32_t s = __ldg(reinterpret_cast<const uint16_t *>(scales + at.scale) + i);
+      // the code of a NaN reads as 448
+      auto finite = [](uint32_t s) { return (s & 0x7f) == 0x7f ? 0x7eu : s; };
+      g[0] = {{w.x, w.y}, finite(s & 0xff)};
+      g[1] = {{w.z, w.w}, finite(s >> 8)};
+    }
+    uint4 *to = reinterpret_cast<uint4 *>(dst + r * D + i * 32);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t o[8];
+      decode16<T>(g[e], up, o);
+      to[2 * e] = make_uint4(o[0], o[1], o[2], o[3]);
+      to[2 * e + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+std::string launch_widen(const WidenArgs &A, int dtype, cudaStream_t s) {
+  const PagedArgs &a = A.c.p;
+  const dim3 grid(A.pages, 2 * a.n_kv_heads, a.n_requests), block(kWideThreads);
+  cudaError_t e;
+  if (dtype == BD_BF16)
+    e = launch_pdl(a.head_dim == 128 ? paged4_widen_kernel<__nv_bfloat16, 128> : paged4_widen_kernel<__nv_bfloat16, 64>, grid, block, 0, s, A);
+  else
+    e = launch_pdl(a.head_dim == 128 ? paged4_widen_kernel<__half, 128> : paged4_widen_kernel<__half, 64>, grid, block, 0, s, A);
+  return e == cudaSuccess ? std::string() : std::string("paged 4-bit attention: ") + cudaGetErrorString(e);
+}
+
+// ------------------------------------------------------------------ host
+struct WideSizes {
+  int64_t pages;  // of a request
+  size_t attention, table, pool;
+  size_t all() const { return attention + table + 2 * pool; }
+};
+WideSizes wide_sizes(const bd_paged4_kv *c, int n_requests, int max_rows, int max_len) {
+  WideSizes w;
+  w.pages = max_len > 0 ? (static_cast<int64_t>(max_len) + kWideSlots - 1) / kWideSlots : 1;
+  w.attention = align256(many_bytes(n_requests, max_rows, c->n_q_heads / c->n_kv_heads, c->head_dim));
+  w.table = align256(static_cast<size_t>(n_requests) * w.pages * 4);
+  w.pool = align256(static_cast<size_t>(n_requests) * w.pages * c->n_kv_heads * kWideSlots * c->head_dim * 2);
+  return w;
+}
+bool is_few(const bd_paged4_kv *c, int max_rows) { return static_cast<int64_t>(max_rows) * (c->n_q_heads / c->n_kv_heads) <= kFewRows4; }
+
+bd_status check_kv4(const bd_paged4_kv *c) {
+  if (!c) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv is NULL");
+  if (c->dtype != BD_BF16 && c->dtype != BD_F16)
+    return refuse(BD_ERR_UNSUPPORTED, "paged 4-bit kv: dtype must be BD_BF16 or BD_F16");
+  if (c->head_dim != 64 && c->head_dim != 128) return refuse(BD_ERR_UNSUPPORTED, "paged 4-bit kv: head_dim must be 64 or 128");
+  if (bd_status st = check_heads(c->n_q_heads, c->n_kv_heads)) return st;
+  if (c->page_size < 1 || c->n_pages < 1) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv: page_size and n_pages must be >= 1");
+  const int low = c->dtype == BD_BF16 ? -64 : -14, high = c->dtype == BD_BF16 ? 64 : 4;
+  if (c->k_exp < low || c->k_exp > high || c->v_exp < low || c->v_exp > high)
+    return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv: k_exp and v_exp must be in -64..64 (BD_BF16) or -14..4 (BD_F16)");
+  const int codes = c->head_dim / 2, scales = c->head_dim / 16;
+  if (!c->k || !c->v || misaligned(c->k, 16) || misaligned(c->v, 16))
+    return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv: k and v must be 16-byte aligned pools");
+  if (!c->k_scale || !c->v_scale || misaligned(c->k_scale, scales) || misaligned(c->v_scale, scales))
+    return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv: k_scale and v_scale must be pools aligned to head_dim / 16 bytes");
+  for (int64_t s : {c->page_stride, c->head_stride, c->slot_stride})
+    if (s < 0 || s % 16) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv: strides must be multiples of 16 bytes, >= 0");
+  for (int64_t s : {c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride})
+    if (s < 0 || s % scales) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv: scale strides must be multiples of head_dim / 16 bytes, >= 0");
+  if ((c->page_size > 1 && (c->slot_stride < codes || c->scale_slot_stride < scales)) ||
+      (c->n_kv_heads > 1 && (c->head_stride < codes || c->scale_head_stride < scales)) ||
+      (c->n_pages > 1 && (c->page_stride < codes || c->scale_page_stride < scales)))
+    return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv: strides must be at least a slot's codes (head_dim / 2) or scales (head_dim / 16)");
+  return BD_OK;
+}
+bd_status check_batch4(const bd_paged4_kv *c, const bd_paged_batch *t) {
+  if (bd_status st = check_kv4(c)) return st;
+  return check_paged_batch(c->page_size, t, true);
+}
+
+Paged4Args args_of(const bd_paged4_kv *c, const bd_paged_batch *t) {
+  use_target_kernels();
+  Paged4Args a = {};
+  a.p.k = c->k;
+  a.p.v = c->v;
+  a.p.page_stride = c->page_stride;
+  a.p.head_stride = c->head_stride;
+  a.p.slot_stride = c->slot_stride;
+  a.p.n_kv_heads = c->n_kv_heads;
+  a.p.group = c->n_q_heads / c->n_kv_heads;
+  a.p.head_dim = c->head_dim;
+  a.p.page_size = c->page_size;
+  a.p.n_pages = c->n_pages;
+  set_batch(a.p, t);
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.scale_page_stride = c->scale_page_stride;
+  a.scale_head_stride = c->scale_head_stride;
+  a.scale_slot_stride = c->scale_slot_stride;
+  a.k_exp = c->k_exp;
+  a.v_exp = c->v_exp;
+  return a;
+}
+
+}  // namespace
+}  // namespace bd
+
+using namespace bd;
+
+extern "C" {
+
+size_t bd_paged4_workspace_bytes(const bd_paged4_kv *kv, int n_requests, int max_rows, int max_len) {
+  if (check_kv4(kv)) return 0;
+  if (n_requests < 1 || n_requests > BD_PAGED_MAX_REQUESTS || max_rows < 0 || max_len < 0 || max_len > (1 << 30)) {
+    refuse(BD_ERR_INVALID_ARG, "paged 4-bit workspace: n_requests must be in 1..1024, max_rows >= 0 and max_len in 0..2^30");
+    return 0;
+  }
+  // a batch made for many rows may hold few: the larger of the two
+  const size_t few = few4_bytes(kv->head_dim);
+  if (is_few(kv, max_rows)) return few;
+  const size_t many = wide_sizes(kv, n_requests, max_rows, max_len).all();
+  return few > many ? few : many;
+}
+
+bd_status bd_paged4_append(const bd_paged4_kv *kv, const bd_paged_batch *batch, const void *k_new, int64_t k_stride,
+                           const void *v_new, int64_t v_stride, void *k_held, void *v_held, void *stream) {
+  if (bd_status st = check_batch4(kv, batch)) return st;
+  if (batch->n_rows == 0) return BD_OK;
+  const int64_t width = static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim;
+  if (bd_status st = check_rows(k_new, k_stride, width, batch->n_rows, "k_new")) return st;
+  if (bd_status st = check_rows(v_new, v_stride, width, batch->n_rows, "v_new")) return st;
+  const int codes = kv->head_dim / 2, scales = kv->head_dim / 16;
+  const void *pools[4] = {kv->k, kv->v, kv->k_scale, kv->v_scale};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(pools[i], i < 2 ? codes : scales, pools[j], j < 2 ? codes : scales))
+        return refuse(BD_ERR_INVALID_ARG, "paged 4-bit append: the slots of the pools overlap");
+  const int64_t held = batch->n_rows * width * 2;
+  const void *ins[2] = {k_new, v_new};
+  void *outs[2] = {k_held, v_held};
+  const int64_t strides[2] = {k_stride, v_stride};
+  for (int i = 0; i < 2; ++i) {
+    if (!outs[i]) continue;
+    if (misaligned(outs[i], 16)) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit append: k_held and v_held must be 16-byte aligned");
+    for (int j = 0; j < 2; ++j) {
+      const bool own = i == j && outs[i] == ins[j] && (strides[j] == width || batch->n_rows == 1);
+      if (!own && overlap(outs[i], held, ins[j], row_bytes(strides[j], width, batch->n_rows)))
+        return refuse(BD_ERR_INVALID_ARG, "paged 4-bit append: k_held or v_held overlaps rows that are not its own");
+    }
+  }
+  if (k_held && v_held && overlap(k_held, held, v_held, held))
+    return refuse(BD_ERR_INVALID_ARG, "paged 4-bit append: k_held and v_held overlap");
+  Paged4AppendArgs A = {};
+  A.c = args_of(kv, batch);
+  A.k_new = static_cast<const uint16_t *>(k_new);
+  A.v_new = static_cast<const uint16_t *>(v_new);
+  A.k_stride = k_stride;
+  A.v_stride = v_stride;
+  A.k_held = static_cast<uint16_t *>(k_held);
+  A.v_held = static_cast<uint16_t *>(v_held);
+  return ran(launch_append4(A, kv->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+bd_status bd_paged4_attention(const bd_paged4_kv *kv, const bd_paged_batch *batch, const void *q, int64_t q_stride, void *out,
+                              int64_t out_stride, float *lse, int window, int n_sink, float scale, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+  if (bd_status st = check_batch4(kv, batch)) return st;
+  if (bd_status st = check_mask(window, n_sink, scale)) return st;
+  if (batch->max_rows == 0) return BD_OK;
+  const int64_t width = static_cast<int64_t>(kv->n_q_heads) * kv->head_dim;
+  if (bd_status st = check_rows(q, q_stride, width, batch->n_rows, "q")) return st;
+  if (bd_status st = check_rows(out, out_stride, width, batch->n_rows, "out")) return st;
+  if (overlap(q, row_bytes(q_stride, width, batch->n_rows), out, row_bytes(out_stride, width, batch->n_rows)))
+    return refuse(BD_ERR_INVALID_ARG, "paged 4-bit attention: q and out overlap");
+  if (misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit attention: lse misaligned");
+  const int group = kv->n_q_heads / kv->n_kv_heads;
+  const WideSizes w = wide_sizes(kv, batch->n_requests, batch->max_rows, batch->max_len);
+  if ((static_cast<int64_t>(batch->max_len) / 16 + 8) * kv->n_kv_heads >= (1ll << 31) ||
+      static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30) ||
+      (static_cast<int64_t>(batch->max_rows) * group / 256 + 1) * batch->n_requests > (1 << 28) ||
+      (!is_few(kv, batch->max_rows) && (w.pages * batch->n_requests > (1 << 30) || 2 * kv->n_kv_heads > 65535)))
+    return refuse(BD_ERR_UNSUPPORTED, "paged 4-bit attention: max_len * n_kv_heads, max_rows * n_q_heads, n_requests * max_rows or "
+                                      "n_requests * max_len too large");
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < bd_paged4_workspace_bytes(kv, batch->n_requests, batch->max_rows, batch->max_len))
+    return refuse(BD_ERR_WORKSPACE, "paged 4-bit attention: workspace NULL, not 256-byte aligned or too small");
+  Paged4Args a = args_of(kv, batch);
+  a.p.q = q;
+  a.p.q_stride = q_stride;
+  a.p.window = window;
+  a.p.n_sink = n_sink;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (is_few(kv, batch->max_rows)) {
+    Paged4AttnArgs A = {};
+    A.c = a;
+    A.c.p.scale_log2 = static_cast<float>(std::ldexp(scale * 1.4426950408889634, kv->k_exp));
+    A.out = out;
+    A.out_stride = out_stride;
+    A.lse = lse;
+    A.out_scale = std::ldexp(1.f, kv->v_exp);
+    return ran(launch_attention_few4(A, workspace, kv->dtype, s));
+  }
+  uint8_t *p = static_cast<uint8_t *>(workspace);
+  PagedAttnArgs A = {};
+  A.p = a.p;
+  A.p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  A.out = out;
+  A.out_stride = out_stride;
+  A.lse = lse;
+  WidenArgs W = {};
+  W.c = a;
+  W.table = reinterpret_cast<int32_t *>(p + w.attention);
+  W.k = reinterpret_cast<uint16_t *>(p + w.attention + w.table);
+  W.v = reinterpret_cast<uint16_t *>(p + w.attention + w.table + w.pool);
+  W.pages = static_cast<int>(w.pages);
+  if (bd_status st = ran(launch_widen(W, kv->dtype, s))) return st;
+  A.p.k = W.k;
+  A.p.v = W.v;
+  A.p.page_size = kWideSlots;
+  A.p.slot_stride = kv->head_dim;
+  A.p.head_stride = static_cast<int64_t>(kWideSlots) * kv->head_dim;
+  A.p.page_stride = A.p.head_stride * kv->n_kv_heads;
+  A.p.n_pages = W.pages * batch->n_requests;
+  A.p.page_table = W.table;
+  A.p.table_width = W.pages;
+  return ran(launch_attention_many(A, workspace, kv->dtype, s));
+}
+
+}  // extern "C"

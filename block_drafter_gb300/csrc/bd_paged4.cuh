@@ -1,0 +1,53 @@
+// Device helpers of the 4-bit cache: slots' places, codes and scales to fp16 pairs.
+#pragma once
+#include "bd_paged4.h"
+#include "bd_paged_device.cuh"
+
+namespace bd {
+
+// Byte offsets of slot j (KV head 0) in the code and the scale pools where it lies in `page`; code -1 (flagged)
+// where that is no page of the pool.
+struct Place4 {
+  int64_t code, scale;
+};
+__device__ __forceinline__ Place4 place4(const Paged4Args &c, int page, int j) {
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.p.n_pages)) {
+    atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+    return {-1, -1};
+  }
+  const int in_page = j % c.p.page_size;
+  return {page * c.p.page_stride + in_page * c.p.slot_stride, page * c.scale_page_stride + in_page * c.scale_slot_stride};
+}
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
+
+// The four bytes of w as fp16 pairs, the low half's value first (exact).
+__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+// Two values (lo in the low half) to the nearest codes, ties to the even one.
+__device__ __forceinline__ uint32_t e2m1_codes(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Two scales (bytes) as fp16; a NaN's code is 448, so that whatever bytes a hidden slot holds are numbers.
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t two) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(two)));
+  asm("min.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x5f005f00u));  // min of a NaN and 448: 448
+  return d;
+}
+
+}  // namespace bd

@@ -1,0 +1,34 @@
+// Paged K/V cache in 4 bits: arguments its kernels share.
+#pragma once
+#include "bd_paged.h"
+
+namespace bd {
+
+// One layer's pools and one batch.  p.k and p.v are the code pools, p's strides are theirs in bytes.
+struct Paged4Args {
+  PagedArgs p;
+  const void *k_scale, *v_scale;
+  int64_t scale_page_stride, scale_head_stride, scale_slot_stride;  // bytes
+  int k_exp, v_exp;
+};
+
+struct Paged4AttnArgs {
+  Paged4Args c;
+  void *out;
+  int64_t out_stride;
+  float *lse;  // [n_rows][n_q_heads] or null
+  float out_scale;  // 2^v_exp
+  // as PagedAttnArgs'
+  PagedJoin *join;
+  float *part_o;
+  float2 *part_ml;
+  int n_ctas, whole, cluster;
+};
+
+// Query rows (of one KV head) of the kernel that reads the codes themselves.
+constexpr int kFewRows4 = 16;
+
+size_t few4_bytes(int head_dim);
+std::string launch_attention_few4(Paged4AttnArgs A, void *workspace, int dtype, cudaStream_t s);
+
+}  // namespace bd

@@ -1,0 +1,614 @@
+// Attention of few rows over a 4-bit cache (bd_paged4_attention with at most kFewRows4 rows of a KV head:
+// decoding and short blocks).
+//
+// The scheme is the 16-bit kernel's -- one pass with the running maximum and sum, units of 16 slots shared out evenly or a
+// cluster a head, every warp alone on every fourth unit -- but what bounds it is not only the bytes (0.5625 a
+// value): each value has to be unpacked and scaled, so the products are laid out for that.
+//   * Slots are the M side of both products (mma.sync m16n8k16, fp16): S^T = K Q^T and O^T = V^T P^T.  The rows of a
+//     KV head are the N side, 8 at a time, so that a token's few rows fill what they use and half as many products
+//     are issued as with the rows on the M side.
+//   * The order of the D products of a score and of a slot's places in the second product is free.  So a lane loads
+//     16 consecutive bytes of each of its two slots (32 values, every fragment of its column group) and, of the
+//     values, 8 bytes of each of four slots (16 values, every fragment of its row group): straight from the pools into
+//     the registers they are unpacked from, kAhead units early; nothing passes through shared memory.
+//   * Codes become fp16 pairs by conversion and are multiplied by the group's scale: exact (2 bits times 4), so
+//     that both products run on exactly the values that the slots stand for.  A value pair is two slots of one
+//     column: their nibbles are brought side by side first.
+//   * The queries are fp16 for both types: a bf16 row is scaled by a power of two that brings its largest value to
+//     2^8, which keeps every value down to 2^-25 of that exact and the rest to 2^-33 of it.
+//   * Weights are fp16 against a reference that moves only when a score exceeds it by 2^8 and is then the maximum:
+//     so no maximum over the lanes is taken but then.  They round to 2^-12 relative, a sixteenth of half a bf16
+//     step; for fp16 rows the rest goes into a second product.
+#include "bd_paged4.cuh"
+#include "bd_paged_attn.cuh"
+
+namespace bd {
+
+BD_DEFINE_ERROR_TAKER(take_error_word_paged4_attn)
+
+namespace {
+
+constexpr int kAhead = 2;     // units of a warp on their way
+constexpr float kHead = 6.f;  // weights are formed against 2^-kHead of the reference: at most 2^14
+constexpr float kMove = 8.f;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+// Both halves of a scale pair's low or high half.
+__device__ __forceinline__ uint32_t twice_lo(uint32_t s) { return __byte_perm(s, s, 0x1010); }
+__device__ __forceinline__ uint32_t twice_hi(uint32_t s) { return __byte_perm(s, s, 0x3232); }
+
+// What a lane holds of a unit.  Lane: quad = lane / 4, kq = lane % 4.
+template <int D> struct Frag {
+  static constexpr int W = D / 64;  // words of a lane's piece of a value slot (2 of a key slot's W)
+  uint32_t k[2][2 * W];             // slots quad, quad + 8: bytes kq * D/8 ..
+  uint32_t v[4][W];                 // slots 2kq, 2kq + 1, 2kq + 8, 2kq + 9: bytes quad * D/16 ..
+  uint32_t ks[2];                   // scales of the key pieces (W bytes)
+  uint32_t vs[4];                   // scale of the value pieces
+};
+
+template <int N> __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
+  if constexpr (N == 4) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+  }
+}
+
+// The part of one (request, KV head) over tiles [t0, t1) by one warp (every kFewWarps-th tile).
+// o[i]: columns (quad * 8W + 2i, + 1) (halves 0, 1 and 2, 3) of rows 8n + 2kq, + 1; m, l: of those rows.
+template <typename T, int D, int NT>
+struct FewWarp4 {
+  static constexpr int W = D / 64, NK = D / 16, NV = D / 16;
+  static constexpr bool kRest = std::is_same<T, __half>::value;
+  float o[NT][NV][4];
+  float m[NT][2], l[NT][2];
+
+  __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int t0, int t1, int warp,
+                                      int lane) {
+    const Paged4Args &c4 = A.c;
+    const PagedArgs &a = c4.p;
+    const int quad = lane >> 2, kq = lane & 3;
+    const int R = rq.rows * a.group;
+    // queries: B fragments of row 8n + quad, and the factor of rows 8n + 2kq, + 1 from products to scores in log2 units
+    uint32_t q[NT][NK][2];
+    float to_log2[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + quad, i = r < R ? r / a.group : 0;
+      const T *src = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + (h * a.group + (r < R ? r - i * a.group : 0)) * D + kq * (D / 4);
+      uint32_t raw[NK][2];
+#pragma unroll
+      for (int t = 0; t < NK; t += 2) {
+        const uint4 x = r < R ? *reinterpret_cast<const uint4 *>(src + t * 4) : make_uint4(0, 0, 0, 0);
+        raw[t][0] = x.x, raw[t][1] = x.y, raw[t + 1][0] = x.z, raw[t + 1][1] = x.w;
+      }
+      int e = 0;  // the row's power of two
+      if constexpr (!kRest) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) top = max(top, max(raw[t][y] & 0x7fffu, raw[t][y] >> 16 & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^8 <= largest < 2^9; infinities and NaN stay what they are
+        if (top >= 0x0080u && top < 0x7f80u) e = min(126, 127 + 8 - static_cast<int>(top >> 7));
+        const float f = pow2(e);
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float2 x = Pair<T>::unpack(raw[t][y]);
+            q[n][t][y] = Pair<__half>::pack(x.x * f, x.y * f);
+          }
+      } else {
+#pragma unroll
+        for (int t = 0; t < NK; ++t) q[n][t][0] = raw[t][0], q[n][t][1] = raw[t][1];
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) to_log2[n][y] = a.scale_log2 * pow2(-__shfl_sync(0xffffffffu, e, 4 * (2 * kq + y)));
+    }
+    // what rows 8n + 2kq, + 1 see: slots <= p, from f on or among the sinks
+    int p[NT][2], f[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = 8 * n + 2 * kq + y;
+        p[n][y] = r < R ? rq.n - rq.rows + r / a.group : -1;
+        f[n][y] = p[n][y] >= 0 ? window_first(a, p[n][y]) : 0;
+        m[n][y] = -INFINITY;
+        l[n][y] = 0.f;
+      }
+    const int p_low = rq.n - rq.rows, f_high = window_first(a, rq.n - 1), f_low = window_first(a, max(0, p_low));
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+
+    const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
+    const uint8_t *K = static_cast<const uint8_t *>(a.k) + h * a.head_stride + kq * (D / 8);
+    const uint8_t *V = static_cast<const uint8_t *>(a.v) + h * a.head_stride + quad * (D / 16);
+    const uint8_t *KS = static_cast<const uint8_t *>(c4.k_scale) + h * c4.scale_head_stride + kq * W;
+    const uint8_t *VS = static_cast<const uint8_t *>(c4.v_scale) + h * c4.scale_head_stride + quad * W / 2;
+    // page of slot lane % 16 of tile t (the load alone), then the slot's place, -1 for a slot no row sees
+    auto page_of = [&](int t) { return __ldg(table + min(tl.at(max(min(t, t1 - 1), 0)) * kUnit + (lane & 15), rq.n - 1) / a.page_size); };
+    auto load = [&](Frag<D> &x, int t, int page) {
+      if (t >= t1) return;
+      const int j = tl.at(t) * kUnit + (lane & 15);
+      Place4 at = {-1, -1};
+      if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, page, j);
+      auto of = [&](int slot, int64_t &code, int64_t &scale) {
+        code = __shfl_sync(0xffffffffu, at.code, slot);
+        scale = __shfl_sync(0xffffffffu, at.scale, slot);
+      };
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        int64_t code, scale;
+        of(quad + 8 * y, code, scale);
+        if (code >= 0) {
+          load_words(x.k[y], K + code);
+          if constexpr (W == 2) x.ks[y] = __ldg(reinterpret_cast<const uint16_t *>(KS + scale));
+          else x.ks[y] = __ldg(KS + scale);
+        } else {
+#pragma unroll
+          for (int w = 0; w < 2 * W; ++w) x.k[y][w] = 0;
+          x.ks[y] = 0;
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        int64_t code, scale;
+        of(2 * kq + (y & 1) + 8 * (y >> 1), code, scale);
+        if (code >= 0) {
+          load_words(x.v[y], V + code);
+          x.vs[y] = __ldg(VS + scale);
+        } else {
+#pragma unroll
+          for (int w = 0; w < W; ++w) x.v[y][w] = 0;
+          x.vs[y] = 0;
+        }
+      }
+    };
+    auto work = [&](const Frag<D> &x, int t) {
+      // scores of slots quad (+ 8), rows 8n + 2kq (+ 1)
+      float c[NT][4] = {};
+      {
+        uint32_t s0 = scales_f16x2(x.ks[0]), s1 = scales_f16x2(x.ks[1]);
+#pragma unroll
+        for (int w = 0; w < 2 * W; ++w) {
+          const uint32_t f0 = w < 2 ? twice_lo(s0) : twice_hi(s0), f1 = w < 2 ? twice_lo(s1) : twice_hi(s1);
+          uint32_t k0[4], k1[4];
+          e2m1_pairs(x.k[0][w], k0);
+          e2m1_pairs(x.k[1][w], k1);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            k0[y] = mul_f16x2(k0[y], f0);
+            k1[y] = mul_f16x2(k1[y], f1);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(c[n], k0[2 * y], k1[2 * y], k0[2 * y + 1], k1[2 * y + 1], q[n][2 * w + y][0], q[n][2 * w + y][1]);
+        }
+      }
+      const int j0 = tl.at(t) * kUnit;
+      const bool masked = !(j0 + kUnit - 1 <= p_low && (j0 >= f_high || j0 + kUnit <= a.n_sink));  // some row does not see all of it
+      bool moves = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          c[n][e] *= to_log2[n][e & 1];
+          if (masked) {
+            const int j = j0 + quad + 8 * (e >> 1);
+            if (!(j <= p[n][e & 1] && (j >= f[n][e & 1] || j < a.n_sink))) c[n][e] = -INFINITY;
+          }
+          moves |= c[n][e] > m[n][e & 1] + kMove;
+        }
+      if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float mx = fmaxf(m[n][y], fmaxf(c[n][y], c[n][y + 2]));
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+            const float w = m[n][y] == mx ? 1.f : exp2_fast(m[n][y] - mx);
+            m[n][y] = mx;
+            l[n][y] *= w;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+              o[n][i][y] *= w;
+              o[n][i][y + 2] *= w;
+            }
+          }
+      }
+      // weights: B fragments of the second product
+      uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kHead, r1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kHead;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float w0 = exp2_fast(c[n][2 * y] - r0), w1 = exp2_fast(c[n][2 * y + 1] - r1);
+          const uint32_t hv = Pair<__half>::pack(w0, w1);
+          hi[n][y] = transpose8x8(hv);
+          if constexpr (kRest) {
+            const float2 back = Pair<__half>::unpack(hv);
+            lo[n][y] = transpose8x8(Pair<__half>::pack(w0 - back.x, w1 - back.y));
+          }
+          l[n][0] += w0;
+          l[n][1] += w1;
+        }
+      }
+      {
+        const uint32_t s0 = scales_f16x2(x.vs[0] | x.vs[1] << 8), s1 = scales_f16x2(x.vs[2] | x.vs[3] << 8);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          // nibbles of two slots side by side: even columns, odd columns
+          const uint32_t even0 = (x.v[0][w] & 0x0f0f0f0fu) | (x.v[1][w] << 4 & 0xf0f0f0f0u), odd0 = (x.v[0][w] >> 4 & 0x0f0f0f0fu) | (x.v[1][w] & 0xf0f0f0f0u);
+          const uint32_t even1 = (x.v[2][w] & 0x0f0f0f0fu) | (x.v[3][w] << 4 & 0xf0f0f0f0u), odd1 = (x.v[2][w] >> 4 & 0x0f0f0f0fu) | (x.v[3][w] & 0xf0f0f0f0u);
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          e2m1_pairs(even0, a0);
+          e2m1_pairs(odd0, a1);
+          e2m1_pairs(even1, a2);
+          e2m1_pairs(odd1, a3);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t b0 = mul_f16x2(a0[y], s0), b1 = mul_f16x2(a1[y], s0), b2 = mul_f16x2(a2[y], s1), b3 = mul_f16x2(a3[y], s1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(o[n][w * 4 + y], b0, b1, b2, b3, hi[n][0], hi[n][1]);
+              if constexpr (kRest) mma_f16(o[n][w * 4 + y], b0, b1, b2, b3, lo[n][0], lo[n][1]);
+            }
+          }
+        }
+      }
+    };
+    // unit i of the warp is tile t0 + warp + i * kFewWarps; fragments of kAhead units are on their way
+    Frag<D> x[kAhead];
+    int page[kAhead];
+    int t = t0 + warp;
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) page[s] = page_of(t + s * kFewWarps);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) load(x[s], t + s * kFewWarps, page[s]);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) page[s] = page_of(t + (kAhead + s) * kFewWarps);
+    while (t < t1) {
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        if (t >= t1) break;
+        work(x[s], t);
+        load(x[s], t + kAhead * kFewWarps, page[s]);
+        page[s] = page_of(t + 2 * kAhead * kFewWarps);
+        t += kFewWarps;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) l[n][y] += __shfl_xor_sync(0xffffffffu, l[n][y], s);
+        if (m[n][y] != -INFINITY) m[n][y] -= kHead;  // the reference the sums are against
+      }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void finish(const Paged4AttnArgs &A, const Request &rq, int h, int r, int d, float4 o, float m, float l) {
+  const int g = A.c.p.group, i = r / g, head = h * g + r - i * g;
+  const float inv = l == 0.f ? 0.f : A.out_scale / l;
+  T *out = static_cast<T *>(A.out) + (rq.row0 + i) * A.out_stride + head * A.c.p.head_dim + d;
+  *reinterpret_cast<uint2 *>(out) = make_uint2(Pair<T>::pack(o.x * inv, o.y * inv), Pair<T>::pack(o.z * inv, o.w * inv));
+  if (d == 0 && A.lse) A.lse[static_cast<int64_t>(rq.row0 + i) * A.c.p.n_kv_heads * g + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+}
+// Rows of a request without a slot: zeros.
+template <typename T, int D> __device__ void no_slots(const Paged4AttnArgs &A, const Request &rq, int tid, int step) {
+  PagedAttnArgs x;
+  x.p = A.c.p;
+  x.out = A.out;
+  x.out_stride = A.out_stride;
+  x.lse = A.lse;
+  empty_rows<T, D>(x, rq, rq.rows, tid, step);
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(const __grid_constant__ Paged4AttnArgs A) {
+  constexpr int ROWS = 8 * NT;
+  __shared__ __align__(16) float so[kFewWarps][ROWS][D + 4];  // the warps' sums
+  __shared__ int64_t start[BD_PAGED_MAX_REQUESTS + 1];
+  __shared__ int64_t warp_sum_s[kFewWarps];
+  __shared__ Request first[kFewThreads];
+  __shared__ float2 ml[kFewWarps][ROWS];
+  __shared__ __align__(8) float2 block_ml[ROWS];  // of a cluster's block, its sums in place of its first warp's
+  const PagedArgs &a = A.c.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.x;
+  int64_t units = 0, u = 0, u1 = 1;
+  int ctas = 1;
+  if (!A.whole) {
+    scan_requests<kFewThreads>(a, start, warp_sum_s, first);
+    units = start[a.n_requests];
+    ctas = ctas_used(units, a.n_requests * a.n_kv_heads, A.n_ctas);
+    for (int b = g; b < a.n_requests; b += gridDim.x)
+      if (start[b + 1] == start[b]) no_slots<T, D>(A, request_of(a, b), tid, kFewThreads);
+    if (tid == 0) A.join[g].np = 0;
+    if (units == 0 || g >= ctas) return;
+    u = share_begin(units, ctas, g);
+    u1 = share_begin(units, ctas, g + 1);
+  }
+  do {
+    int b, h, t0, t1;
+    Request rq;
+    Tiles tl;
+    if (A.whole) {  // one head, or a cluster's block's part of one
+      const int item = g / static_cast<uint32_t>(A.cluster), rank = g - item * A.cluster;
+      b = item / a.n_kv_heads;
+      h = item - b * a.n_kv_heads;
+      rq = request_of(a, b);
+      tl = tiles_of(a, rq);
+      t0 = tl.count * rank / A.cluster;
+      t1 = tl.count * (rank + 1) / A.cluster;
+      u = t0;
+      u1 = t1;
+      if (tl.count == 0) {
+        if (h == 0 && rank == 0) no_slots<T, D>(A, rq, tid, kFewThreads);
+        return;
+      }
+    } else {
+      b = request_at(start, a.n_requests, u);
+      rq = b < kFewThreads ? first[b] : request_of(a, b);
+      tl = tiles_of(a, rq);
+      const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
+      h = in / static_cast<uint32_t>(tl.count);
+      t0 = in - h * tl.count;
+      t1 = static_cast<int>(u1 - u < tl.count - t0 ? t0 + (u1 - u) : tl.count);
+    }
+    const int R = rq.rows * a.group;
+    {
+      FewWarp4<T, D, NT> w;
+      w.run(A, rq, tl, b, h, t0, t1, warp, lane);
+      const int quad = lane >> 2, kq = lane & 3;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int r = 8 * n + 2 * kq + y;
+          float *to = &so[warp][r][quad * (D / 8)];
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 2)
+            *reinterpret_cast<float4 *>(to + 2 * i) = make_float4(w.o[n][i][y], w.o[n][i][y + 2], w.o[n][i + 1][y], w.o[n][i + 1][y + 2]);
+          if (quad == 0) ml[warp][r] = make_float2(w.m[n][y], w.l[n][y]);
+        }
+    }
+    const bool whole = t0 == 0 && t1 == tl.count;
+    const int64_t slot = (2 * g + (t0 > 0 ? 0 : 1)) * kFewRows4;
+    if (tid == 0 && !A.whole && t0 > 0 && share_begin(units, ctas, g - 1) <= u - t0)  // the first block to begin inside this head
+      A.join[g] = {b, h, 0, R, share_owner(units, ctas, u - t0 + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
+    __syncthreads();
+    for (int c = tid; c < R * (D / 4); c += kFewThreads) {  // join the warps
+      const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
+      float2 x[kFewWarps];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFewWarps; ++i) {
+        x[i] = ml[i][r];
+        M = fmaxf(M, x[i].x);
+      }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kFewWarps; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(&so[i][r][d]);
+        const float w = x[i].y == 0.f ? 0.f : exp2f(x[i].x - M);
+        L += w * x[i].y;
+        o.x += w * v.x;
+        o.y += w * v.y;
+        o.z += w * v.z;
+        o.w += w * v.w;
+      }
+      if (A.cluster > 1) {
+        *reinterpret_cast<float4 *>(&so[0][r][d]) = o;
+        if (d == 0) block_ml[r] = make_float2(M, L);
+      } else if (whole) {
+        finish<T>(A, rq, h, r, d, o, M, L);
+      } else {
+        *reinterpret_cast<float4 *>(A.part_o + (slot + r) * D + d) = o;
+        if (d == 0) A.part_ml[slot + r] = make_float2(M, L);
+      }
+    }
+    if (A.cluster > 1) {  // the blocks' parts: a warp takes every kth row
+      __syncwarp();
+      cluster_sync();
+      const int rank = g % static_cast<uint32_t>(A.cluster), d = lane * 4;
+      for (int r = rank + A.cluster * warp; r < R; r += A.cluster * kFewWarps) {
+        float4 v[kMostCluster];
+        const uint32_t at = smem_u32(&so[0][r][d % D]);
+#pragma unroll
+        for (int i = 0; i < kMostCluster; ++i)
+          if (i < A.cluster) v[i] = ld_cluster_f4(cluster_map(at, i));
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (lane < A.cluster) {
+          const uint32_t y = cluster_map(smem_u32(block_ml + r), lane);
+          x = make_float2(ld_cluster_f32(y), ld_cluster_f32(y + 4));
+        }
+        const float M = warp_max(x.x), w = x.y == 0.f ? 0.f : exp2f(x.x - M), L = warp_sum(w * x.y);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kMostCluster; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          if (i < A.cluster) {
+            o.x += wi * v[i].x;
+            o.y += wi * v[i].y;
+            o.z += wi * v[i].z;
+            o.w += wi * v[i].w;
+          }
+        }
+        if (d < D) finish<T>(A, rq, h, r, d, o, M, L);
+      }
+      __syncwarp();
+      cluster_sync();  // every block's sums are read
+      return;
+    }
+    __syncthreads();
+    u += t1 - t0;
+  } while (u < u1);
+}
+
+// ------------------------------------------------------------------ join
+// Block (g, y): rows 4y .. 4y+3 of the join that block g left, as the 16-bit kernel's: parts side by side.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinHeld = 10;  // parts of a thread in registers
+constexpr int kJoinRows = 4;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_constant__ Paged4AttnArgs A) {
+  __shared__ float weight[kJoinRows][kJoinParts];
+  __shared__ float2 row_ml[kJoinRows];
+  __shared__ float4 sums[kJoinThreads];
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const PagedJoin j = A.join[g];
+  const int r0 = blockIdx.y * kJoinRows, n = min(j.n - r0, kJoinRows);
+  if (j.np == 0 || n <= 0) return;
+  const Request rq = {j.len, j.row0, j.rows};
+  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * kFewRows4 + r0; };
+  const int pieces = n * (D / 4);  // at most kJoinThreads
+  const int groups = kJoinThreads / pieces, k = tid / pieces, c = tid - k * pieces;
+  const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
+  // this thread's first parts are on their way while the weights are worked out
+  float4 held[kJoinHeld];
+#pragma unroll
+  for (int x = 0; x < kJoinHeld; ++x) {
+    const int i = k + x * groups;
+    if (k < groups && i < j.np) held[x] = __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d));
+  }
+  if (warp < n) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < j.np; i += 32) {
+      const float2 x = __ldcg(A.part_ml + slot(i) + warp);
+      const float mn = x.y == 0.f ? m : fmaxf(m, x.x);
+      l = (l == 0.f ? 0.f : l * exp2f(m - mn)) + (x.y == 0.f ? 0.f : x.y * exp2f(x.x - mn));
+      m = mn;
+      weight[warp][i] = x.y == 0.f ? -INFINITY : x.x;
+    }
+    const float M = warp_max(m), L = warp_sum(l == 0.f ? 0.f : l * exp2f(m - M));
+    for (int i = lane; i < j.np; i += 32) weight[warp][i] = M == -INFINITY ? 0.f : exp2f(weight[warp][i] - M);
+    if (lane == 0) row_ml[warp] = make_float2(M, L);
+  }
+  __syncthreads();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int i, const float4 &v) {
+    const float w = weight[r][i];
+    o.x += w * v.x;
+    o.y += w * v.y;
+    o.z += w * v.z;
+    o.w += w * v.w;
+  };
+  if (k < groups) {
+#pragma unroll
+    for (int x = 0; x < kJoinHeld; ++x)
+      if (k + x * groups < j.np) add(k + x * groups, held[x]);
+#pragma unroll 4
+    for (int i = k + kJoinHeld * groups; i < j.np; i += groups)
+      add(i, __ldcg(reinterpret_cast<const float4 *>(A.part_o + (slot(i) + r) * D + d)));
+  }
+  if (groups > 1) {
+    sums[tid] = o;
+    __syncthreads();
+    if (k == 0)
+      for (int i = 1; i < groups; ++i) {
+        const float4 v = sums[tid + i * pieces];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+  }
+  if (k == 0) finish<T>(A, rq, j.h, r0 + r, d, o, row_ml[r].x, row_ml[r].y);
+}
+static_assert(kJoinRows * 128 / 4 <= kJoinThreads, "a block's pieces");
+
+// ------------------------------------------------------------------ host
+constexpr int kWholeSlots = 512;
+constexpr int kBlockSlots = 64;
+constexpr int kClusterSlots = 1088, kClusterFilled = 2176;
+constexpr int kJoinSlots = 800, kPartSlots = 2;
+constexpr int kBlocksPerSm = 2;
+
+int few4_blocks() { return kBlocksPerSm * num_sms() < kJoinParts ? kBlocksPerSm * num_sms() : kJoinParts - 1; }
+
+template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
+  const PagedArgs &a = A.c.p;
+  auto kernel = attention_few4<T, D, NT>;
+  static const ClustersAtOnce fit(kernel, kFewThreads, 0);
+  const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
+  int blocks = 1;
+  while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
+  const bool alike = seen < a.max_len || a.n_requests == 1;
+  const int64_t each = (seen + blocks - 1) / blocks, share = heads * seen / A.n_ctas;  // a block's slots, either way
+  if (blocks == 1)
+    A.whole = seen <= kWholeSlots;
+  else if (alike)
+    A.whole = each <= share + kJoinSlots + kPartSlots * A.n_ctas / heads || (heads * blocks >= num_sms() && each <= kClusterFilled);
+  else
+    A.whole = each <= kClusterSlots;
+  A.cluster = A.whole ? blocks : 1;
+  if (A.whole) {
+    const cudaError_t c = allow_cluster(kernel, blocks);
+    if (c != cudaSuccess) return c;
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(heads * blocks)), dim3(kFewThreads), 0, s, blocks, A);
+  }
+  const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), 0, s, A);
+  if (f != cudaSuccess) return f;
+  const int rows = a.max_rows * a.group;
+  return launch_pdl(attention_join4<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
+}
+template <typename T, int D> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
+  return A.c.p.max_rows * A.c.p.group <= 8 ? launch<T, D, 1>(A, s) : launch<T, D, 2>(A, s);
+}
+
+}  // namespace
+
+size_t few4_bytes(int head_dim) {
+  const size_t parts = 2 * static_cast<size_t>(few4_blocks()) * kFewRows4;
+  return align256(few4_blocks() * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
+}
+
+std::string launch_attention_few4(Paged4AttnArgs A, void *workspace, int dtype, cudaStream_t s) {
+  uint8_t *p = static_cast<uint8_t *>(workspace);
+  A.n_ctas = few4_blocks();
+  const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows4;
+  A.join = reinterpret_cast<PagedJoin *>(p);
+  p += align256(A.n_ctas * sizeof(PagedJoin));
+  A.part_o = reinterpret_cast<float *>(p);
+  p += align256(parts * A.c.p.head_dim * 4);
+  A.part_ml = reinterpret_cast<float2 *>(p);
+  cudaError_t e;
+  if (dtype == BD_BF16)
+    e = A.c.p.head_dim == 128 ? launch<__nv_bfloat16, 128>(A, s) : launch<__nv_bfloat16, 64>(A, s);
+  else
+    e = A.c.p.head_dim == 128 ? launch<__half, 128>(A, s) : launch<__half, 64>(A, s);
+  return e == cudaSuccess ? std::string() : std::string("paged 4-bit attention: ") + cudaGetErrorString(e);
+}
+
+}  // namespace bd

@@ -170,4 +170,72 @@ __device__ void empty_rows(const PagedAttnArgs &A, const Request &rq, int rows, 
   }
 }
 
+// ------------------------------------------------------------------ few rows: units and shares
+constexpr int kUnit = 16;  // slots of a unit
+constexpr int kFewWarps = 4;
+constexpr int kFewThreads = 32 * kFewWarps;
+// The slots some row of a request sees, as tiles of kUnit: the sinks' tiles, then those from the
+// earliest row's window on.
+struct Tiles {
+  int sinks, first, count;  // tiles of sinks, first tile behind them, tiles in all
+  __device__ int at(int t) const { return t < sinks ? t : first + t - sinks; }
+};
+__device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq) {
+  Tiles t = {0, 0, 0};
+  if (rq.rows == 0 || rq.n == 0) return t;
+  const int first = window_first(a, max(0, rq.n - rq.rows));
+  t.first = first / kUnit;
+  t.sinks = min((min(a.n_sink, first) + kUnit - 1) / kUnit, t.first);
+  t.count = t.sinks + (rq.n + kUnit - 1) / kUnit - t.first;
+  return t;
+}
+
+// Blocks that work: a unit for each of their four warps, but as many as there are heads (a block takes
+// its heads one after the other, about 2.5 us each).
+__device__ __forceinline__ int ctas_used(int64_t units, int heads, int most) {
+  const int64_t quarter = (units + kFewWarps - 1) >> 2, c = quarter > heads ? quarter : units < heads ? units : heads;
+  return c < 1 ? 1 : static_cast<int>(c < most ? c : most);
+}
+// start[b] = units of the requests before b; all threads of the block.
+// The first NT requests' sizes are kept in `first`.
+template <int NT>
+__device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s, Request *first) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.n_requests; b0 += NT) {
+    const int b = b0 + tid;
+    int64_t v = 0;
+    if (b < a.n_requests) {
+      const Request rq = request_of(a, b);
+      if (b0 == 0) first[tid] = rq;
+      v = static_cast<int64_t>(tiles_of(a, rq).count) * a.n_kv_heads;
+    }
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum_s[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) x += warp_sum_s[w];
+    }
+    if (b < a.n_requests) start[b + 1] = base + x;
+    for (int w = 0; w < NT / 32; ++w) base += warp_sum_s[w];
+    __syncthreads();
+  }
+  if (tid == 0) start[0] = 0;
+  __syncthreads();
+}
+// Request of unit u (the last one that starts at or before it and has units).
+__device__ __forceinline__ int request_at(const int64_t *start, int n, int64_t u) {
+  int lo = 0, hi = n;  // start[lo] <= u < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 }  // namespace bd

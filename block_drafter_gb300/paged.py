@@ -1,4 +1,5 @@
-"""Paged K/V cache of the target model: append, attention, accumulated weights, eviction.
+"""Paged K/V cache of the target model: append, attention, accumulated weights, eviction; the same cache
+in 4 bits; and the page tables and slot maps of a step.
 
 ``PagedCache`` wraps one layer's pools and calls the library's ``bd_paged_*`` entry points
 (``include/blockdrafter.h`` states their semantics); all computation happens in its kernels.
@@ -9,6 +10,16 @@
     cache.attention(batch, q, out, lse=lse, window=4096, n_sink=4)
     cache.weights(batch, q, lse, score, score_in=score, rows_used=accepted)
     cache.evict(batch, score, 8192, kept, new_len, n_sink=4, n_recent=512, score_out=score)
+
+``PagedCache4`` keeps keys and values in 4 bits (``bd_paged4_*``: e2m1 codes, an e4m3 scale for each 16):
+
+    cache = PagedCache4(k_codes, k_scales, v_codes, v_scales, n_q_heads=32, dtype=torch.bfloat16)
+    # codes uint8 [pages, KV heads, page size, D/2], scales [pages, KV heads, page size, D/16]
+
+and ``PageTables`` (``bd_paged_plan``) makes what a batch asks for out of the requests' lengths, on the device:
+
+    tables = PageTables(page_table, held, free_pages, free_count, page_size=64)
+    tables.plan(length, n_new, seq_len, row_start, row_pos, slot_map)
 
 A batch holds the addresses of its device arrays: a program that updates lengths, row starts
 and page tables in place keeps one batch (and its captured graphs) for many steps.  Calls run
@@ -49,6 +60,27 @@ def _need(ok: bool, msg: str):
         raise ValueError(msg)
 
 
+def _handle_of(stream, index: int) -> int:
+    """The given stream's handle, or that of a device's current one."""
+    return _current_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
+
+
+def _on(index: int, fn, *args):
+    """The library's call with the given device current."""
+    if torch.cuda.current_device() == index:
+        fn(*args)
+    else:
+        with torch.cuda.device(index):
+            fn(*args)
+
+
+def _check_ints(name: str, t: torch.Tensor, shape, index: int):
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 {list(shape)} is wanted, got {list(t.shape)} of {t.dtype}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}: the CUDA device of the other tensors is wanted")
+
+
 class PagedBatch:
     """One batch of requests; made by ``PagedCache.batch``."""
 
@@ -73,7 +105,7 @@ class PagedBatch:
         self.struct = B.PagedBatch(n, page_table.shape[1], int(n_rows), int(max_rows), int(max_len),
                                    page_table.data_ptr(), seq_len.data_ptr(),
                                    None if row_start is None else row_start.data_ptr())
-        nbytes = B.paged_workspace_bytes(cache.struct, n, int(max_rows))
+        nbytes = cache._workspace_bytes(n, int(max_rows), int(max_len))
         # Streams that the batch's own workspace is known to; None: the caller's workspace.
         self.streams = None
         if workspace is None:
@@ -98,25 +130,10 @@ class PagedBatch:
         self.streams.add(handle)
 
 
-class PagedCache:
-    """k, v: pools [pages, KV heads, page size, D] of bf16 or fp16 (any strides that are equal
-    for both, with D contiguous -- a [pages, page size, KV heads, D] pool is passed permuted)."""
+class _Cache:
+    """What both caches share: the checks of a call's tensors, batches, streams.  The checks are written
+    for their cost: a decoding step makes one call per layer."""
 
-    def __init__(self, k: torch.Tensor, v: torch.Tensor, n_q_heads: int):
-        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
-              "k and v: two pools [pages, KV heads, page size, D] of one shape, type and layout are wanted")
-        _need(k.dtype in _TYPES, f"pools of {k.dtype} are not supported")
-        _need(k.stride(3) == 1, "the D values of a slot must be contiguous")
-        self.k, self.v, self.dtype, self.device, self.index = k, v, k.dtype, k.device, k.get_device()
-        self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), k.shape[1], k.shape[3]
-        self.scale = 1.0 / math.sqrt(self.head_dim)
-        self.struct = B.PagedKv(self.n_q_heads, self.n_kv_heads, self.head_dim, _TYPES[k.dtype],
-                                k.shape[2], k.shape[0], k.stride(0), k.stride(1), k.stride(2),
-                                k.data_ptr(), v.data_ptr())
-        B.paged_workspace_bytes(self.struct, 1, 1)  # the library's checks of the pools
-        self._on_device("v", v)
-
-    # The checks of a call are written for their cost: a decoding step makes one call per layer.
     def _on_device(self, name: str, t: torch.Tensor):
         if t.get_device() != self.index or self.index < 0:
             raise ValueError(f"{name} is on {t.device}, the pools on {self.device} (a CUDA device is wanted)")
@@ -159,11 +176,19 @@ class PagedCache:
 
     def _call(self, fn, *args, stream: int):
         """The library's call on the pools' device."""
-        if torch.cuda.current_device() == self.index:
-            fn(self.struct, *args, stream)
-        else:
-            with torch.cuda.device(self.index):
-                fn(self.struct, *args, stream)
+        _on(self.index, fn, self.struct, *args, stream)
+
+    def _attention(self, fn, batch, q, out, lse, window, n_sink, scale, stream):
+        qs = self._rows("q", q, batch.q_shape)
+        os = self._rows("out", out, batch.q_shape)
+        if lse is not None:
+            self._lse(lse, batch)
+        stream = self._handle(stream)
+        if batch.streams is not None and stream not in batch.streams:
+            batch._use_on(stream)
+        self._call(fn, batch.struct, q.data_ptr(), qs, out.data_ptr(), os,
+                   None if lse is None else lse.data_ptr(), window, n_sink,
+                   self.scale if scale is None else scale, batch.ws_ptr, batch.ws_bytes, stream=stream)
 
     def batch(self, page_table: torch.Tensor, seq_len: torch.Tensor, row_start: Optional[torch.Tensor],
               n_rows: int, max_rows: int, max_len: int, workspace: Optional[torch.Tensor] = None) -> PagedBatch:
@@ -176,6 +201,28 @@ class PagedCache:
         arrays and of its workspace: keep the batch as long as their graphs are replayed."""
         return PagedBatch(self, page_table, seq_len, row_start, n_rows, max_rows, max_len, workspace)
 
+
+class PagedCache(_Cache):
+    """k, v: pools [pages, KV heads, page size, D] of bf16 or fp16 (any strides that are equal
+    for both, with D contiguous -- a [pages, page size, KV heads, D] pool is passed permuted)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, n_q_heads: int):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
+              "k and v: two pools [pages, KV heads, page size, D] of one shape, type and layout are wanted")
+        _need(k.dtype in _TYPES, f"pools of {k.dtype} are not supported")
+        _need(k.stride(3) == 1, "the D values of a slot must be contiguous")
+        self.k, self.v, self.dtype, self.device, self.index = k, v, k.dtype, k.device, k.get_device()
+        self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), k.shape[1], k.shape[3]
+        self.scale = 1.0 / math.sqrt(self.head_dim)
+        self.struct = B.PagedKv(self.n_q_heads, self.n_kv_heads, self.head_dim, _TYPES[k.dtype],
+                                k.shape[2], k.shape[0], k.stride(0), k.stride(1), k.stride(2),
+                                k.data_ptr(), v.data_ptr())
+        B.paged_workspace_bytes(self.struct, 1, 1)  # the library's checks of the pools
+        self._on_device("v", v)
+
+    def _workspace_bytes(self, n_requests: int, max_rows: int, max_len: int) -> int:
+        return B.paged_workspace_bytes(self.struct, n_requests, max_rows)
+
     def append(self, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
         """Stores the rows' keys and values ([n_rows, KV heads, D]) in their slots."""
         ks = self._rows("k_new", k_new, batch.kv_shape)
@@ -187,16 +234,7 @@ class PagedCache:
         """Attention of the rows q [n_rows, query heads, D] into out, causal, optionally through a
         sliding window beside n_sink first slots; lse float32 [n_rows, query heads] or None.
         scale: 1/sqrt(D) if None."""
-        qs = self._rows("q", q, batch.q_shape)
-        os = self._rows("out", out, batch.q_shape)
-        if lse is not None:
-            self._lse(lse, batch)
-        stream = self._handle(stream)
-        if batch.streams is not None and stream not in batch.streams:
-            batch._use_on(stream)
-        self._call(B.paged_attention, batch.struct, q.data_ptr(), qs, out.data_ptr(), os,
-                   None if lse is None else lse.data_ptr(), window, n_sink,
-                   self.scale if scale is None else scale, batch.ws_ptr, batch.ws_bytes, stream=stream)
+        self._attention(B.paged_attention, batch, q, out, lse, window, n_sink, scale, stream)
 
     def weights(self, batch: PagedBatch, q: torch.Tensor, lse: torch.Tensor, score_out: torch.Tensor,
                 score_in: Optional[torch.Tensor] = None, decay: float = 1.0,
@@ -239,3 +277,97 @@ class PagedCache:
         self._call(B.paged_evict, batch.struct, score.data_ptr(), stride, budget, n_sink, n_recent,
                    None if dst_table is None else dst_table.data_ptr(), width, kept.data_ptr(),
                    len_out.data_ptr(), None if score_out is None else score_out.data_ptr(), ostride, stream=self._handle(stream))
+
+
+class PagedCache4(_Cache):
+    """k_codes, v_codes: uint8 pools [pages, KV heads, page size, D/2]; k_scales, v_scales: pools [pages, KV heads,
+    page size, D/16] of float8_e4m3fn (or uint8).  Any strides that are equal for keys and values, with a slot's
+    bytes contiguous.  dtype: of the calls' rows (bf16 or fp16).  A group of 16 values stands for code * scale *
+    2^k_exp (2^v_exp): the exponents shift the range that is kept to the full precision, 2^-6 * 6 to 2688."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                 n_q_heads: int, dtype: torch.dtype, k_exp: int = 0, v_exp: int = 0):
+        for name, x, y, types in (("codes", k_codes, v_codes, (torch.uint8,)),
+                                  ("scales", k_scales, v_scales, (torch.float8_e4m3fn, torch.uint8))):
+            _need(x.dim() == 4 and x.shape == y.shape and x.dtype == y.dtype and x.stride() == y.stride(),
+                  f"{name}: two pools [pages, KV heads, page size, bytes] of one shape, type and layout are wanted")
+            _need(x.dtype in types, f"{name}: pools of {x.dtype} are not supported")
+            _need(x.stride(3) == 1, f"{name}: the bytes of a slot must be contiguous")
+        _need(k_scales.shape[:3] == k_codes.shape[:3] and 8 * k_scales.shape[3] == k_codes.shape[3],
+              "codes and scales: D/2 and D/16 bytes of the same slots are wanted")
+        _need(dtype in (torch.bfloat16, torch.float16), f"rows of {dtype} are not supported")
+        self.pools = (k_codes, k_scales, v_codes, v_scales)
+        self.dtype, self.device, self.index = dtype, k_codes.device, k_codes.get_device()
+        self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), k_codes.shape[1], 2 * k_codes.shape[3]
+        self.scale = 1.0 / math.sqrt(self.head_dim)
+        self.struct = B.Paged4Kv(self.n_q_heads, self.n_kv_heads, self.head_dim, _TYPES[dtype], k_codes.shape[2],
+                                 k_codes.shape[0], int(k_exp), int(v_exp), *k_codes.stride()[:3], *k_scales.stride()[:3],
+                                 k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
+        B.paged4_workspace_bytes(self.struct, 1, 1, 1)  # the library's checks of the pools
+        for name, t in zip(("k_codes", "k_scales", "v_codes", "v_scales"), self.pools):
+            self._on_device(name, t)
+
+    def _workspace_bytes(self, n_requests: int, max_rows: int, max_len: int) -> int:
+        return B.paged4_workspace_bytes(self.struct, n_requests, max_rows, max_len)
+
+    def append(self, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, k_held: Optional[torch.Tensor] = None,
+               v_held: Optional[torch.Tensor] = None, stream=None):
+        """Rounds the rows' keys and values ([n_rows, KV heads, D]) and stores them in their slots.  k_held, v_held
+        (contiguous, of the rows' shape): the values that the slots now stand for."""
+        ks = self._rows("k_new", k_new, batch.kv_shape)
+        vs = self._rows("v_new", v_new, batch.kv_shape)
+        for name, t in (("k_held", k_held), ("v_held", v_held)):
+            if t is not None:
+                self._rows(name, t, batch.kv_shape)
+                _need(t.is_contiguous(), f"{name}: a contiguous tensor is wanted")
+        self._call(B.paged4_append, batch.struct, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                   None if k_held is None else k_held.data_ptr(), None if v_held is None else v_held.data_ptr(),
+                   stream=self._handle(stream))
+
+    def attention(self, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                  window: int = 0, n_sink: int = 0, scale: Optional[float] = None, stream=None):
+        """As ``PagedCache.attention``, over the values that the slots stand for."""
+        self._attention(B.paged4_attention, batch, q, out, lse, window, n_sink, scale, stream)
+
+
+class PageTables:
+    """Page tables of up to 1024 requests and the stack of free pages.  page_table int32 [requests, entries], held int32
+    [requests] (pages that each request holds), free_pages int32 [pages of the pool] with the free ids in its first
+    free_count[0] entries.  held and free_count are brought up to date in place, or into held_out and
+    free_count_out."""
+
+    def __init__(self, page_table: torch.Tensor, held: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int,
+                 held_out: Optional[torch.Tensor] = None, free_count_out: Optional[torch.Tensor] = None):
+        held_out, free_count_out = held if held_out is None else held_out, free_count if free_count_out is None else free_count_out
+        _need(page_table.dim() == 2 and free_pages.dim() == 1, "page_table [requests, entries] and free_pages [pages] are wanted")
+        n = page_table.shape[0]
+        self.index, self.n_requests = page_table.get_device(), n
+        for name, t, shape in (("page_table", page_table, page_table.shape), ("held", held, (n,)), ("free_pages", free_pages, free_pages.shape),
+                               ("free_count", free_count, (1,)), ("held_out", held_out, (n,)), ("free_count_out", free_count_out, (1,))):
+            _check_ints(name, t, tuple(shape), self.index)
+        self.tensors = (page_table, held, free_pages, free_count, held_out, free_count_out)
+        self.struct = B.PagedPages(n, page_table.shape[1], int(page_size), free_pages.shape[0], page_table.data_ptr(), held.data_ptr(),
+                                   held_out.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr())
+
+    def plan(self, length: torch.Tensor, n_new: torch.Tensor, seq_len: torch.Tensor, row_start: torch.Tensor, row_pos: torch.Tensor,
+             slot_map: torch.Tensor, row_request: Optional[torch.Tensor] = None, n_short: Optional[torch.Tensor] = None,
+             give_back: bool = True, stream=None):
+        """Request b keeps its first length[b] slots and gets n_new[b] rows: pages beyond the need go back (give_back),
+        missing ones are taken, and seq_len [requests], row_start [requests + 1], and of each row row_request, row_pos
+        and slot_map (int64: page * page size + place; all three -1 where a row is no request's, position and slot -1
+        where its request is short of pages) are written.  All int32 but slot_map.  n_short int32 [1]: short requests."""
+        n, index = self.n_requests, self.index
+        rows = row_pos.shape[0] if row_pos.dim() == 1 else -1
+        for name, t, shape in (("length", length, (n,)), ("n_new", n_new, (n,)), ("seq_len", seq_len, (n,)), ("row_start", row_start, (n + 1,)),
+                               ("row_pos", row_pos, (rows,))):
+            if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+                _check_ints(name, t, shape, index)
+        if slot_map.dtype is not torch.int64 or slot_map.shape != (rows,) or not slot_map.is_contiguous() or slot_map.get_device() != index:
+            raise ValueError(f"slot_map: contiguous int64 [{rows}] on the tables' device is wanted")
+        if row_request is not None:
+            _check_ints("row_request", row_request, (rows,), index)
+        if n_short is not None:
+            _check_ints("n_short", n_short, (1,), index)
+        _on(index, B.paged_plan, self.struct, length.data_ptr(), n_new.data_ptr(), int(give_back), rows, seq_len.data_ptr(), row_start.data_ptr(),
+            None if row_request is None else row_request.data_ptr(), row_pos.data_ptr(), slot_map.data_ptr(),
+            None if n_short is None else n_short.data_ptr(), _handle_of(stream, index))

@@ -1,0 +1,134 @@
+"""The target's rows of a step: head norms with the position rotation before they enter a cache, and the log
+probabilities that a verification goes by (``include/blockdrafter.h``: ``bd_head_norm_rope``,
+``bd_token_logprobs``); all computation happens in the library's kernels.
+
+    heads = HeadNormRope(128, inv_freq, q_gain, k_gain, eps=1e-6)
+    heads(q, k, row_pos, q_out, k_out)                  # q_out, k_out may be q and k
+    token_logprobs(logits, tokens, logprob, entropy=entropy, top_ids=ids, top_logprob=alt)
+
+Calls run on the given stream, or on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import binding as B
+from .paged import _TYPES, _handle_of, _need, _on
+
+
+def _two_pi(bits: int) -> int:
+    """2 pi * 2^bits as an integer (Machin: pi / 4 = 4 atan(1/5) - atan(1/239)); the last few bits are off."""
+    def atan_of_inverse(n):
+        term, total, k = (1 << bits) // n, 0, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+    return 8 * (4 * atan_of_inverse(5) - atan_of_inverse(239))
+
+
+def turns_of(inv_freq: torch.Tensor) -> torch.Tensor:
+    """Angles a position (radians, finite) as 2^-64 turns modulo one turn: int64 bits on the same device."""
+    shift = 256
+    two_pi, out = _two_pi(shift), []
+    for f in inv_freq.double().cpu().tolist():
+        n, d = f.as_integer_ratio()
+        x = (2 * n * (1 << (64 + shift)) + d * two_pi) // (2 * d * two_pi) % (1 << 64)
+        out.append(x - (1 << 64) if x >> 63 else x)
+    return torch.tensor(out, dtype=torch.int64, device=inv_freq.device)
+
+
+class HeadNormRope:
+    """Norms of query and key heads over their D values, with gains (of the rows' type, or None for ones), and the rotation of
+    their first 2 * len(inv_freq) values: in halves, or in pairs side by side if interleaved.  inv_freq: the angle a position
+    of each pair in radians (fp64 on the device; None or empty: no rotation)."""
+
+    def __init__(self, head_dim: int, inv_freq: Optional[torch.Tensor], q_gain: Optional[torch.Tensor], k_gain: Optional[torch.Tensor],
+                 eps: float = 1e-6, interleaved: bool = False, dtype: Optional[torch.dtype] = None):
+        given = [t for t in (q_gain, k_gain) if t is not None]
+        if dtype is None:
+            _need(len(given) > 0, "dtype: the rows' type is wanted where no gain gives it")
+            dtype = given[0].dtype
+        _need(dtype in (torch.bfloat16, torch.float16), f"rows of {dtype} are not supported")
+        for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
+            _need(t is None or (t.dtype == dtype and tuple(t.shape) == (head_dim,) and t.is_contiguous()),
+                  f"{name}: contiguous {dtype} [{head_dim}] is wanted")
+        _need(inv_freq is None or (inv_freq.dim() == 1 and inv_freq.dtype == torch.float64), "inv_freq: float64 [pairs] is wanted")
+        self.head_dim, self.dtype, self.rotary_dim = int(head_dim), dtype, 0 if inv_freq is None else 2 * inv_freq.numel()
+        if inv_freq is not None:
+            given.append(inv_freq)
+        self.turns = turns_of(inv_freq) if self.rotary_dim else None
+        self.gains = (q_gain, k_gain)
+        self.index = given[0].get_device() if given else None  # None: that of the calls' rows
+        _need(all(t.get_device() == self.index and t.is_cuda for t in given), "gains and inv_freq: tensors of one CUDA device are wanted")
+        self.struct = B.HeadRope(_TYPES[dtype], self.head_dim, self.rotary_dim, int(interleaved), 0, 0, float(eps),
+                                 *(None if t is None else t.data_ptr() for t in (q_gain, k_gain, self.turns)))
+
+    def _rows(self, name: str, t: torch.Tensor, n: int, heads: int, index: int) -> int:
+        if t.dtype is not self.dtype or t.shape != (n, heads, self.head_dim) or t.get_device() != index:
+            raise ValueError(f"{name}: {[n, heads, self.head_dim]} of {self.dtype} on the gains' device is wanted, got {list(t.shape)} of {t.dtype}")
+        row, head, one = t.stride()
+        if one != 1 or (head != self.head_dim and heads > 1):
+            raise ValueError(f"{name}: a row's heads must be contiguous")
+        return row
+
+    def __call__(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None):
+        """q, k [n_rows, heads, D] (either may be None) into q_out, k_out (None: in place).  pos int32 [n_rows]; rows with a
+        negative position are left as they were."""
+        some = q if q is not None else k
+        _need(some is not None and some.dim() == 3 and some.is_cuda, "q or k: rows [n_rows, heads, D] on a CUDA device are wanted")
+        n, index = some.shape[0], some.get_device() if self.index is None else self.index
+        q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+        hq, hk = (0 if t is None else t.shape[1] if t.dim() == 3 else -1 for t in (q, k))
+        qs, qo = (0, 0) if q is None else (self._rows("q", q, n, hq, index), self._rows("q_out", q_out, n, hq, index))
+        ks, ko = (0, 0) if k is None else (self._rows("k", k, n, hk, index), self._rows("k_out", k_out, n, hk, index))
+        if pos.dtype is not torch.int32 or pos.shape != (n,) or not pos.is_contiguous() or pos.get_device() != index:
+            raise ValueError(f"pos: contiguous int32 [{n}] on the rows' device is wanted")
+        c = self.struct
+        if c.n_q_heads != hq or c.n_kv_heads != hk:
+            c = B.HeadRope.from_buffer_copy(c)
+            c.n_q_heads, c.n_kv_heads = hq, hk
+            self.struct = c
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        _on(index, B.head_norm_rope, c, n, pos.data_ptr(), p(q), qs, p(k), ks, p(q_out), qo, p(k_out), ko, _handle_of(stream, index))
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], logprob: Optional[torch.Tensor],
+                   entropy: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, top_ids: Optional[torch.Tensor] = None,
+                   top_logprob: Optional[torch.Tensor] = None, temperature: float = 1.0, stream=None):
+    """Of each row of logits [rows, vocab] (fp32, bf16 or fp16; rows any stride apart): the log probabilities of
+    tokens int32 [rows] or [rows, n] (-1: none, 0) into logprob (the same shape, float32); optionally the entropy and the
+    log of the sum of exponentials (float32 [rows]), and the k largest logits' ids and log probabilities (top_ids int32
+    [rows, k], top_logprob float32 [rows, k]), equal ones to the lower id."""
+    if logits.dim() != 2 or logits.dtype not in _TYPES or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError(f"logits: [rows, vocab] of float32, bfloat16 or float16 with contiguous rows are wanted, got {list(logits.shape)} of {logits.dtype}")
+    rows, vocab = logits.shape
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError(f"logits are on {logits.device}: a CUDA device is wanted")
+    n, k = 0, 0
+    if tokens is not None:
+        n = 1 if tokens.dim() == 1 else tokens.shape[1] if tokens.dim() == 2 else -1
+        if logprob is None:
+            raise ValueError("logprob: a tensor of the tokens' shape is wanted")
+        for name, t, dtype in (("tokens", tokens, torch.int32), ("logprob", logprob, torch.float32)):
+            if t.dtype is not dtype or t.shape != tokens.shape or t.shape[0] != rows or n < 0 or not t.is_contiguous() or t.get_device() != index:
+                raise ValueError(f"{name}: contiguous {dtype} [{rows}] or [{rows}, n] on the logits' device is wanted")
+    elif logprob is not None:
+        raise ValueError("tokens: the ids that logprob is for are wanted")
+    if top_ids is not None:
+        k = top_ids.shape[1] if top_ids.dim() == 2 else -1
+        if top_ids.dtype is not torch.int32 or k < 0 or top_ids.shape[0] != rows or not top_ids.is_contiguous() or top_ids.get_device() != index:
+            raise ValueError(f"top_ids: contiguous int32 [{rows}, k] on the logits' device is wanted")
+    elif top_logprob is not None:
+        raise ValueError("top_ids: the ids that top_logprob is for are wanted")
+    for name, t, shape in (("entropy", entropy, (rows,)), ("lse", lse, (rows,)), ("top_logprob", top_logprob, (rows, k))):
+        if t is not None and (t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != index):
+            raise ValueError(f"{name}: contiguous float32 {list(shape)} on the logits' device is wanted")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _on(index, B.token_logprobs, logits.data_ptr(), logits.stride(0), _TYPES[logits.dtype], rows, vocab, float(temperature),
+        p(tokens), n, p(logprob), p(entropy), p(lse), k, p(top_ids), p(top_logprob), _handle_of(stream, index))

@@ -549,6 +549,162 @@ bd_status bd_paged_evict(const bd_paged_kv *kv, const bd_paged_batch *batch, con
                          int32_t *len_out, float *score_out, int64_t score_out_stride, void *stream);
 
 /*
+ * Page tables and slot maps of a step, from its requests' lengths (no counterpart in the papers): what
+ * bd_paged_batch and the appends ask for, made on the device.  Request b keeps its first len[b] slots -- the
+ * rows of a drafted block that were not accepted are simply not counted -- and gets n_new[b] rows:
+ *     seq_len[b] = len[b] + n_new[b],  row_start[b] = sum of n_new before b (at most n_rows),
+ * and row i of request b is at row row_start[b] + i with position len[b] + i.  It needs
+ * ceil(seq_len[b] / page_size) pages.  Pages that it holds beyond those go back (give_back != 0) onto the
+ * stack of free page ids, in request and table order; then the pages that requests lack are taken off the
+ * top of the stack, in request and table order, and enter their tables behind the held ones.  Pages are
+ * promised in request order: a request that lacks pages, and for which those promised up to and with it are
+ * more than the stack has, is short: it takes none, its seq_len is 0 (its rows are then neither stored nor
+ * seen), its held pages and table stay, and it is counted in n_short.  A request with a negative length or
+ * row count, whose slots exceed its table's row, with fewer held pages than len needs, or whose rows go past
+ * n_rows is treated the same, sets the device error word (bd_sync_status: BD_ERR_INVALID_ARG) and is counted
+ * too; it neither gives nor promises pages, and a negative row count counts as none.
+ *   len, n_new     dev int32 [n_requests]
+ *   give_back      0: pages beyond the need stay held
+ *   n_rows         length of the row arrays, >= 0 (rows behind the last request get -1)
+ *   seq_len        dev int32 [n_requests] OUT;  row_start dev int32 [n_requests + 1] OUT
+ *   row_request    dev int32 [n_rows] OUT: the row's request, or NULL
+ *   row_pos        dev int32 [n_rows] OUT: the row's position, -1 for rows of no request or a short one
+ *   slot_map       dev int64 [n_rows] OUT: page * page_size + place in the page, -1 likewise
+ *   n_short        dev int32 [1] OUT, or NULL
+ * Errors: BD_ERR_INVALID_ARG (sizes, NULL or misaligned arrays, an output that overlaps another array
+ * but as said below).  One launch; nothing else is kept between calls.
+ */
+typedef struct {
+  int n_requests;             /* 1 .. BD_PAGED_MAX_REQUESTS                                       */
+  int table_width;            /* entries of one page_table row                                    */
+  int page_size;              /* slots per page                                                   */
+  int n_free;                 /* entries of free_pages: as many as the pool has pages             */
+  int32_t *page_table;        /* dev [n_requests, table_width] IN/OUT: entries behind the held    */
+                              /*   pages are written as pages are taken, no other                 */
+  const int32_t *held;        /* dev [n_requests] pages that each request holds                   */
+  int32_t *held_out;          /* dev [n_requests] OUT, may be held                                */
+  int32_t *free_pages;        /* dev [n_free] IN/OUT: the stack, its top at free_count - 1        */
+  const int32_t *free_count;  /* dev [1]                                                          */
+  int32_t *free_count_out;    /* dev [1] OUT, may be free_count                                   */
+} bd_paged_pages;
+
+bd_status bd_paged_plan(const bd_paged_pages *pages, const int32_t *len, const int32_t *n_new, int give_back,
+                        int n_rows, int32_t *seq_len, int32_t *row_start, int32_t *row_request,
+                        int32_t *row_pos, int64_t *slot_map, int32_t *n_short, void *stream);
+
+/*
+ * ------------------------------------------------------------------ paged K/V cache in 4 bits
+ * The same cache with its keys and values in 4 bits, 0.5625 bytes a value: 3.6 times the slots of a 16-bit
+ * pool.  The D values of a slot and KV head are groups of 16.  A group is stored as an e4m3 scale s (sign 0)
+ * and 16 e2m1 codes (1 sign, 2 exponent, 1 fraction bit: 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives) and
+ * stands for the values code * s * 2^k_exp (2^v_exp for values):
+ *     s    = e4m3(max |x| / 6 * 2^-exp), to nearest even, at most 448
+ *     code = e2m1(x * 2^-exp / s), to nearest, ties to the even code, at most 6;  all codes +0 if s = 0
+ * Every step is exact but for these two roundings, so the stored bits are a function of the values alone.
+ * exp only shifts the range (its precision is the scale's): a group is kept to a relative 2^-4 of its
+ * magnitude while max |x| is between 2^-6 * 6 * 2^exp and 2688 * 2^exp.  A group that holds an infinity or
+ * NaN is stored as zeros, a larger one saturates; both set the device error word (bd_sync_status:
+ * BD_ERR_RANGE).  The e4m3 code of a NaN in a scale reads as 448: hidden slots may hold any bytes.
+ *
+ * Requests, slots, rows, visibility, lengths and page ids are as above, and bd_paged_batch and bd_paged_plan serve
+ * both caches.  Products take the stored values exactly.
+ */
+typedef struct {
+  int n_q_heads, n_kv_heads;  /* as in bd_paged_kv                                                */
+  int head_dim;               /* 64 or 128                                                        */
+  int dtype;                  /* of the calls' rows: BD_BF16 or BD_F16                            */
+  int page_size, n_pages;
+  int k_exp, v_exp;           /* -64 .. 64 with BD_BF16, -14 .. 4 with BD_F16                     */
+  int64_t page_stride, head_stride, slot_stride;                    /* bytes between pages, KV    */
+                              /*   heads and slots of the code pools (multiples of 16); the D/2   */
+                              /*   bytes of a slot are contiguous, value 2i in the low half of    */
+                              /*   byte i                                                         */
+  int64_t scale_page_stride, scale_head_stride, scale_slot_stride;  /* bytes, of the scale pools  */
+                              /*   (multiples of D/16); a slot's D/16 scales are contiguous       */
+  void *k, *v;                /* dev code pools, 16-byte aligned                                  */
+  void *k_scale, *v_scale;    /* dev scale pools, aligned to D/16 bytes                           */
+} bd_paged4_kv;
+
+/* Bytes of workspace bd_paged4_attention needs for batches of up to n_requests requests of up to max_rows
+ * rows and max_len slots each (calls of many rows read the slots from a 16-bit copy in it).  Returns 0 for an
+ * invalid or unsupported kv. */
+size_t bd_paged4_workspace_bytes(const bd_paged4_kv *kv, int n_requests, int max_rows, int max_len);
+
+/* Rounds the rows' keys and values and stores them in their slots (rows with p_i < 0 are not stored; two
+ * rows of a call must not share a slot).
+ *   k_new, v_new    as in bd_paged_append
+ *   k_held, v_held  dev [n_rows, n_kv_heads, D] contiguous, 16-byte aligned OUT: the values that the slots
+ *                   now stand for, in the rows' type (exact); rows that are not stored are left as they were;
+ *                   may be NULL, and may be k_new / v_new themselves where those are contiguous */
+bd_status bd_paged4_append(const bd_paged4_kv *kv, const bd_paged_batch *batch, const void *k_new,
+                           int64_t k_stride, const void *v_new, int64_t v_stride, void *k_held,
+                           void *v_held, void *stream);
+
+/* Attention as bd_paged_attention's, over the values that the slots stand for.  All results of a row that
+ * sees a slot are finite where its query is. */
+bd_status bd_paged4_attention(const bd_paged4_kv *kv, const bd_paged_batch *batch, const void *q,
+                              int64_t q_stride, void *out, int64_t out_stride, float *lse, int window,
+                              int n_sink, float scale, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * ------------------------------------------------------------------ target rows
+ * Head norms with the position rotation, of a step's query and key heads in one pass (the per-layer equations
+ * of [DFlash-notes] for a target's own rows, before they are appended): for every head x of D values
+ *     y = gain * x / sqrt(mean(x^2) + eps),
+ * and of its first rotary_dim values the pairs (y_j, y_j+rotary_dim/2), or (y_2j, y_2j+1) if interleaved,
+ * turn by the angle pos * f_j.  Computed in fp32 and rounded once.  The angles are exact for every position:
+ * f_j is given in 2^-64 turns per position, turns[j] = f_j / (2 pi) * 2^64 modulo 2^64 (rounded), and only the
+ * remainder of pos * turns[j] is converted.  Rows with a negative position are left as they were.
+ *   q, k          dev [n_rows, n_q_heads / n_kv_heads, D], rows q_stride / k_stride elements apart (views
+ *                 into one projection's output will do)
+ *   q_out, k_out  the same; each may be its input (same stride) or not overlap any other array
+ *   gains         dev [D] of the rows' type, or NULL for ones
+ *   pos           dev int32 [n_rows] (bd_paged_plan's row_pos);  turns dev uint64 [rotary_dim / 2]
+ * n_q_heads or n_kv_heads may be 0: that side is not touched.  16-byte aligned, strides multiples of 8.
+ * Errors: BD_ERR_INVALID_ARG; BD_ERR_UNSUPPORTED (dtype, head_dim, rotary_dim).
+ */
+typedef struct {
+  int dtype;                  /* BD_BF16 or BD_F16                                                */
+  int head_dim;               /* D: 64, 128 or 256                                                */
+  int rotary_dim;             /* 0, or a multiple of 16 up to D                                   */
+  int interleaved;
+  int n_q_heads, n_kv_heads;
+  float eps;                  /* > 0                                                              */
+  const void *q_gain, *k_gain;
+  const uint64_t *turns;
+} bd_head_rope;
+
+bd_status bd_head_norm_rope(const bd_head_rope *c, int n_rows, const int32_t *pos, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride, void *q_out,
+                            int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+
+/*
+ * Log probabilities of given tokens, with the distribution's entropy and its largest alternatives (no
+ * counterpart in the papers): what a verification accepts by and a server reports.  With z = logits / temperature
+ *     lse = log sum_v exp(z_v),  logprob[r][i] = z_token - lse,  entropy = lse - sum_v p_v z_v  (p = softmax z),
+ * in one pass over the logits, fp32.  The top_k largest logits of a row in descending order, equal ones to the
+ * lower id (NaN counts as -inf), with z - lse.  A logit of -inf has probability 0 and no part in the entropy; a
+ * row with a NaN or +inf, or of -inf alone, has NaN for every fp32 result (lse -inf in the last case).
+ *   logits       dev [rows, vocab], rows row_stride elements apart (>= vocab), aligned to one element
+ *   dtype        BD_BF16, BD_F16 or BD_F32
+ *   tokens       dev int32 [rows, n_given]; -1: none, its logprob is 0; other ids outside the vocabulary: NaN,
+ *                reported by bd_sync_status (BD_ERR_INVALID_ARG)
+ *   logprob      dev fp32 [rows, n_given] OUT;  n_given 0 .. 64 (0: tokens and logprob may be NULL)
+ *   entropy, lse dev fp32 [rows] OUT, or NULL
+ *   top_ids      dev int32 [rows, top_k] OUT;  top_logprob dev fp32 [rows, top_k] OUT, or NULL;
+ *                top_k 0 .. BD_LOGPROB_TOP_MAX and <= vocab
+ * rows 0 .. 2^24, vocab 1 .. 2^24, temperature > 0 and finite.  Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED
+ * (dtype).
+ */
+#define BD_LOGPROB_TOP_MAX 32
+#define BD_LOGPROB_GIVEN_MAX 64
+bd_status bd_token_logprobs(const void *logits, int64_t row_stride, int dtype, int rows, int vocab,
+                            float temperature, const int32_t *tokens, int n_given, float *logprob,
+                            float *entropy, float *lse, int top_k, int32_t *top_ids, float *top_logprob,
+                            void *stream);
+
+/*
  * Measurement hook (no counterpart in the papers): brackets single kernel launches with
  * caller-created CUDA events (cudaEvent_t passed as void*, timing enabled), so that a
  * benchmark can time one kernel of a round, also inside a captured graph.  While a kind

@@ -1,0 +1,99 @@
+"""4-bit paged-cache cases for the GPU tests: the 16-bit cases' requests, with pools whose bytes are all
+ones (the codes of NaN scales among them) wherever no request holds a slot."""
+import dataclasses
+
+import numpy as np
+import torch
+
+from oracle import paged_oracle as P
+from oracle import target_oracle as T
+from paged_harness import TYPES, PagedCase
+
+
+@dataclasses.dataclass
+class Paged4Case(PagedCase):
+    k_exp: int = 0
+    v_exp: int = 0
+
+    @classmethod
+    def of(cls, case, **kw):
+        return cls(**{**dataclasses.asdict(case), **kw})
+
+    def build(self):
+        from block_drafter_gb300.paged import PagedCache4
+        g = torch.Generator().manual_seed(self.seed * 7919 + sum(self.lens) * 31 + sum(self.rows))
+        B, hq, d = len(self.lens), self.hkv * self.group, self.d
+        held = [-(-n // self.page) for n in self.lens]
+        width, total = max(max(held), 1) + self.spare, sum(held) + 2
+        ids = torch.randperm(total, generator=g)
+        table = torch.full((B, width), 2 ** 30, dtype=torch.int32)  # entries behind a length are never followed
+        at = 0
+        for b, h in enumerate(held):
+            table[b, :h] = ids[at:at + h].int()
+            at += h
+
+        def pool(bytes_, pad):
+            shape = (total, self.page, self.hkv, bytes_ + pad) if self.nhd else (total, self.hkv, self.page, bytes_ + pad)
+            return torch.full(shape, 0xff, dtype=torch.uint8)
+
+        def view(p, bytes_):
+            return (p.permute(0, 2, 1, 3) if self.nhd else p)[..., :bytes_]
+
+        self.k, self.v, host = [], [], []  # fp64 contents in slot order
+        for keep, exp in ((self.k, self.k_exp), (self.v, self.v_exp)):
+            codes, scales = pool(d // 2, 16 if self.pad else 0), pool(d // 16, d // 16 if self.pad else 0)
+            for b, n in enumerate(self.lens):
+                c, s = T.encode4(torch.randn(n, self.hkv, d, generator=g).to(torch.bfloat16).double().numpy() * 2.0 ** exp, exp)
+                keep.append(T.decode4(c, s, exp))
+                j = torch.arange(n)
+                view(codes, d // 2)[table[b, j // self.page].long(), :, j % self.page] = torch.from_numpy(c)
+                view(scales, d // 16)[table[b, j // self.page].long(), :, j % self.page] = torch.from_numpy(s)
+            host += [codes, scales]
+        starts = [self.lead]
+        for r in self.rows:
+            starts.append(starts[-1] + r)
+        self.starts, self.n_rows = starts, starts[-1] + self.lead
+        self.q = (torch.randn(self.n_rows, hq, d, generator=g) * self.std).to(TYPES[self.dtype])
+        self.qf = self.q.double().numpy()
+        self.scale = d ** -0.5 * 2.0 ** -self.k_exp
+        dev = [p.cuda() for p in host]
+        self.pools = [view(p, x) for p, x in zip(dev, (d // 2, d // 16) * 2)]
+        self.cache = PagedCache4(*self.pools, n_q_heads=hq, dtype=TYPES[self.dtype], k_exp=self.k_exp, v_exp=self.v_exp)
+        self.table, self.lend = table.cuda(), torch.tensor(self.lens, dtype=torch.int32).cuda()
+        self.startd = torch.tensor(starts, dtype=torch.int32).cuda()
+        self.max_len, self.max_rows = max(self.lens), max(self.rows)
+        self.batch = self.cache.batch(self.table, self.lend, self.startd, self.n_rows, self.max_rows, self.max_len)
+        self.qd = self.strided(self.q)
+        return self
+
+    def attend(self, **kw):
+        return super().attend(**{"scale": self.scale, **kw})
+
+    def check_attention(self, out, lse, requests=None, kernel_rows=16):
+        """Against the oracle over the stored values.  As for the 16-bit cache, but for what the kernel of few rows
+        (up to kernel_rows rows times heads of a KV head) rounds: queries of a bf16 row are off by at most 2^-33 of the row's
+        largest, which a score takes as 2^-33 scale max|q| sum_d |k_d|; weights are fp16, half a step 2^-12, and with
+        fp16 rows the rest is a second operand, whose rounding is 2^-24 of the weight."""
+        t = TYPES[self.dtype]
+        half = torch.finfo(t).eps / 2
+        tiny = torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2
+        few = self.max_rows * self.group <= kernel_rows
+        weight = half if not few else 2.0 ** -12 if self.dtype == "bf16" else 2.0 ** -23
+        got, glse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for b, (n, r) in enumerate(zip(self.lens, self.rows)):
+            if requests is not None and b not in requests:
+                continue
+            s = slice(self.starts[b], self.starts[b] + r)
+            ref, rl, spread, size = P.attention(self.qf[s], self.k[b], self.v[b], self.window, self.n_sink, self.scale)
+            ds = (self.d * 2.0 ** -23) * size + (size + 4) * 2.0 ** -22
+            if few and n:
+                far = np.abs(self.k[b]).sum(-1).max(0).repeat(self.group)  # of each query head's KV head
+                ds = ds + 2.0 ** -33 * self.scale * np.abs(self.qf[s]).max(-1) * far
+            tol = half * np.abs(ref) + tiny + (weight + 2.02 * ds[..., None] + (n + 64) * 2.0 ** -23) * spread
+            empty = np.isinf(rl)
+            assert (np.isneginf(glse[s]) == empty).all(), f"request {b}: rows without a visible slot"
+            err = np.abs(got[s] - ref) - tol
+            assert (err <= 0).all(), f"request {b}: worst {err.max()} beyond {tol.max()}"
+            ltol = ds + (n + 64) * 2.0 ** -23 + np.abs(rl) * 2.0 ** -22
+            lerr = np.abs(glse[s][~empty] - rl[~empty]) - ltol[~empty]
+            assert (lerr <= 0).all(), f"request {b}: lse {lerr.max()}"

@@ -1,0 +1,324 @@
+"""The 4-bit paged cache on the GPU against the 64-bit oracle: append, attention, and steps of them.  Every byte
+that no request holds is 0xff in the pools."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as P
+from oracle import target_oracle as T
+from paged_harness import TYPES, PagedCase
+from target_harness import Paged4Case
+from test_gpu_paged import ATTENTION
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_drafter_gb300 import builder
+    builder.build()
+
+
+def sync():
+    from block_drafter_gb300 import binding
+    binding.sync_status()
+
+
+# ------------------------------------------------------------------ append
+def _rows(kind, shape, dtype, g, exp=0):
+    x = torch.randn(shape, generator=g)
+    if kind == "ties":      # multiples of the middles between codes, under a scale of 1
+        x = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])[torch.randint(0, 8, shape, generator=g)] * x.sign()
+        x[..., 0] = 6.0
+    elif kind == "near":    # those, a step of the type up or down
+        x = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])[torch.randint(0, 7, shape, generator=g)]
+        x = x * (1 + torch.finfo(dtype).eps * torch.randint(-2, 3, shape, generator=g)) * torch.randn(shape, generator=g).sign()
+        x[..., 0] = 6.0 * 2.0 ** torch.randint(-3, 4, shape[:-1], generator=g)
+    elif kind == "wide":    # groups of all sizes, down to zero and to scales of few bits
+        x = x * 2.0 ** torch.randint(-14, 6, shape, generator=g)
+        x[:, :, :16] = 0
+        x[:, :, 16:32] *= 2.0 ** -8
+    return (x * 2.0 ** exp).to(dtype)
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties", "near", "wide"])
+@pytest.mark.parametrize("case", [Paged4Case((1,), (1,)), Paged4Case((17, 300, 64), (1, 16, 64), lead=2),
+                                  Paged4Case((5, 0, 9), (9, 2, 0), page=4, k_exp=3, v_exp=-5),
+                                  Paged4Case((700, 33), (700, 33), page=33, dtype="fp16", d=64, pad=8, nhd=True, k_exp=-14, v_exp=4),
+                                  Paged4Case((3000,), (2900,), hkv=8, page=64)])
+def test_append_stores_the_rows_bits_and_nothing_else(case, kind):
+    c = case.build()
+    t = TYPES[c.dtype]
+    g = torch.Generator().manual_seed(5)
+    new = [_rows(kind, (c.n_rows, c.hkv, c.d), t, g, exp) for exp in (c.k_exp, c.v_exp)]
+    want = [p.cpu().clone() for p in c.pools]
+    held = [torch.full((c.n_rows, c.hkv, c.d), -7.0, dtype=t, device="cuda") for _ in range(2)]
+    values = [x.cpu().clone() for x in held]
+    for side, exp in ((0, c.k_exp), (1, c.v_exp)):
+        codes, scales = T.encode4(new[side].double().numpy(), exp)
+        val = torch.from_numpy(T.decode4(codes, scales, exp)).to(t)
+        assert (val.double().numpy() == T.decode4(codes, scales, exp)).all()   # exact in the rows' type
+        for b, (n, r) in enumerate(zip(c.lens, c.rows)):
+            for i in range(r):
+                p, row = n - r + i, c.starts[b] + i
+                if p >= 0:
+                    page = c.table[b, p // c.page].item()
+                    want[2 * side][page, :, p % c.page] = torch.from_numpy(codes[row])
+                    want[2 * side + 1][page, :, p % c.page] = torch.from_numpy(scales[row])
+                    values[side][row] = val[row]
+    c.cache.append(c.batch, c.strided(new[0]), c.strided(new[1]), k_held=held[0], v_held=held[1])
+    sync()
+    for got, w in zip(c.pools, want):
+        assert torch.equal(got.cpu(), w)
+    for got, w in zip(held, values):
+        assert torch.equal(got.cpu(), w)
+    for p in c.pools:
+        p.fill_(0xff)
+    c.cache.append(c.batch, c.strided(new[0]), c.strided(new[1]))    # without the values
+    sync()
+    inside = [torch.full_like(w, 0xff) for w in want]
+    for b, (n, r) in enumerate(zip(c.lens, c.rows)):
+        j = torch.arange(max(0, n - r), n)
+        pages = c.table[b].cpu().long()[j // c.page]
+        for i, w in zip(inside, want):
+            i[pages, :, j % c.page] = w[pages, :, j % c.page]
+    for got, w in zip(c.pools, inside):
+        assert torch.equal(got.cpu(), w)
+
+
+def test_values_may_replace_the_rows():
+    c = Paged4Case((40, 7), (30, 5)).build()
+    k, v = (torch.randn(35, 2, 128, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in (1, 2))
+    kh, vh = torch.empty_like(k), torch.empty_like(v)
+    c.cache.append(c.batch, k, v, k_held=kh, v_held=vh)
+    c.cache.append(c.batch, k, v, k_held=k, v_held=v)
+    sync()
+    assert torch.equal(k, kh) and torch.equal(v, vh)
+
+
+def test_values_beyond_the_range_saturate_and_are_reported():
+    from block_drafter_gb300 import binding as B
+    c = Paged4Case((2, 40), (2, 1), hkv=1).build()
+    k = torch.ones(3, 1, 128, dtype=torch.bfloat16, device="cuda")
+    held = torch.empty_like(k)
+    for bad, want in ((2688.0, 2688.0), (2704.0, 2688.0), (1e30, 2688.0), (float("inf"), 0.0), (float("-inf"), 0.0), (float("nan"), 0.0)):
+        x = k.clone()
+        x[1, 0, 5] = bad
+        c.cache.append(c.batch, x, k, k_held=held)
+        if bad == 2688.0:
+            B.sync_status()
+        else:
+            with pytest.raises(B.BdError, match="4-bit") as err:
+                B.sync_status()
+            assert err.value.status == -6
+        B.sync_status()
+        # a group of ones: the scale is the e4m3 number nearest to 1/6, 11/64, and 1 / (11/64) = 5.82 is nearest to 6
+        assert held[1, 0, 5].item() == want and held[1, 0, 20].item() == 66 / 64 and held[0, 0, 5].item() == 66 / 64
+        assert (held[1, 0, :5] == 0).all()      # the others of the group: nothing, or far below its scale
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("name", list(ATTENTION))
+def test_attention_matches_the_oracle(name):
+    c = Paged4Case.of(ATTENTION[name]).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    c.check_guards(out, lse)
+    again, lse2 = c.attend()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)   # nothing depends on the run
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128])
+@pytest.mark.parametrize("d,group,dtype", [(128, 4, "bf16"), (64, 1, "bf16"), (128, 1, "fp16"), (64, 2, "fp16")])
+def test_attention_of_every_row_count(rows, d, group, dtype):
+    c = Paged4Case((rows + 150, 129 + rows), (rows, rows), d=d, group=group, hkv=1, dtype=dtype, seed=rows).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40])
+@pytest.mark.parametrize("dtype,k_exp,v_exp", [("bf16", 40, -60), ("bf16", -33, 20), ("fp16", -14, 4), ("fp16", 4, -14)])
+def test_exponents_shift_keys_and_values(rows, dtype, k_exp, v_exp):
+    c = Paged4Case((200, 77), (rows, rows), dtype=dtype, k_exp=k_exp, v_exp=v_exp).build()
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -30, 2.0 ** 30, 2.0 ** 100])
+def test_queries_of_any_size(size):
+    """bf16 queries far outside fp16's range, small ones beside large ones."""
+    c = Paged4Case((300, 41), (2, 1)).build()
+    c.q = (c.q.float() * size * 2.0 ** torch.randint(-20, 1, c.q.shape, generator=torch.Generator().manual_seed(1))).to(torch.bfloat16)
+    c.qf, c.qd, c.scale = c.q.double().numpy(), c.strided(c.q), c.scale / size
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 60])
+def test_a_row_of_bad_queries_is_its_own(rows):
+    c = Paged4Case((100, 90), (rows, rows), hkv=1).build()
+    ref, rl = c.attend()
+    q = c.qd.clone()
+    q[0, 1, 3], q[rows, 0, 0] = float("nan"), float("inf")
+    out, lse = c.outputs()
+    c.cache.attention(c.batch, q, out, lse=lse, scale=c.scale)
+    sync()
+    bad = torch.zeros(c.n_rows, 4, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[rows, 0] = True
+    assert torch.equal(out[~bad], ref[~bad]) and torch.equal(lse[~bad], rl[~bad])
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1]) and not torch.isfinite(out[rows, 0]).any()
+
+
+def test_bad_sizes_and_pages_are_reported_and_other_requests_stand():
+    from block_drafter_gb300 import binding as B
+    for rows in ((2, 3, 1), (2, 30, 1)):
+        for spoil in ("page", "negative_page", "length", "negative_length", "rows", "rows_out"):
+            c = Paged4Case((200, 100, 70), rows).build()
+            if spoil == "page":
+                c.table[1, 6] = 10 ** 6                             # slots 96 .. 99
+            elif spoil == "negative_page":
+                c.table[1, 6] = -1
+            elif spoil == "length":
+                c.lend[1] = 201
+            elif spoil == "negative_length":
+                c.lend[1] = -5
+            elif spoil == "rows":
+                c.startd.copy_(torch.tensor([0, 4, 2, 6]))         # request 1 ends before it begins
+            else:
+                c.startd.copy_(torch.tensor([0, 2, 2 + rows[1], 600]))  # request 2 goes beyond the rows
+            out, lse = c.attend()
+            with pytest.raises(B.BdError) as err:
+                B.sync_status()
+            assert err.value.status == -1
+            B.sync_status()
+            if spoil not in ("rows", "rows_out"):
+                c.check_attention(out, lse, requests=(0, 2))
+            elif spoil == "rows_out":
+                c.check_attention(out, lse, requests=(0, 1))
+            k = torch.randn(c.n_rows, c.hkv, c.d, device="cuda").to(torch.bfloat16)
+            before = c.pools[0].clone()
+            c.cache.append(c.batch, k, k)
+            with pytest.raises(B.BdError):
+                B.sync_status()
+            changed = (c.pools[0] != before).flatten(2).any(2).any(1).sum().item()
+            assert changed <= 5
+
+
+def test_pages_behind_a_window_may_be_given_back():
+    for rows in (1, 30):
+        c = Paged4Case((500, 300), (rows, rows), window=64, n_sink=4).build()
+        ref, rl = c.attend()
+        for b, n in enumerate(c.lens):
+            c.table[b, 1:(n - rows - 64 + 1) // c.page] = -5
+        out, lse = c.attend()
+        sync()
+        assert torch.equal(out, ref) and torch.equal(lse, rl)
+
+
+def test_no_slots_at_all():
+    c = Paged4Case((0, 0), (2, 40)).build()
+    out, lse = c.attend()
+    sync()
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_a_serving_step(rows, graph):
+    """Plan, norms and rotation, append, attention and log probabilities, several steps on tables that start empty; after each
+    step some rows are not accepted.  Against the oracle's own cache; captured once and replayed in one variant."""
+    from block_drafter_gb300.paged import PagedCache4, PageTables
+    from block_drafter_gb300.target import HeadNormRope, token_logprobs
+    Bn, hq, hkv, d, ps, vocab, t, steps = 3, 8, 2, 128, 16, 500, torch.bfloat16, 4
+    width = -(-rows * steps // ps)
+    total = Bn * width
+    g = torch.Generator().manual_seed(rows)
+    cu = lambda *shape, dtype=torch.int32, fill=0: torch.full(shape, fill, dtype=dtype, device="cuda")  # noqa: E731
+    table, held, count = cu(Bn, width, fill=-1), cu(Bn), cu(1, fill=total)
+    stack = torch.randperm(total, generator=g).int().cuda()
+    pools = [cu(total, hkv, ps, x, dtype=torch.uint8, fill=0xff) for x in (d // 2, d // 16, d // 2, d // 16)]
+    n_rows = Bn * rows
+    length, fresh, seq_len, start, pos = cu(Bn), cu(Bn, fill=rows), cu(Bn), cu(Bn + 1), cu(n_rows)
+    slot = cu(n_rows, dtype=torch.int64)
+    freq = torch.tensor([1e4 ** (-2 * j / d) for j in range(d // 2)], dtype=torch.float64, device="cuda")
+    gains = [(1 + 0.1 * torch.randn(d, generator=g)).to(t).cuda() for _ in range(2)]
+    qkv, head = cu(n_rows, hq + 2 * hkv, d, dtype=t), (torch.randn(vocab, hq * d, generator=g) * 0.05).to(t).cuda()
+    out, lse = cu(n_rows, hq, d, dtype=t), cu(n_rows, hq, dtype=torch.float32)
+    kh, vh = cu(n_rows, hkv, d, dtype=t), cu(n_rows, hkv, d, dtype=t)
+    tokens, lp, ent, ids, alt = cu(n_rows), cu(n_rows, dtype=torch.float32), cu(n_rows, dtype=torch.float32), cu(n_rows, 5), cu(n_rows, 5, dtype=torch.float32)
+    logits = cu(n_rows, vocab, dtype=t)
+    tables = PageTables(table, held, stack, count, ps)
+    heads = HeadNormRope(d, freq, *gains)
+    cache = PagedCache4(*pools, n_q_heads=hq, dtype=t)
+    batch = cache.batch(table, seq_len, start, n_rows=n_rows, max_rows=rows, max_len=rows * steps)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+
+    def step():
+        tables.plan(length, fresh, seq_len, start, pos, slot)
+        heads(q, k, pos)
+        cache.append(batch, k, v, k_held=kh, v_held=vh)
+        cache.attention(batch, q, out, lse=lse)
+        torch.matmul(out.view(n_rows, -1), head.t(), out=logits)
+        token_logprobs(logits, tokens, lp, entropy=ent, top_ids=ids, top_logprob=alt)
+
+    run = step
+    if graph:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            fresh.zero_()
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        fresh.fill_(rows)
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            step()
+        run = captured.replay
+    mine = [[np.zeros((0, hkv, d))] * 2 for _ in range(Bn)]
+    for s in range(steps):
+        x = torch.randn(n_rows, hq + 2 * hkv, d, generator=g).to(t)
+        tok = torch.randint(0, vocab, (n_rows,), generator=g).int()
+        qkv.copy_(x)
+        tokens.copy_(tok)
+        run()
+        sync()
+        assert seq_len.tolist() == [m[0].shape[0] + rows for m in mine]
+        places = pos.cpu().numpy()
+        for i, (a, b, gain) in enumerate(((0, hq, gains[0]), (hq, hq + hkv, gains[1]))):
+            want = T.head_norm_rope(x[:, a:b].double().numpy(), gain.double().cpu().numpy(), 1e-6, freq.tolist(), places, False)
+            assert np.abs(qkv[:, a:b].double().cpu().numpy() - want).max() <= 2.0 ** -8 * np.abs(want).max() + 1e-5
+        qf = q.double().cpu().numpy()
+        for b in range(Bn):
+            r = slice(b * rows, (b + 1) * rows)
+            for i, (new, values) in enumerate(((k, kh), (v, vh))):
+                vals = T.decode4(*T.encode4(new[r].double().cpu().numpy()))
+                assert (values[r].double().cpu().numpy() == vals).all()
+                mine[b][i] = np.concatenate([mine[b][i], vals])
+            j = np.arange(mine[b][0].shape[0] - rows, mine[b][0].shape[0])
+            assert (places[r] == j).all()
+            pages = table[b].cpu().numpy()
+            assert (slot[r].cpu().numpy() == pages[j // ps] * ps + j % ps).all()
+            ref, rl, spread, size = P.attention(qf[r], mine[b][0], mine[b][1], 0, 0, d ** -0.5)
+            n = mine[b][0].shape[0]
+            ds = (d * 2.0 ** -23 + 2.0 ** -33 * 40) * size + (size + 4) * 2.0 ** -22
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.02 * ds[..., None] + (n + 64) * 2.0 ** -23) * spread + 1e-30
+            assert (np.abs(out[r].double().cpu().numpy() - ref) <= tol).all()
+            # what is accepted stays: lengths go back by what is not
+            keep = n - int(torch.randint(0, rows, (1,), generator=g))
+            mine[b] = [m[:keep] for m in mine[b]]
+            length[b] = keep
+        for r in range(n_rows):
+            row = logits[r].double().cpu().numpy()
+            a, e, _, order, tops = T.token_logprobs(row, [tok[r].item()], 1.0, 5)
+            assert ids[r].tolist() == order
+            near = lambda got, want: abs(got - want) <= 1e-5 * (1 + abs(want))  # noqa: E731
+            assert near(lp[r].item(), a[0]) and near(ent[r].item(), e)
+            assert all(near(p, w) for p, w in zip(alt[r].tolist(), tops))
+    used = {p for b in range(Bn) for p in table[b, :held[b]].tolist()}
+    free = stack[:count.item()].tolist()
+    assert sorted(free + list(used)) == list(range(total))      # no page lost, none twice

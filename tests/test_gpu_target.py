@@ -1,0 +1,367 @@
+"""Page tables and slot maps, head norms with rotation, and log probabilities on the GPU against the 64-bit oracle."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import target_oracle as T
+from paged_harness import TYPES
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_drafter_gb300 import builder
+    builder.build()
+
+
+def sync():
+    from block_drafter_gb300 import binding
+    binding.sync_status()
+
+
+# ------------------------------------------------------------------ plan
+class Plan:
+    def __init__(self, length, fresh, held, width, page, free, n_rows, seed=0, in_place=True):
+        from block_drafter_gb300.paged import PageTables
+        r = random.Random(seed)
+        n = len(length)
+        real = [min(max(h, 0), width) for h in held]
+        total = sum(real) + free + 3
+        ids = list(range(total))
+        r.shuffle(ids)
+        self.table = np.full((n, width), -4, dtype=np.int32)
+        at = 0
+        for b, h in enumerate(real):
+            self.table[b, :h] = ids[at:at + h]
+            at += h
+        self.free = ids[at:at + free]
+        cu = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.args = (length, fresh, held, page, n_rows)
+        self.len, self.new, self.held = cu(length), cu(fresh), cu(held)
+        self.tab, self.stack, self.count = cu(self.table), cu(self.free + [-9] * (total - free)), cu([free])
+        self.held_out, self.count_out = (self.held, self.count) if in_place else (torch.full_like(self.held, -8), torch.full_like(self.count, -8))
+        self.seq, self.start = cu([-8] * n), cu([-8] * (n + 1))
+        self.req, self.pos, self.slot, self.short = cu([-8] * n_rows), cu([-8] * n_rows), cu([-8] * n_rows).long(), cu([-8])
+        self.tables = PageTables(self.tab, self.held, self.stack, self.count, page, held_out=self.held_out, free_count_out=self.count_out)
+
+    def run(self, give=True):
+        self.tables.plan(self.len, self.new, self.seq, self.start, self.pos, self.slot, row_request=self.req, n_short=self.short, give_back=give)
+
+    def check(self, give=True):
+        length, fresh, held, page, n_rows = self.args
+        w = T.plan(length, fresh, held, self.table, self.free, page, n_rows, give)
+        assert self.seq.tolist() == w["seq_len"] and self.start.tolist() == w["row_start"]
+        assert (self.req.cpu().numpy() == w["request"]).all() and (self.pos.cpu().numpy() == w["pos"]).all()
+        assert (self.slot.cpu().numpy() == w["slot"]).all()
+        assert (self.tab.cpu().numpy() == w["table"]).all()
+        assert self.held_out.tolist() == w["held"] and self.count_out.tolist() == [len(w["free"])]
+        assert self.stack[:len(w["free"])].tolist() == w["free"] and self.short.tolist() == [w["short"]]
+        return w
+
+
+PLANS = {
+    "one": ([0], [1], [0], 4, 16, 3, 1),
+    "one_empty": ([0], [0], [0], 1, 1, 1, 0),
+    "block": ([512, 3, 100, 64], [16, 16, 16, 16], [8, 1, 2, 1], 20, 64, 9, 64),
+    "dropped_rows": ([33, 0, 17, 64], [4, 0, 0, 1], [9, 5, 2, 5], 9, 16, 2, 12),
+    "taken_from_what_is_given": ([10, 0, 40, 16], [1, 30, 40, 0], [6, 0, 3, 4], 8, 16, 1, 80),
+    "short": ([16, 16, 16, 16, 5], [40, 1, 100, 1, 3], [1, 1, 1, 1, 1], 8, 16, 4, 200),
+    "nothing_free": ([16, 0, 15], [1, 1, 1], [1, 0, 1], 3, 16, 0, 3),
+    "page_of_one": ([3, 0], [2, 5], [3, 0], 9, 1, 7, 9),
+    "page_odd": ([32, 33, 34], [1, 1, 1], [1, 1, 2], 3, 33, 2, 3),
+    "large_pages": ([2 ** 20, 5], [7, 2 ** 10], [2, 1], 3, 2 ** 20, 2, 1100),
+}
+
+
+@pytest.mark.parametrize("give", [True, False])
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("name", list(PLANS))
+def test_plans_match_the_oracle(name, in_place, give):
+    p = Plan(*PLANS[name], in_place=in_place)
+    p.run(give)
+    sync()
+    p.check(give)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_large_plans(seed):
+    r = random.Random(seed)
+    n = [1024, 1023, 512, 513, 700, 31][seed]
+    page = r.choice([1, 7, 16, 64])
+    length = [r.randint(0, 40 * page) for _ in range(n)]
+    fresh = [r.choice([0, 1, 1, 16, r.randint(0, 300)]) for _ in range(n)]
+    held = [-(-x // page) + r.choice([0, 0, 1, 5]) for x in length]
+    width = max(max(held), max(-(-(a + b) // page) for a, b in zip(length, fresh)))
+    need = sum(max(0, -(-(a + b) // page) - h) for a, b, h in zip(length, fresh, held))
+    p = Plan(length, fresh, held, width, page, max(0, need - [0, 3, 10 ** 9, 0, need // 2, 0][seed]), sum(fresh) + 77, seed, in_place=seed % 2 == 0)
+    p.run()
+    sync()
+    w = p.check()
+    if seed in (1, 2, 4):
+        assert w["short"] >= (seed != 1)
+    if seed % 2:    # into other arrays: the same again
+        p.run()
+        sync()
+        p.check()
+
+
+@pytest.mark.parametrize("spoil", ["length", "fresh", "both", "held", "held_wide", "too_few_pages", "too_long", "rows"])
+def test_bad_requests_are_reported_and_the_others_planned(spoil):
+    from block_drafter_gb300 import binding as B
+    length, fresh, held, n_rows = [20, 40, 3], [5, 6, 7], [2, 5, 1], 18
+    if spoil in ("length", "both"):
+        length[1] = -1
+    if spoil in ("fresh", "both"):
+        fresh[1] = -2
+    if spoil == "held":
+        held[1] = -1
+    if spoil == "held_wide":
+        held[1] = 100
+    if spoil == "too_few_pages":
+        held[1] = 2
+    if spoil == "too_long":
+        fresh[1] = 2 ** 31 - 1 - 40
+    if spoil == "rows":
+        n_rows = 10                     # the second request's rows go past the end, and so do the third's
+    p = Plan(length, fresh, held, 6, 16, 4, n_rows)
+    p.run()
+    with pytest.raises(B.BdError) as err:
+        B.sync_status()
+    assert err.value.status == -1
+    B.sync_status()
+    w = p.check()
+    assert w["short"] >= 1 and w["seq_len"][0] == 25
+
+
+def test_a_stack_count_out_of_range_is_reported():
+    from block_drafter_gb300 import binding as B
+    for count in (-1, 1000):
+        p = Plan([16], [1], [1], 3, 16, 2, 1)
+        p.count.fill_(count)
+        p.run()
+        with pytest.raises(B.BdError):
+            B.sync_status()
+        assert p.seq.tolist() == [0] and p.short.tolist() == [1] and p.tab.tolist() == p.table.tolist()
+
+
+# ------------------------------------------------------------------ heads
+def heads_case(rows, hq, hkv, d, rotary, interleaved, dtype, far=5000, gains=True, seed=0):
+    g = torch.Generator().manual_seed(seed + rows * 7 + d)
+    t = TYPES[dtype]
+    x = (torch.randn(rows, hq + 2 * hkv, d, generator=g) * 2.0).to(t)
+    gain = [(1 + 0.2 * torch.randn(d, generator=g)).to(t) for _ in range(2)] if gains else [None, None]
+    freq = torch.tensor([1e4 ** (-2 * j / max(rotary, 1)) for j in range(rotary // 2)], dtype=torch.float64)
+    pos = torch.randint(0, far, (rows,), generator=g).int()
+    return x, gain, freq, pos
+
+
+def check_heads(got, x, gain, freq, pos, interleaved, eps=1e-6):
+    """Off by half a step of the type; the norm, gains and rotation in fp32 add a few 2^-23 of the pair's size: sum of D
+    squares D 2^-24, root and products 6 2^-24, cosine and sine and their angle (pi 2^-24 + 2 2^-24), all relative to it."""
+    t = got.dtype
+    want = T.head_norm_rope(x.double().numpy(), None if gain is None else gain.double().numpy(), eps, freq.tolist(), pos.tolist(), interleaved)
+    size = np.abs(T.head_norm_rope(x.double().numpy(), None if gain is None else gain.double().numpy(), eps, [], pos.tolist(), interleaved))
+    half, pair = len(freq), size.copy()
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    pair[..., a] = pair[..., b] = size[..., a] + size[..., b]
+    tiny = torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2
+    tol = torch.finfo(t).eps / 2 * np.abs(want) * (1 + 2.0 ** -10) + (x.shape[-1] + 16) * 2.0 ** -23 * pair + tiny
+    err = np.abs(got.double().cpu().numpy() - want) - tol
+    assert (err <= 0).all(), err.max()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rows,hq,hkv,d,rotary,dtype", [
+    (1, 1, 1, 128, 128, "bf16"), (1, 32, 8, 128, 128, "bf16"), (7, 5, 3, 64, 64, "fp16"), (3, 4, 2, 256, 256, "bf16"), (5, 9, 1, 128, 16, "bf16"),
+    (5, 3, 1, 256, 64, "fp16"), (4, 6, 2, 128, 96, "bf16"), (9, 2, 1, 64, 48, "fp16"), (2, 8, 8, 128, 0, "bf16"), (40, 7, 0, 64, 32, "bf16"),
+    (40, 0, 7, 128, 64, "fp16"), (1300, 2, 1, 64, 64, "bf16"), (2500, 1, 1, 128, 128, "fp16"), (5003, 1, 1, 64, 16, "bf16")])
+def test_heads_match_the_oracle(rows, hq, hkv, d, rotary, dtype, interleaved):
+    from block_drafter_gb300.target import HeadNormRope
+    x, gain, freq, pos = heads_case(rows, hq, hkv, d, rotary, interleaved, dtype)
+    dev = x.cuda()
+    q, k = dev[:, :hq] if hq else None, dev[:, hq:hq + hkv] if hkv else None
+    op = HeadNormRope(d, freq.cuda(), *(w.cuda() for w in gain), interleaved=interleaved)
+    outs = [None if s is None else torch.full(s.shape, -7.0, dtype=s.dtype, device="cuda") for s in (q, k)]
+    op(q, k, pos.cuda(), *outs)
+    sync()
+    assert torch.equal(dev.cpu(), x)
+    for out, a, b, w in ((outs[0], 0, hq, gain[0]), (outs[1], hq, hq + hkv, gain[1])):
+        if out is not None:
+            check_heads(out, x[:, a:b], w, freq, pos, interleaved)
+    op(q, k, pos.cuda())                                            # in place: the same bits, values untouched
+    sync()
+    for out, s in zip(outs, (q, k)):
+        assert out is None or torch.equal(out, s)
+    assert torch.equal(dev[:, hq + hkv:].cpu(), x[:, hq + hkv:])
+
+
+def test_heads_without_gains_and_rotation():
+    from block_drafter_gb300.target import HeadNormRope
+    x, gain, freq, pos = heads_case(6, 3, 2, 128, 64, False, "bf16")
+    q = x[:, :3].contiguous().cuda()
+    HeadNormRope(128, freq.cuda(), None, gain[1].cuda(), eps=1e-5)(q, None, pos.cuda())
+    sync()
+    check_heads(q, x[:, :3], None, freq, pos, False, eps=1e-5)
+    q = x[:, :3].contiguous().cuda()
+    HeadNormRope(128, None, None, None, dtype=torch.bfloat16)(q, None, pos.cuda())
+    sync()
+    check_heads(q, x[:, :3], None, freq[:0], pos, False)
+
+
+@pytest.mark.parametrize("rows", [6, 2000])
+def test_rows_of_no_request_are_left_as_they_were(rows):
+    from block_drafter_gb300.target import HeadNormRope
+    x, gain, freq, pos = heads_case(rows, 4, 2, 128, 128, False, "bf16")
+    pos[::3] = -1
+    dev = x.cuda()
+    HeadNormRope(128, freq.cuda(), *(w.cuda() for w in gain))(dev[:, :4], dev[:, 4:6], pos.cuda())
+    sync()
+    assert torch.equal(dev[::3].cpu(), x[::3])
+    live = pos >= 0
+    check_heads(dev[:, :4][live.cuda()], x[:, :4][live], gain[0], freq, pos[live], False)
+
+
+def test_angles_of_far_positions():
+    from block_drafter_gb300.target import HeadNormRope
+    x, gain, freq, _ = heads_case(8, 2, 1, 128, 128, False, "fp16")
+    pos = torch.tensor([0, 1, 2 ** 20 + 1, 2 ** 24 + 1, 2 ** 27 - 1, 2 ** 30, 2 ** 31 - 2, 2 ** 31 - 1], dtype=torch.int32)
+    q = x[:, :2].contiguous().cuda()
+    HeadNormRope(128, freq.cuda(), gain[0].cuda(), None)(q, None, pos.cuda())
+    sync()
+    # the oracle's angle pos * f is itself off by 2^-53 of up to 2^31: 2^-22
+    want = T.head_norm_rope(x[:, :2].double().numpy(), gain[0].double().numpy(), 1e-6, freq.tolist(), pos.tolist(), False)
+    assert np.abs(q.double().cpu().numpy() - want).max() <= (2.0 ** -11 + 2.0 ** -21) * np.abs(want).max()
+
+
+def test_zero_and_large_heads():
+    from block_drafter_gb300.target import HeadNormRope
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q[1] = 3e18
+    q[2] = float("nan")
+    pos = torch.tensor([5, 0, 1], dtype=torch.int32, device="cuda")
+    HeadNormRope(64, None, None, None, dtype=torch.bfloat16)(q, None, pos)
+    sync()
+    assert (q[0] == 0).all() and (q[1] == 1).all() and torch.isnan(q[2]).all()
+
+
+# ------------------------------------------------------------------ log probabilities
+def logprobs_of(x, tokens, k, temperature=1.0, pad=0, **kw):
+    from block_drafter_gb300.target import token_logprobs
+    rows, vocab = x.shape
+    wide = torch.full((rows, vocab + pad), float("nan"), dtype=x.dtype, device="cuda")
+    wide[:, :vocab] = x.cuda()
+    f = lambda *s: torch.full(s, -7.0, device="cuda")  # noqa: E731
+    lp, ent, lse, ids, alt = f(*tokens.shape), f(rows), f(rows), f(rows, k).int(), f(rows, k)
+    token_logprobs(wide[:, :vocab], tokens.cuda(), lp, entropy=ent, lse=lse, top_ids=ids, top_logprob=alt, temperature=temperature, **kw)
+    return lp, ent, lse, ids, alt
+
+
+def check_logprobs(x, tokens, k, got, temperature=1.0):
+    """fp32: z = x / T and differences of two are off by a few 2^-24 of the largest |z|, sums of n exponentials by
+    (n / 512 + 32) 2^-24 (512 threads' sums and their tree) and 2^-21 for the exponential; the entropy takes both
+    and the same of a mean over at most 60."""
+    lp, ent, lse, ids, alt = (v.cpu().numpy() for v in got)
+    rows, vocab = x.shape
+    for r in range(rows):
+        row = x[r].double().numpy()
+        a, e, l, order, tops = T.token_logprobs(row, tokens[r].reshape(-1).tolist(), temperature, k)
+        assert ids[r].tolist() == order, r
+        z = np.abs(row[np.isfinite(row)] / temperature)
+        tol = 8 * 2.0 ** -24 * (z.max() if z.size else 0) + (vocab / 512 + 32) * 2.0 ** -24 + 2.0 ** -21
+        for g, w in list(zip(lp[r].reshape(-1), a)) + [(lse[r], l)] + list(zip(alt[r], tops)):
+            assert (np.isnan(g) and np.isnan(w)) or g == w or abs(g - w) <= tol, (r, g, w, tol)
+        assert (np.isnan(ent[r]) and np.isnan(e)) or abs(ent[r] - e) <= 64 * tol, (r, ent[r], e)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,vocab,k,n,pad", [
+    (1, 1, 1, 1, 0), (1, 2, 2, 1, 0), (3, 7, 5, 2, 1), (2, 33, 32, 1, 0), (5, 511, 8, 1, 3), (4, 1000, 20, 3, 0), (3, 4099, 1, 1, 1), (2, 8192, 5, 64, 0),
+    (1, 151936, 20, 1, 0), (3, 50257, 32, 2, 2), (200, 2000, 5, 1, 0), (9, 30001, 0, 1, 5), (1, 100003, 32, 1, 0)])
+def test_logprobs_match_the_oracle(rows, vocab, k, n, pad, dtype):
+    g = torch.Generator().manual_seed(vocab)
+    x = (torch.randn(rows, vocab, generator=g) * 3).to(dtype)
+    tokens = torch.randint(0, vocab, (rows, n), generator=g).int()
+    temperature = [1.0, 0.6, 1.7][vocab % 3]
+    got = logprobs_of(x, tokens, k, temperature, pad)
+    sync()
+    check_logprobs(x, tokens, k, got, temperature)
+    again = logprobs_of(x, tokens, k, temperature, pad)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("kind", ["same", "ascending", "descending", "two_values", "few_finite", "lowest", "lowest_and_one", "zeros_of_both_signs", "huge"])
+@pytest.mark.parametrize("rows,vocab,k", [(1, 20000, 20), (400, 5000, 7), (2, 140001, 32)])
+def test_logprobs_of_equal_sorted_and_masked_logits(kind, rows, vocab, k):
+    g = torch.Generator().manual_seed(1)
+    x = torch.zeros(1, vocab)
+    if kind == "same":
+        x += 3.25
+    elif kind == "ascending":
+        x = torch.arange(vocab).float()[None] / vocab * 20
+    elif kind == "descending":
+        x = -torch.arange(vocab).float()[None] / vocab * 20
+    elif kind == "two_values":
+        x = torch.randint(0, 2, (1, vocab), generator=g).float()
+    elif kind == "few_finite":
+        x += float("-inf")
+        x[0, ::vocab // 5] = torch.arange(x[0, ::vocab // 5].numel()).float()
+    elif kind in ("lowest", "lowest_and_one"):
+        x += torch.finfo(torch.float32).min
+        if kind == "lowest_and_one":
+            x[0, 77] = 1.0
+    elif kind == "zeros_of_both_signs":
+        x[0, ::2] = -0.0
+    else:
+        x = torch.randn(1, vocab, generator=g) * 1e30
+    x = x.expand(rows, vocab).contiguous()
+    tokens = torch.tensor([[0, vocab - 1, 77]]).expand(rows, 3).contiguous().int()
+    got = logprobs_of(x, tokens, k)
+    sync()
+    # rows of an odd vocabulary begin at other places within 16 bytes, which changes the order of their sums: each row
+    # is within the tolerance by itself, and every fourth fp32 row begins where the first one does
+    check_logprobs(x[:2], tokens[:2], k, tuple(v[:2] for v in got))
+    for v in got:
+        assert torch.equal(v[::4], v[:1].expand_as(v[::4]))
+    assert torch.equal(got[3], got[3][:1].expand_as(got[3]))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("vocab", [100, 70000])
+def test_rows_that_are_no_distribution(bad, vocab):
+    x = torch.randn(4, vocab, generator=torch.Generator().manual_seed(2))
+    x[1, vocab // 2] = bad
+    x[2] = float("-inf")
+    x[3, 5:] = float("nan")
+    tokens = torch.zeros(4, 1, dtype=torch.int32)
+    got = logprobs_of(x, tokens, 10)
+    sync()
+    check_logprobs(x, tokens, 10, got)
+    assert torch.isneginf(got[2][2]) and torch.isnan(got[0][1:]).all() and not torch.isnan(got[0][0]).any()
+
+
+def test_missing_and_bad_tokens():
+    from block_drafter_gb300 import binding as B
+    x = torch.randn(2, 50, generator=torch.Generator().manual_seed(2))
+    got = logprobs_of(x, torch.tensor([[-1, 3], [4, -1]]).int(), 2)
+    sync()
+    assert got[0][0, 0] == 0 and got[0][1, 1] == 0
+    check_logprobs(x, torch.tensor([[-1, 3], [4, -1]]).int(), 2, got)
+    got = logprobs_of(x, torch.tensor([[50, 3], [4, -2]]).int(), 2)
+    with pytest.raises(B.BdError) as err:
+        B.sync_status()
+    assert err.value.status == -1 and torch.isnan(got[0][0, 0]) and torch.isnan(got[0][1, 1]) and torch.isfinite(got[0][0, 1])
+
+
+def test_logprobs_alone_and_of_one_token_a_row():
+    from block_drafter_gb300.target import token_logprobs
+    x = torch.randn(5, 3000, generator=torch.Generator().manual_seed(2))
+    full = logprobs_of(x, torch.full((5, 1), 7).int(), 3)
+    lp = torch.zeros(5, device="cuda")
+    token_logprobs(x.cuda(), torch.full((5,), 7).int().cuda(), lp)
+    ids = torch.zeros(5, 3, dtype=torch.int32, device="cuda")
+    token_logprobs(x.cuda(), None, None, top_ids=ids)
+    sync()
+    assert torch.equal(lp, full[0][:, 0]) and torch.equal(ids, full[3])
