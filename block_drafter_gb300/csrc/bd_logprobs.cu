@@ -1,20 +1,25 @@
 // Log probabilities of given tokens, entropy and top alternatives (bd_token_logprobs).
 //
-// One pass over a row's logits x with the running maximum m of a softmax, c = log2(e) / temperature:
-//   s = sum 2^d,  t = sum 2^d d,  d = (x - m) c;   m -> m':  w = 2^((m-m') c),  t' = w (t + s (m-m') c),  s' = w s
-//   lse = m c ln2 + ln s,  entropy = ln2 (log2 s - t / s),  logprob = (x_token - m) c ln2 - ln s.
-// The entropy is formed from d <= 0 and not as lse minus a mean: nothing large cancels.
+// One pass over a row's logits x, c = log2(e) / temperature, against a reference m near their maximum, r = m c:
+//   s = sum 2^d,  t = sum 2^d d,  d = x c - r;   m -> m':  w = 2^(r-r'),  t' = w (t + s (r-r')),  s' = w s
+//   lse = ln2 r + ln s,  entropy = ln2 (log2 s - t / s),  logprob = ln2 (x_token c - r) - ln s.
+// The entropy is formed from d and not as lse minus a mean: nothing large cancels.  A thread moves its reference only when a
+// logit is 16 above it (in log2 units).  The sums are against r as it is rounded, so that its rounding is in no result;
+// where it rounds by more than 2^-8 (or overflows: rows of the type's lowest value alone) d is (x - m) c.  Logits 150 below the
+// reference are raised to that: their weight is 0, and that of -inf is no 0 times infinity.
 //
-// The largest logits come out of the same pass: a block keeps those that reach its threshold in a buffer, as keys
-// that order by value, then by the lower id; now and then it thins the buffer to the top_k largest, the last of which is
-// the next threshold.  The first threshold is the top_k-th largest of the threads' maxima over the row's first
-// logits, which the threads still hold then; so of 152 000 logits a few hundred reach the buffer.  Where more reach it than
-// it holds (values in ascending order, many equal ones), the round is done again with the threshold that the buffer
-// gives, which is larger each time.
+// The largest logits come out of the same pass: a thread puts a 16-byte vector that holds a logit at or above the block's
+// threshold aside, in shared memory, which is all that the loop over the row does for them.  Twice the logits of the vectors
+// aside are made keys, which order by value, then by the lower id, and thinned to the top_k largest, the last of which is
+// the next threshold.  The first threshold is the top_k-th largest of 64 maxima of 32 or 64 logits each, the first ones
+// that the threads read; so of 152 000 logits about two hundred get aside.  Where more do than there is room for
+// (values in ascending order, many equal ones), the round is done again with the threshold that those aside give,
+// which is larger each time.
 //
 // Few rows are a cluster's of up to 16 blocks, each with an equal part of the row; the first one joins their sums and
 // candidates through distributed shared memory.  Bound by the bytes of the logits.
 #include <cfloat>
+#include <climits>
 
 #include "bd_checks.h"
 #include "bd_paged_device.cuh"
@@ -32,6 +37,7 @@ constexpr int kLpEach = 4;  // vectors of a thread in flight
 constexpr int kTop = BD_LOGPROB_TOP_MAX;
 constexpr int kKeys = 512;             // candidates that a block thins at once, a thread each
 constexpr int kBuffer = kKeys - kTop;  // those of a round, beside the ones kept before
+constexpr int kAside = 512;            // vectors that a block puts aside in a round, one a thread to make keys of
 static_assert(kLpCluster * kTop <= kKeys && kKeys <= kLpThreads, "the joining block thins every block's candidates");
 
 struct LogprobArgs {
@@ -46,27 +52,68 @@ struct LogprobArgs {
   float *top_logprob;
 };
 
-// 16 bytes of logits as fp32.
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN where one is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 16 bytes of logits: their maximum (NaN counts as -inf), and as fp32, those below `floor` raised to it.
 template <typename T> struct Vec {
-  static constexpr int N = 16 / sizeof(T);
-  static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[N]) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = Pair<T>::unpack(v[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+  static constexpr int N = 8;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (std::is_same<T, __half>::value) asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (std::is_same<T, __half>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float most(const uint4 &w) {
+    const float2 m = Pair<T>::unpack(max2(max2(w.x, w.y), max2(w.z, w.w)));
+    return fmaxf(fmaxf(m.x, m.y), -INFINITY);
+  }
+  static constexpr float kLowest = std::is_same<T, __half>::value ? -65504.f : -1e38f;
+  static __device__ __forceinline__ uint32_t floor_of(float f) { return Pair<T>::pack(f, f); }
+  static __device__ __forceinline__ void unpack(const uint4 &w, uint32_t floor, float2 (&x)[4]) {
+    x[0] = Pair<T>::unpack(max2_nan(w.x, floor));
+    x[1] = Pair<T>::unpack(max2_nan(w.y, floor));
+    x[2] = Pair<T>::unpack(max2_nan(w.z, floor));
+    x[3] = Pair<T>::unpack(max2_nan(w.w, floor));
+  }
+  // Its first element; the others move up.
+  static __device__ __forceinline__ float next(uint4 &w) {
+    const float x = Pair<T>::unpack(w.x).x;
+    w.x = __funnelshift_r(w.x, w.y, 16), w.y = __funnelshift_r(w.y, w.z, 16), w.z = __funnelshift_r(w.z, w.w, 16), w.w >>= 16;
+    return x;
+  }
+  static __device__ __forceinline__ uint4 nothing() {  // -inf
+    const uint32_t x = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(x, x, x, x);
   }
 };
 template <> struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[4]) {
-    x[0] = __uint_as_float(w.x);
-    x[1] = __uint_as_float(w.y);
-    x[2] = __uint_as_float(w.z);
-    x[3] = __uint_as_float(w.w);
+  static __device__ __forceinline__ float most(const uint4 &w) {
+    return fmaxf(fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w))), -INFINITY);
   }
+  static constexpr float kLowest = -1e38f;
+  static __device__ __forceinline__ uint32_t floor_of(float f) { return __float_as_uint(f); }
+  static __device__ __forceinline__ void unpack(const uint4 &w, uint32_t floor, float2 (&x)[2]) {
+    const float f = __uint_as_float(floor);
+    x[0] = make_float2(max_nan(__uint_as_float(w.x), f), max_nan(__uint_as_float(w.y), f));
+    x[1] = make_float2(max_nan(__uint_as_float(w.z), f), max_nan(__uint_as_float(w.w), f));
+  }
+  static __device__ __forceinline__ float next(uint4 &w) {
+    const float x = __uint_as_float(w.x);
+    w = make_uint4(w.y, w.z, w.w, 0);
+    return x;
+  }
+  static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
 // Larger for larger values, among equal ones for lower ids (-0 is 0, NaN counts as -inf).
@@ -80,12 +127,6 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ int key_id(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN where one is
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
   uint64_t v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
@@ -93,11 +134,18 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 }
 
 struct Sums {
-  float m, s, t;
+  float m, s, t;  // the reference (-FLT_MAX: nothing but -inf so far), and the two sums against it
 };
+constexpr float kLarge = 65536.f;  // a larger r is not multiplied out: it rounds by more than 2^-8
+constexpr float kNothing = 150.f;  // 2^-150 is 0
+// Exponent between two references, at most 0 where `to` is the larger one.
+__device__ __forceinline__ float between(float from, float to, float c) {
+  const float r = to * c, d = fabsf(r) < kLarge ? from * c - r : (from - to) * c;
+  return fmaxf(d, -kNothing);
+}
 __device__ __forceinline__ void rescale(Sums &a, float m, float c) {  // m >= a.m
   if (m == a.m) return;
-  const float d = fmaxf((a.m - m) * c, -150.f), w = exp2_fast(d);
+  const float d = between(a.m, m, c), w = exp2_fast(d);
   a.t = w * (a.t + a.s * d);
   a.s *= w;
   a.m = m;
@@ -125,15 +173,40 @@ __device__ __forceinline__ void thin(uint64_t *keys, int n, int k) {
   __syncthreads();
 }
 
+// The same of `lists` lists of k keys in descending order each, side by side.
+__device__ __forceinline__ void thin_lists(uint64_t *keys, int lists, int k) {
+  __syncthreads();
+  const int i = threadIdx.x;
+  uint64_t mine = 0;
+  int rank = k;
+  if (i < lists * k) {
+    mine = keys[i];
+    rank = 0;
+    for (int b = 0; b < lists; ++b) {  // how many of list b are larger
+      int lo = 0, hi = k;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (keys[b * k + mid] > mine) lo = mid + 1; else hi = mid;
+      }
+      rank += lo;
+    }
+  }
+  __syncthreads();
+  if (rank < k && mine != 0) keys[rank] = mine;  // 0 fills up lists that are shorter
+  __syncthreads();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_constant__ LogprobArgs A) {
   using V = Vec<T>;
-  constexpr int N = V::N;
+  constexpr int N = V::N, GROUPS = 64;
   __shared__ __align__(16) uint64_t keys[kKeys], best[kTop];  // this round's candidates; those kept before
-  __shared__ __align__(16) float top_of[kLpThreads];  // the threads' maxima
+  __shared__ __align__(16) float group_top[GROUPS];  // maxima of eight threads' first logits
   __shared__ Sums warp_sums[kLpWarps];
   __shared__ Sums block_sums;
-  __shared__ int count;
+  __shared__ __align__(16) uint4 aside[kAside];      // vectors with candidates,
+  __shared__ int aside_at[kAside];                   // their numbers
+  __shared__ int count, aside_count;
   __shared__ uint64_t first_threshold;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / static_cast<uint32_t>(A.cluster), rank = blockIdx.x - row * A.cluster, k = A.top_k;
@@ -145,131 +218,197 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
   const int v0 = static_cast<int>(static_cast<int64_t>(vecs) * rank / A.cluster);
   const int v1 = static_cast<int>(static_cast<int64_t>(vecs) * (rank + 1) / A.cluster);
-  if (tid == 0) count = 0;
+  if (tid == 0) {
+    count = aside_count = 0;
+    first_threshold = 0;
+  }
   pdl_wait();
   pdl_trigger();
+  uint64_t threshold = 0;   // of the keys that are kept
+  float reach = -INFINITY;  // its value
+  int reach_id = INT_MAX;   // its id
   Sums a = {-FLT_MAX, 0.f, 0.f};
-  uint64_t threshold = 0;  // of the keys that are kept
-  float reach = -INFINITY; // its value
+  uint64_t s2 = 0, t2 = 0;                 // the sums, in two halves
+  float minus_r = 0.f, limit = -FLT_MAX;   // -r; what moves the reference
+  uint32_t floor = 0;
+  bool far = true, slow = true;            // r is not multiplied out; or `floor` is no number of the type
 
-  auto add = [&](const auto &v) {
-    constexpr int n = sizeof(v) / sizeof(v[0]);
-    float m = a.m;
-#pragma unroll
-    for (int e = 0; e < n; ++e) m = fmaxf(m, v[e]);
+  auto fold = [&]() {
+    const float2 s = unpair(s2), t = unpair(t2);
+    a.s += s.x + s.y;
+    a.t += t.x + t.y;
+    s2 = t2 = 0;
+  };
+  auto refer = [&](float m) {
+    fold();
     rescale(a, m, c);
+    const float r = m * c;
+    const float low = (r - kNothing) / c;
+    far = !(fabsf(r) < kLarge);
+    slow = far || low < V::kLowest;
+    minus_r = -r;
+    limit = far ? m : (r + 16.f) / c;
+    floor = V::floor_of(low);
+  };
+  auto add_one = [&](float y) {
+    if (y > limit) refer(y);
+    const float d = max_nan(far ? (y - a.m) * c : fmaf(y, c, minus_r), -kNothing), w = exp2_fast(d);
+    a.s += w;
+    a.t = fmaf(w, d, a.t);
+  };
+  auto add = [&](const uint4 &w) {  // none of it above `limit`
+    float2 y[N / 2];
+    if (!slow) {
+      V::unpack(w, floor, y);
+      const uint64_t c2 = pair(c, c), r2 = pair(minus_r, minus_r);
 #pragma unroll
-    for (int e = 0; e < n; ++e) {
-      const float d = max_nan((v[e] - a.m) * c, -150.f), w = exp2_fast(d);
-      a.s += w;
-      a.t = fmaf(w, d, a.t);
+      for (int e = 0; e < N / 2; ++e) {
+        const uint64_t d = fma2(pair(y[e].x, y[e].y), c2, r2);
+        const float2 z = unpair(d);
+        const uint64_t p = pair(exp2_fast(z.x), exp2_fast(z.y));
+        s2 = add2(s2, p);
+        t2 = fma2(p, d, t2);
+      }
+    } else {
+      uint4 x = w;
+#pragma unroll 1
+      for (int e = 0; e < N; ++e) add_one(V::next(x));
     }
   };
   auto offer = [&](float v, int id) {
-    if (!(v >= reach) && v == v) return;
+    if (v < reach) return;  // a NaN counts as -inf by its key
     const uint64_t key = key_of(v, id);
     if (key < threshold) return;
     const int at = atomicAdd(&count, 1);
     if (at < kBuffer) keys[at] = key;
   };
+  // Whether vector i, of the largest logit m, may hold a key at or above the threshold.  Of those put aside all but one (that
+  // of the threshold's own id) do, so a round that is done again finds fewer each time.
+  auto reaches = [&](float m, int i) { return m > reach || (m == reach && head + i * N <= reach_id); };
+  auto put_aside = [&](const uint4 &w, int i) {
+    const int at = atomicAdd(&aside_count, 1);
+    if (at < kAside) {
+      aside[at] = w;
+      aside_at[at] = i;
+    }
+  };
   // the loose elements
-  float one[1], &loose = one[0];
+  float loose = 0.f;
   int loose_id = -1;
   if (rank == 0) {
     if (tid < head) loose_id = tid;
     else if (tid - head < A.vocab - tail) loose_id = tail + tid - head;
-    if (loose_id >= 0) {
-      loose = to_f<T>(x[loose_id]);
-      add(one);
-    }
+    if (loose_id >= 0) loose = to_f<T>(x[loose_id]);
   }
   // the first vector of every thread, which gives the first threshold
-  float v[N];
-  int at = v0 + tid;
-  const bool has = at < v1;
+  uint4 first = make_uint4(0, 0, 0, 0);
+  const bool has = v0 + tid < v1;
+  if (has) first = __ldg(xv + v0 + tid);
+  if (loose_id >= 0) add_one(loose);
+  float m0 = -INFINITY;
   if (has) {
-    V::unpack(__ldg(xv + at), v);
-    add(v);
+    m0 = V::most(first);
+    if (m0 > limit) refer(m0);
+    add(first);
   }
-  __syncthreads();
   if (k > 0) {
-    if (tid == 0) first_threshold = 0;
-    float m = -INFINITY;
-    if (has)
+    float m = m0;
 #pragma unroll
-      for (int e = 0; e < N; ++e) m = fmaxf(m, v[e]);
-    top_of[tid] = m;
+    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (tid % 8 == 0) group_top[tid / 8] = m;
     __syncthreads();
-    int larger = 0;
-    for (int j = 0; j < kLpThreads; j += 4) {
-      const float4 o = *reinterpret_cast<const float4 *>(top_of + j);
-      larger += (o.x > m || (o.x == m && j < tid)) + (o.y > m || (o.y == m && j + 1 < tid)) + (o.z > m || (o.z == m && j + 2 < tid)) +
-                (o.w > m || (o.w == m && j + 3 < tid));
+    if (tid < GROUPS) {
+      m = group_top[tid];
+      int larger = 0;
+#pragma unroll
+      for (int j = 0; j < GROUPS; j += 4) {
+        const float4 o = *reinterpret_cast<const float4 *>(group_top + j);
+        larger += (o.x > m || (o.x == m && j < tid)) + (o.y > m || (o.y == m && j + 1 < tid)) + (o.z > m || (o.z == m && j + 2 < tid)) +
+                  (o.w > m || (o.w == m && j + 3 < tid));
+      }
+      // k logits are at least this: no smaller value is among the k largest
+      if (larger == k - 1) first_threshold = key_of(m, 0x7fffffff);
     }
-    // k maxima are at least this: no smaller value is among the k largest
-    if (larger == k - 1) first_threshold = key_of(m, 0x7fffffff);
     __syncthreads();
     threshold = first_threshold;
     reach = key_value(threshold);
+    if (has && reaches(m0, v0 + tid)) put_aside(first, v0 + tid);
   }
-  // rounds: the first vectors and loose elements, an eighth of the rest, the rest
-  const int from = v0 + kLpThreads, rest = max(0, v1 - from), cut = from + rest / 8;
-  int kept = 0;  // candidates of the rounds before
-  for (int round = 0; round < 3; ++round) {
-    const int r0 = round == 2 ? cut : from, r1 = round == 0 ? from : round == 1 ? cut : from + rest;
+  // two rounds, or one of a short part: up to an eighth of it, the rest
+  const int from = v0 + kLpThreads, rest = max(0, v1 - from), cut = rest > 2 * kLpEach * kLpThreads ? from + rest / 8 : from + rest;
+  int kept = 0;  // candidates of the round before
+  for (int round = 0; round < 2; ++round) {
+    int r0 = round == 0 ? from : cut;
+    const int r1 = min(v1, round == 0 ? cut : from + rest);
+    if (round == 1 && r0 >= r1) break;
     for (bool again = false;;) {
-      if (round == 0) {
-        if (k > 0) {
-          if (loose_id >= 0) offer(loose, loose_id);
-          if (has)
-#pragma unroll
-            for (int e = 0; e < N; ++e) offer(v[e], head + at * N + e);
+      if (again) {
+        // Every thread a stretch of its own, so that those that come first are from all over the round: of m vectors, in
+        // whatever order their values are, about m k / kAside reach the next threshold.
+        const int64_t len = r1 - r0;
+        const int e = r0 + static_cast<int>(len * (tid + 1) / kLpThreads);
+        for (int i = r0 + static_cast<int>(len * tid / kLpThreads); i < e; ++i) {
+          const uint4 w = __ldg(xv + i);
+          if (reaches(V::most(w), i)) put_aside(w, i);
         }
       } else {
         for (int i = r0 + tid; i < r1; i += kLpEach * kLpThreads) {
           uint4 w[kLpEach];
+          float m[kLpEach], top = -INFINITY;
+          const bool whole = i + (kLpEach - 1) * kLpThreads < r1;
 #pragma unroll
           for (int u = 0; u < kLpEach; ++u)
-            if (i + u * kLpThreads < r1) w[u] = __ldg(xv + i + u * kLpThreads);
+            if (whole || i + u * kLpThreads < r1) w[u] = __ldg(xv + i + u * kLpThreads);
+            else w[u] = V::nothing();
 #pragma unroll
           for (int u = 0; u < kLpEach; ++u) {
-            if (i + u * kLpThreads >= r1) continue;
-            float y[N];
-            V::unpack(w[u], y);
-            if (!again) add(y);
-            if (k > 0) {
-              float m = y[0];
-#pragma unroll
-              for (int e = 1; e < N; ++e) m = fmaxf(m, y[e]);
-              if (!(m < reach)) {
-#pragma unroll 1
-                for (int e = 0; e < N; ++e) offer(y[e], head + (i + u * kLpThreads) * N + e);
-              }
-            }
+            m[u] = V::most(w[u]);
+            top = fmaxf(top, m[u]);
           }
+          if (top > limit) refer(top);
+#pragma unroll
+          for (int u = 0; u < kLpEach; ++u) add(w[u]);
+#pragma unroll
+          for (int u = 0; u < kLpEach; ++u)
+            if (k > 0 && reaches(m[u], i + u * kLpThreads) && (whole || i + u * kLpThreads < r1)) put_aside(w[u], i + u * kLpThreads);
         }
       }
       if (k == 0) break;
       __syncthreads();
-      const int n = count;
-      again = n > kBuffer;
-      if (again) {  // k of those in the buffer are at least the next threshold
-        thin(keys, kBuffer, k);
-      } else {
-        if (tid < kept) keys[n + tid] = best[tid];
-        thin(keys, n + kept, k);
-        kept = min(n + kept, k);
-        if (tid < kept) best[tid] = keys[tid];
+      const int n = aside_count;
+      again = n > kAside;
+      for (bool full = true; full;) {  // keys of those aside
+        if (tid < min(n, kAside)) {
+          uint4 w = aside[tid];
+          const int id = head + aside_at[tid] * N;
+#pragma unroll 1
+          for (int e = 0; e < N; ++e) offer(V::next(w), id + e);
+        }
+        if (loose_id >= 0 && round == 0) offer(loose, loose_id);
+        __syncthreads();
+        const int found = count;
+        full = found > kBuffer;
+        if (!full && !again && tid < kept) keys[found + tid] = best[tid];
+        const int all = full ? kBuffer : again ? found : found + kept;
+        thin(keys, all, k);
+        if (all >= k) {  // k of them are at least the next threshold
+          threshold = max(threshold, keys[k - 1]);
+          reach = key_value(threshold);
+          reach_id = key_id(threshold);
+        }
+        if (!full && !again) {
+          kept = min(all, k);
+          if (tid < kept) best[tid] = keys[tid];
+        }
+        __syncthreads();
+        if (tid == 0) count = aside_count = 0;
+        __syncthreads();
       }
-      if (again || kept == k) {
-        threshold = max(threshold, keys[k - 1]);
-        reach = key_value(threshold);
-      }
-      if (tid == 0) count = 0;
-      __syncthreads();
       if (!again) break;
+      if (round == 0) r0 = v0;  // the first vectors, too
     }
   }
+  fold();
   // the block's sums
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -279,9 +418,17 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   if (lane == 0) warp_sums[warp] = a;
   if (tid < k && tid >= kept) best[tid] = 0;  // below every key
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kLpWarps; ++w) a = join(a, warp_sums[w], c);
-    block_sums = a;
+  auto join_sums = [&](int n) {  // of the first n <= 16 lanes
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const Sums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.t, o)};
+      a = join(a, b, c);
+    }
+    if (lane == 0) block_sums = a;
+  };
+  if (warp == 0) {
+    a = warp_sums[lane % kLpWarps];
+    join_sums(kLpWarps);
   }
   __syncthreads();
   if (A.cluster > 1) {
@@ -290,29 +437,36 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
       const int from_block = k > 0 ? tid / k : A.cluster, which = tid - from_block * k;
       uint64_t key = 0;
       if (from_block < A.cluster) key = ld_cluster_u64(cluster_map(smem_u32(best + which), from_block));
-      if (tid == 0)
-        for (int b = 1; b < A.cluster; ++b) {
-          const uint32_t p = cluster_map(smem_u32(&block_sums), b);
-          a = join(a, {ld_cluster_f32(p), ld_cluster_f32(p + 4), ld_cluster_f32(p + 8)}, c);
+      if (warp == 0) {
+        a = {-FLT_MAX, 0.f, 0.f};
+        if (lane < A.cluster) {
+          const uint32_t p = cluster_map(smem_u32(&block_sums), lane);
+          a = {ld_cluster_f32(p), ld_cluster_f32(p + 4), ld_cluster_f32(p + 8)};
         }
+        __syncwarp();  // its own sums are read before they are replaced
+        join_sums(A.cluster);
+      }
       if (k > 0) {
         if (from_block < A.cluster) keys[tid] = key;
-        thin(keys, A.cluster * k, k);
+        thin_lists(keys, A.cluster, k);
         if (tid < k) best[tid] = keys[tid];
       }
-      if (tid == 0) block_sums = a;
     }
     __syncthreads();
     cluster_sync();  // every block's sums and candidates are read
     if (rank != 0) return;
   }
-  const Sums r = block_sums;
-  const float ln_s = logf(r.s);
+  const Sums all = block_sums;
+  const float r = all.m * c, ln_s = logf(all.s);
+  far = !(fabsf(r) < kLarge);
   if (tid == 0) {
-    if (A.lse) A.lse[row] = r.m * A.inv_t + ln_s;
-    if (A.entropy) A.entropy[row] = ln_s - kLn2 * (r.t / r.s);
+    if (A.lse) A.lse[row] = all.s == 0.f ? -INFINITY : far ? all.m * A.inv_t + ln_s : kLn2 * r + ln_s;
+    if (A.entropy) A.entropy[row] = ln_s - kLn2 * (all.t / all.s);
   }
-  auto logprob = [&](float z) { return r.s == 0.f ? NAN : (z - r.m) * A.inv_t - ln_s; };
+  auto logprob = [&](float z) {
+    const float d = fmaf(z, c, -r);
+    return all.s == 0.f ? NAN : (far || isinf(d) ? (z - all.m) * A.inv_t : kLn2 * d) - ln_s;
+  };
   if (tid < k) {
     const uint64_t key = best[tid];
     A.top_ids[static_cast<int64_t>(row) * k + tid] = key_id(key);
@@ -352,9 +506,8 @@ extern "C" bd_status bd_token_logprobs(const void *logits, int64_t row_stride, i
     return refuse(BD_ERR_INVALID_ARG, "log probabilities: rows must be in 0..2^24 and vocab in 1..2^24");
   if (n_given < 0 || n_given > BD_LOGPROB_GIVEN_MAX || top_k < 0 || top_k > kTop || top_k > vocab)
     return refuse(BD_ERR_INVALID_ARG, "log probabilities: n_given must be in 0..64, top_k in 0..32 and at most vocab");
-  const float scale = static_cast<float>(1.4426950408889634 / temperature), inv_t = static_cast<float>(1.0 / temperature);
-  if (!(temperature > 0.f) || !std::isnormal(scale) || !std::isnormal(inv_t))
-    return refuse(BD_ERR_INVALID_ARG, "log probabilities: temperature and its reciprocal must be > 0 and finite");
+  if (!(temperature >= 0x1p-20f && temperature <= 0x1p20f))
+    return refuse(BD_ERR_INVALID_ARG, "log probabilities: temperature must be in 2^-20..2^20");
   if (rows == 0) return BD_OK;
   const int64_t size = dtype == BD_F32 ? 4 : 2;
   if (!logits || misaligned(logits, size) || (rows > 1 && row_stride < vocab))
@@ -381,8 +534,8 @@ extern "C" bd_status bd_token_logprobs(const void *logits, int64_t row_stride, i
   A.row_stride = rows > 1 ? row_stride : 0;
   A.rows = rows;
   A.vocab = vocab;
-  A.scale = scale;
-  A.inv_t = inv_t;
+  A.scale = static_cast<float>(1.4426950408889634 / temperature);
+  A.inv_t = static_cast<float>(1.0 / temperature);
   A.tokens = tokens;
   A.n_given = n_given;
   A.top_k = top_k;

@@ -694,7 +694,7 @@ bd_status bd_head_norm_rope(const bd_head_rope *c, int n_rows, const int32_t *po
  *   entropy, lse dev fp32 [rows] OUT, or NULL
  *   top_ids      dev int32 [rows, top_k] OUT;  top_logprob dev fp32 [rows, top_k] OUT, or NULL;
  *                top_k 0 .. BD_LOGPROB_TOP_MAX and <= vocab
- * rows 0 .. 2^24, vocab 1 .. 2^24, temperature > 0 and finite.  Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED
+ * rows 0 .. 2^24, vocab 1 .. 2^24, temperature 2^-20 .. 2^20.  Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED
  * (dtype).
  */
 #define BD_LOGPROB_TOP_MAX 32
