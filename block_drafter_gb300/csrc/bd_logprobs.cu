@@ -44,7 +44,7 @@ struct LogprobArgs {
   const void *logits;
   int64_t row_stride;
   int rows, vocab, cluster;
-  float scale, inv_t;  // log2(e) / temperature, 1 / temperature
+  float scale, inv_scale, inv_t;  // log2(e) / temperature, its reciprocal, 1 / temperature
   const int32_t *tokens;
   int n_given, top_k;
   float *logprob, *entropy, *lse;
@@ -243,11 +243,11 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     fold();
     rescale(a, m, c);
     const float r = m * c;
-    const float low = (r - kNothing) / c;
+    const float low = (r - kNothing) * A.inv_scale;
     far = !(fabsf(r) < kLarge);
     slow = far || low < V::kLowest;
     minus_r = -r;
-    limit = far ? m : (r + 16.f) / c;
+    limit = far ? m : (r + 16.f) * A.inv_scale;
     floor = V::floor_of(low);
   };
   auto add_one = [&](float y) {
@@ -535,6 +535,7 @@ extern "C" bd_status bd_token_logprobs(const void *logits, int64_t row_stride, i
   A.rows = rows;
   A.vocab = vocab;
   A.scale = static_cast<float>(1.4426950408889634 / temperature);
+  A.inv_scale = static_cast<float>(temperature / 1.4426950408889634);
   A.inv_t = static_cast<float>(1.0 / temperature);
   A.tokens = tokens;
   A.n_given = n_given;

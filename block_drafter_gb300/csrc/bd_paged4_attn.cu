@@ -28,7 +28,7 @@ BD_DEFINE_ERROR_TAKER(take_error_word_paged4_attn)
 
 namespace {
 
-constexpr int kAhead = 2;     // units of a warp on their way
+constexpr int kAhead = 3;     // units of a warp on their way
 constexpr float kHead = 6.f;  // weights are formed against 2^-kHead of the reference: at most 2^14
 constexpr float kMove = 8.f;
 
@@ -67,9 +67,11 @@ template <int N> __device__ __forceinline__ void load_words(uint32_t (&w)[N], co
   }
 }
 
-// The part of one (request, KV head) over tiles [t0, t1) by one warp (every kFewWarps-th tile).
+// The part of one (request, KV head) over tiles [t0, t1) by one warp (every kFewWarps-th tile).  PAGE16: the pages are
+// multiples of 16 slots, so that a unit lies in one, all of whose bytes may be read: what no row sees of it is masked
+// like what some rows do not see.
 // o[i]: columns (quad * 8W + 2i, + 1) (halves 0, 1 and 2, 3) of rows 8n + 2kq, + 1; m, l: of those rows.
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool PAGE16>
 struct FewWarp4 {
   static constexpr int W = D / 64, NK = D / 16, NV = D / 16;
   static constexpr bool kRest = std::is_same<T, __half>::value;
@@ -146,42 +148,67 @@ struct FewWarp4 {
     const uint8_t *V = static_cast<const uint8_t *>(a.v) + h * a.head_stride + quad * (D / 16);
     const uint8_t *KS = static_cast<const uint8_t *>(c4.k_scale) + h * c4.scale_head_stride + kq * W;
     const uint8_t *VS = static_cast<const uint8_t *>(c4.v_scale) + h * c4.scale_head_stride + quad * W / 2;
-    // page of slot lane % 16 of tile t (the load alone), then the slot's place, -1 for a slot no row sees
-    auto page_of = [&](int t) { return __ldg(table + min(tl.at(max(min(t, t1 - 1), 0)) * kUnit + (lane & 15), rq.n - 1) / a.page_size); };
+    // Page of tile t (of its slot lane % 16): the load alone.
+    auto page_of = [&](int t) {
+      const int tile = tl.at(max(min(t, t1 - 1), 0));
+      if constexpr (PAGE16) return __ldg(table + (A.units_magic ? __umulhi(tile, A.units_magic) : tile));
+      else return __ldg(table + min(tile * kUnit + (lane & 15), rq.n - 1) / a.page_size);
+    };
     auto load = [&](Frag<D> &x, int t, int page) {
       if (t >= t1) return;
-      const int j = tl.at(t) * kUnit + (lane & 15);
-      Place4 at = {-1, -1};
-      if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, page, j);
-      auto of = [&](int slot, int64_t &code, int64_t &scale) {
-        code = __shfl_sync(0xffffffffu, at.code, slot);
-        scale = __shfl_sync(0xffffffffu, at.scale, slot);
-      };
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        int64_t code, scale;
-        of(quad + 8 * y, code, scale);
-        if (code >= 0) {
-          load_words(x.k[y], K + code);
-          if constexpr (W == 2) x.ks[y] = __ldg(reinterpret_cast<const uint16_t *>(KS + scale));
-          else x.ks[y] = __ldg(KS + scale);
-        } else {
-#pragma unroll
-          for (int w = 0; w < 2 * W; ++w) x.k[y][w] = 0;
-          x.ks[y] = 0;
+      if constexpr (PAGE16) {
+        const uint32_t tile = tl.at(t), in = A.units_magic ? tile - __umulhi(tile, A.units_magic) * A.page_units : 0;
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
+          atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+          x = {};
+          return;
         }
-      }
+        // strides of a slot are below 2^27 bytes here: a lane's place in the unit is one 32-bit product
+        const uint32_t ss = static_cast<uint32_t>(a.slot_stride), zs = static_cast<uint32_t>(c4.scale_slot_stride);
+        const int64_t code = page * a.page_stride + static_cast<int64_t>(in) * (16 * ss);
+        const int64_t scale = page * c4.scale_page_stride + static_cast<int64_t>(in) * (16 * zs);
+        const uint8_t *k = K + code, *v = V + code, *ks = KS + scale, *vs = VS + scale;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        int64_t code, scale;
-        of(2 * kq + (y & 1) + 8 * (y >> 1), code, scale);
-        if (code >= 0) {
-          load_words(x.v[y], V + code);
-          x.vs[y] = __ldg(VS + scale);
-        } else {
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t slot = quad + 8 * y;
+          load_words(x.k[y], k + static_cast<uint64_t>(slot) * ss);
+          const uint8_t *z = ks + static_cast<uint64_t>(slot) * zs;
+          if constexpr (W == 2) x.ks[y] = __ldg(reinterpret_cast<const uint16_t *>(z));
+          else x.ks[y] = __ldg(z);
+        }
 #pragma unroll
-          for (int w = 0; w < W; ++w) x.v[y][w] = 0;
-          x.vs[y] = 0;
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t slot = 2 * kq + (y & 1) + 8 * (y >> 1);
+          load_words(x.v[y], v + static_cast<uint64_t>(slot) * ss);
+          x.vs[y] = __ldg(vs + static_cast<uint64_t>(slot) * zs);
+        }
+      } else {
+        const int j = tl.at(t) * kUnit + (lane & 15);
+        Place4 at = {-1, -1};
+        if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, page, j);
+        auto of = [&](int slot, int64_t &code, int64_t &scale) {
+          code = __shfl_sync(0xffffffffu, at.code, slot);
+          scale = __shfl_sync(0xffffffffu, at.scale, slot);
+        };
+        x = {};
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          int64_t code, scale;
+          of(quad + 8 * y, code, scale);
+          if (code >= 0) {
+            load_words(x.k[y], K + code);
+            if constexpr (W == 2) x.ks[y] = __ldg(reinterpret_cast<const uint16_t *>(KS + scale));
+            else x.ks[y] = __ldg(KS + scale);
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          int64_t code, scale;
+          of(2 * kq + (y & 1) + 8 * (y >> 1), code, scale);
+          if (code >= 0) {
+            load_words(x.v[y], V + code);
+            x.vs[y] = __ldg(VS + scale);
+          }
         }
       }
     };
@@ -330,7 +357,7 @@ template <typename T, int D> __device__ void no_slots(const Paged4AttnArgs &A, c
   empty_rows<T, D>(x, rq, rq.rows, tid, step);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool PAGE16>
 __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(const __grid_constant__ Paged4AttnArgs A) {
   constexpr int ROWS = 8 * NT;
   __shared__ __align__(16) float so[kFewWarps][ROWS][D + 4];  // the warps' sums
@@ -386,7 +413,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(c
     }
     const int R = rq.rows * a.group;
     {
-      FewWarp4<T, D, NT> w;
+      FewWarp4<T, D, NT, PAGE16> w;
       w.run(A, rq, tl, b, h, t0, t1, warp, lane);
       const int quad = lane >> 2, kq = lane & 3;
 #pragma unroll
@@ -479,9 +506,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(c
 constexpr int kJoinThreads = 512;
 constexpr int kJoinHeld = 10;  // parts of a thread in registers
 constexpr int kJoinRows = 4;
+constexpr int kJoinParts4 = 640;  // parts of a head at most: the blocks of a launch, and one more
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_constant__ Paged4AttnArgs A) {
-  __shared__ float weight[kJoinRows][kJoinParts];
+  __shared__ float weight[kJoinRows][kJoinParts4];
   __shared__ float2 row_ml[kJoinRows];
   __shared__ float4 sums[kJoinThreads];
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -553,13 +581,17 @@ constexpr int kWholeSlots = 512;
 constexpr int kBlockSlots = 64;
 constexpr int kClusterSlots = 1088, kClusterFilled = 2176;
 constexpr int kJoinSlots = 800, kPartSlots = 2;
-constexpr int kBlocksPerSm = 2;
 
-int few4_blocks() { return kBlocksPerSm * num_sms() < kJoinParts ? kBlocksPerSm * num_sms() : kJoinParts - 1; }
+// Blocks of a launch that is shared out: as many as the SMs hold at once.
+int few4_blocks(int nt) {
+  const int n = (nt == 1 ? 3 : 2) * num_sms();
+  return n < kJoinParts4 ? n : kJoinParts4 - 1;
+}
 
-template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
+template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.c.p;
-  auto kernel = attention_few4<T, D, NT>;
+  auto kernel = attention_few4<T, D, NT, PAGE16>;
+  A.n_ctas = few4_blocks(NT);
   static const ClustersAtOnce fit(kernel, kFewThreads, 0);
   const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
   int blocks = 1;
@@ -583,6 +615,16 @@ template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaS
   const int rows = a.max_rows * a.group;
   return launch_pdl(attention_join4<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
 }
+template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
+  // units of a page, and 2^32 over them rounded up (0: one): tile / units is the upper word of tile * magic while
+  // tile * units < 2^32
+  const PagedArgs &a = A.c.p;
+  const int64_t units = a.page_size / kUnit, strides = a.slot_stride > A.c.scale_slot_stride ? a.slot_stride : A.c.scale_slot_stride;
+  if (a.page_size % kUnit || units * (a.max_len / kUnit + 1) >= (1ll << 32) || strides >= (1 << 27)) return launch<T, D, NT, false>(A, s);
+  A.page_units = static_cast<uint32_t>(units);
+  A.units_magic = units == 1 ? 0 : static_cast<uint32_t>(((1ll << 32) + units - 1) / units);
+  return launch<T, D, NT, true>(A, s);
+}
 template <typename T, int D> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
   return A.c.p.max_rows * A.c.p.group <= 8 ? launch<T, D, 1>(A, s) : launch<T, D, 2>(A, s);
 }
@@ -590,16 +632,15 @@ template <typename T, int D> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t 
 }  // namespace
 
 size_t few4_bytes(int head_dim) {
-  const size_t parts = 2 * static_cast<size_t>(few4_blocks()) * kFewRows4;
-  return align256(few4_blocks() * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
+  const size_t parts = 2 * static_cast<size_t>(few4_blocks(1)) * kFewRows4;
+  return align256(few4_blocks(1) * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
 }
 
 std::string launch_attention_few4(Paged4AttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
-  A.n_ctas = few4_blocks();
-  const size_t parts = 2 * static_cast<size_t>(A.n_ctas) * kFewRows4;
+  const size_t blocks = few4_blocks(1), parts = 2 * blocks * kFewRows4;  // the most that a launch has
   A.join = reinterpret_cast<PagedJoin *>(p);
-  p += align256(A.n_ctas * sizeof(PagedJoin));
+  p += align256(blocks * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);
   p += align256(parts * A.c.p.head_dim * 4);
   A.part_ml = reinterpret_cast<float2 *>(p);
