@@ -9,12 +9,11 @@
 // reference are raised to that: their weight is 0, and that of -inf is no 0 times infinity.
 //
 // The largest logits come out of the same pass: a thread puts a 16-byte vector that holds a logit at or above the block's
-// threshold aside, in shared memory, which is all that the loop over the row does for them.  Twice the logits of the vectors
-// aside are made keys, which order by value, then by the lower id, and thinned to the top_k largest, the last of which is
-// the next threshold.  The first threshold is the top_k-th largest of 64 maxima of 32 or 64 logits each, the first ones
-// that the threads read; so of 152 000 logits about two hundred get aside.  Where more do than there is room for
-// (values in ascending order, many equal ones), the round is done again with the threshold that those aside give,
-// which is larger each time.
+// threshold aside, in shared memory, which is all that the loop over the row does for them.  At the end the logits of the
+// vectors aside are made keys, which order by value, then by the lower id, and thinned to the top_k largest.  The
+// threshold is the top_k-th largest of 128 maxima of 128 or 256 logits each, the first ones that the threads read; so of
+// 152 000 logits about a hundred (of 20, 16 bits) get aside.  Where more do than there is room for (values in ascending order, many
+// equal ones), the row is looked through again with the threshold that those aside give, which is larger each time.
 //
 // Few rows are a cluster's of up to 16 blocks, each with an equal part of the row; the first one joins their sums and
 // candidates through distributed shared memory.  Bound by the bytes of the logits.
@@ -35,9 +34,8 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpCluster = 16;
 constexpr int kLpEach = 4;  // vectors of a thread in flight
 constexpr int kTop = BD_LOGPROB_TOP_MAX;
-constexpr int kKeys = 512;             // candidates that a block thins at once, a thread each
-constexpr int kBuffer = kKeys - kTop;  // those of a round, beside the ones kept before
-constexpr int kAside = 512;            // vectors that a block puts aside in a round, one a thread to make keys of
+constexpr int kKeys = 512;             // candidates that a block thins, a thread each
+constexpr int kAside = 512;            // vectors that a block puts aside, one a thread to make keys of
 static_assert(kLpCluster * kTop <= kKeys && kKeys <= kLpThreads, "the joining block thins every block's candidates");
 
 struct LogprobArgs {
@@ -79,11 +77,19 @@ template <typename T> struct Vec {
   }
   static constexpr float kLowest = std::is_same<T, __half>::value ? -65504.f : -1e38f;
   static __device__ __forceinline__ uint32_t floor_of(float f) { return Pair<T>::pack(f, f); }
-  static __device__ __forceinline__ void unpack(const uint4 &w, uint32_t floor, float2 (&x)[4]) {
-    x[0] = Pair<T>::unpack(max2_nan(w.x, floor));
-    x[1] = Pair<T>::unpack(max2_nan(w.y, floor));
-    x[2] = Pair<T>::unpack(max2_nan(w.z, floor));
-    x[3] = Pair<T>::unpack(max2_nan(w.w, floor));
+  static __device__ __forceinline__ uint64_t two(uint32_t w) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 x = Pair<T>::unpack(w);
+      return pair(x.x, x.y);
+    } else {
+      return pair_bits(w << 16, w & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void unpack(const uint4 &w, uint32_t floor, uint64_t (&x)[4]) {
+    x[0] = two(max2_nan(w.x, floor));
+    x[1] = two(max2_nan(w.y, floor));
+    x[2] = two(max2_nan(w.z, floor));
+    x[3] = two(max2_nan(w.w, floor));
   }
   // Its first element; the others move up.
   static __device__ __forceinline__ float next(uint4 &w) {
@@ -103,10 +109,10 @@ template <> struct Vec<float> {
   }
   static constexpr float kLowest = -1e38f;
   static __device__ __forceinline__ uint32_t floor_of(float f) { return __float_as_uint(f); }
-  static __device__ __forceinline__ void unpack(const uint4 &w, uint32_t floor, float2 (&x)[2]) {
+  static __device__ __forceinline__ void unpack(const uint4 &w, uint32_t floor, uint64_t (&x)[2]) {
     const float f = __uint_as_float(floor);
-    x[0] = make_float2(max_nan(__uint_as_float(w.x), f), max_nan(__uint_as_float(w.y), f));
-    x[1] = make_float2(max_nan(__uint_as_float(w.z), f), max_nan(__uint_as_float(w.w), f));
+    x[0] = pair(max_nan(__uint_as_float(w.x), f), max_nan(__uint_as_float(w.y), f));
+    x[1] = pair(max_nan(__uint_as_float(w.z), f), max_nan(__uint_as_float(w.w), f));
   }
   static __device__ __forceinline__ float next(uint4 &w) {
     const float x = __uint_as_float(w.x);
@@ -116,15 +122,17 @@ template <> struct Vec<float> {
   static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
+// Integers in the order of fp32 numbers.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float ordered_value(uint32_t b) { return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b); }
 // Larger for larger values, among equal ones for lower ids (-0 is 0, NaN counts as -inf).
 __device__ __forceinline__ uint64_t key_of(float x, int id) {
-  const uint32_t b = x != x ? 0xff800000u : __float_as_uint(x + 0.f);
-  return static_cast<uint64_t>(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | static_cast<uint32_t>(~id);
+  return static_cast<uint64_t>(ordered(x != x ? -INFINITY : x + 0.f)) << 32 | static_cast<uint32_t>(~id);
 }
-__device__ __forceinline__ float key_value(uint64_t k) {
-  const uint32_t b = static_cast<uint32_t>(k >> 32);
-  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-}
+__device__ __forceinline__ float key_value(uint64_t k) { return ordered_value(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int key_id(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
 __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
@@ -150,24 +158,48 @@ __device__ __forceinline__ void rescale(Sums &a, float m, float c) {  // m >= a.
   a.s *= w;
   a.m = m;
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  rescale(a, m, c);
-  rescale(b, m, c);
-  return {m, a.s + b.s, a.t + b.t};
+__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t x, int o) {
+  const uint32_t lo = __shfl_xor_sync(0xffffffffu, static_cast<uint32_t>(x), o), hi = __shfl_xor_sync(0xffffffffu, static_cast<uint32_t>(x >> 32), o);
+  return static_cast<uint64_t>(hi) << 32 | lo;
 }
-
-// The k largest of keys[0 .. n), n <= kKeys, to keys[0 .. k) in descending order; all threads.
+// How many keys of `lists` descending lists of n <= 32, `step` keys apart, are larger than one: four lists side by side, their
+// searches being all latency.
+__device__ __forceinline__ int larger_in(const uint64_t *keys, int lists, int n, int step, uint64_t key) {
+  int rank = 0;
+  for (int l = 0; l < lists; l += 4) {
+    int at[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int to = at[x] + s;
+        if (l + x < lists && to <= n && keys[(l + x) * step + to - 1] > key) at[x] = to;
+      }
+    rank += at[0] + at[1] + at[2] + at[3];
+  }
+  return rank;
+}
+// The k <= 32 largest of keys[0 .. n), n <= kKeys, to keys[0 .. k) in descending order; all threads.  Each warp sorts 32 of
+// them among its lanes; a key's place is then the number of larger ones in each sorted list.
 __device__ __forceinline__ void thin(uint64_t *keys, int n, int k) {
   __syncthreads();
-  const int i = threadIdx.x;
+  const int i = threadIdx.x, lane = i & 31, lists = (n + 31) / 32;
   uint64_t mine = 0;
   int rank = k;
-  if (i < n) {
-    mine = keys[i];
-    rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > mine;
+  if (i / 32 < lists) {
+    mine = i < n ? keys[i] : 0;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+      for (int o = size / 2; o > 0; o /= 2) {
+        const uint64_t other = shfl_xor_u64(mine, o);
+        const bool first = (lane & o) == 0, down = (lane & size) == 0 || size == 32;
+        if ((other > mine) == (first == down)) mine = other;
+      }
+    keys[i] = mine;
   }
+  __syncthreads();
+  if (mine != 0 && lane < k) rank = larger_in(keys, lists, k, 32, mine);
   __syncthreads();
   if (rank < k) keys[rank] = mine;
   __syncthreads();
@@ -181,15 +213,7 @@ __device__ __forceinline__ void thin_lists(uint64_t *keys, int lists, int k) {
   int rank = k;
   if (i < lists * k) {
     mine = keys[i];
-    rank = 0;
-    for (int b = 0; b < lists; ++b) {  // how many of list b are larger
-      int lo = 0, hi = k;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (keys[b * k + mid] > mine) lo = mid + 1; else hi = mid;
-      }
-      rank += lo;
-    }
+    rank = larger_in(keys, lists, k, k, mine);
   }
   __syncthreads();
   if (rank < k && mine != 0) keys[rank] = mine;  // 0 fills up lists that are shorter
@@ -199,9 +223,9 @@ __device__ __forceinline__ void thin_lists(uint64_t *keys, int lists, int k) {
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_constant__ LogprobArgs A) {
   using V = Vec<T>;
-  constexpr int N = V::N, GROUPS = 64;
-  __shared__ __align__(16) uint64_t keys[kKeys], best[kTop];  // this round's candidates; those kept before
-  __shared__ __align__(16) float group_top[GROUPS];  // maxima of eight threads' first logits
+  constexpr int N = V::N, GROUPS = 128;
+  __shared__ __align__(16) uint64_t keys[kKeys], best[kTop];  // candidates; the largest
+  __shared__ __align__(16) float group_top[GROUPS];  // maxima of four threads' first logits
   __shared__ Sums warp_sums[kLpWarps];
   __shared__ Sums block_sums;
   __shared__ __align__(16) uint4 aside[kAside];      // vectors with candidates,
@@ -229,7 +253,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   int reach_id = INT_MAX;   // its id
   Sums a = {-FLT_MAX, 0.f, 0.f};
   uint64_t s2 = 0, t2 = 0;                 // the sums, in two halves
-  float minus_r = 0.f, limit = -FLT_MAX;   // -r; what moves the reference
+  const uint64_t c2 = pair(c, c);
+  uint64_t r2 = 0;                         // -r, twice
+  float limit = -FLT_MAX;                  // what moves the reference
   uint32_t floor = 0;
   bool far = true, slow = true;            // r is not multiplied out; or `floor` is no number of the type
 
@@ -246,24 +272,23 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     const float low = (r - kNothing) * A.inv_scale;
     far = !(fabsf(r) < kLarge);
     slow = far || low < V::kLowest;
-    minus_r = -r;
+    r2 = pair(-r, -r);
     limit = far ? m : (r + 16.f) * A.inv_scale;
     floor = V::floor_of(low);
   };
   auto add_one = [&](float y) {
     if (y > limit) refer(y);
-    const float d = max_nan(far ? (y - a.m) * c : fmaf(y, c, minus_r), -kNothing), w = exp2_fast(d);
+    const float d = max_nan(far ? (y - a.m) * c : fmaf(y, c, unpair(r2).x), -kNothing), w = exp2_fast(d);
     a.s += w;
     a.t = fmaf(w, d, a.t);
   };
   auto add = [&](const uint4 &w) {  // none of it above `limit`
-    float2 y[N / 2];
     if (!slow) {
+      uint64_t y[N / 2];
       V::unpack(w, floor, y);
-      const uint64_t c2 = pair(c, c), r2 = pair(minus_r, minus_r);
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) {
-        const uint64_t d = fma2(pair(y[e].x, y[e].y), c2, r2);
+        const uint64_t d = fma2(y[e], c2, r2);
         const float2 z = unpair(d);
         const uint64_t p = pair(exp2_fast(z.x), exp2_fast(z.y));
         s2 = add2(s2, p);
@@ -280,7 +305,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     const uint64_t key = key_of(v, id);
     if (key < threshold) return;
     const int at = atomicAdd(&count, 1);
-    if (at < kBuffer) keys[at] = key;
+    if (at < kKeys) keys[at] = key;
   };
   // Whether vector i, of the largest logit m, may hold a key at or above the threshold.  Of those put aside all but one (that
   // of the threshold's own id) do, so a round that is done again finds fewer each time.
@@ -300,135 +325,122 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     else if (tid - head < A.vocab - tail) loose_id = tail + tid - head;
     if (loose_id >= 0) loose = to_f<T>(x[loose_id]);
   }
-  // the first vector of every thread, which gives the first threshold
-  uint4 first = make_uint4(0, 0, 0, 0);
-  const bool has = v0 + tid < v1;
-  if (has) first = __ldg(xv + v0 + tid);
   if (loose_id >= 0) add_one(loose);
-  float m0 = -INFINITY;
-  if (has) {
-    m0 = V::most(first);
-    if (m0 > limit) refer(m0);
-    add(first);
-  }
-  if (k > 0) {
-    float m = m0;
+  // kLpEach vectors of every thread from i on; the first two times they give the threshold
+  constexpr int kStep = kLpEach * kLpThreads;
+  float top0 = -INFINITY;
+  int times = 0;
+  for (int i = v0 + tid; times < 2 || i < v1; i += kStep, ++times) {
+    uint4 w[kLpEach];
+    float m[kLpEach], top = -INFINITY;
+    const bool whole = i + (kLpEach - 1) * kLpThreads < v1;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (tid % 8 == 0) group_top[tid / 8] = m;
-    __syncthreads();
-    if (tid < GROUPS) {
-      m = group_top[tid];
-      int larger = 0;
+    for (int u = 0; u < kLpEach; ++u)
+      if (whole || i + u * kLpThreads < v1) w[u] = __ldg(xv + i + u * kLpThreads);
+      else w[u] = V::nothing();
 #pragma unroll
-      for (int j = 0; j < GROUPS; j += 4) {
-        const float4 o = *reinterpret_cast<const float4 *>(group_top + j);
-        larger += (o.x > m || (o.x == m && j < tid)) + (o.y > m || (o.y == m && j + 1 < tid)) + (o.z > m || (o.z == m && j + 2 < tid)) +
-                  (o.w > m || (o.w == m && j + 3 < tid));
-      }
-      // k logits are at least this: no smaller value is among the k largest
-      if (larger == k - 1) first_threshold = key_of(m, 0x7fffffff);
+    for (int u = 0; u < kLpEach; ++u) {
+      m[u] = V::most(w[u]);
+      top = fmaxf(top, m[u]);
     }
-    __syncthreads();
-    threshold = first_threshold;
-    reach = key_value(threshold);
-    if (has && reaches(m0, v0 + tid)) put_aside(first, v0 + tid);
-  }
-  // two rounds, or one of a short part: up to an eighth of it, the rest
-  const int from = v0 + kLpThreads, rest = max(0, v1 - from), cut = rest > 2 * kLpEach * kLpThreads ? from + rest / 8 : from + rest;
-  int kept = 0;  // candidates of the round before
-  for (int round = 0; round < 2; ++round) {
-    int r0 = round == 0 ? from : cut;
-    const int r1 = min(v1, round == 0 ? cut : from + rest);
-    if (round == 1 && r0 >= r1) break;
-    for (bool again = false;;) {
-      if (again) {
-        // Every thread a stretch of its own, so that those that come first are from all over the round: of m vectors, in
-        // whatever order their values are, about m k / kAside reach the next threshold.
-        const int64_t len = r1 - r0;
-        const int e = r0 + static_cast<int>(len * (tid + 1) / kLpThreads);
-        for (int i = r0 + static_cast<int>(len * tid / kLpThreads); i < e; ++i) {
-          const uint4 w = __ldg(xv + i);
-          if (reaches(V::most(w), i)) put_aside(w, i);
-        }
-      } else {
-        for (int i = r0 + tid; i < r1; i += kLpEach * kLpThreads) {
-          uint4 w[kLpEach];
-          float m[kLpEach], top = -INFINITY;
-          const bool whole = i + (kLpEach - 1) * kLpThreads < r1;
+    if (top > limit) refer(top);
 #pragma unroll
-          for (int u = 0; u < kLpEach; ++u)
-            if (whole || i + u * kLpThreads < r1) w[u] = __ldg(xv + i + u * kLpThreads);
-            else w[u] = V::nothing();
-#pragma unroll
-          for (int u = 0; u < kLpEach; ++u) {
-            m[u] = V::most(w[u]);
-            top = fmaxf(top, m[u]);
-          }
-          if (top > limit) refer(top);
-#pragma unroll
-          for (int u = 0; u < kLpEach; ++u) add(w[u]);
-#pragma unroll
-          for (int u = 0; u < kLpEach; ++u)
-            if (k > 0 && reaches(m[u], i + u * kLpThreads) && (whole || i + u * kLpThreads < r1)) put_aside(w[u], i + u * kLpThreads);
-        }
-      }
-      if (k == 0) break;
+    for (int u = 0; u < kLpEach; ++u) add(w[u]);
+    if (k == 0) continue;
+    if (times == 0) {
+      top0 = top;
+      continue;
+    }
+    if (times == 1) {
+      float g = fmaxf(top0, top);
+      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+      if (tid % 4 == 0) group_top[tid / 4] = g;
       __syncthreads();
-      const int n = aside_count;
-      again = n > kAside;
-      for (bool full = true; full;) {  // keys of those aside
-        if (tid < min(n, kAside)) {
-          uint4 w = aside[tid];
-          const int id = head + aside_at[tid] * N;
-#pragma unroll 1
-          for (int e = 0; e < N; ++e) offer(V::next(w), id + e);
+      if (tid < GROUPS) {
+        g = group_top[tid];
+        int larger = 0;
+#pragma unroll 4
+        for (int j = 0; j < GROUPS; j += 4) {
+          const float4 o = *reinterpret_cast<const float4 *>(group_top + j);
+          larger += (o.x > g || (o.x == g && j < tid)) + (o.y > g || (o.y == g && j + 1 < tid)) + (o.z > g || (o.z == g && j + 2 < tid)) +
+                    (o.w > g || (o.w == g && j + 3 < tid));
         }
-        if (loose_id >= 0 && round == 0) offer(loose, loose_id);
-        __syncthreads();
-        const int found = count;
-        full = found > kBuffer;
-        if (!full && !again && tid < kept) keys[found + tid] = best[tid];
-        const int all = full ? kBuffer : again ? found : found + kept;
-        thin(keys, all, k);
-        if (all >= k) {  // k of them are at least the next threshold
-          threshold = max(threshold, keys[k - 1]);
-          reach = key_value(threshold);
-          reach_id = key_id(threshold);
-        }
-        if (!full && !again) {
-          kept = min(all, k);
-          if (tid < kept) best[tid] = keys[tid];
-        }
-        __syncthreads();
-        if (tid == 0) count = aside_count = 0;
-        __syncthreads();
+        // k logits are at least this: no smaller value is among the k largest
+        if (larger == k - 1) first_threshold = key_of(g, 0x7fffffff);
       }
-      if (!again) break;
-      if (round == 0) r0 = v0;  // the first vectors, too
+      __syncthreads();
+      threshold = first_threshold;
+      reach = key_value(threshold);
+      if (top0 >= reach)  // those of the first time, read again
+#pragma unroll 1
+        for (int j = i - kStep; j < min(i, v1); j += kLpThreads) {
+          const uint4 x = __ldg(xv + j);
+          if (reaches(V::most(x), j)) put_aside(x, j);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kLpEach; ++u)
+      if (m[u] >= reach)
+        if (reaches(m[u], i + u * kLpThreads) && i + u * kLpThreads < v1) put_aside(w[u], i + u * kLpThreads);
+  }
+  int kept = 0;  // of the k largest
+  for (bool again = k > 0; again;) {
+    __syncthreads();
+    const int n = aside_count;
+    again = n > kAside;
+    for (bool full = true; full;) {  // keys of those aside
+      if (tid < min(n, kAside)) {
+        uint4 w = aside[tid];
+        const int id = head + aside_at[tid] * N;
+#pragma unroll 1
+        for (int e = 0; e < N; ++e) offer(V::next(w), id + e);
+      }
+      if (loose_id >= 0) offer(loose, loose_id);
+      __syncthreads();
+      const int found = count;
+      full = found > kKeys;
+      kept = min(found, kKeys);
+      thin(keys, kept, k);
+      if (kept >= k) {  // k logits are at least the next threshold
+        kept = k;
+        threshold = max(threshold, keys[k - 1]);
+        reach = key_value(threshold);
+        reach_id = key_id(threshold);
+      }
+      if (tid == 0) count = aside_count = 0;
+      __syncthreads();
+    }
+    if (again) {
+      // Every thread a stretch of its own, so that those that come first are from all over the row: of m vectors, in
+      // whatever order their values are, about m k / kAside reach the next threshold.
+      const int64_t len = v1 - v0;
+      const int e = v0 + static_cast<int>(len * (tid + 1) / kLpThreads);
+      for (int i = v0 + static_cast<int>(len * tid / kLpThreads); i < e; ++i) {
+        const uint4 w = __ldg(xv + i);
+        if (reaches(V::most(w), i)) put_aside(w, i);
+      }
     }
   }
+  if (tid < kTop) best[tid] = tid < kept ? keys[tid] : 0;  // 0: below every key
   fold();
-  // the block's sums
+  // the block's sums, all against the largest reference
+  auto join_sums = [&](Sums &a) {
+    const float m = ordered_value(__reduce_max_sync(0xffffffffu, ordered(a.m)));
+    rescale(a, m, c);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Sums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.t, o)};
-    a = join(a, b, c);
-  }
-  if (lane == 0) warp_sums[warp] = a;
-  if (tid < k && tid >= kept) best[tid] = 0;  // below every key
-  __syncthreads();
-  auto join_sums = [&](int n) {  // of the first n <= 16 lanes
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      const Sums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.t, o)};
-      a = join(a, b, c);
+    for (int o = 16; o > 0; o >>= 1) {
+      a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+      a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
     }
-    if (lane == 0) block_sums = a;
   };
+  join_sums(a);
+  if (lane == 0) warp_sums[warp] = a;
+  __syncthreads();
   if (warp == 0) {
-    a = warp_sums[lane % kLpWarps];
-    join_sums(kLpWarps);
+    a = lane < kLpWarps ? warp_sums[lane] : Sums{-FLT_MAX, 0.f, 0.f};
+    join_sums(a);
+    if (lane == 0) block_sums = a;
   }
   __syncthreads();
   if (A.cluster > 1) {
@@ -444,7 +456,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
           a = {ld_cluster_f32(p), ld_cluster_f32(p + 4), ld_cluster_f32(p + 8)};
         }
         __syncwarp();  // its own sums are read before they are replaced
-        join_sums(A.cluster);
+        join_sums(a);
+        if (lane == 0) block_sums = a;
       }
       if (k > 0) {
         if (from_block < A.cluster) keys[tid] = key;
