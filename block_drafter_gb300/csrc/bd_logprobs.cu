@@ -11,8 +11,8 @@
 // The largest logits come out of the same pass: a thread puts a 16-byte vector that holds a logit at or above the block's
 // threshold aside, in shared memory, which is all that the loop over the row does for them.  At the end the logits of the
 // vectors aside are made keys, which order by value, then by the lower id, and thinned to the top_k largest.  The
-// threshold is the top_k-th largest of 128 maxima of 128 or 256 logits each, the first ones that the threads read; so of
-// 152 000 logits about a hundred (of 20, 16 bits) get aside.  Where more do than there is room for (values in ascending order, many
+// threshold is the top_k-th largest of 128 maxima of 128 or 256 logits each (of short parts a half of that), the first ones
+// that the threads read; so of 152 000 logits about a hundred (of 20, 16 bits) get aside.  Where more do than there is room for (values in ascending order, many
 // equal ones), the row is looked through again with the threshold that those aside give, which is larger each time.
 //
 // Few rows are a cluster's of up to 16 blocks, each with an equal part of the row; the first one joins their sums and
@@ -29,14 +29,15 @@ BD_DEFINE_ERROR_TAKER(take_error_word_logprobs)
 
 namespace {
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;
+constexpr int kLpBlocks = 4;  // on an SM: while one selects, the others read
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpCluster = 16;
 constexpr int kLpEach = 4;  // vectors of a thread in flight
 constexpr int kTop = BD_LOGPROB_TOP_MAX;
-constexpr int kKeys = 512;             // candidates that a block thins, a thread each
-constexpr int kAside = 512;            // vectors that a block puts aside, one a thread to make keys of
-static_assert(kLpCluster * kTop <= kKeys && kKeys <= kLpThreads, "the joining block thins every block's candidates");
+constexpr int kKeys = 512;             // candidates that a block thins
+constexpr int kAside = 512;            // vectors that a block puts aside
+static_assert(kLpCluster * kTop <= kKeys && kLpThreads % 32 == 0, "the joining block joins every block's candidates");
 
 struct LogprobArgs {
   const void *logits;
@@ -162,13 +163,16 @@ __device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t x, int o) {
   const uint32_t lo = __shfl_xor_sync(0xffffffffu, static_cast<uint32_t>(x), o), hi = __shfl_xor_sync(0xffffffffu, static_cast<uint32_t>(x >> 32), o);
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
+// Loops here are not unrolled: each runs once a row, and straight code would be fetched for that.
+
 // How many keys of `lists` descending lists of n <= 32, `step` keys apart, are larger than one: four lists side by side, their
 // searches being all latency.
 __device__ __forceinline__ int larger_in(const uint64_t *keys, int lists, int n, int step, uint64_t key) {
   int rank = 0;
+#pragma unroll 1
   for (int l = 0; l < lists; l += 4) {
     int at[4] = {0, 0, 0, 0};
-#pragma unroll
+#pragma unroll 1
     for (int s = 32; s > 0; s >>= 1)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -179,18 +183,29 @@ __device__ __forceinline__ int larger_in(const uint64_t *keys, int lists, int n,
   }
   return rank;
 }
-// The k <= 32 largest of keys[0 .. n), n <= kKeys, to keys[0 .. k) in descending order; all threads.  Each warp sorts 32 of
-// them among its lanes; a key's place is then the number of larger ones in each sorted list.
-__device__ __forceinline__ void thin(uint64_t *keys, int n, int k) {
+// The k largest of `lists` descending lists of n <= 32 keys (0: none), `step` keys apart, to best[0 .. k) in descending order;
+// all threads, after a barrier.
+__device__ __forceinline__ void join_lists(const uint64_t *keys, int lists, int n, int step, int k, uint64_t *best) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < lists * n; i += kLpThreads) {
+    const int list = i / static_cast<uint32_t>(n);
+    const uint64_t key = keys[list * step + i - list * n];
+    const int rank = key ? larger_in(keys, lists, n, step, key) : k;
+    if (rank < k) best[rank] = key;
+  }
   __syncthreads();
-  const int i = threadIdx.x, lane = i & 31, lists = (n + 31) / 32;
-  uint64_t mine = 0;
-  int rank = k;
-  if (i / 32 < lists) {
-    mine = i < n ? keys[i] : 0;
-#pragma unroll
+}
+// The k <= 32 largest of keys[0 .. n), n <= kKeys, to best[0 .. k) in descending order; all threads.  Each warp sorts 32 of
+// them at a time among its lanes; a key's place is then the number of larger ones in each sorted list.
+__device__ __forceinline__ void thin(uint64_t *keys, int n, int k, uint64_t *best) {
+  __syncthreads();
+  const int lane = threadIdx.x & 31, lists = (n + 31) / 32;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < lists * 32; i += kLpThreads) {
+    uint64_t mine = i < n ? keys[i] : 0;
+#pragma unroll 1
     for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
+#pragma unroll 1
       for (int o = size / 2; o > 0; o /= 2) {
         const uint64_t other = shfl_xor_u64(mine, o);
         const bool first = (lane & o) == 0, down = (lane & size) == 0 || size == 32;
@@ -199,33 +214,15 @@ __device__ __forceinline__ void thin(uint64_t *keys, int n, int k) {
     keys[i] = mine;
   }
   __syncthreads();
-  if (mine != 0 && lane < k) rank = larger_in(keys, lists, k, 32, mine);
-  __syncthreads();
-  if (rank < k) keys[rank] = mine;
-  __syncthreads();
-}
-
-// The same of `lists` lists of k keys in descending order each, side by side.
-__device__ __forceinline__ void thin_lists(uint64_t *keys, int lists, int k) {
-  __syncthreads();
-  const int i = threadIdx.x;
-  uint64_t mine = 0;
-  int rank = k;
-  if (i < lists * k) {
-    mine = keys[i];
-    rank = larger_in(keys, lists, k, k, mine);
-  }
-  __syncthreads();
-  if (rank < k && mine != 0) keys[rank] = mine;  // 0 fills up lists that are shorter
-  __syncthreads();
+  join_lists(keys, lists, k, 32, k, best);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_constant__ LogprobArgs A) {
+__global__ void __launch_bounds__(kLpThreads, kLpBlocks) logprobs_kernel(const __grid_constant__ LogprobArgs A) {
   using V = Vec<T>;
   constexpr int N = V::N, GROUPS = 128;
   __shared__ __align__(16) uint64_t keys[kKeys], best[kTop];  // candidates; the largest
-  __shared__ __align__(16) float group_top[GROUPS];  // maxima of four threads' first logits
+  __shared__ __align__(16) float group_top[GROUPS];  // maxima of two threads' first logits
   __shared__ Sums warp_sums[kLpWarps];
   __shared__ Sums block_sums;
   __shared__ __align__(16) uint4 aside[kAside];      // vectors with candidates,
@@ -326,11 +323,12 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     if (loose_id >= 0) loose = to_f<T>(x[loose_id]);
   }
   if (loose_id >= 0) add_one(loose);
-  // kLpEach vectors of every thread from i on; the first two times they give the threshold
+  // kLpEach vectors of every thread from i on; the first few times they give the threshold
   constexpr int kStep = kLpEach * kLpThreads;
-  float top0 = -INFINITY;
+  const int last_first = v1 - v0 > 8 * kStep ? 3 : 1;
+  float early = -INFINITY;
   int times = 0;
-  for (int i = v0 + tid; times < 2 || i < v1; i += kStep, ++times) {
+  for (int i = v0 + tid; times <= last_first || i < v1; i += kStep, ++times) {
     uint4 w[kLpEach];
     float m[kLpEach], top = -INFINITY;
     const bool whole = i + (kLpEach - 1) * kLpThreads < v1;
@@ -347,15 +345,14 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
 #pragma unroll
     for (int u = 0; u < kLpEach; ++u) add(w[u]);
     if (k == 0) continue;
-    if (times == 0) {
-      top0 = top;
+    if (times < last_first) {
+      early = fmaxf(early, top);
       continue;
     }
-    if (times == 1) {
-      float g = fmaxf(top0, top);
+    if (times == last_first) {
+      float g = fmaxf(early, top);
       g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
-      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-      if (tid % 4 == 0) group_top[tid / 4] = g;
+      if (tid % 2 == 0) group_top[tid / 2] = g;
       __syncthreads();
       if (tid < GROUPS) {
         g = group_top[tid];
@@ -372,27 +369,30 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
       __syncthreads();
       threshold = first_threshold;
       reach = key_value(threshold);
-      if (top0 >= reach)  // those of the first time, read again
+      if (early >= reach) {  // those of the times before, read again
 #pragma unroll 1
-        for (int j = i - kStep; j < min(i, v1); j += kLpThreads) {
-          const uint4 x = __ldg(xv + j);
-          if (reaches(V::most(x), j)) put_aside(x, j);
+        for (int j = v0 + tid; j < min(i, v1); j += kStep) {
+          uint4 x[kLpEach];
+#pragma unroll
+          for (int u = 0; u < kLpEach; ++u) x[u] = j + u * kLpThreads < v1 ? __ldg(xv + j + u * kLpThreads) : V::nothing();
+#pragma unroll
+          for (int u = 0; u < kLpEach; ++u)
+            if (V::most(x[u]) >= reach && j + u * kLpThreads < v1) put_aside(x[u], j + u * kLpThreads);
         }
+      }
     }
 #pragma unroll
     for (int u = 0; u < kLpEach; ++u)
-      if (m[u] >= reach)
-        if (reaches(m[u], i + u * kLpThreads) && i + u * kLpThreads < v1) put_aside(w[u], i + u * kLpThreads);
+      if (m[u] >= reach && i + u * kLpThreads < v1) put_aside(w[u], i + u * kLpThreads);
   }
-  int kept = 0;  // of the k largest
   for (bool again = k > 0; again;) {
     __syncthreads();
     const int n = aside_count;
     again = n > kAside;
     for (bool full = true; full;) {  // keys of those aside
-      if (tid < min(n, kAside)) {
-        uint4 w = aside[tid];
-        const int id = head + aside_at[tid] * N;
+      for (int i = tid; i < min(n, kAside); i += kLpThreads) {
+        uint4 w = aside[i];
+        const int id = head + aside_at[i] * N;
 #pragma unroll 1
         for (int e = 0; e < N; ++e) offer(V::next(w), id + e);
       }
@@ -400,11 +400,11 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
       __syncthreads();
       const int found = count;
       full = found > kKeys;
-      kept = min(found, kKeys);
-      thin(keys, kept, k);
+      const int kept = min(found, kKeys);
+      if (tid < kTop) best[tid] = 0;  // below every key
+      thin(keys, kept, k, best);
       if (kept >= k) {  // k logits are at least the next threshold
-        kept = k;
-        threshold = max(threshold, keys[k - 1]);
+        threshold = max(threshold, best[k - 1]);
         reach = key_value(threshold);
         reach_id = key_id(threshold);
       }
@@ -422,7 +422,6 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
       }
     }
   }
-  if (tid < kTop) best[tid] = tid < kept ? keys[tid] : 0;  // 0: below every key
   fold();
   // the block's sums, all against the largest reference
   auto join_sums = [&](Sums &a) {
@@ -446,9 +445,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   if (A.cluster > 1) {
     cluster_sync();
     if (rank == 0) {
-      const int from_block = k > 0 ? tid / k : A.cluster, which = tid - from_block * k;
-      uint64_t key = 0;
-      if (from_block < A.cluster) key = ld_cluster_u64(cluster_map(smem_u32(best + which), from_block));
+      for (int i = tid; i < A.cluster * k; i += kLpThreads) {
+        const int b = i / static_cast<uint32_t>(k);
+        keys[i] = ld_cluster_u64(cluster_map(smem_u32(best + i - b * k), b));
+      }
       if (warp == 0) {
         a = {-FLT_MAX, 0.f, 0.f};
         if (lane < A.cluster) {
@@ -459,11 +459,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
         join_sums(a);
         if (lane == 0) block_sums = a;
       }
-      if (k > 0) {
-        if (from_block < A.cluster) keys[tid] = key;
-        thin_lists(keys, A.cluster, k);
-        if (tid < k) best[tid] = keys[tid];
-      }
+      __syncthreads();
+      if (k > 0) join_lists(keys, A.cluster, k, k, k, best);
     }
     __syncthreads();
     cluster_sync();  // every block's sums and candidates are read
@@ -558,9 +555,10 @@ extern "C" bd_status bd_token_logprobs(const void *logits, int64_t row_stride, i
   A.lse = lse;
   A.top_ids = top_ids;
   A.top_logprob = top_logprob;
-  // blocks of a row while there are SMs left for them and 16 KB of logits for each
+  // blocks of a row while there are two SMs' places left for them (of 152 rows two each 22.3 us, four 30.1 us; of 304 rows one
+  // 34.3 us, two 31.9 us) and 16 KB of logits for each
   A.cluster = 1;
-  while (A.cluster < kLpCluster && static_cast<int64_t>(rows) * A.cluster * 2 <= num_sms() && vocab * size > A.cluster * 16384) A.cluster *= 2;
+  while (A.cluster < kLpCluster && static_cast<int64_t>(rows) * A.cluster * 2 <= 2 * num_sms() && vocab * size > A.cluster * 16384) A.cluster *= 2;
   use_target_kernels();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == BD_F32 ? launch<float>(A, s) : dtype == BD_BF16 ? launch<__nv_bfloat16>(A, s) : launch<__half>(A, s);
