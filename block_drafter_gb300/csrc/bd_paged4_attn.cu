@@ -7,10 +7,10 @@
 //   * Slots are the M side of both products (mma.sync m16n8k16, fp16): S^T = K Q^T and O^T = V^T P^T.  The rows of a
 //     KV head are the N side, 8 at a time, so that a token's few rows fill what they use and half as many products
 //     are issued as with the rows on the M side.
-//   * The order of the D products of a score and of a slot's places in the second product is free.  So a lane loads
+//   * The order of the D products of a score and of a slot's places in the second product is free.  So a lane takes
 //     16 consecutive bytes of each of its two slots (32 values, every fragment of its column group) and, of the
-//     values, 8 bytes of each of four slots (16 values, every fragment of its row group): straight from the pools into
-//     the registers they are unpacked from, kAhead units early; nothing passes through shared memory.
+//     values, 8 bytes of each of four slots (16 values, every fragment of its row group).  They come through the warp's
+//     ring in shared memory, kAhead units early, in an order that keeps both reads free of bank conflicts.
 //   * Codes become fp16 pairs by conversion and are multiplied by the group's scale: exact (2 bits times 4), so
 //     that both products run on exactly the values that the slots stand for.  A value pair is two slots of one
 //     column: their nibbles are brought side by side first.
@@ -28,7 +28,7 @@ BD_DEFINE_ERROR_TAKER(take_error_word_paged4_attn)
 
 namespace {
 
-constexpr int kAhead = 3;     // units of a warp on their way
+constexpr int kAhead = 4;     // units of a warp's ring
 constexpr float kHead = 6.f;  // weights are formed against 2^-kHead of the reference: at most 2^14
 constexpr float kMove = 8.f;
 
@@ -46,6 +46,25 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t twice_lo(uint32_t s) { return __byte_perm(s, s, 0x1010); }
 __device__ __forceinline__ uint32_t twice_hi(uint32_t s) { return __byte_perm(s, s, 0x3232); }
 
+// A unit in a warp's ring: codes of its keys and values, 16 slots of D / 2 bytes, then their scales.  Slots 8 .. 15 lie like
+// 0 .. 7.  The slots a read of values takes at once (0, 2, 4, 6 or 1, 3, 5, 7 of eight) have to be in different banks, and
+// so have neighbours, for the keys: slots 2, 3, 6, 7 (D = 128; slots 4 .. 7 with D = 64) change places in pairs, and with D = 128
+// slots 4 .. 7 have their halves exchanged.
+template <int D> struct Ring {
+  static constexpr int kRow = D / 2, kSide = kUnit * kRow, kScales = kUnit * D / 16;
+  static constexpr int kStage = 2 * kSide + 2 * kScales;
+  static constexpr int kWarp = kAhead * kStage;
+  static constexpr int kSmem = kFewWarps * kWarp;
+  // Byte offset of slot r, from its byte x on (x within one 16-byte piece).
+  static __device__ __forceinline__ int at(int r, int x) {
+    if constexpr (D == 128) return (r ^ (r >> 1 & 1)) * kRow + (x ^ (r >> 2 & 1) * 32);
+    else return (r ^ (r >> 2 & 1)) * kRow + x;
+  }
+};
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes, bool valid) {
+  if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
 // What a lane holds of a unit.  Lane: quad = lane / 4, kq = lane % 4.
 template <int D> struct Frag {
   static constexpr int W = D / 64;  // words of a lane's piece of a value slot (2 of a key slot's W)
@@ -54,16 +73,15 @@ template <int D> struct Frag {
   uint32_t ks[2];                   // scales of the key pieces (W bytes)
   uint32_t vs[4];                   // scale of the value pieces
 };
-
 template <int N> __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
   if constexpr (N == 4) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
   } else if constexpr (N == 2) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
     w[0] = x.x, w[1] = x.y;
   } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
   }
 }
 
@@ -78,8 +96,8 @@ struct FewWarp4 {
   float o[NT][NV][4];
   float m[NT][2], l[NT][2];
 
-  __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int t0, int t1, int warp,
-                                      int lane) {
+  __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int t0, int t1, uint8_t *ring,
+                                      int warp, int lane) {
     const Paged4Args &c4 = A.c;
     const PagedArgs &a = c4.p;
     const int quad = lane >> 2, kq = lane & 3;
@@ -144,72 +162,70 @@ struct FewWarp4 {
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
 
     const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
-    const uint8_t *K = static_cast<const uint8_t *>(a.k) + h * a.head_stride + kq * (D / 8);
-    const uint8_t *V = static_cast<const uint8_t *>(a.v) + h * a.head_stride + quad * (D / 16);
-    const uint8_t *KS = static_cast<const uint8_t *>(c4.k_scale) + h * c4.scale_head_stride + kq * W;
-    const uint8_t *VS = static_cast<const uint8_t *>(c4.v_scale) + h * c4.scale_head_stride + quad * W / 2;
+    // what this lane copies: of the codes 16-byte piece `piece` of slot `slot` (and of slot + 8 with D = 128), of the scales slot
+    // lane % 16's, the keys' (lanes 0 .. 15) or the values'
+    using G = Ring<D>;
+    constexpr int P = D / 32;
+    const int slot = lane / P, piece = lane % P;
+    const uint8_t *K = static_cast<const uint8_t *>(a.k) + h * a.head_stride + piece * 16;
+    const uint8_t *V = static_cast<const uint8_t *>(a.v) + h * a.head_stride + piece * 16;
+    const uint8_t *S = static_cast<const uint8_t *>(lane < 16 ? c4.k_scale : c4.v_scale) + h * c4.scale_head_stride;
+    const uint32_t mine = smem_u32(ring), to_code = mine + G::at(slot, piece * 16);
+    const uint32_t to_scale = mine + 2 * G::kSide + (lane < 16 ? 0 : G::kScales) + (lane & 15) * (D / 16);
     // Page of tile t (of its slot lane % 16): the load alone.
     auto page_of = [&](int t) {
       const int tile = tl.at(max(min(t, t1 - 1), 0));
       if constexpr (PAGE16) return __ldg(table + (A.units_magic ? __umulhi(tile, A.units_magic) : tile));
       else return __ldg(table + min(tile * kUnit + (lane & 15), rq.n - 1) / a.page_size);
     };
-    auto load = [&](Frag<D> &x, int t, int page) {
-      if (t >= t1) return;
-      if constexpr (PAGE16) {
-        const uint32_t tile = tl.at(t), in = A.units_magic ? tile - __umulhi(tile, A.units_magic) * A.page_units : 0;
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
-          atomicOr(&g_error_word, DEVERR_BAD_INDEX);
-          x = {};
-          return;
-        }
-        // strides of a slot are below 2^27 bytes here: a lane's place in the unit is one 32-bit product
-        const uint32_t ss = static_cast<uint32_t>(a.slot_stride), zs = static_cast<uint32_t>(c4.scale_slot_stride);
-        const int64_t code = page * a.page_stride + static_cast<int64_t>(in) * (16 * ss);
-        const int64_t scale = page * c4.scale_page_stride + static_cast<int64_t>(in) * (16 * zs);
-        const uint8_t *k = K + code, *v = V + code, *ks = KS + scale, *vs = VS + scale;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t slot = quad + 8 * y;
-          load_words(x.k[y], k + static_cast<uint64_t>(slot) * ss);
-          const uint8_t *z = ks + static_cast<uint64_t>(slot) * zs;
-          if constexpr (W == 2) x.ks[y] = __ldg(reinterpret_cast<const uint16_t *>(z));
-          else x.ks[y] = __ldg(z);
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint32_t slot = 2 * kq + (y & 1) + 8 * (y >> 1);
-          load_words(x.v[y], v + static_cast<uint64_t>(slot) * ss);
-          x.vs[y] = __ldg(vs + static_cast<uint64_t>(slot) * zs);
-        }
-      } else {
-        const int j = tl.at(t) * kUnit + (lane & 15);
-        Place4 at = {-1, -1};
-        if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, page, j);
-        auto of = [&](int slot, int64_t &code, int64_t &scale) {
-          code = __shfl_sync(0xffffffffu, at.code, slot);
-          scale = __shfl_sync(0xffffffffu, at.scale, slot);
-        };
-        x = {};
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          int64_t code, scale;
-          of(quad + 8 * y, code, scale);
-          if (code >= 0) {
-            load_words(x.k[y], K + code);
-            if constexpr (W == 2) x.ks[y] = __ldg(reinterpret_cast<const uint16_t *>(KS + scale));
-            else x.ks[y] = __ldg(KS + scale);
+    auto copy = [&](int t, int page, int stage) {
+      if (t < t1) {
+        const uint32_t to = stage * G::kStage;
+        if constexpr (PAGE16) {
+          const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
+          if (!ok) atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+          const uint32_t tile = tl.at(t), in = A.units_magic ? tile - __umulhi(tile, A.units_magic) * A.page_units : 0;
+          // strides of a slot are below 2^27 bytes here: a place in the unit is one 32-bit product
+          const uint32_t ss = static_cast<uint32_t>(a.slot_stride), zs = static_cast<uint32_t>(c4.scale_slot_stride);
+          const int64_t pg = ok ? page : 0;
+          const int64_t code = pg * a.page_stride + static_cast<int64_t>(in) * (16 * ss) + static_cast<uint32_t>(slot) * ss;
+          cp_async16(to_code + to, K + code, ok);
+          cp_async16(to_code + to + G::kSide, V + code, ok);
+          if constexpr (D == 128) {
+            cp_async16(to_code + to + 8 * G::kRow, K + code + 8 * ss, ok);
+            cp_async16(to_code + to + G::kSide + 8 * G::kRow, V + code + 8 * ss, ok);
           }
-        }
+          const int64_t scale = pg * c4.scale_page_stride + static_cast<int64_t>(in) * (16 * zs) + static_cast<uint32_t>(lane & 15) * zs;
+          cp_async_small(to_scale + to, S + scale, D / 16, ok);
+        } else {
+          const int j = tl.at(t) * kUnit + (lane & 15);
+          Place4 at = {-1, -1};
+          if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, page, j);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          int64_t code, scale;
-          of(2 * kq + (y & 1) + 8 * (y >> 1), code, scale);
-          if (code >= 0) {
-            load_words(x.v[y], V + code);
-            x.vs[y] = __ldg(VS + scale);
+          for (int y = 0; y < P / 2; ++y) {
+            const int64_t code = __shfl_sync(0xffffffffu, at.code, slot + 8 * y);
+            cp_async16(to_code + to + y * 8 * G::kRow, K + (code < 0 ? 0 : code), code >= 0);
+            cp_async16(to_code + to + y * 8 * G::kRow + G::kSide, V + (code < 0 ? 0 : code), code >= 0);
           }
+          cp_async_small(to_scale + to, S + (at.code < 0 ? 0 : at.scale), D / 16, at.code >= 0);
         }
+      }
+      cp_async_commit();
+    };
+    const uint8_t *from_k = ring + G::at(quad, kq * (D / 8)), *from_ks = ring + 2 * G::kSide + quad * (D / 16) + kq * W;
+    const uint8_t *from_v0 = ring + G::kSide + G::at(2 * kq, quad * (D / 16)), *from_v1 = ring + G::kSide + G::at(2 * kq + 1, quad * (D / 16));
+    const uint8_t *from_vs = ring + 2 * G::kSide + G::kScales + 2 * kq * (D / 16) + quad * W / 2;
+    auto fetch = [&](Frag<D> &x, int stage) {
+      const int o = stage * G::kStage;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        load_words(x.k[y], from_k + o + y * 8 * G::kRow);
+        if constexpr (W == 2) x.ks[y] = *reinterpret_cast<const uint16_t *>(from_ks + o + y * 8 * (D / 16));
+        else x.ks[y] = from_ks[o + y * 8 * (D / 16)];
+        load_words(x.v[2 * y], from_v0 + o + y * 8 * G::kRow);
+        load_words(x.v[2 * y + 1], from_v1 + o + y * 8 * G::kRow);
+        x.vs[2 * y] = from_vs[o + y * 8 * (D / 16)];
+        x.vs[2 * y + 1] = from_vs[o + (y * 8 + 1) * (D / 16)];
       }
     };
     auto work = [&](const Frag<D> &x, int t) {
@@ -308,26 +324,28 @@ struct FewWarp4 {
         }
       }
     };
-    // unit i of the warp is tile t0 + warp + i * kFewWarps; fragments of kAhead units are on their way
-    Frag<D> x[kAhead];
-    int page[kAhead];
-    int t = t0 + warp;
+    // unit i of the warp is tile t0 + warp + i * kFewWarps
+    int t = t0 + warp, page[kAhead];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) page[s] = page_of(t + s * kFewWarps);
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) load(x[s], t + s * kFewWarps, page[s]);
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) page[s] = page_of(t + (kAhead + s) * kFewWarps);
-    while (t < t1) {
-#pragma unroll
-      for (int s = 0; s < kAhead; ++s) {
-        if (t >= t1) break;
-        work(x[s], t);
-        load(x[s], t + kAhead * kFewWarps, page[s]);
-        page[s] = page_of(t + 2 * kAhead * kFewWarps);
-        t += kFewWarps;
+    for (int s = 0; s < kAhead - 1; ++s) copy(t + s * kFewWarps, page[s], s);
+    int next = page[kAhead - 1], stage = 0;
+    for (; t < t1; t += kFewWarps) {
+      cp_async_wait<kAhead - 2>();
+      __syncwarp();
+      Frag<D> x;
+      fetch(x, stage);
+      {  // the stage of the unit before, which every lane has fetched, takes the unit kAhead - 1 ahead
+        const int ahead = t + (kAhead - 1) * kFewWarps;
+        copy(ahead, next, stage == 0 ? kAhead - 1 : stage - 1);
+        next = page_of(ahead + kFewWarps);
       }
+      work(x, t);
+      stage = stage + 1 == kAhead ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
+    __syncwarp();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -357,10 +375,14 @@ template <typename T, int D> __device__ void no_slots(const Paged4AttnArgs &A, c
   empty_rows<T, D>(x, rq, rq.rows, tid, step);
 }
 
+template <int NT> constexpr int few4_per_sm() { return NT == 1 ? 4 : 2; }  // blocks an SM holds at once
+
 template <typename T, int D, int NT, bool PAGE16>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(const __grid_constant__ Paged4AttnArgs A) {
+__global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4(const __grid_constant__ Paged4AttnArgs A) {
   constexpr int ROWS = 8 * NT;
-  __shared__ __align__(16) float so[kFewWarps][ROWS][D + 4];  // the warps' sums
+  extern __shared__ __align__(128) uint8_t sm_raw[];
+  static_assert(ROWS * (D + 4) * 4 <= Ring<D>::kWarp, "a warp's sums take the place of its ring");
+  auto so = [&](int w, int r, int d) { return reinterpret_cast<float *>(sm_raw + w * Ring<D>::kWarp) + r * (D + 4) + d; };
   __shared__ int64_t start[BD_PAGED_MAX_REQUESTS + 1];
   __shared__ int64_t warp_sum_s[kFewWarps];
   __shared__ Request first[kFewThreads];
@@ -414,14 +436,14 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(c
     const int R = rq.rows * a.group;
     {
       FewWarp4<T, D, NT, PAGE16> w;
-      w.run(A, rq, tl, b, h, t0, t1, warp, lane);
+      w.run(A, rq, tl, b, h, t0, t1, sm_raw + warp * Ring<D>::kWarp, warp, lane);
       const int quad = lane >> 2, kq = lane & 3;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int r = 8 * n + 2 * kq + y;
-          float *to = &so[warp][r][quad * (D / 8)];
+          float *to = so(warp, r, quad * (D / 8));
 #pragma unroll
           for (int i = 0; i < D / 16; i += 2)
             *reinterpret_cast<float4 *>(to + 2 * i) = make_float4(w.o[n][i][y], w.o[n][i][y + 2], w.o[n][i + 1][y], w.o[n][i + 1][y + 2]);
@@ -445,7 +467,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(c
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kFewWarps; ++i) {
-        const float4 v = *reinterpret_cast<const float4 *>(&so[i][r][d]);
+        const float4 v = *reinterpret_cast<const float4 *>(so(i, r, d));
         const float w = x[i].y == 0.f ? 0.f : exp2f(x[i].x - M);
         L += w * x[i].y;
         o.x += w * v.x;
@@ -454,7 +476,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(c
         o.w += w * v.w;
       }
       if (A.cluster > 1) {
-        *reinterpret_cast<float4 *>(&so[0][r][d]) = o;
+        *reinterpret_cast<float4 *>(so(0, r, d)) = o;
         if (d == 0) block_ml[r] = make_float2(M, L);
       } else if (whole) {
         finish<T>(A, rq, h, r, d, o, M, L);
@@ -469,7 +491,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 3 : 2) attention_few4(c
       const int rank = g % static_cast<uint32_t>(A.cluster), d = lane * 4;
       for (int r = rank + A.cluster * warp; r < R; r += A.cluster * kFewWarps) {
         float4 v[kMostCluster];
-        const uint32_t at = smem_u32(&so[0][r][d % D]);
+        const uint32_t at = smem_u32(so(0, r, d % D));
 #pragma unroll
         for (int i = 0; i < kMostCluster; ++i)
           if (i < A.cluster) v[i] = ld_cluster_f4(cluster_map(at, i));
@@ -583,16 +605,18 @@ constexpr int kClusterSlots = 1088, kClusterFilled = 2176;
 constexpr int kJoinSlots = 800, kPartSlots = 2;
 
 // Blocks of a launch that is shared out: as many as the SMs hold at once.
-int few4_blocks(int nt) {
-  const int n = (nt == 1 ? 3 : 2) * num_sms();
+int few4_blocks(int per_sm) {
+  const int n = per_sm * num_sms();
   return n < kJoinParts4 ? n : kJoinParts4 - 1;
 }
 
 template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
   const PagedArgs &a = A.c.p;
   auto kernel = attention_few4<T, D, NT, PAGE16>;
-  A.n_ctas = few4_blocks(NT);
-  static const ClustersAtOnce fit(kernel, kFewThreads, 0);
+  A.n_ctas = few4_blocks(few4_per_sm<NT>());
+  static const ClustersAtOnce fit(kernel, kFewThreads, Ring<D>::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kSmem);
+  if (e != cudaSuccess) return e;
   const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
   int blocks = 1;
   while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
@@ -608,9 +632,9 @@ template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnA
   if (A.whole) {
     const cudaError_t c = allow_cluster(kernel, blocks);
     if (c != cudaSuccess) return c;
-    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(heads * blocks)), dim3(kFewThreads), 0, s, blocks, A);
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(heads * blocks)), dim3(kFewThreads), Ring<D>::kSmem, s, blocks, A);
   }
-  const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), 0, s, A);
+  const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Ring<D>::kSmem, s, A);
   if (f != cudaSuccess) return f;
   const int rows = a.max_rows * a.group;
   return launch_pdl(attention_join4<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
@@ -632,13 +656,13 @@ template <typename T, int D> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t 
 }  // namespace
 
 size_t few4_bytes(int head_dim) {
-  const size_t parts = 2 * static_cast<size_t>(few4_blocks(1)) * kFewRows4;
-  return align256(few4_blocks(1) * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
+  const size_t parts = 2 * static_cast<size_t>(few4_blocks(few4_per_sm<1>())) * kFewRows4;
+  return align256(few4_blocks(few4_per_sm<1>()) * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
 }
 
 std::string launch_attention_few4(Paged4AttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
-  const size_t blocks = few4_blocks(1), parts = 2 * blocks * kFewRows4;  // the most that a launch has
+  const size_t blocks = few4_blocks(few4_per_sm<1>()), parts = 2 * blocks * kFewRows4;  // the most that a launch has
   A.join = reinterpret_cast<PagedJoin *>(p);
   p += align256(blocks * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);
