@@ -42,10 +42,15 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// Two scales (bytes) as fp16; a NaN's code is 448, so that whatever bytes a hidden slot holds are numbers.
-__device__ __forceinline__ uint32_t scales_f16x2(uint32_t two) {
+// Two scales (bytes) as fp16.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
   uint32_t d;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(two)));
+  return d;
+}
+// The same, a NaN's code as 448: whatever bytes a hidden slot holds are numbers, which a weight of zero drops.
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t two) {
+  uint32_t d = e4m3_pair(two);
   asm("min.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x5f005f00u));  // min of a NaN and 448: 448
   return d;
 }

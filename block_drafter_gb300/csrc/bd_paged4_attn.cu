@@ -31,6 +31,7 @@ namespace {
 constexpr int kAhead = 4;     // units of a warp's ring
 constexpr float kHead = 6.f;  // weights are formed against 2^-kHead of the reference: at most 2^14
 constexpr float kMove = 8.f;
+constexpr float kNone = -1e30f;  // the reference of a row that has seen nothing: any score moves it
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -94,7 +95,7 @@ struct FewWarp4 {
   static constexpr int W = D / 64, NK = D / 16, NV = D / 16;
   static constexpr bool kRest = std::is_same<T, __half>::value;
   float o[NT][NV][4];
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2];  // what weights are formed against, the maximum less kHead; their sums
 
   __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int t0, int t1, uint8_t *ring,
                                       int warp, int lane) {
@@ -150,7 +151,7 @@ struct FewWarp4 {
         const int r = 8 * n + 2 * kq + y;
         p[n][y] = r < R ? rq.n - rq.rows + r / a.group : -1;
         f[n][y] = p[n][y] >= 0 ? window_first(a, p[n][y]) : 0;
-        m[n][y] = -INFINITY;
+        m[n][y] = kNone;
         l[n][y] = 0.f;
       }
     const int p_low = rq.n - rq.rows, f_high = window_first(a, rq.n - 1), f_low = window_first(a, max(0, p_low));
@@ -167,40 +168,50 @@ struct FewWarp4 {
     using G = Ring<D>;
     constexpr int P = D / 32;
     const int slot = lane / P, piece = lane % P;
-    const uint8_t *K = static_cast<const uint8_t *>(a.k) + h * a.head_stride + piece * 16;
-    const uint8_t *V = static_cast<const uint8_t *>(a.v) + h * a.head_stride + piece * 16;
-    const uint8_t *S = static_cast<const uint8_t *>(lane < 16 ? c4.k_scale : c4.v_scale) + h * c4.scale_head_stride;
+    const uint32_t ss = static_cast<uint32_t>(a.slot_stride), zs = static_cast<uint32_t>(c4.scale_slot_stride);  // PAGE16
+    const int64_t code0 = h * a.head_stride + piece * 16 + (PAGE16 ? slot * a.slot_stride : 0);
+    const uint8_t *K = static_cast<const uint8_t *>(a.k) + code0, *V = static_cast<const uint8_t *>(a.v) + code0;
+    const uint8_t *S = static_cast<const uint8_t *>(lane < 16 ? c4.k_scale : c4.v_scale) + h * c4.scale_head_stride +
+                       (PAGE16 ? (lane & 15) * c4.scale_slot_stride : 0);
     const uint32_t mine = smem_u32(ring), to_code = mine + G::at(slot, piece * 16);
     const uint32_t to_scale = mine + 2 * G::kSide + (lane < 16 ? 0 : G::kScales) + (lane & 15) * (D / 16);
-    // Page of tile t (of its slot lane % 16): the load alone.
-    auto page_of = [&](int t) {
-      const int tile = tl.at(max(min(t, t1 - 1), 0));
-      if constexpr (PAGE16) return __ldg(table + (A.units_magic ? __umulhi(tile, A.units_magic) : tile));
-      else return __ldg(table + min(tile * kUnit + (lane & 15), rq.n - 1) / a.page_size);
+    // Where tile t lies: its page (of its slot lane % 16) -- the load alone -- and its unit in that.
+    struct Spot {
+      int page;
+      uint32_t in;
     };
-    auto copy = [&](int t, int page, int stage) {
+    auto spot_of = [&](int t) {
+      const uint32_t tile = tl.at(max(min(t, t1 - 1), 0));
+      if constexpr (PAGE16) {
+        const uint32_t q = A.units_magic ? __umulhi(tile, A.units_magic) : tile;
+        return Spot{__ldg(table + q), tile - q * A.page_units};
+      } else {
+        return Spot{__ldg(table + min(static_cast<int>(tile) * kUnit + (lane & 15), rq.n - 1) / a.page_size), 0};
+      }
+    };
+    auto copy = [&](int t, const Spot &spot, int stage) {
       if (t < t1) {
         const uint32_t to = stage * G::kStage;
         if constexpr (PAGE16) {
-          const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
+          const bool ok = static_cast<unsigned>(spot.page) < static_cast<unsigned>(a.n_pages);
           if (!ok) atomicOr(&g_error_word, DEVERR_BAD_INDEX);
-          const uint32_t tile = tl.at(t), in = A.units_magic ? tile - __umulhi(tile, A.units_magic) * A.page_units : 0;
-          // strides of a slot are below 2^27 bytes here: a place in the unit is one 32-bit product
-          const uint32_t ss = static_cast<uint32_t>(a.slot_stride), zs = static_cast<uint32_t>(c4.scale_slot_stride);
-          const int64_t pg = ok ? page : 0;
-          const int64_t code = pg * a.page_stride + static_cast<int64_t>(in) * (16 * ss) + static_cast<uint32_t>(slot) * ss;
+          const uint32_t page = ok ? spot.page : 0;
+          // strides are below 2^32 bytes here, of a slot below 2^27
+          const uint64_t code = static_cast<uint64_t>(page) * static_cast<uint32_t>(a.page_stride) + static_cast<uint64_t>(spot.in) * (16 * ss);
           cp_async16(to_code + to, K + code, ok);
           cp_async16(to_code + to + G::kSide, V + code, ok);
           if constexpr (D == 128) {
-            cp_async16(to_code + to + 8 * G::kRow, K + code + 8 * ss, ok);
-            cp_async16(to_code + to + G::kSide + 8 * G::kRow, V + code + 8 * ss, ok);
+            const uint64_t second = code + 8 * ss;
+            cp_async16(to_code + to + 8 * G::kRow, K + second, ok);
+            cp_async16(to_code + to + G::kSide + 8 * G::kRow, V + second, ok);
           }
-          const int64_t scale = pg * c4.scale_page_stride + static_cast<int64_t>(in) * (16 * zs) + static_cast<uint32_t>(lane & 15) * zs;
+          const uint64_t scale =
+              static_cast<uint64_t>(page) * static_cast<uint32_t>(c4.scale_page_stride) + static_cast<uint64_t>(spot.in) * (16 * zs);
           cp_async_small(to_scale + to, S + scale, D / 16, ok);
         } else {
           const int j = tl.at(t) * kUnit + (lane & 15);
           Place4 at = {-1, -1};
-          if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, page, j);
+          if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, spot.page, j);
 #pragma unroll
           for (int y = 0; y < P / 2; ++y) {
             const int64_t code = __shfl_sync(0xffffffffu, at.code, slot + 8 * y);
@@ -232,7 +243,8 @@ struct FewWarp4 {
       // scores of slots quad (+ 8), rows 8n + 2kq (+ 1)
       float c[NT][4] = {};
       {
-        uint32_t s0 = scales_f16x2(x.ks[0]), s1 = scales_f16x2(x.ks[1]);
+        // a NaN among the keys' scales is a hidden slot's, whose scores are dropped
+        const uint32_t s0 = e4m3_pair(x.ks[0]), s1 = e4m3_pair(x.ks[1]);
 #pragma unroll
         for (int w = 0; w < 2 * W; ++w) {
           const uint32_t f0 = w < 2 ? twice_lo(s0) : twice_hi(s0), f1 = w < 2 ? twice_lo(s1) : twice_hi(s1);
@@ -252,27 +264,31 @@ struct FewWarp4 {
       }
       const int j0 = tl.at(t) * kUnit;
       const bool masked = !(j0 + kUnit - 1 <= p_low && (j0 >= f_high || j0 + kUnit <= a.n_sink));  // some row does not see all of it
-      bool moves = false;
+      if (masked) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[n][e] *= to_log2[n][e & 1];
-          if (masked) {
+          for (int e = 0; e < 4; ++e) {
             const int j = j0 + quad + 8 * (e >> 1);
             if (!(j <= p[n][e & 1] && (j >= f[n][e & 1] || j < a.n_sink))) c[n][e] = -INFINITY;
           }
-          moves |= c[n][e] > m[n][e & 1] + kMove;
-        }
-      if (__any_sync(0xffffffffu, moves)) {
+      }
+      float most = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+          most = max3(most, fmaf(c[n][e], to_log2[n][0], -m[n][0]), fmaf(c[n][e + 1], to_log2[n][1], -m[n][1]));
+      if (__any_sync(0xffffffffu, most > kHead + kMove)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float mx = fmaxf(m[n][y], fmaxf(c[n][y], c[n][y + 2]));
+            float mx = fmaxf(c[n][y], c[n][y + 2]) * to_log2[n][y];
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            const float w = m[n][y] == mx ? 1.f : exp2_fast(m[n][y] - mx);
+            mx = fmaxf(mx - kHead, m[n][y]);
+            const float w = exp2_fast(m[n][y] - mx);
             m[n][y] = mx;
             l[n][y] *= w;
 #pragma unroll
@@ -286,10 +302,9 @@ struct FewWarp4 {
       uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kHead, r1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kHead;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float w0 = exp2_fast(c[n][2 * y] - r0), w1 = exp2_fast(c[n][2 * y + 1] - r1);
+          const float w0 = exp2_fast(fmaf(c[n][2 * y], to_log2[n][0], -m[n][0])), w1 = exp2_fast(fmaf(c[n][2 * y + 1], to_log2[n][1], -m[n][1]));
           const uint32_t hv = Pair<__half>::pack(w0, w1);
           hi[n][y] = transpose8x8(hv);
           if constexpr (kRest) {
@@ -325,12 +340,13 @@ struct FewWarp4 {
       }
     };
     // unit i of the warp is tile t0 + warp + i * kFewWarps
-    int t = t0 + warp, page[kAhead];
+    int t = t0 + warp, stage = 0;
+    Spot spots[kAhead];
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) page[s] = page_of(t + s * kFewWarps);
+    for (int s = 0; s < kAhead; ++s) spots[s] = spot_of(t + s * kFewWarps);
 #pragma unroll
-    for (int s = 0; s < kAhead - 1; ++s) copy(t + s * kFewWarps, page[s], s);
-    int next = page[kAhead - 1], stage = 0;
+    for (int s = 0; s < kAhead - 1; ++s) copy(t + s * kFewWarps, spots[s], s);
+    Spot next = spots[kAhead - 1];
     for (; t < t1; t += kFewWarps) {
       cp_async_wait<kAhead - 2>();
       __syncwarp();
@@ -339,7 +355,7 @@ struct FewWarp4 {
       {  // the stage of the unit before, which every lane has fetched, takes the unit kAhead - 1 ahead
         const int ahead = t + (kAhead - 1) * kFewWarps;
         copy(ahead, next, stage == 0 ? kAhead - 1 : stage - 1);
-        next = page_of(ahead + kFewWarps);
+        next = spot_of(ahead + kFewWarps);
       }
       work(x, t);
       stage = stage + 1 == kAhead ? 0 : stage + 1;
@@ -352,7 +368,7 @@ struct FewWarp4 {
       for (int y = 0; y < 2; ++y) {
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) l[n][y] += __shfl_xor_sync(0xffffffffu, l[n][y], s);
-        if (m[n][y] != -INFINITY) m[n][y] -= kHead;  // the reference the sums are against
+        if (m[n][y] == kNone) m[n][y] = -INFINITY;
       }
   }
 };
@@ -644,7 +660,9 @@ template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaS
   // tile * units < 2^32
   const PagedArgs &a = A.c.p;
   const int64_t units = a.page_size / kUnit, strides = a.slot_stride > A.c.scale_slot_stride ? a.slot_stride : A.c.scale_slot_stride;
-  if (a.page_size % kUnit || units * (a.max_len / kUnit + 1) >= (1ll << 32) || strides >= (1 << 27)) return launch<T, D, NT, false>(A, s);
+  if (a.page_size % kUnit || units * (a.max_len / kUnit + 1) >= (1ll << 32) || strides >= (1 << 27) || a.page_stride >= (1ll << 32) ||
+      A.c.scale_page_stride >= (1ll << 32))
+    return launch<T, D, NT, false>(A, s);
   A.page_units = static_cast<uint32_t>(units);
   A.units_magic = units == 1 ? 0 : static_cast<uint32_t>(((1ll << 32) + units - 1) / units);
   return launch<T, D, NT, true>(A, s);

@@ -604,7 +604,8 @@ bd_status bd_paged_plan(const bd_paged_pages *pages, const int32_t *len, const i
  * exp only shifts the range (its precision is the scale's): a group is kept to a relative 2^-4 of its
  * magnitude while max |x| is between 2^-6 * 6 * 2^exp and 2688 * 2^exp.  A group that holds an infinity or
  * NaN is stored as zeros, a larger one saturates; both set the device error word (bd_sync_status:
- * BD_ERR_RANGE).  The e4m3 code of a NaN in a scale reads as 448: hidden slots may hold any bytes.
+ * BD_ERR_RANGE).  Slots that a row does not see may hold any bytes; what a scale with the e4m3 code of a NaN, which no append
+ * writes, stands for in a slot that it does see is unspecified.
  *
  * Requests, slots, rows, visibility, lengths and page ids are as above, and bd_paged_batch and bd_paged_plan serve
  * both caches.  Products take the stored values exactly.
