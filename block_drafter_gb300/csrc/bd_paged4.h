@@ -23,7 +23,7 @@ struct Paged4AttnArgs {
   float *part_o;
   float2 *part_ml;
   int n_ctas, whole, cluster;
-  uint32_t page_units, units_magic;  // units of 16 slots of a page, and what divides by them
+  uint32_t page_units, units_magic;  // 16-slot places of a page, and what divides by them
 };
 
 // Query rows (of one KV head) of the kernel that reads the codes themselves.

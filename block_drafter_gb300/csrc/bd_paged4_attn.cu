@@ -1,7 +1,7 @@
 // Attention of few rows over a 4-bit cache (bd_paged4_attention with at most kFewRows4 rows of a KV head:
 // decoding and short blocks).
 //
-// The scheme is the 16-bit kernel's -- one pass with the running maximum and sum, units of 16 slots shared out evenly or a
+// The scheme is the 16-bit kernel's -- one pass with the running maximum and sum, units of 32 slots shared out evenly or a
 // cluster a head, every warp alone on every fourth unit -- but what bounds it is not only the bytes (0.5625 a
 // value): each value has to be unpacked and scaled, so the products are laid out for that.
 //   * Slots are the M side of both products (mma.sync m16n8k16, fp16): S^T = K Q^T and O^T = V^T P^T.  The rows of a
@@ -28,7 +28,8 @@ BD_DEFINE_ERROR_TAKER(take_error_word_paged4_attn)
 
 namespace {
 
-constexpr int kAhead = 4;     // units of a warp's ring
+constexpr int kUnit4 = 32;    // slots of a unit: two steps of the products, whose chains run side by side
+constexpr int kAhead = 2;     // units of a warp's ring
 constexpr float kHead = 6.f;  // weights are formed against 2^-kHead of the reference: at most 2^14
 constexpr float kMove = 8.f;
 constexpr float kNone = -1e30f;  // the reference of a row that has seen nothing: any score moves it
@@ -47,12 +48,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t twice_lo(uint32_t s) { return __byte_perm(s, s, 0x1010); }
 __device__ __forceinline__ uint32_t twice_hi(uint32_t s) { return __byte_perm(s, s, 0x3232); }
 
-// A unit in a warp's ring: codes of its keys and values, 16 slots of D / 2 bytes, then their scales.  Slots 8 .. 15 lie like
+// A unit in a warp's ring: codes of its keys and values, 32 slots of D / 2 bytes, then their scales.  Slots 8 .. 15 (and on) lie like
 // 0 .. 7.  The slots a read of values takes at once (0, 2, 4, 6 or 1, 3, 5, 7 of eight) have to be in different banks, and
 // so have neighbours, for the keys: slots 2, 3, 6, 7 (D = 128; slots 4 .. 7 with D = 64) change places in pairs, and with D = 128
 // slots 4 .. 7 have their halves exchanged.
 template <int D> struct Ring {
-  static constexpr int kRow = D / 2, kSide = kUnit * kRow, kScales = kUnit * D / 16;
+  static constexpr int kRow = D / 2, kSide = kUnit4 * kRow, kScales = kUnit4 * D / 16;
   static constexpr int kStage = 2 * kSide + 2 * kScales;
   static constexpr int kWarp = kAhead * kStage;
   static constexpr int kSmem = kFewWarps * kWarp;
@@ -66,7 +67,7 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, in
   if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
-// What a lane holds of a unit.  Lane: quad = lane / 4, kq = lane % 4.
+// What a lane holds of half a unit.  Lane: quad = lane / 4, kq = lane % 4.
 template <int D> struct Frag {
   static constexpr int W = D / 64;  // words of a lane's piece of a value slot (2 of a key slot's W)
   uint32_t k[2][2 * W];             // slots quad, quad + 8: bytes kq * D/8 ..
@@ -163,62 +164,81 @@ struct FewWarp4 {
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
 
     const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
-    // what this lane copies: of the codes 16-byte piece `piece` of slot `slot` (and of slot + 8 with D = 128), of the scales slot
-    // lane % 16's, the keys' (lanes 0 .. 15) or the values'
+    // what this lane copies: of the codes 16-byte piece `piece` of slots `slot` + STEP y, of the scales slot `lane`'s
     using G = Ring<D>;
-    constexpr int P = D / 32;
+    constexpr int P = D / 32, STEP = 32 / P, Y = kUnit4 / STEP;
     const int slot = lane / P, piece = lane % P;
     const uint32_t ss = static_cast<uint32_t>(a.slot_stride), zs = static_cast<uint32_t>(c4.scale_slot_stride);  // PAGE16
     const int64_t code0 = h * a.head_stride + piece * 16 + (PAGE16 ? slot * a.slot_stride : 0);
+    const int64_t scale0 = h * c4.scale_head_stride + (PAGE16 ? (lane & 15) * c4.scale_slot_stride : 0);
     const uint8_t *K = static_cast<const uint8_t *>(a.k) + code0, *V = static_cast<const uint8_t *>(a.v) + code0;
-    const uint8_t *S = static_cast<const uint8_t *>(lane < 16 ? c4.k_scale : c4.v_scale) + h * c4.scale_head_stride +
-                       (PAGE16 ? (lane & 15) * c4.scale_slot_stride : 0);
-    const uint32_t mine = smem_u32(ring), to_code = mine + G::at(slot, piece * 16);
-    const uint32_t to_scale = mine + 2 * G::kSide + (lane < 16 ? 0 : G::kScales) + (lane & 15) * (D / 16);
-    // Where tile t lies: its page (of its slot lane % 16) -- the load alone -- and its unit in that.
+    const uint8_t *KS = static_cast<const uint8_t *>(c4.k_scale) + scale0, *VS = static_cast<const uint8_t *>(c4.v_scale) + scale0;
+    const uint32_t to_code = smem_u32(ring) + G::at(slot, piece * 16), to_scale = smem_u32(ring) + 2 * G::kSide + lane * (D / 16);
+    // Where tile t lies.  PAGE16: its halves' pages -- the loads alone -- and 16-slot places in those; else the page of its
+    // slot `lane`.
     struct Spot {
-      int page;
-      uint32_t in;
+      int page[PAGE16 ? 2 : 1];
+      uint32_t in[PAGE16 ? 2 : 1];
     };
     auto spot_of = [&](int t) {
-      const uint32_t tile = tl.at(max(min(t, t1 - 1), 0));
+      const int tile = tl.at(max(min(t, t1 - 1), 0));
+      Spot s;
       if constexpr (PAGE16) {
-        const uint32_t q = A.units_magic ? __umulhi(tile, A.units_magic) : tile;
-        return Spot{__ldg(table + q), tile - q * A.page_units};
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t u = min(2 * tile + y, (rq.n - 1) / 16), q = A.units_magic ? __umulhi(u, A.units_magic) : u;
+          s.page[y] = __ldg(table + q);
+          s.in[y] = u - q * A.page_units;
+        }
       } else {
-        return Spot{__ldg(table + min(static_cast<int>(tile) * kUnit + (lane & 15), rq.n - 1) / a.page_size), 0};
+        s.page[0] = __ldg(table + min(tile * kUnit4 + lane, rq.n - 1) / a.page_size);
       }
+      return s;
     };
     auto copy = [&](int t, const Spot &spot, int stage) {
       if (t < t1) {
         const uint32_t to = stage * G::kStage;
+        const int j0 = tl.at(t) * kUnit4;
         if constexpr (PAGE16) {
-          const bool ok = static_cast<unsigned>(spot.page) < static_cast<unsigned>(a.n_pages);
-          if (!ok) atomicOr(&g_error_word, DEVERR_BAD_INDEX);
-          const uint32_t page = ok ? spot.page : 0;
-          // strides are below 2^32 bytes here, of a slot below 2^27
-          const uint64_t code = static_cast<uint64_t>(page) * static_cast<uint32_t>(a.page_stride) + static_cast<uint64_t>(spot.in) * (16 * ss);
-          cp_async16(to_code + to, K + code, ok);
-          cp_async16(to_code + to + G::kSide, V + code, ok);
-          if constexpr (D == 128) {
-            const uint64_t second = code + 8 * ss;
-            cp_async16(to_code + to + 8 * G::kRow, K + second, ok);
-            cp_async16(to_code + to + G::kSide + 8 * G::kRow, V + second, ok);
-          }
-          const uint64_t scale =
-              static_cast<uint64_t>(page) * static_cast<uint32_t>(c4.scale_page_stride) + static_cast<uint64_t>(spot.in) * (16 * zs);
-          cp_async_small(to_scale + to, S + scale, D / 16, ok);
-        } else {
-          const int j = tl.at(t) * kUnit + (lane & 15);
-          Place4 at = {-1, -1};
-          if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, spot.page, j);
+          bool ok[2];
+          uint64_t code[2], scale[2];
 #pragma unroll
-          for (int y = 0; y < P / 2; ++y) {
-            const int64_t code = __shfl_sync(0xffffffffu, at.code, slot + 8 * y);
-            cp_async16(to_code + to + y * 8 * G::kRow, K + (code < 0 ? 0 : code), code >= 0);
-            cp_async16(to_code + to + y * 8 * G::kRow + G::kSide, V + (code < 0 ? 0 : code), code >= 0);
+          for (int y = 0; y < 2; ++y) {
+            // the page of a half that no row sees is not looked at
+            const int j = j0 + 16 * y;
+            ok[y] = j < rq.n && (j + 16 > f_low || j < a.n_sink);
+            if (ok[y] && static_cast<unsigned>(spot.page[y]) >= static_cast<unsigned>(a.n_pages)) {
+              atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+              ok[y] = false;
+            }
+            const uint32_t page = ok[y] ? spot.page[y] : 0;
+            // strides are below 2^32 bytes here, of a slot below 2^27
+            code[y] = static_cast<uint64_t>(page) * static_cast<uint32_t>(a.page_stride) + static_cast<uint64_t>(spot.in[y]) * (16 * ss);
+            scale[y] = static_cast<uint64_t>(page) * static_cast<uint32_t>(c4.scale_page_stride) + static_cast<uint64_t>(spot.in[y]) * (16 * zs);
           }
-          cp_async_small(to_scale + to, S + (at.code < 0 ? 0 : at.scale), D / 16, at.code >= 0);
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const int half = y * STEP / 16;
+            const uint64_t c = code[half] + y * STEP % 16 * ss;
+            cp_async16(to_code + to + y * STEP * G::kRow, K + c, ok[half]);
+            cp_async16(to_code + to + y * STEP * G::kRow + G::kSide, V + c, ok[half]);
+          }
+          const uint64_t z = lane < 16 ? scale[0] : scale[1];
+          const bool zok = lane < 16 ? ok[0] : ok[1];
+          cp_async_small(to_scale + to, KS + z, D / 16, zok);
+          cp_async_small(to_scale + to + G::kScales, VS + z, D / 16, zok);
+        } else {
+          const int j = j0 + lane;
+          Place4 at = {-1, -1};
+          if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, spot.page[0], j);
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const int64_t code = __shfl_sync(0xffffffffu, at.code, slot + STEP * y);
+            cp_async16(to_code + to + y * STEP * G::kRow, K + (code < 0 ? 0 : code), code >= 0);
+            cp_async16(to_code + to + y * STEP * G::kRow + G::kSide, V + (code < 0 ? 0 : code), code >= 0);
+          }
+          cp_async_small(to_scale + to, KS + (at.code < 0 ? 0 : at.scale), D / 16, at.code >= 0);
+          cp_async_small(to_scale + to + G::kScales, VS + (at.code < 0 ? 0 : at.scale), D / 16, at.code >= 0);
         }
       }
       cp_async_commit();
@@ -226,65 +246,103 @@ struct FewWarp4 {
     const uint8_t *from_k = ring + G::at(quad, kq * (D / 8)), *from_ks = ring + 2 * G::kSide + quad * (D / 16) + kq * W;
     const uint8_t *from_v0 = ring + G::kSide + G::at(2 * kq, quad * (D / 16)), *from_v1 = ring + G::kSide + G::at(2 * kq + 1, quad * (D / 16));
     const uint8_t *from_vs = ring + 2 * G::kSide + G::kScales + 2 * kq * (D / 16) + quad * W / 2;
-    auto fetch = [&](Frag<D> &x, int stage) {
-      const int o = stage * G::kStage;
+    // the fragments of slots r .. r + 15 of the stage at byte o
+    auto fetch_keys = [&](Frag<D> &x, int o, int r) {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        load_words(x.k[y], from_k + o + y * 8 * G::kRow);
-        if constexpr (W == 2) x.ks[y] = *reinterpret_cast<const uint16_t *>(from_ks + o + y * 8 * (D / 16));
-        else x.ks[y] = from_ks[o + y * 8 * (D / 16)];
-        load_words(x.v[2 * y], from_v0 + o + y * 8 * G::kRow);
-        load_words(x.v[2 * y + 1], from_v1 + o + y * 8 * G::kRow);
-        x.vs[2 * y] = from_vs[o + y * 8 * (D / 16)];
-        x.vs[2 * y + 1] = from_vs[o + (y * 8 + 1) * (D / 16)];
+        load_words(x.k[y], from_k + o + (r + y * 8) * G::kRow);
+        if constexpr (W == 2) x.ks[y] = *reinterpret_cast<const uint16_t *>(from_ks + o + (r + y * 8) * (D / 16));
+        else x.ks[y] = from_ks[o + (r + y * 8) * (D / 16)];
       }
     };
-    auto work = [&](const Frag<D> &x, int t) {
-      // scores of slots quad (+ 8), rows 8n + 2kq (+ 1)
-      float c[NT][4] = {};
-      {
-        // a NaN among the keys' scales is a hidden slot's, whose scores are dropped
-        const uint32_t s0 = e4m3_pair(x.ks[0]), s1 = e4m3_pair(x.ks[1]);
+    auto fetch_values = [&](Frag<D> &x, int o, int r) {
 #pragma unroll
-        for (int w = 0; w < 2 * W; ++w) {
-          const uint32_t f0 = w < 2 ? twice_lo(s0) : twice_hi(s0), f1 = w < 2 ? twice_lo(s1) : twice_hi(s1);
-          uint32_t k0[4], k1[4];
-          e2m1_pairs(x.k[0][w], k0);
-          e2m1_pairs(x.k[1][w], k1);
+      for (int y = 0; y < 2; ++y) {
+        load_words(x.v[2 * y], from_v0 + o + (r + y * 8) * G::kRow);
+        load_words(x.v[2 * y + 1], from_v1 + o + (r + y * 8) * G::kRow);
+        x.vs[2 * y] = from_vs[o + (r + y * 8) * (D / 16)];
+        x.vs[2 * y + 1] = from_vs[o + (r + y * 8 + 1) * (D / 16)];
+      }
+    };
+    // scores of slots quad (+ 8) of half a unit, rows 8n + 2kq (+ 1)
+    auto scores = [&](const Frag<D> &x, float (&c)[NT][4]) {
+      // a NaN among the keys' scales is a hidden slot's, whose scores are dropped
+      const uint32_t s0 = e4m3_pair(x.ks[0]), s1 = e4m3_pair(x.ks[1]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            k0[y] = mul_f16x2(k0[y], f0);
-            k1[y] = mul_f16x2(k1[y], f1);
+      for (int w = 0; w < 2 * W; ++w) {
+        const uint32_t f0 = w < 2 ? twice_lo(s0) : twice_hi(s0), f1 = w < 2 ? twice_lo(s1) : twice_hi(s1);
+        uint32_t k0[4], k1[4];
+        e2m1_pairs(x.k[0][w], k0);
+        e2m1_pairs(x.k[1][w], k1);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          k0[y] = mul_f16x2(k0[y], f0);
+          k1[y] = mul_f16x2(k1[y], f1);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(c[n], k0[2 * y], k1[2 * y], k0[2 * y + 1], k1[2 * y + 1], q[n][2 * w + y][0], q[n][2 * w + y][1]);
+      }
+    };
+    auto values = [&](const Frag<D> &x, const uint32_t (&hi)[NT][2], const uint32_t (&lo)[NT][2]) {
+      const uint32_t s0 = scales_f16x2(x.vs[0] | x.vs[1] << 8), s1 = scales_f16x2(x.vs[2] | x.vs[3] << 8);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        // nibbles of two slots side by side: even columns, odd columns
+        const uint32_t even0 = (x.v[0][w] & 0x0f0f0f0fu) | (x.v[1][w] << 4 & 0xf0f0f0f0u), odd0 = (x.v[0][w] >> 4 & 0x0f0f0f0fu) | (x.v[1][w] & 0xf0f0f0f0u);
+        const uint32_t even1 = (x.v[2][w] & 0x0f0f0f0fu) | (x.v[3][w] << 4 & 0xf0f0f0f0u), odd1 = (x.v[2][w] >> 4 & 0x0f0f0f0fu) | (x.v[3][w] & 0xf0f0f0f0u);
+        uint32_t a0[4], a1[4], a2[4], a3[4];
+        e2m1_pairs(even0, a0);
+        e2m1_pairs(odd0, a1);
+        e2m1_pairs(even1, a2);
+        e2m1_pairs(odd1, a3);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t b0 = mul_f16x2(a0[y], s0), b1 = mul_f16x2(a1[y], s0), b2 = mul_f16x2(a2[y], s1), b3 = mul_f16x2(a3[y], s1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(o[n][w * 4 + y], b0, b1, b2, b3, hi[n][0], hi[n][1]);
+            if constexpr (kRest) mma_f16(o[n][w * 4 + y], b0, b1, b2, b3, lo[n][0], lo[n][1]);
           }
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(c[n], k0[2 * y], k1[2 * y], k0[2 * y + 1], k1[2 * y + 1], q[n][2 * w + y][0], q[n][2 * w + y][1]);
         }
       }
-      const int j0 = tl.at(t) * kUnit;
-      const bool masked = !(j0 + kUnit - 1 <= p_low && (j0 >= f_high || j0 + kUnit <= a.n_sink));  // some row does not see all of it
-      if (masked) {
+    };
+    auto work = [&](int t, int stage) {
+      const int at = stage * G::kStage;
+      Frag<D> x;
+      float c[2][NT][4] = {};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int half = 0; half < 2; ++half) {
+        fetch_keys(x, at, 16 * half);
+        scores(x, c[half]);
+      }
+      const int j0 = tl.at(t) * kUnit4;
+      if (!(j0 + kUnit4 - 1 <= p_low && (j0 >= f_high || j0 + kUnit4 <= a.n_sink))) {  // some row does not see all of it
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = j0 + quad + 8 * (e >> 1);
-            if (!(j <= p[n][e & 1] && (j >= f[n][e & 1] || j < a.n_sink))) c[n][e] = -INFINITY;
-          }
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = j0 + 16 * half + quad + 8 * (e >> 1);
+              if (!(j <= p[n][e & 1] && (j >= f[n][e & 1] || j < a.n_sink))) c[half][n][e] = -INFINITY;
+            }
       }
       float most = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2)
-          most = max3(most, fmaf(c[n][e], to_log2[n][0], -m[n][0]), fmaf(c[n][e + 1], to_log2[n][1], -m[n][1]));
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            most = max3(most, fmaf(c[half][n][e], to_log2[n][0], -m[n][0]), fmaf(c[half][n][e + 1], to_log2[n][1], -m[n][1]));
       if (__any_sync(0xffffffffu, most > kHead + kMove)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float mx = fmaxf(c[n][y], c[n][y + 2]) * to_log2[n][y];
+            float mx = fmaxf(fmaxf(c[0][n][y], c[0][n][y + 2]), fmaxf(c[1][n][y], c[1][n][y + 2])) * to_log2[n][y];
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
             mx = fmaxf(mx - kHead, m[n][y]);
@@ -299,44 +357,27 @@ struct FewWarp4 {
           }
       }
       // weights: B fragments of the second product
-      uint32_t hi[NT][2], lo[NT][2];
+      uint32_t hi[2][NT][2], lo[2][NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float w0 = exp2_fast(fmaf(c[n][2 * y], to_log2[n][0], -m[n][0])), w1 = exp2_fast(fmaf(c[n][2 * y + 1], to_log2[n][1], -m[n][1]));
-          const uint32_t hv = Pair<__half>::pack(w0, w1);
-          hi[n][y] = transpose8x8(hv);
-          if constexpr (kRest) {
-            const float2 back = Pair<__half>::unpack(hv);
-            lo[n][y] = transpose8x8(Pair<__half>::pack(w0 - back.x, w1 - back.y));
-          }
-          l[n][0] += w0;
-          l[n][1] += w1;
-        }
-      }
-      {
-        const uint32_t s0 = scales_f16x2(x.vs[0] | x.vs[1] << 8), s1 = scales_f16x2(x.vs[2] | x.vs[3] << 8);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          // nibbles of two slots side by side: even columns, odd columns
-          const uint32_t even0 = (x.v[0][w] & 0x0f0f0f0fu) | (x.v[1][w] << 4 & 0xf0f0f0f0u), odd0 = (x.v[0][w] >> 4 & 0x0f0f0f0fu) | (x.v[1][w] & 0xf0f0f0f0u);
-          const uint32_t even1 = (x.v[2][w] & 0x0f0f0f0fu) | (x.v[3][w] << 4 & 0xf0f0f0f0u), odd1 = (x.v[2][w] >> 4 & 0x0f0f0f0fu) | (x.v[3][w] & 0xf0f0f0f0u);
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          e2m1_pairs(even0, a0);
-          e2m1_pairs(odd0, a1);
-          e2m1_pairs(even1, a2);
-          e2m1_pairs(odd1, a3);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t b0 = mul_f16x2(a0[y], s0), b1 = mul_f16x2(a1[y], s0), b2 = mul_f16x2(a2[y], s1), b3 = mul_f16x2(a3[y], s1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_f16(o[n][w * 4 + y], b0, b1, b2, b3, hi[n][0], hi[n][1]);
-              if constexpr (kRest) mma_f16(o[n][w * 4 + y], b0, b1, b2, b3, lo[n][0], lo[n][1]);
+          for (int y = 0; y < 2; ++y) {
+            const float w0 = exp2_fast(fmaf(c[half][n][2 * y], to_log2[n][0], -m[n][0])), w1 = exp2_fast(fmaf(c[half][n][2 * y + 1], to_log2[n][1], -m[n][1]));
+            const uint32_t hv = Pair<__half>::pack(w0, w1);
+            hi[half][n][y] = transpose8x8(hv);
+            if constexpr (kRest) {
+              const float2 back = Pair<__half>::unpack(hv);
+              lo[half][n][y] = transpose8x8(Pair<__half>::pack(w0 - back.x, w1 - back.y));
             }
+            l[n][0] += w0;
+            l[n][1] += w1;
           }
-        }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        fetch_values(x, at, 16 * half);
+        values(x, hi[half], lo[half]);
       }
     };
     // unit i of the warp is tile t0 + warp + i * kFewWarps
@@ -350,14 +391,12 @@ struct FewWarp4 {
     for (; t < t1; t += kFewWarps) {
       cp_async_wait<kAhead - 2>();
       __syncwarp();
-      Frag<D> x;
-      fetch(x, stage);
-      {  // the stage of the unit before, which every lane has fetched, takes the unit kAhead - 1 ahead
+      {  // the stage of the unit before, which every lane is done with, takes the unit kAhead - 1 ahead
         const int ahead = t + (kAhead - 1) * kFewWarps;
         copy(ahead, next, stage == 0 ? kAhead - 1 : stage - 1);
         next = spot_of(ahead + kFewWarps);
       }
-      work(x, t);
+      work(t, stage);
       stage = stage + 1 == kAhead ? 0 : stage + 1;
     }
     cp_async_wait<0>();
@@ -412,7 +451,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
   int64_t units = 0, u = 0, u1 = 1;
   int ctas = 1;
   if (!A.whole) {
-    scan_requests<kFewThreads>(a, start, warp_sum_s, first);
+    scan_requests<kFewThreads, kUnit4>(a, start, warp_sum_s, first);
     units = start[a.n_requests];
     ctas = ctas_used(units, a.n_requests * a.n_kv_heads, A.n_ctas);
     for (int b = g; b < a.n_requests; b += gridDim.x)
@@ -431,7 +470,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
       b = item / a.n_kv_heads;
       h = item - b * a.n_kv_heads;
       rq = request_of(a, b);
-      tl = tiles_of(a, rq);
+      tl = tiles_of<kUnit4>(a, rq);
       t0 = tl.count * rank / A.cluster;
       t1 = tl.count * (rank + 1) / A.cluster;
       u = t0;
@@ -443,7 +482,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
     } else {
       b = request_at(start, a.n_requests, u);
       rq = b < kFewThreads ? first[b] : request_of(a, b);
-      tl = tiles_of(a, rq);
+      tl = tiles_of<kUnit4>(a, rq);
       const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
       h = in / static_cast<uint32_t>(tl.count);
       t0 = in - h * tl.count;
@@ -656,11 +695,11 @@ template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnA
   return launch_pdl(attention_join4<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
 }
 template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
-  // units of a page, and 2^32 over them rounded up (0: one): tile / units is the upper word of tile * magic while
-  // tile * units < 2^32
+  // 16-slot places of a page, and 2^32 over them rounded up (0: one): u / units is the upper word of u * magic while
+  // u * units < 2^32
   const PagedArgs &a = A.c.p;
-  const int64_t units = a.page_size / kUnit, strides = a.slot_stride > A.c.scale_slot_stride ? a.slot_stride : A.c.scale_slot_stride;
-  if (a.page_size % kUnit || units * (a.max_len / kUnit + 1) >= (1ll << 32) || strides >= (1 << 27) || a.page_stride >= (1ll << 32) ||
+  const int64_t units = a.page_size / 16, strides = a.slot_stride > A.c.scale_slot_stride ? a.slot_stride : A.c.scale_slot_stride;
+  if (a.page_size % 16 || units * (a.max_len / 16 + 2) >= (1ll << 32) || strides >= (1 << 27) || a.page_stride >= (1ll << 32) ||
       A.c.scale_page_stride >= (1ll << 32))
     return launch<T, D, NT, false>(A, s);
   A.page_units = static_cast<uint32_t>(units);

@@ -174,19 +174,19 @@ __device__ void empty_rows(const PagedAttnArgs &A, const Request &rq, int rows, 
 constexpr int kUnit = 16;  // slots of a unit
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * kFewWarps;
-// The slots some row of a request sees, as tiles of kUnit: the sinks' tiles, then those from the
+// The slots some row of a request sees, as tiles of UNIT slots: the sinks' tiles, then those from the
 // earliest row's window on.
 struct Tiles {
   int sinks, first, count;  // tiles of sinks, first tile behind them, tiles in all
   __device__ int at(int t) const { return t < sinks ? t : first + t - sinks; }
 };
-__device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq) {
+template <int UNIT = kUnit> __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Request &rq) {
   Tiles t = {0, 0, 0};
   if (rq.rows == 0 || rq.n == 0) return t;
   const int first = window_first(a, max(0, rq.n - rq.rows));
-  t.first = first / kUnit;
-  t.sinks = min((min(a.n_sink, first) + kUnit - 1) / kUnit, t.first);
-  t.count = t.sinks + (rq.n + kUnit - 1) / kUnit - t.first;
+  t.first = first / UNIT;
+  t.sinks = min((min(a.n_sink, first) + UNIT - 1) / UNIT, t.first);
+  t.count = t.sinks + (rq.n + UNIT - 1) / UNIT - t.first;
   return t;
 }
 
@@ -198,7 +198,7 @@ __device__ __forceinline__ int ctas_used(int64_t units, int heads, int most) {
 }
 // start[b] = units of the requests before b; all threads of the block.
 // The first NT requests' sizes are kept in `first`.
-template <int NT>
+template <int NT, int UNIT = kUnit>
 __device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s, Request *first) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t base = 0;
@@ -208,7 +208,7 @@ __device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_
     if (b < a.n_requests) {
       const Request rq = request_of(a, b);
       if (b0 == 0) first[tid] = rq;
-      v = static_cast<int64_t>(tiles_of(a, rq).count) * a.n_kv_heads;
+      v = static_cast<int64_t>(tiles_of<UNIT>(a, rq).count) * a.n_kv_heads;
     }
     int64_t x = v;
 #pragma unroll
