@@ -45,8 +45,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return d;
 }
 // Both halves of a scale pair's low or high half.
-__device__ __forceinline__ uint32_t twice_lo(uint32_t s) { return __byte_perm(s, s, 0x1010); }
-__device__ __forceinline__ uint32_t twice_hi(uint32_t s) { return __byte_perm(s, s, 0x3232); }
+__device__ __forceinline__ uint32_t twice_lo(uint32_t s) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(s));
+  return d;
+}
+__device__ __forceinline__ uint32_t twice_hi(uint32_t s) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(s));
+  return d;
+}
+// p + n * stride in one instruction.
+__device__ __forceinline__ const uint8_t *step(const uint8_t *p, uint32_t stride, uint32_t n) {
+  uint64_t d;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(d) : "r"(stride), "r"(n), "l"(reinterpret_cast<uint64_t>(p)));
+  return reinterpret_cast<const uint8_t *>(d);
+}
 
 // A unit in a warp's ring: codes of its keys and values, 32 slots of D / 2 bytes, then their scales.  Slots 8 .. 15 (and on) lie like
 // 0 .. 7.  The slots a read of values takes at once (0, 2, 4, 6 or 1, 3, 5, 7 of eight) have to be in different banks, and
@@ -164,78 +178,68 @@ struct FewWarp4 {
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
 
     const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
-    // what this lane copies: of the codes 16-byte piece `piece` of slots `slot` + STEP y, of the scales slot `lane`'s
+    // What this lane copies: of its half of a unit (lanes 0 .. 15: the first) the codes' 16-byte piece `piece` of slots
+    // `slot` + STEP y, and the scales of slot `lane`.
     using G = Ring<D>;
-    constexpr int P = D / 32, STEP = 32 / P, Y = kUnit4 / STEP;
-    const int slot = lane / P, piece = lane % P;
+    constexpr int P = D / 32, STEP = 16 / P, Y = 16 / STEP;
+    const int half0 = lane & 16, slot = (lane & 15) / P, piece = lane % P;
     const uint32_t ss = static_cast<uint32_t>(a.slot_stride), zs = static_cast<uint32_t>(c4.scale_slot_stride);  // PAGE16
     const int64_t code0 = h * a.head_stride + piece * 16 + (PAGE16 ? slot * a.slot_stride : 0);
     const int64_t scale0 = h * c4.scale_head_stride + (PAGE16 ? (lane & 15) * c4.scale_slot_stride : 0);
     const uint8_t *K = static_cast<const uint8_t *>(a.k) + code0, *V = static_cast<const uint8_t *>(a.v) + code0;
     const uint8_t *KS = static_cast<const uint8_t *>(c4.k_scale) + scale0, *VS = static_cast<const uint8_t *>(c4.v_scale) + scale0;
-    const uint32_t to_code = smem_u32(ring) + G::at(slot, piece * 16), to_scale = smem_u32(ring) + 2 * G::kSide + lane * (D / 16);
-    // Where tile t lies.  PAGE16: its halves' pages -- the loads alone -- and 16-slot places in those; else the page of its
-    // slot `lane`.
+    uint32_t to_code[Y];
+#pragma unroll
+    for (int y = 0; y < Y; ++y) to_code[y] = smem_u32(ring) + G::at(half0 + slot + STEP * y, piece * 16);
+    const uint32_t to_scale = smem_u32(ring) + 2 * G::kSide + lane * (D / 16);
+    // Where tile t lies: the page -- the load alone -- of this lane's half and that half's 16-slot place in it, or the page of the
+    // tile's slot `lane`.
     struct Spot {
-      int page[PAGE16 ? 2 : 1];
-      uint32_t in[PAGE16 ? 2 : 1];
+      int page;
+      uint32_t in;
     };
     auto spot_of = [&](int t) {
       const int tile = tl.at(max(min(t, t1 - 1), 0));
-      Spot s;
       if constexpr (PAGE16) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t u = min(2 * tile + y, (rq.n - 1) / 16), q = A.units_magic ? __umulhi(u, A.units_magic) : u;
-          s.page[y] = __ldg(table + q);
-          s.in[y] = u - q * A.page_units;
-        }
+        const uint32_t u = min(2 * tile + (half0 >> 4), (rq.n - 1) >> 4), q = A.units_magic ? __umulhi(u, A.units_magic) : u;
+        return Spot{__ldg(table + q), u - q * A.page_units};
       } else {
-        s.page[0] = __ldg(table + min(tile * kUnit4 + lane, rq.n - 1) / a.page_size);
+        return Spot{__ldg(table + min(tile * kUnit4 + lane, rq.n - 1) / a.page_size), 0};
       }
-      return s;
     };
     auto copy = [&](int t, const Spot &spot, int stage) {
       if (t < t1) {
         const uint32_t to = stage * G::kStage;
         const int j0 = tl.at(t) * kUnit4;
         if constexpr (PAGE16) {
-          bool ok[2];
-          uint64_t code[2], scale[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            // the page of a half that no row sees is not looked at
-            const int j = j0 + 16 * y;
-            ok[y] = j < rq.n && (j + 16 > f_low || j < a.n_sink);
-            if (ok[y] && static_cast<unsigned>(spot.page[y]) >= static_cast<unsigned>(a.n_pages)) {
-              atomicOr(&g_error_word, DEVERR_BAD_INDEX);
-              ok[y] = false;
-            }
-            const uint32_t page = ok[y] ? spot.page[y] : 0;
-            // strides are below 2^32 bytes here, of a slot below 2^27
-            code[y] = static_cast<uint64_t>(page) * static_cast<uint32_t>(a.page_stride) + static_cast<uint64_t>(spot.in[y]) * (16 * ss);
-            scale[y] = static_cast<uint64_t>(page) * static_cast<uint32_t>(c4.scale_page_stride) + static_cast<uint64_t>(spot.in[y]) * (16 * zs);
+          // the page of a half that no row sees is not looked at
+          const int j = j0 + half0;
+          bool ok = j < rq.n && (j + 16 > f_low || j < a.n_sink);
+          if (ok && static_cast<unsigned>(spot.page) >= static_cast<unsigned>(a.n_pages)) {
+            atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+            ok = false;
           }
+          const uint32_t page = ok ? spot.page : 0;
+          // strides are below 2^32 bytes here, of a slot below 2^27
+          const uint64_t code = static_cast<uint64_t>(page) * static_cast<uint32_t>(a.page_stride) + static_cast<uint64_t>(spot.in) * (16 * ss);
+          const uint64_t scale = static_cast<uint64_t>(page) * static_cast<uint32_t>(c4.scale_page_stride) + static_cast<uint64_t>(spot.in) * (16 * zs);
+          const uint8_t *k = K + code, *v = V + code;
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
-            const int half = y * STEP / 16;
-            const uint64_t c = code[half] + y * STEP % 16 * ss;
-            cp_async16(to_code + to + y * STEP * G::kRow, K + c, ok[half]);
-            cp_async16(to_code + to + y * STEP * G::kRow + G::kSide, V + c, ok[half]);
+            cp_async16(to_code[y] + to, y ? step(k, STEP * ss, y) : k, ok);
+            cp_async16(to_code[y] + to + G::kSide, y ? step(v, STEP * ss, y) : v, ok);
           }
-          const uint64_t z = lane < 16 ? scale[0] : scale[1];
-          const bool zok = lane < 16 ? ok[0] : ok[1];
-          cp_async_small(to_scale + to, KS + z, D / 16, zok);
-          cp_async_small(to_scale + to + G::kScales, VS + z, D / 16, zok);
+          cp_async_small(to_scale + to, KS + scale, D / 16, ok);
+          cp_async_small(to_scale + to + G::kScales, VS + scale, D / 16, ok);
         } else {
           const int j = j0 + lane;
           Place4 at = {-1, -1};
-          if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, spot.page[0], j);
+          if (j < rq.n && (j < a.n_sink || j >= f_low)) at = place4(c4, spot.page, j);
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
-            const int64_t code = __shfl_sync(0xffffffffu, at.code, slot + STEP * y);
-            cp_async16(to_code + to + y * STEP * G::kRow, K + (code < 0 ? 0 : code), code >= 0);
-            cp_async16(to_code + to + y * STEP * G::kRow + G::kSide, V + (code < 0 ? 0 : code), code >= 0);
+            const int64_t code = __shfl_sync(0xffffffffu, at.code, half0 + slot + STEP * y);
+            cp_async16(to_code[y] + to, K + (code < 0 ? 0 : code), code >= 0);
+            cp_async16(to_code[y] + to + G::kSide, V + (code < 0 ? 0 : code), code >= 0);
           }
           cp_async_small(to_scale + to, KS + (at.code < 0 ? 0 : at.scale), D / 16, at.code >= 0);
           cp_async_small(to_scale + to + G::kScales, VS + (at.code < 0 ? 0 : at.scale), D / 16, at.code >= 0);
