@@ -375,7 +375,7 @@ bd_status bd_paged4_attention(const bd_paged4_kv *kv, const bd_paged_batch *batc
   if (misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit attention: lse misaligned");
   const int group = kv->n_q_heads / kv->n_kv_heads;
   const WideSizes w = wide_sizes(kv, batch->n_requests, batch->max_rows, batch->max_len);
-  if ((static_cast<int64_t>(batch->max_len) / 16 + 8) * kv->n_kv_heads >= (1ll << 31) ||
+  if ((static_cast<int64_t>(batch->max_len) / 16 + 8) * kv->n_kv_heads >= (1ll << 30) ||
       static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30) ||
       (static_cast<int64_t>(batch->max_rows) * group / 256 + 1) * batch->n_requests > (1 << 28) ||
       (!is_few(kv, batch->max_rows) && (w.pages * batch->n_requests > (1 << 30) || 2 * kv->n_kv_heads > 65535)))

@@ -23,11 +23,12 @@ struct Paged4AttnArgs {
   float *part_o;
   float2 *part_ml;
   int n_ctas, whole, cluster;
+  int groups;  // in which a KV head's rows are taken, at most
   uint32_t page_units, units_magic;  // 16-slot places of a page, and what divides by them
 };
 
 // Query rows (of one KV head) of the kernel that reads the codes themselves.
-constexpr int kFewRows4 = 16;
+constexpr int kFewRows4 = 96;
 
 size_t few4_bytes(int head_dim);
 std::string launch_attention_few4(Paged4AttnArgs A, void *workspace, int dtype, cudaStream_t s);

@@ -108,54 +108,61 @@ template <int N> __device__ __forceinline__ void load_words(uint32_t (&w)[N], co
 template <typename T, int D, int NT, bool PAGE16>
 struct FewWarp4 {
   static constexpr int W = D / 64, NK = D / 16, NV = D / 16;
-  static constexpr bool kRest = std::is_same<T, __half>::value;
+  static constexpr bool QS = NT > 1;
+  static constexpr bool kScaled = !std::is_same<T, __half>::value;  // queries are
+  static constexpr bool kRest = !kScaled && NT <= 2;                // the rest of the weights is multiplied, too
   float o[NT][NV][4];
   float m[NT][2], l[NT][2];  // what weights are formed against, the maximum less kHead; their sums
 
-  __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int t0, int t1, uint8_t *ring,
-                                      int warp, int lane) {
+  __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int from, int R, int t0, int t1,
+                                      uint8_t *ring, uint4 (*qs)[NK / 2][32], float *row_log2, int warp, int lane) {
     const Paged4Args &c4 = A.c;
     const PagedArgs &a = c4.p;
     const int quad = lane >> 2, kq = lane & 3;
-    const int R = rq.rows * a.group;
-    // queries: B fragments of row 8n + quad, and the factor of rows 8n + 2kq, + 1 from products to scores in log2 units
-    uint32_t q[NT][NK][2];
+    // Queries: B fragments of row 8n + quad, and the factor of rows 8n + 2kq, + 1 from products to scores in log2 units.
+    // Of up to 8 rows every warp holds them; of more they lie in shared memory, where warp n (and n + 4 ..) puts 8 rows.
+    uint4 q[QS ? 1 : NT][NK / 2];
     float to_log2[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + quad, i = r < R ? r / a.group : 0;
-      const T *src = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + (h * a.group + (r < R ? r - i * a.group : 0)) * D + kq * (D / 4);
-      uint32_t raw[NK][2];
+    for (int n = QS ? warp : 0; n < NT; n += QS ? kFewWarps : 1) {
+      const int r = 8 * n + quad, i = r < R ? (from + r) / a.group : 0;
+      const T *src = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + (h * a.group + (r < R ? from + r - i * a.group : 0)) * D + kq * (D / 4);
+      uint4 raw[NK / 2];
 #pragma unroll
-      for (int t = 0; t < NK; t += 2) {
-        const uint4 x = r < R ? *reinterpret_cast<const uint4 *>(src + t * 4) : make_uint4(0, 0, 0, 0);
-        raw[t][0] = x.x, raw[t][1] = x.y, raw[t + 1][0] = x.z, raw[t + 1][1] = x.w;
-      }
+      for (int t = 0; t < NK / 2; ++t) raw[t] = r < R ? *reinterpret_cast<const uint4 *>(src + t * 8) : make_uint4(0, 0, 0, 0);
       int e = 0;  // the row's power of two
-      if constexpr (!kRest) {
+      if constexpr (kScaled) {
         uint32_t top = 0;
+        auto larger = [&](uint32_t w) { top = max(top, max(w & 0x7fffu, w >> 16 & 0x7fffu)); };
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) top = max(top, max(raw[t][y] & 0x7fffu, raw[t][y] >> 16 & 0x7fffu));
+        for (int t = 0; t < NK / 2; ++t) larger(raw[t].x), larger(raw[t].y), larger(raw[t].z), larger(raw[t].w);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^8 <= largest < 2^9; infinities and NaN stay what they are
         if (top >= 0x0080u && top < 0x7f80u) e = min(126, 127 + 8 - static_cast<int>(top >> 7));
         const float f = pow2(e);
+        auto scaled = [&](uint32_t w) {
+          const float2 x = Pair<T>::unpack(w);
+          return Pair<__half>::pack(x.x * f, x.y * f);
+        };
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
+        for (int t = 0; t < NK / 2; ++t) raw[t] = make_uint4(scaled(raw[t].x), scaled(raw[t].y), scaled(raw[t].z), scaled(raw[t].w));
+      }
+      if constexpr (QS) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float2 x = Pair<T>::unpack(raw[t][y]);
-            q[n][t][y] = Pair<__half>::pack(x.x * f, x.y * f);
-          }
+        for (int t = 0; t < NK / 2; ++t) qs[n][t][lane] = raw[t];
+        if (kq == 0) row_log2[r] = a.scale_log2 * pow2(-e);
       } else {
 #pragma unroll
-        for (int t = 0; t < NK; ++t) q[n][t][0] = raw[t][0], q[n][t][1] = raw[t][1];
-      }
+        for (int t = 0; t < NK / 2; ++t) q[n][t] = raw[t];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) to_log2[n][y] = a.scale_log2 * pow2(-__shfl_sync(0xffffffffu, e, 4 * (2 * kq + y)));
+        for (int y = 0; y < 2; ++y) to_log2[n][y] = a.scale_log2 * pow2(-__shfl_sync(0xffffffffu, e, 4 * (2 * kq + y)));
+      }
+    }
+    if constexpr (QS) {
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) to_log2[n][0] = row_log2[8 * n + 2 * kq], to_log2[n][1] = row_log2[8 * n + 2 * kq + 1];
     }
     // what rows 8n + 2kq, + 1 see: slots <= p, from f on or among the sinks
     int p[NT][2], f[NT][2];
@@ -164,12 +171,14 @@ struct FewWarp4 {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = 8 * n + 2 * kq + y;
-        p[n][y] = r < R ? rq.n - rq.rows + r / a.group : -1;
+        p[n][y] = r < R ? rq.n - rq.rows + (from + r) / a.group : -1;
         f[n][y] = p[n][y] >= 0 ? window_first(a, p[n][y]) : 0;
         m[n][y] = kNone;
         l[n][y] = 0.f;
       }
-    const int p_low = rq.n - rq.rows, f_high = window_first(a, rq.n - 1), f_low = window_first(a, max(0, p_low));
+    // the slots of the first and the last of these rows, where their windows begin, and where the request's first row's does
+    const int p_low = rq.n - rq.rows + from / a.group, p_high = rq.n - rq.rows + (from + R - 1) / a.group;
+    const int f_high = window_first(a, max(0, p_high)), f_low = window_first(a, max(0, rq.n - rq.rows));
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -268,25 +277,33 @@ struct FewWarp4 {
         x.vs[2 * y + 1] = from_vs[o + (r + y * 8 + 1) * (D / 16)];
       }
     };
-    // scores of slots quad (+ 8) of half a unit, rows 8n + 2kq (+ 1)
-    auto scores = [&](const Frag<D> &x, float (&c)[NT][4]) {
+    // scores of slots quad (+ 8) of the halves of the unit, rows 8n + 2kq (+ 1)
+    auto scores = [&](const Frag<D> (&x)[2], float (&c)[2][NT][4]) {
       // a NaN among the keys' scales is a hidden slot's, whose scores are dropped
-      const uint32_t s0 = e4m3_pair(x.ks[0]), s1 = e4m3_pair(x.ks[1]);
+      const uint32_t s[2][2] = {{e4m3_pair(x[0].ks[0]), e4m3_pair(x[0].ks[1])}, {e4m3_pair(x[1].ks[0]), e4m3_pair(x[1].ks[1])}};
 #pragma unroll
       for (int w = 0; w < 2 * W; ++w) {
-        const uint32_t f0 = w < 2 ? twice_lo(s0) : twice_hi(s0), f1 = w < 2 ? twice_lo(s1) : twice_hi(s1);
-        uint32_t k0[4], k1[4];
-        e2m1_pairs(x.k[0][w], k0);
-        e2m1_pairs(x.k[1][w], k1);
+        uint32_t k[2][2][4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          k0[y] = mul_f16x2(k0[y], f0);
-          k1[y] = mul_f16x2(k1[y], f1);
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const uint32_t f = w < 2 ? twice_lo(s[half][z]) : twice_hi(s[half][z]);
+            e2m1_pairs(x[half].k[z][w], k[half][z]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) k[half][z][y] = mul_f16x2(k[half][z][y], f);
+          }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint4 f;
+          if constexpr (QS) f = qs[n][w][lane];
+          else f = q[n][w];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            mma_f16(c[half][n], k[half][0][0], k[half][1][0], k[half][0][1], k[half][1][1], f.x, f.y);
+            mma_f16(c[half][n], k[half][0][2], k[half][1][2], k[half][0][3], k[half][1][3], f.z, f.w);
+          }
         }
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(c[n], k0[2 * y], k1[2 * y], k0[2 * y + 1], k1[2 * y + 1], q[n][2 * w + y][0], q[n][2 * w + y][1]);
       }
     };
     auto values = [&](const Frag<D> &x, const uint32_t (&hi)[NT][2], const uint32_t (&lo)[NT][2]) {
@@ -314,12 +331,12 @@ struct FewWarp4 {
     };
     auto work = [&](int t, int stage) {
       const int at = stage * G::kStage;
-      Frag<D> x;
       float c[2][NT][4] = {};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        fetch_keys(x, at, 16 * half);
-        scores(x, c[half]);
+      {
+        Frag<D> x[2];
+        fetch_keys(x[0], at, 0);
+        fetch_keys(x[1], at, 16);
+        scores(x, c);
       }
       const int j0 = tl.at(t) * kUnit4;
       if (!(j0 + kUnit4 - 1 <= p_low && (j0 >= f_high || j0 + kUnit4 <= a.n_sink))) {  // some row does not see all of it
@@ -380,6 +397,7 @@ struct FewWarp4 {
           }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        Frag<D> x;
         fetch_values(x, at, 16 * half);
         values(x, hi[half], lo[half]);
       }
@@ -434,14 +452,21 @@ template <typename T, int D> __device__ void no_slots(const Paged4AttnArgs &A, c
   empty_rows<T, D>(x, rq, rq.rows, tid, step);
 }
 
-template <int NT> constexpr int few4_per_sm() { return NT == 1 ? 4 : 2; }  // blocks an SM holds at once
+template <int NT> constexpr int few4_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }  // blocks an SM holds at once
+// A warp's ring, in whose place its sums come at the end; all of a block's, and its queries.
+template <int D, int NT> constexpr int few4_region() {
+  return 8 * NT * (D + 4) * 4 > Ring<D>::kWarp ? 8 * NT * (D + 4) * 4 : Ring<D>::kWarp;
+}
+template <int D, int NT> constexpr int few4_smem() { return kFewWarps * few4_region<D, NT>() + (NT > 1 ? NT * D * 16 : 0); }
 
 template <typename T, int D, int NT, bool PAGE16>
 __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4(const __grid_constant__ Paged4AttnArgs A) {
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t sm_raw[];
-  static_assert(ROWS * (D + 4) * 4 <= Ring<D>::kWarp, "a warp's sums take the place of its ring");
-  auto so = [&](int w, int r, int d) { return reinterpret_cast<float *>(sm_raw + w * Ring<D>::kWarp) + r * (D + 4) + d; };
+  constexpr int REGION = few4_region<D, NT>();
+  auto so = [&](int w, int r, int d) { return reinterpret_cast<float *>(sm_raw + w * REGION) + r * (D + 4) + d; };
+  uint4(*qs)[D / 32][32] = reinterpret_cast<uint4(*)[D / 32][32]>(sm_raw + kFewWarps * REGION);
+  __shared__ float row_log2[ROWS];
   __shared__ int64_t start[BD_PAGED_MAX_REQUESTS + 1];
   __shared__ int64_t warp_sum_s[kFewWarps];
   __shared__ Request first[kFewThreads];
@@ -455,7 +480,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
   int64_t units = 0, u = 0, u1 = 1;
   int ctas = 1;
   if (!A.whole) {
-    scan_requests<kFewThreads, kUnit4>(a, start, warp_sum_s, first);
+    scan_requests<kFewThreads, kUnit4, ROWS>(a, start, warp_sum_s, first);
     units = start[a.n_requests];
     ctas = ctas_used(units, a.n_requests * a.n_kv_heads, A.n_ctas);
     for (int b = g; b < a.n_requests; b += gridDim.x)
@@ -466,21 +491,23 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
     u1 = share_begin(units, ctas, g + 1);
   }
   do {
-    int b, h, t0, t1;
+    int b, h, from, t0, t1;  // `from`: the first of these rows among the head's
     Request rq;
     Tiles tl;
-    if (A.whole) {  // one head, or a cluster's block's part of one
+    if (A.whole) {  // one head's rows, or a cluster's block's part of them
       const int item = g / static_cast<uint32_t>(A.cluster), rank = g - item * A.cluster;
-      b = item / a.n_kv_heads;
-      h = item - b * a.n_kv_heads;
+      const int head = item / static_cast<uint32_t>(A.groups);
+      from = (item - head * A.groups) * ROWS;
+      b = head / a.n_kv_heads;
+      h = head - b * a.n_kv_heads;
       rq = request_of(a, b);
       tl = tiles_of<kUnit4>(a, rq);
       t0 = tl.count * rank / A.cluster;
       t1 = tl.count * (rank + 1) / A.cluster;
       u = t0;
       u1 = t1;
-      if (tl.count == 0) {
-        if (h == 0 && rank == 0) no_slots<T, D>(A, rq, tid, kFewThreads);
+      if (tl.count == 0 || from >= rq.rows * a.group) {
+        if (tl.count == 0 && h == 0 && rank == 0 && from == 0) no_slots<T, D>(A, rq, tid, kFewThreads);
         return;
       }
     } else {
@@ -488,14 +515,16 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
       rq = b < kFewThreads ? first[b] : request_of(a, b);
       tl = tiles_of<kUnit4>(a, rq);
       const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
-      h = in / static_cast<uint32_t>(tl.count);
-      t0 = in - h * tl.count;
+      const uint32_t item = in / static_cast<uint32_t>(tl.count), groups = (rq.rows * a.group + ROWS - 1) / ROWS;
+      h = item / groups;
+      from = (item - h * groups) * ROWS;
+      t0 = in - item * tl.count;
       t1 = static_cast<int>(u1 - u < tl.count - t0 ? t0 + (u1 - u) : tl.count);
     }
-    const int R = rq.rows * a.group;
+    const int R = min(ROWS, rq.rows * a.group - from);
     {
       FewWarp4<T, D, NT, PAGE16> w;
-      w.run(A, rq, tl, b, h, t0, t1, sm_raw + warp * Ring<D>::kWarp, warp, lane);
+      w.run(A, rq, tl, b, h, from, R, t0, t1, sm_raw + warp * REGION, qs, row_log2, warp, lane);
       const int quad = lane >> 2, kq = lane & 3;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -510,9 +539,9 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
         }
     }
     const bool whole = t0 == 0 && t1 == tl.count;
-    const int64_t slot = (2 * g + (t0 > 0 ? 0 : 1)) * kFewRows4;
+    const int64_t slot = static_cast<int64_t>(2 * g + (t0 > 0 ? 0 : 1)) * ROWS;
     if (tid == 0 && !A.whole && t0 > 0 && share_begin(units, ctas, g - 1) <= u - t0)  // the first block to begin inside this head
-      A.join[g] = {b, h, 0, R, share_owner(units, ctas, u - t0 + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
+      A.join[g] = {b, h, from, R, share_owner(units, ctas, u - t0 + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
     __syncthreads();
     for (int c = tid; c < R * (D / 4); c += kFewThreads) {  // join the warps
       const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
@@ -538,7 +567,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
         *reinterpret_cast<float4 *>(so(0, r, d)) = o;
         if (d == 0) block_ml[r] = make_float2(M, L);
       } else if (whole) {
-        finish<T>(A, rq, h, r, d, o, M, L);
+        finish<T>(A, rq, h, from + r, d, o, M, L);
       } else {
         *reinterpret_cast<float4 *>(A.part_o + (slot + r) * D + d) = o;
         if (d == 0) A.part_ml[slot + r] = make_float2(M, L);
@@ -571,7 +600,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
             o.w += wi * v[i].w;
           }
         }
-        if (d < D) finish<T>(A, rq, h, r, d, o, M, L);
+        if (d < D) finish<T>(A, rq, h, from + r, d, o, M, L);
       }
       __syncwarp();
       cluster_sync();  // every block's sums are read
@@ -589,7 +618,7 @@ constexpr int kJoinHeld = 10;  // parts of a thread in registers
 constexpr int kJoinRows = 4;
 constexpr int kJoinParts4 = 640;  // parts of a head at most: the blocks of a launch, and one more
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_constant__ Paged4AttnArgs A) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_constant__ Paged4AttnArgs A, int part_rows) {
   __shared__ float weight[kJoinRows][kJoinParts4];
   __shared__ float2 row_ml[kJoinRows];
   __shared__ float4 sums[kJoinThreads];
@@ -600,7 +629,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_con
   const int r0 = blockIdx.y * kJoinRows, n = min(j.n - r0, kJoinRows);
   if (j.np == 0 || n <= 0) return;
   const Request rq = {j.len, j.row0, j.rows};
-  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * kFewRows4 + r0; };
+  auto slot = [&](int i) { return static_cast<int64_t>(2 * (g - 1 + i) + (i == 0 ? 1 : 0)) * part_rows + r0; };
   const int pieces = n * (D / 4);  // at most kJoinThreads
   const int groups = kJoinThreads / pieces, k = tid / pieces, c = tid - k * pieces;
   const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
@@ -653,7 +682,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_con
         o.w += v.w;
       }
   }
-  if (k == 0) finish<T>(A, rq, j.h, r0 + r, d, o, row_ml[r].x, row_ml[r].y);
+  if (k == 0) finish<T>(A, rq, j.h, j.from + r0 + r, d, o, row_ml[r].x, row_ml[r].y);
 }
 static_assert(kJoinRows * 128 / 4 <= kJoinThreads, "a block's pieces");
 
@@ -673,10 +702,11 @@ template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnA
   const PagedArgs &a = A.c.p;
   auto kernel = attention_few4<T, D, NT, PAGE16>;
   A.n_ctas = few4_blocks(few4_per_sm<NT>());
-  static const ClustersAtOnce fit(kernel, kFewThreads, Ring<D>::kSmem);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kSmem);
+  constexpr int SMEM = few4_smem<D, NT>();
+  static const ClustersAtOnce fit(kernel, kFewThreads, SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
+  const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads * A.groups;
   int blocks = 1;
   while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
   const bool alike = seen < a.max_len || a.n_requests == 1;
@@ -691,12 +721,12 @@ template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnA
   if (A.whole) {
     const cudaError_t c = allow_cluster(kernel, blocks);
     if (c != cudaSuccess) return c;
-    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(heads * blocks)), dim3(kFewThreads), Ring<D>::kSmem, s, blocks, A);
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(heads * blocks)), dim3(kFewThreads), SMEM, s, blocks, A);
   }
-  const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), Ring<D>::kSmem, s, A);
+  const cudaError_t f = launch_pdl(kernel, dim3(A.n_ctas), dim3(kFewThreads), SMEM, s, A);
   if (f != cudaSuccess) return f;
-  const int rows = a.max_rows * a.group;
-  return launch_pdl(attention_join4<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A);
+  const int rows = a.max_rows * a.group < 8 * NT ? a.max_rows * a.group : 8 * NT;
+  return launch_pdl(attention_join4<T, D>, dim3(A.n_ctas, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, A, 8 * NT);
 }
 template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
   // 16-slot places of a page, and 2^32 over them rounded up (0: one): u / units is the upper word of u * magic while
@@ -711,23 +741,28 @@ template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaS
   return launch<T, D, NT, true>(A, s);
 }
 template <typename T, int D> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
-  return A.c.p.max_rows * A.c.p.group <= 8 ? launch<T, D, 1>(A, s) : launch<T, D, 2>(A, s);
+  const int rows = A.c.p.max_rows * A.c.p.group;
+  A.groups = rows <= 16 ? 1 : (rows + 31) / 32;
+  return rows <= 8 ? launch<T, D, 1>(A, s) : rows <= 16 ? launch<T, D, 2>(A, s) : launch<T, D, 4>(A, s);
 }
 
 }  // namespace
 
+// Rows of all parts, of the launches that have most.
+static size_t few4_part_rows() {
+  const size_t a = few4_blocks(few4_per_sm<1>()) * 8, b = few4_blocks(few4_per_sm<2>()) * 16, c = few4_blocks(few4_per_sm<4>()) * 32;
+  return 2 * (a > b ? a > c ? a : c : b > c ? b : c);
+}
 size_t few4_bytes(int head_dim) {
-  const size_t parts = 2 * static_cast<size_t>(few4_blocks(few4_per_sm<1>())) * kFewRows4;
-  return align256(few4_blocks(few4_per_sm<1>()) * sizeof(PagedJoin)) + align256(parts * head_dim * 4) + align256(parts * 8);
+  return align256(few4_blocks(few4_per_sm<1>()) * sizeof(PagedJoin)) + align256(few4_part_rows() * head_dim * 4) + align256(few4_part_rows() * 8);
 }
 
 std::string launch_attention_few4(Paged4AttnArgs A, void *workspace, int dtype, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
-  const size_t blocks = few4_blocks(few4_per_sm<1>()), parts = 2 * blocks * kFewRows4;  // the most that a launch has
   A.join = reinterpret_cast<PagedJoin *>(p);
-  p += align256(blocks * sizeof(PagedJoin));
+  p += align256(few4_blocks(few4_per_sm<1>()) * sizeof(PagedJoin));
   A.part_o = reinterpret_cast<float *>(p);
-  p += align256(parts * A.c.p.head_dim * 4);
+  p += align256(few4_part_rows() * A.c.p.head_dim * 4);
   A.part_ml = reinterpret_cast<float2 *>(p);
   cudaError_t e;
   if (dtype == BD_BF16)

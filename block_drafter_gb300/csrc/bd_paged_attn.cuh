@@ -198,7 +198,8 @@ __device__ __forceinline__ int ctas_used(int64_t units, int heads, int most) {
 }
 // start[b] = units of the requests before b; all threads of the block.
 // The first NT requests' sizes are kept in `first`.
-template <int NT, int UNIT = kUnit>
+// ROWS: a KV head's rows are taken so many at a time, each by units of its own; 0: all at once.
+template <int NT, int UNIT = kUnit, int ROWS = 0>
 __device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_sum_s, Request *first) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t base = 0;
@@ -209,6 +210,7 @@ __device__ void scan_requests(const PagedArgs &a, int64_t *start, int64_t *warp_
       const Request rq = request_of(a, b);
       if (b0 == 0) first[tid] = rq;
       v = static_cast<int64_t>(tiles_of<UNIT>(a, rq).count) * a.n_kv_heads;
+      if (ROWS > 0) v *= (rq.rows * a.group + ROWS - 1) / ROWS;
     }
     int64_t x = v;
 #pragma unroll
