@@ -54,30 +54,36 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_rope_kernel(const __gr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int piece = lane % L, sub = lane / L, half = c.rotary_dim / 2;
   const int r0 = blockIdx.x * A.rows_per_cta, n = min(A.rows_per_cta, A.n_rows - r0);
-  const int heads = c.n_q_heads + c.n_kv_heads, units = (heads + H * kHeadsEach - 1) / (H * kHeadsEach);
+  // units of H * kHeadsEach heads, the queries' before the keys'
+  const int q_units = (c.n_q_heads + H * kHeadsEach - 1) / (H * kHeadsEach), units = q_units + (c.n_kv_heads + H * kHeadsEach - 1) / (H * kHeadsEach);
   pdl_wait();
   pdl_trigger();
   uint4 raw[kHeadsEach];
-  auto load = [&](int u) {  // unit u: heads of row u / units
-    const int r = u / units, h0 = (u - r * units) * H * kHeadsEach + sub;
+  struct Unit {
+    int r, h0, heads;  // row; this lane's first head; the side's heads
+    bool q;
+  };
+  auto unit = [&](int u) {
+    Unit x;
+    x.r = u / units;
+    const int i = u - x.r * units;
+    x.q = i < q_units;
+    x.heads = x.q ? c.n_q_heads : c.n_kv_heads;
+    x.h0 = (x.q ? i : i - q_units) * H * kHeadsEach + sub;
+    return x;
+  };
+  auto load = [&](const Unit &x) {
+    const int64_t row = r0 + x.r;
+    const uint16_t *src = (x.q ? A.q + row * A.q_stride : A.k + row * A.k_stride) + x.h0 * D + piece * 8;
 #pragma unroll
     for (int i = 0; i < kHeadsEach; ++i) {
-      const int h = h0 + i * H;
       raw[i] = make_uint4(0, 0, 0, 0);
-      if (r >= n || h >= heads) continue;
-      const int64_t row = r0 + r;
-      const uint16_t *src = h < c.n_q_heads ? A.q + row * A.q_stride + h * D : A.k + row * A.k_stride + (h - c.n_q_heads) * D;
-      raw[i] = *reinterpret_cast<const uint4 *>(src + piece * 8);
+      if (x.r < n && x.h0 + i * H < x.heads) raw[i] = *reinterpret_cast<const uint4 *>(src + i * H * D);
     }
   };
-  load(warp);
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  // this lane's gains, and those of its half-split partners
+  load(unit(warp));
   const bool first = piece * 8 < half, turned = piece * 8 < c.rotary_dim;
   const int partner = !turned ? piece : first ? piece + half / 8 : piece - half / 8;
-  const uint4 *qg = static_cast<const uint4 *>(c.q_gain), *kg = static_cast<const uint4 *>(c.k_gain);
-  const uint4 qg0 = qg ? __ldg(qg + piece) : none, qg1 = qg ? __ldg(qg + partner) : none;
-  const uint4 kg0 = kg ? __ldg(kg + piece) : none, kg1 = kg ? __ldg(kg + partner) : none;
   if (tid < n) pos_s[tid] = A.pos[r0 + tid];
   for (int x = tid; x < n * half; x += kHeadThreads) {
     const int r = x / half, j = x - r * half;
@@ -89,35 +95,38 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_rope_kernel(const __gr
   }
   __syncthreads();
   for (int u = warp; u < n * units; u += kHeadThreads / 32) {
-    if (u != warp) load(u);
-    const int r = u / units, h0 = (u - r * units) * H * kHeadsEach + sub;
-    const int64_t row = r0 + r;
-    const bool skip = pos_s[r] < 0;
-    float co[8], si[8];
-    if (INTERLEAVED) {
+    const Unit x = unit(u);
+    if (u != warp) load(x);
+    // What the unit's heads have in common: y = (x a + x' b) / norm, x' the other value of the pair, with the gains in a and b.
+    float a[8], b[8];
+    {
+      const uint4 *gain = static_cast<const uint4 *>(x.q ? c.q_gain : c.k_gain);
+      float g[8], o[8];
+      unpack8<T>(gain ? __ldg(gain + piece) : make_uint4(0, 0, 0, 0), g);
+      if (!INTERLEAVED) unpack8<T>(gain ? __ldg(gain + partner) : make_uint4(0, 0, 0, 0), o);
+      if (!gain)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = piece * 4 + e;
-        co[e] = turned ? cs[r][0][j] : 1.f;
-        si[e] = turned ? cs[r][1][j] : 0.f;
-      }
-    } else {
-      const int j0 = first ? piece * 8 : piece * 8 - half;
+        for (int e = 0; e < 8; ++e) g[e] = o[e] = 1.f;
+      const int j0 = INTERLEAVED ? piece * 4 : first ? piece * 8 : piece * 8 - half;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        co[e] = turned ? cs[r][0][j0 + e] : 1.f;
-        si[e] = !turned ? 0.f : first ? -cs[r][1][j0 + e] : cs[r][1][j0 + e];
+        const int j = INTERLEAVED ? j0 + e / 2 : j0 + e;
+        const float co = turned ? cs[x.r][0][j] : 1.f, si = turned ? cs[x.r][1][j] : 0.f;
+        a[e] = g[e] * co;
+        b[e] = INTERLEAVED ? (e & 1 ? g[e - 1] * si : -g[e + 1 < 8 ? e + 1 : 7] * si) : first ? -o[e] * si : o[e] * si;
       }
     }
+    const int64_t row = r0 + x.r;
+    uint16_t *dst = (x.q ? A.q_out + row * A.q_out_stride : A.k_out + row * A.k_out_stride) + x.h0 * D + piece * 8;
+    const bool store = pos_s[x.r] >= 0;
 #pragma unroll
     for (int i = 0; i < kHeadsEach; ++i) {
-      const int h = h0 + i * H;
-      float x[8], y[8], g[8];
-      unpack8<T>(raw[i], x);
-      auto mean_square = [&](float f) {  // of x f
+      float v[8], y[8];
+      unpack8<T>(raw[i], v);
+      auto mean_square = [&](float f) {  // of v f
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += x[e] * f * (x[e] * f);
+        for (int e = 0; e < 8; ++e) sum += v[e] * f * (v[e] * f);
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         return sum * (1.f / D);
@@ -128,16 +137,11 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_rope_kernel(const __gr
         const float small = mean_square(0x1p-70f);
         if (mean == INFINITY) inv = rsqrtf(small) * 0x1p-70f;
       }
-      const bool is_q = h < c.n_q_heads, plain = is_q ? qg == nullptr : kg == nullptr;
-      unpack8<T>(is_q ? qg0 : kg0, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= plain ? inv : inv * g[e];
+      for (int e = 0; e < 8; ++e) v[e] *= inv;
       if (INTERLEAVED) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = x[2 * e] * co[e] - x[2 * e + 1] * si[e];
-          y[2 * e + 1] = x[2 * e] * si[e] + x[2 * e + 1] * co[e];
-        }
+        for (int e = 0; e < 8; ++e) y[e] = v[e] * a[e] + v[e ^ 1] * b[e];
       } else {
         uint4 other;
         const int from = sub * L + partner;
@@ -146,15 +150,12 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_rope_kernel(const __gr
         other.z = __shfl_sync(0xffffffffu, raw[i].z, from);
         other.w = __shfl_sync(0xffffffffu, raw[i].w, from);
         unpack8<T>(other, y);
-        unpack8<T>(is_q ? qg1 : kg1, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e] * co[e] + y[e] * (plain ? inv : inv * g[e]) * si[e];
+        for (int e = 0; e < 8; ++e) y[e] = v[e] * a[e] + y[e] * inv * b[e];
       }
-      if (h < heads && !skip) {
-        uint16_t *dst = is_q ? A.q_out + row * A.q_out_stride + h * D : A.k_out + row * A.k_out_stride + (h - c.n_q_heads) * D;
-        *reinterpret_cast<uint4 *>(dst + piece * 8) =
+      if (store && x.h0 + i * H < x.heads)
+        *reinterpret_cast<uint4 *>(dst + i * H * D) =
             make_uint4(Pair<T>::pack(y[0], y[1]), Pair<T>::pack(y[2], y[3]), Pair<T>::pack(y[4], y[5]), Pair<T>::pack(y[6], y[7]));
-      }
     }
   }
 }

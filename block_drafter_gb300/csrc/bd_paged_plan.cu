@@ -4,11 +4,11 @@
 // pages promised, and whether a request's promise is within the stack.  Page x that a request takes is the
 // stack's entry (top - 1 - its place among the promises); where that entry is one that was given
 // back in this call, the same sums say whose it was, so that no thread waits for another's store.  So every
-// block works the sums out for itself (1024 requests are two loads and four scans) and takes an equal part of the
-// rows and of the moved pages, which it finds by binary search in shared memory.  The held counts and the stack's
-// count may be written in place: the blocks are one cluster, and write behind its barrier what others read.
-// Bound by its latency: the launch, one round trip for the counts, the scans, one more for tables and stack (a step
-// of 8 requests 16 rows each; 512 requests, 66 000 rows, 3200 pages).
+// block works the sums out for itself (1024 requests are two loads and two scans) and takes an equal part of the
+// rows and of the moved pages, which it finds by binary search in shared memory; of its threads some write the requests'
+// places and move pages, the others the rows.  Nothing that the rows' and pages' threads read is written in the launch.
+// Bound by its latency: the launch, one round trip for the counts, the scans, one more for tables and stack (8 requests of 16
+// rows 3.8 us).
 #include "bd_checks.h"
 #include "bd_paged_device.cuh"
 
@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanEach = BD_PAGED_MAX_REQUESTS / kPlanThreads;  // requests of a thread
-constexpr int kPlanCluster = 8;
+constexpr int kPlanMovers = 128;  // threads that write the requests' places and move pages, beside the others' rows
 
 struct PlanArgs {
   bd_paged_pages p;
@@ -29,6 +29,7 @@ struct PlanArgs {
   int32_t *seq_len, *row_start, *row_request, *row_pos;
   int64_t *slot_map;
   int32_t *n_short;
+  int counts, rest;  // whether held_out and free_count_out are written, and all else
 };
 
 // Sum of the threads before this one, and of all (two uses need a barrier between them).
@@ -75,7 +76,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   __shared__ int short_s, taken_s;
   const bd_paged_pages &p = A.p;
   const int tid = threadIdx.x, B = p.n_requests, ps = p.page_size;
-  const int at = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
   if (tid == 0) short_s = taken_s = 0;
   pdl_wait();
   pdl_trigger();
@@ -146,16 +146,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     pages[1] = takes_end;
   }
   __syncthreads();
-  // whatever a block writes in place the others have read
-  if (gridDim.x > 1) cluster_sync();
-
-  for (int b = at; b < B; b += step) {
-    const bool served = keep_s[b] >= 0;
-    const int fresh_b = rows_before[b + 1] - rows_before[b], h = held_s[b], n = need_s[b];
-    A.seq_len[b] = served ? keep_s[b] + fresh_b : 0;
-    A.row_start[b] = rows_before[b];
-    p.held_out[b] = !served ? h : n > h || A.give_back ? n : h;
-  }
   // page x of the promises, from 0 on: the stack from its top down
   auto page_at = [&](int x) {
     const int i = static_cast<int>(top) - 1 - x;
@@ -163,19 +153,35 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     const int b = owner(gives_before, B, i - free);
     return p.page_table[static_cast<int64_t>(b) * p.table_width + need_s[b] + i - free - gives_before[b]];
   };
-  if (at == 0) {
-    A.row_start[B] = rows_before[B];
-    *p.free_count_out = static_cast<int>(top) - taken_s;
-    if (A.n_short) *A.n_short = short_s;
+  if (tid < kPlanMovers) {
+    const int at = blockIdx.x * kPlanMovers + tid, step = gridDim.x * kPlanMovers;
+    for (int b = at; b < B; b += step) {
+      const bool served = keep_s[b] >= 0;
+      const int fresh_b = rows_before[b + 1] - rows_before[b], h = held_s[b], n = need_s[b];
+      if (A.rest) {
+        A.seq_len[b] = served ? keep_s[b] + fresh_b : 0;
+        A.row_start[b] = rows_before[b];
+      }
+      if (A.counts) p.held_out[b] = !served ? h : n > h || A.give_back ? n : h;
+    }
+    if (at == 0) {
+      if (A.counts) *p.free_count_out = static_cast<int>(top) - taken_s;
+      A.row_start[B] = rows_before[B];
+      if (A.n_short) *A.n_short = short_s;
+    }
+    if (!A.rest) return;
+    for (int g = at; g < gives_before[B]; g += step) {
+      const int b = owner(gives_before, B, g);
+      p.free_pages[free + g] = p.page_table[static_cast<int64_t>(b) * p.table_width + need_s[b] + g - gives_before[b]];
+    }
+    for (int t = at; t < takes_before[B]; t += step) {
+      const int b = owner(takes_before, B, t);
+      if (keep_s[b] >= 0) p.page_table[static_cast<int64_t>(b) * p.table_width + held_s[b] + t - takes_before[b]] = page_at(t);
+    }
+    return;
   }
-  for (int g = at; g < gives_before[B]; g += step) {
-    const int b = owner(gives_before, B, g);
-    p.free_pages[free + g] = p.page_table[static_cast<int64_t>(b) * p.table_width + need_s[b] + g - gives_before[b]];
-  }
-  for (int t = at; t < takes_before[B]; t += step) {
-    const int b = owner(takes_before, B, t);
-    if (keep_s[b] >= 0) p.page_table[static_cast<int64_t>(b) * p.table_width + held_s[b] + t - takes_before[b]] = page_at(t);
-  }
+  if (!A.rest) return;
+  const int at = blockIdx.x * (kPlanThreads - kPlanMovers) + tid - kPlanMovers, step = gridDim.x * (kPlanThreads - kPlanMovers);
   for (int r = at; r < A.n_rows; r += step) {
     int b = -1, pos = -1;
     int64_t slot = -1;
@@ -194,11 +200,21 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   }
 }
 
-// Blocks: one while its threads have at most four rows each.
-std::string launch_plan(const PlanArgs &A, cudaStream_t s) {
-  int blocks = 1;
-  while (blocks < kPlanCluster && A.n_rows > 4 * blocks * kPlanThreads) blocks *= 2;
-  const cudaError_t e = launch_pdl_cluster(paged_plan_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, blocks, A);
+// A thread a row, up to two blocks an SM.  Several blocks do not write what others of them read: held counts and the stack's
+// count in place are a second launch's, which works the sums out again (512 requests, 66 000 rows: 2 us of it).
+std::string launch_plan(PlanArgs A, cudaStream_t s) {
+  constexpr int kRows = kPlanThreads - kPlanMovers;
+  int blocks = A.n_rows <= kRows ? 1 : (A.n_rows + kRows - 1) / kRows;
+  if (blocks > 2 * num_sms()) blocks = 2 * num_sms();
+  const bool in_place = A.p.held_out == A.p.held || A.p.free_count_out == A.p.free_count, twice = blocks > 1 && in_place;
+  A.counts = !twice;
+  A.rest = 1;
+  cudaError_t e = launch_pdl(paged_plan_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, A);
+  if (e == cudaSuccess && twice) {
+    A.counts = 1;
+    A.rest = 0;
+    e = launch_pdl(paged_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, A);
+  }
   return e == cudaSuccess ? std::string() : std::string("paged plan: ") + cudaGetErrorString(e);
 }
 
@@ -238,7 +254,7 @@ extern "C" bd_status bd_paged_plan(const bd_paged_pages *pages, const int32_t *l
         return refuse(BD_ERR_INVALID_ARG, std::string("paged plan: ") + x.name + " and " + y.name + " overlap");
     }
   }
-  PlanArgs A = {p, len, n_new, give_back != 0, n_rows, seq_len, row_start, row_request, row_pos, slot_map, n_short};
+  PlanArgs A = {p, len, n_new, give_back != 0, n_rows, seq_len, row_start, row_request, row_pos, slot_map, n_short, 1, 1};
   use_target_kernels();
   return ran(launch_plan(A, static_cast<cudaStream_t>(stream)));
 }
