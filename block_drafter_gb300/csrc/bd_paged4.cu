@@ -10,16 +10,18 @@ namespace bd {
 BD_DEFINE_ERROR_TAKER(take_error_word_paged4)
 
 // ------------------------------------------------------------------ append
-// A thread takes groups of 16 values (32 bytes in, 9 out), kAppend4Each of them on their way while the block finds
-// its rows' requests and slots.  The codes are exact with one reciprocal for the 16: y = x (1/s) is off by 2^-23 and is put right by
-// its remainder, y + (x - y s) (1/s).  A border between two codes is a middle g (3 bits) times s (4 bits): where x is one, the
-// remainder is exact and y becomes g itself, the tie; a value of at most 11 bits that is none is off it by more than
-// 2^-12.  Bound by the bytes and, nearly, by instructions (about 12 a value).
+// A thread takes groups of 16 values (32 bytes in, 9 out), the first on its way while the block finds its rows' requests and
+// slots.  Eight blocks an SM: 23 700 rows of 8 heads x 2 x 128 take 37.5 us (5.9 TB/s), two groups a thread at once with fewer
+// blocks 39.5, halves of groups, whose loads and stores are dense but which work out every scale twice, 59.
+// The codes are exact without divisions.  A value's quotient by the scale is formed as x (1/s), off by about 2^-22, and
+// rounded to fp16's 11 bits before it is rounded to a code: a border between two codes is a middle g (3 bits) times s (4 bits);
+// a value of at most 11 bits that is not g s is off it by more than 2^-12, further than the errors, and one that is becomes
+// g itself, the tie.  The scale's, max / 6, is put right by its remainder, which is 0 on a border between two scales.
+// Bound by the bytes and by instructions, about 15 a value, about as much.
 namespace {
 
 constexpr int kAppend4Threads = 256;
 constexpr int kAppend4Rows = 32;
-constexpr int kAppend4Each = 2;
 
 struct Paged4AppendArgs {
   Paged4Args c;
@@ -30,147 +32,149 @@ struct Paged4AppendArgs {
 };
 
 __device__ __forceinline__ float e4m3_value(uint32_t byte) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(byte)));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(d)));
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3_pair(byte))));
 }
 
 struct Group4 {
   uint32_t codes[2], scale;
 };
-// 16 values (two a word) to their codes and scale; up, down: 2^exp, 2^-exp.
-template <typename T> __device__ __forceinline__ Group4 encode16(const uint32_t (&w)[8], float up, float down, bool &bad) {
+// 16 values (two a word) to their codes and scale; down: 2^-exp.
+template <typename T> __device__ __forceinline__ Group4 encode16(const uint32_t (&w)[8], float down, bool &bad) {
   constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
   uint32_t tops = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) tops = __vmaxu2(tops, w[i] & 0x7fff7fffu);
   const uint32_t top = max(tops & 0xffffu, tops >> 16);
   const float most = Pair<T>::unpack(top).x * down;
-  Group4 g = {{0, 0}, 0};
-  if (top >= kInf) {
-    bad = true;
-    return g;
-  }
-  bad |= most > 2688.f;
-  g.scale = e4m3x2(__fdiv_rn(most, 6.f), 0.f) & 0xffu;
+  bad = !(most <= 2688.f) || top >= kInf;
+  float sixth = most * (1.f / 6.f);
+  sixth = fmaf(fmaf(-sixth, 6.f, most), 1.f / 6.f, sixth);
+  Group4 g = {{0, 0}, most <= 2688.f ? e4m3x2(sixth, 0.f) & 0xffu : 0x7eu};
   const float s = e4m3_value(g.scale);
-  if (s == 0.f) {
-    g.scale = 0;
-    return g;
-  }
-  const float f = __frcp_rn(s) * down, back = s * up;
+  if (s == 0.f || top >= kInf) return {{0, 0}, 0};
+  float f;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
+  f *= down;
   float y[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 x = Pair<T>::unpack(w[i]);
-    const float a = x.x * f, b = x.y * f;
-    y[2 * i] = copysignf(fmaf(fmaf(-a, back, x.x), f, a), x.x);  // of -0, too
-    y[2 * i + 1] = copysignf(fmaf(fmaf(-b, back, x.y), f, b), x.y);
+    const float2 z = Pair<__half>::unpack(Pair<__half>::pack(x.x * f, x.y * f));
+    y[2 * i] = z.x;
+    y[2 * i + 1] = z.y;
   }
   g.codes[0] = e2m1_codes8(y);
   g.codes[1] = e2m1_codes8(y + 8);
   return g;
 }
 
-// The values that a group stands for, in T (exact: 2 bits times 4).
-template <typename T> __device__ __forceinline__ void decode16(const Group4 &g, float up, uint32_t (&w)[8]) {
-  // code times scale is a multiple of 2^-10 up to 2688: fp16 holds it
-  const uint32_t s = __byte_perm(e4m3_pair(g.scale), 0, 0x1010);
+// The values that 8 codes and a scale stand for, in T (exact: code times scale is a multiple of 2^-10 up to 2688, which fp16
+// holds).
+template <typename T> __device__ __forceinline__ uint4 decode8(uint32_t codes, uint32_t scale, float up) {
+  const uint32_t s = __byte_perm(e4m3_pair(scale), 0, 0x1010);
+  uint32_t p[4], w[4];
+  e2m1_pairs(codes, p);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t p[4];
-    e2m1_pairs(g.codes[i], p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 x = Pair<__half>::unpack(mul_f16x2(p[j], s));
-      w[i * 4 + j] = Pair<T>::pack(x.x * up, x.y * up);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = Pair<__half>::unpack(mul_f16x2(p[j], s));
+    w[j] = Pair<T>::pack(x.x * up, x.y * up);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kAppend4Threads) paged4_append_kernel(const __grid_constant__ Paged4AppendArgs A) {
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppend4Threads, 8) paged4_append_kernel(const __grid_constant__ Paged4AppendArgs A) {
+  constexpr uint32_t G = D / 16;  // groups of a head
   const PagedArgs &a = A.c.p;
   __shared__ Place4 place[kAppend4Rows];  // of the row's slot, code -1: not stored
   __shared__ int2 slot[kAppend4Rows];     // the row's request and slot (negative: none)
-  const int r0 = blockIdx.x * A.rows_per_cta, r1 = min(a.n_rows, r0 + A.rows_per_cta);
-  const uint32_t per_head = a.head_dim / 16, per_side = a.n_kv_heads * per_head, per_row = 2 * per_side;
-  const int groups = (r1 - r0) * per_row;
+  const int r0 = blockIdx.x * A.rows_per_cta, n = min(A.rows_per_cta, a.n_rows - r0);
+  const uint32_t per_side = a.n_kv_heads * G, per_row = 2 * per_side;
   if (threadIdx.x < kAppend4Rows) slot[threadIdx.x] = make_int2(0, -1);
   pdl_wait();
   pdl_trigger();
-  uint4 v[kAppend4Each][2];
-  auto load = [&](int c0) {
-#pragma unroll
-    for (int u = 0; u < kAppend4Each; ++u) {
-      const uint32_t c = c0 + u * kAppend4Threads, r = c / per_row, x = c - r * per_row;
-      if (static_cast<int>(c) >= groups) continue;
-      const uint4 *src = reinterpret_cast<const uint4 *>(x < per_side ? A.k_new + (r0 + r) * A.k_stride + x * 16
-                                                                      : A.v_new + (r0 + r) * A.v_stride + (x - per_side) * 16);
-      v[u][0] = __ldcs(src);
-      v[u][1] = __ldcs(src + 1);
+  // Group x of row r, and how a thread gets from one of its groups to the next.
+  struct At {
+    uint32_t r, x;
+  };
+  const uint32_t step_r = kAppend4Threads / per_row, step_x = kAppend4Threads - step_r * per_row;
+  auto step = [&](At &t) {
+    t.r += step_r;
+    t.x += step_x;
+    if (t.x >= per_row) {
+      t.x -= per_row;
+      ++t.r;
     }
   };
-  load(threadIdx.x);
+  uint4 v[2];
+  auto load = [&](At t) {
+    if (static_cast<int>(t.r) >= n) return;
+    const int64_t row = r0 + t.r;
+    const uint4 *src = reinterpret_cast<const uint4 *>(t.x < per_side ? A.k_new + row * A.k_stride + t.x * 16
+                                                                      : A.v_new + row * A.v_stride + (t.x - per_side) * 16);
+    v[0] = __ldcs(src);
+    v[1] = __ldcs(src + 1);
+  };
+  At at;
+  at.r = threadIdx.x / per_row;
+  at.x = threadIdx.x - at.r * per_row;
+  load(at);
   __syncthreads();
   for (int b = threadIdx.x; b < a.n_requests; b += kAppend4Threads) {
-    const int s = a.row_start[b], e = a.row_start[b + 1], n = request_len(a, b);
+    const int s = a.row_start[b], e = a.row_start[b + 1], len = request_len(a, b);
     if (s < 0 || e < s || e > a.n_rows || e - s > a.max_rows) {
       atomicOr(&g_error_word, DEVERR_BAD_INDEX);
       continue;
     }
-    for (int r = max(s, r0); r < min(e, r1); ++r) slot[r - r0] = make_int2(b, n - (e - r));
+    for (int r = max(s, r0); r < min(e, r0 + n); ++r) slot[r - r0] = make_int2(b, len - (e - r));
   }
   __syncthreads();
   if (threadIdx.x < kAppend4Rows) {
     const int2 p = slot[threadIdx.x];
-    Place4 at = {-1, -1};
-    if (p.y >= 0) at = place4(A.c, __ldg(a.page_table + static_cast<int64_t>(p.x) * a.table_width + p.y / a.page_size), p.y);
-    place[threadIdx.x] = at;
+    Place4 to = {-1, -1};
+    if (p.y >= 0) to = place4(A.c, __ldg(a.page_table + static_cast<int64_t>(p.x) * a.table_width + p.y / a.page_size), p.y);
+    place[threadIdx.x] = to;
   }
   __syncthreads();
-  const float k_down = pow2(-A.c.k_exp), v_down = pow2(-A.c.v_exp), k_up = pow2(A.c.k_exp), v_up = pow2(A.c.v_exp);
-  for (int c0 = threadIdx.x; c0 < groups; c0 += kAppend4Each * kAppend4Threads) {
-    if (c0 != static_cast<int>(threadIdx.x)) load(c0);
-#pragma unroll
-    for (int u = 0; u < kAppend4Each; ++u) {
-      const uint32_t c = c0 + u * kAppend4Threads, r = c / per_row, x = c - r * per_row;
-      if (static_cast<int>(c) >= groups) continue;
-      const Place4 to = place[r];
-      if (to.code < 0) continue;
-      const bool key = x < per_side;
-      const uint32_t w = key ? x : x - per_side, h = w / per_head, i = w - h * per_head;
-      const uint32_t in[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
-      bool bad = false;
-      const Group4 g = encode16<T>(in, key ? k_up : v_up, key ? k_down : v_down, bad);
-      if (bad) atomicOr(&g_error_word, DEVERR_4BIT);
-      uint8_t *codes = static_cast<uint8_t *>(const_cast<void *>(key ? a.k : a.v));
-      uint8_t *scales = static_cast<uint8_t *>(const_cast<void *>(key ? A.c.k_scale : A.c.v_scale));
-      *reinterpret_cast<uint2 *>(codes + to.code + h * a.head_stride + i * 8) = make_uint2(g.codes[0], g.codes[1]);
-      scales[to.scale + h * A.c.scale_head_stride + i] = static_cast<uint8_t>(g.scale);
-      uint16_t *held = key ? A.k_held : A.v_held;
-      if (held) {
-        uint32_t o[8];
-        decode16<T>(g, key ? k_up : v_up, o);
-        uint4 *dst = reinterpret_cast<uint4 *>(held + (static_cast<int64_t>(r0 + r) * per_side + w) * 16);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+  bool all_fine = true;
+  for (bool first = true; static_cast<int>(at.r) < n; first = false, step(at)) {
+    if (!first) load(at);
+    const Place4 to = place[at.r];
+    if (to.code < 0) continue;
+    const bool key = at.x < per_side;
+    const uint32_t w = key ? at.x : at.x - per_side, h = w / G, i = w % G;
+    const uint32_t in[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    bool bad;
+    const Group4 g = encode16<T>(in, pow2(key ? -A.c.k_exp : -A.c.v_exp), bad);
+    all_fine = all_fine && !bad;
+    uint8_t *codes = static_cast<uint8_t *>(const_cast<void *>(key ? a.k : a.v));
+    uint8_t *scales = static_cast<uint8_t *>(const_cast<void *>(key ? A.c.k_scale : A.c.v_scale));
+    *reinterpret_cast<uint2 *>(codes + to.code + h * a.head_stride + i * 8) = make_uint2(g.codes[0], g.codes[1]);
+    scales[to.scale + h * A.c.scale_head_stride + i] = static_cast<uint8_t>(g.scale);
+    uint16_t *held = key ? A.k_held : A.v_held;
+    if (held) {
+      const float up = pow2(key ? A.c.k_exp : A.c.v_exp);
+      uint4 *dst = reinterpret_cast<uint4 *>(held + (static_cast<int64_t>(r0 + at.r) * per_side + w) * 16);
+      dst[0] = decode8<T>(g.codes[0], g.scale, up);
+      dst[1] = decode8<T>(g.codes[1], g.scale, up);
     }
   }
+  if (!all_fine) atomicOr(&g_error_word, DEVERR_4BIT);
 }
 
 std::string launch_append4(Paged4AppendArgs &A, int dtype, cudaStream_t s) {
-  // as many rows as its threads take in two turns, while two blocks an SM are left (23 700 rows of 8 heads: in one turn 43.4 us, two
-  // 42.5 us, four 45.6 us)
+  // as many rows as its threads take in two turns, while two blocks an SM are left (23 700 rows of 8 heads: in two turns 37.5 us,
+  // in four 39.1 us, in eight 45.7 us)
   const int groups = 2 * A.c.p.n_kv_heads * A.c.p.head_dim / 16;
   A.rows_per_cta = 1;
-  while (2 * A.rows_per_cta <= kAppend4Rows && 2 * A.rows_per_cta * groups <= 2 * kAppend4Each * kAppend4Threads &&
+  while (2 * A.rows_per_cta <= kAppend4Rows && 2 * A.rows_per_cta * groups <= 2 * kAppend4Threads &&
          A.c.p.n_rows >= 4 * A.rows_per_cta * num_sms())
     A.rows_per_cta *= 2;
   const int grid = (A.c.p.n_rows + A.rows_per_cta - 1) / A.rows_per_cta;
-  const cudaError_t e = launch_pdl(dtype == BD_BF16 ? paged4_append_kernel<__nv_bfloat16> : paged4_append_kernel<__half>, dim3(grid),
-                                   dim3(kAppend4Threads), 0, s, A);
+  const bool wide = A.c.p.head_dim == 128;
+  const auto kernel = dtype == BD_BF16 ? (wide ? paged4_append_kernel<__nv_bfloat16, 128> : paged4_append_kernel<__nv_bfloat16, 64>)
+                                       : (wide ? paged4_append_kernel<__half, 128> : paged4_append_kernel<__half, 64>);
+  const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kAppend4Threads), 0, s, A);
   return e == cudaSuccess ? std::string() : std::string("paged 4-bit append: ") + cudaGetErrorString(e);
 }
 
@@ -208,23 +212,17 @@ template <typename T, int D> __global__ void __launch_bounds__(kWideThreads) pag
     const int x = u * kWideThreads + threadIdx.x, r = x / P, i = x - r * P, j = j0 + r;
     Place4 at = {-1, -1};  // slots that no row sees are zeros: no value of a tile is not finite
     if (j < rq.n && any_seen(a, j, 1, f_low, rq.n - 1)) at = place4(A.c, __ldg(table + j / a.page_size), j);
-    Group4 g[2] = {};
+    uint4 w = make_uint4(0, 0, 0, 0);
+    uint32_t z = 0;
     if (at.code >= 0) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(codes + at.code) + i);
-      const uint32_t s = __ldg(reinterpret_cast<const uint16_t *>(scales + at.scale) + i);
-      // the code of a NaN reads as 448
-      auto finite = [](uint32_t s) { return (s & 0x7f) == 0x7f ? 0x7eu : s; };
-      g[0] = {{w.x, w.y}, finite(s & 0xff)};
-      g[1] = {{w.z, w.w}, finite(s >> 8)};
+      w = __ldg(reinterpret_cast<const uint4 *>(codes + at.code) + i);
+      z = __ldg(reinterpret_cast<const uint16_t *>(scales + at.scale) + i);
     }
     uint4 *to = reinterpret_cast<uint4 *>(dst + r * D + i * 32);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t o[8];
-      decode16<T>(g[e], up, o);
-      to[2 * e] = make_uint4(o[0], o[1], o[2], o[3]);
-      to[2 * e + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
+    to[0] = decode8<T>(w.x, z & 0xff, up);
+    to[1] = decode8<T>(w.y, z & 0xff, up);
+    to[2] = decode8<T>(w.z, z >> 8, up);
+    to[3] = decode8<T>(w.w, z >> 8, up);
   }
 }
 
