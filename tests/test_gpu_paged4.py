@@ -1,5 +1,7 @@
 """The 4-bit paged cache on the GPU against the 64-bit oracle: append, attention, and steps of them.  Every byte
 that no request holds is 0xff in the pools."""
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -322,3 +324,109 @@ def test_a_serving_step(rows, graph):
     used = {p for b in range(Bn) for p in table[b, :held[b]].tolist()}
     free = stack[:count.item()].tolist()
     assert sorted(free + list(used)) == list(range(total))      # no page lost, none twice
+
+
+# ------------------------------------------------------------------ drawn cases, shared workspaces, graphs, far offsets
+def _drawn(seed):
+    r = random.Random(seed)
+    group = r.choice([1, 2, 3, 4, 5, 7, 8, 16, 32, 48, 96, 128])
+    most = max(1, r.choice([8, 16, 96, 200]) // group)
+    n = r.randint(1, 9)
+    lens = [r.choice([0, 1, r.randint(1, 40), r.randint(1, 700), r.randint(600, 2500)]) for _ in range(n)]
+    return Paged4Case(tuple(lens), tuple(r.randint(0, most) for _ in range(n - 1)) + (most,), hkv=r.choice([1, 1, 2, 3]), group=group, d=r.choice([64, 128]),
+                      page=r.choice([1, 5, 16, 16, 32, 33, 48, 64, 128, 256, 1000]), dtype=r.choice(["bf16", "fp16"]), window=r.choice([0, 0, 1, 30, 129, 700]),
+                      n_sink=r.choice([0, 1, 4, 20, 300]), nhd=r.random() < 0.4, pad=r.choice([0, 0, 1]), lead=r.choice([0, 3]),
+                      std=r.choice([0.3, 1.0, 4.0]), spare=r.choice([0, 2]), seed=seed)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_attention_of_drawn_cases(seed):
+    c = _drawn(seed).build()
+    c.batch.workspace.fill_(255)
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    c.check_guards(out, lse)
+
+
+def test_batches_may_share_a_workspace_and_come_on_any_stream():
+    cases = [Paged4Case((900, 70, 300), (r, 1, r), seed=r).build() for r in (1, 4, 13, 40)]
+    ws = torch.full((max(c.batch.ws_bytes for c in cases),), 255, dtype=torch.uint8, device="cuda")
+    batches = [c.cache.batch(c.table, c.lend, c.startd, c.n_rows, c.max_rows, c.max_len, workspace=ws) for c in cases]
+    wants = [c.attend() for c in cases]
+    side, outs = torch.cuda.Stream(), []
+    for round_ in range(2):
+        for c, b in zip(cases, batches):     # one after the other on one stream
+            out, lse = c.outputs()
+            c.cache.attention(b, c.qd, out, lse=lse, scale=c.scale)
+            outs.append((out, lse))
+    torch.cuda.synchronize()
+    for c in cases:                          # with its own workspace, on another stream
+        out, lse = c.outputs()
+        side.wait_stream(torch.cuda.current_stream())
+        c.cache.attention(c.batch, c.qd, out, lse=lse, scale=c.scale, stream=side)
+        outs.append((out, lse))
+    torch.cuda.synchronize()
+    sync()
+    for (out, lse), (ref, rl) in zip(outs, wants * 3):
+        assert torch.equal(out, ref) and torch.equal(lse, rl)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 20, 40])
+def test_a_captured_call_serves_other_lengths(rows):
+    c = Paged4Case((1500, 1500, 1500), (rows,) * 3).build()
+    out, lse = c.outputs()
+    c.cache.attention(c.batch, c.qd, out, lse=lse, scale=c.scale)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.cache.attention(c.batch, c.qd, out, lse=lse, scale=c.scale)
+    k, v = c.k, c.v
+    for lens in ((1500, 1500, 1500), (0, 1, 1499), (rows, 16, 17), (0, 0, 0), (700, 2, 1500)):
+        c.lend.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.lens, c.k, c.v = lens, [x[:n] for x, n in zip(k, lens)], [x[:n] for x, n in zip(v, lens)]
+        graph.replay()
+        sync()
+        c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40])
+@pytest.mark.parametrize("page_stride", [2 ** 31 - 2 ** 20, 2 ** 32 + 4096])
+def test_offsets_beyond_32_bits(page_stride, rows):
+    """Pages 2 and 4 GB apart, three of them."""
+    from block_drafter_gb300.paged import PagedCache4
+    c = Paged4Case((100, 90), (rows, rows), page=64).build()     # 4 pages in use, of 6: 3 of them far apart, the first request's
+    big = torch.empty(2 * page_stride + (1 << 20), dtype=torch.uint8, device="cuda")
+    far = []
+    for i, p in enumerate(c.pools):
+        x = big.as_strided((3,) + p.shape[1:], (page_stride,) + p.stride()[1:], i << 17)
+        x[1:].copy_(p[c.table[0, :2].long()])
+        far.append(x)
+    table = torch.tensor([[1, 2]], dtype=torch.int32, device="cuda")
+    cache = PagedCache4(*far, n_q_heads=8, dtype=torch.bfloat16)
+    batch = cache.batch(table, c.lend[:1].clone(), c.startd[:2].clone(), rows, rows, 100)
+    want, wl = c.attend()
+    out, lse = torch.empty_like(want[:rows]), torch.empty_like(wl[:rows])
+    cache.attention(batch, c.qd[:rows].contiguous(), out, lse=lse, scale=c.scale)
+    sync()
+    half = Paged4Case((100,), (rows,), page=64)
+    half.k, half.v, half.starts, half.qf, half.scale, half.max_rows = c.k[:1], c.v[:1], [0, rows], c.qf, c.scale, rows
+    half.check_attention(out, lse)
+    new = torch.randn(rows, 2, 128, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    cache.append(batch, new, new)
+    sync()
+    codes, scales = T.encode4(new.double().cpu().numpy(), 0)
+    j = torch.arange(100 - rows, 100)
+    for p, w in zip(far, (codes, scales) * 2):
+        got = torch.stack([p[1 + x // 64, :, x % 64] for x in j.tolist()])
+        assert torch.equal(got.cpu(), torch.from_numpy(w))
+
+
+def test_as_many_requests_as_there_may_be():
+    r = random.Random(1)
+    lens = tuple(r.choice([0, 1, 2, 15, 16, 17, 33]) for _ in range(1024))
+    for rows in (1, 5):
+        c = Paged4Case(lens, (rows,) * 1024, hkv=1, d=64).build()
+        out, lse = c.attend()
+        sync()
+        c.check_attention(out, lse)

@@ -382,3 +382,85 @@ def test_logprobs_alone_and_of_one_token_a_row():
     token_logprobs(x.cuda(), None, None, top_ids=ids)
     sync()
     assert torch.equal(lp, full[0][:, 0]) and torch.equal(ids, full[3])
+
+
+# ------------------------------------------------------------------ captured plans, far offsets, other streams
+@pytest.mark.parametrize("rows", [40, 3000])
+def test_a_captured_plan_in_place(rows):
+    """Replayed over what the replays before it left, on one block and on several."""
+    n, page, steps = 20, 16, 6
+    p = Plan([0] * n, [rows // n] * n, [0] * n, steps * rows // n // page + 2, page, steps * rows // page + 2 * n, rows)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        p.run()
+    r, length, held, table, free = random.Random(2), [0] * n, [0] * n, p.table, p.free
+    for _ in range(steps):
+        p.len.copy_(torch.tensor(length, dtype=torch.int32))
+        graph.replay()
+        sync()
+        p.args, p.table, p.free = (length, [rows // n] * n, held, page, rows), table, free
+        w = p.check()
+        held, table, free = w["held"], w["table"], w["free"]
+        length = [x - r.randint(0, rows // n) for x in w["seq_len"]]
+
+
+def test_rows_and_heads_far_apart():
+    """Offsets beyond 2^31 elements and 2^32 bytes."""
+    from block_drafter_gb300.target import HeadNormRope, token_logprobs
+    big = torch.empty(2 * (2 ** 30 + 8) + 2 ** 18, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((3, 100001), (2 ** 30 + 8, 1))
+    x.copy_((torch.randn(3, 100001, generator=torch.Generator().manual_seed(1)) * 3).bfloat16())
+    near = x.contiguous()
+    tokens = torch.tensor([5, 100000, -1], dtype=torch.int32, device="cuda")
+    side, got = torch.cuda.Stream(), []
+    for y in (x, near):
+        o = [torch.full((3,), -8.0, device="cuda"), torch.full((3,), -8.0, device="cuda"), torch.full((3, 4), -8, dtype=torch.int32, device="cuda")]
+        side.wait_stream(torch.cuda.current_stream())
+        token_logprobs(y, tokens, o[0], entropy=o[1], top_ids=o[2], stream=side)
+        got.append(o)
+    torch.cuda.synchronize()
+    sync()
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][0][2] == 0
+    assert (got[0][2].cpu() == near.float().cpu().sort(descending=True, stable=True).indices[:, :4]).all()
+    h = big.as_strided((3, 4, 128), (2 ** 30 + 8, 128, 1))
+    freq = torch.tensor([1e4 ** (-2 * j / 128) for j in range(64)], dtype=torch.float64, device="cuda")
+    op = HeadNormRope(128, freq, None, None, dtype=torch.bfloat16)
+    pos = torch.tensor([7, 2 ** 31 - 1, -1], dtype=torch.int32, device="cuda")
+    want = h.contiguous()
+    op(want, None, pos)
+    op(h, None, pos)
+    sync()
+    assert torch.equal(h, want)
+
+
+def test_a_captured_step_of_log_probabilities_and_heads():
+    from block_drafter_gb300.target import HeadNormRope, token_logprobs
+    g = torch.Generator().manual_seed(4)
+    op = HeadNormRope(64, torch.tensor([0.5, 0.01], dtype=torch.float64, device="cuda").repeat(8), None, None, dtype=torch.float16)
+    src = torch.randn(9, 6, 64, generator=g).half().cuda()
+    q, k, pos = src[:, :4], src[:, 4:], torch.arange(9, dtype=torch.int32, device="cuda")
+    qo, ko = torch.empty(9, 4, 64, dtype=torch.float16, device="cuda"), torch.empty(9, 2, 64, dtype=torch.float16, device="cuda")
+    logits, tokens = torch.empty(9, 40000, device="cuda"), torch.empty(9, dtype=torch.int32, device="cuda")
+    lp, ids = torch.empty(9, device="cuda"), torch.empty(9, 20, dtype=torch.int32, device="cuda")
+
+    def step():
+        op(q, k, pos, qo, ko)
+        token_logprobs(logits, tokens, lp, top_ids=ids)
+    logits.zero_()
+    tokens.zero_()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        src.copy_(torch.randn(9, 6, 64, generator=g))
+        logits.copy_(torch.randn(9, 40000, generator=g))
+        tokens.copy_(torch.randint(0, 40000, (9,), generator=g))
+        graph.replay()
+        got = [x.clone() for x in (qo, ko, lp, ids)]
+        step()
+        sync()
+        assert all(torch.equal(a, b) for a, b in zip(got, (qo, ko, lp, ids)))
+        assert (ids.cpu() == logits.cpu().sort(descending=True, stable=True).indices[:, :20]).all()
