@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["bd_abi.cu", "bd_gemm.cu", "bd_attention.cu", "bd_small.cu", "bd_noalloc.cu", "bd_pack.cu",
            "bd_head8.cu", "bd_bridge.cu", "bd_paged.cu", "bd_paged_attn.cu",
            "bd_paged_tc.cu", "bd_paged_wt.cu", "bd_paged_plan.cu", "bd_paged4.cu",
-           "bd_paged4_attn.cu", "bd_heads.cu", "bd_logprobs.cu"]
+           "bd_paged4_attn.cu", "bd_paged4_tc.cu", "bd_heads.cu", "bd_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-Xptxas", "-v", f"-I{INCLUDE}"]

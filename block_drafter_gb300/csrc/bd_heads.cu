@@ -17,7 +17,7 @@ static std::atomic<bool> target_used{false};  // some call of these files has la
 void use_target_kernels() { target_used.store(true, std::memory_order_release); }
 unsigned take_error_words_target() {
   if (!target_used.load(std::memory_order_acquire)) return 0;
-  return take_error_word_paged_plan() | take_error_word_paged4() | take_error_word_paged4_attn() | take_error_word_logprobs();
+  return take_error_word_paged_plan() | take_error_word_paged4() | take_error_word_paged4_attn() | take_error_word_paged4_tc() | take_error_word_logprobs();
 }
 
 namespace {

@@ -157,6 +157,7 @@ unsigned take_error_words_target();
 unsigned take_error_word_paged_plan();
 unsigned take_error_word_paged4();
 unsigned take_error_word_paged4_attn();
+unsigned take_error_word_paged4_tc();
 unsigned take_error_word_logprobs();
 
 }  // namespace bd

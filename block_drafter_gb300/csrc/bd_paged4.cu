@@ -251,7 +251,12 @@ WideSizes wide_sizes(const bd_paged4_kv *c, int n_requests, int max_rows, int ma
   w.pool = align256(static_cast<size_t>(n_requests) * w.pages * c->n_kv_heads * kWideSlots * c->head_dim * 2);
   return w;
 }
-bool is_few(const bd_paged4_kv *c, int max_rows) { return static_cast<int64_t>(max_rows) * (c->n_q_heads / c->n_kv_heads) <= kFewRows4; }
+// Which kernel takes calls of so many rows of a KV head.
+enum class Path { few, block, wide };
+Path path_of(const bd_paged4_kv *c, int max_rows) {
+  const int64_t rows = static_cast<int64_t>(max_rows) * (c->n_q_heads / c->n_kv_heads);
+  return rows <= kFewRows4 ? Path::few : rows <= kBlockRows4 ? Path::block : Path::wide;
+}
 
 bd_status check_kv4(const bd_paged4_kv *c) {
   if (!c) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit kv is NULL");
@@ -320,11 +325,15 @@ size_t bd_paged4_workspace_bytes(const bd_paged4_kv *kv, int n_requests, int max
     refuse(BD_ERR_INVALID_ARG, "paged 4-bit workspace: n_requests must be in 1..1024, max_rows >= 0 and max_len in 0..2^30");
     return 0;
   }
-  // a batch made for many rows may hold few: the larger of the two
+  // a batch made for many rows may hold few: the largest of the kernels'
+  const Path path = path_of(kv, max_rows);
   const size_t few = few4_bytes(kv->head_dim);
-  if (is_few(kv, max_rows)) return few;
-  const size_t many = wide_sizes(kv, n_requests, max_rows, max_len).all();
-  return few > many ? few : many;
+  if (path == Path::few) return few;
+  const size_t block = block4_bytes(n_requests, max_rows, kv->n_q_heads / kv->n_kv_heads, kv->head_dim);
+  const size_t most = few > block ? few : block;
+  if (path == Path::block) return most;
+  const size_t wide = wide_sizes(kv, n_requests, max_rows, max_len).all();
+  return most > wide ? most : wide;
 }
 
 bd_status bd_paged4_append(const bd_paged4_kv *kv, const bd_paged_batch *batch, const void *k_new, int64_t k_stride,
@@ -379,11 +388,12 @@ bd_status bd_paged4_attention(const bd_paged4_kv *kv, const bd_paged_batch *batc
     return refuse(BD_ERR_INVALID_ARG, "paged 4-bit attention: q and out overlap");
   if (misaligned(lse, 4)) return refuse(BD_ERR_INVALID_ARG, "paged 4-bit attention: lse misaligned");
   const int group = kv->n_q_heads / kv->n_kv_heads;
+  const Path path = path_of(kv, batch->max_rows);
   const WideSizes w = wide_sizes(kv, batch->n_requests, batch->max_rows, batch->max_len);
   if ((static_cast<int64_t>(batch->max_len) / 16 + 8) * kv->n_kv_heads >= (1ll << 30) ||
       static_cast<int64_t>(batch->max_rows) * kv->n_q_heads > (1 << 30) ||
       (static_cast<int64_t>(batch->max_rows) * group / 256 + 1) * batch->n_requests > (1 << 28) ||
-      (!is_few(kv, batch->max_rows) && (w.pages * batch->n_requests > (1 << 30) || 2 * kv->n_kv_heads > 65535)))
+      (path == Path::wide && (w.pages * batch->n_requests > (1 << 30) || 2 * kv->n_kv_heads > 65535)))
     return refuse(BD_ERR_UNSUPPORTED, "paged 4-bit attention: max_len * n_kv_heads, max_rows * n_q_heads, n_requests * max_rows or "
                                       "n_requests * max_len too large");
   if (!workspace || misaligned(workspace, 256) ||
@@ -395,23 +405,24 @@ bd_status bd_paged4_attention(const bd_paged4_kv *kv, const bd_paged_batch *batc
   a.p.window = window;
   a.p.n_sink = n_sink;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (is_few(kv, batch->max_rows)) {
+  if (path != Path::wide) a.p.scale_log2 = static_cast<float>(std::ldexp(scale * 1.4426950408889634, kv->k_exp));
+  if (path == Path::few) {
     Paged4AttnArgs A = {};
     A.c = a;
-    A.c.p.scale_log2 = static_cast<float>(std::ldexp(scale * 1.4426950408889634, kv->k_exp));
     A.out = out;
     A.out_stride = out_stride;
     A.lse = lse;
     A.out_scale = std::ldexp(1.f, kv->v_exp);
     return ran(launch_attention_few4(A, workspace, kv->dtype, s));
   }
-  uint8_t *p = static_cast<uint8_t *>(workspace);
   PagedAttnArgs A = {};
   A.p = a.p;
-  A.p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
   A.out = out;
   A.out_stride = out_stride;
   A.lse = lse;
+  if (path == Path::block) return ran(launch_attention_block4(A, a, workspace, kv->dtype, s));
+  A.p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  uint8_t *p = static_cast<uint8_t *>(workspace);
   WidenArgs W = {};
   W.c = a;
   W.table = reinterpret_cast<int32_t *>(p + w.attention);

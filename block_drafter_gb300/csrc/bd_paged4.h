@@ -23,14 +23,18 @@ struct Paged4AttnArgs {
   float *part_o;
   float2 *part_ml;
   int n_ctas, whole, cluster;
-  int groups;  // in which a KV head's rows are taken, at most
   uint32_t page_units, units_magic;  // 16-slot places of a page, and what divides by them
 };
 
-// Query rows (of one KV head) of the kernel that reads the codes themselves.
-constexpr int kFewRows4 = 96;
+// Query rows (of one KV head) of the kernels that read the codes themselves: of few rows, and of blocks; more read a 16-bit
+// copy.  8 requests of up to 16 384 slots, 8 KV heads: 16 rows 46 us, as a block 66 us; 128 rows as a block 72 us, over the copy
+// 186 us (of which it takes two thirds); 192 rows 196 us, as two items of a block twice the 72 us.
+constexpr int kFewRows4 = 16;
+constexpr int kBlockRows4 = 128;
 
 size_t few4_bytes(int head_dim);
+size_t block4_bytes(int n_requests, int max_rows, int group, int head_dim);
 std::string launch_attention_few4(Paged4AttnArgs A, void *workspace, int dtype, cudaStream_t s);
+std::string launch_attention_block4(PagedAttnArgs A, const Paged4Args &c, void *workspace, int dtype, cudaStream_t s);
 
 }  // namespace bd

@@ -110,11 +110,11 @@ struct FewWarp4 {
   static constexpr int W = D / 64, NK = D / 16, NV = D / 16;
   static constexpr bool QS = NT > 1;
   static constexpr bool kScaled = !std::is_same<T, __half>::value;  // queries are
-  static constexpr bool kRest = !kScaled && NT <= 2;                // the rest of the weights is multiplied, too
+  static constexpr bool kRest = !kScaled;                           // the rest of the weights is multiplied, too
   float o[NT][NV][4];
   float m[NT][2], l[NT][2];  // what weights are formed against, the maximum less kHead; their sums
 
-  __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int from, int R, int t0, int t1,
+  __device__ __forceinline__ void run(const Paged4AttnArgs &A, const Request &rq, const Tiles &tl, int b, int h, int R, int t0, int t1,
                                       uint8_t *ring, uint4 (*qs)[NK / 2][32], float *row_log2, int warp, int lane) {
     const Paged4Args &c4 = A.c;
     const PagedArgs &a = c4.p;
@@ -125,8 +125,8 @@ struct FewWarp4 {
     float to_log2[NT][2];
 #pragma unroll
     for (int n = QS ? warp : 0; n < NT; n += QS ? kFewWarps : 1) {
-      const int r = 8 * n + quad, i = r < R ? (from + r) / a.group : 0;
-      const T *src = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + (h * a.group + (r < R ? from + r - i * a.group : 0)) * D + kq * (D / 4);
+      const int r = 8 * n + quad, i = r < R ? r / a.group : 0;
+      const T *src = static_cast<const T *>(a.q) + (rq.row0 + i) * a.q_stride + (h * a.group + (r < R ? r - i * a.group : 0)) * D + kq * (D / 4);
       uint4 raw[NK / 2];
 #pragma unroll
       for (int t = 0; t < NK / 2; ++t) raw[t] = r < R ? *reinterpret_cast<const uint4 *>(src + t * 8) : make_uint4(0, 0, 0, 0);
@@ -171,14 +171,13 @@ struct FewWarp4 {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = 8 * n + 2 * kq + y;
-        p[n][y] = r < R ? rq.n - rq.rows + (from + r) / a.group : -1;
+        p[n][y] = r < R ? rq.n - rq.rows + r / a.group : -1;
         f[n][y] = p[n][y] >= 0 ? window_first(a, p[n][y]) : 0;
         m[n][y] = kNone;
         l[n][y] = 0.f;
       }
-    // the slots of the first and the last of these rows, where their windows begin, and where the request's first row's does
-    const int p_low = rq.n - rq.rows + from / a.group, p_high = rq.n - rq.rows + (from + R - 1) / a.group;
-    const int f_high = window_first(a, max(0, p_high)), f_low = window_first(a, max(0, rq.n - rq.rows));
+    // the first row's slot, and where its window and the last row's begin
+    const int p_low = rq.n - rq.rows, f_high = window_first(a, max(0, rq.n - 1)), f_low = window_first(a, max(0, p_low));
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -452,7 +451,7 @@ template <typename T, int D> __device__ void no_slots(const Paged4AttnArgs &A, c
   empty_rows<T, D>(x, rq, rq.rows, tid, step);
 }
 
-template <int NT> constexpr int few4_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }  // blocks an SM holds at once
+template <int NT> constexpr int few4_per_sm() { return NT == 1 ? 4 : 3; }  // blocks an SM holds at once
 // A warp's ring, in whose place its sums come at the end; all of a block's, and its queries.
 template <int D, int NT> constexpr int few4_region() {
   return 8 * NT * (D + 4) * 4 > Ring<D>::kWarp ? 8 * NT * (D + 4) * 4 : Ring<D>::kWarp;
@@ -491,23 +490,21 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
     u1 = share_begin(units, ctas, g + 1);
   }
   do {
-    int b, h, from, t0, t1;  // `from`: the first of these rows among the head's
+    int b, h, t0, t1;
     Request rq;
     Tiles tl;
     if (A.whole) {  // one head's rows, or a cluster's block's part of them
       const int item = g / static_cast<uint32_t>(A.cluster), rank = g - item * A.cluster;
-      const int head = item / static_cast<uint32_t>(A.groups);
-      from = (item - head * A.groups) * ROWS;
-      b = head / a.n_kv_heads;
-      h = head - b * a.n_kv_heads;
+      b = item / static_cast<uint32_t>(a.n_kv_heads);
+      h = item - b * a.n_kv_heads;
       rq = request_of(a, b);
       tl = tiles_of<kUnit4>(a, rq);
       t0 = tl.count * rank / A.cluster;
       t1 = tl.count * (rank + 1) / A.cluster;
       u = t0;
       u1 = t1;
-      if (tl.count == 0 || from >= rq.rows * a.group) {
-        if (tl.count == 0 && h == 0 && rank == 0 && from == 0) no_slots<T, D>(A, rq, tid, kFewThreads);
+      if (tl.count == 0) {
+        if (h == 0 && rank == 0) no_slots<T, D>(A, rq, tid, kFewThreads);
         return;
       }
     } else {
@@ -515,16 +512,14 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
       rq = b < kFewThreads ? first[b] : request_of(a, b);
       tl = tiles_of<kUnit4>(a, rq);
       const uint32_t in = static_cast<uint32_t>(u - start[b]);  // below 2^31: checked by the host
-      const uint32_t item = in / static_cast<uint32_t>(tl.count), groups = (rq.rows * a.group + ROWS - 1) / ROWS;
-      h = item / groups;
-      from = (item - h * groups) * ROWS;
-      t0 = in - item * tl.count;
+      h = in / static_cast<uint32_t>(tl.count);
+      t0 = in - h * tl.count;
       t1 = static_cast<int>(u1 - u < tl.count - t0 ? t0 + (u1 - u) : tl.count);
     }
-    const int R = min(ROWS, rq.rows * a.group - from);
+    const int R = rq.rows * a.group;
     {
       FewWarp4<T, D, NT, PAGE16> w;
-      w.run(A, rq, tl, b, h, from, R, t0, t1, sm_raw + warp * REGION, qs, row_log2, warp, lane);
+      w.run(A, rq, tl, b, h, R, t0, t1, sm_raw + warp * REGION, qs, row_log2, warp, lane);
       const int quad = lane >> 2, kq = lane & 3;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -541,7 +536,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
     const bool whole = t0 == 0 && t1 == tl.count;
     const int64_t slot = static_cast<int64_t>(2 * g + (t0 > 0 ? 0 : 1)) * ROWS;
     if (tid == 0 && !A.whole && t0 > 0 && share_begin(units, ctas, g - 1) <= u - t0)  // the first block to begin inside this head
-      A.join[g] = {b, h, from, R, share_owner(units, ctas, u - t0 + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
+      A.join[g] = {b, h, 0, R, share_owner(units, ctas, u - t0 + tl.count - 1) - g + 2, rq.row0, rq.n, rq.rows};
     __syncthreads();
     for (int c = tid; c < R * (D / 4); c += kFewThreads) {  // join the warps
       const int r = c / (D / 4), d = (c - r * (D / 4)) * 4;
@@ -567,7 +562,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
         *reinterpret_cast<float4 *>(so(0, r, d)) = o;
         if (d == 0) block_ml[r] = make_float2(M, L);
       } else if (whole) {
-        finish<T>(A, rq, h, from + r, d, o, M, L);
+        finish<T>(A, rq, h, r, d, o, M, L);
       } else {
         *reinterpret_cast<float4 *>(A.part_o + (slot + r) * D + d) = o;
         if (d == 0) A.part_ml[slot + r] = make_float2(M, L);
@@ -600,7 +595,7 @@ __global__ void __launch_bounds__(kFewThreads, few4_per_sm<NT>()) attention_few4
             o.w += wi * v[i].w;
           }
         }
-        if (d < D) finish<T>(A, rq, h, from + r, d, o, M, L);
+        if (d < D) finish<T>(A, rq, h, r, d, o, M, L);
       }
       __syncwarp();
       cluster_sync();  // every block's sums are read
@@ -682,7 +677,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_con
         o.w += v.w;
       }
   }
-  if (k == 0) finish<T>(A, rq, j.h, j.from + r0 + r, d, o, row_ml[r].x, row_ml[r].y);
+  if (k == 0) finish<T>(A, rq, j.h, r0 + r, d, o, row_ml[r].x, row_ml[r].y);
 }
 static_assert(kJoinRows * 128 / 4 <= kJoinThreads, "a block's pieces");
 
@@ -706,7 +701,7 @@ template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnA
   static const ClustersAtOnce fit(kernel, kFewThreads, SMEM);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads * A.groups;
+  const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
   int blocks = 1;
   while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
   const bool alike = seen < a.max_len || a.n_requests == 1;
@@ -741,17 +736,15 @@ template <typename T, int D, int NT> cudaError_t launch(Paged4AttnArgs &A, cudaS
   return launch<T, D, NT, true>(A, s);
 }
 template <typename T, int D> cudaError_t launch(Paged4AttnArgs &A, cudaStream_t s) {
-  const int rows = A.c.p.max_rows * A.c.p.group;
-  A.groups = rows <= 16 ? 1 : (rows + 31) / 32;
-  return rows <= 8 ? launch<T, D, 1>(A, s) : rows <= 16 ? launch<T, D, 2>(A, s) : launch<T, D, 4>(A, s);
+  return A.c.p.max_rows * A.c.p.group <= 8 ? launch<T, D, 1>(A, s) : launch<T, D, 2>(A, s);
 }
 
 }  // namespace
 
 // Rows of all parts, of the launches that have most.
 static size_t few4_part_rows() {
-  const size_t a = few4_blocks(few4_per_sm<1>()) * 8, b = few4_blocks(few4_per_sm<2>()) * 16, c = few4_blocks(few4_per_sm<4>()) * 32;
-  return 2 * (a > b ? a > c ? a : c : b > c ? b : c);
+  const size_t a = few4_blocks(few4_per_sm<1>()) * 8, b = few4_blocks(few4_per_sm<2>()) * 16;
+  return 2 * (a > b ? a : b);
 }
 size_t few4_bytes(int head_dim) {
   return align256(few4_blocks(few4_per_sm<1>()) * sizeof(PagedJoin)) + align256(few4_part_rows() * head_dim * 4) + align256(few4_part_rows() * 8);

@@ -1,0 +1,278 @@
+// Attention of blocks over a 4-bit cache (bd_paged4_attention with kFewRows4 + 1 .. kBlockRows4 rows of a KV head) on the
+// tensor cores: the kernel of the 16-bit cache (bd_paged_tc.cu), with two warps that bring the codes and four that
+// work their values out and store them as the tiles that the products read.
+//
+// Codes times scale are fp16 numbers (2 bits times 4), so the products run on exactly what the slots stand for, in fp16 for
+// both types: a bf16 row of queries is scaled by a power of two that brings its largest value to 2^8, which keeps every
+// value down to 2^-25 of that exact and the rest to 2^-33 of it.  Weights round to 2^-12 relative, as fp16 does.
+//
+// 8 requests of 16 rows over up to 16 384 slots (8 KV heads, group 4, D = 128): 69 us, where the codes and scales are 16 us of
+// the copy rate and the products 12 us of the tensor cores' (24 with the half of a 128-row tile that 64 rows leave).  About
+// 1800 cycles a tile, the two streams' waits for their products and 32 exponentials a cycle on the half of an SM
+// whose TMEM lanes hold the rows; the rest is a block's beginning and its items' queries and results.  With the unpacking
+// left to two warps it took 100 us, with four that copied for themselves 87.
+#include "bd_paged4.cuh"
+#include "bd_paged_many.cuh"
+
+namespace bd {
+
+BD_DEFINE_ERROR_TAKER(take_error_word_paged4_tc)
+
+namespace {
+
+constexpr int kStages = 3;  // tiles whose codes are on their way or being unpacked
+
+__device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void *src, int bytes, bool valid) {
+  if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+
+struct Pool4 {
+  static constexpr bool k4 = true;
+  template <typename T> using Op = __half;
+  template <typename T> static constexpr bool kScaled = !std::is_same<T, __half>::value;  // rows of queries are
+  static constexpr int kThreads = 512, kLoaders = 4, kCopiers = 2;
+  static constexpr int kRegsSoftmax = 184, kRegsOther = 72, kRegsLoaders = 72;  // in all what 512 threads of 128 start with
+  template <int D> static constexpr int slots() { return D == 128 ? 4 : 8; }
+  // a tile's keys and values: codes, then scales of each
+  template <int D> static constexpr uint32_t side_bytes() { return kTileSlots * (D / 2 + D / 16); }
+  // and the stages' barriers
+  template <int D> static constexpr uint32_t stage_bytes() { return kStages * 2 * side_bytes<D>() + 64; }
+  static_assert(2 * kStages * 8 <= 64, "barriers");
+  PoolMaps maps;  // of the codes: boxes of D/2 bytes x `box` slots; box 0: row by row
+  int box;
+  uint32_t page_magic, page_shift;  // j / page_size is the upper word of j * magic, shifted (magic 0: one slot a page)
+  const void *k_scale, *v_scale;
+  int64_t page_stride, head_stride, slot_stride;  // of the scale pools, bytes
+  float v_scale_up;                               // 2^v_exp
+  __host__ __device__ float out_scale() const { return v_scale_up; }
+
+  // A row of D values at `at` of a swizzled tile (row & 7: swizzle) becomes fp16 times a power of two; returns the inverse.
+  template <typename T, int D> static __device__ __forceinline__ float scale_row(uint32_t at, int swizzle) {
+    auto piece = [&](int c) { return at + (c >> 3) * kAtom + (((c & 7) ^ swizzle) << 4); };
+    auto get = [&](int c, uint32_t (&w)[4]) {
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(piece(c)) : "memory");
+    };
+    uint32_t tops = 0;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      uint32_t w[4];
+      get(c, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tops = __vmaxu2(tops, w[i] & 0x7fff7fffu);
+    }
+    const uint32_t top = max(tops & 0xffffu, tops >> 16);
+    // 2^8 <= largest < 2^9; infinities and NaN stay what they are
+    const int shift = top >= 0x0080u && top < 0x7f80u ? min(126, 127 + 8 - static_cast<int>(top >> 7)) : 0;
+    const float f = pow2(shift);
+#pragma unroll 2
+    for (int c = 0; c < D / 8; ++c) {
+      uint32_t w[4];
+      get(c, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = Pair<T>::unpack(w[i]);
+        w[i] = Pair<__half>::pack(x.x * f, x.y * f);
+      }
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(c)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+    return pow2(-shift);
+  }
+
+  struct Stages {
+    uint32_t first;  // shared-memory address of the first one
+    uint64_t *landed, *freed;
+  };
+  template <int D> static __device__ __forceinline__ Stages stages_of(uint32_t ring) {
+    using C = Tc<D, Pool4>;
+    const uint32_t first = ring + (C::kOffStage - C::kOffRing);
+    uint64_t *bars = static_cast<uint64_t *>(__cvta_shared_to_generic(first + kStages * 2 * side_bytes<D>()));
+    return {first, bars, bars + kStages};
+  }
+  template <int D> static __device__ void init(uint32_t ring) {
+    const Stages g = stages_of<D>(ring);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&g.landed[i], 33 * kCopiers);
+      mbar_init(&g.freed[i], kLoaders);
+    }
+    fence_barrier_init();
+  }
+  template <int D>
+  static __device__ void copy(const PagedAttnArgs &A, const Pool4 &src, const Segment *segs, uint32_t ring, const Bars &B, int warp, int lane);
+  template <typename T, int D>
+  static __device__ void load(const PagedAttnArgs &A, const Pool4 &src, const Segment *segs, uint32_t ring, const Bars &B, int warp, int lane);
+};
+
+// Byte r of a stage's codes has its 16-byte pieces exchanged by r: TMA's swizzle of 64 bytes (32 with D = 64).
+template <int D> __device__ __forceinline__ int swizzle4(int r) { return D == 128 ? r >> 1 & 3 : r >> 2 & 1; }
+
+// Warp w copies slots 64w .. 64w+63 of every tile: codes by TMA, in boxes of as many slots as lie together in a page (a power
+// of two, 8 to 64; other page sizes row by row with cp.async), scales with cp.async; zeros where no row sees the slot.
+template <int D>
+__device__ void Pool4::copy(const PagedAttnArgs &A, const Pool4 &src, const Segment *segs, uint32_t ring, const Bars &B, int warp, int lane) {
+  constexpr uint32_t ROW = D / 2, SIDE = side_bytes<D>(), CODES = kTileSlots * ROW;
+  constexpr int P = D / 32, RI = 32 / P, Y = 64 / RI;  // pieces of a row; rows of a turn, turns
+  const PagedArgs &a = A.p;
+  const Stages g = stages_of<D>(ring);
+  const uint32_t to0 = g.first + warp * 64 * ROW, scales0 = g.first + CODES + warp * 64 * (D / 16);
+  const int box = src.box, cr = lane / P, cp = lane % P;
+  const bool leads[2] = {box && lane % box == 0, box && (32 + lane) % box == 0};  // this lane's slots: a box's first
+  Segments walk(B, segs);
+  uint32_t filled = 0;
+  auto leave = [&]() {  // nothing is in flight when the block ends
+    cp_async_wait<0>();
+    bool ok = true;
+    for (uint32_t i = filled < kStages ? 0 : filled - kStages; box && ok && i < filled; ++i) ok = mbar_wait(&g.landed[i % kStages], (i / kStages) & 1);
+  };
+  while (const Segment *seg = walk.next()) {
+    const Segment s = *seg;
+    walk.done(lane);
+    const int32_t *table = a.page_table + static_cast<int64_t>(s.b) * a.table_width;
+    const uint8_t *K = static_cast<const uint8_t *>(a.k) + s.h * a.head_stride + cp * 16, *V = static_cast<const uint8_t *>(a.v) + s.h * a.head_stride + cp * 16;
+    const uint8_t *KS = static_cast<const uint8_t *>(src.k_scale) + s.h * src.head_stride, *VS = static_cast<const uint8_t *>(src.v_scale) + s.h * src.head_stride;
+    const int f_low = window_first(a, max(0, s.p_low)), p_high = s.p_high;
+    // this lane's slots of a tile (rows lane and 32 + lane), their pages (ahead of their use) and places in them
+    auto slot_of = [&](int t, int k) { return s.tile(min(t, s.t1 - 1)) * kTileSlots + warp * 64 + k * 32 + lane; };
+    int page[2];
+    uint32_t in_page[2];
+    auto locate = [&](int t) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t j = min(slot_of(t, k), p_high), x = src.page_magic ? __umulhi(j, src.page_magic) >> src.page_shift : j;
+        page[k] = __ldg(table + x);
+        in_page[k] = j - x * a.page_size;
+      }
+    };
+    locate(s.t0);
+    for (int t = s.t0; t < s.t1; ++t, ++filled) {
+      const uint32_t st = filled % kStages, to = to0 + st * 2 * SIDE, to_scale = scales0 + st * 2 * SIDE;
+      if (filled >= kStages && !wait_warp(B, &g.freed[st], (filled / kStages - 1) & 1)) return leave();
+      if (lane == 0) mbar_arrive_expect_tx(&g.landed[st], box ? 2 * 64 * ROW : 0);
+      int64_t code[2], scale[2];
+      bool in[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = slot_of(t, k), r = k * 32 + lane;
+        const bool known = static_cast<unsigned>(page[k]) < static_cast<unsigned>(a.n_pages);
+        const bool seen = any_seen(a, j, 1, f_low, p_high), box_seen = leads[k] && any_seen(a, j, box, f_low, p_high);
+        if (!known && (seen || box_seen)) atomicOr(&g_error_word, DEVERR_BAD_INDEX);
+        in[k] = seen && known;
+        code[k] = in[k] ? page[k] * a.page_stride + in_page[k] * a.slot_stride : -1;
+        scale[k] = in[k] ? page[k] * src.page_stride + in_page[k] * src.slot_stride : 0;
+        if (leads[k]) {
+          const int pg = box_seen && known ? page[k] : a.n_pages;  // beyond the pool: zeros
+          tma_load_4d(to + r * ROW, &src.maps.k, &g.landed[st], 0, in_page[k], s.h, pg);
+          tma_load_4d(to + r * ROW + SIDE, &src.maps.v, &g.landed[st], 0, in_page[k], s.h, pg);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t dst = to_scale + (k * 32 + lane) * (D / 16);
+        cp_async_bytes(dst, KS + scale[k], D / 16, in[k]);
+        cp_async_bytes(dst + SIDE, VS + scale[k], D / 16, in[k]);
+      }
+      if (!box) {
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          const int r = y * RI + cr;
+          const int64_t off = __shfl_sync(0xffffffffu, y * RI < 32 ? code[0] : code[1], r & 31);
+          const uint32_t dst = to + r * ROW + ((cp ^ swizzle4<D>(r)) << 4);
+          cp_async16(dst, K + (off < 0 ? 0 : off), off >= 0);
+          cp_async16(dst + SIDE, V + (off < 0 ? 0 : off), off >= 0);
+        }
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&g.landed[st])) : "memory");
+      locate(t + 1);
+    }
+  }
+  leave();
+}
+
+// Warp w unpacks slots 32w .. 32w+31 of every tile: eight lanes read the same piece of eight rows, which lie in different
+// banks; a lane's 32 values are four whole 16-byte pieces of the tile's row, which the tile's swizzle spreads the same way.
+template <typename T, int D>
+__device__ void Pool4::load(const PagedAttnArgs &A, const Pool4 &src, const Segment *segs, uint32_t ring, const Bars &B, int warp, int lane) {
+  using C = Tc<D, Pool4>;
+  constexpr uint32_t NS = C::kSlots, ROW = D / 2, SIDE = side_bytes<D>(), CODES = kTileSlots * ROW;
+  constexpr int P = D / 32, RI = 32 / P, Y = 32 / RI;  // pieces of a row; rows of a turn, turns
+  const Stages g = stages_of<D>(ring);
+  const int r = lane % RI, p = lane / RI;
+  const uint32_t from0 = g.first + (warp * 32 + r) * ROW, scales0 = g.first + CODES + (warp * 32 + r) * (D / 16) + p * 2;
+  const uint32_t to0 = ring + (p >> 1) * kAtom + (warp * 32 + r) * 128;
+  Segments walk(B, segs);
+  uint32_t q = 0, read = 0;  // ring tiles filled, stages read
+  while (const Segment *seg = walk.next()) {
+    const int n = seg->t1 - seg->t0;
+    walk.done(lane);
+    for (int t = 0; t < n; ++t, ++read) {
+      const uint32_t st = read % kStages;
+      if (!wait_warp(B, &g.landed[st], (read / kStages) & 1)) return;
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v, ++q) {
+        const uint32_t from = from0 + (2 * st + v) * SIDE, from_scale = scales0 + (2 * st + v) * SIDE, to = to0 + q % NS * C::kTile;
+        uint32_t w[Y][4];
+        uint16_t z[Y];
+#pragma unroll
+        for (int u = 0; u < Y; ++u) {
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                       : "r"(from + u * RI * ROW + ((p ^ swizzle4<D>(u * RI + r)) << 4)) : "memory");
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(z[u]) : "r"(from_scale + u * RI * (D / 16)) : "memory");
+        }
+        if (q >= NS && !wait_warp(B, &B.empty[q % NS], ((q / NS) - 1) & 1)) return;
+#pragma unroll
+        for (int u = 0; u < Y; ++u) {
+          const uint32_t both = e4m3_pair(z[u]), f[2] = {__byte_perm(both, 0, 0x1010), __byte_perm(both, 0, 0x3232)};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t o[4];
+            e2m1_pairs(w[u][x], o);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[y] = mul_f16x2(o[y], f[x >> 1]);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + u * RI * 128 + ((((p & 1) * 4 + x) ^ (lane & 7)) << 4)),
+                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+          }
+        }
+        fence_proxy_async_shared();
+        mbar_arrive(&B.full[q % NS]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&g.freed[st]);
+    }
+  }
+}
+
+inline bool code_map(CUtensorMap *m, const PagedArgs &a, const void *pool, int box) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim / 2), static_cast<cuuint64_t>(a.page_size),
+                              static_cast<cuuint64_t>(a.n_kv_heads), static_cast<cuuint64_t>(a.n_pages)};
+  const int64_t stride[3] = {a.slot_stride, a.head_stride, a.page_stride};
+  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(a.head_dim / 2), static_cast<cuuint32_t>(box), 1, 1};
+  return tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, pool, 4, dims, stride, boxes,
+                   a.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+}
+
+}  // namespace
+
+size_t block4_bytes(int n_requests, int max_rows, int group, int head_dim) { return many_workspace_bytes(n_requests, max_rows, group, head_dim); }
+
+std::string launch_attention_block4(PagedAttnArgs A, const Paged4Args &c, void *workspace, int dtype, cudaStream_t s) {
+  const PagedArgs &a = A.p;
+  const int rows = box_rows(a.page_size), box = rows > 64 ? 64 : rows;
+  uint32_t shift = 0, magic = 0;
+  if (a.page_size > 1) {  // 2^(32 + shift) over the size, rounded up, where 2^shift < size <= 2^(shift + 1): exact below 2^31
+    while ((2ll << shift) < a.page_size) ++shift;
+    magic = static_cast<uint32_t>(((1ull << (32 + shift)) + a.page_size - 1) / a.page_size);
+  }
+  Pool4 src = {{}, box, magic, shift, c.k_scale, c.v_scale, c.scale_page_stride, c.scale_head_stride, c.scale_slot_stride, std::ldexp(1.f, c.v_exp)};
+  if (box && !(code_map(&src.maps.k, a, a.k, box) && code_map(&src.maps.v, a, a.v, box))) src.box = 0;
+  set_many_workspace(A, workspace);
+  cudaError_t e;
+  if (dtype == BD_BF16)
+    e = a.head_dim == 128 ? launch_tc<__nv_bfloat16, 128>(A, src, s) : launch_tc<__nv_bfloat16, 64>(A, src, s);
+  else
+    e = a.head_dim == 128 ? launch_tc<__half, 128>(A, src, s) : launch_tc<__half, 64>(A, src, s);
+  return e == cudaSuccess ? std::string() : std::string("paged 4-bit attention: ") + cudaGetErrorString(e);
+}
+
+}  // namespace bd

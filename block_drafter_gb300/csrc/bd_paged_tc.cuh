@@ -89,8 +89,9 @@ inline int box_rows(int page_size) {
   return b >= 8 ? b : 0;
 }
 
-// Tiled map of 16-bit values, 128-byte swizzled, boxes of 64 x box[1] x ...; strides in elements.
-inline bool tiled_map(CUtensorMap *m, const void *p, bool bf16, int rank, const cuuint64_t *dims, const int64_t *stride, const cuuint32_t *boxes) {
+// Tiled map, boxes of boxes[0] x boxes[1] x ...; strides in bytes.
+inline bool tiled_map(CUtensorMap *m, CUtensorMapDataType type, const void *p, int rank, const cuuint64_t *dims, const int64_t *stride,
+                      const cuuint32_t *boxes, CUtensorMapSwizzle swizzle) {
   using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -104,11 +105,17 @@ inline bool tiled_map(CUtensorMap *m, const void *p, bool bf16, int rank, const 
   }();
   if (!encode) return false;
   cuuint64_t strides[3];
-  for (int i = 0; i + 1 < rank; ++i) strides[i] = dims[i + 1] > 1 ? static_cast<cuuint64_t>(stride[i]) * 2 : 16;
+  for (int i = 0; i + 1 < rank; ++i) strides[i] = dims[i + 1] > 1 ? static_cast<cuuint64_t>(stride[i]) : 16;
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(p), dims,
-                strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(m, type, rank, const_cast<void *>(p), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The same of 16-bit values, 128-byte swizzled, boxes of 64 x box[1] x ...; strides in elements.
+inline bool tiled_map(CUtensorMap *m, const void *p, bool bf16, int rank, const cuuint64_t *dims, const int64_t *stride, const cuuint32_t *boxes) {
+  int64_t bytes[3];
+  for (int i = 0; i + 1 < rank; ++i) bytes[i] = stride[i] * 2;
+  return tiled_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, rank, dims, bytes, boxes,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 inline bool pool_map(CUtensorMap *m, const PagedArgs &a, const void *pool, bool bf16, int box) {
