@@ -149,7 +149,7 @@ def test_bad_4_bit_attention_arguments_are_refused(B):
                         (dict(scale=float("nan")), -1, b"scale"), (dict(ws=None), -5, b"workspace"), (dict(ws=0x100010), -5, b"workspace"),
                         (dict(n=0), -5, b"workspace")):
         assert _attend4(B, kv, bt, **kw) == st and msg in L.bd_last_error(), kw
-    many = _batch(B, n_rows=66, max_rows=33)      # 132 rows of a KV head read a copy, which grows with the slots
+    many = _batch(B, n_rows=40, max_rows=33)      # 132 rows of a KV head read a copy, which grows with the slots
     need = L.bd_paged4_workspace_bytes(kv, 2, 33, 100)
     assert _attend4(B, kv, many, n=need - 1) == -5
     assert L.bd_paged4_workspace_bytes(kv, 2, 33, 1000) > need > L.bd_paged4_workspace_bytes(kv, 2, 1, 100)
