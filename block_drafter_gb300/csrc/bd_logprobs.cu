@@ -16,7 +16,8 @@
 // equal ones), the row is looked through again with the threshold that those aside give, which is larger each time.
 //
 // Few rows are a cluster's of up to 16 blocks, each with an equal part of the row; the first one joins their sums and
-// candidates through distributed shared memory.  Bound by the bytes of the logits.
+// candidates through distributed shared memory.  2047 rows of 151 936 16-bit logits, top 20: 157 us, 4.0 TB/s, bound by the
+// instructions of a logit (exponential, two sums, comparison) before the bytes; 8 rows of fp32, top 8: 11.7 us, by latency.
 #include <cfloat>
 #include <climits>
 

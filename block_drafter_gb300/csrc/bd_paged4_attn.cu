@@ -1,5 +1,5 @@
 // Attention of few rows over a 4-bit cache (bd_paged4_attention with at most kFewRows4 rows of a KV head:
-// decoding and short blocks).
+// decoding, short blocks).
 //
 // The scheme is the 16-bit kernel's -- one pass with the running maximum and sum, units of 32 slots shared out evenly or a
 // cluster a head, every warp alone on every fourth unit -- but what bounds it is not only the bytes (0.5625 a
@@ -682,9 +682,22 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join4(const __grid_con
 static_assert(kJoinRows * 128 / 4 <= kJoinThreads, "a block's pieces");
 
 // ------------------------------------------------------------------ host
-constexpr int kWholeSlots = 512;
-constexpr int kBlockSlots = 64;
-constexpr int kClusterSlots = 1088, kClusterFilled = 2176;
+// us of one row of group 4, D = 128, pages of 64 (equal lengths / lengths from an eighth of it up).
+// A head is one block's up to kSoloSlots slots or kSoloHeads times the heads: a cluster's start and join cost more
+// (8 heads of 256 slots: one block 4.9, clusters 5.9, of 512 6.5 and 5.9; 64 heads of 512: 6.7 and 7.4, of 1024 9.4 and 8.2; 128 heads of
+// 1024: 9.5 and 10.4, of 2048 15.3 and 14.0; 256 heads of 2048: 22.2 and 23.2, of 4096 38.7 and 38.2).
+constexpr int kSoloSlots = 512, kSoloHeads = 12;
+// Where no clusters fit, a head is still one block's up to kWholeSlots, in as many rounds as it takes: sharing out costs the
+// sum of the lengths in every block and the join (512 heads of 1024 slots: 21.6/18.6, shared out 35.1/32.4; of 4096 66.5/57.9 and
+// 74.2/56.9, of 8192 126.6/109 and 125.3/87.4; 640 heads of 4096: 84.3/62.6 and 87.7/69.0; 2048 heads of 2048 114/81 and 137/111).
+constexpr int kWholeSlots = 4096;
+constexpr int kBlockSlots = 64;  // of a cluster's block, at least (8 heads of 1024 slots: sixteen blocks 6.7, one 9.3)
+// A cluster is as slow as its longest head, and max_len only bounds it: up to kClusterSlots slots a block (64 heads of 16 384
+// slots: 37.7/29.0, shared out 40.6/30.6; 128 heads of 8192 37.8/30.1 and 42.2/31.5; 64 heads of 32 768, 4096 a block, 68.1/50.3 and
+// 66.5/44.7).  Where the heads are alike, as a window or a call of one request makes them, a block's slots are weighed against an
+// even share and kJoinSlots + kPartSlots for each of a head's parts for the join (8 heads of 16 384 slots: 13.4, shared out
+// 15.5; of 32 768 21.4 and 19.0), or, where clusters give every SM a block, bounded by kClusterFilled.
+constexpr int kClusterSlots = 2048, kClusterFilled = 2176;
 constexpr int kJoinSlots = 800, kPartSlots = 2;
 
 // Blocks of a launch that is shared out: as many as the SMs hold at once.
@@ -703,7 +716,8 @@ template <typename T, int D, int NT, bool PAGE16> cudaError_t launch(Paged4AttnA
   if (e != cudaSuccess) return e;
   const int64_t seen = visible_slots(a), heads = static_cast<int64_t>(a.n_requests) * a.n_kv_heads;
   int blocks = 1;
-  while (blocks < kMostCluster && seen > (blocks > 1 ? blocks : 2) * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
+  if (seen >= kSoloSlots && seen > kSoloHeads * heads)
+    while (blocks < kMostCluster && seen > blocks * kBlockSlots && heads <= fit.of(2 * blocks)) blocks *= 2;
   const bool alike = seen < a.max_len || a.n_requests == 1;
   const int64_t each = (seen + blocks - 1) / blocks, share = heads * seen / A.n_ctas;  // a block's slots, either way
   if (blocks == 1)

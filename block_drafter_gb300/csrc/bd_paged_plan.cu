@@ -8,7 +8,7 @@
 // rows and of the moved pages, which it finds by binary search in shared memory; of its threads some write the requests'
 // places and move pages, the others the rows.  Nothing that the rows' and pages' threads read is written in the launch.
 // Bound by its latency: the launch, one round trip for the counts, the scans, one more for tables and stack (8 requests of 16
-// rows 3.8 us).
+// rows 3.9 us; 512 requests, 66 000 rows, counts in place: 6.0 us, on one block alone 18.6 us).
 #include "bd_checks.h"
 #include "bd_paged_device.cuh"
 

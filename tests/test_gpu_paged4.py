@@ -430,3 +430,15 @@ def test_as_many_requests_as_there_may_be():
         out, lse = c.attend()
         sync()
         c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("rows,page,dtype,d", [(1, 64, "bf16", 128), (4, 16, "fp16", 64), (2, 33, "fp16", 128), (3, 33, "bf16", 64), (5, 64, "bf16", 64)])
+def test_long_requests_are_shared_out(rows, page, dtype, d):
+    """More slots than a cluster takes: shares and a joining launch, short and empty requests among them."""
+    c = Paged4Case((37000, 3, 0, 9001), (rows, min(rows, 3), rows, 1), hkv=1, page=page, dtype=dtype, d=d, seed=rows).build()
+    c.batch.workspace.fill_(255)
+    out, lse = c.attend()
+    sync()
+    c.check_attention(out, lse)
+    again, lse2 = c.attend()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
