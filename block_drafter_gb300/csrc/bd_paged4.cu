@@ -181,7 +181,8 @@ std::string launch_append4(Paged4AppendArgs &A, int dtype, cudaStream_t s) {
 // ------------------------------------------------------------------ the 16-bit copy
 // Calls of many rows use each slot often (a prompt of 8192 rows and group 4 reads every tile 128 times): its values are
 // worked out once into pages of kWideSlots slots of a pool in the workspace, which the 16-bit attention reads.
-// A block takes the keys or values of one head's kWideSlots slots, a thread 32 codes at a time.
+// A block takes the keys or values of one head's kWideSlots slots, a thread 8 codes at a time, so that a warp's values lie side by
+// side.
 constexpr int kWideSlots = 128;
 constexpr int kWideThreads = 256;
 
@@ -193,37 +194,41 @@ struct WidenArgs {
 };
 
 template <typename T, int D> __global__ void __launch_bounds__(kWideThreads) paged4_widen_kernel(const __grid_constant__ WidenArgs A) {
-  constexpr int P = D / 32;  // 16-byte pieces of a slot's codes
+  constexpr int W = D / 8;  // words of a slot's codes
+  __shared__ Place4 place[kWideSlots];  // of the page's slots; code -1: zeros
   const PagedArgs &a = A.c.p;
-  const int page = blockIdx.x, b = blockIdx.z, h = blockIdx.y >> 1, side = blockIdx.y & 1;
+  const int page = blockIdx.x, b = blockIdx.z, h = blockIdx.y >> 1, side = blockIdx.y & 1, tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0 && blockIdx.y == 0) A.table[b * A.pages + page] = b * A.pages + page;
+  if (tid == 0 && blockIdx.y == 0) A.table[b * A.pages + page] = b * A.pages + page;
   const Request rq = request_of(a, b);
   const int j0 = page * kWideSlots, f_low = window_first(a, max(0, rq.n - rq.rows));
   if (rq.rows == 0 || j0 >= rq.n || !any_seen(a, j0, kWideSlots, f_low, rq.n - 1)) return;
+  if (tid < kWideSlots) {
+    const int j = j0 + tid;
+    Place4 at = {-1, -1};  // slots that no row sees are zeros: no value of a tile is not finite
+    if (j < rq.n && any_seen(a, j, 1, f_low, rq.n - 1)) at = place4(A.c, __ldg(a.page_table + static_cast<int64_t>(b) * a.table_width + j / a.page_size), j);
+    place[tid] = at;
+  }
+  __syncthreads();
   const uint8_t *codes = static_cast<const uint8_t *>(side ? a.v : a.k) + h * a.head_stride;
   const uint8_t *scales = static_cast<const uint8_t *>(side ? A.c.v_scale : A.c.k_scale) + h * A.c.scale_head_stride;
   uint16_t *dst = (side ? A.v : A.k) + ((static_cast<int64_t>(b) * A.pages + page) * a.n_kv_heads + h) * kWideSlots * D;
-  const int32_t *table = a.page_table + static_cast<int64_t>(b) * a.table_width;
   const float up = pow2(side ? A.c.v_exp : A.c.k_exp);
+  constexpr int U = kWideSlots * W / kWideThreads;
+  uint32_t w[U], z[U];
 #pragma unroll
-  for (int u = 0; u < kWideSlots * P / kWideThreads; ++u) {
-    const int x = u * kWideThreads + threadIdx.x, r = x / P, i = x - r * P, j = j0 + r;
-    Place4 at = {-1, -1};  // slots that no row sees are zeros: no value of a tile is not finite
-    if (j < rq.n && any_seen(a, j, 1, f_low, rq.n - 1)) at = place4(A.c, __ldg(table + j / a.page_size), j);
-    uint4 w = make_uint4(0, 0, 0, 0);
-    uint32_t z = 0;
+  for (int u = 0; u < U; ++u) {
+    const int x = u * kWideThreads + tid, i = x % W;
+    const Place4 at = place[x / W];
+    w[u] = z[u] = 0;
     if (at.code >= 0) {
-      w = __ldg(reinterpret_cast<const uint4 *>(codes + at.code) + i);
-      z = __ldg(reinterpret_cast<const uint16_t *>(scales + at.scale) + i);
+      w[u] = __ldg(reinterpret_cast<const uint32_t *>(codes + at.code) + i);
+      z[u] = __ldg(scales + at.scale + i / 2);
     }
-    uint4 *to = reinterpret_cast<uint4 *>(dst + r * D + i * 32);
-    to[0] = decode8<T>(w.x, z & 0xff, up);
-    to[1] = decode8<T>(w.y, z & 0xff, up);
-    to[2] = decode8<T>(w.z, z >> 8, up);
-    to[3] = decode8<T>(w.w, z >> 8, up);
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u) reinterpret_cast<uint4 *>(dst)[u * kWideThreads + tid] = decode8<T>(w[u], z[u], up);
 }
 
 std::string launch_widen(const WidenArgs &A, int dtype, cudaStream_t s) {

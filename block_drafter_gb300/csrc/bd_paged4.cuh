@@ -19,6 +19,12 @@ __device__ __forceinline__ Place4 place4(const Paged4Args &c, int page, int j) {
   return {page * c.p.page_stride + in_page * c.p.slot_stride, page * c.scale_page_stride + in_page * c.scale_slot_stride};
 }
 
+// A slot's scales (4 or 8 bytes) to shared memory, zeros where not valid.
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes, bool valid) {
+  if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
 
 // The four bytes of w as fp16 pairs, the low half's value first (exact).

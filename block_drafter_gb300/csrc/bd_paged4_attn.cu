@@ -77,10 +77,6 @@ template <int D> struct Ring {
     else return (r ^ (r >> 2 & 1)) * kRow + x;
   }
 };
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes, bool valid) {
-  if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-}
 // What a lane holds of half a unit.  Lane: quad = lane / 4, kq = lane % 4.
 template <int D> struct Frag {
   static constexpr int W = D / 64;  // words of a lane's piece of a value slot (2 of a key slot's W)

@@ -22,11 +22,6 @@ namespace {
 
 constexpr int kStages = 3;  // tiles whose codes are on their way or being unpacked
 
-__device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void *src, int bytes, bool valid) {
-  if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-}
-
 struct Pool4 {
   static constexpr bool k4 = true;
   template <typename T> using Op = __half;
@@ -168,8 +163,8 @@ __device__ void Pool4::copy(const PagedAttnArgs &A, const Pool4 &src, const Segm
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t dst = to_scale + (k * 32 + lane) * (D / 16);
-        cp_async_bytes(dst, KS + scale[k], D / 16, in[k]);
-        cp_async_bytes(dst + SIDE, VS + scale[k], D / 16, in[k]);
+        cp_async_small(dst, KS + scale[k], D / 16, in[k]);
+        cp_async_small(dst + SIDE, VS + scale[k], D / 16, in[k]);
       }
       if (!box) {
 #pragma unroll

@@ -643,7 +643,7 @@ bd_status bd_paged4_append(const bd_paged4_kv *kv, const bd_paged_batch *batch, 
                            void *v_held, void *stream);
 
 /* Attention as bd_paged_attention's, over the values that the slots stand for.  All results of a row that
- * sees a slot are finite where its query is. */
+ * sees a slot are finite where its query and its scores are. */
 bd_status bd_paged4_attention(const bd_paged4_kv *kv, const bd_paged_batch *batch, const void *q,
                               int64_t q_stride, void *out, int64_t out_stride, float *lse, int window,
                               int n_sink, float scale, void *workspace, size_t workspace_bytes,
