@@ -572,7 +572,7 @@ bd_status bd_paged_evict(const bd_paged_kv *kv, const bd_paged_batch *batch, con
  *   slot_map       dev int64 [n_rows] OUT: page * page_size + place in the page, -1 likewise
  *   n_short        dev int32 [1] OUT, or NULL
  * Errors: BD_ERR_INVALID_ARG (sizes, NULL or misaligned arrays, an output that overlaps another array
- * but as said below).  One launch; a second one where more than 384 rows' call brings held or free_count up to date in
+ * but as said below).  One launch, or two where a call of more than 384 rows brings held or free_count up to date in
  * place.  Nothing else is kept between calls.
  */
 typedef struct {

@@ -71,14 +71,14 @@ class Paged4Case(PagedCase):
 
     def check_attention(self, out, lse, requests=None):
         """Against the oracle over the stored values.  As for the 16-bit cache, but for what the kernel that reads the codes
-        (up to 96 rows times heads of a KV head) rounds: queries of a bf16 row are off by at most 2^-33 of the row's
+        (up to 128 rows times heads of a KV head) rounds: queries of a bf16 row are off by at most 2^-33 of the row's
         largest, which a score takes as 2^-33 scale max|q| sum_d |k_d|; weights are fp16, half a step 2^-12, and with
         up to 16 fp16 rows the rest is a second operand, whose rounding is 2^-24 of the weight."""
         t = TYPES[self.dtype]
         half = torch.finfo(t).eps / 2
         tiny = torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2
         rows = self.max_rows * self.group
-        few = rows <= 96
+        few = rows <= 128
         weight = half if not few else 2.0 ** -12 if self.dtype == "bf16" or rows > 16 else 2.0 ** -23
         got, glse = out.double().cpu().numpy(), lse.double().cpu().numpy()
         for b, (n, r) in enumerate(zip(self.lens, self.rows)):
